@@ -97,6 +97,19 @@ def load():
     lib.fa_fwd_tile_rows.restype = i
     lib.fa_work_schedule.argtypes = [i, i, i, i, ctypes.POINTER(ctypes.c_int)]
     lib.fa_work_schedule.restype = i
+    ll = ctypes.c_longlong
+    lib.fa_rope_table.argtypes = [ctypes.POINTER(ctypes.c_double), i, ctypes.POINTER(ctypes.c_uint64)]
+    lib.fa_rope_table.restype = i
+    lib.fa_rope.argtypes = [vp, vp] + [ll] * 6 + [vp, vp] + [i] * 6 + [f, i, vp]
+    lib.fa_rope.restype = i
+    lib.fa_cache_append_fp8.argtypes = [vp, vp] + [ll] * 6 + [vp] * 9 + [i] * 6 + [f] + [i] * 4 + [vp]
+    lib.fa_cache_append_fp8.restype = i
+    lib.fa_decode_paged_fp8_workspace_bytes.argtypes = [i] * 8
+    lib.fa_decode_paged_fp8_workspace_bytes.restype = sz
+    lib.fa_decode_paged_fp8.argtypes = [vp] * 10 + [i] * 9 + [f, i, vp, sz, vp]
+    lib.fa_decode_paged_fp8.restype = i
+    lib.fa_cache_evict_fp8.argtypes = [vp] * 11 + [i] * 10 + [vp]
+    lib.fa_cache_evict_fp8.restype = i
     _lib = lib
     return lib
 
@@ -372,6 +385,56 @@ def fa_decode_noalloc(q, kcache, vcache, o, lse, B, H, Nk, d, scale, num_splits,
               int(num_splits), _stream(stream)), "fa_decode_noalloc")
 
 
+def fa_rope_table(inv_freq):
+    """Turns per position (Python ints, 2^-64 turn) of the angles per position ``inv_freq`` (radians)."""
+    fn = load().fa_rope_table
+    n = len(inv_freq)
+    turns = (ctypes.c_uint64 * max(1, n))()
+    _raise(fn((ctypes.c_double * max(1, n))(*inv_freq), n, turns), "fa_rope_table")
+    return list(turns)
+
+
+def fa_rope(x, y, x_strides, y_strides, positions, turns, B, H, N, d, rot, interleaved, magnitude, inverse,
+            stream=None):
+    _raise(load().fa_rope(_ptr(x), _ptr(y), *x_strides, *y_strides, _ptr(positions), _ptr(turns), B, H, N, d, rot,
+                          int(bool(interleaved)), float(magnitude), int(bool(inverse)), _stream(stream)), "fa_rope")
+
+
+def fa_cache_append_fp8(k, v, k_strides, v_strides, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens,
+                        new_lens, positions, turns, B, Hkv, N, d, rot, interleaved, magnitude, page_size,
+                        scale_block, max_pages, num_pages, stream=None):
+    _raise(load().fa_cache_append_fp8(_ptr(k), _ptr(v), *k_strides, *v_strides, _ptr(k_pages), _ptr(v_pages),
+                                      _ptr(k_scale), _ptr(v_scale), _ptr(block_table), _ptr(seq_lens),
+                                      _ptr(new_lens), _ptr(positions), _ptr(turns), B, Hkv, N, d, rot,
+                                      int(bool(interleaved)), float(magnitude), page_size, scale_block, max_pages,
+                                      num_pages, _stream(stream)), "fa_cache_append_fp8")
+
+
+def fa_decode_paged_fp8_workspace_bytes(B, Hq, Hkv, Nq, d, max_tokens, num_splits, weights):
+    return load().fa_decode_paged_fp8_workspace_bytes(B, Hq, Hkv, Nq, d, max_tokens, int(num_splits),
+                                                      int(bool(weights)))
+
+
+def fa_decode_paged_fp8(q, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, o, lse, weights, B, Hq, Hkv,
+                        Nq, page_size, scale_block, max_pages, num_pages, d, scale, num_splits, workspace,
+                        workspace_bytes, stream=None):
+    _raise(load().fa_decode_paged_fp8(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale),
+                                      _ptr(block_table), _ptr(seq_lens), _ptr(o), _ptr(lse), _ptr(weights), B, Hq,
+                                      Hkv, Nq, page_size, scale_block, max_pages, num_pages, d, float(scale),
+                                      int(num_splits), _ptr(workspace), int(workspace_bytes), _stream(stream)),
+           "fa_decode_paged_fp8")
+
+
+def fa_cache_evict_fp8(k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, weights, new_table, new_lens,
+                       new_weights, kept, B, Hkv, page_size, scale_block, max_pages, new_max_pages, num_pages, d,
+                       keep, recent, stream=None):
+    _raise(load().fa_cache_evict_fp8(_ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale), _ptr(block_table),
+                                     _ptr(seq_lens), _ptr(weights), _ptr(new_table), _ptr(new_lens),
+                                     _ptr(new_weights), _ptr(kept), B, Hkv, page_size, scale_block, max_pages,
+                                     new_max_pages, num_pages, d, int(keep), int(recent), _stream(stream)),
+           "fa_cache_evict_fp8")
+
+
 # ------------------------------------------------------------------ conveniences
 def _check(t, name, shape):
     if not (t.is_cuda and t.dtype == torch.bfloat16 and t.is_contiguous()):
@@ -451,3 +514,194 @@ def decode(q, kcache, vcache, scale=None, num_splits=0, stream=None, workspace=N
     fa_decode(q, kcache, vcache, o, lse, B, H, Nk, d, scale, num_splits, workspace,
               workspace.numel() * workspace.element_size(), stream)
     return (o, lse) if want_lse else o
+
+
+# ------------------------------------------------------------------ rotary positions and the 8-bit cache
+def _need(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _on(t, name, dtype, shape, dev):
+    """A contiguous tensor of this type, shape and device."""
+    if not (t.device == dev and t.dtype == dtype and t.is_contiguous() and tuple(t.shape) == shape):
+        raise ValueError("%s must be a contiguous %s tensor of shape %s on %s" % (name, dtype, shape, dev))
+
+
+class _Launching:
+    """Makes ``dev`` the current device and ``stream`` (None: the current one) the stream on which torch allocates,
+    so that what a call allocates belongs to the stream that uses it."""
+
+    def __init__(self, dev, stream):
+        self.held = []
+        if dev.index is not None and dev.index != torch.cuda.current_device():
+            self.held.append(torch.cuda.device(dev))
+        if stream is not None:
+            if not hasattr(stream, "cuda_stream"):
+                stream = torch.cuda.ExternalStream(int(stream), device=dev)
+            self.held.append(torch.cuda.stream(stream))
+
+    def __enter__(self):
+        for c in self.held:
+            c.__enter__()
+
+    def __exit__(self, *e):
+        for c in reversed(self.held):
+            c.__exit__(*e)
+
+
+def rope_frequencies(rot, base=10000.0, scaling=None, factor=1.0, original_context=None, beta_fast=32.0,
+                     beta_slow=1.0):
+    """Angle per position of each of rot / 2 pairs (Python floats), and the magnitude for ``rope``.
+
+    scaling None: base^(-2i/rot).  "linear": positions divided by factor.  "ntk": the base times
+    factor^(rot / (rot - 2)), which stretches the longest wave by factor and leaves the shortest.  "yarn": by parts;
+    pairs that turn more than beta_fast times within original_context tokens keep their frequency, those that turn
+    less than beta_slow times are divided by factor, the ones between are blended linearly in their number of turns;
+    magnitude 0.1 ln(factor) + 1.
+    """
+    _need(rot >= 2 and rot % 2 == 0, "rot must be even and at least 2")
+    _need(base > 0 and factor >= 1.0, "base must be positive and factor at least 1")
+    if scaling == "ntk" and rot > 2:
+        base = base * factor ** (rot / (rot - 2.0))
+    f = [base ** (-2.0 * i / rot) for i in range(rot // 2)]
+    if scaling is None or scaling == "ntk":
+        return f, 1.0
+    if scaling == "linear":
+        return [x / factor for x in f], 1.0
+    _need(scaling == "yarn", "scaling must be None, 'linear', 'ntk' or 'yarn'")
+    _need(original_context is not None and original_context >= 1, "yarn needs the original context's length")
+    _need(beta_fast > beta_slow, "beta_fast must be above beta_slow")
+    out = []
+    for x in f:
+        keep = (original_context * x / (2.0 * math.pi) - beta_slow) / (beta_fast - beta_slow)
+        keep = min(1.0, max(0.0, keep))
+        out.append(x * keep + x / factor * (1.0 - keep))
+    return out, 0.1 * math.log(factor) + 1.0
+
+
+def rope_table(inv_freq, device="cuda"):
+    """The device table (int64 [rot / 2], the bits of fa_rope_table's values) of angles per position in radians."""
+    turns = fa_rope_table([float(x) for x in inv_freq])
+    return torch.tensor([t - (1 << 64) if t >= 1 << 63 else t for t in turns], dtype=torch.int64, device=device)
+
+
+def _bhnd(t, name, dev=None):
+    """(strides) of a bf16 CUDA tensor [B, H, N, d] whose innermost dimension is dense."""
+    if not (t.is_cuda and t.dtype == torch.bfloat16 and t.dim() == 4 and (dev is None or t.device == dev)):
+        raise ValueError("%s must be a bf16 CUDA tensor [B, H, N, d]" % name)
+    s = t.stride()
+    if s[3] != 1:
+        raise ValueError("%s must be dense in its last dimension" % name)
+    return s[:3]
+
+
+def rope(x, turns, positions=None, interleaved=False, magnitude=1.0, inverse=False, out=None, stream=None):
+    """x [B,H,N,d] (bf16, any strides that fa_rope takes) rotated by its tokens' positions: pairs 0 .. len(turns) - 1,
+    the columns behind them copied.  turns: rope_table(...).  positions: int32 [B,N] on the device, or None (0..N-1).
+    inverse=True turns back: the gradient of x from the gradient of the result.  out: where to write (may be x);
+    default a new contiguous tensor."""
+    B, H, N, d = x.shape
+    xs = _bhnd(x, "x")
+    dev = x.device
+    half = turns.shape[0] if turns.dim() == 1 else -1
+    _on(turns, "turns", torch.int64, (half,), dev)
+    if positions is not None:
+        _on(positions, "positions", torch.int32, (B, N), dev)
+    if out is not None:
+        _need(out.shape == x.shape, "out must have x's shape")
+        _bhnd(out, "out", dev)
+    with _Launching(dev, stream):
+        y = torch.empty((B, H, N, d), dtype=torch.bfloat16, device=dev) if out is None else out
+        fa_rope(x, y, xs, y.stride()[:3], positions, turns, B, H, N, d, 2 * half, interleaved, magnitude, inverse,
+                stream)
+    return y
+
+
+def _pages(k_pages, v_pages, k_scale, v_scale, block_table, seq_lens):
+    """Checks the paged 8-bit cache; (device, B, num_pages, Hkv, page, d, scale_block, max_pages)."""
+    dev = k_pages.device
+    _need(k_pages.is_cuda and k_pages.dim() == 4, "k_pages must be a CUDA tensor [num_pages, Hkv, page, d]")
+    _need(k_scale.dim() == 3 and block_table.dim() == 2, "k_scale must have 3 dimensions and block_table 2")
+    num_pages, Hkv, page, d = k_pages.shape
+    blocks = k_scale.shape[2]
+    _need(blocks >= 1 and page % blocks == 0, "k_scale must have a divisor of the page size as its last dimension")
+    for t, n in ((k_pages, "k_pages"), (v_pages, "v_pages")):
+        _on(t, n, torch.uint8, (num_pages, Hkv, page, d), dev)
+    for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        _on(t, n, torch.float32, (num_pages, Hkv, blocks), dev)
+    B, max_pages = block_table.shape
+    _on(block_table, "block_table", torch.int32, (B, max_pages), dev)
+    _on(seq_lens, "seq_lens", torch.int32, (B,), dev)
+    return dev, B, num_pages, Hkv, page, d, page // blocks, max_pages
+
+
+def cache_append_fp8(k, v, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, new_lens=None, turns=None,
+                     positions=None, interleaved=False, magnitude=1.0, stream=None):
+    """Writes k, v [B,Hkv,N,d] (bf16, any strides that fa_rope takes) behind the seq_lens[b] tokens that the paged
+    8-bit cache holds of each sequence: the first new_lens[b] of them (None: all N).  With turns, k is rotated on the
+    way (positions int32 [B,N], or None: seq_lens[b] + i).  Changes the pages and scales, not seq_lens."""
+    dev, B, num_pages, Hkv, page, d, sb, max_pages = _pages(k_pages, v_pages, k_scale, v_scale, block_table, seq_lens)
+    ks, vs = _bhnd(k, "k", dev), _bhnd(v, "v", dev)
+    N = k.shape[2]
+    _need(tuple(k.shape) == (B, Hkv, N, d) and tuple(v.shape) == (B, Hkv, N, d),
+          "k and v must have shape %s" % ((B, Hkv, N, d),))
+    if new_lens is not None:
+        _on(new_lens, "new_lens", torch.int32, (B,), dev)
+    half = 0
+    if turns is not None:
+        half = turns.shape[0] if turns.dim() == 1 else -1
+        _on(turns, "turns", torch.int64, (half,), dev)
+        if positions is not None:
+            _on(positions, "positions", torch.int32, (B, N), dev)
+    else:
+        positions = None
+    with _Launching(dev, stream):
+        fa_cache_append_fp8(k, v, ks, vs, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, new_lens,
+                            positions, turns, B, Hkv, N, d, 2 * half, interleaved, magnitude, page, sb, max_pages,
+                            num_pages, stream)
+
+
+def decode_paged_fp8(q, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, scale=None, weights=None,
+                     num_splits=0, stream=None, workspace=None):
+    """O [B,Hq,Nq,d] bf16 and LSE [B,Hq,Nq] fp32 of the last Nq tokens (q [B,Hq,Nq,d], or [B,Hq,d] for one, which
+    gives O [B,Hq,d] and LSE [B,Hq]) over the paged 8-bit cache, which holds them already.  weights: fp32
+    [B,Hkv,max_pages*page] to which every token's attention weight is added, or None."""
+    dev, B, num_pages, Hkv, page, d, sb, max_pages = _pages(k_pages, v_pages, k_scale, v_scale, block_table, seq_lens)
+    _need(q.dim() in (3, 4), "q must have 3 or 4 dimensions")
+    Hq, Nq = q.shape[1], (q.shape[2] if q.dim() == 4 else 1)
+    _on(q, "q", torch.bfloat16, (B, Hq, Nq, d) if q.dim() == 4 else (B, Hq, d), dev)
+    if weights is not None:
+        _on(weights, "weights", torch.float32, (B, Hkv, max_pages * page), dev)
+    scale = 1.0 / math.sqrt(d) if scale is None else scale
+    with _Launching(dev, stream):
+        if workspace is None:
+            nbytes = fa_decode_paged_fp8_workspace_bytes(B, Hq, Hkv, Nq, d, max_pages * page, num_splits,
+                                                         weights is not None)
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        o = torch.empty_like(q)
+        lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=dev)
+        fa_decode_paged_fp8(q, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, o, lse, weights, B, Hq, Hkv,
+                            Nq, page, sb, max_pages, num_pages, d, scale, num_splits, workspace,
+                            workspace.numel() * workspace.element_size(), stream)
+    return o, lse
+
+
+def cache_evict_fp8(k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, weights, new_table, keep, recent=0,
+                    stream=None):
+    """Copies, of each sequence and kv head, the last ``recent`` tokens and the keep - recent others of largest
+    accumulated weight into the pages of new_table (int32 [B, new_max_pages], disjoint from the pages read).  Returns
+    (new_lens int32 [B], new_weights fp32 and kept int32 [B,Hkv,new_max_pages*page]): the kept tokens' weights and
+    source indices, 0 and -1 behind them."""
+    dev, B, num_pages, Hkv, page, d, sb, max_pages = _pages(k_pages, v_pages, k_scale, v_scale, block_table, seq_lens)
+    _on(weights, "weights", torch.float32, (B, Hkv, max_pages * page), dev)
+    new_max_pages = new_table.shape[1] if new_table.dim() == 2 else -1
+    _on(new_table, "new_table", torch.int32, (B, new_max_pages), dev)
+    with _Launching(dev, stream):
+        new_lens = torch.empty((B,), dtype=torch.int32, device=dev)
+        new_weights = torch.empty((B, Hkv, new_max_pages * page), dtype=torch.float32, device=dev)
+        kept = torch.empty((B, Hkv, new_max_pages * page), dtype=torch.int32, device=dev)
+        fa_cache_evict_fp8(k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, weights, new_table, new_lens,
+                           new_weights, kept, B, Hkv, page, sb, max_pages, new_max_pages, num_pages, d, keep, recent,
+                           stream)
+    return new_lens, new_weights, kept

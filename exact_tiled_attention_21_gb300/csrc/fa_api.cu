@@ -722,6 +722,331 @@ int fa_fwd_fp8(const void* q, const void* k, const void* v, const float* q_scale
     return launch_fwd_fp8(a, (cudaStream_t)stream) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
+}  // extern "C"
+
+// ---------------------------------------------------------------- rotary positions and the 8-bit cache
+namespace {
+
+// Strides of a [B, H, N, d] tensor: d innermost, the others multiples of 8 elements (16 bytes); that of a
+// dimension of size 1 is not used (set to 0).
+int check_strides(long long* sb, long long* sh, long long* sn, int B, int H, int N) {
+    if (B == 1) *sb = 0;
+    if (H == 1) *sh = 0;
+    if (N == 1) *sn = 0;
+    if (*sb < 0 || *sh < 0 || *sn < 0) return FA_ERR_INVALID_ARG;
+    if ((*sb | *sh | *sn) & 7) return FA_ERR_ALIGNMENT;
+    return FA_OK;
+}
+
+// Whether no two elements of such a tensor share an address.
+bool strides_distinct(long long sb, long long sh, long long sn, int B, int H, int N, int d) {
+    std::pair<long long, int> s[3] = {{sb, B}, {sh, H}, {sn, N}};
+    std::sort(s, s + 3);
+    long long extent = d;
+    for (const auto& x : s) {
+        if (x.second == 1) continue;
+        if (x.first < extent) return false;
+        extent += x.first * (x.second - 1);
+    }
+    return true;
+}
+
+int check_rotation(int d, int rot, int interleaved, float magnitude) {
+    if (interleaved != 0 && interleaved != 1) return FA_ERR_INVALID_ARG;
+    if (!std::isfinite(magnitude) || rot < 1 || rot > d) return FA_ERR_INVALID_ARG;
+    return rot % 16 ? FA_ERR_UNSUPPORTED : FA_OK;
+}
+
+constexpr long long kMaxCacheTokens = 1ll << 30;  // of one sequence: token arithmetic stays in int
+
+// Sizes of the paged 8-bit cache that its three entry points share.
+int check_cache(int B, int Hkv, int page, int sb, int max_pages, int num_pages, int d) {
+    if (B < 1 || Hkv < 1 || page < 1 || sb < 1 || max_pages < 1 || num_pages < 1) return FA_ERR_INVALID_ARG;
+    if (page % sb) return FA_ERR_INVALID_ARG;
+    if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+    if (sb > 128) return FA_ERR_UNSUPPORTED;
+    if ((long long)max_pages * page > kMaxCacheTokens || (long long)B * Hkv > (1ll << 24)) return FA_ERR_UNSUPPORTED;
+    // cache rows (num_pages * Hkv * page) are counted in 32 bits
+    if ((long long)num_pages * Hkv > 0xFFFFFFFEll / page) return FA_ERR_UNSUPPORTED;
+    return FA_OK;
+}
+
+// The most splits that the automatic choice of the 8-bit decode takes: one per step (keys that a CTA takes at a time),
+// 256, and 4096 CTAs in all, which bounds the workspace.  items: CTAs per split.
+int fp8_most_splits(long long items, long long max_tokens, long long step) {
+    return (int)std::max<long long>(1, std::min({256ll, (max_tokens + step - 1) / step, 4096 / items}));
+}
+int fp8_step(int d) { return d == 128 ? kFp8ChunkKeys128 : kFp8ChunkKeys64; }
+long long fp8_items(int B, int Hq, int Hkv, int Nq) { return (long long)B * Hkv * (((long long)(Hq / Hkv) * Nq + 15) / 16); }
+
+// Automatic splits.  `resident` CTAs run at once: a launch costs about waves * (steps per chunk + a fixed cost of about
+// two steps), and the merge reads every split, so the fewest splits of the cheapest count are taken.
+int fp8_splits(long long items, long long max_tokens, long long step, long long resident) {
+    const long long most = fp8_most_splits(items, max_tokens, step);
+    long long best = 1, best_cost = LLONG_MAX;
+    for (long long sp = 1; sp <= most; ++sp) {
+        const long long per = (max_tokens + sp - 1) / sp, steps = (per + step - 1) / step;
+        const long long waves = (items * sp + resident - 1) / resident;
+        const long long cost = waves * (steps + 2) * 64 + sp;
+        if (cost < best_cost) {
+            best_cost = cost;
+            best = sp;
+        }
+    }
+    return (int)best;
+}
+
+int g_fp8_blocks[kMaxDevices][2] = {};  // resident CTAs per SM of the 8-bit split kernel, by device and d (64, 128)
+
+int fp8_resident(int d, int num_sms, long long* resident) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return FA_ERR_CUDA;
+    std::lock_guard<std::mutex> lock(g_mu);
+    int& c = g_fp8_blocks[dev][d == 128 ? 1 : 0];
+    if (!c) {
+        int b = 0;
+        if (decode_fp8_blocks_per_sm(d, &b) != cudaSuccess || b < 1) return FA_ERR_CUDA;
+        c = b;
+    }
+    *resident = (long long)num_sms * c;
+    return FA_OK;
+}
+
+size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+// Workspace of the 8-bit decode: partial outputs, partial LSEs, and with weights the scores, whose rows are padded
+// to a multiple of four keys.
+struct Fp8Workspace {
+    size_t part_lse, scores, bytes;
+    long long score_stride;
+};
+Fp8Workspace fp8_workspace(int B, int Hq, int Nq, int d, long long max_tokens, int splits, bool weights) {
+    Fp8Workspace w;
+    const size_t rows = (size_t)B * Hq * Nq;
+    w.part_lse = splits > 1 ? align256(rows * splits * d * 4) : 0;
+    w.scores = w.part_lse + align256(rows * splits * 4);
+    w.score_stride = (max_tokens + 3) & ~3ll;
+    w.bytes = w.scores + (weights ? align256(rows * (size_t)w.score_stride * 4) : 0);
+    return w;
+}
+
+}  // namespace
+
+extern "C" {
+
+int fa_rope_table(const double* inv_freq, int n, uint64_t* turns) {
+    if (!inv_freq || !turns || n < 1) return FA_ERR_INVALID_ARG;
+    for (int i = 0; i < n; ++i)
+        if (!std::isfinite(inv_freq[i])) return FA_ERR_INVALID_ARG;
+    for (int i = 0; i < n; ++i) {
+        const double t = inv_freq[i] / 6.283185307179586;  // turns per position; whole turns drop out
+        const double f = t - std::floor(t);                // [0, 1]
+        // 2^64 f in two 32-bit steps, each exact in a double
+        const double hi = std::floor(f * 4294967296.0), lo = std::nearbyint((f * 4294967296.0 - hi) * 4294967296.0);
+        turns[i] = ((uint64_t)hi << 32) + (uint64_t)lo;
+    }
+    return FA_OK;
+}
+
+int fa_rope(const void* x, void* y, long long x_sb, long long x_sh, long long x_sn, long long y_sb, long long y_sh,
+            long long y_sn, const int* positions, const uint64_t* turns, int B, int H, int N, int d, int rot,
+            int interleaved, float magnitude, int inverse, void* stream) {
+    if (!x || !y || !turns || B < 1 || H < 1 || N < 1) return FA_ERR_INVALID_ARG;
+    if (inverse != 0 && inverse != 1) return FA_ERR_INVALID_ARG;
+    if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+    int st = check_rotation(d, rot, interleaved, magnitude);
+    if (st != FA_OK) return st;
+    if ((long long)B * N > 0x7FFFFFFFll || (long long)B * H > (1ll << 24)) return FA_ERR_UNSUPPORTED;
+    if (!aligned16(x) || !aligned16(y) || !aligned16(turns) || (positions && !aligned4(positions)))
+        return FA_ERR_ALIGNMENT;
+    if ((st = check_strides(&x_sb, &x_sh, &x_sn, B, H, N)) != FA_OK) return st;
+    if ((st = check_strides(&y_sb, &y_sh, &y_sn, B, H, N)) != FA_OK) return st;
+    if (!strides_distinct(y_sb, y_sh, y_sn, B, H, N, d)) return FA_ERR_INVALID_ARG;
+    if (x == y && (x_sb != y_sb || x_sh != y_sh || x_sn != y_sn)) return FA_ERR_INVALID_ARG;
+    RopeLaunch a;
+    st = device_state(nullptr, &a.num_sms);
+    if (st != FA_OK) return st;
+    a.x = x;
+    a.y = y;
+    a.xb = x_sb;
+    a.xh = x_sh;
+    a.xn = x_sn;
+    a.yb = y_sb;
+    a.yh = y_sh;
+    a.yn = y_sn;
+    a.positions = positions;
+    a.turns = turns;
+    a.tokens = (long long)B * N;
+    a.H = H;
+    a.N = N;
+    a.d = d;
+    a.rot = rot;
+    a.interleaved = interleaved;
+    a.inverse = inverse;
+    a.hpt = 1;
+    a.magnitude = magnitude;
+    return launched(launch_rope(a, (cudaStream_t)stream));
+}
+
+int fa_cache_append_fp8(const void* k, const void* v, long long k_sb, long long k_sh, long long k_sn, long long v_sb,
+                        long long v_sh, long long v_sn, void* k_pages, void* v_pages, float* k_scale, float* v_scale,
+                        const int* block_table, const int* seq_lens, const int* new_lens, const int* positions,
+                        const uint64_t* turns, int B, int Hkv, int N, int d, int rot, int interleaved, float magnitude,
+                        int page_size, int scale_block, int max_pages, int num_pages, void* stream) {
+    if (!k || !v || !k_pages || !v_pages || !k_scale || !v_scale || !block_table || !seq_lens || N < 1)
+        return FA_ERR_INVALID_ARG;
+    int st = check_cache(B, Hkv, page_size, scale_block, max_pages, num_pages, d);
+    if (st != FA_OK) return st;
+    if (turns && (st = check_rotation(d, rot, interleaved, magnitude)) != FA_OK) return st;
+    if (N > kMaxCacheTokens || (long long)B * N > 0x7FFFFFFFll) return FA_ERR_UNSUPPORTED;
+    if (!aligned16(k) || !aligned16(v) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(turns) ||
+        !aligned4(k_scale) || !aligned4(v_scale) || !aligned4(block_table) || !aligned4(seq_lens) ||
+        !aligned4(new_lens) || !aligned4(positions))
+        return FA_ERR_ALIGNMENT;
+    if ((st = check_strides(&k_sb, &k_sh, &k_sn, B, Hkv, N)) != FA_OK) return st;
+    if ((st = check_strides(&v_sb, &v_sh, &v_sn, B, Hkv, N)) != FA_OK) return st;
+    CacheAppendLaunch a;
+    st = device_state(&a.err, nullptr);
+    if (st != FA_OK) return st;
+    a.k = k;
+    a.v = v;
+    a.kb = k_sb;
+    a.kh = k_sh;
+    a.kn = k_sn;
+    a.vb = v_sb;
+    a.vh = v_sh;
+    a.vn = v_sn;
+    a.kp = static_cast<uint8_t*>(k_pages);
+    a.vp = static_cast<uint8_t*>(v_pages);
+    a.ks = k_scale;
+    a.vs = v_scale;
+    a.table = block_table;
+    a.lens = seq_lens;
+    a.new_lens = new_lens;
+    a.positions = positions;
+    a.turns = turns;
+    a.B = B;
+    a.Hkv = Hkv;
+    a.N = N;
+    a.d = d;
+    a.rot = rot;
+    a.interleaved = turns ? interleaved : 0;
+    a.page = page_size;
+    a.sb = scale_block;
+    a.max_pages = max_pages;
+    a.num_pages = num_pages;
+    a.magnitude = magnitude;
+    return launched(launch_cache_append(a, (cudaStream_t)stream));
+}
+
+size_t fa_decode_paged_fp8_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d, int max_tokens, int num_splits,
+                                           int weights) {
+    if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || Nq < 1 || Nq > 16 || (d != 64 && d != 128) || max_tokens < 1 || num_splits > 256) return 0;
+    if (max_tokens > kMaxCacheTokens || (long long)B * Hq > (1ll << 24) || (weights != 0 && weights != 1)) return 0;
+    const int splits = num_splits > 0 ? num_splits : fp8_most_splits(fp8_items(B, Hq, Hkv, Nq), max_tokens, fp8_step(d));
+    return std::max<size_t>(256, fp8_workspace(B, Hq, Nq, d, max_tokens, splits, weights != 0).bytes);
+}
+
+int fa_decode_paged_fp8(const void* q, const void* k_pages, const void* v_pages, const float* k_scale,
+                        const float* v_scale, const int* block_table, const int* seq_lens, void* o, float* lse,
+                        float* weights, int B, int Hq, int Hkv, int Nq, int page_size, int scale_block, int max_pages,
+                        int num_pages, int d, float scale, int num_splits, void* workspace, size_t workspace_bytes,
+                        void* stream) {
+    if (!q || !k_pages || !v_pages || !k_scale || !v_scale || !block_table || !seq_lens || !o) return FA_ERR_INVALID_ARG;
+    if (!scale_ok(scale) || num_splits > 256 || Hq < 1 || Nq < 1) return FA_ERR_INVALID_ARG;
+    int st = check_cache(B, Hkv, page_size, scale_block, max_pages, num_pages, d);
+    if (st != FA_OK) return st;
+    if (Hq % Hkv) return FA_ERR_INVALID_ARG;
+    if (Nq > 16 || (long long)B * Hq > (1ll << 24)) return FA_ERR_UNSUPPORTED;
+    if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(o) || !aligned4(k_scale) ||
+        !aligned4(v_scale) || !aligned4(block_table) || !aligned4(seq_lens) || !aligned4(lse) || !aligned4(weights))
+        return FA_ERR_ALIGNMENT;
+    PagedDecodeFp8Launch a;
+    int num_sms = 0;
+    st = device_state(&a.err, &num_sms);
+    if (st != FA_OK) return st;
+    const long long max_tokens = (long long)max_pages * page_size;
+    if (num_splits <= 0) {
+        long long resident = 0;
+        st = fp8_resident(d, num_sms, &resident);
+        if (st != FA_OK) return st;
+        num_splits = fp8_splits(fp8_items(B, Hq, Hkv, Nq), max_tokens, fp8_step(d), resident);
+    }
+    const Fp8Workspace ws = fp8_workspace(B, Hq, Nq, d, max_tokens, num_splits, weights != nullptr);
+    if (!workspace || workspace_bytes < ws.bytes) return FA_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return FA_ERR_ALIGNMENT;
+    char* base = static_cast<char*>(workspace);
+    a.q = q;
+    a.kp = static_cast<const uint8_t*>(k_pages);
+    a.vp = static_cast<const uint8_t*>(v_pages);
+    a.ks = k_scale;
+    a.vs = v_scale;
+    a.table = block_table;
+    a.lens = seq_lens;
+    a.o = o;
+    a.lse = lse;
+    a.weights = weights;
+    a.part_o = reinterpret_cast<float*>(base);
+    a.part_lse = reinterpret_cast<float*>(base + ws.part_lse);
+    a.scores = reinterpret_cast<float*>(base + ws.scores);
+    a.score_stride = ws.score_stride;
+    a.B = B;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.Nq = Nq;
+    a.page = page_size;
+    a.sb = scale_block;
+    a.max_pages = max_pages;
+    a.num_pages = num_pages;
+    a.d = d;
+    a.splits = num_splits;
+    a.scale = scale;
+    return launched(launch_decode_paged_fp8(a, (cudaStream_t)stream));
+}
+
+int fa_cache_evict_fp8(void* k_pages, void* v_pages, float* k_scale, float* v_scale, const int* block_table,
+                       const int* seq_lens, const float* weights, const int* new_table, int* new_lens,
+                       float* new_weights, int* kept, int B, int Hkv, int page_size, int scale_block, int max_pages,
+                       int new_max_pages, int num_pages, int d, int keep, int recent, void* stream) {
+    if (!k_pages || !v_pages || !k_scale || !v_scale || !block_table || !seq_lens || !weights || !new_table ||
+        !new_lens || !new_weights || !kept)
+        return FA_ERR_INVALID_ARG;
+    int st = check_cache(B, Hkv, page_size, scale_block, max_pages, num_pages, d);
+    if (st != FA_OK) return st;
+    if (new_max_pages < 1 || keep < 1 || recent < 0 || recent > keep) return FA_ERR_INVALID_ARG;
+    if ((long long)new_max_pages * page_size > kMaxCacheTokens) return FA_ERR_UNSUPPORTED;
+    if (keep > (long long)new_max_pages * page_size) return FA_ERR_INVALID_ARG;
+    if (!aligned16(k_pages) || !aligned16(v_pages) || !aligned4(k_scale) || !aligned4(v_scale) ||
+        !aligned4(block_table) || !aligned4(seq_lens) || !aligned4(weights) || !aligned4(new_table) ||
+        !aligned4(new_lens) || !aligned4(new_weights) || !aligned4(kept))
+        return FA_ERR_ALIGNMENT;
+    CacheEvictLaunch a;
+    st = device_state(&a.err, nullptr);
+    if (st != FA_OK) return st;
+    a.kp = static_cast<uint8_t*>(k_pages);
+    a.vp = static_cast<uint8_t*>(v_pages);
+    a.ks = k_scale;
+    a.vs = v_scale;
+    a.table = block_table;
+    a.lens = seq_lens;
+    a.weights = weights;
+    a.new_table = new_table;
+    a.new_lens = new_lens;
+    a.new_weights = new_weights;
+    a.kept = kept;
+    a.B = B;
+    a.Hkv = Hkv;
+    a.page = page_size;
+    a.sb = scale_block;
+    a.max_pages = max_pages;
+    a.new_max_pages = new_max_pages;
+    a.num_pages = num_pages;
+    a.d = d;
+    a.keep = keep;
+    a.recent = recent;
+    return launched(launch_cache_evict(a, (cudaStream_t)stream));
+}
+
 int fa_selftest_wait_timeout(uint64_t timeout_ns, void* stream) {
     if (timeout_ns < 1000ull || timeout_ns > 1000000000ull) return FA_ERR_INVALID_ARG;
     DevError* err = nullptr;

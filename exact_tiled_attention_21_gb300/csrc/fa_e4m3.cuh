@@ -1,0 +1,72 @@
+// e4m3 conversions and the mma / cp.async wrappers of the 8-bit cache kernels.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "fa_ptx.cuh"
+
+namespace fa {
+
+// Two e4m3 bytes (low half of w) as two halves: exact (NaN stays NaN).
+__device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t w) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(w));
+    return r;
+}
+__device__ __forceinline__ uint32_t e4m3x2_hi_to_half2(uint32_t w) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}" : "=r"(r) : "r"(w));
+    return r;
+}
+__device__ __forceinline__ float2 half2_to_float2(uint32_t w) {
+    return __half22float2(*reinterpret_cast<__half2*>(&w));
+}
+// Four values to e4m3 bytes: nearest, ties to even, saturated at +-448, NaN kept.
+__device__ __forceinline__ uint32_t e4m3x4(float x0, float x1, float x2, float x3) {
+    uint16_t lo, hi;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(x1), "f"(x0));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(x3), "f"(x2));
+    return (uint32_t)lo | ((uint32_t)hi << 16);
+}
+
+// Sixteen e4m3 bytes with scale `from` as e4m3 bytes with scale `to`, each
+// value rounded to nearest once more.  Powers of two only shift the exponent,
+// so nothing changes but values that become subnormal.
+__device__ __forceinline__ uint4 e4m3_rescale16(uint4 x, float from, float to) {
+    uint32_t* w = reinterpret_cast<uint32_t*>(&x);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 a = half2_to_float2(e4m3x2_to_half2(w[i])), b = half2_to_float2(e4m3x2_hi_to_half2(w[i]));
+        w[i] = e4m3x4(__fdiv_rn(__fmul_rn(a.x, from), to), __fdiv_rn(__fmul_rn(a.y, from), to),
+                      __fdiv_rn(__fmul_rn(b.x, from), to), __fdiv_rn(__fmul_rn(b.y, from), to));
+    }
+    return x;
+}
+
+// D (16 x 8, fp32) += A (16 x 16, f16) * B (16 x 8, f16), one warp.  With g = lane / 4, t = lane % 4:
+// a = rows g, g + 8, g, g + 8 at columns 2t (+1) and 2t + 8 (+1); b = rows 2t (+1) and 2t + 8 (+1) of
+// column g; d = rows g, g, g + 8, g + 8 at columns 2t, 2t + 1, 2t, 2t + 1.
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Asynchronous copies to shared memory; `ok` = false fills with zeros and reads nothing.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool ok) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, bool ok) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(ok ? 8 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool ok) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(ok ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+}  // namespace fa

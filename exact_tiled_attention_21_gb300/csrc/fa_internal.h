@@ -142,6 +142,86 @@ struct Fp8FwdLaunch {
     uint64_t timeout_ns;
 };
 
+struct RopeLaunch {
+    const void* x;        // bf16 [B, H, N, d], element strides xb, xh, xn, 1
+    void* y;              // the same with yb, yh, yn; may be x itself
+    long long xb, xh, xn, yb, yh, yn;
+    const int* positions; // int32 [B, N], or null (position n)
+    const uint64_t* turns;  // [rot / 2]
+    long long tokens;     // B * N
+    int H, N, d, rot, interleaved, inverse;
+    int hpt;              // heads per thread (set by the launch)
+    float magnitude;
+    int num_sms;
+};
+
+// Division of 0 <= n < 2^31 by a fixed d >= 1 (round-up multiplier: q = (mulhi(n, mul) + n) >> shift).
+struct FastDiv {
+    uint32_t d = 1, mul = 0, shift = 0;
+    FastDiv() = default;
+    explicit FastDiv(uint32_t v) : d(v) {
+        while ((1ull << shift) < v) ++shift;
+        mul = (uint32_t)(((1ull << 32) * ((1ull << shift) - v)) / v + 1);
+    }
+#ifdef __CUDACC__
+    __device__ __forceinline__ uint32_t div(uint32_t n) const { return (__umulhi(n, mul) + n) >> shift; }
+#endif
+};
+
+struct CacheAppendLaunch {
+    const void* k;        // bf16 [B, Hkv, N, d] by strides
+    const void* v;
+    long long kb, kh, kn, vb, vh, vn;
+    uint8_t* kp;          // e4m3 [num_pages, Hkv, page, d]
+    uint8_t* vp;
+    float* ks;            // fp32 [num_pages, Hkv, page / sb]
+    float* vs;
+    const int* table;     // int32 [B, max_pages]
+    const int* lens;      // int32 [B] tokens already in the cache
+    const int* new_lens;  // int32 [B], or null (N)
+    const int* positions; // int32 [B, N], or null (lens[b] + i)
+    const uint64_t* turns;  // [rot / 2], or null (no rotation)
+    int B, Hkv, N, d, rot, interleaved, page, sb, max_pages, num_pages;
+    float magnitude;
+    DevError* err;
+};
+
+struct CacheEvictLaunch {
+    uint8_t* kp;
+    uint8_t* vp;
+    float* ks;
+    float* vs;
+    const int* table;      // int32 [B, max_pages]: the pages to read
+    const int* lens;       // int32 [B]
+    const float* weights;  // fp32 [B, Hkv, max_pages * page]
+    const int* new_table;  // int32 [B, new_max_pages]: the pages to write
+    int* new_lens;         // int32 [B]
+    float* new_weights;    // fp32 [B, Hkv, new_max_pages * page]
+    int* kept;             // int32 [B, Hkv, new_max_pages * page]
+    int B, Hkv, page, sb, max_pages, new_max_pages, num_pages, d, keep, recent;
+    DevError* err;
+};
+
+struct PagedDecodeFp8Launch {
+    const void* q;         // bf16 [B, Hq, Nq, d]
+    const uint8_t* kp;     // e4m3 [num_pages, Hkv, page, d]
+    const uint8_t* vp;
+    const float* ks;       // fp32 [num_pages, Hkv, page / sb]
+    const float* vs;
+    const int* table;      // int32 [B, max_pages]
+    const int* lens;       // int32 [B]
+    void* o;               // bf16 [B, Hq, Nq, d]
+    float* lse;            // fp32 [B, Hq, Nq], or null
+    float* weights;        // fp32 [B, Hkv, max_pages * page], or null
+    float* part_o;         // fp32 [B*Hq*Nq, splits, d]
+    float* part_lse;       // fp32 [B*Hq*Nq, splits]
+    float* scores;         // fp32 [B*Hq*Nq, score_stride] (log2 units), with weights only
+    long long score_stride;
+    int B, Hq, Hkv, Nq, page, sb, max_pages, num_pages, d, splits;
+    float scale;
+    DevError* err;
+};
+
 // The dynamic shared-memory limit of kernel K, raised once per device: the
 // attribute stays with the function in the context, and setting it costs a
 // driver call per launch otherwise.
@@ -206,6 +286,13 @@ cudaError_t decode_split_blocks_per_sm(int d, int* blocks);  // resident CTAs of
 cudaError_t launch_decode_paged(const PagedDecodeLaunch& a, cudaStream_t s);
 cudaError_t launch_decode_paged_mma(const PagedDecodeLaunch& a, cudaStream_t s);
 cudaError_t launch_fwd_fp8(const Fp8FwdLaunch& a, cudaStream_t s);  // V^T copy, then the forward
+cudaError_t launch_rope(RopeLaunch a, cudaStream_t s);
+cudaError_t launch_cache_append(const CacheAppendLaunch& a, cudaStream_t s);
+cudaError_t launch_cache_evict(const CacheEvictLaunch& a, cudaStream_t s);  // choose the tokens, then move them
+cudaError_t launch_decode_paged_fp8(const PagedDecodeFp8Launch& a, cudaStream_t s);
+cudaError_t decode_fp8_blocks_per_sm(int d, int* blocks);  // resident CTAs of its split kernel on one SM
+// Keys that one CTA of the fp8 split kernel takes per step: its chunks are multiples of this.
+constexpr int kFp8ChunkKeys64 = 256, kFp8ChunkKeys128 = 128;
 // LSE-weighted merge of per-split partials into o (bf16) and lse (fp32, may be null).
 cudaError_t launch_decode_combine(const float* part_o, const float* part_lse, void* o, float* lse, int BH,
                                   int splits, int d, cudaStream_t s);

@@ -25,7 +25,8 @@ enum : int {
     kSiteQFull = 1, kSiteQEmpty, kSiteKvFull, kSiteKvEmpty, kSiteSFull, kSitePFull, kSiteOFinal,
     kSiteTeardown, kSiteBwdQFull, kSiteBwdQEmpty, kSiteBwdKvFull, kSiteBwdS, kSiteBwdP, kSiteBwdDP,
     kSiteBwdDS, kSiteBwdDQ, kSiteBwdDone, kSiteAlign, kSiteProbe, kSitePagedTable,
-    kSitePagedQ, kSitePagedKv, kSitePagedS, kSitePagedP, kSitePagedPv, kSitePagedO, kSiteSeqLen
+    kSitePagedQ, kSitePagedKv, kSitePagedS, kSitePagedP, kSitePagedPv, kSitePagedO, kSiteSeqLen, kSiteCacheTable,
+    kSiteCacheLen
 };
 
 constexpr int kErrTimeout = -6;
@@ -51,6 +52,16 @@ __device__ __forceinline__ void record_error(const WaitCtl& c, int code, int sit
         __threadfence();
     }
     *c.abort = 1;
+}
+
+// Records a device-side argument check that failed (kernels without waits).
+__device__ __forceinline__ void record_invalid(DevError* err, int site, int aux) {
+    if (atomicCAS(&err->code, 0, kErrInvalid) == 0) {
+        err->site = site;
+        err->block = (int)blockIdx.x;
+        err->aux = aux;
+        __threadfence();
+    }
 }
 
 // ------------------------------------------------------------------ smem / mbarrier

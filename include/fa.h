@@ -299,6 +299,127 @@ int fa_decode_paged(const void *q, const void *k_pages, const void *v_pages, con
                     int max_pages, int num_pages, int d, float scale, int num_splits, void *workspace,
                     size_t workspace_bytes, void *stream);
 
+/* ---- Rotary positions and a paged KV cache held in 8 bits -------------------
+ * A serving step with them: fa_rope on the queries, fa_cache_append_fp8 on the
+ * new keys (rotated on the way) and values, fa_decode_paged_fp8, and, when a
+ * sequence has outgrown its budget, fa_cache_evict_fp8.  (The cache stays in
+ * memory and is streamed: zimaspace.com "Wie reduziert Flash Attention ...",
+ * section "Weniger IO bedeutet nicht, dass der KV-Cache entfaellt"; 8 bits
+ * halve what is streamed.)
+ *
+ * The cache: k_pages, v_pages e4m3 bytes [num_pages, Hkv, page_size, d] (OCP
+ * FP8, no infinities); k_scale, v_scale fp32 [num_pages, Hkv, page_size /
+ * scale_block], one per block of scale_block consecutive tokens of a page and
+ * kv head, positive and finite.  An element stands for its e4m3 value times its
+ * block's scale.  scale_block divides page_size and is at most 128; any page
+ * size >= 1.  block_table int32 [B, max_pages]: physical page of each logical
+ * page; seq_lens int32 [B], 0 <= seq_lens[b] <= max_pages * page_size <= 2^30.
+ * Scales, tables, lengths, positions, lse and weights need 4-byte alignment
+ * only.  A length out of range is clamped, a page index outside [0, num_pages)
+ * is never dereferenced (reads give zeros, writes are left out); either is
+ * recorded as FA_ERR_INVALID_ARG in the device error word.  num_pages * Hkv *
+ * page_size must stay below 2^32 - 1 (FA_ERR_UNSUPPORTED). */
+
+/* Turns per position for fa_rope and fa_cache_append_fp8: turns[i] =
+ * inv_freq[i] / (2 pi) modulo whole turns, in units of 2^-64 turn.  inv_freq[i]
+ * (finite, host memory) is pair i's angle per position in radians; scalings for
+ * long contexts change these frequencies (and the magnitude below).  n >= 1.
+ * Host only; copy the n values to the device. */
+int fa_rope_table(const double *inv_freq, int n, uint64_t *turns);
+
+/* Rotary positions.  x and y: bf16 [B, H, N, d] with element strides (sb, sh,
+ * sn, 1), multiples of 8 (FA_ERR_ALIGNMENT) and >= 0; those of a dimension of
+ * size 1 are ignored.  y's elements must be distinct (FA_ERR_INVALID_ARG); y may
+ * be x with the same strides, but may not overlap it otherwise.  For token
+ * (b, n) at position p = positions[b * N + n] (int32 [B, N], any value; NULL: n)
+ * the pair i < rot / 2 turns by the angle a = p * inv_freq[i]:
+ *     y1 = magnitude (x1 cos a - x2 sin a),  y2 = magnitude (x2 cos a + x1 sin a)
+ * where the pair is columns (2i, 2i + 1) if interleaved, else (i, i + rot / 2);
+ * columns from rot on are copied.  inverse = 1 turns by -a with the same
+ * magnitude: the transpose, i.e. the gradient of x from the gradient of y.  The
+ * angle is reduced exactly at any position (see fa_rope_table); cos and sin are
+ * within 2^-20; computed in fp32, rounded to bf16 once.  rot: a multiple of 16
+ * (FA_ERR_UNSUPPORTED), 16 <= rot <= d; turns: device [rot / 2], 16-byte
+ * aligned; magnitude finite.  B * N <= 2^31 - 1, B * H <= 2^24. */
+int fa_rope(const void *x, void *y, long long x_sb, long long x_sh, long long x_sn, long long y_sb,
+            long long y_sh, long long y_sn, const int *positions, const uint64_t *turns, int B, int H, int N,
+            int d, int rot, int interleaved, float magnitude, int inverse, void *stream);
+
+/* Writes new tokens into the cache.  k, v: bf16 [B, Hkv, N, d] with strides as
+ * fa_rope's x.  Sequence b has seq_lens[b] tokens in the cache and gets its
+ * first n_b = new_lens[b] (0..N; NULL: N) tokens at seq_lens[b], seq_lens[b] + 1,
+ * ...; tokens that would not fit max_pages * page_size are left out and
+ * recorded.  seq_lens is not changed.  If turns is not NULL, K is rotated first
+ * as by fa_rope (same arguments; positions NULL: seq_lens[b] + i) and rounded
+ * to bf16: the result is, bit for bit, that of fa_rope followed by this call
+ * without turns.  With turns NULL, rot, interleaved, magnitude and positions
+ * are ignored.
+ * Scales: s = the smallest power of two >= 2^-126 with amax <= 448 s over the
+ * finite new elements of the block; if the block holds earlier tokens of the
+ * sequence, the larger of s and its present scale.  If that grows the scale, the
+ * block's earlier tokens are rescaled to it (exact unless they become
+ * subnormal).  Elements are rounded to nearest, infinities saturate at 448
+ * times the scale, NaN stays NaN.  Slots behind the new tokens keep their
+ * bytes.  No page may be written for two sequences at once. */
+int fa_cache_append_fp8(const void *k, const void *v, long long k_sb, long long k_sh, long long k_sn,
+                        long long v_sb, long long v_sh, long long v_sn, void *k_pages, void *v_pages,
+                        float *k_scale, float *v_scale, const int *block_table, const int *seq_lens,
+                        const int *new_lens, const int *positions, const uint64_t *turns, int B, int Hkv, int N,
+                        int d, int rot, int interleaved, float magnitude, int page_size, int scale_block,
+                        int max_pages, int num_pages, void *stream);
+
+/* Bytes of workspace fa_decode_paged_fp8 needs; max_tokens = max_pages *
+ * page_size, weights = 1 if it is given accumulated weights (which takes fp32
+ * scores of every query row and token besides the partials).  num_splits <= 0:
+ * for the most splits that the automatic choice takes (one per 128 tokens at
+ * d = 128, 256 at d = 64; at most 256, and 4096 divided by B * Hkv * ceil(Hq /
+ * Hkv * Nq / 16)).  Returns 0 for invalid sizes.  Host only, no device call. */
+size_t fa_decode_paged_fp8_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d, int max_tokens, int num_splits,
+                                           int weights);
+
+/* Attention of the last Nq (1..16) tokens of each sequence over the 8-bit
+ * cache, which holds them already: one token, or a few drafted ones.  q, o: bf16
+ * [B, Hq, Nq, d]; lse fp32 [B, Hq, Nq] or NULL.  Query head h reads kv head h /
+ * (Hq / Hkv); query t sees the tokens j <= seq_lens[b] - Nq + t (the bottom-right
+ * mask of fa_fwd).  A query that sees none (an empty sequence) gets O = 0,
+ * LSE = -inf.  Scores and sums are fp32; the softmax weights are rounded to fp16
+ * (relative 2^-11) for the value product only.
+ * weights fp32 [B, Hkv, max_pages * page_size] or NULL: weights[b, kvh, j] +=
+ * the sum of token j's attention weights over the group's heads and the Nq
+ * queries (what fa_cache_evict_fp8 selects by); tokens >= seq_lens[b] are left
+ * as they are.
+ * num_splits (<= 256) cuts each sequence into chunks of whole steps (128 tokens
+ * at d = 128, 256 at d = 64); <= 0 lets the library choose from the sizes.
+ * Results do not depend on the run (fixed order of additions).  Tokens past
+ * seq_lens[b] are never used.  A NaN in V reaches every query of its sequence and
+ * kv head, also those of the Nq that do not see its token.  workspace: 16-byte
+ * aligned, at least fa_decode_paged_fp8_workspace_bytes(...); contents do not
+ * matter; calls that may overlap need one each. */
+int fa_decode_paged_fp8(const void *q, const void *k_pages, const void *v_pages, const float *k_scale,
+                        const float *v_scale, const int *block_table, const int *seq_lens, void *o, float *lse,
+                        float *weights, int B, int Hq, int Hkv, int Nq, int page_size, int scale_block,
+                        int max_pages, int num_pages, int d, float scale, int num_splits, void *workspace,
+                        size_t workspace_bytes, void *stream);
+
+/* Eviction by accumulated attention weight: per sequence b and kv head, the
+ * min(seq_lens[b], keep) tokens that stay are the last `recent` (0..keep) and,
+ * of the others, the keep - recent with the largest weights[b, kvh, j]; of equal
+ * ones (+0 = -0) the lowest index, and NaN counts as largest.  A sequence of at
+ * most keep tokens keeps all.  The kept tokens are copied in order into the
+ * pages of new_table int32 [B, new_max_pages] (keep <= new_max_pages *
+ * page_size), from slot 0 on.  Those pages must be disjoint from every page that
+ * the call reads and from each other's; the source pages stay as they are (they
+ * may be shared), so a page can be freed by its owner afterwards.  A block's
+ * scale is the largest of its tokens' source scales; tokens of smaller scale
+ * are rescaled to it.  Outputs: new_lens int32 [B]; kept int32 and new_weights
+ * fp32 [B, Hkv, new_max_pages * page_size]: the source index of each kept token
+ * and its weight, then -1 and 0 (so new_weights goes on accumulating).  Rotation
+ * stays as it was applied: later tokens go on with their own positions. */
+int fa_cache_evict_fp8(void *k_pages, void *v_pages, float *k_scale, float *v_scale, const int *block_table,
+                       const int *seq_lens, const float *weights, const int *new_table, int *new_lens,
+                       float *new_weights, int *kept, int B, int Hkv, int page_size, int scale_block,
+                       int max_pages, int new_max_pages, int num_pages, int d, int keep, int recent, void *stream);
+
 /* Size of the scratch array that fa_decode_noalloc uses instead of a workspace. */
 #define FA_DECODE_NOALLOC_SCRATCH_BYTES ((size_t)16 << 20)
 

@@ -29,7 +29,10 @@ Modules:
 * ``twopass`` — O2: a separate C implementation (``twopass.c``), streaming key
   blocks in fp64 (pass 1: row max and row sum; pass 2: normalised weighted sum).
 
-Every function is pinned by ``tests/test_oracle_pins.py`` (closed forms,
+* ``cache``   — rotary positions and the paged 8-bit cache: append, attention,
+  eviction, token by token.  Pinned by ``tests/test_cache_oracle_pins.py``.
+
+Every other function is pinned by ``tests/test_oracle_pins.py`` (closed forms,
 invariants, a library routine, finite differences, hand-derived golden values).
 No function is "parity unpinned".
 """
