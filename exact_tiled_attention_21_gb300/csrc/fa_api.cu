@@ -796,16 +796,16 @@ int fp8_splits(long long items, long long max_tokens, long long step, long long 
     return (int)best;
 }
 
-int g_fp8_blocks[kMaxDevices][2] = {};  // resident CTAs per SM of the 8-bit split kernel, by device and d (64, 128)
+int g_fp8_blocks[kMaxDevices][2][2] = {};  // resident CTAs per SM of the 8-bit split kernel, by device, d and rows
 
-int fp8_resident(int d, int num_sms, long long* resident) {
+int fp8_resident(int d, bool one, int num_sms, long long* resident) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return FA_ERR_CUDA;
     std::lock_guard<std::mutex> lock(g_mu);
-    int& c = g_fp8_blocks[dev][d == 128 ? 1 : 0];
+    int& c = g_fp8_blocks[dev][d == 128 ? 1 : 0][one ? 1 : 0];
     if (!c) {
         int b = 0;
-        if (decode_fp8_blocks_per_sm(d, &b) != cudaSuccess || b < 1) return FA_ERR_CUDA;
+        if (decode_fp8_blocks_per_sm(d, one, &b) != cudaSuccess || b < 1) return FA_ERR_CUDA;
         c = b;
     }
     *resident = (long long)num_sms * c;
@@ -968,7 +968,7 @@ int fa_decode_paged_fp8(const void* q, const void* k_pages, const void* v_pages,
     const long long max_tokens = (long long)max_pages * page_size;
     if (num_splits <= 0) {
         long long resident = 0;
-        st = fp8_resident(d, num_sms, &resident);
+        st = fp8_resident(d, Hq / Hkv * Nq <= 8, num_sms, &resident);
         if (st != FA_OK) return st;
         num_splits = fp8_splits(fp8_items(B, Hq, Hkv, Nq), max_tokens, fp8_step(d), resident);
     }

@@ -4,19 +4,21 @@
 // Every byte of the cache is read once per 16 query rows (the Hq / Hkv heads of
 // a group times the new tokens), 2 d bytes per key for 4 d flops per row: bound
 // by HBM.  So each warp works alone.  It streams its own keys through a private
-// ring of cp.async copies, in which every lane copies exactly the bytes that it
-// will read as matrix fragments, so nothing waits for another warp until the
-// warps' results are merged at the end.  One CTA (4 warps) takes a chunk of one
+// ring of cp.async copies, so nothing waits for another warp until the warps'
+// results are merged at the end.  One CTA (4 warps) takes a chunk of one
 // (sequence, kv head, 16 rows).
 //
 // The products are mma.sync m16n8k16 with fp16 operands and fp32 sums, because
 // an e4m3 value is exact in fp16 and the fragments can be read straight from
-// the cache's rows: the order of d within Q K^T and of the keys within P V is
-// free, so a lane's 16 consecutive bytes of a K row are the k-indices of its B
-// fragments, and its 16 bytes of each of four V rows the k-pairs of its B
-// fragments for d / 8 columns.  tcgen05 would need the bytes widened and written
-// back to shared memory first (the queries are not 8 bits wide), and its 128
-// rows are eight times what there is.
+// the cache's rows.  Both are taken transposed, S^T = K Q^T and O^T = V^T P^T,
+// so that the keys (and d) fill the 16 rows of a product and the queries its 8
+// columns: up to 8 query rows cost half of what 16 do (NB = 1 or 2 column
+// tiles).  The order of d within K Q^T and of the keys within V^T P^T is free: a
+// lane's 16 consecutive bytes of a K row are the k-indices of its A fragments,
+// and its d / 8 bytes of each of four V rows the k-pairs of its A fragments.  P
+// turns from S^T's accumulators into the B fragments by an 8 x 8 transpose.
+// tcgen05 would need the bytes widened and written back to shared memory first
+// (the queries are not 8 bits wide), for 128-row products of at most 16 columns.
 //
 // q is scaled by a power of two per row into fp16's range (exact but for
 // elements 2^-28 below the row's largest).  With x_j the score in log2 units,
@@ -36,9 +38,9 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
 template <int D>
 struct Cfg {
     static constexpr int KEYS = D == 128 ? 32 : 64;     // keys per warp and step (8 KB of K and V)
-    static constexpr int STAGES = 3;                    // steps in flight
+    static constexpr int STAGES = 2;                    // steps in flight
     static constexpr int HALF = KEYS * D;               // bytes of K (and of V) per step
-    static constexpr int SLOT = 2 * HALF + 8 * KEYS;    // K, V, K scales, V scales
+    static constexpr int SLOT = 2 * HALF + 8 * KEYS;    // K, V, K scales, log2 of V scales
     static constexpr int RING = STAGES * SLOT;          // per warp
     static constexpr int OROW = D + 4;                  // row of the merge buffer, floats
     static constexpr int SMEM = kWarps * RING;
@@ -67,12 +69,12 @@ struct Params {
     DevError* err;
 };
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 2) decode_fp8_kernel(const Params a) {
+template <int D, int NB>
+__global__ void __launch_bounds__(kThreads, 3) decode_fp8_kernel(const Params a) {
     using C = Cfg<D>;
-    constexpr int KEYS = C::KEYS, NT = KEYS / 8, KS = D / 16, DT = D / 8;
+    constexpr int KEYS = C::KEYS, MT = KEYS / 16, KS = D / 16, DT = D / 8, ROWS = 8 * NB;
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ float s_stat[kWarps][3][16];
+    __shared__ float s_stat[kWarps][3][ROWS];
     pdl_launch_dependents();
     pdl_wait();
 
@@ -92,29 +94,138 @@ __global__ void __launch_bounds__(kThreads, 2) decode_fp8_kernel(const Params a)
     const int per = (len + a.splits - 1) / a.splits;
     const int chunk = (per + CHUNK - 1) / CHUNK * CHUNK;
     const int k0 = (int)min((long long)split * chunk, (long long)len), k1 = min(k0 + chunk, len);
+    const int r0 = rt * ROWS, nrows = min(ROWS, a.rows - r0);  // query rows of this tile
+    const long long row0 = ((long long)b * a.Hq + (long long)kvh * (a.Hq / a.Hkv)) * a.Nq + r0;
 
-    // rows of this tile, and the keys that each of this lane's two rows sees: j < lim
-    const int r0 = rt * 16, nrows = min(16, a.rows - r0);
-    const long long row0 = ((long long)b * a.Hq + (long long)kvh * (a.Hq / a.Hkv)) * a.Nq + r0;  // first row of the tile
-    const int lim_lo = min(k1, len - a.Nq + (r0 + g) % a.Nq + 1), lim_hi = min(k1, len - a.Nq + (r0 + g + 8) % a.Nq + 1);
+    // ---- the ring
+    uint8_t* ring = smem + warp * C::RING;
+    const uint32_t ring_u = smem_u32(ring);
+    const int* trow = a.table + (long long)b * a.max_pages;
+    const int first = k0 + warp * KEYS;                       // this warp's first key
+    const int steps = first < k1 ? (k1 - first + CHUNK - 1) / CHUNK : 0;
+    // A copy instruction moves whole rows (D / 16 lanes a row, so that a quarter warp asks for 128 consecutive bytes);
+    // the fragments' readers find their 16 bytes (V at D = 64: 8) at
+    //   K: (key / 8, half h of D = 128, lane' = 4 (key % 8) + t), lane' ^ 4 h
+    //   V: (key / 16, r, 32-byte slot 4 s + (t ^ s), rest of the column), s = column / 32, at D = 64 t ^ s ^ 2 (r % 2),
+    //   where key % 16 = 2 t + r % 2 + 8 (r / 2).
+    // The exclusive-ors keep both the copies and the reads free of bank conflicts.  A 32-byte sector of a row stays
+    // together: a copy whose sector is torn apart in shared memory fetches it from L2 once per piece (V in 16-byte
+    // pieces: 1.5 times the bytes in all, which bound the kernel at 58 us of a 128k-token, 8-head cache).
+    constexpr int LPR = D / 16, RPI = 32 / LPR;  // lanes per row, rows per copy instruction
+    const int cr = lane / LPR, cc = lane % LPR;
+    const uint8_t* kp = a.kp + cc * 16;
+    const uint8_t* vp = a.vp + cc * 16;
+    uint32_t kdst, vdst[2];  // this lane's slots (bytes) of the first copies
+    if constexpr (D == 128) {
+        kdst = ((cc >> 2) * 32 + ((4 * cr + (cc & 3)) ^ (cc & 4))) * 16;
+        vdst[0] = C::HALF + ((cr & 1) * 16 + 4 * (cc >> 1) + ((cr >> 1) ^ (cc >> 1))) * 32 + (cc & 1) * 16;
+        vdst[1] = vdst[0] ^ 64;  // t + 2
+    } else {
+        kdst = (4 * cr + cc) * 16;
+        vdst[0] = C::HALF + ((cr & 1) * 8 + 4 * (cc >> 1) + ((cr >> 1) ^ ((cc >> 1) | (cr & 1) << 1))) * 32 + (cc & 1) * 16;
+        vdst[1] = vdst[0] + 2 * 8 * 32;  // r + 2
+    }
+    bool bad = false;
+    using Keys = int[KEYS / 32];     // of lane's key (+ 32) of a step
+    using Scales = float[KEYS / 32];
+    auto fetch_pages = [&](int it, Keys& pg) {
+#pragma unroll
+        for (int i = 0; i < KEYS / 32; ++i) {
+            const int key = first + it * CHUNK + i * 32 + lane;
+            pg[i] = (it < steps && key < k1) ? trow[a.page.div(key)] : -1;
+        }
+    };
+    // Scales are loaded, not copied (a 4-byte copy asks L2 once per lane, a load once per sector), and put into the
+    // ring one step later, when they have arrived; V's as logarithms.
+    auto put_scales = [&](int slot, const Scales& ks, const Scales& vs) {
+        float* f = reinterpret_cast<float*>(ring + slot * C::SLOT + 2 * C::HALF) + lane;
+#pragma unroll
+        for (int i = 0; i < KEYS / 32; ++i) {
+            f[i * 32] = ks[i];
+            f[KEYS + i * 32] = lg2(vs[i]);
+        }
+    };
+    // ALL: every key of the step is there.
+    auto copy = [&](uint32_t base, const uint32_t (&row)[KEYS / 32], const bool ALL) {
+#pragma unroll
+        for (int n = 0; n < KEYS / RPI; ++n) {
+            const uint32_t rr = __shfl_sync(0xffffffffu, row[n * RPI / 32], (n * RPI + cr) & 31);
+            const bool ok = ALL || rr != ~0u;
+            const size_t off = (size_t)(ok ? rr : 0u) * D;
+            uint32_t ko, vo;  // slots of copy n
+            if constexpr (D == 128) {  // keys 4 n + cr
+                ko = ((n >> 1) * 64 + (n & 1) * 16) * 16;
+                vo = ((n >> 2) * 128 + ((n >> 1) & 1) * 64) * 16;
+            } else {                   // keys 8 n + cr
+                ko = n * 32 * 16;
+                vo = (n >> 1) * 64 * 16;
+            }
+            cp_async16(base + kdst + ko, kp + off, ok);
+            cp_async16(base + vdst[n & 1] + vo, vp + off, ok);
+        }
+    };
+    auto issue = [&](int it, int slot, const Keys& pages, Scales& ks, Scales& vs) {
+        if (it < steps) {
+            uint32_t row[KEYS / 32];  // cache row of key lane (+ 32), ~0 for none
+            bool all = true;
+#pragma unroll
+            for (int i = 0; i < KEYS / 32; ++i) {
+                const int key = first + it * CHUNK + i * 32 + lane;
+                const int pg = pages[i];
+                const bool in = key < k1, ok = in && (unsigned)pg < (unsigned)a.num_pages;
+                bad |= in && !ok;
+                all &= ok;
+                const uint32_t at = (uint32_t)key - a.page.div(key) * P;
+                const uint32_t head = (uint32_t)pg * a.Hkv + kvh;
+                row[i] = ok ? head * P + at : ~0u;
+                const uint32_t blk = ok ? head * a.blocks_per_page + a.sb.div(at) : 0u;
+                ks[i] = ok ? __ldg(a.ks + blk) : 0.f;
+                vs[i] = ok ? __ldg(a.vs + blk) : 0.f;
+            }
+            if (__all_sync(0xffffffffu, all))
+                copy(ring_u + slot * C::SLOT, row, true);
+            else
+                copy(ring_u + slot * C::SLOT, row, false);
+        }
+        cp_async_commit();
+    };
+    Keys pg_next;             // pages of the step after those in flight
+    Scales ks_next, vs_next;  // scales of the step issued last
+    {
+        Keys pg[C::STAGES];
+        Scales ks[C::STAGES], vs[C::STAGES];
+#pragma unroll
+        for (int s = 0; s < C::STAGES; ++s) fetch_pages(s, pg[s]);
+        fetch_pages(C::STAGES, pg_next);
+#pragma unroll
+        for (int s = 0; s < C::STAGES; ++s) {
+#pragma unroll
+            for (int i = 0; i < KEYS / 32; ++i) ks[s][i] = vs[s][i] = 0.f;
+            issue(s, s, pg[s], ks[s], vs[s]);
+        }
+#pragma unroll
+        for (int s = 0; s + 1 < C::STAGES; ++s) put_scales(s, ks[s], vs[s]);
+#pragma unroll
+        for (int i = 0; i < KEYS / 32; ++i) {
+            ks_next[i] = ks[C::STAGES - 1][i];
+            vs_next[i] = vs[C::STAGES - 1][i];
+        }
+    }
 
-    // ---- Q fragments: k-step s of lane t is columns (D = 128: 64 (s / 4) +) 16 t + 4 (s % 4) .. + 3
-    uint32_t qa[KS][4];
-    float sc_lo, sc_hi;
+    // ---- Q fragments: k-step s of lane (g, t) is row g, columns (D = 128: 64 (s / 4) +) 16 t + 4 (s % 4) .. + 3
+    uint32_t qb[NB][KS][2];
+    float sc[NB][2];  // score scale of the rows whose scores this lane holds: 8 nb + 2 t, + 1
+    int lim[NB][2];   // and the keys that they see: j < lim
 #pragma unroll
-    for (int hi = 0; hi < 2; ++hi) {
-        const int r = g + 8 * hi;
-        uint32_t w[D / 8];  // D / 4 columns per lane
-        if (r < nrows) {
-            const uint4* src = reinterpret_cast<const uint4*>(a.q + (row0 + r) * D + t * 16);
+    for (int nb = 0; nb < NB; ++nb) {
+        uint32_t w[D / 8];
+        if (nb * 8 + g < nrows) {
+            const uint4* src = reinterpret_cast<const uint4*>(a.q + (row0 + nb * 8 + g) * D + t * 16);
 #pragma unroll
-            for (int i = 0; i < D / 64; ++i)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const uint4 x = src[i * 8 + j];
-                    w[i * 8 + j * 4] = x.x, w[i * 8 + j * 4 + 1] = x.y, w[i * 8 + j * 4 + 2] = x.z,
-                                  w[i * 8 + j * 4 + 3] = x.w;
-                }
+            for (int i = 0; i < D / 32; ++i) {
+                const uint4 x = src[i / 2 * 8 + i % 2];
+                w[i * 4] = x.x, w[i * 4 + 1] = x.y, w[i * 4 + 2] = x.z, w[i * 4 + 3] = x.w;
+            }
         } else {
 #pragma unroll
             for (int i = 0; i < D / 8; ++i) w[i] = 0;
@@ -131,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_fp8_kernel(const Params a)
         if (big == 0.f || !(big <= 3.4e38f)) e = 0;
         e = max(e, -112);  // 2^-e stays a normal number
         const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-        (hi ? sc_hi : sc_lo) = a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);
+        const float up = a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);
 #pragma unroll
         for (int s = 0; s < KS; ++s)
 #pragma unroll
@@ -139,241 +250,210 @@ __global__ void __launch_bounds__(kThreads, 2) decode_fp8_kernel(const Params a)
                 const uint32_t x = w[s * 2 + j];
                 const __half2 h = __floats2half2_rn(__uint_as_float(x << 16) * down,
                                                     __uint_as_float(x & 0xFFFF0000u) * down);
-                qa[s][hi + 2 * j] = *reinterpret_cast<const uint32_t*>(&h);
+                qb[nb][s][j] = *reinterpret_cast<const uint32_t*>(&h);
             }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            sc[nb][j] = __shfl_sync(0xffffffffu, up, (2 * t + j) * 4);
+            lim[nb][j] = min(k1, len - a.Nq + (r0 + nb * 8 + 2 * t + j) % a.Nq + 1);
+        }
     }
 
-    // ---- the ring
-    uint8_t* ring = smem + warp * C::RING;
-    const uint32_t ring_u = smem_u32(ring);
-    const int* trow = a.table + (long long)b * a.max_pages;
-    const int first = k0 + warp * KEYS;                       // this warp's first key
-    const int steps = first < k1 ? (k1 - first + CHUNK - 1) / CHUNK : 0;
-    bool bad = false;
-    int pg_next[KEYS / 32];  // pages of the next step's keys (one step ahead of their use)
-    auto fetch_pages = [&](int it) {
+    float acc[D / 16][NB][4];
 #pragma unroll
-        for (int i = 0; i < KEYS / 32; ++i) {
-            const int key = first + it * CHUNK + i * 32 + lane;
-            pg_next[i] = (it < steps && key < k1) ? trow[a.page.div(key)] : -1;
-        }
-    };
-    auto issue = [&](int it, int slot) {
-        if (it < steps) {
-            const uint32_t base = ring_u + slot * C::SLOT;
-            uint32_t row[KEYS / 32];  // cache row of key lane (+ 32), ~0 for none
+    for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-            for (int i = 0; i < KEYS / 32; ++i) {
-                const int key = first + it * CHUNK + i * 32 + lane;
-                const int pg = pg_next[i];
-                const bool in = key < k1, ok = in && (unsigned)pg < (unsigned)a.num_pages;
-                bad |= in && !ok;
-                const uint32_t at = (uint32_t)key - a.page.div(key) * P;
-                const uint32_t head = (uint32_t)pg * a.Hkv + kvh;
-                row[i] = ok ? head * P + at : ~0u;
-                const uint32_t blk = ok ? head * a.blocks_per_page + a.sb.div(at) : 0u;
-                const uint32_t dst = base + 2 * C::HALF + (i * 32 + lane) * 4;
-                cp_async4(dst, a.ks + blk, ok);
-                cp_async4(dst + 4 * KEYS, a.vs + blk, ok);
-            }
-            fetch_pages(it + 1);
-            // K: lane (g, t) takes 16 bytes at 16 t (+ 64) of keys 8 j + g
+        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                const uint32_t rr = __shfl_sync(0xffffffffu, row[j / 4], (j % 4) * 8 + g);
-                const uint8_t* src = a.kp + (size_t)(rr == ~0u ? 0u : rr) * D + t * 16;
+            for (int c = 0; c < 4; ++c) acc[i][nb][c] = 0.f;
+    float m[NB][2], M[NB][2], l[NB][2];  // of rows 8 nb + 2 t + j
 #pragma unroll
-                for (int i = 0; i < D / 64; ++i)
-                    cp_async16(base + ((j * (D / 64) + i) * 32 + lane) * 16, src + i * 64, rr != ~0u);
-            }
-            // V: lane (g, t) takes d / 8 bytes at g d / 8 of keys 16 i + 2 t, + 1, + 8, + 9
+    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-            for (int i = 0; i < KEYS / 16; ++i)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const uint32_t rr =
-                        __shfl_sync(0xffffffffu, row[i / 2], (i % 2) * 16 + 2 * t + (r & 1) + (r >> 1) * 8);
-                    const uint8_t* src = a.vp + (size_t)(rr == ~0u ? 0u : rr) * D + g * DT;
-                    const uint32_t dst = base + C::HALF + ((i * 4 + r) * 32 + lane) * DT;
-                    if constexpr (D == 128)
-                        cp_async16(dst, src, rr != ~0u);
-                    else
-                        cp_async8(dst, src, rr != ~0u);
-                }
-        }
-        cp_async_commit();
-    };
+        for (int j = 0; j < 2; ++j) m[nb][j] = M[nb][j] = -INFINITY, l[nb][j] = 0.f;
 
-    float acc[DT][4];
-#pragma unroll
-    for (int j = 0; j < DT; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
-    float m_lo = -INFINITY, m_hi = -INFINITY, M_lo = -INFINITY, M_hi = -INFINITY, l_lo = 0.f, l_hi = 0.f;
-
-    fetch_pages(0);
-#pragma unroll
-    for (int s = 0; s < C::STAGES; ++s) issue(s, s);
     int slot = 0;
     for (int it = 0; it < steps; ++it) {
+        put_scales(slot == 0 ? C::STAGES - 1 : slot - 1, ks_next, vs_next);
         cp_async_wait<C::STAGES - 1>();
-        __syncwarp();  // the scales were copied by other lanes
+        __syncwarp();  // every lane's copies are there
         const uint8_t* st = ring + slot * C::SLOT;
         const int key0 = first + it * CHUNK;
-        float S[NT][4];
-        const uint4* kf = reinterpret_cast<const uint4*>(st) + lane;
+        float S[MT][NB][4];  // keys 16 i + g, + 8 (c / 2) of rows 8 nb + 2 t + c % 2
+        const uint4* kf = reinterpret_cast<const uint4*>(st);
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            S[j][0] = S[j][1] = S[j][2] = S[j][3] = 0.f;
+        for (int i = 0; i < MT; ++i) {
 #pragma unroll
-            for (int i = 0; i < D / 64; ++i) {
-                const uint4 x = kf[(j * (D / 64) + i) * 32];
-                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            for (int nb = 0; nb < NB; ++nb) S[i][nb][0] = S[i][nb][1] = S[i][nb][2] = S[i][nb][3] = 0.f;
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    mma_16816(S[j], qa[i * 4 + c], e4m3x2_to_half2(w[c]), e4m3x2_hi_to_half2(w[c]));
-            }
-        }
-        const float2* ksf = reinterpret_cast<const float2*>(st + 2 * C::HALF);
-        const float2* vsf = ksf + KEYS / 2;
+            for (int h = 0; h < D / 64; ++h) {
+                const int at = h * 32 + (lane ^ (4 * h));
+                const uint4 x = kf[2 * i * (D / 64) * 32 + at], y = kf[(2 * i + 1) * (D / 64) * 32 + at];
+                const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            const float2 k2 = ksf[j * 4 + t];
-            S[j][0] *= sc_lo * k2.x;
-            S[j][1] *= sc_lo * k2.y;
-            S[j][2] *= sc_hi * k2.x;
-            S[j][3] *= sc_hi * k2.y;
-        }
-        if (key0 + KEYS > min(k1, len - a.Nq + 1)) {  // some row does not see every key
+                for (int c = 0; c < 4; ++c) {
+                    const uint32_t ka[4] = {e4m3x2_to_half2(xw[c]), e4m3x2_to_half2(yw[c]), e4m3x2_hi_to_half2(xw[c]),
+                                            e4m3x2_hi_to_half2(yw[c])};
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                const int key = key0 + j * 8 + 2 * t;
-                if (key >= lim_lo) S[j][0] = -INFINITY;
-                if (key + 1 >= lim_lo) S[j][1] = -INFINITY;
-                if (key >= lim_hi) S[j][2] = -INFINITY;
-                if (key + 1 >= lim_hi) S[j][3] = -INFINITY;
-            }
-        }
-        if (a.scores) {  // score_stride is even and covers every key, so a pair fits
-            float* sr = a.scores + (row0 + g) * a.score_stride;
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                const int key = key0 + j * 8 + 2 * t;
-                if (key < k1) {
-                    if (g < nrows) *reinterpret_cast<float2*>(sr + key) = make_float2(S[j][0], S[j][1]);
-                    if (g + 8 < nrows)
-                        *reinterpret_cast<float2*>(sr + 8 * a.score_stride + key) = make_float2(S[j][2], S[j][3]);
+                    for (int nb = 0; nb < NB; ++nb) mma_16816(S[i][nb], ka, qb[nb][h * 4 + c][0], qb[nb][h * 4 + c][1]);
                 }
             }
         }
-        // ---- softmax: p = 2^(x - m) into l; w = 2^(x + log2 vs - M) for the value product
-        float mx_lo = -INFINITY, mx_hi = -INFINITY;
+        const float* ksf = reinterpret_cast<const float*>(st + 2 * C::HALF) + g;
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            mx_lo = fmax3(mx_lo, S[j][0], S[j][1]);
-            mx_hi = fmax3(mx_hi, S[j][2], S[j][3]);
-        }
-        mx_lo = fmaxf(mx_lo, __shfl_xor_sync(0xffffffffu, mx_lo, 1));
-        mx_hi = fmaxf(mx_hi, __shfl_xor_sync(0xffffffffu, mx_hi, 1));
-        mx_lo = fmaxf(mx_lo, __shfl_xor_sync(0xffffffffu, mx_lo, 2));
-        mx_hi = fmaxf(mx_hi, __shfl_xor_sync(0xffffffffu, mx_hi, 2));
-        const float mn_lo = fmaxf(m_lo, mx_lo), mn_hi = fmaxf(m_hi, mx_hi);
-        const float b_lo = mn_lo == -INFINITY ? 0.f : mn_lo, b_hi = mn_hi == -INFINITY ? 0.f : mn_hi;
-        l_lo *= ex2(m_lo - b_lo);
-        l_hi *= ex2(m_hi - b_hi);
-        m_lo = mn_lo;
-        m_hi = mn_hi;
-        float Mx_lo = -INFINITY, Mx_hi = -INFINITY;
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            const float2 v2 = vsf[j * 4 + t];
-            const float v0 = lg2(v2.x), v1 = lg2(v2.y);
-            l_lo += ex2(S[j][0] - b_lo) + ex2(S[j][1] - b_lo);
-            l_hi += ex2(S[j][2] - b_hi) + ex2(S[j][3] - b_hi);
-            S[j][0] += v0;
-            S[j][1] += v1;
-            S[j][2] += v0;
-            S[j][3] += v1;
-            Mx_lo = fmax3(Mx_lo, S[j][0], S[j][1]);
-            Mx_hi = fmax3(Mx_hi, S[j][2], S[j][3]);
-        }
-        Mx_lo = fmaxf(Mx_lo, __shfl_xor_sync(0xffffffffu, Mx_lo, 1));
-        Mx_hi = fmaxf(Mx_hi, __shfl_xor_sync(0xffffffffu, Mx_hi, 1));
-        Mx_lo = fmaxf(Mx_lo, __shfl_xor_sync(0xffffffffu, Mx_lo, 2));
-        Mx_hi = fmaxf(Mx_hi, __shfl_xor_sync(0xffffffffu, Mx_hi, 2));
-        if (__any_sync(0xffffffffu, Mx_lo > M_lo || Mx_hi > M_hi)) {
-            const float n_lo = fmaxf(M_lo, Mx_lo), n_hi = fmaxf(M_hi, Mx_hi);
-            const float f_lo = n_lo == -INFINITY ? 0.f : ex2(M_lo - n_lo), f_hi = n_hi == -INFINITY ? 0.f : ex2(M_hi - n_hi);
-            M_lo = n_lo;
-            M_hi = n_hi;
-#pragma unroll
-            for (int j = 0; j < DT; ++j) {
-                acc[j][0] *= f_lo;
-                acc[j][1] *= f_lo;
-                acc[j][2] *= f_hi;
-                acc[j][3] *= f_hi;
-            }
-        }
-        const float B_lo = M_lo == -INFINITY ? 0.f : M_lo, B_hi = M_hi == -INFINITY ? 0.f : M_hi;
-        const uint8_t* vf = st + C::HALF + lane * DT;
-#pragma unroll
-        for (int i = 0; i < KEYS / 16; ++i) {
-            uint32_t pa[4];
+        for (int i = 0; i < MT; ++i)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const float(&x)[4] = S[2 * i + h];
-                const __half2 lo = __floats2half2_rn(ex2(x[0] - B_lo), ex2(x[1] - B_lo));
-                const __half2 hi = __floats2half2_rn(ex2(x[2] - B_hi), ex2(x[3] - B_hi));
-                pa[2 * h] = *reinterpret_cast<const uint32_t*>(&lo);
-                pa[2 * h + 1] = *reinterpret_cast<const uint32_t*>(&hi);
+                const float kscale = ksf[i * 16 + h * 8];
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) {
+                    S[i][nb][2 * h] *= sc[nb][0] * kscale;
+                    S[i][nb][2 * h + 1] *= sc[nb][1] * kscale;
+                }
             }
+        if (key0 + KEYS > min(k1, len - a.Nq + 1)) {  // some row does not see every key
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        if (key0 + i * 16 + (c >> 1) * 8 + g >= lim[nb][c & 1]) S[i][nb][c] = -INFINITY;
+        }
+        if (a.scores) {
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    float* sr = a.scores + (row0 + nb * 8 + 2 * t + j) * a.score_stride + key0 + g;
+#pragma unroll
+                    for (int i = 0; i < MT; ++i)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            if (nb * 8 + 2 * t + j < nrows && key0 + i * 16 + h * 8 + g < k1)
+                                sr[i * 16 + h * 8] = S[i][nb][2 * h + j];
+                }
+        }
+        // ---- softmax: p = 2^(x - m) into l; w = 2^(x + log2 vs - M) for the value product
+        float base[NB][2];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float mx = m[nb][j];
+#pragma unroll
+                for (int i = 0; i < MT; ++i) mx = fmax3(mx, S[i][nb][j], S[i][nb][2 + j]);
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+                base[nb][j] = mx == -INFINITY ? 0.f : mx;
+                l[nb][j] *= ex2(m[nb][j] - base[nb][j]);
+                m[nb][j] = mx;
+            }
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float lv = ksf[KEYS + i * 16 + h * 8];
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        l[nb][j] += ex2(S[i][nb][2 * h + j] - base[nb][j]);
+                        S[i][nb][2 * h + j] += lv;
+                    }
+            }
+        float Mx[NB][2];
+        bool grown = false;
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float mx = M[nb][j];
+#pragma unroll
+                for (int i = 0; i < MT; ++i) mx = fmax3(mx, S[i][nb][j], S[i][nb][2 + j]);
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+                Mx[nb][j] = mx;
+                grown |= mx > M[nb][j];
+            }
+        if (__any_sync(0xffffffffu, grown)) {
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+                float f[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    f[j] = Mx[nb][j] == -INFINITY ? 0.f : ex2(M[nb][j] - Mx[nb][j]);
+                    M[nb][j] = Mx[nb][j];
+                }
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) acc[i][nb][c] *= f[c & 1];
+            }
+        }
+        uint32_t pb[MT][NB][2];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+            const float b0 = M[nb][0] == -INFINITY ? 0.f : M[nb][0], b1 = M[nb][1] == -INFINITY ? 0.f : M[nb][1];
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const __half2 w = __floats2half2_rn(ex2(S[i][nb][2 * h] - b0), ex2(S[i][nb][2 * h + 1] - b1));
+                    pb[i][nb][h] = transpose8x8(*reinterpret_cast<const uint32_t*>(&w));
+                }
+        }
+        const uint8_t* vf = st + C::HALF;
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
             uint32_t v[4][DT / 4];
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 if constexpr (D == 128) {
-                    const uint4 x = *reinterpret_cast<const uint4*>(vf + (i * 4 + r) * 32 * DT);
+                    const uint4 x = *reinterpret_cast<const uint4*>(vf + ((i * 4 + r) * 16 + 4 * (g >> 1) + (t ^ (g >> 1))) * 32 + (g & 1) * 16);
                     v[r][0] = x.x, v[r][1] = x.y, v[r][2] = x.z, v[r][3] = x.w;
                 } else {
-                    const uint2 x = *reinterpret_cast<const uint2*>(vf + (i * 4 + r) * 32 * DT);
+                    const uint2 x = *reinterpret_cast<const uint2*>(
+                        vf + ((i * 4 + r) * 8 + 4 * (g >> 2) + (t ^ ((g >> 2) | (r & 1) << 1))) * 32 + (g & 3) * 8);
                     v[r][0] = x.x, v[r][1] = x.y;
                 }
             }
 #pragma unroll
-            for (int c = 0; c < DT / 4; ++c) {
-                const uint32_t x0 = __byte_perm(v[0][c], v[1][c], 0x5140), y0 = __byte_perm(v[2][c], v[3][c], 0x5140);
-                const uint32_t x1 = __byte_perm(v[0][c], v[1][c], 0x7362), y1 = __byte_perm(v[2][c], v[3][c], 0x7362);
-                mma_16816(acc[4 * c], pa, e4m3x2_to_half2(x0), e4m3x2_to_half2(y0));
-                mma_16816(acc[4 * c + 1], pa, e4m3x2_hi_to_half2(x0), e4m3x2_hi_to_half2(y0));
-                mma_16816(acc[4 * c + 2], pa, e4m3x2_to_half2(x1), e4m3x2_to_half2(y1));
-                mma_16816(acc[4 * c + 3], pa, e4m3x2_hi_to_half2(x1), e4m3x2_hi_to_half2(y1));
-            }
+            for (int c = 0; c < DT / 4; ++c)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {  // columns g d / 8 + 4 c + 2 h (row g of the fragment) and + 1 (row g + 8)
+                    const uint32_t sel = h ? 0x7362u : 0x5140u;
+                    const uint32_t x = __byte_perm(v[0][c], v[1][c], sel), y = __byte_perm(v[2][c], v[3][c], sel);
+                    const uint32_t va[4] = {e4m3x2_to_half2(x), e4m3x2_hi_to_half2(x), e4m3x2_to_half2(y),
+                                            e4m3x2_hi_to_half2(y)};
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb) mma_16816(acc[2 * c + h][nb], va, pb[i][nb][0], pb[i][nb][1]);
+                }
         }
-        __syncwarp();  // every lane has read the scales of this slot
-        issue(it + C::STAGES, slot);
+        __syncwarp();  // every lane has read this slot
+        issue(it + C::STAGES, slot, pg_next, ks_next, vs_next);
+        fetch_pages(it + C::STAGES + 1, pg_next);
         slot = slot + 1 == C::STAGES ? 0 : slot + 1;
     }
     cp_async_wait<0>();
     if (__any_sync(0xffffffffu, bad) && lane == 0) record_invalid(a.err, kSiteCacheTable, -1);
 
     // ---- merge the warps: O = sum_w O_w 2^(M_w - m) / l
-    l_lo += __shfl_xor_sync(0xffffffffu, l_lo, 1);
-    l_hi += __shfl_xor_sync(0xffffffffu, l_hi, 1);
-    l_lo += __shfl_xor_sync(0xffffffffu, l_lo, 2);
-    l_hi += __shfl_xor_sync(0xffffffffu, l_hi, 2);
     __syncwarp();
-    if (t == 0) {
-        s_stat[warp][0][g] = m_lo, s_stat[warp][0][g + 8] = m_hi;
-        s_stat[warp][1][g] = l_lo, s_stat[warp][1][g + 8] = l_hi;
-        s_stat[warp][2][g] = M_lo, s_stat[warp][2][g + 8] = M_hi;
-    }
     float* mine = reinterpret_cast<float*>(ring);
 #pragma unroll
-    for (int j = 0; j < DT; ++j) {
-        mine[g * C::OROW + 2 * t * DT + j] = acc[j][0];
-        mine[g * C::OROW + (2 * t + 1) * DT + j] = acc[j][1];
-        mine[(g + 8) * C::OROW + 2 * t * DT + j] = acc[j][2];
-        mine[(g + 8) * C::OROW + (2 * t + 1) * DT + j] = acc[j][3];
-    }
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int r = nb * 8 + 2 * t + j;
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) l[nb][j] += __shfl_xor_sync(0xffffffffu, l[nb][j], d);
+            if (g == 0) s_stat[warp][0][r] = m[nb][j], s_stat[warp][1][r] = l[nb][j], s_stat[warp][2][r] = M[nb][j];
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+                *reinterpret_cast<float2*>(mine + r * C::OROW + g * DT + 2 * i) =
+                    make_float2(acc[i][nb][j], acc[i][nb][2 + j]);
+        }
     __syncthreads();
     for (int i = tid; i < nrows * (D / 4); i += kThreads) {
         const int r = i / (D / 4), c = (i % (D / 4)) * 4;
@@ -503,10 +583,10 @@ __global__ void __launch_bounds__(kWeightThreads) weights_fp8_kernel(const float
     if (j + 3 < len) w[3] += sum.w;
 }
 
-template <int D>
+template <int D, int NB>
 cudaError_t launch_d(const PagedDecodeFp8Launch& a, cudaStream_t s) {
     using C = Cfg<D>;
-    cudaError_t e = set_smem_limit_once<decode_fp8_kernel<D>>(C::SMEM);
+    cudaError_t e = set_smem_limit_once<decode_fp8_kernel<D, NB>>(C::SMEM);
     if (e != cudaSuccess) return e;
     Params p;
     p.q = (const __nv_bfloat16*)a.q;
@@ -529,7 +609,7 @@ cudaError_t launch_d(const PagedDecodeFp8Launch& a, cudaStream_t s) {
     p.num_pages = a.num_pages;
     p.splits = a.splits;
     p.rows = a.Hq / a.Hkv * a.Nq;
-    p.row_tiles = (p.rows + 15) / 16;
+    p.row_tiles = (p.rows + 8 * NB - 1) / (8 * NB);
     p.blocks_per_page = (uint32_t)(a.page / a.sb);
     p.page = FastDiv((uint32_t)a.page);
     p.sb = FastDiv((uint32_t)a.sb);
@@ -537,7 +617,7 @@ cudaError_t launch_d(const PagedDecodeFp8Launch& a, cudaStream_t s) {
     p.err = a.err;
     const long long ctas = (long long)a.B * a.Hkv * a.splits * p.row_tiles;
     if (ctas > 0x7FFFFFFFll) return cudaErrorInvalidValue;
-    e = launch_dependent(decode_fp8_kernel<D>, dim3((unsigned)ctas), dim3(kThreads), C::SMEM, s, p);
+    e = launch_dependent(decode_fp8_kernel<D, NB>, dim3((unsigned)ctas), dim3(kThreads), C::SMEM, s, p);
     if (e != cudaSuccess) return e;
     const long long rows = (long long)a.B * a.Hq * a.Nq;
     if (a.splits > 1) {
@@ -556,15 +636,21 @@ cudaError_t launch_d(const PagedDecodeFp8Launch& a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_decode_paged_fp8(const PagedDecodeFp8Launch& a, cudaStream_t s) {
-    return a.d == 128 ? launch_d<128>(a, s) : launch_d<64>(a, s);
+    const bool one = a.Hq / a.Hkv * a.Nq <= 8;
+    if (a.d == 128) return one ? launch_d<128, 1>(a, s) : launch_d<128, 2>(a, s);
+    return one ? launch_d<64, 1>(a, s) : launch_d<64, 2>(a, s);
 }
 
-cudaError_t decode_fp8_blocks_per_sm(int d, int* blocks) {
-    cudaError_t e = d == 128 ? set_smem_limit_once<decode_fp8_kernel<128>>(Cfg<128>::SMEM)
-                             : set_smem_limit_once<decode_fp8_kernel<64>>(Cfg<64>::SMEM);
+template <int D, int NB>
+static cudaError_t blocks_per_sm(int* blocks) {
+    const cudaError_t e = set_smem_limit_once<decode_fp8_kernel<D, NB>>(Cfg<D>::SMEM);
     if (e != cudaSuccess) return e;
-    return d == 128 ? cudaOccupancyMaxActiveBlocksPerMultiprocessor(blocks, decode_fp8_kernel<128>, kThreads, Cfg<128>::SMEM)
-                    : cudaOccupancyMaxActiveBlocksPerMultiprocessor(blocks, decode_fp8_kernel<64>, kThreads, Cfg<64>::SMEM);
+    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(blocks, decode_fp8_kernel<D, NB>, kThreads, Cfg<D>::SMEM);
+}
+
+cudaError_t decode_fp8_blocks_per_sm(int d, bool one, int* blocks) {
+    if (d == 128) return one ? blocks_per_sm<128, 1>(blocks) : blocks_per_sm<128, 2>(blocks);
+    return one ? blocks_per_sm<64, 1>(blocks) : blocks_per_sm<64, 2>(blocks);
 }
 
 }  // namespace fa

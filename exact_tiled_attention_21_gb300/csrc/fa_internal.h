@@ -290,7 +290,8 @@ cudaError_t launch_rope(RopeLaunch a, cudaStream_t s);
 cudaError_t launch_cache_append(const CacheAppendLaunch& a, cudaStream_t s);
 cudaError_t launch_cache_evict(const CacheEvictLaunch& a, cudaStream_t s);  // choose the tokens, then move them
 cudaError_t launch_decode_paged_fp8(const PagedDecodeFp8Launch& a, cudaStream_t s);
-cudaError_t decode_fp8_blocks_per_sm(int d, int* blocks);  // resident CTAs of its split kernel on one SM
+// Resident CTAs on one SM of its split kernel for 1..8 query rows per kv head (one) or more.
+cudaError_t decode_fp8_blocks_per_sm(int d, bool one, int* blocks);
 // Keys that one CTA of the fp8 split kernel takes per step: its chunks are multiples of this.
 constexpr int kFp8ChunkKeys64 = 256, kFp8ChunkKeys128 = 128;
 // LSE-weighted merge of per-split partials into o (bf16) and lse (fp32, may be null).

@@ -11,18 +11,21 @@
 
 namespace fa {
 
-// cos and sin of a fraction of a turn, times mag.  The top 32 bits, as a signed
-// fraction in [-1/2, 1/2), lose at most 2^-25 turn in the fp32 conversion; the
-// hardware sine and cosine are within 2^-20.5 on [-pi, pi].  Both are far below
-// the half step of the bf16 result (2^-9), and cost 1/5 of the library pair.
+// cos and sin of a fraction of a turn, times mag: the nearest quarter turn
+// comes off in integers, which leaves an angle of at most pi / 4 exactly (to
+// 2^-32 turn), where the Taylor polynomials to x^9 and x^10 are within 2^-29.
+// Each result is within 2^-22; the hardware's sine and cosine (2^-20.5) flip
+// enough bf16 roundings to show in the cache's bytes.
 __device__ __forceinline__ void turn_cos_sin(int pos, uint64_t turns, float mag, float& c, float& s) {
-    const uint64_t t = (uint64_t)(int64_t)pos * turns;
-    const float a = (float)(int32_t)(uint32_t)(t >> 32) * 1.4629180792671596e-09f;  // 2 pi / 2^32
-    float cc, ss;
-    asm("cos.approx.ftz.f32 %0, %1;" : "=f"(cc) : "f"(a));
-    asm("sin.approx.ftz.f32 %0, %1;" : "=f"(ss) : "f"(a));
-    c = cc * mag;
-    s = ss * mag;
+    const uint32_t t = (uint32_t)(((uint64_t)(int64_t)pos * turns) >> 32);
+    const uint32_t q = (t + 0x20000000u) >> 30;
+    const float a = (float)(int32_t)(t - (q << 30)) * 1.4629180792671596e-09f;  // 2 pi / 2^32
+    const float z = a * a;
+    const float sn = fmaf(a * z, fmaf(z, fmaf(z, fmaf(z, 1.f / 362880.f, -1.f / 5040.f), 1.f / 120.f), -1.f / 6.f), a);
+    const float cs = fmaf(z, fmaf(z, fmaf(z, fmaf(z, fmaf(z, -1.f / 3628800.f, 1.f / 40320.f), -1.f / 720.f), 1.f / 24.f),
+                                  -0.5f), 1.f);
+    c = __uint_as_float(__float_as_uint((q & 1) ? sn : cs) ^ (((q + 1) & 2) << 30)) * mag;
+    s = __uint_as_float(__float_as_uint((q & 1) ? cs : sn) ^ ((q & 2) << 30)) * mag;
 }
 
 // The same for the eight pairs of one task (turns: 16-byte aligned).
