@@ -104,9 +104,9 @@ def load():
     lib.fa_rope.restype = i
     lib.fa_cache_append_fp8.argtypes = [vp, vp] + [ll] * 6 + [vp] * 9 + [i] * 6 + [f] + [i] * 4 + [vp]
     lib.fa_cache_append_fp8.restype = i
-    lib.fa_decode_paged_fp8_workspace_bytes.argtypes = [i] * 8
+    lib.fa_decode_paged_fp8_workspace_bytes.argtypes = [i] * 7
     lib.fa_decode_paged_fp8_workspace_bytes.restype = sz
-    lib.fa_decode_paged_fp8.argtypes = [vp] * 10 + [i] * 9 + [f, i, vp, sz, vp]
+    lib.fa_decode_paged_fp8.argtypes = [vp] * 10 + [i] * 9 + [f, vp, sz, vp]
     lib.fa_decode_paged_fp8.restype = i
     lib.fa_cache_evict_fp8.argtypes = [vp] * 11 + [i] * 10 + [vp]
     lib.fa_cache_evict_fp8.restype = i
@@ -410,19 +410,17 @@ def fa_cache_append_fp8(k, v, k_strides, v_strides, k_pages, v_pages, k_scale, v
                                       num_pages, _stream(stream)), "fa_cache_append_fp8")
 
 
-def fa_decode_paged_fp8_workspace_bytes(B, Hq, Hkv, Nq, d, max_tokens, num_splits, weights):
-    return load().fa_decode_paged_fp8_workspace_bytes(B, Hq, Hkv, Nq, d, max_tokens, int(num_splits),
-                                                      int(bool(weights)))
+def fa_decode_paged_fp8_workspace_bytes(B, Hq, Hkv, Nq, d, max_tokens, weights):
+    return load().fa_decode_paged_fp8_workspace_bytes(B, Hq, Hkv, Nq, d, max_tokens, int(bool(weights)))
 
 
 def fa_decode_paged_fp8(q, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, o, lse, weights, B, Hq, Hkv,
-                        Nq, page_size, scale_block, max_pages, num_pages, d, scale, num_splits, workspace,
-                        workspace_bytes, stream=None):
+                        Nq, page_size, scale_block, max_pages, num_pages, d, scale, workspace, workspace_bytes,
+                        stream=None):
     _raise(load().fa_decode_paged_fp8(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale),
                                       _ptr(block_table), _ptr(seq_lens), _ptr(o), _ptr(lse), _ptr(weights), B, Hq,
                                       Hkv, Nq, page_size, scale_block, max_pages, num_pages, d, float(scale),
-                                      int(num_splits), _ptr(workspace), int(workspace_bytes), _stream(stream)),
-           "fa_decode_paged_fp8")
+                                      _ptr(workspace), int(workspace_bytes), _stream(stream)), "fa_decode_paged_fp8")
 
 
 def fa_cache_evict_fp8(k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, weights, new_table, new_lens,
@@ -676,7 +674,7 @@ def cache_append_fp8(k, v, k_pages, v_pages, k_scale, v_scale, block_table, seq_
 
 
 def decode_paged_fp8(q, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, scale=None, weights=None,
-                     num_splits=0, stream=None, workspace=None):
+                     stream=None, workspace=None):
     """O [B,Hq,Nq,d] bf16 and LSE [B,Hq,Nq] fp32 of the last Nq tokens (q [B,Hq,Nq,d], or [B,Hq,d] for one, which
     gives O [B,Hq,d] and LSE [B,Hq]) over the paged 8-bit cache, which holds them already.  weights: fp32
     [B,Hkv,max_pages*page] to which every token's attention weight is added, or None."""
@@ -685,7 +683,7 @@ def decode_paged_fp8(q, k_pages, v_pages, k_scale, v_scale, block_table, seq_len
     if not _here(index, stream):
         with _Launching(index, stream):
             return decode_paged_fp8(q, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, scale, weights,
-                                    num_splits, None, workspace)
+                                    None, workspace)
     shape = q.shape
     _need(len(shape) in (3, 4), "q must have 3 or 4 dimensions")
     Hq, Nq = shape[1], (shape[2] if len(shape) == 4 else 1)
@@ -693,8 +691,7 @@ def decode_paged_fp8(q, k_pages, v_pages, k_scale, v_scale, block_table, seq_len
     wp = None if weights is None else _on(weights, "weights", torch.float32, (B, Hkv, max_pages * page), index)
     lib, device = load(), q.device
     if workspace is None:
-        nbytes = lib.fa_decode_paged_fp8_workspace_bytes(B, Hq, Hkv, Nq, d, max_pages * page, num_splits,
-                                                         weights is not None)
+        nbytes = lib.fa_decode_paged_fp8_workspace_bytes(B, Hq, Hkv, Nq, d, max_pages * page, weights is not None)
         workspace = torch.empty((nbytes,), dtype=torch.uint8, device=device)
     else:
         nbytes = workspace.numel() * workspace.element_size()
@@ -702,7 +699,7 @@ def decode_paged_fp8(q, k_pages, v_pages, k_scale, v_scale, block_table, seq_len
     o = torch.empty(shape, dtype=torch.bfloat16, device=device)
     lse = torch.empty(shape[:-1], dtype=torch.float32, device=device)
     _raise(lib.fa_decode_paged_fp8(qp, *ptrs, o.data_ptr(), lse.data_ptr(), wp, B, Hq, Hkv, Nq, page, sb, max_pages,
-                                   num_pages, d, d ** -0.5 if scale is None else scale, num_splits,
+                                   num_pages, d, d ** -0.5 if scale is None else scale,
                                    workspace.data_ptr(), nbytes, _raw_stream(index)), "fa_decode_paged_fp8")
     return o, lse
 

@@ -771,62 +771,40 @@ int check_cache(int B, int Hkv, int page, int sb, int max_pages, int num_pages, 
     return FA_OK;
 }
 
-// The most splits that the automatic choice of the 8-bit decode takes: one per step (keys that a CTA takes at a time),
-// 256, and 4096 CTAs in all, which bounds the workspace.  items: CTAs per split.
-int fp8_most_splits(long long items, long long max_tokens, long long step) {
-    return (int)std::max<long long>(1, std::min({256ll, (max_tokens + step - 1) / step, 4096 / items}));
-}
-int fp8_step(int d) { return d == 128 ? kFp8ChunkKeys128 : kFp8ChunkKeys64; }
-long long fp8_items(int B, int Hq, int Hkv, int Nq) { return (long long)B * Hkv * (((long long)(Hq / Hkv) * Nq + 15) / 16); }
+int g_fp8_blocks[kMaxDevices][2][3] = {};  // resident CTAs per SM of the 8-bit decode, by device, d and tile rows
 
-// Automatic splits.  `resident` CTAs run at once: a launch costs about waves * (steps per chunk + a fixed cost of about
-// two steps), and the merge reads every split, so the fewest splits of the cheapest count are taken.
-int fp8_splits(long long items, long long max_tokens, long long step, long long resident) {
-    const long long most = fp8_most_splits(items, max_tokens, step);
-    long long best = 1, best_cost = LLONG_MAX;
-    for (long long sp = 1; sp <= most; ++sp) {
-        const long long per = (max_tokens + sp - 1) / sp, steps = (per + step - 1) / step;
-        const long long waves = (items * sp + resident - 1) / resident;
-        const long long cost = waves * (steps + 2) * 64 + sp;
-        if (cost < best_cost) {
-            best_cost = cost;
-            best = sp;
-        }
-    }
-    return (int)best;
-}
+constexpr int kFp8MostWorkers = 1024;  // bounds the workspace; three CTAs on each of 152 SMs are 456
 
-int g_fp8_blocks[kMaxDevices][2][2] = {};  // resident CTAs per SM of the 8-bit split kernel, by device, d and rows
-
-int fp8_resident(int d, bool one, int num_sms, long long* resident) {
+// CTAs that the 8-bit decode shares its steps among: as many as run at once.
+int fp8_workers(int d, int tile, int num_sms, int* workers) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return FA_ERR_CUDA;
     std::lock_guard<std::mutex> lock(g_mu);
-    int& c = g_fp8_blocks[dev][d == 128 ? 1 : 0][one ? 1 : 0];
+    int& c = g_fp8_blocks[dev][d == 128 ? 1 : 0][tile == 8 ? 0 : tile == 16 ? 1 : 2];
     if (!c) {
         int b = 0;
-        if (decode_fp8_blocks_per_sm(d, one, &b) != cudaSuccess || b < 1) return FA_ERR_CUDA;
+        if (decode_fp8_blocks_per_sm(d, tile, &b) != cudaSuccess || b < 1) return FA_ERR_CUDA;
         c = b;
     }
-    *resident = (long long)num_sms * c;
+    *workers = std::min(kFp8MostWorkers, num_sms * c);
     return FA_OK;
 }
 
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
-// Workspace of the 8-bit decode: partial outputs, partial LSEs, and with weights the scores, whose rows are padded
-// to a multiple of four keys.
+// Workspace of the 8-bit decode: partial outputs and LSEs of every segment (at most one more per worker than there are
+// items), the sequences' first steps, and with weights the scores of every row and token.
 struct Fp8Workspace {
-    size_t part_lse, scores, bytes;
-    long long score_stride;
+    size_t part_lse, prefix, scores, bytes;
 };
-Fp8Workspace fp8_workspace(int B, int Hq, int Nq, int d, long long max_tokens, int splits, bool weights) {
+Fp8Workspace fp8_workspace(int B, int Hq, int Hkv, int Nq, int d, long long max_tokens, bool weights) {
+    const int rows = Hq / Hkv * Nq, tile = fp8_tile_rows(rows);
+    const size_t slots = (size_t)kFp8MostWorkers + (size_t)B * Hkv * ((rows + tile - 1) / tile);
     Fp8Workspace w;
-    const size_t rows = (size_t)B * Hq * Nq;
-    w.part_lse = splits > 1 ? align256(rows * splits * d * 4) : 0;
-    w.scores = w.part_lse + align256(rows * splits * 4);
-    w.score_stride = (max_tokens + 3) & ~3ll;
-    w.bytes = w.scores + (weights ? align256(rows * (size_t)w.score_stride * 4) : 0);
+    w.part_lse = align256(slots * tile * d * 4);
+    w.prefix = w.part_lse + align256(slots * tile * 4);
+    w.scores = w.prefix + align256(((size_t)B + 1) * 8);
+    w.bytes = w.scores + (weights ? align256((size_t)B * Hkv * ((rows + 3) & ~3) * (size_t)max_tokens * 4) : 0);
     return w;
 }
 
@@ -939,21 +917,18 @@ int fa_cache_append_fp8(const void* k, const void* v, long long k_sb, long long 
     return launched(launch_cache_append(a, (cudaStream_t)stream));
 }
 
-size_t fa_decode_paged_fp8_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d, int max_tokens, int num_splits,
-                                           int weights) {
-    if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || Nq < 1 || Nq > 16 || (d != 64 && d != 128) || max_tokens < 1 || num_splits > 256) return 0;
+size_t fa_decode_paged_fp8_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d, int max_tokens, int weights) {
+    if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || Nq < 1 || Nq > 16 || (d != 64 && d != 128) || max_tokens < 1) return 0;
     if (max_tokens > kMaxCacheTokens || (long long)B * Hq > (1ll << 24) || (weights != 0 && weights != 1)) return 0;
-    const int splits = num_splits > 0 ? num_splits : fp8_most_splits(fp8_items(B, Hq, Hkv, Nq), max_tokens, fp8_step(d));
-    return std::max<size_t>(256, fp8_workspace(B, Hq, Nq, d, max_tokens, splits, weights != 0).bytes);
+    return fp8_workspace(B, Hq, Hkv, Nq, d, max_tokens, weights != 0).bytes;
 }
 
 int fa_decode_paged_fp8(const void* q, const void* k_pages, const void* v_pages, const float* k_scale,
                         const float* v_scale, const int* block_table, const int* seq_lens, void* o, float* lse,
                         float* weights, int B, int Hq, int Hkv, int Nq, int page_size, int scale_block, int max_pages,
-                        int num_pages, int d, float scale, int num_splits, void* workspace, size_t workspace_bytes,
-                        void* stream) {
+                        int num_pages, int d, float scale, void* workspace, size_t workspace_bytes, void* stream) {
     if (!q || !k_pages || !v_pages || !k_scale || !v_scale || !block_table || !seq_lens || !o) return FA_ERR_INVALID_ARG;
-    if (!scale_ok(scale) || num_splits > 256 || Hq < 1 || Nq < 1) return FA_ERR_INVALID_ARG;
+    if (!scale_ok(scale) || Hq < 1 || Nq < 1) return FA_ERR_INVALID_ARG;
     int st = check_cache(B, Hkv, page_size, scale_block, max_pages, num_pages, d);
     if (st != FA_OK) return st;
     if (Hq % Hkv) return FA_ERR_INVALID_ARG;
@@ -965,14 +940,9 @@ int fa_decode_paged_fp8(const void* q, const void* k_pages, const void* v_pages,
     int num_sms = 0;
     st = device_state(&a.err, &num_sms);
     if (st != FA_OK) return st;
-    const long long max_tokens = (long long)max_pages * page_size;
-    if (num_splits <= 0) {
-        long long resident = 0;
-        st = fp8_resident(d, Hq / Hkv * Nq <= 8, num_sms, &resident);
-        if (st != FA_OK) return st;
-        num_splits = fp8_splits(fp8_items(B, Hq, Hkv, Nq), max_tokens, fp8_step(d), resident);
-    }
-    const Fp8Workspace ws = fp8_workspace(B, Hq, Nq, d, max_tokens, num_splits, weights != nullptr);
+    st = fp8_workers(d, fp8_tile_rows(Hq / Hkv * Nq), num_sms, &a.workers);
+    if (st != FA_OK) return st;
+    const Fp8Workspace ws = fp8_workspace(B, Hq, Hkv, Nq, d, (long long)max_pages * page_size, weights != nullptr);
     if (!workspace || workspace_bytes < ws.bytes) return FA_ERR_WORKSPACE;
     if (!aligned16(workspace)) return FA_ERR_ALIGNMENT;
     char* base = static_cast<char*>(workspace);
@@ -989,7 +959,7 @@ int fa_decode_paged_fp8(const void* q, const void* k_pages, const void* v_pages,
     a.part_o = reinterpret_cast<float*>(base);
     a.part_lse = reinterpret_cast<float*>(base + ws.part_lse);
     a.scores = reinterpret_cast<float*>(base + ws.scores);
-    a.score_stride = ws.score_stride;
+    a.prefix = reinterpret_cast<long long*>(base + ws.prefix);
     a.B = B;
     a.Hq = Hq;
     a.Hkv = Hkv;
@@ -999,7 +969,6 @@ int fa_decode_paged_fp8(const void* q, const void* k_pages, const void* v_pages,
     a.max_pages = max_pages;
     a.num_pages = num_pages;
     a.d = d;
-    a.splits = num_splits;
     a.scale = scale;
     return launched(launch_decode_paged_fp8(a, (cudaStream_t)stream));
 }

@@ -1,24 +1,32 @@
 // Attention of 1..16 new tokens per sequence over a paged cache held in 8 bits
 // (e4m3 with one fp32 scale per block of sb tokens and kv head).
 //
-// Every byte of the cache is read once per 16 query rows (the Hq / Hkv heads of
+// Every byte of the cache is read once per 32 query rows (the Hq / Hkv heads of
 // a group times the new tokens), 2 d bytes per key for 4 d flops per row: bound
-// by HBM.  So each warp works alone.  It streams its own keys through a private
-// ring of cp.async copies, so nothing waits for another warp until the warps'
-// results are merged at the end.  One CTA (4 warps) takes a chunk of one
-// (sequence, kv head, 16 rows).
+// by HBM.  So each warp works alone: it streams its own keys through a private
+// ring of cp.async copies, and nothing waits for another warp until the four
+// warps' results of a CTA are merged.
+//
+// The work is one list of steps (128 keys at d = 128, 256 at d = 64) over all
+// sequences, kv heads and row tiles, cut into equal shares for as many CTAs as
+// run at once, from the lengths on the device: any batch of lengths, and any
+// capacity of the block table, keeps every SM busy to the end.  A CTA's share
+// crosses from one (sequence, kv head, row tile) to the next as it comes; the
+// part of one that a CTA holds is a segment.  Segment results go to the
+// workspace at slot CTA + item (which grows by one from each segment to the
+// next) and a second kernel merges the segments of each row.
 //
 // The products are mma.sync m16n8k16 with fp16 operands and fp32 sums, because
 // an e4m3 value is exact in fp16 and the fragments can be read straight from
 // the cache's rows.  Both are taken transposed, S^T = K Q^T and O^T = V^T P^T,
 // so that the keys (and d) fill the 16 rows of a product and the queries its 8
-// columns: up to 8 query rows cost half of what 16 do (NB = 1 or 2 column
+// columns: up to 8 query rows cost half of what 16 do (NB = 1, 2 or 4 column
 // tiles).  The order of d within K Q^T and of the keys within V^T P^T is free: a
 // lane's 16 consecutive bytes of a K row are the k-indices of its A fragments,
 // and its d / 8 bytes of each of four V rows the k-pairs of its A fragments.  P
 // turns from S^T's accumulators into the B fragments by an 8 x 8 transpose.
 // tcgen05 would need the bytes widened and written back to shared memory first
-// (the queries are not 8 bits wide), for 128-row products of at most 16 columns.
+// (the queries are not 8 bits wide), for 128-row products of at most 32 columns.
 //
 // q is scaled by a power of two per row into fp16's range (exact but for
 // elements 2^-28 below the row's largest).  With x_j the score in log2 units,
@@ -26,6 +34,9 @@
 // 2^(x_j + log2 vs_j - M) in fp16 (relative 2^-11, an eighth of the result's
 // own bf16 step) with its own running maximum M, so that a block's scale can
 // have any size.  Result: O 2^(M - m) / l.
+#include <algorithm>
+#include <climits>
+
 #include "fa_e4m3.cuh"
 #include "fa_internal.h"
 
@@ -35,17 +46,21 @@ namespace {
 constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
 
-template <int D>
+template <int D, int NB>
 struct Cfg {
     static constexpr int KEYS = D == 128 ? 32 : 64;     // keys per warp and step (8 KB of K and V)
+    static constexpr int STEP = kWarps * KEYS;          // keys per CTA and step
     static constexpr int STAGES = 2;                    // steps in flight
     static constexpr int HALF = KEYS * D;               // bytes of K (and of V) per step
     static constexpr int SLOT = 2 * HALF + 8 * KEYS;    // K, V, K scales, log2 of V scales
     static constexpr int RING = STAGES * SLOT;          // per warp
-    static constexpr int OROW = D + 4;                  // row of the merge buffer, floats
-    static constexpr int SMEM = kWarps * RING;
-    static_assert(16 * OROW * 4 <= RING, "merge buffer");
-    static_assert(kWarps * KEYS == (D == 128 ? kFp8ChunkKeys128 : kFp8ChunkKeys64), "chunk rule");
+    static constexpr int ROWS = 8 * NB;                 // query rows per tile
+    static constexpr int OROW = D + 4;                  // row of the merge buffer (in the ring), floats
+    static constexpr bool QSMEM = NB > 2;               // Q fragments in shared memory instead of registers
+    static constexpr int QBYTES = QSMEM ? ROWS * D * 2 : 0;
+    static constexpr int SMEM = kWarps * RING + QBYTES;
+    static constexpr int CTAS = NB > 2 ? 2 : 3;         // per SM (255 and 168 registers)
+    static_assert(ROWS * OROW * 4 <= RING, "merge buffer");
 };
 
 struct Params {
@@ -58,51 +73,113 @@ struct Params {
     const int* lens;
     __nv_bfloat16* o;
     float* lse;
-    float* part_o;
-    float* part_lse;
-    float* scores;
-    long long score_stride;
-    int Hq, Hkv, Nq, max_pages, num_pages, splits, rows, row_tiles;
+    float* weights;
+    float* part_o;       // [slot][ROWS][D], normalised
+    float* part_lse;     // [slot][ROWS], log2
+    float* scores;       // per (sequence, kv head) and tile [key][rows of the tile], log2; null without weights
+    long long* prefix;   // [B + 1] steps before each sequence, per (kv head, row tile)
+    int B, Hq, Hkv, Nq, max_pages, num_pages, rows, row_tiles, workers;
     uint32_t blocks_per_page;
     FastDiv page, sb;
     float scale_log2;
     DevError* err;
 };
 
+__device__ __forceinline__ int clamp_len(int len, int cap) { return min(max(len, 0), cap); }
+
+// Steps of all sequences before q (64-bit warp scan of the lengths): the sequence that step q falls in, its first step
+// and length.  With q beyond the end: sequence B and the total.  prefix: also written, if not null.
+template <int STEP>
+__device__ __forceinline__ void find_sequence(const int* lens, int B, int cap, long long q, long long* prefix, int& b,
+                                              long long& start, int& len) {
+    const int lane = threadIdx.x & 31;
+    long long base = 0;
+    b = B;
+    for (int b0 = 0; b0 < B; b0 += 32) {
+        const int l = b0 + lane < B ? clamp_len(lens[b0 + lane], cap) : 0;
+        const uint32_t n = (uint32_t)(l + STEP - 1) / STEP;
+        uint32_t incl = n;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const uint32_t up = __shfl_up_sync(0xffffffffu, incl, d);
+            if (lane >= d) incl += up;
+        }
+        if (prefix && b0 + lane < B) prefix[b0 + lane] = base + incl - n;
+        const uint32_t hit = __ballot_sync(0xffffffffu, base + incl > q);
+        if (hit) {
+            const int f = __ffs(hit) - 1;
+            b = b0 + f;
+            len = __shfl_sync(0xffffffffu, l, f);
+            start = base + __shfl_sync(0xffffffffu, incl - n, f);
+            return;
+        }
+        base += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    start = base;
+    len = 0;
+    if (prefix && lane == 0) prefix[B] = base;
+}
+
+// Where the scores [key][rows of the tile] of a tile begin.  A (sequence, kv head)'s rows are padded to a multiple of
+// four, so that a tile with a multiple of two or four rows has its scores of a key aligned to as many.
+template <int ROWS>
+__device__ __forceinline__ long long scores_at(const Params& a, long long bh, int rt, int cap) {
+    return (bh * ((a.rows + 3) & ~3) + rt * ROWS) * cap;
+}
+
 template <int D, int NB>
-__global__ void __launch_bounds__(kThreads, 3) decode_fp8_kernel(const Params a) {
-    using C = Cfg<D>;
-    constexpr int KEYS = C::KEYS, MT = KEYS / 16, KS = D / 16, DT = D / 8, ROWS = 8 * NB;
-    extern __shared__ __align__(16) uint8_t smem[];
+__global__ void __launch_bounds__(kThreads, Cfg<D, NB>::CTAS) decode_fp8_kernel(const Params a) {
+    using C = Cfg<D, NB>;
+    constexpr int KEYS = C::KEYS, MT = KEYS / 16, KS = D / 16, DT = D / 8, ROWS = C::ROWS, STEP = C::STEP;
+    extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float s_stat[kWarps][3][ROWS];
+    __shared__ float s_up[ROWS];
     pdl_launch_dependents();
     pdl_wait();
 
-    int idx = blockIdx.x;
-    const int rt = idx % a.row_tiles; idx /= a.row_tiles;
-    const int split = idx % a.splits; idx /= a.splits;
-    const int kvh = idx % a.Hkv;
-    const int b = idx / a.Hkv;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int P = (int)a.page.d, cap = a.max_pages * P;
-    int len = a.lens[b];
-    if (len < 0 || len > cap) {
-        if (tid == 0) record_invalid(a.err, kSiteCacheLen, len);
-        len = len < 0 ? 0 : cap;
+    if (blockIdx.x == 0)
+        for (int i = tid; i < a.B; i += kThreads)
+            if (a.lens[i] < 0 || a.lens[i] > cap) record_invalid(a.err, kSiteCacheLen, a.lens[i]);
+    // this CTA's share [u, u1) of the steps
+    const long long per_step = (long long)a.Hkv * a.row_tiles;
+    long long u, u1;
+    {
+        int b, len;
+        long long total;
+        find_sequence<STEP>(a.lens, a.B, cap, LLONG_MAX, blockIdx.x == 0 && warp == 0 ? a.prefix : nullptr, b, total, len);
+        total *= per_step;
+        const long long workers = min((long long)a.workers, total);  // at least one step each
+        if (blockIdx.x >= workers) return;
+        u = blockIdx.x * total / workers;
+        u1 = (blockIdx.x + 1ll) * total / workers;
     }
-    constexpr int CHUNK = kWarps * KEYS;
-    const int per = (len + a.splits - 1) / a.splits;
-    const int chunk = (per + CHUNK - 1) / CHUNK * CHUNK;
-    const int k0 = (int)min((long long)split * chunk, (long long)len), k1 = min(k0 + chunk, len);
-    const int r0 = rt * ROWS, nrows = min(ROWS, a.rows - r0);  // query rows of this tile
-    const long long row0 = ((long long)b * a.Hq + (long long)kvh * (a.Hq / a.Hkv)) * a.Nq + r0;
-
-    // ---- the ring
+    bool bad = false;
     uint8_t* ring = smem + warp * C::RING;
     const uint32_t ring_u = smem_u32(ring);
+    uint2* qsm = reinterpret_cast<uint2*>(smem + kWarps * C::RING);
+
+    while (u < u1) {
+    int b, len;
+    long long start;
+    find_sequence<STEP>(a.lens, a.B, cap, u / per_step, nullptr, b, start, len);
+    const uint32_t n = (uint32_t)(len + STEP - 1) / STEP;          // steps of the sequence
+    const long long in_b = u - start * per_step;
+    const int item_b = (int)(in_b / n), s0 = (int)(in_b - (long long)item_b * n);
+    const int s1 = (int)min((long long)n, s0 + (u1 - u));          // the segment: steps [s0, s1) of the item
+    const int kvh = item_b / a.row_tiles, rt = item_b - kvh * a.row_tiles;
+    const int k0 = s0 * STEP, k1 = min(s1 * STEP, len);
+    const int r0 = rt * ROWS, nrows = min(ROWS, a.rows - r0);      // query rows of the tile
+    const long long row0 = ((long long)b * a.Hkv + kvh) * a.rows + r0;  // (b, head, token) flattened
+    const long long slot_out = blockIdx.x + (long long)b * per_step + item_b;
+    const bool whole = s0 == 0 && s1 == (int)n;
+    u += s1 - s0;
+
+    // ---- the ring
     const int* trow = a.table + (long long)b * a.max_pages;
     const int first = k0 + warp * KEYS;                       // this warp's first key
-    const int steps = first < k1 ? (k1 - first + CHUNK - 1) / CHUNK : 0;
+    const int steps = first < k1 ? (k1 - first + STEP - 1) / STEP : 0;
     // A copy instruction moves whole rows (D / 16 lanes a row, so that a quarter warp asks for 128 consecutive bytes);
     // the fragments' readers find their 16 bytes (V at D = 64: 8) at
     //   K: (key / 8, half h of D = 128, lane' = 4 (key % 8) + t), lane' ^ 4 h
@@ -125,13 +202,12 @@ __global__ void __launch_bounds__(kThreads, 3) decode_fp8_kernel(const Params a)
         vdst[0] = C::HALF + ((cr & 1) * 8 + 4 * (cc >> 1) + ((cr >> 1) ^ ((cc >> 1) | (cr & 1) << 1))) * 32 + (cc & 1) * 16;
         vdst[1] = vdst[0] + 2 * 8 * 32;  // r + 2
     }
-    bool bad = false;
     using Keys = int[KEYS / 32];     // of lane's key (+ 32) of a step
     using Scales = float[KEYS / 32];
     auto fetch_pages = [&](int it, Keys& pg) {
 #pragma unroll
         for (int i = 0; i < KEYS / 32; ++i) {
-            const int key = first + it * CHUNK + i * 32 + lane;
+            const int key = first + it * STEP + i * 32 + lane;
             pg[i] = (it < steps && key < k1) ? trow[a.page.div(key)] : -1;
         }
     };
@@ -170,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 3) decode_fp8_kernel(const Params a)
             bool all = true;
 #pragma unroll
             for (int i = 0; i < KEYS / 32; ++i) {
-                const int key = first + it * CHUNK + i * 32 + lane;
+                const int key = first + it * STEP + i * 32 + lane;
                 const int pg = pages[i];
                 const bool in = key < k1, ok = in && (unsigned)pg < (unsigned)a.num_pages;
                 bad |= in && !ok;
@@ -213,11 +289,13 @@ __global__ void __launch_bounds__(kThreads, 3) decode_fp8_kernel(const Params a)
     }
 
     // ---- Q fragments: k-step s of lane (g, t) is row g, columns (D = 128: 64 (s / 4) +) 16 t + 4 (s % 4) .. + 3
-    uint32_t qb[NB][KS][2];
+    uint32_t qb[C::QSMEM ? 1 : NB][KS][2];
     float sc[NB][2];  // score scale of the rows whose scores this lane holds: 8 nb + 2 t, + 1
     int lim[NB][2];   // and the keys that they see: j < lim
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
+    for (int f = 0; f < (C::QSMEM ? 1 : NB); ++f) {
+        const int nb = C::QSMEM ? warp : f;  // in shared memory each warp makes one column tile
+        static_assert(!C::QSMEM || NB == kWarps, "one column tile per warp");
         uint32_t w[D / 8];
         if (nb * 8 + g < nrows) {
             const uint4* src = reinterpret_cast<const uint4*>(a.q + (row0 + nb * 8 + g) * D + t * 16);
@@ -244,20 +322,31 @@ __global__ void __launch_bounds__(kThreads, 3) decode_fp8_kernel(const Params a)
         const float down = __uint_as_float((uint32_t)(127 - e) << 23);
         const float up = a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);
 #pragma unroll
-        for (int s = 0; s < KS; ++s)
+        for (int s = 0; s < KS; ++s) {
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const uint32_t x = w[s * 2 + j];
                 const __half2 h = __floats2half2_rn(__uint_as_float(x << 16) * down,
                                                     __uint_as_float(x & 0xFFFF0000u) * down);
-                qb[nb][s][j] = *reinterpret_cast<const uint32_t*>(&h);
+                qb[f][s][j] = *reinterpret_cast<const uint32_t*>(&h);
             }
+            if constexpr (C::QSMEM) qsm[(s * NB + nb) * 32 + lane] = make_uint2(qb[0][s][0], qb[0][s][1]);
+        }
+        if constexpr (C::QSMEM) {
+            if (t == 0) s_up[nb * 8 + g] = up;
+        } else {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            sc[nb][j] = __shfl_sync(0xffffffffu, up, (2 * t + j) * 4);
-            lim[nb][j] = min(k1, len - a.Nq + (r0 + nb * 8 + 2 * t + j) % a.Nq + 1);
+            for (int j = 0; j < 2; ++j) sc[f][j] = __shfl_sync(0xffffffffu, up, (2 * t + j) * 4);
         }
     }
+    if constexpr (C::QSMEM) __syncthreads();
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            if constexpr (C::QSMEM) sc[nb][j] = s_up[nb * 8 + 2 * t + j];
+            lim[nb][j] = min(k1, len - a.Nq + (r0 + nb * 8 + 2 * t + j) % a.Nq + 1);
+        }
 
     float acc[D / 16][NB][4];
 #pragma unroll
@@ -278,24 +367,40 @@ __global__ void __launch_bounds__(kThreads, 3) decode_fp8_kernel(const Params a)
         cp_async_wait<C::STAGES - 1>();
         __syncwarp();  // every lane's copies are there
         const uint8_t* st = ring + slot * C::SLOT;
-        const int key0 = first + it * CHUNK;
+        const int key0 = first + it * STEP;
         float S[MT][NB][4];  // keys 16 i + g, + 8 (c / 2) of rows 8 nb + 2 t + c % 2
         const uint4* kf = reinterpret_cast<const uint4*>(st);
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
+        for (int i = 0; i < MT; ++i)
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) S[i][nb][0] = S[i][nb][1] = S[i][nb][2] = S[i][nb][3] = 0.f;
 #pragma unroll
-            for (int h = 0; h < D / 64; ++h) {
-                const int at = h * 32 + (lane ^ (4 * h));
-                const uint4 x = kf[2 * i * (D / 64) * 32 + at], y = kf[(2 * i + 1) * (D / 64) * 32 + at];
-                const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+        for (int h = 0; h < D / 64; ++h) {
+            uint32_t w[2 * MT][4];
+            const int at = h * 32 + (lane ^ (4 * h));
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const uint32_t ka[4] = {e4m3x2_to_half2(xw[c]), e4m3x2_to_half2(yw[c]), e4m3x2_hi_to_half2(xw[c]),
-                                            e4m3x2_hi_to_half2(yw[c])};
+            for (int i = 0; i < 2 * MT; ++i) {
+                const uint4 x = kf[i * (D / 64) * 32 + at];
+                w[i][0] = x.x, w[i][1] = x.y, w[i][2] = x.z, w[i][3] = x.w;
+            }
 #pragma unroll
-                    for (int nb = 0; nb < NB; ++nb) mma_16816(S[i][nb], ka, qb[nb][h * 4 + c][0], qb[nb][h * 4 + c][1]);
+            for (int c = 0; c < 4; ++c) {
+                uint32_t q0[NB], q1[NB];
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) {
+                    if constexpr (C::QSMEM) {
+                        const uint2 x = qsm[((h * 4 + c) * NB + nb) * 32 + lane];
+                        q0[nb] = x.x, q1[nb] = x.y;
+                    } else {
+                        q0[nb] = qb[nb][h * 4 + c][0], q1[nb] = qb[nb][h * 4 + c][1];
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    const uint32_t ka[4] = {e4m3x2_to_half2(w[2 * i][c]), e4m3x2_to_half2(w[2 * i + 1][c]),
+                                            e4m3x2_hi_to_half2(w[2 * i][c]), e4m3x2_hi_to_half2(w[2 * i + 1][c])};
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb) mma_16816(S[i][nb], ka, q0[nb], q1[nb]);
                 }
             }
         }
@@ -320,19 +425,24 @@ __global__ void __launch_bounds__(kThreads, 3) decode_fp8_kernel(const Params a)
                     for (int c = 0; c < 4; ++c)
                         if (key0 + i * 16 + (c >> 1) * 8 + g >= lim[nb][c & 1]) S[i][nb][c] = -INFINITY;
         }
-        if (a.scores) {
+        if (a.scores) {  // [key][row of the tile]: a lane's two rows are neighbours
+            float* sr = a.scores + scores_at<ROWS>(a, (long long)b * a.Hkv + kvh, rt, cap) + (long long)(key0 + g) * nrows + 2 * t;
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
+            for (int i = 0; i < MT; ++i)
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    float* sr = a.scores + (row0 + nb * 8 + 2 * t + j) * a.score_stride + key0 + g;
+                for (int h = 0; h < 2; ++h)
+                    if (key0 + i * 16 + h * 8 + g < k1)
 #pragma unroll
-                    for (int i = 0; i < MT; ++i)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h)
-                            if (nb * 8 + 2 * t + j < nrows && key0 + i * 16 + h * 8 + g < k1)
-                                sr[i * 16 + h * 8] = S[i][nb][2 * h + j];
-                }
+                        for (int nb = 0; nb < NB; ++nb) {
+                            float* at = sr + (i * 16 + h * 8) * nrows + nb * 8;
+                            if ((nrows & 1) == 0) {
+                                if (nb * 8 + 2 * t < nrows)
+                                    *reinterpret_cast<float2*>(at) = make_float2(S[i][nb][2 * h], S[i][nb][2 * h + 1]);
+                            } else {
+                                if (nb * 8 + 2 * t < nrows) at[0] = S[i][nb][2 * h];
+                                if (nb * 8 + 2 * t + 1 < nrows) at[1] = S[i][nb][2 * h + 1];
+                            }
+                        }
         }
         // ---- softmax: p = 2^(x - m) into l; w = 2^(x + log2 vs - M) for the value product
         float base[NB][2];
@@ -436,7 +546,6 @@ __global__ void __launch_bounds__(kThreads, 3) decode_fp8_kernel(const Params a)
         slot = slot + 1 == C::STAGES ? 0 : slot + 1;
     }
     cp_async_wait<0>();
-    if (__any_sync(0xffffffffu, bad) && lane == 0) record_invalid(a.err, kSiteCacheTable, -1);
 
     // ---- merge the warps: O = sum_w O_w 2^(M_w - m) / l
     __syncwarp();
@@ -476,116 +585,146 @@ __global__ void __launch_bounds__(kThreads, 3) decode_fp8_kernel(const Params a)
             o.w = fmaf(x.w, f, o.w);
         }
         const float lse2 = l == 0.f ? -INFINITY : m + lg2(l);
-        if (a.splits == 1) {
+        if (whole) {
             *reinterpret_cast<uint2*>(a.o + (row0 + r) * D + c) = make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
             if (a.lse && c == 0) a.lse[row0 + r] = lse2 * kLn2;
-            if (a.scores && c == 0) a.part_lse[row0 + r] = lse2;
         } else {
-            *reinterpret_cast<float4*>(a.part_o + ((row0 + r) * a.splits + split) * D + c) = o;
-            if (c == 0) a.part_lse[(row0 + r) * a.splits + split] = lse2;
+            *reinterpret_cast<float4*>(a.part_o + (slot_out * ROWS + r) * D + c) = o;
         }
+        if (c == 0) a.part_lse[slot_out * ROWS + r] = lse2;
     }
+    __syncthreads();  // the merge buffers are the next segment's ring
+    }
+    if (__any_sync(0xffffffffu, bad) && lane == 0) record_invalid(a.err, kSiteCacheTable, -1);
 }
 
-// ------------------------------------------------------------------ merge of the splits
-// One warp per row: LSE = M + log2 sum 2^(lse_s - M), O = sum 2^(lse_s - LSE) o_s.  A split or row without
-// keys has lse = -inf; a row without keys gets O = 0, LSE = -inf.
-template <int D>
-__global__ void __launch_bounds__(128) combine_fp8_kernel(const float* __restrict__ part_o, const float* __restrict__ part_lse,
-                                                          __nv_bfloat16* __restrict__ o, float* __restrict__ lse,
-                                                          long long rows, int splits) {
-    pdl_launch_dependents();
-    pdl_wait();
-    constexpr int PER = D / 32;
-    const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+// ------------------------------------------------------------------ merge of the segments, and the weights
+// The segments of item i (sequence b, kv head, row tile) are those of the CTAs that hold its first to its last step;
+// CTA c's is in slot c + i.  Returns their number (0: an empty sequence) and the first one's slot.
+__device__ __forceinline__ int find_segments(const Params& a, int b, int item_b, long long& slot) {
+    const long long per_step = (long long)a.Hkv * a.row_tiles;
+    const long long p0 = a.prefix[b], n = a.prefix[b + 1] - p0, total = a.prefix[a.B] * per_step;
+    if (n == 0) return 0;
+    const long long s0 = p0 * per_step + item_b * n, s1 = s0 + n - 1;  // first and last step
+    const long long workers = min((long long)a.workers, total);
+    const long long c0 = ((s0 + 1) * workers - 1) / total, c1 = ((s1 + 1) * workers - 1) / total;
+    slot = c0 + b * per_step + item_b;
+    return (int)(c1 - c0) + 1;
+}
+
+// log2-domain LSE of a row over its segments, by one warp; M: the largest partial one (0 for none).  +inf sum: NaN stays.
+__device__ __forceinline__ float merge_lse(const float* pl, int stride, int segs, float& base) {
     const int lane = threadIdx.x & 31;
-    if (row >= rows) return;
-    const float* pl = part_lse + row * splits;
     float M = -INFINITY;
-    for (int s = lane; s < splits; s += 32) M = fmaxf(M, pl[s]);
+    for (int s = lane; s < segs; s += 32) M = fmaxf(M, pl[(long long)s * stride]);
     for (int w = 16; w >= 1; w >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
-    const float base = M == -INFINITY ? 0.f : M;
+    base = M == -INFINITY ? 0.f : M;
     float sum = 0.f;
-    for (int s = lane; s < splits; s += 32) sum += ex2(pl[s] - base);
+    for (int s = lane; s < segs; s += 32) sum += ex2(pl[(long long)s * stride] - base);
     for (int w = 16; w >= 1; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    float out[PER];
-#pragma unroll
-    for (int i = 0; i < PER; ++i) out[i] = 0.f;
-    const float* po = part_o + row * splits * D + lane * PER;
-    for (int s = 0; s < splits; ++s) {
-        const float w = ex2(pl[s] - base) * inv;
-        if constexpr (PER == 4) {
-            const float4 v = *reinterpret_cast<const float4*>(po + (long long)s * D);
-            out[0] = fmaf(w, v.x, out[0]);
-            out[1] = fmaf(w, v.y, out[1]);
-            out[2] = fmaf(w, v.z, out[2]);
-            out[3] = fmaf(w, v.w, out[3]);
-        } else {
-            const float2 v = *reinterpret_cast<const float2*>(po + (long long)s * D);
-            out[0] = fmaf(w, v.x, out[0]);
-            out[1] = fmaf(w, v.y, out[1]);
-        }
-    }
-    __nv_bfloat16* ob = o + row * D + lane * PER;
-#pragma unroll
-    for (int i = 0; i < PER; i += 2)
-        *reinterpret_cast<__nv_bfloat162*>(ob + i) = __floats2bfloat162_rn(out[i], out[i + 1]);
-    if (lse && lane == 0) lse[row] = sum == 0.f ? -INFINITY : (M + lg2(sum)) * kLn2;
+    return sum;
 }
 
-// ------------------------------------------------------------------ accumulated weights
-// weights[b, kvh, j] += sum over the group's rows of 2^(x_j - LSE), from the scores that the split kernel left.
-// One thread takes four keys; the rows' LSEs come from the splits' partial ones.  Fixed order of additions.
-constexpr int kWeightThreads = 128;
-__global__ void __launch_bounds__(kWeightThreads) weights_fp8_kernel(const float* __restrict__ scores, long long stride,
-                                                                     const float* __restrict__ part_lse,
-                                                                     const int* __restrict__ lens,
-                                                                     float* __restrict__ weights, int Hkv, int rows,
-                                                                     int splits, int cap) {
-    extern __shared__ float s_lse[];
+constexpr int kFinishThreads = 128;
+
+// Blocks below `row_blocks`: one row each; LSE = M + log2 sum 2^(lse_s - M), O = sum 2^(lse_s - M) o_s / sum, the
+// segments dealt to groups of D / 4 threads.  A row without keys gets O = 0, LSE = -inf; a row whose item was one
+// segment is already written.
+// The others, with weights: 128 tokens of one (sequence, kv head) each; weights[j] += sum over the rows of
+// 2^(x_j - LSE), one thread per token, in a fixed order.
+template <int D, int ROWS>
+__global__ void __launch_bounds__(kFinishThreads) finish_fp8_kernel(const Params a, unsigned row_blocks, int weight_blocks) {
+    constexpr int LANES = D / 4, GROUPS = kFinishThreads / LANES, AHEAD = 4;
+    extern __shared__ float s_lse[];  // weights: LSE of the rows
+    __shared__ float4 s_o[GROUPS][LANES];
     pdl_launch_dependents();
     pdl_wait();
-    const int per_bh = (cap + kWeightThreads * 4 - 1) / (kWeightThreads * 4);
-    const long long bh = blockIdx.x / per_bh;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int len = min(max(lens[bh / Hkv], 0), cap);
-    const int j0 = (int)(blockIdx.x % per_bh) * kWeightThreads * 4;
+    if (blockIdx.x < row_blocks) {
+        const long long row = blockIdx.x, bh = row / a.rows;
+        const int r = (int)(row - bh * a.rows), b = (int)(bh / a.Hkv), rt = r / ROWS;
+        long long slot = 0;
+        const int segs = find_segments(a, b, (int)(bh % a.Hkv) * a.row_tiles + rt, slot);
+        if (segs == 1) return;
+        const int grp = tid / LANES, col = tid % LANES;
+        const long long at = slot * ROWS + (r - rt * ROWS);
+        const float* pl = a.part_lse + at;
+        const float4* po = reinterpret_cast<const float4*>(a.part_o + at * D) + col;
+        float4 v[AHEAD];  // the first segments, loaded before the weights are known
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i)
+            if (grp + i * GROUPS < segs) v[i] = po[(long long)(grp + i * GROUPS) * ROWS * LANES];
+        float base;
+        const float sum = merge_lse(pl, ROWS, segs, base);
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int s0 = grp; s0 < segs; s0 += AHEAD * GROUPS) {
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) {
+                const int s = s0 + i * GROUPS;
+                if (s < segs) {
+                    const float w = ex2(pl[(long long)s * ROWS] - base) * inv;
+                    o.x = fmaf(w, v[i].x, o.x);
+                    o.y = fmaf(w, v[i].y, o.y);
+                    o.z = fmaf(w, v[i].z, o.z);
+                    o.w = fmaf(w, v[i].w, o.w);
+                }
+                if (s + AHEAD * GROUPS < segs) v[i] = po[(long long)(s + AHEAD * GROUPS) * ROWS * LANES];
+            }
+        }
+        s_o[grp][col] = o;
+        __syncthreads();
+        if (grp == 0) {
+#pragma unroll
+            for (int i = 1; i < GROUPS; ++i) {
+                const float4 x = s_o[i][col];
+                o.x += x.x;
+                o.y += x.y;
+                o.z += x.z;
+                o.w += x.w;
+            }
+            *reinterpret_cast<uint2*>(a.o + row * D + col * 4) = make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
+            if (a.lse && col == 0) a.lse[row] = sum == 0.f ? -INFINITY : (base + lg2(sum)) * kLn2;
+        }
+        return;
+    }
+    const unsigned idx = blockIdx.x - row_blocks;
+    const long long bh = idx / weight_blocks;
+    const int b = (int)(bh / a.Hkv), kvh = (int)(bh % a.Hkv), cap = a.max_pages * (int)a.page.d;
+    const int len = clamp_len(a.lens[b], cap), j0 = (int)(idx % weight_blocks) * kFinishThreads;
     if (j0 >= len) return;
-    for (int r = warp; r < rows; r += kWeightThreads / 32) {
-        const float* pl = part_lse + (bh * rows + r) * splits;
-        float M = -INFINITY;
-        for (int s = lane; s < splits; s += 32) M = fmaxf(M, pl[s]);
-        for (int w = 16; w >= 1; w >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
-        const float base = M == -INFINITY ? 0.f : M;
-        float sum = 0.f;
-        for (int s = lane; s < splits; s += 32) sum += ex2(pl[s] - base);
-        for (int w = 16; w >= 1; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
-        if (lane == 0) s_lse[r] = sum == 0.f ? INFINITY : M + lg2(sum);  // no keys: every weight 2^-inf = 0
+    for (int r = warp; r < a.rows; r += kFinishThreads / 32) {
+        long long slot = 0;
+        const int segs = find_segments(a, b, kvh * a.row_tiles + r / ROWS, slot);
+        float base;
+        const float sum = merge_lse(a.part_lse + slot * ROWS + r % ROWS, ROWS, segs, base);
+        if (lane == 0) s_lse[r] = sum == 0.f ? INFINITY : base + lg2(sum);  // no keys: every weight 2^-inf = 0
     }
     __syncthreads();
-    const int j = j0 + tid * 4;
+    const int j = j0 + tid;
     if (j >= len) return;
-    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-    const float* sr = scores + bh * rows * stride + j;
-    for (int r = 0; r < rows; ++r, sr += stride) {
-        const float4 x = *reinterpret_cast<const float4*>(sr);
-        const float z = s_lse[r];
-        sum.x += ex2(x.x - z);
-        sum.y += ex2(x.y - z);
-        sum.z += ex2(x.z - z);
-        sum.w += ex2(x.w - z);
+    float* w = a.weights + bh * cap + j;
+    float sum = 0.f;
+    const float before = *w;
+    for (int rt = 0; rt < a.row_tiles; ++rt) {
+        const int nrows = min(ROWS, a.rows - rt * ROWS);
+        const float* sr = a.scores + scores_at<ROWS>(a, bh, rt, cap) + (long long)j * nrows;
+        const float* z = s_lse + rt * ROWS;
+        if ((nrows & 3) == 0) {
+            for (int r = 0; r < nrows; r += 4) {
+                const float4 x = *reinterpret_cast<const float4*>(sr + r);
+                sum += (ex2(x.x - z[r]) + ex2(x.y - z[r + 1])) + (ex2(x.z - z[r + 2]) + ex2(x.w - z[r + 3]));
+            }
+        } else {
+            for (int r = 0; r < nrows; ++r) sum += ex2(sr[r] - z[r]);
+        }
     }
-    float* w = weights + bh * cap + j;
-    w[0] += sum.x;
-    if (j + 1 < len) w[1] += sum.y;
-    if (j + 2 < len) w[2] += sum.z;
-    if (j + 3 < len) w[3] += sum.w;
+    *w = before + sum;
 }
 
 template <int D, int NB>
 cudaError_t launch_d(const PagedDecodeFp8Launch& a, cudaStream_t s) {
-    using C = Cfg<D>;
+    using C = Cfg<D, NB>;
     cudaError_t e = set_smem_limit_once<decode_fp8_kernel<D, NB>>(C::SMEM);
     if (e != cudaSuccess) return e;
     Params p;
@@ -598,59 +737,56 @@ cudaError_t launch_d(const PagedDecodeFp8Launch& a, cudaStream_t s) {
     p.lens = a.lens;
     p.o = (__nv_bfloat16*)a.o;
     p.lse = a.lse;
+    p.weights = a.weights;
     p.part_o = a.part_o;
     p.part_lse = a.part_lse;
     p.scores = a.weights ? a.scores : nullptr;
-    p.score_stride = a.score_stride;
+    p.prefix = a.prefix;
+    p.B = a.B;
     p.Hq = a.Hq;
     p.Hkv = a.Hkv;
     p.Nq = a.Nq;
     p.max_pages = a.max_pages;
     p.num_pages = a.num_pages;
-    p.splits = a.splits;
     p.rows = a.Hq / a.Hkv * a.Nq;
-    p.row_tiles = (p.rows + 8 * NB - 1) / (8 * NB);
+    p.row_tiles = (p.rows + C::ROWS - 1) / C::ROWS;
     p.blocks_per_page = (uint32_t)(a.page / a.sb);
     p.page = FastDiv((uint32_t)a.page);
     p.sb = FastDiv((uint32_t)a.sb);
     p.scale_log2 = a.scale * kLog2e;
     p.err = a.err;
-    const long long ctas = (long long)a.B * a.Hkv * a.splits * p.row_tiles;
-    if (ctas > 0x7FFFFFFFll) return cudaErrorInvalidValue;
-    e = launch_dependent(decode_fp8_kernel<D, NB>, dim3((unsigned)ctas), dim3(kThreads), C::SMEM, s, p);
-    if (e != cudaSuccess) return e;
-    const long long rows = (long long)a.B * a.Hq * a.Nq;
-    if (a.splits > 1) {
-        e = launch_dependent(combine_fp8_kernel<D>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, s,
-                             (const float*)a.part_o, (const float*)a.part_lse, p.o, a.lse, rows, a.splits);
-        if (e != cudaSuccess) return e;
-    }
-    if (!a.weights) return cudaSuccess;
     const int cap = a.max_pages * a.page;
-    const long long blocks = (long long)((cap + kWeightThreads * 4 - 1) / (kWeightThreads * 4)) * a.B * a.Hkv;
+    const long long bh = (long long)a.B * a.Hkv;
+    // no more CTAs than steps at full lengths
+    p.workers = (int)std::min<long long>(a.workers, bh * p.row_tiles * ((cap + C::STEP - 1) / C::STEP));
+    e = launch_dependent(decode_fp8_kernel<D, NB>, dim3(p.workers), dim3(kThreads), C::SMEM, s, p);
+    if (e != cudaSuccess) return e;
+    const int weight_blocks = a.weights ? (cap + kFinishThreads - 1) / kFinishThreads : 0;
+    const long long row_blocks = bh * p.rows, blocks = row_blocks + bh * weight_blocks;
     if (blocks > 0x7FFFFFFFll) return cudaErrorInvalidValue;
-    return launch_dependent(weights_fp8_kernel, dim3((unsigned)blocks), dim3(kWeightThreads), (size_t)p.rows * 4, s, (const float*)a.scores, a.score_stride,
-                            (const float*)a.part_lse, a.lens, a.weights, a.Hkv, p.rows, a.splits, cap);
+    return launch_dependent(finish_fp8_kernel<D, C::ROWS>, dim3((unsigned)blocks), dim3(kFinishThreads),
+                            a.weights ? (size_t)p.rows * 4 : 0, s, p, (unsigned)row_blocks, weight_blocks);
+}
+
+template <int D, int NB>
+cudaError_t blocks_per_sm(int* blocks) {
+    using C = Cfg<D, NB>;
+    const cudaError_t e = set_smem_limit_once<decode_fp8_kernel<D, NB>>(C::SMEM);
+    if (e != cudaSuccess) return e;
+    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(blocks, decode_fp8_kernel<D, NB>, kThreads, C::SMEM);
 }
 
 }  // namespace
 
 cudaError_t launch_decode_paged_fp8(const PagedDecodeFp8Launch& a, cudaStream_t s) {
-    const bool one = a.Hq / a.Hkv * a.Nq <= 8;
-    if (a.d == 128) return one ? launch_d<128, 1>(a, s) : launch_d<128, 2>(a, s);
-    return one ? launch_d<64, 1>(a, s) : launch_d<64, 2>(a, s);
+    const int tile = fp8_tile_rows(a.Hq / a.Hkv * a.Nq);
+    if (a.d == 128) return tile == 8 ? launch_d<128, 1>(a, s) : tile == 16 ? launch_d<128, 2>(a, s) : launch_d<128, 4>(a, s);
+    return tile == 8 ? launch_d<64, 1>(a, s) : tile == 16 ? launch_d<64, 2>(a, s) : launch_d<64, 4>(a, s);
 }
 
-template <int D, int NB>
-static cudaError_t blocks_per_sm(int* blocks) {
-    const cudaError_t e = set_smem_limit_once<decode_fp8_kernel<D, NB>>(Cfg<D>::SMEM);
-    if (e != cudaSuccess) return e;
-    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(blocks, decode_fp8_kernel<D, NB>, kThreads, Cfg<D>::SMEM);
-}
-
-cudaError_t decode_fp8_blocks_per_sm(int d, bool one, int* blocks) {
-    if (d == 128) return one ? blocks_per_sm<128, 1>(blocks) : blocks_per_sm<128, 2>(blocks);
-    return one ? blocks_per_sm<64, 1>(blocks) : blocks_per_sm<64, 2>(blocks);
+cudaError_t decode_fp8_blocks_per_sm(int d, int tile, int* n) {
+    if (d == 128) return tile == 8 ? blocks_per_sm<128, 1>(n) : tile == 16 ? blocks_per_sm<128, 2>(n) : blocks_per_sm<128, 4>(n);
+    return tile == 8 ? blocks_per_sm<64, 1>(n) : tile == 16 ? blocks_per_sm<64, 2>(n) : blocks_per_sm<64, 4>(n);
 }
 
 }  // namespace fa

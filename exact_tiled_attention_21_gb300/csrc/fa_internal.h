@@ -213,11 +213,12 @@ struct PagedDecodeFp8Launch {
     void* o;               // bf16 [B, Hq, Nq, d]
     float* lse;            // fp32 [B, Hq, Nq], or null
     float* weights;        // fp32 [B, Hkv, max_pages * page], or null
-    float* part_o;         // fp32 [B*Hq*Nq, splits, d]
-    float* part_lse;       // fp32 [B*Hq*Nq, splits]
-    float* scores;         // fp32 [B*Hq*Nq, score_stride] (log2 units), with weights only
-    long long score_stride;
-    int B, Hq, Hkv, Nq, page, sb, max_pages, num_pages, d, splits;
+    float* part_o;         // fp32 [workers + items, tile rows, d]
+    float* part_lse;       // fp32 [workers + items, tile rows]
+    float* scores;         // fp32 [B*Hkv, rows padded to 4, max_pages * page] in all (log2 units), with weights only
+    long long* prefix;     // [B + 1]
+    int B, Hq, Hkv, Nq, page, sb, max_pages, num_pages, d;
+    int workers;           // CTAs to share the steps among
     float scale;
     DevError* err;
 };
@@ -290,10 +291,9 @@ cudaError_t launch_rope(RopeLaunch a, cudaStream_t s);
 cudaError_t launch_cache_append(const CacheAppendLaunch& a, cudaStream_t s);
 cudaError_t launch_cache_evict(const CacheEvictLaunch& a, cudaStream_t s);  // choose the tokens, then move them
 cudaError_t launch_decode_paged_fp8(const PagedDecodeFp8Launch& a, cudaStream_t s);
-// Resident CTAs on one SM of its split kernel for 1..8 query rows per kv head (one) or more.
-cudaError_t decode_fp8_blocks_per_sm(int d, bool one, int* blocks);
-// Keys that one CTA of the fp8 split kernel takes per step: its chunks are multiples of this.
-constexpr int kFp8ChunkKeys64 = 256, kFp8ChunkKeys128 = 128;
+// Query rows (of one kv head) that a pass over the cache serves: the tile that holds `rows`, or the largest.
+inline int fp8_tile_rows(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
+cudaError_t decode_fp8_blocks_per_sm(int d, int tile_rows, int* blocks);  // resident CTAs of its first kernel on one SM
 // LSE-weighted merge of per-split partials into o (bf16) and lse (fp32, may be null).
 cudaError_t launch_decode_combine(const float* part_o, const float* part_lse, void* o, float* lse, int BH,
                                   int splits, int d, cudaStream_t s);

@@ -370,12 +370,9 @@ int fa_cache_append_fp8(const void *k, const void *v, long long k_sb, long long 
 
 /* Bytes of workspace fa_decode_paged_fp8 needs; max_tokens = max_pages *
  * page_size, weights = 1 if it is given accumulated weights (which takes fp32
- * scores of every query row and token besides the partials).  num_splits <= 0:
- * for the most splits that the automatic choice takes (one per 128 tokens at
- * d = 128, 256 at d = 64; at most 256, and 4096 divided by B * Hkv * ceil(Hq /
- * Hkv * Nq / 16)).  Returns 0 for invalid sizes.  Host only, no device call. */
-size_t fa_decode_paged_fp8_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d, int max_tokens, int num_splits,
-                                           int weights);
+ * scores of every query row and token besides the partials).  Returns 0 for
+ * invalid sizes.  Host only, no device call. */
+size_t fa_decode_paged_fp8_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d, int max_tokens, int weights);
 
 /* Attention of the last Nq (1..16) tokens of each sequence over the 8-bit
  * cache, which holds them already: one token, or a few drafted ones.  q, o: bf16
@@ -388,9 +385,9 @@ size_t fa_decode_paged_fp8_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d
  * the sum of token j's attention weights over the group's heads and the Nq
  * queries (what fa_cache_evict_fp8 selects by); tokens >= seq_lens[b] are left
  * as they are.
- * num_splits (<= 256) cuts each sequence into chunks of whole steps (128 tokens
- * at d = 128, 256 at d = 64); <= 0 lets the library choose from the sizes.
- * Results do not depend on the run (fixed order of additions).  Tokens past
+ * The tokens of all sequences are dealt out evenly, by their lengths, to the
+ * CTAs that run at once, so there is no number of splits to choose.  Results do
+ * not depend on the run (fixed order of additions).  Tokens past
  * seq_lens[b] are never used.  A NaN in V reaches every query of its sequence and
  * kv head, also those of the Nq that do not see its token.  workspace: 16-byte
  * aligned, at least fa_decode_paged_fp8_workspace_bytes(...); contents do not
@@ -398,8 +395,8 @@ size_t fa_decode_paged_fp8_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d
 int fa_decode_paged_fp8(const void *q, const void *k_pages, const void *v_pages, const float *k_scale,
                         const float *v_scale, const int *block_table, const int *seq_lens, void *o, float *lse,
                         float *weights, int B, int Hq, int Hkv, int Nq, int page_size, int scale_block,
-                        int max_pages, int num_pages, int d, float scale, int num_splits, void *workspace,
-                        size_t workspace_bytes, void *stream);
+                        int max_pages, int num_pages, int d, float scale, void *workspace, size_t workspace_bytes,
+                        void *stream);
 
 /* Eviction by accumulated attention weight: per sequence b and kv head, the
  * min(seq_lens[b], keep) tokens that stay are the last `recent` (0..keep) and,

@@ -114,15 +114,15 @@ def test_append_pointer_checks(lib):
 
 
 def _decode(lib, p=(16,) * 8, lse=16, w=0, B=1, Hq=4, Hkv=2, Nq=1, page=16, sb=8, mp=4, np=9, d=64, scale=0.125,
-            splits=2, ws=16, nbytes=1 << 30):
-    return lib.fa_decode_paged_fp8(*map(vp, p), vp(lse), vp(w), B, Hq, Hkv, Nq, page, sb, mp, np, d, scale, splits,
+            ws=16, nbytes=1 << 30):
+    return lib.fa_decode_paged_fp8(*map(vp, p), vp(lse), vp(w), B, Hq, Hkv, Nq, page, sb, mp, np, d, scale,
                                    vp(ws), nbytes, None)
 
 
 @pytest.mark.parametrize("bad,status", CACHE_BAD + [
     (dict(Hq=3), fa.FA_ERR_INVALID_ARG), (dict(Hq=0), fa.FA_ERR_INVALID_ARG), (dict(Nq=0), fa.FA_ERR_INVALID_ARG),
     (dict(Nq=17), fa.FA_ERR_UNSUPPORTED), (dict(scale=0.0), fa.FA_ERR_INVALID_ARG), (dict(scale=NAN), fa.FA_ERR_INVALID_ARG),
-    (dict(splits=257), fa.FA_ERR_INVALID_ARG), (dict(lse=6), fa.FA_ERR_ALIGNMENT), (dict(w=2), fa.FA_ERR_ALIGNMENT),
+    (dict(lse=6), fa.FA_ERR_ALIGNMENT), (dict(w=2), fa.FA_ERR_ALIGNMENT),
 ])
 def test_decode_refusals(lib, bad, status):
     assert _decode(lib, **bad) == status
@@ -139,16 +139,14 @@ def test_decode_pointer_checks(lib):
 
 def test_decode_workspace_query():
     q = fa.fa_decode_paged_fp8_workspace_bytes
-    assert q(2, 8, 2, 1, 128, 4096, 4, False) >= 2 * 8 * 4 * 129 * 4
-    assert q(2, 8, 2, 1, 128, 4096, 1, False) >= 2 * 8 * 4
-    assert q(2, 8, 2, 3, 128, 4097, 4, True) >= 2 * 8 * 3 * (4 * 129 + 4097) * 4
-    # automatic: enough for every count it may take, bounded by 4096 CTAs
-    assert q(1, 8, 8, 1, 128, 1 << 20, 0, False) >= q(1, 8, 8, 1, 128, 1 << 20, 256, False)
-    assert q(32, 32, 8, 1, 128, 1 << 20, 0, False) <= q(32, 32, 8, 1, 128, 1 << 20, 16, False)
-    assert q(4096, 32, 8, 1, 128, 4096, 0, False) <= q(4096, 32, 8, 1, 128, 4096, 1, False)
-    for bad in ((0, 8, 2, 1, 128, 64, 0, 0), (1, 7, 2, 1, 128, 64, 0, 0), (1, 8, 0, 1, 128, 64, 0, 0),
-                (1, 8, 2, 17, 128, 64, 0, 0), (1, 8, 2, 1, 96, 64, 0, 0), (1, 8, 2, 1, 64, 0, 0, 0),
-                (1, 8, 2, 1, 64, 64, 300, 0)):
+    # a slot (rows of a tile by d + 1 floats) for each of 1024 CTAs and for each item
+    assert q(2, 8, 2, 1, 128, 4096, False) >= (1024 + 4) * 8 * 129 * 4 + 3 * 8
+    assert q(2, 40, 2, 4, 64, 4096, False) >= (1024 + 2 * 2 * 3) * 32 * 65 * 4
+    # and the scores, rows padded to a multiple of four
+    assert q(2, 10, 2, 3, 128, 4097, True) - q(2, 10, 2, 3, 128, 4097, False) >= 2 * 2 * 16 * 4097 * 4
+    assert q(1, 8, 8, 1, 128, 1, False) == q(1, 8, 8, 1, 128, 1 << 30, False) > 0
+    for bad in ((0, 8, 2, 1, 128, 64, 0), (1, 7, 2, 1, 128, 64, 0), (1, 8, 0, 1, 128, 64, 0),
+                (1, 8, 2, 17, 128, 64, 0), (1, 8, 2, 1, 96, 64, 0), (1, 8, 2, 1, 64, 0, 0)):
         assert q(*bad) == 0, bad
 
 

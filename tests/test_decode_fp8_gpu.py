@@ -23,39 +23,46 @@ def _case(seed, B, Hq, Hkv, Nq, page, sb, lens, d):
     return bf16(np.random.default_rng(seed + 1), (B, Hq, Nq, d), 0.3), c, table_of(seed + 2, B, maxp, B * maxp + 2)
 
 
-# (Hq, Hkv, Nq, page, sb, lens, d, splits)
+# (Hq, Hkv, Nq, page, sb, lens, d)
 CASES = [
-    (1, 1, 1, 16, 16, [1], 64, 1),
-    (8, 2, 1, 16, 16, [1, 37, 200], 128, 4),
-    (8, 2, 1, 16, 16, [0, 33, 0, 128, 129], 128, 0),      # sequences without tokens
-    (6, 2, 1, 64, 32, [64, 1000], 64, 16),
-    (16, 2, 1, 32, 8, [1500, 513], 128, 7),
-    (32, 2, 1, 16, 4, [300, 17], 128, 2),                 # 16 heads a group: a full row tile
-    (40, 2, 1, 16, 16, [300, 17], 64, 2),                 # 20: two row tiles
-    (5, 1, 1, 1, 1, [77], 128, 3),                        # single-token pages and scales
-    (4, 4, 1, 20, 20, [129, 1], 64, 3),
-    (4, 2, 1, 33, 11, [500, 64], 128, 256),               # more splits than steps
-    (7, 1, 1, 128, 128, [2000], 64, 0),
-    (3, 3, 1, 256, 64, [1000, 255], 128, 5),
-    (8, 2, 4, 16, 16, [4, 3, 1, 0, 500], 128, 3),         # drafted tokens: rows that see no key
-    (2, 2, 16, 48, 24, [16, 100, 31], 64, 2),
-    (16, 1, 5, 64, 64, [300, 5], 128, 0),                 # 80 rows: five row tiles
-    (6, 2, 2, 32, 16, [33, 64, 95], 64, 1),
-    (8, 8, 1, 64, 64, [9000], 128, 1),                    # one split: many turns of the ring
-    (8, 8, 1, 64, 64, [9000], 64, 0),
+    (1, 1, 1, 16, 16, [1], 64),
+    (8, 2, 1, 16, 16, [1, 37, 200], 128),
+    (8, 2, 1, 16, 16, [0, 33, 0, 128, 129], 128),      # sequences without tokens
+    (8, 2, 1, 16, 16, [0, 0], 64),                     # none at all
+    (6, 2, 1, 64, 32, [64, 1000], 64),
+    (16, 2, 1, 32, 8, [1500, 513], 128),
+    (32, 2, 1, 16, 4, [300, 17], 128),                 # 16 heads a group: two column tiles
+    (40, 2, 1, 16, 16, [300, 17], 64),                 # 20: a tile of 32 rows, partly empty
+    (5, 1, 1, 1, 1, [77], 128),                        # single-token pages and scales
+    (4, 4, 1, 20, 20, [129, 1], 64),
+    (4, 2, 1, 33, 11, [500, 64], 128),
+    (7, 1, 1, 128, 128, [2000], 64),
+    (3, 3, 1, 256, 64, [1000, 255], 128),
+    (8, 2, 4, 16, 16, [4, 3, 1, 0, 500], 128),         # drafted tokens: rows that see no key
+    (2, 2, 16, 48, 24, [16, 100, 31], 64),
+    (16, 1, 5, 64, 64, [300, 5], 128),                 # 80 rows: three row tiles
+    (21, 3, 5, 32, 32, [300, 70], 128),                # 35 rows: an odd number in the last tile, an odd kv head
+    (21, 3, 5, 32, 32, [301, 71], 64),
+    (9, 3, 3, 16, 16, [130, 20], 128),                 # 9 rows
+    (6, 2, 2, 32, 16, [33, 64, 95], 64),
+    (8, 8, 1, 64, 64, [9000], 128),                    # long: segments of many steps
+    (8, 8, 1, 64, 64, [9000], 64),
+    (4, 1, 1, 64, 64, [70000], 128),                   # one kv head over every SM: hundreds of segments to merge
+    (1, 1, 1, 16, 16, list(range(0, 200, 3)) * 2, 64),  # more sequences than one scan step, some empty
+    (2, 1, 2, 16, 16, [130] * 300, 128),               # more items than CTAs: shares that cross several
 ]
 
 
 @pytest.mark.parametrize("weights", [False, True])
-@pytest.mark.parametrize("Hq,Hkv,Nq,page,sb,lens,d,splits", CASES)
-def test_decode_parity(cuda_lib, Hq, Hkv, Nq, page, sb, lens, d, splits, weights):
+@pytest.mark.parametrize("Hq,Hkv,Nq,page,sb,lens,d", CASES)
+def test_decode_parity(cuda_lib, Hq, Hkv, Nq, page, sb, lens, d, weights):
     B = len(lens)
     q, c, table = _case(page * 3 + Hq + d, B, Hq, Hkv, Nq, page, sb, lens, d)
     g = to_gpu(c)
     cap = table.shape[1] * page
     w0 = np.random.default_rng(1).uniform(0, 2, (B, Hkv, cap)).astype(np.float32)
     w = torch.from_numpy(w0).to(DEV) if weights else None
-    o, lse = cuda_lib.decode_paged_fp8(q.to(DEV), *args(g), ints(table), ints(lens), weights=w, num_splits=splits)
+    o, lse = cuda_lib.decode_paged_fp8(q.to(DEV), *args(g), ints(table), ints(lens), weights=w)
     _ok(cuda_lib)
     w_ref = w0.astype(np.float64)
     ref = oc.decode(f64(q), c, table, lens, 1 / math.sqrt(d), w_ref)
@@ -64,7 +71,7 @@ def test_decode_parity(cuda_lib, Hq, Hkv, Nq, page, sb, lens, d, splits, weights
         for b in range(B):
             assert np.array_equal(w[b, :, lens[b]:].cpu().numpy(), w0[b, :, lens[b]:])   # behind the sequence
     if Nq == 1:
-        o3, l3 = cuda_lib.decode_paged_fp8(q[:, :, 0].to(DEV), *args(g), ints(table), ints(lens), num_splits=splits)
+        o3, l3 = cuda_lib.decode_paged_fp8(q[:, :, 0].to(DEV), *args(g), ints(table), ints(lens))
         assert torch.equal(o3, o[:, :, 0]) and torch.equal(l3, lse[:, :, 0])
 
 
@@ -141,7 +148,7 @@ def test_decode_nan_shows(cuda_lib):
     q, c, table = _case(41, 1, 4, 2, 1, 16, 16, [50], 64)
     c["k"][table[0, 1], 0, 3, 5] = 0x7F
     c["v"][table[0, 2], 1, 7, 9] = 0xFF
-    o, lse = cuda_lib.decode_paged_fp8(q.to(DEV), *args(to_gpu(c)), ints(table), ints([50]), num_splits=2)
+    o, lse = cuda_lib.decode_paged_fp8(q.to(DEV), *args(to_gpu(c)), ints(table), ints([50]))
     assert o[0, :2].isnan().all() and lse[0, :2].isnan().all()
     assert o[0, 2:, 0, 9].isnan().all() and int(o[0, 2:].isnan().sum()) == 2 and lse[0, 2:].isfinite().all()
 
@@ -152,7 +159,7 @@ def test_decode_sharp_softmax(cuda_lib):
     q = q * 30
     w_ref = np.zeros((2, 2, table.shape[1] * 32))
     w = torch.zeros(w_ref.shape, device=DEV)
-    o, lse = cuda_lib.decode_paged_fp8(q.to(DEV), *args(to_gpu(c)), ints(table), ints([400, 399]), weights=w, num_splits=2)
+    o, lse = cuda_lib.decode_paged_fp8(q.to(DEV), *args(to_gpu(c)), ints(table), ints([400, 399]), weights=w)
     ref = oc.decode(f64(q), c, table, [400, 399], 1 / math.sqrt(128), w_ref)
     check_decode(o, lse, ref, w, w_ref)
 
@@ -234,14 +241,14 @@ def test_decode_repeats_streams_and_graphs(cuda_lib):
 def test_decode_own_workspace_and_refusals(cuda_lib):
     q, c, table = _case(91, 2, 8, 2, 1, 16, 16, [100, 50], 64)
     g, qd, tab, lens = to_gpu(c), q.to(DEV), ints(table), ints([100, 50])
-    n = cuda_lib.fa_decode_paged_fp8_workspace_bytes(2, 8, 2, 1, 64, table.shape[1] * 16, 2, True)
+    n = cuda_lib.fa_decode_paged_fp8_workspace_bytes(2, 8, 2, 1, 64, table.shape[1] * 16, True)
     ws = torch.full((n,), 0xFF, dtype=torch.uint8, device=DEV)   # its contents (NaN here) do not matter
     w = torch.zeros((2, 2, table.shape[1] * 16), device=DEV)
-    o, lse = cuda_lib.decode_paged_fp8(qd, *args(g), tab, lens, weights=w, num_splits=2, workspace=ws)
+    o, lse = cuda_lib.decode_paged_fp8(qd, *args(g), tab, lens, weights=w, workspace=ws)
     w_ref = np.zeros(w.shape)
     check_decode(o, lse, oc.decode(f64(q), c, table, [100, 50], 0.125, w_ref), w, w_ref)
     with pytest.raises(fa_mod.FAError) as e:
-        cuda_lib.decode_paged_fp8(qd, *args(g), tab, lens, weights=w, num_splits=2, workspace=ws[:n - 256])
+        cuda_lib.decode_paged_fp8(qd, *args(g), tab, lens, weights=w, workspace=ws[:n - 256])
     assert e.value.status == fa_mod.FA_ERR_WORKSPACE
     for bad in (dict(q=qd.float()), dict(q=qd[:1]), dict(q=qd[..., :32]), dict(w=w[:, :1].contiguous()), dict(w=w.double()),
                 dict(lens=lens.long()), dict(tab=tab.t())):
