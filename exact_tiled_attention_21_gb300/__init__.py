@@ -515,45 +515,32 @@ def decode(q, kcache, vcache, scale=None, num_splits=0, stream=None, workspace=N
 
 
 # ------------------------------------------------------------------ rotary positions and the 8-bit cache
+_torch_binding = None
+
+
+def _native():
+    """The native binding (csrc/fa_torch.cpp): checks, allocations and the C call in one step."""
+    global _torch_binding
+    if _torch_binding is None:
+        load()
+        try:
+            from . import _fa_torch
+        except ImportError as e:
+            raise FAError(FA_ERR_CUDA, "loading _fa_torch.so (not built; call build()): %s" % e)
+        _torch_binding = _fa_torch
+    return _torch_binding
+
+
 def _need(ok, what):
     if not ok:
         raise ValueError(what)
 
 
-def _on(t, name, dtype, shape, index):
-    """A contiguous tensor of this type and shape on this device."""
-    if t.dtype is not dtype or t.get_device() != index or t.shape != shape or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous %s tensor of shape %s on cuda:%d" % (name, dtype, tuple(shape), index))
-    return t.data_ptr()
-
-
-class _Launching:
-    """Makes the tensors' device the current one and ``stream`` torch's current stream, so that what a call allocates
-    belongs to the stream that uses it."""
-
-    def __init__(self, index, stream):
-        self.held = [torch.cuda.device(index)]
-        if stream is not None:
-            if not hasattr(stream, "cuda_stream"):
-                stream = torch.cuda.ExternalStream(int(stream), device=index)
-            self.held.append(torch.cuda.stream(stream))
-
-    def __enter__(self):
-        for c in self.held:
-            c.__enter__()
-
-    def __exit__(self, *e):
-        for c in reversed(self.held):
-            c.__exit__(*e)
-
-
-def _here(index, stream):
-    """Whether a call on tensors of device ``index`` can go ahead as things stand (else: within _Launching)."""
-    return stream is None and index == torch.cuda.current_device()
-
-
-_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
-    lambda index: torch.cuda.current_stream(index).cuda_stream)
+def _on_stream(stream, t):
+    """torch's current stream set to ``stream``, so that what a call allocates belongs to the stream that uses it."""
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=t.device)
+    return torch.cuda.stream(stream)
 
 
 def rope_frequencies(rot, base=10000.0, scaling=None, factor=1.0, original_context=None, beta_fast=32.0,
@@ -592,58 +579,18 @@ def rope_table(inv_freq, device="cuda"):
     return torch.tensor([t - (1 << 64) if t >= 1 << 63 else t for t in turns], dtype=torch.int64, device=device)
 
 
-def _bhnd(t, name, index=None):
-    """Strides of a bf16 CUDA tensor [B, H, N, d] whose innermost dimension is dense."""
-    if not (t.is_cuda and t.dtype is torch.bfloat16 and t.dim() == 4 and (index is None or t.get_device() == index)):
-        raise ValueError("%s must be a bf16 CUDA tensor [B, H, N, d]" % name)
-    s = t.stride()
-    if s[3] != 1:
-        raise ValueError("%s must be dense in its last dimension" % name)
-    return s
-
-
 def rope(x, turns, positions=None, interleaved=False, magnitude=1.0, inverse=False, out=None, stream=None):
     """x [B,H,N,d] (bf16, any strides that fa_rope takes) rotated by its tokens' positions: pairs 0 .. len(turns) - 1,
     the columns behind them copied.  turns: rope_table(...).  positions: int32 [B,N] on the device, or None (0..N-1).
     inverse=True turns back: the gradient of x from the gradient of the result.  out: where to write (may be x);
     default a new contiguous tensor."""
-    xb, xh, xn, _ = _bhnd(x, "x")
-    shape = x.shape
-    B, H, N, d = shape
-    index = x.get_device()
-    if not _here(index, stream):
-        with _Launching(index, stream):
+    if stream is not None:
+        with _on_stream(stream, x):
             return rope(x, turns, positions, interleaved, magnitude, inverse, out)
-    half = turns.shape[0] if turns.dim() == 1 else -1
-    tp = _on(turns, "turns", torch.int64, (half,), index)
-    pp = None if positions is None else _on(positions, "positions", torch.int32, (B, N), index)
-    if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=x.device)
-    else:
-        _need(out.shape == shape, "out must have x's shape")
-    yb, yh, yn, _ = _bhnd(out, "out", index)
-    _raise(load().fa_rope(x.data_ptr(), out.data_ptr(), xb, xh, xn, yb, yh, yn, pp, tp, B, H, N, d, 2 * half,
-                          bool(interleaved), magnitude, bool(inverse), _raw_stream(index)), "fa_rope")
-    return out
-
-
-def _pages(k_pages, v_pages, k_scale, v_scale, block_table, seq_lens):
-    """Checks the paged 8-bit cache; (device index, B, num_pages, Hkv, page, d, scale_block, max_pages, pointers)."""
-    _need(k_pages.is_cuda and k_pages.dim() == 4, "k_pages must be a CUDA tensor [num_pages, Hkv, page, d]")
-    _need(k_scale.dim() == 3 and block_table.dim() == 2, "k_scale must have 3 dimensions and block_table 2")
-    index = k_pages.get_device()
-    shape = k_pages.shape
-    num_pages, Hkv, page, d = shape
-    scales = k_scale.shape
-    blocks = scales[2]
-    _need(scales[0] == num_pages and scales[1] == Hkv and blocks >= 1 and page % blocks == 0,
-          "k_scale must have shape [num_pages, Hkv, a divisor of the page size]")
-    B, max_pages = block_table.shape
-    ptrs = (_on(k_pages, "k_pages", torch.uint8, shape, index), _on(v_pages, "v_pages", torch.uint8, shape, index),
-            _on(k_scale, "k_scale", torch.float32, scales, index), _on(v_scale, "v_scale", torch.float32, scales, index),
-            _on(block_table, "block_table", torch.int32, (B, max_pages), index),
-            _on(seq_lens, "seq_lens", torch.int32, (B,), index))
-    return index, B, num_pages, Hkv, page, d, page // blocks, max_pages, ptrs
+    r = (_torch_binding or _native()).rope(x, turns, positions, interleaved, magnitude, inverse, out)
+    if r.__class__ is int:
+        raise FAError(r, "fa_rope")
+    return r
 
 
 def cache_append_fp8(k, v, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, new_lens=None, turns=None,
@@ -651,26 +598,14 @@ def cache_append_fp8(k, v, k_pages, v_pages, k_scale, v_scale, block_table, seq_
     """Writes k, v [B,Hkv,N,d] (bf16, any strides that fa_rope takes) behind the seq_lens[b] tokens that the paged
     8-bit cache holds of each sequence: the first new_lens[b] of them (None: all N).  With turns, k is rotated on the
     way (positions int32 [B,N], or None: seq_lens[b] + i).  Changes the pages and scales, not seq_lens."""
-    index, B, num_pages, Hkv, page, d, sb, max_pages, ptrs = _pages(k_pages, v_pages, k_scale, v_scale, block_table,
-                                                                    seq_lens)
-    kb, kh, kn, _ = _bhnd(k, "k", index)
-    vb, vh, vn, _ = _bhnd(v, "v", index)
-    N = k.shape[2]
-    _need(k.shape == (B, Hkv, N, d) and v.shape == (B, Hkv, N, d), "k and v must have shape [B, Hkv, N, d]")
-    if not _here(index, stream):
-        with _Launching(index, stream):
+    if stream is not None:
+        with _on_stream(stream, k):
             return cache_append_fp8(k, v, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, new_lens, turns,
                                     positions, interleaved, magnitude)
-    np_ = None if new_lens is None else _on(new_lens, "new_lens", torch.int32, (B,), index)
-    half, tp, pp = 0, None, None
-    if turns is not None:
-        half = turns.shape[0] if turns.dim() == 1 else -1
-        tp = _on(turns, "turns", torch.int64, (half,), index)
-        if positions is not None:
-            pp = _on(positions, "positions", torch.int32, (B, N), index)
-    _raise(load().fa_cache_append_fp8(k.data_ptr(), v.data_ptr(), kb, kh, kn, vb, vh, vn, *ptrs, np_, pp, tp, B, Hkv, N,
-                                      d, 2 * half, bool(interleaved), magnitude, page, sb, max_pages, num_pages,
-                                      _raw_stream(index)), "fa_cache_append_fp8")
+    st = (_torch_binding or _native()).append(k, v, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, new_lens,
+                                              turns, positions, interleaved, magnitude)
+    if st != FA_OK:
+        raise FAError(st, "fa_cache_append_fp8")
 
 
 def decode_paged_fp8(q, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, scale=None, weights=None,
@@ -678,30 +613,15 @@ def decode_paged_fp8(q, k_pages, v_pages, k_scale, v_scale, block_table, seq_len
     """O [B,Hq,Nq,d] bf16 and LSE [B,Hq,Nq] fp32 of the last Nq tokens (q [B,Hq,Nq,d], or [B,Hq,d] for one, which
     gives O [B,Hq,d] and LSE [B,Hq]) over the paged 8-bit cache, which holds them already.  weights: fp32
     [B,Hkv,max_pages*page] to which every token's attention weight is added, or None."""
-    index, B, num_pages, Hkv, page, d, sb, max_pages, ptrs = _pages(k_pages, v_pages, k_scale, v_scale, block_table,
-                                                                    seq_lens)
-    if not _here(index, stream):
-        with _Launching(index, stream):
+    if stream is not None:
+        with _on_stream(stream, q):
             return decode_paged_fp8(q, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, scale, weights,
                                     None, workspace)
-    shape = q.shape
-    _need(len(shape) in (3, 4), "q must have 3 or 4 dimensions")
-    Hq, Nq = shape[1], (shape[2] if len(shape) == 4 else 1)
-    qp = _on(q, "q", torch.bfloat16, (B, Hq, Nq, d) if len(shape) == 4 else (B, Hq, d), index)
-    wp = None if weights is None else _on(weights, "weights", torch.float32, (B, Hkv, max_pages * page), index)
-    lib, device = load(), q.device
-    if workspace is None:
-        nbytes = lib.fa_decode_paged_fp8_workspace_bytes(B, Hq, Hkv, Nq, d, max_pages * page, weights is not None)
-        workspace = torch.empty((nbytes,), dtype=torch.uint8, device=device)
-    else:
-        nbytes = workspace.numel() * workspace.element_size()
-        _need(workspace.get_device() == index and workspace.is_contiguous(), "workspace must be contiguous, on q's device")
-    o = torch.empty(shape, dtype=torch.bfloat16, device=device)
-    lse = torch.empty(shape[:-1], dtype=torch.float32, device=device)
-    _raise(lib.fa_decode_paged_fp8(qp, *ptrs, o.data_ptr(), lse.data_ptr(), wp, B, Hq, Hkv, Nq, page, sb, max_pages,
-                                   num_pages, d, d ** -0.5 if scale is None else scale,
-                                   workspace.data_ptr(), nbytes, _raw_stream(index)), "fa_decode_paged_fp8")
-    return o, lse
+    r = (_torch_binding or _native()).decode(q, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, scale,
+                                             weights, workspace)
+    if r.__class__ is int:
+        raise FAError(r, "fa_decode_paged_fp8")
+    return r
 
 
 def cache_evict_fp8(k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, weights, new_table, keep, recent=0,
@@ -710,20 +630,12 @@ def cache_evict_fp8(k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, w
     accumulated weight into the pages of new_table (int32 [B, new_max_pages], disjoint from the pages read).  Returns
     (new_lens int32 [B], new_weights fp32 and kept int32 [B,Hkv,new_max_pages*page]): the kept tokens' weights and
     source indices, 0 and -1 behind them."""
-    index, B, num_pages, Hkv, page, d, sb, max_pages, ptrs = _pages(k_pages, v_pages, k_scale, v_scale, block_table,
-                                                                    seq_lens)
-    if not _here(index, stream):
-        with _Launching(index, stream):
+    if stream is not None:
+        with _on_stream(stream, k_pages):
             return cache_evict_fp8(k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, weights, new_table, keep,
                                    recent)
-    wp = _on(weights, "weights", torch.float32, (B, Hkv, max_pages * page), index)
-    new_max_pages = new_table.shape[1] if new_table.dim() == 2 else -1
-    tp = _on(new_table, "new_table", torch.int32, (B, new_max_pages), index)
-    device = k_pages.device
-    new_lens = torch.empty((B,), dtype=torch.int32, device=device)
-    new_weights = torch.empty((B, Hkv, new_max_pages * page), dtype=torch.float32, device=device)
-    kept = torch.empty((B, Hkv, new_max_pages * page), dtype=torch.int32, device=device)
-    _raise(load().fa_cache_evict_fp8(*ptrs, wp, tp, new_lens.data_ptr(), new_weights.data_ptr(), kept.data_ptr(), B, Hkv,
-                                     page, sb, max_pages, new_max_pages, num_pages, d, keep, recent,
-                                     _raw_stream(index)), "fa_cache_evict_fp8")
-    return new_lens, new_weights, kept
+    r = (_torch_binding or _native()).evict(k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, weights,
+                                            new_table, keep, recent)
+    if r.__class__ is int:
+        raise FAError(r, "fa_cache_evict_fp8")
+    return r

@@ -35,6 +35,7 @@
 // own bf16 step) with its own running maximum M, so that a block's scale can
 // have any size.  Result: O 2^(M - m) / l.
 #include <algorithm>
+#include <cfloat>
 #include <climits>
 
 #include "fa_e4m3.cuh"
@@ -55,12 +56,16 @@ struct Cfg {
     static constexpr int SLOT = 2 * HALF + 8 * KEYS;    // K, V, K scales, log2 of V scales
     static constexpr int RING = STAGES * SLOT;          // per warp
     static constexpr int ROWS = 8 * NB;                 // query rows per tile
-    static constexpr int OROW = D + 4;                  // row of the merge buffer (in the ring), floats
-    static constexpr bool QSMEM = NB > 2;               // Q fragments in shared memory instead of registers
-    static constexpr int QBYTES = QSMEM ? ROWS * D * 2 : 0;
-    static constexpr int SMEM = kWarps * RING + QBYTES;
-    static constexpr int CTAS = NB > 2 ? 2 : 3;         // per SM (255 and 168 registers)
-    static_assert(ROWS * OROW * 4 <= RING, "merge buffer");
+    static constexpr int OROW = D + 4;                  // row of a merge buffer, floats
+    static constexpr int BUFS = NB > 2 ? 1 : kWarps;    // merge buffers: one for each warp, or one in turn
+    static constexpr int MERGE = kWarps * RING;         // byte offsets of the merge buffers
+    static constexpr int QFRAGS = MERGE + BUFS * ROWS * OROW * 4;  // and of Q's fragments,
+    static constexpr bool QSMEM = NB > 2;                          // which NB <= 2 has in registers
+    static constexpr int SMEM = QFRAGS + (QSMEM ? ROWS * D * 2 : 0);
+    // Registers: three CTAs' worth where that is enough.  Two run per SM: memory alone takes as long with one (128k
+    // tokens: 51 us), and computing on top 68 us with one, 55 with two, 58 with three.
+    static constexpr int REGS_FOR = NB > 1 ? 2 : 3, CTAS = 2;
+    static_assert(CTAS * (SMEM + 4096) <= 227 * 1024, "shared memory");
 };
 
 struct Params {
@@ -120,6 +125,27 @@ __device__ __forceinline__ void find_sequence(const int* lens, int B, int cap, l
     if (prefix && lane == 0) prefix[B] = base;
 }
 
+// A position in the list of steps.
+struct Cursor {
+    int b, len, n;        // sequence, its length and steps
+    int kvh, rt, s;       // kv head, row tile and step
+};
+
+template <int STEP>
+__device__ __forceinline__ void advance(Cursor& c, const Params& a, int cap) {
+    if (++c.s < c.n) return;
+    c.s = 0;
+    if (++c.rt < a.row_tiles) return;
+    c.rt = 0;
+    if (++c.kvh < a.Hkv) return;
+    c.kvh = 0;
+    do {
+        ++c.b;
+        c.len = c.b < a.B ? clamp_len(__ldg(a.lens + c.b), cap) : 0;
+    } while (c.len == 0 && c.b < a.B);
+    c.n = (c.len + STEP - 1) / STEP;
+}
+
 // Where the scores [key][rows of the tile] of a tile begin.  A (sequence, kv head)'s rows are padded to a multiple of
 // four, so that a tile with a multiple of two or four rows has its scores of a key aligned to as many.
 template <int ROWS>
@@ -128,11 +154,11 @@ __device__ __forceinline__ long long scores_at(const Params& a, long long bh, in
 }
 
 template <int D, int NB>
-__global__ void __launch_bounds__(kThreads, Cfg<D, NB>::CTAS) decode_fp8_kernel(const Params a) {
+__global__ void __launch_bounds__(kThreads, Cfg<D, NB>::REGS_FOR) decode_fp8_kernel(const Params a) {
     using C = Cfg<D, NB>;
     constexpr int KEYS = C::KEYS, MT = KEYS / 16, KS = D / 16, DT = D / 8, ROWS = C::ROWS, STEP = C::STEP;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ float s_stat[kWarps][3][ROWS];
+    __shared__ float s_stat[kWarps][2][ROWS];  // m and l
     __shared__ float s_up[ROWS];
     pdl_launch_dependents();
     pdl_wait();
@@ -155,31 +181,24 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::CTAS) decode_fp8_kernel(
         u = blockIdx.x * total / workers;
         u1 = (blockIdx.x + 1ll) * total / workers;
     }
+    Cursor cur;
+    {
+        long long start;
+        find_sequence<STEP>(a.lens, a.B, cap, u / per_step, nullptr, cur.b, start, cur.len);
+        cur.n = (cur.len + STEP - 1) / STEP;
+        const long long in_b = u - start * per_step;
+        const int item_b = (int)(in_b / cur.n);
+        cur.s = (int)(in_b - (long long)item_b * cur.n);
+        cur.kvh = item_b / a.row_tiles;
+        cur.rt = item_b - cur.kvh * a.row_tiles;
+    }
+    const int count = (int)min(u1 - u, (long long)INT_MAX);  // steps (2^47 in all / workers; far below 2^31 in memory)
+
+    // ---- the ring: this warp's keys of the steps ahead, whatever item they are of
     bool bad = false;
     uint8_t* ring = smem + warp * C::RING;
     const uint32_t ring_u = smem_u32(ring);
-    uint2* qsm = reinterpret_cast<uint2*>(smem + kWarps * C::RING);
-
-    while (u < u1) {
-    int b, len;
-    long long start;
-    find_sequence<STEP>(a.lens, a.B, cap, u / per_step, nullptr, b, start, len);
-    const uint32_t n = (uint32_t)(len + STEP - 1) / STEP;          // steps of the sequence
-    const long long in_b = u - start * per_step;
-    const int item_b = (int)(in_b / n), s0 = (int)(in_b - (long long)item_b * n);
-    const int s1 = (int)min((long long)n, s0 + (u1 - u));          // the segment: steps [s0, s1) of the item
-    const int kvh = item_b / a.row_tiles, rt = item_b - kvh * a.row_tiles;
-    const int k0 = s0 * STEP, k1 = min(s1 * STEP, len);
-    const int r0 = rt * ROWS, nrows = min(ROWS, a.rows - r0);      // query rows of the tile
-    const long long row0 = ((long long)b * a.Hkv + kvh) * a.rows + r0;  // (b, head, token) flattened
-    const long long slot_out = blockIdx.x + (long long)b * per_step + item_b;
-    const bool whole = s0 == 0 && s1 == (int)n;
-    u += s1 - s0;
-
-    // ---- the ring
-    const int* trow = a.table + (long long)b * a.max_pages;
-    const int first = k0 + warp * KEYS;                       // this warp's first key
-    const int steps = first < k1 ? (k1 - first + STEP - 1) / STEP : 0;
+    uint2* qsm = reinterpret_cast<uint2*>(smem + C::QFRAGS);
     // A copy instruction moves whole rows (D / 16 lanes a row, so that a quarter warp asks for 128 consecutive bytes);
     // the fragments' readers find their 16 bytes (V at D = 64: 8) at
     //   K: (key / 8, half h of D = 128, lane' = 4 (key % 8) + t), lane' ^ 4 h
@@ -204,12 +223,23 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::CTAS) decode_fp8_kernel(
     }
     using Keys = int[KEYS / 32];     // of lane's key (+ 32) of a step
     using Scales = float[KEYS / 32];
-    auto fetch_pages = [&](int it, Keys& pg) {
+    Cursor ahead = cur;            // the step after those in `to_issue`
+    int fetched = 0, issued = 0;
+    struct {
+        Keys page;                 // pages of the lane's keys, loaded one step before their use
+        int key0, len, kvh;
+    } to_issue;
+    auto fetch_pages = [&]() {
+        to_issue.key0 = ahead.s * STEP + warp * KEYS;
+        to_issue.len = ahead.len;
+        to_issue.kvh = ahead.kvh;
+        const int* trow = a.table + (long long)ahead.b * a.max_pages;
 #pragma unroll
         for (int i = 0; i < KEYS / 32; ++i) {
-            const int key = first + it * STEP + i * 32 + lane;
-            pg[i] = (it < steps && key < k1) ? trow[a.page.div(key)] : -1;
+            const int key = to_issue.key0 + i * 32 + lane;
+            to_issue.page[i] = (fetched < count && key < ahead.len) ? trow[a.page.div(key)] : -1;
         }
+        if (++fetched < count) advance<STEP>(ahead, a, cap);
     };
     // Scales are loaded, not copied (a 4-byte copy asks L2 once per lane, a load once per sector), and put into the
     // ring one step later, when they have arrived; V's as logarithms.
@@ -240,19 +270,19 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::CTAS) decode_fp8_kernel(
             cp_async16(base + vdst[n & 1] + vo, vp + off, ok);
         }
     };
-    auto issue = [&](int it, int slot, const Keys& pages, Scales& ks, Scales& vs) {
-        if (it < steps) {
+    auto issue = [&](int slot, Scales& ks, Scales& vs) {
+        if (issued < count) {
             uint32_t row[KEYS / 32];  // cache row of key lane (+ 32), ~0 for none
             bool all = true;
 #pragma unroll
             for (int i = 0; i < KEYS / 32; ++i) {
-                const int key = first + it * STEP + i * 32 + lane;
-                const int pg = pages[i];
-                const bool in = key < k1, ok = in && (unsigned)pg < (unsigned)a.num_pages;
+                const int key = to_issue.key0 + i * 32 + lane;
+                const int pg = to_issue.page[i];
+                const bool in = key < to_issue.len, ok = in && (unsigned)pg < (unsigned)a.num_pages;
                 bad |= in && !ok;
                 all &= ok;
                 const uint32_t at = (uint32_t)key - a.page.div(key) * P;
-                const uint32_t head = (uint32_t)pg * a.Hkv + kvh;
+                const uint32_t head = (uint32_t)pg * a.Hkv + to_issue.kvh;
                 row[i] = ok ? head * P + at : ~0u;
                 const uint32_t blk = ok ? head * a.blocks_per_page + a.sb.div(at) : 0u;
                 ks[i] = ok ? __ldg(a.ks + blk) : 0.f;
@@ -263,35 +293,45 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::CTAS) decode_fp8_kernel(
             else
                 copy(ring_u + slot * C::SLOT, row, false);
         }
+        ++issued;
         cp_async_commit();
     };
-    Keys pg_next;             // pages of the step after those in flight
     Scales ks_next, vs_next;  // scales of the step issued last
+    static_assert(C::STAGES == 2, "the start below");
     {
-        Keys pg[C::STAGES];
-        Scales ks[C::STAGES], vs[C::STAGES];
+        Scales ks, vs;
+        fetch_pages();
+        auto first = to_issue;
+        fetch_pages();
+        auto second = to_issue;
+        fetch_pages();
+        const auto third = to_issue;
+        to_issue = first;
 #pragma unroll
-        for (int s = 0; s < C::STAGES; ++s) fetch_pages(s, pg[s]);
-        fetch_pages(C::STAGES, pg_next);
-#pragma unroll
-        for (int s = 0; s < C::STAGES; ++s) {
-#pragma unroll
-            for (int i = 0; i < KEYS / 32; ++i) ks[s][i] = vs[s][i] = 0.f;
-            issue(s, s, pg[s], ks[s], vs[s]);
-        }
-#pragma unroll
-        for (int s = 0; s + 1 < C::STAGES; ++s) put_scales(s, ks[s], vs[s]);
-#pragma unroll
-        for (int i = 0; i < KEYS / 32; ++i) {
-            ks_next[i] = ks[C::STAGES - 1][i];
-            vs_next[i] = vs[C::STAGES - 1][i];
-        }
+        for (int i = 0; i < KEYS / 32; ++i) ks[i] = vs[i] = ks_next[i] = vs_next[i] = 0.f;
+        issue(0, ks, vs);
+        to_issue = second;
+        issue(1, ks_next, vs_next);
+        to_issue = third;
+        put_scales(0, ks, vs);
     }
 
-    // ---- Q fragments: k-step s of lane (g, t) is row g, columns (D = 128: 64 (s / 4) +) 16 t + 4 (s % 4) .. + 3
+    // ---- what a segment holds
     uint32_t qb[C::QSMEM ? 1 : NB][KS][2];
     float sc[NB][2];  // score scale of the rows whose scores this lane holds: 8 nb + 2 t, + 1
-    int lim[NB][2];   // and the keys that they see: j < lim
+    float acc[D / 16][NB][4];
+    float m[NB][2], M[NB][2], l[NB][2];  // of rows 8 nb + 2 t + j; the maxima start at the lowest number: a row
+                                         // that sees no key keeps l = 0 (2^(-inf - m))
+    int seg = 0;  // first step of the segment within its item
+    bool begins = true;
+    int slot = 0;
+    for (int it = 0; it < count; ++it) {
+    const int r0 = cur.rt * ROWS, nrows = min(ROWS, a.rows - r0);      // query rows of the tile
+    const long long bh = (long long)cur.b * a.Hkv + cur.kvh;
+    const long long row0 = bh * a.rows + r0;                           // (b, head, token) flattened
+    if (begins) {
+    seg = cur.s;
+    // ---- Q fragments: k-step s of lane (g, t) is row g, columns (D = 128: 64 (s / 4) +) 16 t + 4 (s % 4) .. + 3
 #pragma unroll
     for (int f = 0; f < (C::QSMEM ? 1 : NB); ++f) {
         const int nb = C::QSMEM ? warp : f;  // in shared memory each warp makes one column tile
@@ -339,35 +379,28 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::CTAS) decode_fp8_kernel(
             for (int j = 0; j < 2; ++j) sc[f][j] = __shfl_sync(0xffffffffu, up, (2 * t + j) * 4);
         }
     }
-    if constexpr (C::QSMEM) __syncthreads();
+    if constexpr (C::QSMEM) {
+        __syncthreads();
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            if constexpr (C::QSMEM) sc[nb][j] = s_up[nb * 8 + 2 * t + j];
-            lim[nb][j] = min(k1, len - a.Nq + (r0 + nb * 8 + 2 * t + j) % a.Nq + 1);
-        }
-
-    float acc[D / 16][NB][4];
+        for (int nb = 0; nb < NB; ++nb) sc[nb][0] = s_up[nb * 8 + 2 * t], sc[nb][1] = s_up[nb * 8 + 2 * t + 1];
+    }
 #pragma unroll
     for (int i = 0; i < D / 16; ++i)
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
             for (int c = 0; c < 4; ++c) acc[i][nb][c] = 0.f;
-    float m[NB][2], M[NB][2], l[NB][2];  // of rows 8 nb + 2 t + j
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) m[nb][j] = M[nb][j] = -INFINITY, l[nb][j] = 0.f;
+        for (int j = 0; j < 2; ++j) m[nb][j] = M[nb][j] = -FLT_MAX, l[nb][j] = 0.f;
+    }
 
-    int slot = 0;
-    for (int it = 0; it < steps; ++it) {
-        put_scales(slot == 0 ? C::STAGES - 1 : slot - 1, ks_next, vs_next);
+    const int key0 = cur.s * STEP + warp * KEYS;
         cp_async_wait<C::STAGES - 1>();
         __syncwarp();  // every lane's copies are there
         const uint8_t* st = ring + slot * C::SLOT;
-        const int key0 = first + it * STEP;
+        if (key0 < cur.len) {
         float S[MT][NB][4];  // keys 16 i + g, + 8 (c / 2) of rows 8 nb + 2 t + c % 2
         const uint4* kf = reinterpret_cast<const uint4*>(st);
 #pragma unroll
@@ -416,22 +449,26 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::CTAS) decode_fp8_kernel(
                     S[i][nb][2 * h + 1] *= sc[nb][1] * kscale;
                 }
             }
-        if (key0 + KEYS > min(k1, len - a.Nq + 1)) {  // some row does not see every key
+        if (key0 + KEYS > cur.len - a.Nq + 1) {  // some row does not see every key
 #pragma unroll
-            for (int i = 0; i < MT; ++i)
+            for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                for (int nb = 0; nb < NB; ++nb)
+                for (int j = 0; j < 2; ++j) {
+                    const int lim = cur.len - a.Nq + (r0 + nb * 8 + 2 * t + j) % a.Nq + 1 - key0 - g;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        if (key0 + i * 16 + (c >> 1) * 8 + g >= lim[nb][c & 1]) S[i][nb][c] = -INFINITY;
+                    for (int i = 0; i < MT; ++i)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            if (i * 16 + h * 8 >= lim) S[i][nb][2 * h + j] = -INFINITY;
+                }
         }
         if (a.scores) {  // [key][row of the tile]: a lane's two rows are neighbours
-            float* sr = a.scores + scores_at<ROWS>(a, (long long)b * a.Hkv + kvh, rt, cap) + (long long)(key0 + g) * nrows + 2 * t;
+            float* sr = a.scores + scores_at<ROWS>(a, bh, cur.rt, cap) + (long long)(key0 + g) * nrows + 2 * t;
 #pragma unroll
             for (int i = 0; i < MT; ++i)
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
-                    if (key0 + i * 16 + h * 8 + g < k1)
+                    if (key0 + i * 16 + h * 8 + g < cur.len)
 #pragma unroll
                         for (int nb = 0; nb < NB; ++nb) {
                             float* at = sr + (i * 16 + h * 8) * nrows + nb * 8;
@@ -445,7 +482,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::CTAS) decode_fp8_kernel(
                         }
         }
         // ---- softmax: p = 2^(x - m) into l; w = 2^(x + log2 vs - M) for the value product
-        float base[NB][2];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -455,8 +491,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::CTAS) decode_fp8_kernel(
                 for (int i = 0; i < MT; ++i) mx = fmax3(mx, S[i][nb][j], S[i][nb][2 + j]);
 #pragma unroll
                 for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-                base[nb][j] = mx == -INFINITY ? 0.f : mx;
-                l[nb][j] *= ex2(m[nb][j] - base[nb][j]);
+                l[nb][j] *= ex2(m[nb][j] - mx);
                 m[nb][j] = mx;
             }
 #pragma unroll
@@ -468,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::CTAS) decode_fp8_kernel(
                 for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        l[nb][j] += ex2(S[i][nb][2 * h + j] - base[nb][j]);
+                        l[nb][j] += ex2(S[i][nb][2 * h + j] - m[nb][j]);
                         S[i][nb][2 * h + j] += lv;
                     }
             }
@@ -492,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::CTAS) decode_fp8_kernel(
                 float f[2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    f[j] = Mx[nb][j] == -INFINITY ? 0.f : ex2(M[nb][j] - Mx[nb][j]);
+                    f[j] = ex2(M[nb][j] - Mx[nb][j]);
                     M[nb][j] = Mx[nb][j];
                 }
 #pragma unroll
@@ -504,12 +539,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::CTAS) decode_fp8_kernel(
         uint32_t pb[MT][NB][2];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-            const float b0 = M[nb][0] == -INFINITY ? 0.f : M[nb][0], b1 = M[nb][1] == -INFINITY ? 0.f : M[nb][1];
 #pragma unroll
             for (int i = 0; i < MT; ++i)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const __half2 w = __floats2half2_rn(ex2(S[i][nb][2 * h] - b0), ex2(S[i][nb][2 * h + 1] - b1));
+                    const __half2 w = __floats2half2_rn(ex2(S[i][nb][2 * h] - M[nb][0]),
+                                                        ex2(S[i][nb][2 * h + 1] - M[nb][1]));
                     pb[i][nb][h] = transpose8x8(*reinterpret_cast<const uint32_t*>(&w));
                 }
         }
@@ -540,61 +575,98 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::CTAS) decode_fp8_kernel(
                     for (int nb = 0; nb < NB; ++nb) mma_16816(acc[2 * c + h][nb], va, pb[i][nb][0], pb[i][nb][1]);
                 }
         }
+        }
+        put_scales(slot ^ 1, ks_next, vs_next);
         __syncwarp();  // every lane has read this slot
-        issue(it + C::STAGES, slot, pg_next, ks_next, vs_next);
-        fetch_pages(it + C::STAGES + 1, pg_next);
-        slot = slot + 1 == C::STAGES ? 0 : slot + 1;
+        issue(slot, ks_next, vs_next);
+        fetch_pages();
+        slot ^= 1;
+
+    // ---- at the segment's end, merge the warps: O = sum_w O_w 2^(M_w - m) / l
+    const bool item_ends = cur.s + 1 == cur.n;
+    begins = item_ends || it + 1 == count;
+    if (begins) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int r = nb * 8 + 2 * t + j;
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) l[nb][j] += __shfl_xor_sync(0xffffffffu, l[nb][j], d);
+                if (g == 0) s_stat[warp][0][r] = m[nb][j], s_stat[warp][1][r] = l[nb][j];
+            }
+        __syncthreads();
+        float f[NB][2];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int r = nb * 8 + 2 * t + j;
+                float top = s_stat[0][0][r];
+#pragma unroll
+                for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s_stat[w][0][r]);
+                f[nb][j] = ex2(M[nb][j] - top);
+            }
+        float* buf = reinterpret_cast<float*>(smem + C::MERGE) + (warp % C::BUFS) * ROWS * C::OROW;
+#pragma unroll 1
+        for (int turn = 0; turn < kWarps / C::BUFS; ++turn) {
+            if (warp / C::BUFS == turn) {
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int i = 0; i < D / 16; ++i) {
+                            float2* at = reinterpret_cast<float2*>(buf + (nb * 8 + 2 * t + j) * C::OROW + g * DT + 2 * i);
+                            float2 x = make_float2(acc[i][nb][j] * f[nb][j], acc[i][nb][2 + j] * f[nb][j]);
+                            if (turn) {
+                                const float2 y = *at;
+                                x.x += y.x;
+                                x.y += y.y;
+                            }
+                            *at = x;
+                        }
+            }
+            __syncthreads();
+        }
+        const bool whole = seg == 0 && item_ends;
+        const long long slot_out = blockIdx.x + bh * a.row_tiles + cur.rt;
+        for (int i = tid; i < nrows * (D / 4); i += kThreads) {
+            const int r = i / (D / 4), c = (i % (D / 4)) * 4;
+            float top = s_stat[0][0][r];
+#pragma unroll
+            for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s_stat[w][0][r]);
+            float sum = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) sum += s_stat[w][1][r] * ex2(s_stat[w][0][r] - top);
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;  // 0: the row sees no key; NaN stays
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < C::BUFS; ++w) {
+                const float4 x = *reinterpret_cast<const float4*>(smem + C::MERGE + ((w * ROWS + r) * C::OROW + c) * 4);
+                o.x += x.x;
+                o.y += x.y;
+                o.z += x.z;
+                o.w += x.w;
+            }
+            o.x *= inv;
+            o.y *= inv;
+            o.z *= inv;
+            o.w *= inv;
+            const float lse2 = sum == 0.f ? -INFINITY : top + lg2(sum);
+            if (whole) {
+                *reinterpret_cast<uint2*>(a.o + (row0 + r) * D + c) = make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
+                if (a.lse && c == 0) a.lse[row0 + r] = lse2 * kLn2;
+            } else {
+                *reinterpret_cast<float4*>(a.part_o + (slot_out * ROWS + r) * D + c) = o;
+            }
+            if (c == 0) a.part_lse[slot_out * ROWS + r] = lse2;
+        }
+        __syncthreads();  // the buffers and Q are the next segment's
+    }
+    if (it + 1 < count) advance<STEP>(cur, a, cap);
     }
     cp_async_wait<0>();
-
-    // ---- merge the warps: O = sum_w O_w 2^(M_w - m) / l
-    __syncwarp();
-    float* mine = reinterpret_cast<float*>(ring);
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int r = nb * 8 + 2 * t + j;
-#pragma unroll
-            for (int d = 4; d < 32; d <<= 1) l[nb][j] += __shfl_xor_sync(0xffffffffu, l[nb][j], d);
-            if (g == 0) s_stat[warp][0][r] = m[nb][j], s_stat[warp][1][r] = l[nb][j], s_stat[warp][2][r] = M[nb][j];
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i)
-                *reinterpret_cast<float2*>(mine + r * C::OROW + g * DT + 2 * i) =
-                    make_float2(acc[i][nb][j], acc[i][nb][2 + j]);
-        }
-    __syncthreads();
-    for (int i = tid; i < nrows * (D / 4); i += kThreads) {
-        const int r = i / (D / 4), c = (i % (D / 4)) * 4;
-        float m = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) m = fmaxf(m, s_stat[w][0][r]);
-        const float base = m == -INFINITY ? 0.f : m;
-        float l = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) l += s_stat[w][1][r] * ex2(s_stat[w][0][r] - base);
-        const float inv = l == 0.f ? 0.f : 1.f / l;  // 0: the row sees no key; NaN stays
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            const float4 x = *reinterpret_cast<const float4*>(smem + w * C::RING + (r * C::OROW + c) * 4);
-            const float f = ex2(s_stat[w][2][r] - base) * inv;
-            o.x = fmaf(x.x, f, o.x);
-            o.y = fmaf(x.y, f, o.y);
-            o.z = fmaf(x.z, f, o.z);
-            o.w = fmaf(x.w, f, o.w);
-        }
-        const float lse2 = l == 0.f ? -INFINITY : m + lg2(l);
-        if (whole) {
-            *reinterpret_cast<uint2*>(a.o + (row0 + r) * D + c) = make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
-            if (a.lse && c == 0) a.lse[row0 + r] = lse2 * kLn2;
-        } else {
-            *reinterpret_cast<float4*>(a.part_o + (slot_out * ROWS + r) * D + c) = o;
-        }
-        if (c == 0) a.part_lse[slot_out * ROWS + r] = lse2;
-    }
-    __syncthreads();  // the merge buffers are the next segment's ring
-    }
     if (__any_sync(0xffffffffu, bad) && lane == 0) record_invalid(a.err, kSiteCacheTable, -1);
 }
 
@@ -625,12 +697,12 @@ __device__ __forceinline__ float merge_lse(const float* pl, int stride, int segs
     return sum;
 }
 
-constexpr int kFinishThreads = 128;
+constexpr int kFinishThreads = 128, kWeightTokens = 4;  // tokens per thread of the weights
 
 // Blocks below `row_blocks`: one row each; LSE = M + log2 sum 2^(lse_s - M), O = sum 2^(lse_s - M) o_s / sum, the
 // segments dealt to groups of D / 4 threads.  A row without keys gets O = 0, LSE = -inf; a row whose item was one
 // segment is already written.
-// The others, with weights: 128 tokens of one (sequence, kv head) each; weights[j] += sum over the rows of
+// The others, with weights: 512 tokens of one (sequence, kv head) each; weights[j] += sum over the rows of
 // 2^(x_j - LSE), one thread per token, in a fixed order.
 template <int D, int ROWS>
 __global__ void __launch_bounds__(kFinishThreads) finish_fp8_kernel(const Params a, unsigned row_blocks, int weight_blocks) {
@@ -639,7 +711,7 @@ __global__ void __launch_bounds__(kFinishThreads) finish_fp8_kernel(const Params
     __shared__ float4 s_o[GROUPS][LANES];
     pdl_launch_dependents();
     pdl_wait();
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x;
     if (blockIdx.x < row_blocks) {
         const long long row = blockIdx.x, bh = row / a.rows;
         const int r = (int)(row - bh * a.rows), b = (int)(bh / a.Hkv), rt = r / ROWS;
@@ -691,35 +763,55 @@ __global__ void __launch_bounds__(kFinishThreads) finish_fp8_kernel(const Params
     const unsigned idx = blockIdx.x - row_blocks;
     const long long bh = idx / weight_blocks;
     const int b = (int)(bh / a.Hkv), kvh = (int)(bh % a.Hkv), cap = a.max_pages * (int)a.page.d;
-    const int len = clamp_len(a.lens[b], cap), j0 = (int)(idx % weight_blocks) * kFinishThreads;
+    const int len = clamp_len(a.lens[b], cap), j0 = (int)(idx % weight_blocks) * kFinishThreads * kWeightTokens;
     if (j0 >= len) return;
-    for (int r = warp; r < a.rows; r += kFinishThreads / 32) {
+    // the rows' LSEs, a tile at a time: kFinishThreads / ROWS lanes per row
+    constexpr int LPR = kFinishThreads / ROWS;
+    for (int rt = 0; rt < a.row_tiles; ++rt) {
         long long slot = 0;
-        const int segs = find_segments(a, b, kvh * a.row_tiles + r / ROWS, slot);
-        float base;
-        const float sum = merge_lse(a.part_lse + slot * ROWS + r % ROWS, ROWS, segs, base);
-        if (lane == 0) s_lse[r] = sum == 0.f ? INFINITY : base + lg2(sum);  // no keys: every weight 2^-inf = 0
+        const int segs = find_segments(a, b, kvh * a.row_tiles + rt, slot);
+        const int r = tid / LPR;
+        const float* pl = a.part_lse + slot * ROWS + r;
+        const bool row = rt * ROWS + r < a.rows;
+        float M = -FLT_MAX, sum = 0.f;
+        for (int s = tid % LPR; row && s < segs; s += LPR) M = fmaxf(M, pl[(long long)s * ROWS]);
+#pragma unroll
+        for (int w = LPR / 2; w >= 1; w >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
+        for (int s = tid % LPR; row && s < segs; s += LPR) sum += ex2(pl[(long long)s * ROWS] - M);
+#pragma unroll
+        for (int w = LPR / 2; w >= 1; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+        if (row && tid % LPR == 0) s_lse[rt * ROWS + r] = sum == 0.f ? INFINITY : M + lg2(sum);  // no keys: 2^-inf = 0
     }
     __syncthreads();
-    const int j = j0 + tid;
-    if (j >= len) return;
-    float* w = a.weights + bh * cap + j;
-    float sum = 0.f;
-    const float before = *w;
+    float sum[kWeightTokens], before[kWeightTokens];
+    float* w = a.weights + bh * cap + j0 + tid;
+#pragma unroll
+    for (int i = 0; i < kWeightTokens; ++i) {
+        sum[i] = 0.f;
+        before[i] = j0 + tid + i * kFinishThreads < len ? w[i * kFinishThreads] : 0.f;
+    }
     for (int rt = 0; rt < a.row_tiles; ++rt) {
         const int nrows = min(ROWS, a.rows - rt * ROWS);
-        const float* sr = a.scores + scores_at<ROWS>(a, bh, rt, cap) + (long long)j * nrows;
+        const float* sr = a.scores + scores_at<ROWS>(a, bh, rt, cap);
         const float* z = s_lse + rt * ROWS;
-        if ((nrows & 3) == 0) {
-            for (int r = 0; r < nrows; r += 4) {
-                const float4 x = *reinterpret_cast<const float4*>(sr + r);
-                sum += (ex2(x.x - z[r]) + ex2(x.y - z[r + 1])) + (ex2(x.z - z[r + 2]) + ex2(x.w - z[r + 3]));
+#pragma unroll
+        for (int i = 0; i < kWeightTokens; ++i) {
+            const int j = j0 + tid + i * kFinishThreads;
+            if (j >= len) continue;
+            const float* x = sr + (long long)j * nrows;
+            if ((nrows & 3) == 0) {
+                for (int r = 0; r < nrows; r += 4) {
+                    const float4 v = *reinterpret_cast<const float4*>(x + r);
+                    sum[i] += (ex2(v.x - z[r]) + ex2(v.y - z[r + 1])) + (ex2(v.z - z[r + 2]) + ex2(v.w - z[r + 3]));
+                }
+            } else {
+                for (int r = 0; r < nrows; ++r) sum[i] += ex2(x[r] - z[r]);
             }
-        } else {
-            for (int r = 0; r < nrows; ++r) sum += ex2(sr[r] - z[r]);
         }
     }
-    *w = before + sum;
+#pragma unroll
+    for (int i = 0; i < kWeightTokens; ++i)
+        if (j0 + tid + i * kFinishThreads < len) w[i * kFinishThreads] = before[i] + sum[i];
 }
 
 template <int D, int NB>
@@ -761,7 +853,8 @@ cudaError_t launch_d(const PagedDecodeFp8Launch& a, cudaStream_t s) {
     p.workers = (int)std::min<long long>(a.workers, bh * p.row_tiles * ((cap + C::STEP - 1) / C::STEP));
     e = launch_dependent(decode_fp8_kernel<D, NB>, dim3(p.workers), dim3(kThreads), C::SMEM, s, p);
     if (e != cudaSuccess) return e;
-    const int weight_blocks = a.weights ? (cap + kFinishThreads - 1) / kFinishThreads : 0;
+    constexpr int per_block = kFinishThreads * kWeightTokens;
+    const int weight_blocks = a.weights ? (cap + per_block - 1) / per_block : 0;
     const long long row_blocks = bh * p.rows, blocks = row_blocks + bh * weight_blocks;
     if (blocks > 0x7FFFFFFFll) return cudaErrorInvalidValue;
     return launch_dependent(finish_fp8_kernel<D, C::ROWS>, dim3((unsigned)blocks), dim3(kFinishThreads),
@@ -773,7 +866,9 @@ cudaError_t blocks_per_sm(int* blocks) {
     using C = Cfg<D, NB>;
     const cudaError_t e = set_smem_limit_once<decode_fp8_kernel<D, NB>>(C::SMEM);
     if (e != cudaSuccess) return e;
-    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(blocks, decode_fp8_kernel<D, NB>, kThreads, C::SMEM);
+    const cudaError_t f = cudaOccupancyMaxActiveBlocksPerMultiprocessor(blocks, decode_fp8_kernel<D, NB>, kThreads, C::SMEM);
+    *blocks = std::min(*blocks, C::CTAS);
+    return f;
 }
 
 }  // namespace
