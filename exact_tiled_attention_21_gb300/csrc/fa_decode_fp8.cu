@@ -45,6 +45,7 @@ namespace fa {
 namespace {
 
 constexpr int kWarps = 4, kThreads = kWarps * 32;
+constexpr float kSlack = 8.f;  // how far (log2) a score may exceed the reference that its weight is relative to
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
 
 template <int D, int NB>
@@ -56,7 +57,8 @@ struct Cfg {
     static constexpr int SLOT = 2 * HALF + 8 * KEYS;    // K, V, K scales, log2 of V scales
     static constexpr int RING = STAGES * SLOT;          // per warp
     static constexpr int ROWS = 8 * NB;                 // query rows per tile
-    static constexpr int OROW = D + 4;                  // row of a merge buffer, floats
+    static constexpr int OROW = D + 4;                  // row of a merge buffer, floats; within it column d (of 8 runs of
+                                                        // D / 8: g, then 2 i + e) is at 16 i + 2 g + e: no bank conflicts
     static constexpr int BUFS = NB > 2 ? 1 : kWarps;    // merge buffers: one for each warp, or one in turn
     static constexpr int MERGE = kWarps * RING;         // byte offsets of the merge buffers
     static constexpr int QFRAGS = MERGE + BUFS * ROWS * OROW * 4;  // and of Q's fragments,
@@ -159,7 +161,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::REGS_FOR) decode_fp8_ker
     constexpr int KEYS = C::KEYS, MT = KEYS / 16, KS = D / 16, DT = D / 8, ROWS = C::ROWS, STEP = C::STEP;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float s_stat[kWarps][2][ROWS];  // m and l
-    __shared__ float s_up[ROWS];
+    __shared__ __align__(8) float s_up[ROWS];
+    __shared__ Cursor s_ahead[kWarps];
     pdl_launch_dependents();
     pdl_wait();
 
@@ -223,7 +226,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::REGS_FOR) decode_fp8_ker
     }
     using Keys = int[KEYS / 32];     // of lane's key (+ 32) of a step
     using Scales = float[KEYS / 32];
-    Cursor ahead = cur;            // the step after those in `to_issue`
+    Cursor& ahead = s_ahead[warp];  // the step after those in `to_issue`; in shared memory to spare registers
+    if (lane == 0) ahead = cur;
+    __syncwarp();
     int fetched = 0, issued = 0;
     struct {
         Keys page;                 // pages of the lane's keys, loaded one step before their use
@@ -239,7 +244,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::REGS_FOR) decode_fp8_ker
             const int key = to_issue.key0 + i * 32 + lane;
             to_issue.page[i] = (fetched < count && key < ahead.len) ? trow[a.page.div(key)] : -1;
         }
-        if (++fetched < count) advance<STEP>(ahead, a, cap);
+        if (++fetched < count) {
+            Cursor next = ahead;
+            advance<STEP>(next, a, cap);
+            __syncwarp();
+            if (lane == 0) ahead = next;
+            __syncwarp();
+        }
     };
     // Scales are loaded, not copied (a 4-byte copy asks L2 once per lane, a load once per sector), and put into the
     // ring one step later, when they have arrived; V's as logarithms.
@@ -318,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::REGS_FOR) decode_fp8_ker
 
     // ---- what a segment holds
     uint32_t qb[C::QSMEM ? 1 : NB][KS][2];
-    float sc[NB][2];  // score scale of the rows whose scores this lane holds: 8 nb + 2 t, + 1
+    float sc[C::QSMEM ? 1 : NB][2];  // (NB <= 2) score scale of the rows whose scores this lane holds: 8 nb + 2 t, + 1
     float acc[D / 16][NB][4];
     float m[NB][2], M[NB][2], l[NB][2];  // of rows 8 nb + 2 t + j; the maxima start at the lowest number: a row
                                          // that sees no key keeps l = 0 (2^(-inf - m))
@@ -381,8 +392,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::REGS_FOR) decode_fp8_ker
     }
     if constexpr (C::QSMEM) {
         __syncthreads();
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) sc[nb][0] = s_up[nb * 8 + 2 * t], sc[nb][1] = s_up[nb * 8 + 2 * t + 1];
     }
 #pragma unroll
     for (int i = 0; i < D / 16; ++i)
@@ -445,11 +454,16 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::REGS_FOR) decode_fp8_ker
                 const float kscale = ksf[i * 16 + h * 8];
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb) {
-                    S[i][nb][2 * h] *= sc[nb][0] * kscale;
-                    S[i][nb][2 * h + 1] *= sc[nb][1] * kscale;
+                    float2 x;
+                    if constexpr (C::QSMEM)
+                        x = *reinterpret_cast<const float2*>(s_up + nb * 8 + 2 * t);
+                    else
+                        x = make_float2(sc[nb][0], sc[nb][1]);
+                    S[i][nb][2 * h] *= x.x * kscale;
+                    S[i][nb][2 * h + 1] *= x.y * kscale;
                 }
             }
-        if (key0 + KEYS > cur.len - a.Nq + 1) {  // some row does not see every key
+        if (key0 + MT * 16 > cur.len - a.Nq + 1) {  // some row does not see every key
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -481,19 +495,31 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::REGS_FOR) decode_fp8_ker
                             }
                         }
         }
-        // ---- softmax: p = 2^(x - m) into l; w = 2^(x + log2 vs - M) for the value product
+        // ---- softmax: p = 2^(x - m) into l; w = 2^(x + log2 vs - M) for the value product.  m and M need not be the
+        // maxima, only within 2^8 of them (fp16 holds 2^15): most steps find no larger one and skip the reductions.
+        float mx[NB][2];
+        bool grown = false;
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                float mx = m[nb][j];
+                mx[nb][j] = fmaxf(S[0][nb][j], S[0][nb][2 + j]);
 #pragma unroll
-                for (int i = 0; i < MT; ++i) mx = fmax3(mx, S[i][nb][j], S[i][nb][2 + j]);
-#pragma unroll
-                for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-                l[nb][j] *= ex2(m[nb][j] - mx);
-                m[nb][j] = mx;
+                for (int i = 1; i < MT; ++i) mx[nb][j] = fmax3(mx[nb][j], S[i][nb][j], S[i][nb][2 + j]);
+                grown |= mx[nb][j] > m[nb][j] + kSlack;
             }
+        if (__any_sync(0xffffffffu, grown)) {
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    float x = fmaxf(m[nb][j], mx[nb][j]);
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+                    l[nb][j] *= ex2(m[nb][j] - x);
+                    m[nb][j] = x;
+                }
+        }
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -507,34 +533,32 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::REGS_FOR) decode_fp8_ker
                         S[i][nb][2 * h + j] += lv;
                     }
             }
-        float Mx[NB][2];
-        bool grown = false;
+        grown = false;
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                float mx = M[nb][j];
+                mx[nb][j] = fmaxf(S[0][nb][j], S[0][nb][2 + j]);
 #pragma unroll
-                for (int i = 0; i < MT; ++i) mx = fmax3(mx, S[i][nb][j], S[i][nb][2 + j]);
-#pragma unroll
-                for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-                Mx[nb][j] = mx;
-                grown |= mx > M[nb][j];
+                for (int i = 1; i < MT; ++i) mx[nb][j] = fmax3(mx[nb][j], S[i][nb][j], S[i][nb][2 + j]);
+                grown |= mx[nb][j] > M[nb][j] + kSlack;
             }
         if (__any_sync(0xffffffffu, grown)) {
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-                float f[2];
+            for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    f[j] = ex2(M[nb][j] - Mx[nb][j]);
-                    M[nb][j] = Mx[nb][j];
+                    float x = fmaxf(M[nb][j], mx[nb][j]);
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+                    const float f = ex2(M[nb][j] - x);
+                    M[nb][j] = x;
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i) {
+                        acc[i][nb][j] *= f;
+                        acc[i][nb][2 + j] *= f;
+                    }
                 }
-#pragma unroll
-                for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) acc[i][nb][c] *= f[c & 1];
-            }
         }
         uint32_t pb[MT][NB][2];
 #pragma unroll
@@ -617,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::REGS_FOR) decode_fp8_ker
                     for (int j = 0; j < 2; ++j)
 #pragma unroll
                         for (int i = 0; i < D / 16; ++i) {
-                            float2* at = reinterpret_cast<float2*>(buf + (nb * 8 + 2 * t + j) * C::OROW + g * DT + 2 * i);
+                            float2* at = reinterpret_cast<float2*>(buf + (nb * 8 + 2 * t + j) * C::OROW + i * 16 + g * 2);
                             float2 x = make_float2(acc[i][nb][j] * f[nb][j], acc[i][nb][2 + j] * f[nb][j]);
                             if (turn) {
                                 const float2 y = *at;
@@ -632,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::REGS_FOR) decode_fp8_ker
         const bool whole = seg == 0 && item_ends;
         const long long slot_out = blockIdx.x + bh * a.row_tiles + cur.rt;
         for (int i = tid; i < nrows * (D / 4); i += kThreads) {
-            const int r = i / (D / 4), c = (i % (D / 4)) * 4;
+            const int r = i / (D / 4), c = (i % (D / 4)) * 4, at = c % DT * 8 + c / DT * 2;
             float top = s_stat[0][0][r];
 #pragma unroll
             for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s_stat[w][0][r]);
@@ -643,11 +667,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::REGS_FOR) decode_fp8_ker
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int w = 0; w < C::BUFS; ++w) {
-                const float4 x = *reinterpret_cast<const float4*>(smem + C::MERGE + ((w * ROWS + r) * C::OROW + c) * 4);
-                o.x += x.x;
-                o.y += x.y;
-                o.z += x.z;
-                o.w += x.w;
+                const float* x = reinterpret_cast<const float*>(smem + C::MERGE) + (w * ROWS + r) * C::OROW + at;
+                o.x += x[0];
+                o.y += x[1];
+                o.z += x[16];
+                o.w += x[17];
             }
             o.x *= inv;
             o.y *= inv;
