@@ -884,7 +884,7 @@ int fa_cache_append_fp8(const void* k, const void* v, long long k_sb, long long 
     if ((st = check_strides(&k_sb, &k_sh, &k_sn, B, Hkv, N)) != FA_OK) return st;
     if ((st = check_strides(&v_sb, &v_sh, &v_sn, B, Hkv, N)) != FA_OK) return st;
     CacheAppendLaunch a;
-    st = device_state(&a.err, nullptr);
+    st = device_state(&a.err, &a.num_sms);
     if (st != FA_OK) return st;
     a.k = k;
     a.v = v;
@@ -990,7 +990,7 @@ int fa_cache_evict_fp8(void* k_pages, void* v_pages, float* k_scale, float* v_sc
         !aligned4(new_lens) || !aligned4(new_weights) || !aligned4(kept))
         return FA_ERR_ALIGNMENT;
     CacheEvictLaunch a;
-    st = device_state(&a.err, nullptr);
+    st = device_state(&a.err, &a.num_sms);
     if (st != FA_OK) return st;
     a.kp = static_cast<uint8_t*>(k_pages);
     a.vp = static_cast<uint8_t*>(v_pages);

@@ -31,38 +31,60 @@ __device__ __forceinline__ float scale_for(uint32_t amax_bf16) {
     return __uint_as_float((uint32_t)max(e, 1) << 23);
 }
 
-// Magnitude bits of the two finite bf16 of a word (infinities and NaN count as 0: they saturate or stay NaN).
-__device__ __forceinline__ uint32_t amax2(uint32_t w) {
-    const uint32_t lo = w & 0x7FFFu, hi = (w >> 16) & 0x7FFFu;
-    return max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u);
+// Largest magnitudes of the two halves of bf16 pairs; NaN wins.
+__device__ __forceinline__ uint32_t abs_max2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a & 0x7FFF7FFFu), "r"(b & 0x7FFF7FFFu));
+    return r;
 }
-
-__device__ __forceinline__ uint2 quantise8(uint4 x, float inv, float s, bool pow2) {
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    uint32_t r[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        float f[4] = {bf_lo(w[2 * i]), bf_hi(w[2 * i]), bf_lo(w[2 * i + 1]), bf_hi(w[2 * i + 1])};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) f[j] = pow2 ? f[j] * inv : __fdiv_rn(f[j], s);
-        r[i] = e4m3x4(f[0], f[1], f[2], f[3]);
+__device__ __forceinline__ uint32_t abs_max(uint4 x, uint4 y) {
+    const uint32_t a = abs_max2(abs_max2(abs_max2(x.x, x.y), abs_max2(x.z, x.w)), abs_max2(abs_max2(y.x, y.y), abs_max2(y.z, y.w)));
+    uint32_t m = max(a & 0x7FFFu, (a >> 16) & 0x7FFFu);
+    if (m >= 0x7F80u) {  // infinities and NaN: the largest finite one (they saturate, or stay NaN)
+        const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+        m = 0;
+#pragma unroll 1
+        for (int i = 0; i < 16; ++i) {
+            const uint32_t v = (w[i / 2] >> (i % 2 * 16)) & 0x7FFFu;
+            if (v < 0x7F80u) m = max(m, v);
+        }
     }
-    return make_uint2(r[0], r[1]);
+    return m;
 }
 
-// One CTA per (sequence, touched block of sb tokens, kv head); the first 128 threads take K, the others V.
-// A thread holds TPT tasks (16 columns of a token: the pieces that a rotation pairs) in registers between the
-// block's maximum and the quantisation, so new tokens are read once.  If the scale grows, the block's earlier
-// tokens are requantised in place.
+// Eight bf16 as e4m3 bytes of their values divided by s; pow2: by its exact inverse.
+__device__ __forceinline__ uint2 quantise8(uint4 x, float inv, float s, bool pow2) {
+    float f[8] = {bf_lo(x.x), bf_hi(x.x), bf_lo(x.y), bf_hi(x.y), bf_lo(x.z), bf_hi(x.z), bf_lo(x.w), bf_hi(x.w)};
+    if (pow2) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] *= inv;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = __fdiv_rn(f[i], s);
+    }
+    return make_uint2(e4m3x4(f[0], f[1], f[2], f[3]), e4m3x4(f[4], f[5], f[6], f[7]));
+}
+
+// One CTA per (sequence, touched block of sb tokens, run of kv heads); the first 128 threads take K, the others V.
+// The block's cosines and sines are made once, in shared memory, by all threads, and serve every head of the run: with
+// a pair of them per head and element the sines alone were half of the instructions.  A thread holds TPT tasks (16
+// columns of a token: the pieces that a rotation pairs) in registers between the block's maximum and the quantisation,
+// so new tokens are read once.  If the scale grows, the block's earlier tokens are requantised in place.
+struct AppendPlan {
+    int blocks, heads, groups;  // blocks of sb tokens that N tokens can touch; kv heads per CTA, and runs of them
+    FastDiv page, sb;
+};
+
 template <int D, int TPT, bool INTER>
-__global__ void __launch_bounds__(2 * kHalf) cache_append_kernel(const CacheAppendLaunch a, int blocks) {
-    __shared__ uint32_t s_max[2][4];
+__global__ void __launch_bounds__(2 * kHalf, TPT > 2 ? 2 : 4) cache_append_kernel(const CacheAppendLaunch a, const AppendPlan plan) {
+    extern __shared__ __align__(16) float2 s_turn[];  // [token][pair of pairs j < 4][task][2]
+    __shared__ uint32_t s_max[2][2][4];
     pdl_launch_dependents();
     pdl_wait();
     constexpr int TPR = D / 16;
-    const int h = blockIdx.x % a.Hkv;
-    const int blk = (blockIdx.x / a.Hkv) % blocks;
-    const int b = blockIdx.x / a.Hkv / blocks;
+    const int group = blockIdx.x % plan.groups;
+    const int blk = (blockIdx.x / plan.groups) % plan.blocks;
+    const int b = blockIdx.x / plan.groups / plan.blocks;
     const int is_v = threadIdx.x / kHalf, tid = threadIdx.x % kHalf;
     const int cap = a.max_pages * a.page;
     int len = a.lens[b], n = a.new_lens ? a.new_lens[b] : a.N;
@@ -71,84 +93,120 @@ __global__ void __launch_bounds__(2 * kHalf) cache_append_kernel(const CacheAppe
         len = min(max(len, 0), cap);
         n = min(min(max(n, 0), a.N), cap - len);
     }
-    const int first = (len / a.sb + blk) * a.sb;  // the block's first token
+    const int first = ((int)plan.sb.div(len) + blk) * a.sb;  // the block's first token
     if (first >= len + n) return;
-    const int pg = a.table[(long long)b * a.max_pages + first / a.page];
+    const int lpage = (int)plan.page.div(first), at = first - lpage * a.page;  // logical page, token within it
+    const int pg = a.table[(long long)b * a.max_pages + lpage];
     if ((unsigned)pg >= (unsigned)a.num_pages) {
         if (threadIdx.x == 0) record_invalid(a.err, kSiteCacheTable, pg);
         return;
     }
-    const int at = first % a.page;  // token within the page
-    const long long head = (long long)pg * a.Hkv + h;
-    uint8_t* dst = (is_v ? a.vp : a.kp) + (head * a.page + at) * D;
-    float* sc = (is_v ? a.vs : a.ks) + head * (a.page / a.sb) + at / a.sb;
     const int t0 = max(len - first, 0), t1 = min(a.sb, len + n - first);  // new tokens [t0, t1) of the block
-    const __nv_bfloat16* src = is_v ? (const __nv_bfloat16*)a.v + b * a.vb + h * a.vh
-                                    : (const __nv_bfloat16*)a.k + b * a.kb + h * a.kh;
-    const long long sn = is_v ? a.vn : a.kn;
-
-    uint4 x[TPT], y[TPT];
-    uint32_t big = 0;
-#pragma unroll
-    for (int i = 0; i < TPT; ++i) {
-        const int task = tid + i * kHalf, tok = task / TPR, p = task % TPR;
-        if (tok < t0 || tok >= t1) continue;
-        const int idx = first + tok - len;
-        int c0, c1;
-        task_columns<INTER>(p, is_v || !a.turns ? 0 : a.rot, c0, c1);
-        x[i] = *reinterpret_cast<const uint4*>(src + idx * sn + c0);
-        y[i] = *reinterpret_cast<const uint4*>(src + idx * sn + c1);
-    }
-#pragma unroll
-    for (int i = 0; i < TPT; ++i) {
-        const int task = tid + i * kHalf, tok = task / TPR, p = task % TPR;
-        if (tok < t0 || tok >= t1) continue;
-        if (!is_v && a.turns && p < a.rot / 16) {
-            const int idx = first + tok - len;
-            const int pos = a.positions ? a.positions[(long long)b * a.N + idx] : len + idx;
-            float c[8], s[8];
-            task_cos_sin(pos, a.turns + p * 8, a.magnitude, c, s);
-            rotate16<INTER>(x[i], y[i], c, s);  // rounded to bf16: the bytes of fa_rope followed by this append
+    const int turned = a.turns ? a.rot / 16 : 0;                          // tasks of a row that rotate
+    if (turned) {
+        const int q = threadIdx.x % 64;  // one pair for each of up to 64 threads, four tokens at a time
+        if (q < turned * 8) {
+            const uint64_t turns = a.turns[q];
+            for (int tok = t0 + threadIdx.x / 64; tok < t1; tok += 2 * kHalf / 64) {
+                const int pos = a.positions ? a.positions[(long long)b * a.N + first + tok - len] : first + tok;
+                float2 cs;
+                turn_cos_sin(pos, turns, a.magnitude, cs.x, cs.y);
+                s_turn[((tok * 4 + q % 8 / 2) * turned + q / 8) * 2 + q % 2] = cs;
+            }
         }
-        big = max(big, max(max(amax2(x[i].x), amax2(x[i].y)), max(amax2(x[i].z), amax2(x[i].w))));
-        big = max(big, max(max(amax2(y[i].x), amax2(y[i].y)), max(amax2(y[i].z), amax2(y[i].w))));
+        __syncthreads();
     }
-    const float old = t0 > 0 ? *sc : 0.f;
-    const float to = fmaxf(old, scale_for(half_max(big, s_max, is_v)));  // every thread has read the old scale
-    const bool pow2 = (__float_as_uint(to) & 0x7FFFFFu) == 0 && to >= 1.17549435e-38f && to <= 1.7e38f;
-    const float inv = pow2 ? __uint_as_float((254u << 23) - __float_as_uint(to)) : 0.f;
-    if (to != old) {
-        for (int i = tid; i < t0 * TPR; i += kHalf) {
-            uint4* at16 = reinterpret_cast<uint4*>(dst) + i;
-            *at16 = e4m3_rescale16(*at16, old, to);
-        }
-        if (tid == 0) *sc = to;
-    }
+    // what a task needs in every head: its pieces' columns and places
+    const int nb = (int)plan.sb.div(a.page), h0 = group * plan.heads, h1 = min(h0 + plan.heads, a.Hkv);
+    const long long sn = is_v ? a.vn : a.kn, sh = is_v ? a.vh : a.kh;
+    const __nv_bfloat16* src[TPT];
+    int out[TPT], apart[TPT];  // offset of the first piece in the block, and from it to the second; apart = 0: no token
+    const float2* cs[TPT];
 #pragma unroll
     for (int i = 0; i < TPT; ++i) {
         const int task = tid + i * kHalf, tok = task / TPR, p = task % TPR;
-        if (tok < t0 || tok >= t1) continue;
         int c0, c1;
-        task_columns<INTER>(p, is_v || !a.turns ? 0 : a.rot, c0, c1);
-        const uint2 u = quantise8(x[i], inv, to, pow2), w = quantise8(y[i], inv, to, pow2);
-        uint8_t* row = dst + tok * D;
-        if (c1 == c0 + 8) {
-            *reinterpret_cast<uint4*>(row + c0) = make_uint4(u.x, u.y, w.x, w.y);
-        } else {
-            *reinterpret_cast<uint2*>(row + c0) = u;
-            *reinterpret_cast<uint2*>(row + c1) = w;
+        task_columns<INTER>(p, is_v ? 0 : turned * 16, c0, c1);
+        apart[i] = tok >= t0 && tok < t1 ? c1 - c0 : 0;
+        out[i] = tok * D + c0;
+        src[i] = (is_v ? (const __nv_bfloat16*)a.v + b * a.vb : (const __nv_bfloat16*)a.k + b * a.kb) +
+                 (first + tok - len) * sn + h0 * sh + c0;
+        cs[i] = !is_v && p < turned ? s_turn + (tok * 4 * turned + p) * 2 : nullptr;
+    }
+    uint8_t* dst = (is_v ? a.vp : a.kp) + (((long long)pg * a.Hkv + h0) * a.page + at) * D;
+    float* sc = (is_v ? a.vs : a.ks) + ((long long)pg * a.Hkv + h0) * nb + plan.sb.div(at);
+    for (int h = h0; h < h1; ++h, dst += (long long)a.page * D, sc += nb) {
+        const float old = t0 > 0 ? *sc : 0.f;
+        uint4 x[TPT], y[TPT];
+        uint32_t big = 0;
+#pragma unroll
+        for (int i = 0; i < TPT; ++i)
+            if (apart[i]) {
+                x[i] = *reinterpret_cast<const uint4*>(src[i]);
+                y[i] = *reinterpret_cast<const uint4*>(src[i] + apart[i]);
+                src[i] += sh;
+            }
+#pragma unroll
+        for (int i = 0; i < TPT; ++i) {
+            if (!apart[i]) continue;
+            if (cs[i]) {
+                float c[8], s[8];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float4 v = *reinterpret_cast<const float4*>(cs[i] + j * turned * 2);
+                    c[2 * j] = v.x, s[2 * j] = v.y, c[2 * j + 1] = v.z, s[2 * j + 1] = v.w;
+                }
+                rotate16<INTER>(x[i], y[i], c, s);  // rounded to bf16: the bytes of fa_rope followed by this append
+            }
+            big = max(big, abs_max(x[i], y[i]));
+        }
+        const float to = fmaxf(old, scale_for(half_max(big, s_max[h & 1], is_v)));  // all threads have read the old scale
+        const bool pow2 = is_pow2(to) && to <= 1.7e38f;                            // 1 / to is normal
+        const float inv = pow2 ? __uint_as_float((254u << 23) - __float_as_uint(to)) : 0.f;
+        if (to != old) {
+            for (int i = tid; i < t0 * TPR; i += kHalf) {
+                uint4* at16 = reinterpret_cast<uint4*>(dst) + i;
+                *at16 = e4m3_rescale16(*at16, old, to);
+            }
+            if (tid == 0) *sc = to;
+        }
+#pragma unroll
+        for (int i = 0; i < TPT; ++i) {
+            if (!apart[i]) continue;
+            const uint2 u = quantise8(x[i], inv, to, pow2), w = quantise8(y[i], inv, to, pow2);
+            if (apart[i] == 8) {
+                *reinterpret_cast<uint4*>(dst + out[i]) = make_uint4(u.x, u.y, w.x, w.y);
+            } else {
+                *reinterpret_cast<uint2*>(dst + out[i]) = u;
+                *reinterpret_cast<uint2*>(dst + out[i] + apart[i]) = w;
+            }
         }
     }
 }
 
+template <int D, int TPT, bool INTER>
+cudaError_t launch_append_dti(const CacheAppendLaunch& a, cudaStream_t s) {
+    AppendPlan plan;
+    plan.blocks = (a.N + a.sb - 2) / a.sb + 1;
+    plan.page = FastDiv((uint32_t)a.page);
+    plan.sb = FastDiv((uint32_t)a.sb);
+    // heads per CTA: up to eight share the sines while there are four CTAs for every SM
+    plan.heads = 8;
+    const long long cells = (long long)a.B * plan.blocks;
+    while (plan.heads > 1 && cells * ((a.Hkv + plan.heads - 1) / plan.heads) < 4ll * a.num_sms) plan.heads /= 2;
+    plan.groups = (a.Hkv + plan.heads - 1) / plan.heads;
+    const long long ctas = cells * plan.groups;
+    if (ctas > 0x7FFFFFFFll) return cudaErrorInvalidValue;
+    const int smem = a.turns ? a.sb * (a.rot / 2) * 8 : 0;  // at most 64 KB
+    cudaError_t e = set_smem_limit_once<cache_append_kernel<D, TPT, INTER>>(64 * 1024);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(cache_append_kernel<D, TPT, INTER>, dim3((unsigned)ctas), dim3(2 * kHalf), (size_t)smem, s, a,
+                            plan);
+}
+
 template <int D, int TPT>
 cudaError_t launch_append_dt(const CacheAppendLaunch& a, cudaStream_t s) {
-    const int blocks = (a.N + a.sb - 2) / a.sb + 1;  // of sb tokens that N tokens can touch
-    const long long ctas = (long long)a.B * blocks * a.Hkv;
-    if (ctas > 0x7FFFFFFFll) return cudaErrorInvalidValue;
-    const dim3 grid((unsigned)ctas), block(2 * kHalf);
-    return a.interleaved ? launch_dependent(cache_append_kernel<D, TPT, true>, grid, block, 0, s, a, blocks)
-                         : launch_dependent(cache_append_kernel<D, TPT, false>, grid, block, 0, s, a, blocks);
+    return a.interleaved ? launch_append_dti<D, TPT, true>(a, s) : launch_append_dti<D, TPT, false>(a, s);
 }
 
 template <int D>
@@ -162,9 +220,11 @@ cudaError_t launch_append_d(const CacheAppendLaunch& a, cudaStream_t s) {
 
 // ------------------------------------------------------------------ eviction
 // Which tokens stay: the last `recent`, and of the others the keep - recent with the largest weights (ties: lowest
-// index).  One CTA per (sequence, kv head): a radix selection over the weights' order-preserving integer keys finds
-// the smallest key that stays and how many equal ones do; a pass in index order then writes the list.
-constexpr int kSelThreads = 1024, kSelWarps = kSelThreads / 32;
+// index).  A cluster of 1 to 8 CTAs per (sequence, kv head), each with a run of the tokens, whose order-preserving
+// integer keys stay in its registers: three histograms (11, 11 and 10 bits), summed over the cluster's shared
+// memories, find the smallest key that stays and how many equal ones do; one count over the cluster then gives every
+// kept token its place in index order.  The weights are read once.
+constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32, kSelBins = 2048;
 
 // Integer whose order is the float's, with -0 = +0 and NaN above everything.
 __device__ __forceinline__ uint32_t order_key(float w) {
@@ -174,53 +234,100 @@ __device__ __forceinline__ uint32_t order_key(float w) {
     return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const CacheEvictLaunch a) {
-    __shared__ uint32_t s_hist[2048];
+__device__ __forceinline__ uint4 ld_cluster_u4(const uint32_t* p, uint32_t rank) {
+    uint4 v;
+    asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(mapa_shared(smem_u32(p), rank))
+                 : "memory");
+    return v;
+}
+
+__device__ __forceinline__ uint32_t ld_cluster_u32(const uint32_t* p, uint32_t rank) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(mapa_shared(smem_u32(p), rank)) : "memory");
+    return v;
+}
+
+static_assert(kSelBins == 4 * kSelThreads, "four bins per thread");
+
+// PER: keys of a thread in registers (0: any number; they are read again in each pass).
+template <int PER>
+__global__ void __launch_bounds__(kSelThreads, PER > 8 ? 1 : 2) evict_select_kernel(const CacheEvictLaunch a, int ctas) {
+    __shared__ __align__(16) uint32_t s_hist[2][kSelBins];
     __shared__ uint32_t s_warp[kSelWarps];
-    __shared__ uint32_t s_digit, s_left;
+    __shared__ uint32_t s_digit, s_left, s_counts[2];
     pdl_launch_dependents();
     pdl_wait();
-    const int b = blockIdx.x / a.Hkv, h = blockIdx.x % a.Hkv;
+    const int rank = blockIdx.x % ctas;
+    const long long bh = blockIdx.x / ctas;
+    const int b = (int)(bh / a.Hkv);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int cap = a.max_pages * a.page, ncap = a.new_max_pages * a.page;
     int n = a.lens[b];
     if (n < 0 || n > cap) {
-        if (tid == 0) record_invalid(a.err, kSiteCacheLen, n);
+        if (tid == 0 && rank == 0) record_invalid(a.err, kSiteCacheLen, n);
         n = min(max(n, 0), cap);
     }
     const int stay = min(n, a.keep);
-    if (h == 0 && tid == 0) a.new_lens[b] = stay;
-    const float* w = a.weights + (long long)blockIdx.x * cap;
-    int* kept = a.kept + (long long)blockIdx.x * ncap;
-    float* nw = a.new_weights + (long long)blockIdx.x * ncap;
-    for (int j = stay + tid; j < ncap; j += kSelThreads) {
+    if (bh % a.Hkv == 0 && rank == 0 && tid == 0) a.new_lens[b] = stay;
+    const float* w = a.weights + bh * cap;
+    int* kept = a.kept + bh * ncap;
+    float* nw = a.new_weights + bh * ncap;
+    for (int j = stay + rank * kSelThreads + tid; j < ncap; j += ctas * kSelThreads) {
         kept[j] = -1;
         nw[j] = 0.f;
     }
-    if (n <= a.keep) {
-        for (int j = tid; j < n; j += kSelThreads) {
+    if (n <= a.keep) {  // the whole cluster alike
+        for (int j = rank * kSelThreads + tid; j < n; j += ctas * kSelThreads) {
             kept[j] = j;
             nw[j] = w[j];
         }
         return;
     }
+    // this CTA's run of tokens, cut into a run for each warp; a warp takes 32 consecutive tokens at a time
+    const int per_warp = ((n + ctas * kSelWarps - 1) / (ctas * kSelWarps) + 31) / 32 * 32;
+    const int first = (rank * kSelWarps + warp) * per_warp + lane, rounds = per_warp / 32;
     const int cand = n - a.recent;  // candidates [0, cand): `left` of them stay
+    uint32_t keys[PER ? PER : 1] = {};
+    if constexpr (PER > 0) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) keys[i] = i < rounds && first + i * 32 < cand ? order_key(w[first + i * 32]) : 0;
+    }
+    auto key_of = [&](int i) { return PER ? keys[PER ? i : 0] : order_key(w[first + i * 32]); };
     uint32_t left = (uint32_t)(a.keep - a.recent), key = 0, known = 0;  // key's bits under the mask `known` are settled
+    for (int i = tid; i < 2 * kSelBins; i += kSelThreads) s_hist[0][i] = 0;
+    __syncthreads();
     if (left > 0) {
         int shift = 21;
 #pragma unroll 1
         for (int pass = 0; pass < 3; ++pass) {
-            const int bits = pass == 2 ? 10 : 11;
-            for (int i = tid; i < 2048; i += kSelThreads) s_hist[i] = 0;
-            __syncthreads();
-            for (int j = tid; j < cand; j += kSelThreads) {
-                const uint32_t k = order_key(w[j]);
-                if ((k & known) == key) atomicAdd(&s_hist[(k >> shift) & ((1u << bits) - 1)], 1u);
-            }
-            __syncthreads();
-            // bins from the largest down: thread t holds bins 2047 - 2t and 2046 - 2t
-            const uint32_t c0 = s_hist[2047 - 2 * tid], c1 = s_hist[2046 - 2 * tid];
-            uint32_t sum = c0 + c1, incl = sum;
+            uint32_t* hist = s_hist[pass & 1];
+            const uint32_t mask = pass == 2 ? 1023 : 2047;
+#pragma unroll
+            for (int i = 0; i < (PER ? PER : rounds); ++i)
+                if (i < rounds && first + i * 32 < cand) {
+                    const uint32_t k = key_of(i);
+                    if ((k & known) == key) atomicAdd(&hist[(k >> shift) & mask], 1u);
+                }
+            if (ctas > 1)
+                cluster_sync();
+            else
+                __syncthreads();
+            // bins from the largest down: thread t holds bins 2047 - 4t .. 2044 - 4t of the cluster
+            const uint32_t* mine = hist + kSelBins - 4 - 4 * tid;
+            uint4 c = *reinterpret_cast<const uint4*>(mine);
+            uint4 o[7];
+#pragma unroll
+            for (int r = 1; r < 8; ++r)
+                if (r < ctas) o[r - 1] = ld_cluster_u4(mine, (rank + r) % ctas);
+#pragma unroll
+            for (int r = 1; r < 8; ++r)
+                if (r < ctas) c.x += o[r - 1].x, c.y += o[r - 1].y, c.z += o[r - 1].z, c.w += o[r - 1].w;
+            if (pass == 1)  // everyone has read the first histogram by now: the third takes its place
+                *reinterpret_cast<uint4*>(s_hist[0] + 4 * tid) = make_uint4(0, 0, 0, 0);
+            const uint32_t sum = (c.x + c.y) + (c.z + c.w);
+            uint32_t incl = sum;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
                 const uint32_t up = __shfl_up_sync(0xffffffffu, incl, d);
@@ -228,127 +335,204 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const CacheEv
             }
             if (lane == 31) s_warp[warp] = incl;
             __syncthreads();
-            uint32_t before = incl - sum;
-            for (int i = 0; i < warp; ++i) before += s_warp[i];
+            uint32_t before = lane < warp ? s_warp[lane] : 0;
+            before = __reduce_add_sync(0xffffffffu, before) + incl - sum;
             if (before < left && before + sum >= left) {  // exactly one thread
-                const bool second = before + c0 < left;
-                s_digit = (uint32_t)(2047 - 2 * tid - (second ? 1 : 0));
-                s_left = left - before - (second ? c0 : 0);
+                const uint32_t count[4] = {c.w, c.z, c.y, c.x};
+                uint32_t skip = 0;
+                int i = 0;
+                while (i < 3 && before + skip + count[i] < left) skip += count[i++];
+                s_digit = (uint32_t)(kSelBins - 1 - 4 * tid - i);
+                s_left = left - before - skip;
             }
             __syncthreads();
             key |= s_digit << shift;
-            known |= ((1u << bits) - 1) << shift;
+            known |= mask << shift;
             left = s_left;
             shift -= pass == 0 ? 11 : 10;
-            __syncthreads();
         }
     } else {
         key = 0xFFFFFFFFu;  // none of the candidates: no equal one is admitted either
     }
-    // in index order: keys above `key` stay, and the first `left` equal ones
-    uint32_t base = 0, equal_base = 0;
-    for (int j0 = 0; j0 < n; j0 += kSelThreads) {
-        const int j = j0 + tid;
-        float wj = 0.f;
-        bool above = false, equal = false;
-        if (j < n) {
-            wj = w[j];
-            const uint32_t k = order_key(wj);
-            above = j >= cand || (k > key);
-            equal = j < cand && k == key;
+    // in index order: keys above `key` and the recent tokens stay, and the first `left` equal ones
+    uint32_t above = 0, equal = 0;
+#pragma unroll
+    for (int i = 0; i < (PER ? PER : rounds); ++i)
+        if (i < rounds) {
+            const int j = first + i * 32;
+            const uint32_t k = j < cand ? key_of(i) : 0;
+            above += __popc(__ballot_sync(0xffffffffu, j < n && (j >= cand || k > key)));
+            equal += __popc(__ballot_sync(0xffffffffu, j < cand && k == key));
         }
-        const uint32_t ma = __ballot_sync(0xffffffffu, above), me = __ballot_sync(0xffffffffu, equal);
-        __syncthreads();  // the previous round's sums have been read
-        if (lane == 0) s_warp[warp] = __popc(ma) | (__popc(me) << 16);
-        __syncthreads();
-        uint32_t pre = 0, all = 0;
-        for (int i = 0; i < kSelWarps; ++i) {
-            const uint32_t v = s_warp[i];
-            if (i < warp) pre += v;
-            all += v;
+    // counts before this warp: of the CTA's other warps, and of the cluster's CTAs before this one
+    __shared__ uint32_t s_above[kSelWarps], s_equal[kSelWarps];
+    if (lane == 0) s_above[warp] = above, s_equal[warp] = equal;
+    __syncthreads();
+    uint32_t ba = __reduce_add_sync(0xffffffffu, lane < warp ? s_above[lane] : 0);
+    uint32_t be = __reduce_add_sync(0xffffffffu, lane < warp ? s_equal[lane] : 0);
+    if (ctas > 1) {
+        if (warp == kSelWarps - 1 && lane == 0) s_counts[0] = ba + above, s_counts[1] = be + equal;
+        cluster_sync();
+        uint32_t oa = 0, oe = 0;
+        if (lane < rank) {
+            oa = ld_cluster_u32(&s_counts[0], lane);
+            oe = ld_cluster_u32(&s_counts[1], lane);
         }
-        const uint32_t below = (1u << lane) - 1;
-        const uint32_t ra = base + (pre & 0xFFFFu) + __popc(ma & below);                // kept by key before j
-        const uint32_t re = equal_base + (pre >> 16) + __popc(me & below);              // equal ones before j
-        if (above || (equal && re < left)) {
-            const uint32_t at = ra + min(re, left);
-            kept[at] = j;
-            nw[at] = wj;
-        }
-        base += all & 0xFFFFu;
-        equal_base += all >> 16;
+        ba += __reduce_add_sync(0xffffffffu, oa);
+        be += __reduce_add_sync(0xffffffffu, oe);
     }
+    const uint32_t below = (1u << lane) - 1;
+#pragma unroll
+    for (int i = 0; i < (PER ? PER : rounds); ++i)
+        if (i < rounds) {
+            const int j = first + i * 32;
+            const uint32_t k = j < cand ? key_of(i) : 0;
+            const bool up = j < n && (j >= cand || k > key), eq = j < cand && k == key;
+            const uint32_t ma = __ballot_sync(0xffffffffu, up), me = __ballot_sync(0xffffffffu, eq);
+            const uint32_t ra = ba + __popc(ma & below), re = be + __popc(me & below);  // before j
+            if (up || (eq && re < left)) {
+                const uint32_t at = ra + min(re, left);
+                kept[at] = j;
+                nw[at] = w[j];
+            }
+            ba += __popc(ma);
+            be += __popc(me);
+        }
+    if (ctas > 1) cluster_sync();  // the others may still read this CTA's counts
 }
 
-// One CTA per (sequence, kv head, block of sb kept tokens): K by the first 128 threads, V by the others.  The block's
-// scale is the largest of its tokens' source scales; tokens that came with that scale are copied byte for byte.
+// Moves the kept tokens, a block of sb of them per turn of a CTA: K by the first 128 threads, V by the others.  The
+// block's scale is the largest of its tokens' source scales; tokens that came with that scale are copied byte for byte.
+// Reading a token takes three loads that depend on each other (its index, its page, its row), so the CTAs are resident
+// ones that run over the blocks with the index two blocks ahead and the page one block ahead of the row.
+constexpr int kMoveCtas = 4;  // per SM
+
+struct MovePlan {
+    int blocks, step_bh, step_blk;  // blocks per (sequence, kv head); the grid's size as (sequence, kv head)s and blocks
+    int bhs;
+    FastDiv page, sb, heads;
+};
+
 template <int D, int TPT>
-__global__ void __launch_bounds__(2 * kHalf) evict_move_kernel(const CacheEvictLaunch a) {
-    __shared__ uint32_t s_max[2][4];
+__global__ void __launch_bounds__(2 * kHalf, kMoveCtas) evict_move_kernel(const CacheEvictLaunch a, const MovePlan plan) {
+    __shared__ uint32_t s_max[2][2][4];
     pdl_launch_dependents();
     pdl_wait();
     constexpr int TPR = D / 16;
-    const int blocks = (a.keep + a.sb - 1) / a.sb;
-    const int blk = blockIdx.x % blocks;
-    const long long bh = blockIdx.x / blocks;
-    const int b = (int)(bh / a.Hkv), h = (int)(bh % a.Hkv);
     const int is_v = threadIdx.x / kHalf, tid = threadIdx.x % kHalf;
-    const int cap = a.max_pages * a.page, ncap = a.new_max_pages * a.page;
-    const int stay = min(min(max(a.lens[b], 0), cap), a.keep);
-    const int first = blk * a.sb, count = min(a.sb, stay - first);
-    if (count <= 0) return;
-    const int npg = a.new_table[(long long)b * a.new_max_pages + first / a.page];
-    if ((unsigned)npg >= (unsigned)a.num_pages) {
-        if (threadIdx.x == 0) record_invalid(a.err, kSiteCacheTable, npg);
-        return;
-    }
-    const int at = first % a.page, bpp = a.page / a.sb;
-    const long long nhead = (long long)npg * a.Hkv + h;
-    uint8_t* dst = (is_v ? a.vp : a.kp) + (nhead * a.page + at) * D;
-    const uint8_t* pool = is_v ? a.vp : a.kp;
-    const float* scales = is_v ? a.vs : a.ks;
-    const int* kept = a.kept + bh * ncap + first;
-    uint4 x[TPT];
-    float sc[TPT];
-    uint32_t big = 0;
+    const int ncap = a.new_max_pages * a.page, bpp = (int)plan.sb.div(a.page);
+    uint8_t* pool = is_v ? a.vp : a.kp;
+    float* scales = is_v ? a.vs : a.ks;
+    struct Item {
+        int bh, blk;
+    };
+    auto advance = [&](Item& it) {
+        it.bh += plan.step_bh;
+        it.blk += plan.step_blk;
+        if (it.blk >= plan.blocks) it.blk -= plan.blocks, ++it.bh;
+    };
+    // stage 1: the source indices of an item's tokens (-1: none)
+    auto load_kept = [&](const Item& it, int (&kept)[TPT]) {
+        const int first = it.blk * a.sb;
+        const int* list = a.kept + (long long)it.bh * ncap + first;
 #pragma unroll
-    for (int i = 0; i < TPT; ++i) {
-        const int task = tid + i * kHalf, tok = task / TPR;
-        x[i] = make_uint4(0, 0, 0, 0);
-        sc[i] = 0.f;
-        if (tok >= count) continue;
-        const int j = kept[tok];
-        const int pg = a.table[(long long)b * a.max_pages + j / a.page];
-        if ((unsigned)pg >= (unsigned)a.num_pages) {
-            record_invalid(a.err, kSiteCacheTable, pg);  // reads as zeros
-            continue;
+        for (int i = 0; i < TPT; ++i) {
+            const int tok = (tid + i * kHalf) / TPR;
+            kept[i] = it.bh < plan.bhs && tok < a.sb && first + tok < ncap ? list[tok] : -1;
         }
-        const int o = j % a.page;
-        const long long head = (long long)pg * a.Hkv + h;
-        sc[i] = scales[head * bpp + o / a.sb];
-        x[i] = *reinterpret_cast<const uint4*>(pool + (head * a.page + o) * D + (task % TPR) * 16);
-        big = max(big, __float_as_uint(fabsf(sc[i])));  // scales are positive: their bits order as they do
-    }
-    const float to = __uint_as_float(half_max(big, s_max, is_v));
-    if (tid == 0) (is_v ? a.vs : a.ks)[nhead * bpp + at / a.sb] = to;
+    };
+    // stage 2: their pages, and the page that the block goes to
+    auto load_pages = [&](const Item& it, const int (&kept)[TPT], int (&page)[TPT], int& to) {
+        const int b = it.bh < plan.bhs ? (int)plan.heads.div(it.bh) : 0;
+        const int* trow = a.table + (long long)b * a.max_pages;
 #pragma unroll
-    for (int i = 0; i < TPT; ++i) {
-        const int task = tid + i * kHalf;
-        if (task / TPR >= count) continue;
-        reinterpret_cast<uint4*>(dst)[task] = sc[i] == to ? x[i] : e4m3_rescale16(x[i], sc[i], to);
+        for (int i = 0; i < TPT; ++i) page[i] = kept[i] >= 0 ? trow[plan.page.div(kept[i])] : 0;
+        to = a.new_table[(long long)b * a.new_max_pages + plan.page.div(it.blk * a.sb)];
+    };
+    int kept[TPT], page[TPT], kept1[TPT], to_page;
+    Item item{(int)(blockIdx.x / plan.blocks), (int)(blockIdx.x % plan.blocks)}, next = item;
+    load_kept(item, kept);
+    advance(next);
+    load_kept(next, kept1);
+    load_pages(item, kept, page, to_page);
+    int turn = 0;
+    for (; item.bh < plan.bhs; turn ^= 1) {
+        const int h = item.bh - (int)plan.heads.div(item.bh) * a.Hkv;
+        uint4 x[TPT];
+        float sc[TPT];
+        uint32_t big = 0;  // bits of the largest scale (positive: they order as they do) + 1; 0: no token
+#pragma unroll
+        for (int i = 0; i < TPT; ++i) {
+            x[i] = make_uint4(0, 0, 0, 0);
+            sc[i] = 0.f;
+            if (kept[i] < 0) continue;
+            if ((unsigned)page[i] >= (unsigned)a.num_pages) {
+                record_invalid(a.err, kSiteCacheTable, page[i]);  // reads as zeros
+                continue;
+            }
+            const uint32_t o = kept[i] - plan.page.div(kept[i]) * a.page;
+            const uint32_t head = (uint32_t)page[i] * a.Hkv + h;  // rows are counted in 32 bits
+            sc[i] = scales[head * bpp + plan.sb.div(o)];
+            x[i] = *reinterpret_cast<const uint4*>(pool + (size_t)(head * a.page + o) * D + (tid + i * kHalf) % TPR * 16);
+        }
+        // the stages of the blocks behind this one
+        int kept2[TPT], page1[TPT], to_page1;
+        Item after = next;
+        advance(after);
+        load_kept(after, kept2);
+        load_pages(next, kept1, page1, to_page1);
+#pragma unroll
+        for (int i = 0; i < TPT; ++i)
+            if (kept[i] >= 0) big = max(big, (__float_as_uint(sc[i]) & 0x7FFFFFFFu) + 1);
+        big = half_max(big, s_max[turn], is_v);
+        if (big) {
+            const float to = __uint_as_float(big - 1);
+            if ((unsigned)to_page < (unsigned)a.num_pages) {
+                const uint32_t at = item.blk * a.sb - plan.page.div(item.blk * a.sb) * a.page;
+                const uint32_t head = (uint32_t)to_page * a.Hkv + h;
+                uint4* dst = reinterpret_cast<uint4*>(pool + (size_t)(head * a.page + at) * D);
+                if (tid == 0) scales[head * bpp + plan.sb.div(at)] = to;
+#pragma unroll
+                for (int i = 0; i < TPT; ++i)
+                    if (kept[i] >= 0) dst[tid + i * kHalf] = sc[i] == to ? x[i] : e4m3_rescale16(x[i], sc[i], to);
+            } else if (tid == 0) {
+                record_invalid(a.err, kSiteCacheTable, to_page);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < TPT; ++i) {
+            kept[i] = kept1[i];
+            kept1[i] = kept2[i];
+            page[i] = page1[i];
+        }
+        to_page = to_page1;
+        item = next;
+        next = after;
     }
+}
+
+template <int D, int TPT>
+cudaError_t launch_move_t(const CacheEvictLaunch& a, cudaStream_t s) {
+    MovePlan plan;
+    plan.blocks = (a.keep + a.sb - 1) / a.sb;
+    plan.bhs = a.B * a.Hkv;
+    plan.page = FastDiv((uint32_t)a.page);
+    plan.sb = FastDiv((uint32_t)a.sb);
+    plan.heads = FastDiv((uint32_t)a.Hkv);
+    const long long items = (long long)plan.bhs * plan.blocks, most = (long long)kMoveCtas * a.num_sms;
+    const int grid = (int)(items < most ? items : most);
+    plan.step_bh = grid / plan.blocks;
+    plan.step_blk = grid % plan.blocks;
+    return launch_dependent(evict_move_kernel<D, TPT>, dim3(grid), dim3(2 * kHalf), 0, s, a, plan);
 }
 
 template <int D>
 cudaError_t launch_move(const CacheEvictLaunch& a, cudaStream_t s) {
-    const long long ctas = (long long)a.B * a.Hkv * ((a.keep + a.sb - 1) / a.sb);
-    if (ctas > 0x7FFFFFFFll) return cudaErrorInvalidValue;
-    const dim3 grid((unsigned)ctas), block(2 * kHalf);
     const int tasks = a.sb * (D / 16);
-    if (tasks <= kHalf) return launch_dependent(evict_move_kernel<D, 1>, grid, block, 0, s, a);
-    if (tasks <= 2 * kHalf) return launch_dependent(evict_move_kernel<D, 2>, grid, block, 0, s, a);
-    if (tasks <= 4 * kHalf) return launch_dependent(evict_move_kernel<D, 4>, grid, block, 0, s, a);
-    return launch_dependent(evict_move_kernel<D, 8>, grid, block, 0, s, a);
+    if (tasks <= kHalf) return launch_move_t<D, 1>(a, s);
+    if (tasks <= 2 * kHalf) return launch_move_t<D, 2>(a, s);
+    if (tasks <= 4 * kHalf) return launch_move_t<D, 4>(a, s);
+    return launch_move_t<D, 8>(a, s);
 }
 
 }  // namespace
@@ -358,7 +542,26 @@ cudaError_t launch_cache_append(const CacheAppendLaunch& a, cudaStream_t s) {
 }
 
 cudaError_t launch_cache_evict(const CacheEvictLaunch& a, cudaStream_t s) {
-    cudaError_t e = launch_dependent(evict_select_kernel, dim3((unsigned)a.B * a.Hkv), dim3(kSelThreads), 0, s, a);
+    // CTAs per (sequence, kv head): more while that still leaves each 2048 tokens and all of them fit at once
+    const long long bh = (long long)a.B * a.Hkv, cap = (long long)a.max_pages * a.page;
+    int ctas = 1;
+    while (ctas < 8 && cap >= 4096ll * ctas && bh * ctas * 2 <= a.num_sms) ctas *= 2;
+    if (bh * ctas > 0x7FFFFFFFll) return cudaErrorInvalidValue;
+    const long long per = (cap + (long long)ctas * kSelThreads - 1) / ((long long)ctas * kSelThreads);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(bh * ctas));
+    cfg.blockDim = dim3(kSelThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {(unsigned)ctas, 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    cudaError_t e = per <= 8    ? cudaLaunchKernelEx(&cfg, evict_select_kernel<8>, a, ctas)
+                    : per <= 32 ? cudaLaunchKernelEx(&cfg, evict_select_kernel<32>, a, ctas)
+                                : cudaLaunchKernelEx(&cfg, evict_select_kernel<0>, a, ctas);
     if (e != cudaSuccess) return e;
     return a.d == 128 ? launch_move<128>(a, s) : launch_move<64>(a, s);
 }

@@ -59,7 +59,7 @@ struct Cfg {
     static constexpr int ROWS = 8 * NB;                 // query rows per tile
     static constexpr int OROW = D + 4;                  // row of a merge buffer, floats; within it column d (of 8 runs of
                                                         // D / 8: g, then 2 i + e) is at 16 i + 2 g + e: no bank conflicts
-    static constexpr int BUFS = NB > 2 ? 1 : kWarps;    // merge buffers: one for each warp, or one in turn
+    static constexpr int BUFS = NB > 2 ? 2 : kWarps;    // merge buffers: one for each warp, or two in turns
     static constexpr int MERGE = kWarps * RING;         // byte offsets of the merge buffers
     static constexpr int QFRAGS = MERGE + BUFS * ROWS * OROW * 4;  // and of Q's fragments,
     static constexpr bool QSMEM = NB > 2;                          // which NB <= 2 has in registers
@@ -67,7 +67,7 @@ struct Cfg {
     // Registers: three CTAs' worth where that is enough.  Two run per SM: memory alone takes as long with one (128k
     // tokens: 51 us), and computing on top 68 us with one, 55 with two, 58 with three.
     static constexpr int REGS_FOR = NB > 1 ? 2 : 3, CTAS = 2;
-    static_assert(CTAS * (SMEM + 4096) <= 227 * 1024, "shared memory");
+    static_assert(CTAS * (SMEM + 2560) <= 227 * 1024, "shared memory");
 };
 
 struct Params {

@@ -29,11 +29,36 @@ __device__ __forceinline__ uint32_t e4m3x4(float x0, float x1, float x2, float x
     return (uint32_t)lo | ((uint32_t)hi << 16);
 }
 
+// Whether a positive float is a power of two in the normal range.
+__device__ __forceinline__ bool is_pow2(float s) {
+    const uint32_t u = __float_as_uint(s);
+    return (u & 0x807FFFFFu) == 0 && u - 0x00800000u < 0x7F000000u;
+}
+
 // Sixteen e4m3 bytes with scale `from` as e4m3 bytes with scale `to`, each
-// value rounded to nearest once more.  Powers of two only shift the exponent,
-// so nothing changes but values that become subnormal.
+// value rounded to nearest once more.  Between powers of two, downwards, that
+// is a product in fp16: it is exact wherever the result does not round to zero
+// (four significant bits above 2^-14), 3 instructions for 2 values against 40
+// with fp32 divisions, which bound the eviction at 62 us of B = 32, 1024 of
+// 4096 tokens.
 __device__ __forceinline__ uint4 e4m3_rescale16(uint4 x, float from, float to) {
     uint32_t* w = reinterpret_cast<uint32_t*>(&x);
+    if (from <= to && is_pow2(from) && is_pow2(to)) {
+        const int e = (int)(__float_as_uint(to) >> 23) - (int)(__float_as_uint(from) >> 23);
+        const __half2 f = __float2half2_rn(__uint_as_float((uint32_t)(127 - min(e, 126)) << 23));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint16_t r[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                uint32_t h = j ? e4m3x2_hi_to_half2(w[i]) : e4m3x2_to_half2(w[i]);
+                const __half2 p = __hmul2(*reinterpret_cast<const __half2*>(&h), f);
+                asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r[j]) : "r"(*reinterpret_cast<const uint32_t*>(&p)));
+            }
+            w[i] = (uint32_t)r[0] | ((uint32_t)r[1] << 16);
+        }
+        return x;
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const float2 a = half2_to_float2(e4m3x2_to_half2(w[i])), b = half2_to_float2(e4m3x2_hi_to_half2(w[i]));

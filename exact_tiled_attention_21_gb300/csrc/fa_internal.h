@@ -183,6 +183,7 @@ struct CacheAppendLaunch {
     const uint64_t* turns;  // [rot / 2], or null (no rotation)
     int B, Hkv, N, d, rot, interleaved, page, sb, max_pages, num_pages;
     float magnitude;
+    int num_sms;
     DevError* err;
 };
 
@@ -199,6 +200,7 @@ struct CacheEvictLaunch {
     float* new_weights;    // fp32 [B, Hkv, new_max_pages * page]
     int* kept;             // int32 [B, Hkv, new_max_pages * page]
     int B, Hkv, page, sb, max_pages, new_max_pages, num_pages, d, keep, recent;
+    int num_sms;
     DevError* err;
 };
 
