@@ -795,7 +795,7 @@ size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 // Workspace of the 8-bit decode: partial outputs and LSEs of every segment (at most one more per worker than there are
 // items), the sequences' first steps, and with weights the scores of every row and token.
 struct Fp8Workspace {
-    size_t part_lse, prefix, scores, bytes;
+    size_t part_lse, prefix, lse2, scores, bytes;
 };
 Fp8Workspace fp8_workspace(int B, int Hq, int Hkv, int Nq, int d, long long max_tokens, bool weights) {
     const int rows = Hq / Hkv * Nq, tile = fp8_tile_rows(rows);
@@ -803,7 +803,8 @@ Fp8Workspace fp8_workspace(int B, int Hq, int Hkv, int Nq, int d, long long max_
     Fp8Workspace w;
     w.part_lse = align256(slots * tile * d * 4);
     w.prefix = w.part_lse + align256(slots * tile * 4);
-    w.scores = w.prefix + align256(((size_t)B + 1) * 8);
+    w.lse2 = w.prefix + align256(((size_t)B + 1) * 8);
+    w.scores = w.lse2 + (weights ? align256((size_t)B * Hq * Nq * 4) : 0);
     w.bytes = w.scores + (weights ? align256((size_t)B * Hkv * ((rows + 3) & ~3) * (size_t)max_tokens * 4) : 0);
     return w;
 }
@@ -960,6 +961,7 @@ int fa_decode_paged_fp8(const void* q, const void* k_pages, const void* v_pages,
     a.part_lse = reinterpret_cast<float*>(base + ws.part_lse);
     a.scores = reinterpret_cast<float*>(base + ws.scores);
     a.prefix = reinterpret_cast<long long*>(base + ws.prefix);
+    a.lse2 = reinterpret_cast<float*>(base + ws.lse2);
     a.B = B;
     a.Hq = Hq;
     a.Hkv = Hkv;

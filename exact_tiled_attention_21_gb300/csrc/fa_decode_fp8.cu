@@ -3,25 +3,28 @@
 //
 // Every byte of the cache is read once per 32 query rows (the Hq / Hkv heads of
 // a group times the new tokens), 2 d bytes per key for 4 d flops per row: bound
-// by HBM.  So each warp works alone: it streams its own keys through a private
-// ring of cp.async copies, and nothing waits for another warp until the four
-// warps' results of a CTA are merged.
+// by HBM for 8 rows, by the instructions that widen the bytes for 32.  A CTA has
+// four warps.  Each streams 32 keys per step through a ring of cp.async copies
+// and holds 8 query rows; with up to 8 rows the warps take different keys and
+// wait for nobody until the end, with 16 or 32 the warps of a group of RG = 2 or
+// 4 read each other's keys for rows of their own.  (All rows in every warp
+// instead, in 255 registers: 50 us against 33 for 8 sequences of 8000 tokens, 4 kv
+// heads, 32 rows.)
 //
-// The work is one list of steps (128 keys at d = 128, 256 at d = 64) over all
-// sequences, kv heads and row tiles, cut into equal shares for as many CTAs as
-// run at once, from the lengths on the device: any batch of lengths, and any
-// capacity of the block table, keeps every SM busy to the end.  A CTA's share
-// crosses from one (sequence, kv head, row tile) to the next as it comes; the
-// part of one that a CTA holds is a segment.  Segment results go to the
-// workspace at slot CTA + item (which grows by one from each segment to the
-// next) and a second kernel merges the segments of each row.
+// The work is one list of steps of 128 keys over all sequences, kv heads and row
+// tiles, cut into equal shares for as many CTAs as run at once, from the lengths
+// on the device: any batch of lengths, and any capacity of the block table, keeps
+// every SM busy to the end.  A CTA's share crosses from one (sequence, kv head,
+// row tile) to the next as it comes, the copies running ahead; the part of one
+// that a CTA holds is a segment.  Segment results go to the workspace at slot
+// CTA + item (which grows by one from each segment to the next) and a second
+// kernel merges the segments of each row.
 //
 // The products are mma.sync m16n8k16 with fp16 operands and fp32 sums, because
 // an e4m3 value is exact in fp16 and the fragments can be read straight from
 // the cache's rows.  Both are taken transposed, S^T = K Q^T and O^T = V^T P^T,
 // so that the keys (and d) fill the 16 rows of a product and the queries its 8
-// columns: up to 8 query rows cost half of what 16 do (NB = 1, 2 or 4 column
-// tiles).  The order of d within K Q^T and of the keys within V^T P^T is free: a
+// columns.  The order of d within K Q^T and of the keys within V^T P^T is free: a
 // lane's 16 consecutive bytes of a K row are the k-indices of its A fragments,
 // and its d / 8 bytes of each of four V rows the k-pairs of its A fragments.  P
 // turns from S^T's accumulators into the B fragments by an 8 x 8 transpose.
@@ -32,8 +35,8 @@
 // elements 2^-28 below the row's largest).  With x_j the score in log2 units,
 // the softmax sums l = sum 2^(x_j - m) stay in fp32; the V product takes
 // 2^(x_j + log2 vs_j - M) in fp16 (relative 2^-11, an eighth of the result's
-// own bf16 step) with its own running maximum M, so that a block's scale can
-// have any size.  Result: O 2^(M - m) / l.
+// own bf16 step) with its own reference M, so that a block's scale can have any
+// size.  Result: O 2^(M - m) / l.
 #include <algorithm>
 #include <cfloat>
 #include <climits>
@@ -45,29 +48,28 @@ namespace fa {
 namespace {
 
 constexpr int kWarps = 4, kThreads = kWarps * 32;
+constexpr int kKeys = 32, kStep = kWarps * kKeys;  // keys per warp and step, and per CTA
+constexpr int kStages = 2;                         // steps in flight
 constexpr float kSlack = 8.f;  // how far (log2) a score may exceed the reference that its weight is relative to
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
 
-template <int D, int NB>
+template <int D, int RG>
 struct Cfg {
-    static constexpr int KEYS = D == 128 ? 32 : 64;     // keys per warp and step (8 KB of K and V)
-    static constexpr int STEP = kWarps * KEYS;          // keys per CTA and step
-    static constexpr int STAGES = 2;                    // steps in flight
-    static constexpr int HALF = KEYS * D;               // bytes of K (and of V) per step
-    static constexpr int SLOT = 2 * HALF + 8 * KEYS;    // K, V, K scales, log2 of V scales
-    static constexpr int RING = STAGES * SLOT;          // per warp
-    static constexpr int ROWS = 8 * NB;                 // query rows per tile
-    static constexpr int OROW = D + 4;                  // row of a merge buffer, floats; within it column d (of 8 runs of
-                                                        // D / 8: g, then 2 i + e) is at 16 i + 2 g + e: no bank conflicts
-    static constexpr int BUFS = NB > 2 ? 2 : kWarps;    // merge buffers: one for each warp, or two in turns
-    static constexpr int MERGE = kWarps * RING;         // byte offsets of the merge buffers
-    static constexpr int QFRAGS = MERGE + BUFS * ROWS * OROW * 4;  // and of Q's fragments,
-    static constexpr bool QSMEM = NB > 2;                          // which NB <= 2 has in registers
-    static constexpr int SMEM = QFRAGS + (QSMEM ? ROWS * D * 2 : 0);
-    // Registers: three CTAs' worth where that is enough.  Two run per SM: memory alone takes as long with one (128k
-    // tokens: 51 us), and computing on top 68 us with one, 55 with two, 58 with three.
-    static constexpr int REGS_FOR = NB > 1 ? 2 : 3, CTAS = 2;
-    static_assert(CTAS * (SMEM + 2560) <= 227 * 1024, "shared memory");
+    static constexpr int ROWS = 8 * RG, KG = kWarps / RG;  // query rows per tile; groups of warps with different keys
+    static constexpr int HALF = kKeys * D;                 // bytes of K (and of V) per warp and step
+    static constexpr int SLOT = 2 * HALF + 8 * kKeys;      // K, V, K scales, log2 of V scales
+    static constexpr int RING = kStages * SLOT;            // per warp
+    static constexpr int MERGE = kWarps * RING;            // byte offset of the merge buffers, one for each warp but the
+                                                           // first group's
+    static constexpr int OROW = D + 4;                     // a row of them, floats; within it column d (of 8 runs of
+                                                           // D / 8: g, then 2 i + e) is at 16 i + 2 g + e: no bank conflicts
+    static constexpr int SMEM = MERGE + (kWarps - RG) * 8 * OROW * 4;
+    // CTAs per SM, and those that the registers are made for.  d = 128, up to 8 rows: bound by HBM, and a third CTA
+    // only costs (128k tokens: 68 us with one, 55 with two, 58 with three; the copies alone 51 with one).  d = 64: bound
+    // by instructions, four CTAs 28.9 us, three 30.2, five 30.6 (16 sequences of 3000 tokens, 16 heads).  32 rows: 51 us
+    // with two CTAs of up to 255 registers, 55 with two of 168, 56 with three (8 sequences of 8000 tokens, 4 kv heads).
+    static constexpr int CTAS = D == 64 ? 4 : 2, REGS_FOR = D == 64 ? 4 : RG == 4 ? 2 : 3;
+    static_assert(CTAS * (SMEM + 1536) <= 227 * 1024, "shared memory");
 };
 
 struct Params {
@@ -85,6 +87,7 @@ struct Params {
     float* part_lse;     // [slot][ROWS], log2
     float* scores;       // per (sequence, kv head) and tile [key][rows of the tile], log2; null without weights
     long long* prefix;   // [B + 1] steps before each sequence, per (kv head, row tile)
+    float* lse2;         // [B*Hq*Nq] log2 LSE of each row, with weights
     int B, Hq, Hkv, Nq, max_pages, num_pages, rows, row_tiles, workers;
     uint32_t blocks_per_page;
     FastDiv page, sb;
@@ -96,7 +99,6 @@ __device__ __forceinline__ int clamp_len(int len, int cap) { return min(max(len,
 
 // Steps of all sequences before q (64-bit warp scan of the lengths): the sequence that step q falls in, its first step
 // and length.  With q beyond the end: sequence B and the total.  prefix: also written, if not null.
-template <int STEP>
 __device__ __forceinline__ void find_sequence(const int* lens, int B, int cap, long long q, long long* prefix, int& b,
                                               long long& start, int& len) {
     const int lane = threadIdx.x & 31;
@@ -104,7 +106,7 @@ __device__ __forceinline__ void find_sequence(const int* lens, int B, int cap, l
     b = B;
     for (int b0 = 0; b0 < B; b0 += 32) {
         const int l = b0 + lane < B ? clamp_len(lens[b0 + lane], cap) : 0;
-        const uint32_t n = (uint32_t)(l + STEP - 1) / STEP;
+        const uint32_t n = (uint32_t)(l + kStep - 1) / kStep;
         uint32_t incl = n;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -133,7 +135,6 @@ struct Cursor {
     int kvh, rt, s;       // kv head, row tile and step
 };
 
-template <int STEP>
 __device__ __forceinline__ void advance(Cursor& c, const Params& a, int cap) {
     if (++c.s < c.n) return;
     c.s = 0;
@@ -145,7 +146,7 @@ __device__ __forceinline__ void advance(Cursor& c, const Params& a, int cap) {
         ++c.b;
         c.len = c.b < a.B ? clamp_len(__ldg(a.lens + c.b), cap) : 0;
     } while (c.len == 0 && c.b < a.B);
-    c.n = (c.len + STEP - 1) / STEP;
+    c.n = (c.len + kStep - 1) / kStep;
 }
 
 // Where the scores [key][rows of the tile] of a tile begin.  A (sequence, kv head)'s rows are padded to a multiple of
@@ -155,53 +156,85 @@ __device__ __forceinline__ long long scores_at(const Params& a, long long bh, in
     return (bh * ((a.rows + 3) & ~3) + rt * ROWS) * cap;
 }
 
-template <int D, int NB>
-__global__ void __launch_bounds__(kThreads, Cfg<D, NB>::REGS_FOR) decode_fp8_kernel(const Params a) {
-    using C = Cfg<D, NB>;
-    constexpr int KEYS = C::KEYS, MT = KEYS / 16, KS = D / 16, DT = D / 8, ROWS = C::ROWS, STEP = C::STEP;
+template <int D, int RG>
+__global__ void __launch_bounds__(kThreads, Cfg<D, RG>::REGS_FOR) decode_fp8_kernel(const Params a) {
+    using C = Cfg<D, RG>;
+    constexpr int MT = kKeys / 16, KS = D / 16, DT = D / 8, ROWS = C::ROWS, KG = C::KG;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ float s_stat[kWarps][2][ROWS];  // m and l
-    __shared__ __align__(8) float s_up[ROWS];
+    __shared__ float s_stat[kWarps][2][8];  // m and l of a warp's rows
     __shared__ Cursor s_ahead[kWarps];
     pdl_launch_dependents();
     pdl_wait();
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    const int rg = warp % RG, kg = warp / RG;  // row group, and group of warps that share keys
     const int P = (int)a.page.d, cap = a.max_pages * P;
     if (blockIdx.x == 0)
         for (int i = tid; i < a.B; i += kThreads)
             if (a.lens[i] < 0 || a.lens[i] > cap) record_invalid(a.err, kSiteCacheLen, a.lens[i]);
-    // this CTA's share [u, u1) of the steps
+    // ---- this CTA's share of the steps: `count` of them from `cur`
     const long long per_step = (long long)a.Hkv * a.row_tiles;
-    long long u, u1;
+    Cursor cur;
+    int count;
     {
         int b, len;
-        long long total;
-        find_sequence<STEP>(a.lens, a.B, cap, LLONG_MAX, blockIdx.x == 0 && warp == 0 ? a.prefix : nullptr, b, total, len);
+        long long total, start;
+        find_sequence(a.lens, a.B, cap, LLONG_MAX, blockIdx.x == 0 && warp == 0 ? a.prefix : nullptr, b, total, len);
         total *= per_step;
         const long long workers = min((long long)a.workers, total);  // at least one step each
         if (blockIdx.x >= workers) return;
-        u = blockIdx.x * total / workers;
-        u1 = (blockIdx.x + 1ll) * total / workers;
-    }
-    Cursor cur;
-    {
-        long long start;
-        find_sequence<STEP>(a.lens, a.B, cap, u / per_step, nullptr, cur.b, start, cur.len);
-        cur.n = (cur.len + STEP - 1) / STEP;
+        const long long u = blockIdx.x * total / workers;
+        count = (int)((blockIdx.x + 1ll) * total / workers - u);
+        find_sequence(a.lens, a.B, cap, u / per_step, nullptr, cur.b, start, cur.len);
+        cur.n = (cur.len + kStep - 1) / kStep;
         const long long in_b = u - start * per_step;
         const int item_b = (int)(in_b / cur.n);
         cur.s = (int)(in_b - (long long)item_b * cur.n);
         cur.kvh = item_b / a.row_tiles;
         cur.rt = item_b - cur.kvh * a.row_tiles;
     }
-    const int count = (int)min(u1 - u, (long long)INT_MAX);  // steps (2^47 in all / workers; far below 2^31 in memory)
 
-    // ---- the ring: this warp's keys of the steps ahead, whatever item they are of
-    bool bad = false;
-    uint8_t* ring = smem + warp * C::RING;
-    const uint32_t ring_u = smem_u32(ring);
-    uint2* qsm = reinterpret_cast<uint2*>(smem + C::QFRAGS);
+    // ---- Q fragments: k-step s of lane (g, t) is row g, columns (D = 128: 64 (s / 4) +) 16 t + 4 (s % 4) .. + 3
+    uint32_t qb[KS][2];
+    float sc[2];  // score scale of the rows whose scores this lane holds: 2 t, 2 t + 1 of its row group
+    auto load_q = [&](uint32_t (&w)[D / 8]) {
+        const int r = cur.rt * ROWS + rg * 8 + g;
+        const uint4* src =
+            reinterpret_cast<const uint4*>(a.q + (((long long)cur.b * a.Hkv + cur.kvh) * a.rows + r) * D + t * 16);
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+            const uint4 x = r < a.rows ? src[i / 2 * 8 + i % 2] : make_uint4(0, 0, 0, 0);
+            w[i * 4] = x.x, w[i * 4 + 1] = x.y, w[i * 4 + 2] = x.z, w[i * 4 + 3] = x.w;
+        }
+    };
+    auto make_q = [&](const uint32_t (&w)[D / 8]) {
+        float big = 0.f;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+            big = fmaxf(big, fmaxf(fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xFFFF0000u))));
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+        // power of two that brings the row's largest element into [2^14, 2^15); rows of zeros, and of infinities (which
+        // stay what they are), keep theirs
+        int e = (int)(__float_as_uint(big) >> 23) - 127 - 14;
+        if (big == 0.f || !(big <= 3.4e38f)) e = 0;
+        e = max(e, -112);  // 2^-e stays a normal number
+        const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+        const float up = a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint32_t x = w[s * 2 + j];
+                const __half2 h = __floats2half2_rn(__uint_as_float(x << 16) * down,
+                                                    __uint_as_float(x & 0xFFFF0000u) * down);
+                qb[s][j] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) sc[j] = __shfl_sync(0xffffffffu, up, (2 * t + j) * 4);
+    };
+
+    // ---- the ring: this warp's 32 keys of the steps ahead, whatever item they are of
     // A copy instruction moves whole rows (D / 16 lanes a row, so that a quarter warp asks for 128 consecutive bytes);
     // the fragments' readers find their 16 bytes (V at D = 64: 8) at
     //   K: (key / 8, half h of D = 128, lane' = 4 (key % 8) + t), lane' ^ 4 h
@@ -210,6 +243,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::REGS_FOR) decode_fp8_ker
     // The exclusive-ors keep both the copies and the reads free of bank conflicts.  A 32-byte sector of a row stays
     // together: a copy whose sector is torn apart in shared memory fetches it from L2 once per piece (V in 16-byte
     // pieces: 1.5 times the bytes in all, which bound the kernel at 58 us of a 128k-token, 8-head cache).
+    uint8_t* ring = smem + warp * C::RING;
+    const uint32_t ring_u = smem_u32(ring);
     constexpr int LPR = D / 16, RPI = 32 / LPR;  // lanes per row, rows per copy instruction
     const int cr = lane / LPR, cc = lane % LPR;
     const uint8_t* kp = a.kp + cc * 16;
@@ -224,29 +259,24 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::REGS_FOR) decode_fp8_ker
         vdst[0] = C::HALF + ((cr & 1) * 8 + 4 * (cc >> 1) + ((cr >> 1) ^ ((cc >> 1) | (cr & 1) << 1))) * 32 + (cc & 1) * 16;
         vdst[1] = vdst[0] + 2 * 8 * 32;  // r + 2
     }
-    using Keys = int[KEYS / 32];     // of lane's key (+ 32) of a step
-    using Scales = float[KEYS / 32];
-    Cursor& ahead = s_ahead[warp];  // the step after those in `to_issue`; in shared memory to spare registers
+    Cursor& ahead = s_ahead[warp];  // the step after `to_issue`; in shared memory to spare registers
     if (lane == 0) ahead = cur;
     __syncwarp();
     int fetched = 0, issued = 0;
+    bool bad = false;
     struct {
-        Keys page;                 // pages of the lane's keys, loaded one step before their use
-        int key0, len, kvh;
+        int page, key, len, kvh;  // the lane's key and its page, loaded one step before its use
     } to_issue;
-    auto fetch_pages = [&]() {
-        to_issue.key0 = ahead.s * STEP + warp * KEYS;
+    auto fetch_page = [&]() {
+        to_issue.key = ahead.s * kStep + warp * kKeys + lane;
         to_issue.len = ahead.len;
         to_issue.kvh = ahead.kvh;
-        const int* trow = a.table + (long long)ahead.b * a.max_pages;
-#pragma unroll
-        for (int i = 0; i < KEYS / 32; ++i) {
-            const int key = to_issue.key0 + i * 32 + lane;
-            to_issue.page[i] = (fetched < count && key < ahead.len) ? trow[a.page.div(key)] : -1;
-        }
+        to_issue.page = fetched < count && to_issue.key < ahead.len
+                            ? a.table[(long long)ahead.b * a.max_pages + a.page.div(to_issue.key)]
+                            : -1;
         if (++fetched < count) {
             Cursor next = ahead;
-            advance<STEP>(next, a, cap);
+            advance(next, a, cap);
             __syncwarp();
             if (lane == 0) ahead = next;
             __syncwarp();
@@ -254,19 +284,17 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::REGS_FOR) decode_fp8_ker
     };
     // Scales are loaded, not copied (a 4-byte copy asks L2 once per lane, a load once per sector), and put into the
     // ring one step later, when they have arrived; V's as logarithms.
-    auto put_scales = [&](int slot, const Scales& ks, const Scales& vs) {
+    float ks_next = 0.f, vs_next = 0.f;
+    auto put_scales = [&](int slot, float ks, float vs) {
         float* f = reinterpret_cast<float*>(ring + slot * C::SLOT + 2 * C::HALF) + lane;
-#pragma unroll
-        for (int i = 0; i < KEYS / 32; ++i) {
-            f[i * 32] = ks[i];
-            f[KEYS + i * 32] = lg2(vs[i]);
-        }
+        f[0] = ks;
+        f[kKeys] = lg2(vs);
     };
     // ALL: every key of the step is there.
-    auto copy = [&](uint32_t base, const uint32_t (&row)[KEYS / 32], const bool ALL) {
+    auto copy = [&](uint32_t base, uint32_t row, const bool ALL) {
 #pragma unroll
-        for (int n = 0; n < KEYS / RPI; ++n) {
-            const uint32_t rr = __shfl_sync(0xffffffffu, row[n * RPI / 32], (n * RPI + cr) & 31);
+        for (int n = 0; n < kKeys / RPI; ++n) {
+            const uint32_t rr = __shfl_sync(0xffffffffu, row, n * RPI + cr);
             const bool ok = ALL || rr != ~0u;
             const size_t off = (size_t)(ok ? rr : 0u) * D;
             uint32_t ko, vo;  // slots of copy n
@@ -281,25 +309,18 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::REGS_FOR) decode_fp8_ker
             cp_async16(base + vdst[n & 1] + vo, vp + off, ok);
         }
     };
-    auto issue = [&](int slot, Scales& ks, Scales& vs) {
+    auto issue = [&](int slot, float& ks, float& vs) {
         if (issued < count) {
-            uint32_t row[KEYS / 32];  // cache row of key lane (+ 32), ~0 for none
-            bool all = true;
-#pragma unroll
-            for (int i = 0; i < KEYS / 32; ++i) {
-                const int key = to_issue.key0 + i * 32 + lane;
-                const int pg = to_issue.page[i];
-                const bool in = key < to_issue.len, ok = in && (unsigned)pg < (unsigned)a.num_pages;
-                bad |= in && !ok;
-                all &= ok;
-                const uint32_t at = (uint32_t)key - a.page.div(key) * P;
-                const uint32_t head = (uint32_t)pg * a.Hkv + to_issue.kvh;
-                row[i] = ok ? head * P + at : ~0u;
-                const uint32_t blk = ok ? head * a.blocks_per_page + a.sb.div(at) : 0u;
-                ks[i] = ok ? __ldg(a.ks + blk) : 0.f;
-                vs[i] = ok ? __ldg(a.vs + blk) : 0.f;
-            }
-            if (__all_sync(0xffffffffu, all))
+            const int key = to_issue.key, pg = to_issue.page;
+            const bool in = key < to_issue.len, ok = in && (unsigned)pg < (unsigned)a.num_pages;
+            bad |= in && !ok;
+            const uint32_t at = (uint32_t)key - a.page.div(key) * P;
+            const uint32_t head = (uint32_t)pg * a.Hkv + to_issue.kvh;
+            const uint32_t row = ok ? head * P + at : ~0u;  // cache row of the lane's key, ~0 for none
+            const uint32_t blk = ok ? head * a.blocks_per_page + a.sb.div(at) : 0u;
+            ks = ok ? __ldg(a.ks + blk) : 0.f;
+            vs = ok ? __ldg(a.vs + blk) : 0.f;
+            if (__all_sync(0xffffffffu, ok))
                 copy(ring_u + slot * C::SLOT, row, true);
             else
                 copy(ring_u + slot * C::SLOT, row, false);
@@ -307,388 +328,304 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::REGS_FOR) decode_fp8_ker
         ++issued;
         cp_async_commit();
     };
-    Scales ks_next, vs_next;  // scales of the step issued last
-    static_assert(C::STAGES == 2, "the start below");
-    {
-        Scales ks, vs;
-        fetch_pages();
-        auto first = to_issue;
-        fetch_pages();
-        auto second = to_issue;
-        fetch_pages();
+    // a step's keys are read by the warps of the group
+    auto group_sync = [&]() {
+        if constexpr (RG == 1)
+            __syncwarp();
+        else if (RG == kWarps || kg == 0)
+            bar_sync(1, RG * 32);
+        else
+            bar_sync(2, RG * 32);
+    };
+    static_assert(kStages == 2, "the start");
+    {   // the loads of the first steps depend on each other (lengths, pages, rows): the queries' come in between
+        uint32_t w[D / 8];
+        fetch_page();
+        const auto first = to_issue;
+        fetch_page();
+        const auto second = to_issue;
+        load_q(w);
+        fetch_page();
         const auto third = to_issue;
+        float ks = 0.f, vs = 0.f;
         to_issue = first;
-#pragma unroll
-        for (int i = 0; i < KEYS / 32; ++i) ks[i] = vs[i] = ks_next[i] = vs_next[i] = 0.f;
         issue(0, ks, vs);
         to_issue = second;
         issue(1, ks_next, vs_next);
         to_issue = third;
+        make_q(w);
         put_scales(0, ks, vs);
     }
 
-    // ---- what a segment holds
-    uint32_t qb[C::QSMEM ? 1 : NB][KS][2];
-    float sc[C::QSMEM ? 1 : NB][2];  // (NB <= 2) score scale of the rows whose scores this lane holds: 8 nb + 2 t, + 1
-    float acc[D / 16][NB][4];
-    float m[NB][2], M[NB][2], l[NB][2];  // of rows 8 nb + 2 t + j; the maxima start at the lowest number: a row
-                                         // that sees no key keeps l = 0 (2^(-inf - m))
-    int seg = 0;  // first step of the segment within its item
+    // ---- the steps
+    float acc[D / 16][4];      // columns g d / 8 + 2 i + c / 2 of rows 2 t + c % 2
+    float m[2], M[2], l[2];    // of rows 2 t + j; the references start at the lowest number: a row that sees no key
+                               // keeps l = 0 (2^(-inf - m))
+    int seg = 0, slot = 0;     // first step of the segment within its item; ring slot
     bool begins = true;
-    int slot = 0;
     for (int it = 0; it < count; ++it) {
-    const int r0 = cur.rt * ROWS, nrows = min(ROWS, a.rows - r0);      // query rows of the tile
-    const long long bh = (long long)cur.b * a.Hkv + cur.kvh;
-    const long long row0 = bh * a.rows + r0;                           // (b, head, token) flattened
-    if (begins) {
-    seg = cur.s;
-    // ---- Q fragments: k-step s of lane (g, t) is row g, columns (D = 128: 64 (s / 4) +) 16 t + 4 (s % 4) .. + 3
-#pragma unroll
-    for (int f = 0; f < (C::QSMEM ? 1 : NB); ++f) {
-        const int nb = C::QSMEM ? warp : f;  // in shared memory each warp makes one column tile
-        static_assert(!C::QSMEM || NB == kWarps, "one column tile per warp");
-        uint32_t w[D / 8];
-        if (nb * 8 + g < nrows) {
-            const uint4* src = reinterpret_cast<const uint4*>(a.q + (row0 + nb * 8 + g) * D + t * 16);
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-                const uint4 x = src[i / 2 * 8 + i % 2];
-                w[i * 4] = x.x, w[i * 4 + 1] = x.y, w[i * 4 + 2] = x.z, w[i * 4 + 3] = x.w;
+        const int r0 = cur.rt * ROWS + rg * 8, nrows = min(ROWS, a.rows - cur.rt * ROWS);  // of the warp, of the tile
+        const long long bh = (long long)cur.b * a.Hkv + cur.kvh;
+        if (begins) {
+            if (it > 0) {
+                uint32_t w[D / 8];
+                load_q(w);
+                make_q(w);
             }
-        } else {
+            seg = cur.s;
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i) w[i] = 0;
+            for (int i = 0; i < D / 16; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) m[j] = M[j] = -FLT_MAX, l[j] = 0.f;
         }
-        float big = 0.f;
+        cp_async_wait<kStages - 1>();
+        group_sync();  // every lane's copies are there
+#pragma unroll 1
+        for (int part = 0; part < RG; ++part) {
+            const int key0 = cur.s * kStep + (kg * RG + part) * kKeys;
+            if (key0 >= cur.len || rg * 8 >= nrows) break;
+            const uint8_t* st = smem + (kg * RG + part) * C::RING + slot * C::SLOT;
+            float S[MT][4];  // keys 16 i + g, + 8 (c / 2) of rows 2 t + c % 2
+            const uint4* kf = reinterpret_cast<const uint4*>(st);
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i)
-            big = fmaxf(big, fmaxf(fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xFFFF0000u))));
-        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
-        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-        // power of two that brings the row's largest element into [2^14, 2^15); rows of zeros, and of
-        // infinities (which stay what they are), keep theirs
-        int e = (int)(__float_as_uint(big) >> 23) - 127 - 14;
-        if (big == 0.f || !(big <= 3.4e38f)) e = 0;
-        e = max(e, -112);  // 2^-e stays a normal number
-        const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-        const float up = a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);
+            for (int i = 0; i < MT; ++i) S[i][0] = S[i][1] = S[i][2] = S[i][3] = 0.f;
 #pragma unroll
-        for (int s = 0; s < KS; ++s) {
+            for (int h = 0; h < D / 64; ++h) {
+                uint32_t w[2 * MT][4];
+                const int at = h * 32 + (lane ^ (4 * h));
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const uint32_t x = w[s * 2 + j];
-                const __half2 h = __floats2half2_rn(__uint_as_float(x << 16) * down,
-                                                    __uint_as_float(x & 0xFFFF0000u) * down);
-                qb[f][s][j] = *reinterpret_cast<const uint32_t*>(&h);
-            }
-            if constexpr (C::QSMEM) qsm[(s * NB + nb) * 32 + lane] = make_uint2(qb[0][s][0], qb[0][s][1]);
-        }
-        if constexpr (C::QSMEM) {
-            if (t == 0) s_up[nb * 8 + g] = up;
-        } else {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) sc[f][j] = __shfl_sync(0xffffffffu, up, (2 * t + j) * 4);
-        }
-    }
-    if constexpr (C::QSMEM) {
-        __syncthreads();
-    }
-#pragma unroll
-    for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) acc[i][nb][c] = 0.f;
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) m[nb][j] = M[nb][j] = -FLT_MAX, l[nb][j] = 0.f;
-    }
-
-    const int key0 = cur.s * STEP + warp * KEYS;
-        cp_async_wait<C::STAGES - 1>();
-        __syncwarp();  // every lane's copies are there
-        const uint8_t* st = ring + slot * C::SLOT;
-        if (key0 < cur.len) {
-        float S[MT][NB][4];  // keys 16 i + g, + 8 (c / 2) of rows 8 nb + 2 t + c % 2
-        const uint4* kf = reinterpret_cast<const uint4*>(st);
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb) S[i][nb][0] = S[i][nb][1] = S[i][nb][2] = S[i][nb][3] = 0.f;
-#pragma unroll
-        for (int h = 0; h < D / 64; ++h) {
-            uint32_t w[2 * MT][4];
-            const int at = h * 32 + (lane ^ (4 * h));
-#pragma unroll
-            for (int i = 0; i < 2 * MT; ++i) {
-                const uint4 x = kf[i * (D / 64) * 32 + at];
-                w[i][0] = x.x, w[i][1] = x.y, w[i][2] = x.z, w[i][3] = x.w;
-            }
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                uint32_t q0[NB], q1[NB];
-#pragma unroll
-                for (int nb = 0; nb < NB; ++nb) {
-                    if constexpr (C::QSMEM) {
-                        const uint2 x = qsm[((h * 4 + c) * NB + nb) * 32 + lane];
-                        q0[nb] = x.x, q1[nb] = x.y;
-                    } else {
-                        q0[nb] = qb[nb][h * 4 + c][0], q1[nb] = qb[nb][h * 4 + c][1];
-                    }
+                for (int i = 0; i < 2 * MT; ++i) {
+                    const uint4 x = kf[i * (D / 64) * 32 + at];
+                    w[i][0] = x.x, w[i][1] = x.y, w[i][2] = x.z, w[i][3] = x.w;
                 }
 #pragma unroll
-                for (int i = 0; i < MT; ++i) {
-                    const uint32_t ka[4] = {e4m3x2_to_half2(w[2 * i][c]), e4m3x2_to_half2(w[2 * i + 1][c]),
-                                            e4m3x2_hi_to_half2(w[2 * i][c]), e4m3x2_hi_to_half2(w[2 * i + 1][c])};
+                for (int c = 0; c < 4; ++c)
 #pragma unroll
-                    for (int nb = 0; nb < NB; ++nb) mma_16816(S[i][nb], ka, q0[nb], q1[nb]);
-                }
-            }
-        }
-        const float* ksf = reinterpret_cast<const float*>(st + 2 * C::HALF) + g;
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const float kscale = ksf[i * 16 + h * 8];
-#pragma unroll
-                for (int nb = 0; nb < NB; ++nb) {
-                    float2 x;
-                    if constexpr (C::QSMEM)
-                        x = *reinterpret_cast<const float2*>(s_up + nb * 8 + 2 * t);
-                    else
-                        x = make_float2(sc[nb][0], sc[nb][1]);
-                    S[i][nb][2 * h] *= x.x * kscale;
-                    S[i][nb][2 * h + 1] *= x.y * kscale;
-                }
-            }
-        if (key0 + MT * 16 > cur.len - a.Nq + 1) {  // some row does not see every key
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int lim = cur.len - a.Nq + (r0 + nb * 8 + 2 * t + j) % a.Nq + 1 - key0 - g;
-#pragma unroll
-                    for (int i = 0; i < MT; ++i)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h)
-                            if (i * 16 + h * 8 >= lim) S[i][nb][2 * h + j] = -INFINITY;
-                }
-        }
-        if (a.scores) {  // [key][row of the tile]: a lane's two rows are neighbours
-            float* sr = a.scores + scores_at<ROWS>(a, bh, cur.rt, cap) + (long long)(key0 + g) * nrows + 2 * t;
-#pragma unroll
-            for (int i = 0; i < MT; ++i)
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    if (key0 + i * 16 + h * 8 + g < cur.len)
-#pragma unroll
-                        for (int nb = 0; nb < NB; ++nb) {
-                            float* at = sr + (i * 16 + h * 8) * nrows + nb * 8;
-                            if ((nrows & 1) == 0) {
-                                if (nb * 8 + 2 * t < nrows)
-                                    *reinterpret_cast<float2*>(at) = make_float2(S[i][nb][2 * h], S[i][nb][2 * h + 1]);
-                            } else {
-                                if (nb * 8 + 2 * t < nrows) at[0] = S[i][nb][2 * h];
-                                if (nb * 8 + 2 * t + 1 < nrows) at[1] = S[i][nb][2 * h + 1];
-                            }
-                        }
-        }
-        // ---- softmax: p = 2^(x - m) into l; w = 2^(x + log2 vs - M) for the value product.  m and M need not be the
-        // maxima, only within 2^8 of them (fp16 holds 2^15): most steps find no larger one and skip the reductions.
-        float mx[NB][2];
-        bool grown = false;
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                mx[nb][j] = fmaxf(S[0][nb][j], S[0][nb][2 + j]);
-#pragma unroll
-                for (int i = 1; i < MT; ++i) mx[nb][j] = fmax3(mx[nb][j], S[i][nb][j], S[i][nb][2 + j]);
-                grown |= mx[nb][j] > m[nb][j] + kSlack;
-            }
-        if (__any_sync(0xffffffffu, grown)) {
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    float x = fmaxf(m[nb][j], mx[nb][j]);
-#pragma unroll
-                    for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-                    l[nb][j] *= ex2(m[nb][j] - x);
-                    m[nb][j] = x;
-                }
-        }
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const float lv = ksf[KEYS + i * 16 + h * 8];
-#pragma unroll
-                for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        l[nb][j] += ex2(S[i][nb][2 * h + j] - m[nb][j]);
-                        S[i][nb][2 * h + j] += lv;
+                    for (int i = 0; i < MT; ++i) {
+                        const uint32_t ka[4] = {e4m3x2_to_half2(w[2 * i][c]), e4m3x2_to_half2(w[2 * i + 1][c]),
+                                                e4m3x2_hi_to_half2(w[2 * i][c]), e4m3x2_hi_to_half2(w[2 * i + 1][c])};
+                        mma_16816(S[i], ka, qb[h * 4 + c][0], qb[h * 4 + c][1]);
                     }
             }
-        grown = false;
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                mx[nb][j] = fmaxf(S[0][nb][j], S[0][nb][2 + j]);
-#pragma unroll
-                for (int i = 1; i < MT; ++i) mx[nb][j] = fmax3(mx[nb][j], S[i][nb][j], S[i][nb][2 + j]);
-                grown |= mx[nb][j] > M[nb][j] + kSlack;
-            }
-        if (__any_sync(0xffffffffu, grown)) {
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    float x = fmaxf(M[nb][j], mx[nb][j]);
-#pragma unroll
-                    for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-                    const float f = ex2(M[nb][j] - x);
-                    M[nb][j] = x;
-#pragma unroll
-                    for (int i = 0; i < D / 16; ++i) {
-                        acc[i][nb][j] *= f;
-                        acc[i][nb][2 + j] *= f;
-                    }
-                }
-        }
-        uint32_t pb[MT][NB][2];
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
+            const float* ksf = reinterpret_cast<const float*>(st + 2 * C::HALF) + g;
 #pragma unroll
             for (int i = 0; i < MT; ++i)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const __half2 w = __floats2half2_rn(ex2(S[i][nb][2 * h] - M[nb][0]),
-                                                        ex2(S[i][nb][2 * h + 1] - M[nb][1]));
-                    pb[i][nb][h] = transpose8x8(*reinterpret_cast<const uint32_t*>(&w));
+                    const float kscale = ksf[i * 16 + h * 8];
+                    S[i][2 * h] *= sc[0] * kscale;
+                    S[i][2 * h + 1] *= sc[1] * kscale;
                 }
-        }
-        const uint8_t* vf = st + C::HALF;
+            if (key0 + kKeys > cur.len - a.Nq + 1) {  // some row does not see every key
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            uint32_t v[4][DT / 4];
+                for (int j = 0; j < 2; ++j) {
+                    const int lim = cur.len - a.Nq + (r0 + 2 * t + j) % a.Nq + 1 - key0 - g;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                if constexpr (D == 128) {
-                    const uint4 x = *reinterpret_cast<const uint4*>(vf + ((i * 4 + r) * 16 + 4 * (g >> 1) + (t ^ (g >> 1))) * 32 + (g & 1) * 16);
-                    v[r][0] = x.x, v[r][1] = x.y, v[r][2] = x.z, v[r][3] = x.w;
-                } else {
-                    const uint2 x = *reinterpret_cast<const uint2*>(
-                        vf + ((i * 4 + r) * 8 + 4 * (g >> 2) + (t ^ ((g >> 2) | (r & 1) << 1))) * 32 + (g & 3) * 8);
-                    v[r][0] = x.x, v[r][1] = x.y;
+                    for (int i = 0; i < MT; ++i)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            if (i * 16 + h * 8 >= lim) S[i][2 * h + j] = -INFINITY;
+                }
+            }
+            if (a.scores) {  // [key][row of the tile]: a lane's two rows are neighbours
+                const int r = rg * 8 + 2 * t;
+                float* sr = a.scores + scores_at<ROWS>(a, bh, cur.rt, cap) + (long long)(key0 + g) * nrows + r;
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        if (key0 + i * 16 + h * 8 + g < cur.len) {
+                            float* at = sr + (i * 16 + h * 8) * nrows;
+                            if ((nrows & 1) == 0) {
+                                if (r < nrows) *reinterpret_cast<float2*>(at) = make_float2(S[i][2 * h], S[i][2 * h + 1]);
+                            } else {
+                                if (r < nrows) at[0] = S[i][2 * h];
+                                if (r + 1 < nrows) at[1] = S[i][2 * h + 1];
+                            }
+                        }
+            }
+            // ---- softmax: p = 2^(x - m) into l; w = 2^(x + log2 vs - M) for the value product.  m and M need not be
+            // the maxima, only within 2^8 of them (fp16 holds 2^15): most steps find no larger one and skip the
+            // reductions.
+            float mx[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                mx[j] = fmaxf(S[0][j], S[0][2 + j]);
+#pragma unroll
+                for (int i = 1; i < MT; ++i) mx[j] = fmax3(mx[j], S[i][j], S[i][2 + j]);
+            }
+            if (__any_sync(0xffffffffu, mx[0] > m[0] + kSlack || mx[1] > m[1] + kSlack)) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    float x = fmaxf(m[j], mx[j]);
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+                    l[j] *= ex2(m[j] - x);
+                    m[j] = x;
                 }
             }
 #pragma unroll
-            for (int c = 0; c < DT / 4; ++c)
+            for (int i = 0; i < MT; ++i)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {  // columns g d / 8 + 4 c + 2 h (row g of the fragment) and + 1 (row g + 8)
-                    const uint32_t sel = h ? 0x7362u : 0x5140u;
-                    const uint32_t x = __byte_perm(v[0][c], v[1][c], sel), y = __byte_perm(v[2][c], v[3][c], sel);
-                    const uint32_t va[4] = {e4m3x2_to_half2(x), e4m3x2_hi_to_half2(x), e4m3x2_to_half2(y),
-                                            e4m3x2_hi_to_half2(y)};
+                for (int h = 0; h < 2; ++h) {
+                    const float lv = ksf[kKeys + i * 16 + h * 8];
 #pragma unroll
-                    for (int nb = 0; nb < NB; ++nb) mma_16816(acc[2 * c + h][nb], va, pb[i][nb][0], pb[i][nb][1]);
+                    for (int j = 0; j < 2; ++j) {
+                        l[j] += ex2(S[i][2 * h + j] - m[j]);
+                        S[i][2 * h + j] += lv;
+                    }
                 }
-        }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                mx[j] = fmaxf(S[0][j], S[0][2 + j]);
+#pragma unroll
+                for (int i = 1; i < MT; ++i) mx[j] = fmax3(mx[j], S[i][j], S[i][2 + j]);
+            }
+            if (__any_sync(0xffffffffu, mx[0] > M[0] + kSlack || mx[1] > M[1] + kSlack)) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    float x = fmaxf(M[j], mx[j]);
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+                    const float f = ex2(M[j] - x);
+                    M[j] = x;
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i) {
+                        acc[i][j] *= f;
+                        acc[i][2 + j] *= f;
+                    }
+                }
+            }
+            uint32_t pb[MT][2];
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const __half2 w = __floats2half2_rn(ex2(S[i][2 * h] - M[0]), ex2(S[i][2 * h + 1] - M[1]));
+                    pb[i][h] = transpose8x8(*reinterpret_cast<const uint32_t*>(&w));
+                }
+            const uint8_t* vf = st + C::HALF;
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                uint32_t v[4][DT / 4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    if constexpr (D == 128) {
+                        const uint4 x = *reinterpret_cast<const uint4*>(
+                            vf + ((i * 4 + r) * 16 + 4 * (g >> 1) + (t ^ (g >> 1))) * 32 + (g & 1) * 16);
+                        v[r][0] = x.x, v[r][1] = x.y, v[r][2] = x.z, v[r][3] = x.w;
+                    } else {
+                        const uint2 x = *reinterpret_cast<const uint2*>(
+                            vf + ((i * 4 + r) * 8 + 4 * (g >> 2) + (t ^ ((g >> 2) | (r & 1) << 1))) * 32 + (g & 3) * 8);
+                        v[r][0] = x.x, v[r][1] = x.y;
+                    }
+                }
+#pragma unroll
+                for (int c = 0; c < DT / 4; ++c)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {  // columns g d / 8 + 4 c + 2 h (row g of the fragment) and + 1 (row g + 8)
+                        const uint32_t sel = h ? 0x7362u : 0x5140u;
+                        const uint32_t x = __byte_perm(v[0][c], v[1][c], sel), y = __byte_perm(v[2][c], v[3][c], sel);
+                        const uint32_t va[4] = {e4m3x2_to_half2(x), e4m3x2_hi_to_half2(x), e4m3x2_to_half2(y),
+                                                e4m3x2_hi_to_half2(y)};
+                        mma_16816(acc[2 * c + h], va, pb[i][0], pb[i][1]);
+                    }
+            }
         }
         put_scales(slot ^ 1, ks_next, vs_next);
-        __syncwarp();  // every lane has read this slot
+        group_sync();  // every lane has read this slot
         issue(slot, ks_next, vs_next);
-        fetch_pages();
+        fetch_page();
         slot ^= 1;
 
-    // ---- at the segment's end, merge the warps: O = sum_w O_w 2^(M_w - m) / l
-    const bool item_ends = cur.s + 1 == cur.n;
-    begins = item_ends || it + 1 == count;
-    if (begins) {
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
+        // ---- at the segment's end: O = sum over the warps with these rows of O_w 2^(M_w - m) / l
+        const bool item_ends = cur.s + 1 == cur.n;
+        begins = item_ends || it + 1 == count;
+        if (begins) {
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const int r = nb * 8 + 2 * t + j;
 #pragma unroll
-                for (int d = 4; d < 32; d <<= 1) l[nb][j] += __shfl_xor_sync(0xffffffffu, l[nb][j], d);
-                if (g == 0) s_stat[warp][0][r] = m[nb][j], s_stat[warp][1][r] = l[nb][j];
+                for (int d = 4; d < 32; d <<= 1) l[j] += __shfl_xor_sync(0xffffffffu, l[j], d);
+                if (KG > 1 && g == 0) s_stat[warp][0][2 * t + j] = m[j], s_stat[warp][1][2 * t + j] = l[j];
             }
-        __syncthreads();
-        float f[NB][2];
+            float f[2];
+            if constexpr (KG > 1) {
+                __syncthreads();
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
+                for (int j = 0; j < 2; ++j) {
+                    const int r = 2 * t + j;
+                    float top = m[j], sum = 0.f;
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int r = nb * 8 + 2 * t + j;
-                float top = s_stat[0][0][r];
+                    for (int w = 0; w < KG; ++w) top = fmaxf(top, s_stat[w * RG + rg][0][r]);
 #pragma unroll
-                for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s_stat[w][0][r]);
-                f[nb][j] = ex2(M[nb][j] - top);
-            }
-        float* buf = reinterpret_cast<float*>(smem + C::MERGE) + (warp % C::BUFS) * ROWS * C::OROW;
-#pragma unroll 1
-        for (int turn = 0; turn < kWarps / C::BUFS; ++turn) {
-            if (warp / C::BUFS == turn) {
+                    for (int w = 0; w < KG; ++w) sum += s_stat[w * RG + rg][1][r] * ex2(s_stat[w * RG + rg][0][r] - top);
+                    f[j] = ex2(M[j] - top);
+                    m[j] = top;
+                    l[j] = sum;
+                }
+                float* buf = reinterpret_cast<float*>(smem + C::MERGE);
+                if (kg > 0) {
 #pragma unroll
-                for (int nb = 0; nb < NB; ++nb)
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int i = 0; i < D / 16; ++i)
+                            *reinterpret_cast<float2*>(buf + ((warp - RG) * 8 + 2 * t + j) * C::OROW + i * 16 + g * 2) =
+                                make_float2(acc[i][j] * f[j], acc[i][2 + j] * f[j]);
+                }
+                __syncthreads();
+                if (kg == 0) {
 #pragma unroll
                     for (int j = 0; j < 2; ++j)
 #pragma unroll
                         for (int i = 0; i < D / 16; ++i) {
-                            float2* at = reinterpret_cast<float2*>(buf + (nb * 8 + 2 * t + j) * C::OROW + i * 16 + g * 2);
-                            float2 x = make_float2(acc[i][nb][j] * f[nb][j], acc[i][nb][2 + j] * f[nb][j]);
-                            if (turn) {
-                                const float2 y = *at;
+                            float2 x = make_float2(acc[i][j] * f[j], acc[i][2 + j] * f[j]);
+#pragma unroll
+                            for (int w = 1; w < KG; ++w) {
+                                const float2 y = *reinterpret_cast<const float2*>(
+                                    buf + (((w - 1) * RG + rg) * 8 + 2 * t + j) * C::OROW + i * 16 + g * 2);
                                 x.x += y.x;
                                 x.y += y.y;
                             }
-                            *at = x;
+                            acc[i][j] = x.x;
+                            acc[i][2 + j] = x.y;
                         }
-            }
-            __syncthreads();
-        }
-        const bool whole = seg == 0 && item_ends;
-        const long long slot_out = blockIdx.x + bh * a.row_tiles + cur.rt;
-        for (int i = tid; i < nrows * (D / 4); i += kThreads) {
-            const int r = i / (D / 4), c = (i % (D / 4)) * 4, at = c % DT * 8 + c / DT * 2;
-            float top = s_stat[0][0][r];
-#pragma unroll
-            for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s_stat[w][0][r]);
-            float sum = 0.f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) sum += s_stat[w][1][r] * ex2(s_stat[w][0][r] - top);
-            const float inv = sum == 0.f ? 0.f : 1.f / sum;  // 0: the row sees no key; NaN stays
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int w = 0; w < C::BUFS; ++w) {
-                const float* x = reinterpret_cast<const float*>(smem + C::MERGE) + (w * ROWS + r) * C::OROW + at;
-                o.x += x[0];
-                o.y += x[1];
-                o.z += x[16];
-                o.w += x[17];
-            }
-            o.x *= inv;
-            o.y *= inv;
-            o.z *= inv;
-            o.w *= inv;
-            const float lse2 = sum == 0.f ? -INFINITY : top + lg2(sum);
-            if (whole) {
-                *reinterpret_cast<uint2*>(a.o + (row0 + r) * D + c) = make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
-                if (a.lse && c == 0) a.lse[row0 + r] = lse2 * kLn2;
+                    f[0] = f[1] = 1.f;
+                }
             } else {
-                *reinterpret_cast<float4*>(a.part_o + (slot_out * ROWS + r) * D + c) = o;
+                f[0] = ex2(M[0] - m[0]);
+                f[1] = ex2(M[1] - m[1]);
             }
-            if (c == 0) a.part_lse[slot_out * ROWS + r] = lse2;
+            if (kg == 0) {
+                const bool whole = seg == 0 && item_ends;
+                const long long slot_out = blockIdx.x + bh * a.row_tiles + cur.rt;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int r = rg * 8 + 2 * t + j;
+                    if (r >= nrows) continue;
+                    const float scale = l[j] == 0.f ? 0.f : f[j] / l[j];  // l = 0: the row sees no key; NaN stays
+                    const float lse2 = l[j] == 0.f ? -INFINITY : m[j] + lg2(l[j]);
+                    const long long row = bh * a.rows + cur.rt * ROWS + r;  // (b, head, token) flattened
+                    float o[DT];
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i) o[2 * i] = acc[i][j] * scale, o[2 * i + 1] = acc[i][2 + j] * scale;
+                    if (whole) {
+                        uint4* dst = reinterpret_cast<uint4*>(a.o + row * D + g * DT);
+#pragma unroll
+                        for (int i = 0; i < DT / 8; ++i)
+                            dst[i] = make_uint4(pack_bf16(o[8 * i], o[8 * i + 1]), pack_bf16(o[8 * i + 2], o[8 * i + 3]),
+                                                pack_bf16(o[8 * i + 4], o[8 * i + 5]), pack_bf16(o[8 * i + 6], o[8 * i + 7]));
+                        if (a.lse && g == 0) a.lse[row] = lse2 * kLn2;
+                    } else {
+                        float4* dst = reinterpret_cast<float4*>(a.part_o + (slot_out * ROWS + r) * D + g * DT);
+#pragma unroll
+                        for (int i = 0; i < DT / 4; ++i)
+                            dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                    }
+                    if (g == 0) a.part_lse[slot_out * ROWS + r] = lse2;
+                }
+            }
         }
-        __syncthreads();  // the buffers and Q are the next segment's
-    }
-    if (it + 1 < count) advance<STEP>(cur, a, cap);
+        if (it + 1 < count) advance(cur, a, cap);
     }
     cp_async_wait<0>();
     if (__any_sync(0xffffffffu, bad) && lane == 0) record_invalid(a.err, kSiteCacheTable, -1);
@@ -721,127 +658,136 @@ __device__ __forceinline__ float merge_lse(const float* pl, int stride, int segs
     return sum;
 }
 
-constexpr int kFinishThreads = 128, kWeightTokens = 4;  // tokens per thread of the weights
+constexpr int kFinishThreads = 128;
 
-// Blocks below `row_blocks`: one row each; LSE = M + log2 sum 2^(lse_s - M), O = sum 2^(lse_s - M) o_s / sum, the
-// segments dealt to groups of D / 4 threads.  A row without keys gets O = 0, LSE = -inf; a row whose item was one
-// segment is already written.
-// The others, with weights: 512 tokens of one (sequence, kv head) each; weights[j] += sum over the rows of
-// 2^(x_j - LSE), one thread per token, in a fixed order.
+// One block per row: LSE = M + log2 sum 2^(lse_s - M), O = sum 2^(lse_s - M) o_s / sum, the segments dealt to groups of
+// D / 4 threads.  A row without keys gets O = 0, LSE = -inf; a row whose item was one segment is already written.  (A
+// warp per row where there are few segments: one sequence of 777 tokens 12.3 us against 10.3.)
 template <int D, int ROWS>
-__global__ void __launch_bounds__(kFinishThreads) finish_fp8_kernel(const Params a, unsigned row_blocks, int weight_blocks) {
+__global__ void __launch_bounds__(kFinishThreads) finish_fp8_kernel(const Params a) {
     constexpr int LANES = D / 4, GROUPS = kFinishThreads / LANES, AHEAD = 4;
-    extern __shared__ float s_lse[];  // weights: LSE of the rows
     __shared__ float4 s_o[GROUPS][LANES];
     pdl_launch_dependents();
     pdl_wait();
     const int tid = threadIdx.x;
-    if (blockIdx.x < row_blocks) {
-        const long long row = blockIdx.x, bh = row / a.rows;
-        const int r = (int)(row - bh * a.rows), b = (int)(bh / a.Hkv), rt = r / ROWS;
-        long long slot = 0;
-        const int segs = find_segments(a, b, (int)(bh % a.Hkv) * a.row_tiles + rt, slot);
-        if (segs == 1) return;
-        const int grp = tid / LANES, col = tid % LANES;
-        const long long at = slot * ROWS + (r - rt * ROWS);
-        const float* pl = a.part_lse + at;
-        const float4* po = reinterpret_cast<const float4*>(a.part_o + at * D) + col;
-        float4 v[AHEAD];  // the first segments, loaded before the weights are known
-#pragma unroll
-        for (int i = 0; i < AHEAD; ++i)
-            if (grp + i * GROUPS < segs) v[i] = po[(long long)(grp + i * GROUPS) * ROWS * LANES];
-        float base;
-        const float sum = merge_lse(pl, ROWS, segs, base);
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int s0 = grp; s0 < segs; s0 += AHEAD * GROUPS) {
-#pragma unroll
-            for (int i = 0; i < AHEAD; ++i) {
-                const int s = s0 + i * GROUPS;
-                if (s < segs) {
-                    const float w = ex2(pl[(long long)s * ROWS] - base) * inv;
-                    o.x = fmaf(w, v[i].x, o.x);
-                    o.y = fmaf(w, v[i].y, o.y);
-                    o.z = fmaf(w, v[i].z, o.z);
-                    o.w = fmaf(w, v[i].w, o.w);
-                }
-                if (s + AHEAD * GROUPS < segs) v[i] = po[(long long)(s + AHEAD * GROUPS) * ROWS * LANES];
-            }
-        }
-        s_o[grp][col] = o;
-        __syncthreads();
-        if (grp == 0) {
-#pragma unroll
-            for (int i = 1; i < GROUPS; ++i) {
-                const float4 x = s_o[i][col];
-                o.x += x.x;
-                o.y += x.y;
-                o.z += x.z;
-                o.w += x.w;
-            }
-            *reinterpret_cast<uint2*>(a.o + row * D + col * 4) = make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
-            if (a.lse && col == 0) a.lse[row] = sum == 0.f ? -INFINITY : (base + lg2(sum)) * kLn2;
-        }
+    const long long row = blockIdx.x, bh = row / a.rows;
+    const int r = (int)(row - bh * a.rows), b = (int)(bh / a.Hkv), rt = r / ROWS;
+    long long slot = 0;
+    const int segs = find_segments(a, b, (int)(bh % a.Hkv) * a.row_tiles + rt, slot);
+    const long long at = slot * ROWS + (r - rt * ROWS);
+    const float* pl = a.part_lse + at;
+    if (segs == 1) {
+        if (a.weights && tid == 0) a.lse2[row] = pl[0];
         return;
     }
-    const unsigned idx = blockIdx.x - row_blocks;
-    const long long bh = idx / weight_blocks;
-    const int b = (int)(bh / a.Hkv), kvh = (int)(bh % a.Hkv), cap = a.max_pages * (int)a.page.d;
-    const int len = clamp_len(a.lens[b], cap), j0 = (int)(idx % weight_blocks) * kFinishThreads * kWeightTokens;
-    if (j0 >= len) return;
-    // the rows' LSEs, a tile at a time: kFinishThreads / ROWS lanes per row
-    constexpr int LPR = kFinishThreads / ROWS;
-    for (int rt = 0; rt < a.row_tiles; ++rt) {
-        long long slot = 0;
-        const int segs = find_segments(a, b, kvh * a.row_tiles + rt, slot);
-        const int r = tid / LPR;
-        const float* pl = a.part_lse + slot * ROWS + r;
-        const bool row = rt * ROWS + r < a.rows;
-        float M = -FLT_MAX, sum = 0.f;
-        for (int s = tid % LPR; row && s < segs; s += LPR) M = fmaxf(M, pl[(long long)s * ROWS]);
+    const int grp = tid / LANES, col = tid % LANES;
+    const float4* po = reinterpret_cast<const float4*>(a.part_o + at * D) + col;
+    float4 v[AHEAD];  // the first segments, loaded before the weights are known
 #pragma unroll
-        for (int w = LPR / 2; w >= 1; w >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
-        for (int s = tid % LPR; row && s < segs; s += LPR) sum += ex2(pl[(long long)s * ROWS] - M);
+    for (int i = 0; i < AHEAD; ++i)
+        if (grp + i * GROUPS < segs) v[i] = po[(long long)(grp + i * GROUPS) * ROWS * LANES];
+    float base;
+    const float sum = merge_lse(pl, ROWS, segs, base);
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s0 = grp; s0 < segs; s0 += AHEAD * GROUPS) {
 #pragma unroll
-        for (int w = LPR / 2; w >= 1; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
-        if (row && tid % LPR == 0) s_lse[rt * ROWS + r] = sum == 0.f ? INFINITY : M + lg2(sum);  // no keys: 2^-inf = 0
+        for (int i = 0; i < AHEAD; ++i) {
+            const int s = s0 + i * GROUPS;
+            if (s < segs) {
+                const float w = ex2(pl[(long long)s * ROWS] - base) * inv;
+                o.x = fmaf(w, v[i].x, o.x);
+                o.y = fmaf(w, v[i].y, o.y);
+                o.z = fmaf(w, v[i].z, o.z);
+                o.w = fmaf(w, v[i].w, o.w);
+            }
+            if (s + AHEAD * GROUPS < segs) v[i] = po[(long long)(s + AHEAD * GROUPS) * ROWS * LANES];
+        }
     }
+    s_o[grp][col] = o;
     __syncthreads();
-    float sum[kWeightTokens], before[kWeightTokens];
-    float* w = a.weights + bh * cap + j0 + tid;
+    if (grp > 0) return;
 #pragma unroll
-    for (int i = 0; i < kWeightTokens; ++i) {
-        sum[i] = 0.f;
-        before[i] = j0 + tid + i * kFinishThreads < len ? w[i * kFinishThreads] : 0.f;
+    for (int i = 1; i < GROUPS; ++i) {
+        const float4 x = s_o[i][col];
+        o.x += x.x;
+        o.y += x.y;
+        o.z += x.z;
+        o.w += x.w;
     }
-    for (int rt = 0; rt < a.row_tiles; ++rt) {
-        const int nrows = min(ROWS, a.rows - rt * ROWS);
-        const float* sr = a.scores + scores_at<ROWS>(a, bh, rt, cap);
-        const float* z = s_lse + rt * ROWS;
+    *reinterpret_cast<uint2*>(a.o + row * D + col * 4) = make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
+    if (col == 0) {
+        const float lse2 = sum == 0.f ? -INFINITY : base + lg2(sum);
+        if (a.lse) a.lse[row] = lse2 * kLn2;
+        if (a.weights) a.lse2[row] = lse2;
+    }
+}
+
+// weights[j] += sum over the rows of 2^(x_j - LSE), in a fixed order.  A thread takes four pieces of 16 bytes of scores.
+// With 4, 8, 16 or 32 rows (VEC) a token's scores are 1, 2, 4 or 8 lanes' pieces; otherwise a thread takes whole tokens.
+constexpr int kWeightThreads = 256, kPieces = 4;
+
+template <int ROWS, bool VEC>
+__global__ void __launch_bounds__(kWeightThreads) weights_fp8_kernel(const Params a, int blocks) {
+    pdl_launch_dependents();
+    pdl_wait();
+    const long long bh = blockIdx.x / blocks;
+    const int cap = a.max_pages * (int)a.page.d, len = clamp_len(a.lens[bh / a.Hkv], cap), tid = threadIdx.x;
+    const int lanes = VEC ? a.rows / 4 : 1, per = kWeightThreads / lanes;  // lanes per token, tokens per piece of the block
+    const int first = (int)(blockIdx.x % blocks) * per * kPieces + tid / lanes;
+    float* weights = a.weights + bh * cap;
+    const float* lse2 = a.lse2 + bh * a.rows;
+    float sum[kPieces], before[kPieces];
+    if constexpr (VEC) {
+        const float* scores = a.scores + scores_at<ROWS>(a, bh, 0, cap) + tid % lanes * 4;
+        float4 x[kPieces];
 #pragma unroll
-        for (int i = 0; i < kWeightTokens; ++i) {
-            const int j = j0 + tid + i * kFinishThreads;
-            if (j >= len) continue;
-            const float* x = sr + (long long)j * nrows;
-            if ((nrows & 3) == 0) {
-                for (int r = 0; r < nrows; r += 4) {
-                    const float4 v = *reinterpret_cast<const float4*>(x + r);
-                    sum[i] += (ex2(v.x - z[r]) + ex2(v.y - z[r + 1])) + (ex2(v.z - z[r + 2]) + ex2(v.w - z[r + 3]));
+        for (int q = 0; q < kPieces; ++q) {
+            const int j = first + q * per;
+            if (j >= cap) continue;  // (behind the sequence's end: read, not used)
+            x[q] = *reinterpret_cast<const float4*>(scores + (long long)j * a.rows);
+            before[q] = weights[j];
+        }
+        float4 z = *reinterpret_cast<const float4*>(lse2 + tid % lanes * 4);
+        if (z.x == -INFINITY) z.x = INFINITY;  // a row without keys: every weight 2^-inf = 0
+        if (z.y == -INFINITY) z.y = INFINITY;
+        if (z.z == -INFINITY) z.z = INFINITY;
+        if (z.w == -INFINITY) z.w = INFINITY;
+#pragma unroll
+        for (int q = 0; q < kPieces; ++q) {
+            sum[q] = (ex2(x[q].x - z.x) + ex2(x[q].y - z.y)) + (ex2(x[q].z - z.z) + ex2(x[q].w - z.w));
+            for (int w = lanes / 2; w >= 1; w >>= 1) sum[q] += __shfl_xor_sync(0xffffffffu, sum[q], w);
+        }
+    } else {
+#pragma unroll
+        for (int q = 0; q < kPieces; ++q) {
+            sum[q] = 0.f;
+            before[q] = first + q * per < len ? weights[first + q * per] : 0.f;
+        }
+        for (int rt = 0; rt < a.row_tiles; ++rt) {
+            const int nrows = min(ROWS, a.rows - rt * ROWS);
+            const float* scores = a.scores + scores_at<ROWS>(a, bh, rt, cap);
+            for (int r = 0; r < nrows; ++r) {
+                const float l = lse2[rt * ROWS + r], z = l == -INFINITY ? INFINITY : l;
+#pragma unroll
+                for (int q = 0; q < kPieces; ++q) {
+                    const int j = first + q * per;
+                    if (j < len) sum[q] += ex2(scores[(long long)j * nrows + r] - z);
                 }
-            } else {
-                for (int r = 0; r < nrows; ++r) sum[i] += ex2(x[r] - z[r]);
             }
         }
     }
 #pragma unroll
-    for (int i = 0; i < kWeightTokens; ++i)
-        if (j0 + tid + i * kFinishThreads < len) w[i * kFinishThreads] = before[i] + sum[i];
+    for (int q = 0; q < kPieces; ++q) {
+        const int j = first + q * per;
+        if (j < len && tid % lanes == 0) weights[j] = before[q] + sum[q];
+    }
 }
 
-template <int D, int NB>
+template <int D, int RG>
 cudaError_t launch_d(const PagedDecodeFp8Launch& a, cudaStream_t s) {
-    using C = Cfg<D, NB>;
-    cudaError_t e = set_smem_limit_once<decode_fp8_kernel<D, NB>>(C::SMEM);
+    using C = Cfg<D, RG>;
+    cudaError_t e = set_smem_limit_once<decode_fp8_kernel<D, RG>>(C::SMEM);
     if (e != cudaSuccess) return e;
     Params p;
     p.q = (const __nv_bfloat16*)a.q;
@@ -858,6 +804,7 @@ cudaError_t launch_d(const PagedDecodeFp8Launch& a, cudaStream_t s) {
     p.part_lse = a.part_lse;
     p.scores = a.weights ? a.scores : nullptr;
     p.prefix = a.prefix;
+    p.lse2 = a.lse2;
     p.B = a.B;
     p.Hq = a.Hq;
     p.Hkv = a.Hkv;
@@ -874,23 +821,27 @@ cudaError_t launch_d(const PagedDecodeFp8Launch& a, cudaStream_t s) {
     const int cap = a.max_pages * a.page;
     const long long bh = (long long)a.B * a.Hkv;
     // no more CTAs than steps at full lengths
-    p.workers = (int)std::min<long long>(a.workers, bh * p.row_tiles * ((cap + C::STEP - 1) / C::STEP));
-    e = launch_dependent(decode_fp8_kernel<D, NB>, dim3(p.workers), dim3(kThreads), C::SMEM, s, p);
+    p.workers = (int)std::min<long long>(a.workers, bh * p.row_tiles * ((cap + kStep - 1) / kStep));
+    e = launch_dependent(decode_fp8_kernel<D, RG>, dim3(p.workers), dim3(kThreads), C::SMEM, s, p);
     if (e != cudaSuccess) return e;
-    constexpr int per_block = kFinishThreads * kWeightTokens;
-    const int weight_blocks = a.weights ? (cap + per_block - 1) / per_block : 0;
-    const long long row_blocks = bh * p.rows, blocks = row_blocks + bh * weight_blocks;
-    if (blocks > 0x7FFFFFFFll) return cudaErrorInvalidValue;
-    return launch_dependent(finish_fp8_kernel<D, C::ROWS>, dim3((unsigned)blocks), dim3(kFinishThreads),
-                            a.weights ? (size_t)p.rows * 4 : 0, s, p, (unsigned)row_blocks, weight_blocks);
+    const long long row_blocks = bh * p.rows;
+    if (row_blocks > 0x7FFFFFFFll) return cudaErrorInvalidValue;
+    e = launch_dependent(finish_fp8_kernel<D, C::ROWS>, dim3((unsigned)row_blocks), dim3(kFinishThreads), 0, s, p);
+    if (e != cudaSuccess || !a.weights) return e;
+    const bool vec = p.rows == 4 || p.rows == 8 || p.rows == 16 || p.rows == 32;
+    const int tokens = kWeightThreads * kPieces / (vec ? p.rows / 4 : 1), blocks = (cap + tokens - 1) / tokens;
+    if (bh * blocks > 0x7FFFFFFFll) return cudaErrorInvalidValue;
+    const dim3 grid((unsigned)(bh * blocks)), block(kWeightThreads);
+    return vec ? launch_dependent(weights_fp8_kernel<C::ROWS, true>, grid, block, 0, s, p, blocks)
+               : launch_dependent(weights_fp8_kernel<C::ROWS, false>, grid, block, 0, s, p, blocks);
 }
 
-template <int D, int NB>
+template <int D, int RG>
 cudaError_t blocks_per_sm(int* blocks) {
-    using C = Cfg<D, NB>;
-    const cudaError_t e = set_smem_limit_once<decode_fp8_kernel<D, NB>>(C::SMEM);
+    using C = Cfg<D, RG>;
+    const cudaError_t e = set_smem_limit_once<decode_fp8_kernel<D, RG>>(C::SMEM);
     if (e != cudaSuccess) return e;
-    const cudaError_t f = cudaOccupancyMaxActiveBlocksPerMultiprocessor(blocks, decode_fp8_kernel<D, NB>, kThreads, C::SMEM);
+    const cudaError_t f = cudaOccupancyMaxActiveBlocksPerMultiprocessor(blocks, decode_fp8_kernel<D, RG>, kThreads, C::SMEM);
     *blocks = std::min(*blocks, C::CTAS);
     return f;
 }

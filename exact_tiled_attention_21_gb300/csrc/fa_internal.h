@@ -219,6 +219,7 @@ struct PagedDecodeFp8Launch {
     float* part_lse;       // fp32 [workers + items, tile rows]
     float* scores;         // fp32 [B*Hkv, rows padded to 4, max_pages * page] in all (log2 units), with weights only
     long long* prefix;     // [B + 1]
+    float* lse2;           // fp32 [B*Hq*Nq], with weights only
     int B, Hq, Hkv, Nq, page, sb, max_pages, num_pages, d;
     int workers;           // CTAs to share the steps among
     float scale;
