@@ -13,17 +13,26 @@ namespace fa {
 
 // cos and sin of a fraction of a turn, times mag: the nearest quarter turn
 // comes off in integers, which leaves an angle of at most pi / 4 exactly (to
-// 2^-32 turn), where the Taylor polynomials to x^9 and x^10 are within 2^-29.
-// Each result is within 2^-22; the hardware's sine and cosine (2^-20.5) flip
-// enough bf16 roundings to show in the cache's bytes.
+// 2^-32 turn), held in two floats; the Taylor polynomials to x^9 and x^10 are
+// within 2^-29 there, and the large terms are added last, with what their
+// rounding left, so that 19 of 20 results are the correctly rounded ones and
+// all are within 2^-23.9.  The hardware's sine and cosine (2^-20.5), and sums
+// of 2^-23, flip enough bf16 roundings to show in the cache's bytes.
 __device__ __forceinline__ void turn_cos_sin(int pos, uint64_t turns, float mag, float& c, float& s) {
     const uint32_t t = (uint32_t)(((uint64_t)(int64_t)pos * turns) >> 32);
     const uint32_t q = (t + 0x20000000u) >> 30;
-    const float a = (float)(int32_t)(t - (q << 30)) * 1.4629180792671596e-09f;  // 2 pi / 2^32
-    const float z = a * a;
-    const float sn = fmaf(a * z, fmaf(z, fmaf(z, fmaf(z, 1.f / 362880.f, -1.f / 5040.f), 1.f / 120.f), -1.f / 6.f), a);
-    const float cs = fmaf(z, fmaf(z, fmaf(z, fmaf(z, fmaf(z, -1.f / 3628800.f, 1.f / 40320.f), -1.f / 720.f), 1.f / 24.f),
-                                  -0.5f), 1.f);
+    const int r = (int)(t - (q << 30));                      // |r| <= 2^29
+    constexpr float kHi = 1.4629180792671596e-09f;           // 2 pi / 2^32 as two floats
+    constexpr float kLo = (float)(1.4629180792671596e-09 - (double)kHi);
+    const float rh = (float)(r & ~0xFF), rl = (float)(r & 0xFF);  // both exact
+    const float a = rh * kHi;
+    const float lo = fmaf(rl, kHi, fmaf(rh, kLo, fmaf(rh, kHi, -a)));
+    const float z = a * a, ze = fmaf(a, a, -z), hz = 0.5f * z;
+    const float ps = fmaf(z, fmaf(z, fmaf(z, 1.f / 362880.f, -1.f / 5040.f), 1.f / 120.f), -1.f / 6.f);
+    const float pc = fmaf(z, fmaf(z, fmaf(z, -1.f / 3628800.f, 1.f / 40320.f), -1.f / 720.f), 1.f / 24.f);
+    const float sn = a + fmaf(a * z, ps, fmaf(lo, -hz, lo));                   // sin a + lo cos a
+    const float one = 1.f - hz, left = (1.f - one) - hz;
+    const float cs = one + (left + fmaf(z * z, pc, fmaf(-0.5f, ze, -(lo * a))));  // cos a - lo sin a
     c = __uint_as_float(__float_as_uint((q & 1) ? sn : cs) ^ (((q + 1) & 2) << 30)) * mag;
     s = __uint_as_float(__float_as_uint((q & 1) ? cs : sn) ^ ((q & 2) << 30)) * mag;
 }

@@ -338,7 +338,7 @@ int fa_rope_table(const double *inv_freq, int n, uint64_t *turns);
  * columns from rot on are copied.  inverse = 1 turns by -a with the same
  * magnitude: the transpose, i.e. the gradient of x from the gradient of y.  The
  * angle is reduced exactly at any position (see fa_rope_table); cos and sin are
- * within 2^-22; computed in fp32, rounded to bf16 once.  rot: a multiple of 16
+ * within 2^-23; computed in fp32, rounded to bf16 once.  rot: a multiple of 16
  * (FA_ERR_UNSUPPORTED), 16 <= rot <= d; turns: device [rot / 2], 16-byte
  * aligned; magnitude finite.  B * N <= 2^31 - 1, B * H <= 2^24. */
 int fa_rope(const void *x, void *y, long long x_sb, long long x_sh, long long x_sn, long long y_sb,
