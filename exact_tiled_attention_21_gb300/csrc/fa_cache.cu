@@ -289,12 +289,13 @@ __global__ void __launch_bounds__(kSelThreads, PER > 8 ? 1 : 2) evict_select_ker
     const int per_warp = ((n + ctas * kSelWarps - 1) / (ctas * kSelWarps) + 31) / 32 * 32;
     const int first = (rank * kSelWarps + warp) * per_warp + lane, rounds = per_warp / 32;
     const int cand = n - a.recent;  // candidates [0, cand): `left` of them stay
-    uint32_t keys[PER ? PER : 1] = {};
+    float held[PER ? PER : 1] = {};  // loaded all at once, from clamped places
     if constexpr (PER > 0) {
 #pragma unroll
-        for (int i = 0; i < PER; ++i) keys[i] = i < rounds && first + i * 32 < cand ? order_key(w[first + i * 32]) : 0;
+        for (int i = 0; i < PER; ++i) held[i] = w[min(first + i * 32, n - 1)];
     }
-    auto key_of = [&](int i) { return PER ? keys[PER ? i : 0] : order_key(w[first + i * 32]); };
+    auto weight = [&](int i) { return PER ? held[PER ? i : 0] : w[first + i * 32]; };
+    auto key_of = [&](int i) { return order_key(weight(i)); };
     uint32_t left = (uint32_t)(a.keep - a.recent), key = 0, known = 0;  // key's bits under the mask `known` are settled
     for (int i = tid; i < 2 * kSelBins; i += kSelThreads) s_hist[0][i] = 0;
     __syncthreads();
@@ -393,7 +394,7 @@ __global__ void __launch_bounds__(kSelThreads, PER > 8 ? 1 : 2) evict_select_ker
             if (up || (eq && re < left)) {
                 const uint32_t at = ra + min(re, left);
                 kept[at] = j;
-                nw[at] = w[j];
+                nw[at] = weight(i);
             }
             ba += __popc(ma);
             be += __popc(me);
