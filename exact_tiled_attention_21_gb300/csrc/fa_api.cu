@@ -934,6 +934,10 @@ int fa_decode_paged_fp8(const void* q, const void* k_pages, const void* v_pages,
     if (st != FA_OK) return st;
     if (Hq % Hkv) return FA_ERR_INVALID_ARG;
     if (Nq > 16 || (long long)B * Hq > (1ll << 24)) return FA_ERR_UNSUPPORTED;
+    // steps of 128 tokens over all sequences, kv heads and row tiles are counted in 32 bits per CTA
+    const int rows = Hq / Hkv * Nq, tile = fp8_tile_rows(rows);
+    if ((long long)B * Hkv * ((rows + tile - 1) / tile) > (1ll << 31) / (((long long)max_pages * page_size + 127) / 128))
+        return FA_ERR_UNSUPPORTED;
     if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(o) || !aligned4(k_scale) ||
         !aligned4(v_scale) || !aligned4(block_table) || !aligned4(seq_lens) || !aligned4(lse) || !aligned4(weights))
         return FA_ERR_ALIGNMENT;
@@ -941,7 +945,7 @@ int fa_decode_paged_fp8(const void* q, const void* k_pages, const void* v_pages,
     int num_sms = 0;
     st = device_state(&a.err, &num_sms);
     if (st != FA_OK) return st;
-    st = fp8_workers(d, fp8_tile_rows(Hq / Hkv * Nq), num_sms, &a.workers);
+    st = fp8_workers(d, tile, num_sms, &a.workers);
     if (st != FA_OK) return st;
     const Fp8Workspace ws = fp8_workspace(B, Hq, Hkv, Nq, d, (long long)max_pages * page_size, weights != nullptr);
     if (!workspace || workspace_bytes < ws.bytes) return FA_ERR_WORKSPACE;

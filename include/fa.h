@@ -387,7 +387,10 @@ size_t fa_decode_paged_fp8_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d
  * as they are.
  * The tokens of all sequences are dealt out evenly, by their lengths, to the
  * CTAs that run at once, so there is no number of splits to choose.  Results do
- * not depend on the run (fixed order of additions).  Tokens past
+ * not depend on the run (fixed order of additions), but for rounding on the
+ * batch that a sequence is in.  Steps of 128 tokens over all sequences at full
+ * capacity, kv heads and tiles of 32 query rows must stay within 2^31
+ * (FA_ERR_UNSUPPORTED).  Tokens past
  * seq_lens[b] are never used.  A NaN in V reaches every query of its sequence and
  * kv head, also those of the Nq that do not see its token.  workspace: 16-byte
  * aligned, at least fa_decode_paged_fp8_workspace_bytes(...); contents do not

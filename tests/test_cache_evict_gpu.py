@@ -49,6 +49,9 @@ CASES = [
     (2, 48, 24, [2500, 2049], 1, 0, 64),
     (1, 33, 11, [1025], 1024, 1, 64),                # one token goes
     (2, 256, 64, [5000], 700, 77, 128),
+    (8, 64, 32, [5000, 4000, 1, 3000, 80, 0, 64, 2500, 5000, 700], 70, 10, 64),  # one CTA per kv head, many tokens each
+    (1, 256, 128, [140000], 90, 5, 64),              # more tokens than a cluster's registers hold
+    (2, 128, 128, [40000, 39999], 300, 300, 64),     # a cluster of eight, recent ones only
 ]
 
 

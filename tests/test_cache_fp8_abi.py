@@ -121,7 +121,7 @@ def _decode(lib, p=(16,) * 8, lse=16, w=0, B=1, Hq=4, Hkv=2, Nq=1, page=16, sb=8
 
 @pytest.mark.parametrize("bad,status", CACHE_BAD + [
     (dict(Hq=3), fa.FA_ERR_INVALID_ARG), (dict(Hq=0), fa.FA_ERR_INVALID_ARG), (dict(Nq=0), fa.FA_ERR_INVALID_ARG),
-    (dict(Nq=17), fa.FA_ERR_UNSUPPORTED), (dict(scale=0.0), fa.FA_ERR_INVALID_ARG), (dict(scale=NAN), fa.FA_ERR_INVALID_ARG),
+    (dict(Nq=17), fa.FA_ERR_UNSUPPORTED), (dict(B=1 << 10, Hkv=4, mp=1 << 26), fa.FA_ERR_UNSUPPORTED), (dict(scale=0.0), fa.FA_ERR_INVALID_ARG), (dict(scale=NAN), fa.FA_ERR_INVALID_ARG),
     (dict(lse=6), fa.FA_ERR_ALIGNMENT), (dict(w=2), fa.FA_ERR_ALIGNMENT),
 ])
 def test_decode_refusals(lib, bad, status):

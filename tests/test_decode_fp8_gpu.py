@@ -143,6 +143,20 @@ def test_decode_scale_ranges(cuda_lib):
     _ok(cuda_lib)
 
 
+def test_decode_wide_table(cuda_lib):
+    """A block table of far more pages than any sequence uses: the work goes by the lengths, and the result is that of
+    a narrow one, bit for bit."""
+    lens = [300, 0, 129]
+    q, c, table = _case(35, 3, 8, 2, 1, 16, 8, lens, 128)
+    g = to_gpu(c)
+    wide = np.full((3, 5000), -7, dtype=np.int32)
+    wide[:, :table.shape[1]] = table
+    a = cuda_lib.decode_paged_fp8(q.to(DEV), *args(g), ints(table), ints(lens))
+    b = cuda_lib.decode_paged_fp8(q.to(DEV), *args(g), ints(wide), ints(lens))
+    _ok(cuda_lib)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
 def test_decode_nan_shows(cuda_lib):
     """A NaN in a visible key or value, or in q, reaches its row's output."""
     q, c, table = _case(41, 1, 4, 2, 1, 16, 16, [50], 64)
