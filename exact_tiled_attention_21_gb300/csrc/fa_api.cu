@@ -862,7 +862,6 @@ int fa_rope(const void* x, void* y, long long x_sb, long long x_sh, long long x_
     a.rot = rot;
     a.interleaved = interleaved;
     a.inverse = inverse;
-    a.hpt = 1;
     a.magnitude = magnitude;
     return launched(launch_rope(a, (cudaStream_t)stream));
 }
@@ -877,7 +876,7 @@ int fa_cache_append_fp8(const void* k, const void* v, long long k_sb, long long 
     int st = check_cache(B, Hkv, page_size, scale_block, max_pages, num_pages, d);
     if (st != FA_OK) return st;
     if (turns && (st = check_rotation(d, rot, interleaved, magnitude)) != FA_OK) return st;
-    if (N > kMaxCacheTokens || (long long)B * N > 0x7FFFFFFFll) return FA_ERR_UNSUPPORTED;
+    if (N > kMaxCacheTokens || (long long)B * Hkv * N > 0x7FFFFFFFll) return FA_ERR_UNSUPPORTED;
     if (!aligned16(k) || !aligned16(v) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(turns) ||
         !aligned4(k_scale) || !aligned4(v_scale) || !aligned4(block_table) || !aligned4(seq_lens) ||
         !aligned4(new_lens) || !aligned4(positions))
@@ -936,11 +935,12 @@ int fa_decode_paged_fp8(const void* q, const void* k_pages, const void* v_pages,
     if (Nq > 16 || (long long)B * Hq > (1ll << 24)) return FA_ERR_UNSUPPORTED;
     // steps of 128 tokens over all sequences, kv heads and row tiles are counted in 32 bits per CTA
     const int rows = Hq / Hkv * Nq, tile = fp8_tile_rows(rows);
-    if ((long long)B * Hkv * ((rows + tile - 1) / tile) > (1ll << 31) / (((long long)max_pages * page_size + 127) / 128))
+    if ((long long)B * Hkv * ((rows + tile - 1) / tile) > 0x7FFFFFFFll / (((long long)max_pages * page_size + 127) / 128))
         return FA_ERR_UNSUPPORTED;
     if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(o) || !aligned4(k_scale) ||
         !aligned4(v_scale) || !aligned4(block_table) || !aligned4(seq_lens) || !aligned4(lse) || !aligned4(weights))
         return FA_ERR_ALIGNMENT;
+    if (o == q) return FA_ERR_INVALID_ARG;  // other CTAs may still read the row that one writes
     PagedDecodeFp8Launch a;
     int num_sms = 0;
     st = device_state(&a.err, &num_sms);
@@ -995,6 +995,7 @@ int fa_cache_evict_fp8(void* k_pages, void* v_pages, float* k_scale, float* v_sc
         !aligned4(block_table) || !aligned4(seq_lens) || !aligned4(weights) || !aligned4(new_table) ||
         !aligned4(new_lens) || !aligned4(new_weights) || !aligned4(kept))
         return FA_ERR_ALIGNMENT;
+    if (new_lens == seq_lens || new_weights == weights) return FA_ERR_INVALID_ARG;  // read while the other is written
     CacheEvictLaunch a;
     st = device_state(&a.err, &a.num_sms);
     if (st != FA_OK) return st;

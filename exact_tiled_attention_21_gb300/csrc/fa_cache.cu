@@ -196,7 +196,6 @@ cudaError_t launch_append_dti(const CacheAppendLaunch& a, cudaStream_t s) {
     while (plan.heads > 1 && cells * ((a.Hkv + plan.heads - 1) / plan.heads) < 4ll * a.num_sms) plan.heads /= 2;
     plan.groups = (a.Hkv + plan.heads - 1) / plan.heads;
     const long long ctas = cells * plan.groups;
-    if (ctas > 0x7FFFFFFFll) return cudaErrorInvalidValue;
     const int smem = a.turns ? a.sb * (a.rot / 2) * 8 : 0;  // at most 64 KB
     cudaError_t e = set_smem_limit_once<cache_append_kernel<D, TPT, INTER>>(64 * 1024);
     if (e != cudaSuccess) return e;
@@ -547,7 +546,6 @@ cudaError_t launch_cache_evict(const CacheEvictLaunch& a, cudaStream_t s) {
     const long long bh = (long long)a.B * a.Hkv, cap = (long long)a.max_pages * a.page;
     int ctas = 1;
     while (ctas < 8 && cap >= 4096ll * ctas && bh * ctas * 2 <= a.num_sms) ctas *= 2;
-    if (bh * ctas > 0x7FFFFFFFll) return cudaErrorInvalidValue;
     const long long per = (cap + (long long)ctas * kSelThreads - 1) / ((long long)ctas * kSelThreads);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(bh * ctas));

@@ -734,7 +734,8 @@ __global__ void __launch_bounds__(kWeightThreads) weights_fp8_kernel(const Param
     const long long bh = blockIdx.x / blocks;
     const int cap = a.max_pages * (int)a.page.d, len = clamp_len(a.lens[bh / a.Hkv], cap), tid = threadIdx.x;
     const int lanes = VEC ? a.rows / 4 : 1, per = kWeightThreads / lanes;  // lanes per token, tokens per piece of the block
-    const int first = (int)(blockIdx.x % blocks) * per * kPieces + tid / lanes;
+    const int begin = (int)(blockIdx.x % blocks) * per * kPieces, first = begin + tid / lanes;
+    if (begin >= len) return;
     float* weights = a.weights + bh * cap;
     const float* lse2 = a.lse2 + bh * a.rows;
     float sum[kPieces], before[kPieces];
@@ -825,12 +826,10 @@ cudaError_t launch_d(const PagedDecodeFp8Launch& a, cudaStream_t s) {
     e = launch_dependent(decode_fp8_kernel<D, RG>, dim3(p.workers), dim3(kThreads), C::SMEM, s, p);
     if (e != cudaSuccess) return e;
     const long long row_blocks = bh * p.rows;
-    if (row_blocks > 0x7FFFFFFFll) return cudaErrorInvalidValue;
     e = launch_dependent(finish_fp8_kernel<D, C::ROWS>, dim3((unsigned)row_blocks), dim3(kFinishThreads), 0, s, p);
     if (e != cudaSuccess || !a.weights) return e;
     const bool vec = p.rows == 4 || p.rows == 8 || p.rows == 16 || p.rows == 32;
     const int tokens = kWeightThreads * kPieces / (vec ? p.rows / 4 : 1), blocks = (cap + tokens - 1) / tokens;
-    if (bh * blocks > 0x7FFFFFFFll) return cudaErrorInvalidValue;
     const dim3 grid((unsigned)(bh * blocks)), block(kWeightThreads);
     return vec ? launch_dependent(weights_fp8_kernel<C::ROWS, true>, grid, block, 0, s, p, blocks)
                : launch_dependent(weights_fp8_kernel<C::ROWS, false>, grid, block, 0, s, p, blocks);

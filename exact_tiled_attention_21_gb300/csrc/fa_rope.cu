@@ -60,7 +60,6 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeLaunch a) 
 
 cudaError_t launch_rope(RopeLaunch a, cudaStream_t s) {
     const long long blocks = (a.tokens * (a.d / 16) + kRopeThreads - 1) / kRopeThreads;
-    if (blocks > 0x7FFFFFFFll) return cudaErrorInvalidValue;
     // heads per thread: up to four share the sines while every SM still has four CTAs (8192 tokens of 32 heads: 1 head
     // 48.9 us, 2 31.6, 4 25.1, 8 26.2, 16 26.3)
     a.hpt = 4;

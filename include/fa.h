@@ -349,7 +349,8 @@ int fa_rope(const void *x, void *y, long long x_sb, long long x_sh, long long x_
  * fa_rope's x.  Sequence b has seq_lens[b] tokens in the cache and gets its
  * first n_b = new_lens[b] (0..N; NULL: N) tokens at seq_lens[b], seq_lens[b] + 1,
  * ...; tokens that would not fit max_pages * page_size are left out and
- * recorded.  seq_lens is not changed.  If turns is not NULL, K is rotated first
+ * recorded.  seq_lens is not changed.  B * Hkv * N <= 2^31 - 1
+ * (FA_ERR_UNSUPPORTED).  If turns is not NULL, K is rotated first
  * as by fa_rope (same arguments; positions NULL: seq_lens[b] + i) and rounded
  * to bf16: the result is, bit for bit, that of fa_rope followed by this call
  * without turns.  With turns NULL, rot, interleaved, magnitude and positions
@@ -389,12 +390,13 @@ size_t fa_decode_paged_fp8_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d
  * CTAs that run at once, so there is no number of splits to choose.  Results do
  * not depend on the run (fixed order of additions), but for rounding on the
  * batch that a sequence is in.  Steps of 128 tokens over all sequences at full
- * capacity, kv heads and tiles of 32 query rows must stay within 2^31
- * (FA_ERR_UNSUPPORTED).  Tokens past
- * seq_lens[b] are never used.  A NaN in V reaches every query of its sequence and
- * kv head, also those of the Nq that do not see its token.  workspace: 16-byte
- * aligned, at least fa_decode_paged_fp8_workspace_bytes(...); contents do not
- * matter; calls that may overlap need one each. */
+ * capacity, kv heads and tiles of 32 query rows must stay below 2^31
+ * (FA_ERR_UNSUPPORTED).  Tokens past seq_lens[b] are never used.  A NaN in V
+ * reaches every query of its sequence and kv head, also those of the Nq that do
+ * not see its token.  No output may overlap an input or the cache (o = q:
+ * FA_ERR_INVALID_ARG).  workspace: 16-byte aligned, at least
+ * fa_decode_paged_fp8_workspace_bytes(...); contents do not matter; calls that
+ * may overlap need one each. */
 int fa_decode_paged_fp8(const void *q, const void *k_pages, const void *v_pages, const float *k_scale,
                         const float *v_scale, const int *block_table, const int *seq_lens, void *o, float *lse,
                         float *weights, int B, int Hq, int Hkv, int Nq, int page_size, int scale_block,
@@ -413,8 +415,10 @@ int fa_decode_paged_fp8(const void *q, const void *k_pages, const void *v_pages,
  * scale is the largest of its tokens' source scales; tokens of smaller scale
  * are rescaled to it.  Outputs: new_lens int32 [B]; kept int32 and new_weights
  * fp32 [B, Hkv, new_max_pages * page_size]: the source index of each kept token
- * and its weight, then -1 and 0 (so new_weights goes on accumulating).  Rotation
- * stays as it was applied: later tokens go on with their own positions. */
+ * and its weight, then -1 and 0 (so new_weights goes on accumulating).  No
+ * output may overlap an input (new_lens = seq_lens or new_weights = weights:
+ * FA_ERR_INVALID_ARG).  Rotation stays as it was applied: later tokens go on with
+ * their own positions. */
 int fa_cache_evict_fp8(void *k_pages, void *v_pages, float *k_scale, float *v_scale, const int *block_table,
                        const int *seq_lens, const float *weights, const int *new_table, int *new_lens,
                        float *new_weights, int *kept, int B, int Hkv, int page_size, int scale_block,

@@ -95,6 +95,7 @@ def _append(lib, p=(16,) * 8, extra=(0, 0, 0), ks=(0, 0, 64), vs=(0, 0, 64), B=1
 
 @pytest.mark.parametrize("bad,status", CACHE_BAD + [
     (dict(N=0), fa.FA_ERR_INVALID_ARG), (dict(N=(1 << 30) + 1), fa.FA_ERR_UNSUPPORTED),
+    (dict(N=1 << 30), fa.FA_ERR_UNSUPPORTED),
     (dict(ks=(0, 0, 4)), fa.FA_ERR_ALIGNMENT), (dict(vs=(0, -8, 64)), fa.FA_ERR_INVALID_ARG),
     (dict(extra=(0, 0, 16), rot=20), fa.FA_ERR_UNSUPPORTED), (dict(extra=(0, 0, 16), rot=80), fa.FA_ERR_INVALID_ARG),
     (dict(extra=(0, 0, 16), mag=NAN), fa.FA_ERR_INVALID_ARG), (dict(extra=(0, 0, 8)), fa.FA_ERR_ALIGNMENT),
@@ -113,7 +114,7 @@ def test_append_pointer_checks(lib):
         assert _append(lib, p=p) == fa.FA_ERR_ALIGNMENT, i
 
 
-def _decode(lib, p=(16,) * 8, lse=16, w=0, B=1, Hq=4, Hkv=2, Nq=1, page=16, sb=8, mp=4, np=9, d=64, scale=0.125,
+def _decode(lib, p=(16,) * 7 + (32,), lse=16, w=0, B=1, Hq=4, Hkv=2, Nq=1, page=16, sb=8, mp=4, np=9, d=64, scale=0.125,
             ws=16, nbytes=1 << 30):
     return lib.fa_decode_paged_fp8(*map(vp, p), vp(lse), vp(w), B, Hq, Hkv, Nq, page, sb, mp, np, d, scale,
                                    vp(ws), nbytes, None)
@@ -121,7 +122,9 @@ def _decode(lib, p=(16,) * 8, lse=16, w=0, B=1, Hq=4, Hkv=2, Nq=1, page=16, sb=8
 
 @pytest.mark.parametrize("bad,status", CACHE_BAD + [
     (dict(Hq=3), fa.FA_ERR_INVALID_ARG), (dict(Hq=0), fa.FA_ERR_INVALID_ARG), (dict(Nq=0), fa.FA_ERR_INVALID_ARG),
-    (dict(Nq=17), fa.FA_ERR_UNSUPPORTED), (dict(B=1 << 10, Hkv=4, mp=1 << 26), fa.FA_ERR_UNSUPPORTED), (dict(scale=0.0), fa.FA_ERR_INVALID_ARG), (dict(scale=NAN), fa.FA_ERR_INVALID_ARG),
+    (dict(Nq=17), fa.FA_ERR_UNSUPPORTED), (dict(B=1 << 10, Hkv=4, mp=1 << 26), fa.FA_ERR_UNSUPPORTED),
+    (dict(B=1 << 7, Hkv=2, mp=1 << 26), fa.FA_ERR_UNSUPPORTED), (dict(p=(16,) * 8), fa.FA_ERR_INVALID_ARG),
+    (dict(scale=0.0), fa.FA_ERR_INVALID_ARG), (dict(scale=NAN), fa.FA_ERR_INVALID_ARG),
     (dict(lse=6), fa.FA_ERR_ALIGNMENT), (dict(w=2), fa.FA_ERR_ALIGNMENT),
 ])
 def test_decode_refusals(lib, bad, status):
@@ -150,7 +153,7 @@ def test_decode_workspace_query():
         assert q(*bad) == 0, bad
 
 
-def _evict(lib, p=(16,) * 11, B=1, Hkv=2, page=16, sb=8, mp=4, nmp=2, np=9, d=64, keep=20, recent=4):
+def _evict(lib, p=(16,) * 8 + (32,) * 3, B=1, Hkv=2, page=16, sb=8, mp=4, nmp=2, np=9, d=64, keep=20, recent=4):
     return lib.fa_cache_evict_fp8(*map(vp, p), B, Hkv, page, sb, mp, nmp, np, d, keep, recent, None)
 
 
@@ -158,6 +161,7 @@ def _evict(lib, p=(16,) * 11, B=1, Hkv=2, page=16, sb=8, mp=4, nmp=2, np=9, d=64
     (dict(keep=0), fa.FA_ERR_INVALID_ARG), (dict(keep=33), fa.FA_ERR_INVALID_ARG), (dict(recent=-1), fa.FA_ERR_INVALID_ARG),
     (dict(recent=21), fa.FA_ERR_INVALID_ARG), (dict(nmp=0), fa.FA_ERR_INVALID_ARG),
     (dict(nmp=1 << 27), fa.FA_ERR_UNSUPPORTED),
+    (dict(p=(16,) * 9 + (32,) * 2), fa.FA_ERR_INVALID_ARG), (dict(p=(16,) * 8 + (32,) + (16,) + (32,)), fa.FA_ERR_INVALID_ARG),
 ])
 def test_evict_refusals(lib, bad, status):
     assert _evict(lib, **bad) == status
