@@ -190,7 +190,8 @@ cudaError_t launch_append_dti(const CacheAppendLaunch& a, cudaStream_t s) {
     plan.blocks = (a.N + a.sb - 2) / a.sb + 1;
     plan.page = FastDiv((uint32_t)a.page);
     plan.sb = FastDiv((uint32_t)a.sb);
-    // heads per CTA: up to eight share the sines while there are four CTAs for every SM
+    // heads per CTA: up to eight share the sines while there are four CTAs for every SM (8 ragged prompts of up to 2048 tokens, 8
+    // heads: 1 head 37.3 us, 2 28.8, 4 28.1, 8 28.0; 32 single tokens of 8 heads: 8.9 us with 8, 6.2 with 1)
     plan.heads = 8;
     const long long cells = (long long)a.B * plan.blocks;
     while (plan.heads > 1 && cells * ((a.Hkv + plan.heads - 1) / plan.heads) < 4ll * a.num_sms) plan.heads /= 2;
@@ -405,7 +406,7 @@ __global__ void __launch_bounds__(kSelThreads, PER > 8 ? 1 : 2) evict_select_ker
 // block's scale is the largest of its tokens' source scales; tokens that came with that scale are copied byte for byte.
 // Reading a token takes three loads that depend on each other (its index, its page, its row), so the CTAs are resident
 // ones that run over the blocks with the index two blocks ahead and the page one block ahead of the row.
-constexpr int kMoveCtas = 4;  // per SM
+constexpr int kMoveCtas = 4;  // per SM (the eviction of 32 sequences of 4096 tokens, 8 heads: 3 CTAs 46.8 us, 4 44.9, 6 54.6)
 
 struct MovePlan {
     int blocks, step_bh, step_blk;  // blocks per (sequence, kv head); the grid's size as (sequence, kv head)s and blocks
@@ -542,7 +543,8 @@ cudaError_t launch_cache_append(const CacheAppendLaunch& a, cudaStream_t s) {
 }
 
 cudaError_t launch_cache_evict(const CacheEvictLaunch& a, cudaStream_t s) {
-    // CTAs per (sequence, kv head): more while that still leaves each 2048 tokens and all of them fit at once
+    // CTAs per (sequence, kv head): more while that still leaves each 2048 tokens and all of them fit at once (one
+    // sequence of 64k tokens, 8 heads, with the move: 1 CTA 191 us, 2 109, 4 32.5, 8 31.8)
     const long long bh = (long long)a.B * a.Hkv, cap = (long long)a.max_pages * a.page;
     int ctas = 1;
     while (ctas < 8 && cap >= 4096ll * ctas && bh * ctas * 2 <= a.num_sms) ctas *= 2;
@@ -558,6 +560,8 @@ cudaError_t launch_cache_evict(const CacheEvictLaunch& a, cudaStream_t s) {
     attr[1].val.clusterDim = {(unsigned)ctas, 1, 1};
     cfg.attrs = attr;
     cfg.numAttrs = 2;
+    // keys in registers: 8 per thread leave two CTAs per SM (32 sequences of 4096 tokens, 8 heads: 45 us; 32 registers 55,
+    // none 51), 32 save a long sequence the second and third read (64k tokens: 32 us; none 51)
     cudaError_t e = per <= 8    ? cudaLaunchKernelEx(&cfg, evict_select_kernel<8>, a, ctas)
                     : per <= 32 ? cudaLaunchKernelEx(&cfg, evict_select_kernel<32>, a, ctas)
                                 : cudaLaunchKernelEx(&cfg, evict_select_kernel<0>, a, ctas);

@@ -3,13 +3,16 @@
 //
 // Every byte of the cache is read once per 32 query rows (the Hq / Hkv heads of
 // a group times the new tokens), 2 d bytes per key for 4 d flops per row: bound
-// by HBM for 8 rows, by the instructions that widen the bytes for 32.  A CTA has
-// four warps.  Each streams 32 keys per step through a ring of cp.async copies
-// and holds 8 query rows; with up to 8 rows the warps take different keys and
-// wait for nobody until the end, with 16 or 32 the warps of a group of RG = 2 or
-// 4 read each other's keys for rows of their own.  (All rows in every warp
-// instead, in 255 registers: 50 us against 33 for 8 sequences of 8000 tokens, 4 kv
-// heads, 32 rows.)
+// by HBM for 8 rows, by the latencies of widening and multiplying for more (32
+// rows: 2 warps per scheduler, 35% of the issue slots, HBM 25%).  A CTA has four
+// warps.  Each streams 32 keys per step through a ring of cp.async copies and
+// holds 8 query rows, or 16 where there are more, so that a widened fragment
+// serves two products.  Up to 16 rows the warps take different keys and wait for
+// nobody until the end; with 32 two warps read each other's keys, each for rows
+// of its own.  8 sequences of 8000 tokens, 4 kv heads, d = 128: 24.5 us for 8 rows,
+// 29.8 for 16, 39.2 for 32 (8 rows in each of four warps that share keys: 42.6, and
+// 99.6 against 83.8 for 80 rows; 32 rows in every warp: spills, 50 against 33 without
+// the second kernel).
 //
 // The work is one list of steps of 128 keys over all sequences, kv heads and row
 // tiles, cut into equal shares for as many CTAs as run at once, from the lengths
@@ -53,9 +56,10 @@ constexpr int kStages = 2;                         // steps in flight
 constexpr float kSlack = 8.f;  // how far (log2) a score may exceed the reference that its weight is relative to
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
 
-template <int D, int RG>
+template <int D, int ROWS_>
 struct Cfg {
-    static constexpr int ROWS = 8 * RG, KG = kWarps / RG;  // query rows per tile; groups of warps with different keys
+    static constexpr int ROWS = ROWS_, NB = ROWS == 8 ? 1 : 2;  // query rows per tile; a warp's, in eights
+    static constexpr int RG = ROWS / (8 * NB), KG = kWarps / RG;  // row groups; groups of warps with different keys
     static constexpr int HALF = kKeys * D;                 // bytes of K (and of V) per warp and step
     static constexpr int SLOT = 2 * HALF + 8 * kKeys;      // K, V, K scales, log2 of V scales
     static constexpr int RING = kStages * SLOT;            // per warp
@@ -63,12 +67,12 @@ struct Cfg {
                                                            // first group's
     static constexpr int OROW = D + 4;                     // a row of them, floats; within it column d (of 8 runs of
                                                            // D / 8: g, then 2 i + e) is at 16 i + 2 g + e: no bank conflicts
-    static constexpr int SMEM = MERGE + (kWarps - RG) * 8 * OROW * 4;
+    static constexpr int SMEM = MERGE + (kWarps - RG) * 8 * NB * OROW * 4;
     // CTAs per SM, and those that the registers are made for.  d = 128, up to 8 rows: bound by HBM, and a third CTA
     // only costs (128k tokens: 68 us with one, 55 with two, 58 with three; the copies alone 51 with one).  d = 64: bound
-    // by instructions, four CTAs 28.9 us, three 30.2, five 30.6 (16 sequences of 3000 tokens, 16 heads).  32 rows: 51 us
-    // with two CTAs of up to 255 registers, 55 with two of 168, 56 with three (8 sequences of 8000 tokens, 4 kv heads).
-    static constexpr int CTAS = D == 64 ? 4 : 2, REGS_FOR = D == 64 ? 4 : RG == 4 ? 2 : 3;
+    // by instructions, four CTAs 28.9 us, three 30.2, five 30.6 (16 sequences of 3000 tokens, 16 heads).  16 rows per
+    // warp take 249 registers at d = 128 and more than 128 at d = 64.
+    static constexpr int CTAS = D == 64 ? 4 : 2, REGS_FOR = NB == 2 ? (D == 64 ? 3 : 2) : D == 64 ? 4 : 3;
     static_assert(CTAS * (SMEM + 1536) <= 227 * 1024, "shared memory");
 };
 
@@ -156,12 +160,12 @@ __device__ __forceinline__ long long scores_at(const Params& a, long long bh, in
     return (bh * ((a.rows + 3) & ~3) + rt * ROWS) * cap;
 }
 
-template <int D, int RG>
-__global__ void __launch_bounds__(kThreads, Cfg<D, RG>::REGS_FOR) decode_fp8_kernel(const Params a) {
-    using C = Cfg<D, RG>;
-    constexpr int MT = kKeys / 16, KS = D / 16, DT = D / 8, ROWS = C::ROWS, KG = C::KG;
+template <int D, int ROWS>
+__global__ void __launch_bounds__(kThreads, Cfg<D, ROWS>::REGS_FOR) decode_fp8_kernel(const Params a) {
+    using C = Cfg<D, ROWS>;
+    constexpr int MT = kKeys / 16, KS = D / 16, DT = D / 8, NB = C::NB, RG = C::RG, KG = C::KG;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ float s_stat[kWarps][2][8];  // m and l of a warp's rows
+    __shared__ float s_stat[kWarps][2][8 * NB];  // m and l of a warp's rows
     __shared__ Cursor s_ahead[kWarps];
     pdl_launch_dependents();
     pdl_wait();
@@ -195,10 +199,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, RG>::REGS_FOR) decode_fp8_ker
     }
 
     // ---- Q fragments: k-step s of lane (g, t) is row g, columns (D = 128: 64 (s / 4) +) 16 t + 4 (s % 4) .. + 3
-    uint32_t qb[KS][2];
-    float sc[2];  // score scale of the rows whose scores this lane holds: 2 t, 2 t + 1 of its row group
-    auto load_q = [&](uint32_t (&w)[D / 8]) {
-        const int r = cur.rt * ROWS + rg * 8 + g;
+    uint32_t qb[NB][KS][2];
+    float sc[NB][2];  // score scale of the rows whose scores this lane holds: 2 t, 2 t + 1 of each eight
+    auto load_q = [&](int nb, uint32_t (&w)[D / 8]) {
+        const int r = cur.rt * ROWS + (rg * NB + nb) * 8 + g;
         const uint4* src =
             reinterpret_cast<const uint4*>(a.q + (((long long)cur.b * a.Hkv + cur.kvh) * a.rows + r) * D + t * 16);
 #pragma unroll
@@ -207,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, RG>::REGS_FOR) decode_fp8_ker
             w[i * 4] = x.x, w[i * 4 + 1] = x.y, w[i * 4 + 2] = x.z, w[i * 4 + 3] = x.w;
         }
     };
-    auto make_q = [&](const uint32_t (&w)[D / 8]) {
+    auto make_q = [&](int nb, const uint32_t (&w)[D / 8]) {
         float big = 0.f;
 #pragma unroll
         for (int i = 0; i < D / 8; ++i)
@@ -228,10 +232,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, RG>::REGS_FOR) decode_fp8_ker
                 const uint32_t x = w[s * 2 + j];
                 const __half2 h = __floats2half2_rn(__uint_as_float(x << 16) * down,
                                                     __uint_as_float(x & 0xFFFF0000u) * down);
-                qb[s][j] = *reinterpret_cast<const uint32_t*>(&h);
+                qb[nb][s][j] = *reinterpret_cast<const uint32_t*>(&h);
             }
 #pragma unroll
-        for (int j = 0; j < 2; ++j) sc[j] = __shfl_sync(0xffffffffu, up, (2 * t + j) * 4);
+        for (int j = 0; j < 2; ++j) sc[nb][j] = __shfl_sync(0xffffffffu, up, (2 * t + j) * 4);
     };
 
     // ---- the ring: this warp's 32 keys of the steps ahead, whatever item they are of
@@ -339,12 +343,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, RG>::REGS_FOR) decode_fp8_ker
     };
     static_assert(kStages == 2, "the start");
     {   // the loads of the first steps depend on each other (lengths, pages, rows): the queries' come in between
-        uint32_t w[D / 8];
+        uint32_t w[NB][D / 8];
         fetch_page();
         const auto first = to_issue;
         fetch_page();
         const auto second = to_issue;
-        load_q(w);
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) load_q(nb, w[nb]);
         fetch_page();
         const auto third = to_issue;
         float ks = 0.f, vs = 0.f;
@@ -353,42 +358,48 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, RG>::REGS_FOR) decode_fp8_ker
         to_issue = second;
         issue(1, ks_next, vs_next);
         to_issue = third;
-        make_q(w);
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) make_q(nb, w[nb]);
         put_scales(0, ks, vs);
     }
 
     // ---- the steps
-    float acc[D / 16][4];      // columns g d / 8 + 2 i + c / 2 of rows 2 t + c % 2
-    float m[2], M[2], l[2];    // of rows 2 t + j; the references start at the lowest number: a row that sees no key
-                               // keeps l = 0 (2^(-inf - m))
-    int seg = 0, slot = 0;     // first step of the segment within its item; ring slot
+    float acc[NB][D / 16][4];                // columns g d / 8 + 2 i + c / 2 of rows 2 t + c % 2 of each eight
+    float m[NB][2], M[NB][2], l[NB][2];      // of rows 2 t + j; the references start at the lowest number: a row that sees
+                                             // no key keeps l = 0 (2^(-inf - m))
+    int seg = 0, slot = 0;                   // first step of the segment within its item; ring slot
     bool begins = true;
     for (int it = 0; it < count; ++it) {
-        const int r0 = cur.rt * ROWS + rg * 8, nrows = min(ROWS, a.rows - cur.rt * ROWS);  // of the warp, of the tile
+        const int r0 = cur.rt * ROWS + rg * NB * 8, nrows = min(ROWS, a.rows - cur.rt * ROWS);  // of the warp, of the tile
         const long long bh = (long long)cur.b * a.Hkv + cur.kvh;
         if (begins) {
-            if (it > 0) {
-                uint32_t w[D / 8];
-                load_q(w);
-                make_q(w);
-            }
             seg = cur.s;
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+            for (int nb = 0; nb < NB; ++nb) {
+                if (it > 0) {
+                    uint32_t w[D / 8];
+                    load_q(nb, w);
+                    make_q(nb, w);
+                }
 #pragma unroll
-            for (int j = 0; j < 2; ++j) m[j] = M[j] = -FLT_MAX, l[j] = 0.f;
+                for (int i = 0; i < D / 16; ++i) acc[nb][i][0] = acc[nb][i][1] = acc[nb][i][2] = acc[nb][i][3] = 0.f;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) m[nb][j] = M[nb][j] = -FLT_MAX, l[nb][j] = 0.f;
+            }
         }
         cp_async_wait<kStages - 1>();
         group_sync();  // every lane's copies are there
 #pragma unroll 1
         for (int part = 0; part < RG; ++part) {
             const int key0 = cur.s * kStep + (kg * RG + part) * kKeys;
-            if (key0 >= cur.len || rg * 8 >= nrows) break;
+            if (key0 >= cur.len || rg * NB * 8 >= nrows) break;
             const uint8_t* st = smem + (kg * RG + part) * C::RING + slot * C::SLOT;
-            float S[MT][4];  // keys 16 i + g, + 8 (c / 2) of rows 2 t + c % 2
+            float S[NB][MT][4];  // keys 16 i + g, + 8 (c / 2) of rows 2 t + c % 2
             const uint4* kf = reinterpret_cast<const uint4*>(st);
 #pragma unroll
-            for (int i = 0; i < MT; ++i) S[i][0] = S[i][1] = S[i][2] = S[i][3] = 0.f;
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int i = 0; i < MT; ++i) S[nb][i][0] = S[nb][i][1] = S[nb][i][2] = S[nb][i][3] = 0.f;
 #pragma unroll
             for (int h = 0; h < D / 64; ++h) {
                 uint32_t w[2 * MT][4];
@@ -404,7 +415,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, RG>::REGS_FOR) decode_fp8_ker
                     for (int i = 0; i < MT; ++i) {
                         const uint32_t ka[4] = {e4m3x2_to_half2(w[2 * i][c]), e4m3x2_to_half2(w[2 * i + 1][c]),
                                                 e4m3x2_hi_to_half2(w[2 * i][c]), e4m3x2_hi_to_half2(w[2 * i + 1][c])};
-                        mma_16816(S[i], ka, qb[h * 4 + c][0], qb[h * 4 + c][1]);
+#pragma unroll
+                        for (int nb = 0; nb < NB; ++nb) mma_16816(S[nb][i], ka, qb[nb][h * 4 + c][0], qb[nb][h * 4 + c][1]);
                     }
             }
             const float* ksf = reinterpret_cast<const float*>(st + 2 * C::HALF) + g;
@@ -413,97 +425,104 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, RG>::REGS_FOR) decode_fp8_ker
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const float kscale = ksf[i * 16 + h * 8];
-                    S[i][2 * h] *= sc[0] * kscale;
-                    S[i][2 * h + 1] *= sc[1] * kscale;
-                }
-            if (key0 + kKeys > cur.len - a.Nq + 1) {  // some row does not see every key
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int lim = cur.len - a.Nq + (r0 + 2 * t + j) % a.Nq + 1 - key0 - g;
+                    for (int nb = 0; nb < NB; ++nb) {
+                        S[nb][i][2 * h] *= sc[nb][0] * kscale;
+                        S[nb][i][2 * h + 1] *= sc[nb][1] * kscale;
+                    }
+                }
+            uint32_t pb[NB][MT][2];
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+                auto& x = S[nb];
+                if (key0 + kKeys > cur.len - a.Nq + 1) {  // some row does not see every key
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int lim = cur.len - a.Nq + (r0 + nb * 8 + 2 * t + j) % a.Nq + 1 - key0 - g;
+#pragma unroll
+                        for (int i = 0; i < MT; ++i)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+                                if (i * 16 + h * 8 >= lim) x[i][2 * h + j] = -INFINITY;
+                    }
+                }
+                if (a.scores) {  // [key][row of the tile]: a lane's two rows are neighbours
+                    const int r = (rg * NB + nb) * 8 + 2 * t;
+                    float* sr = a.scores + scores_at<ROWS>(a, bh, cur.rt, cap) + (long long)(key0 + g) * nrows + r;
 #pragma unroll
                     for (int i = 0; i < MT; ++i)
 #pragma unroll
                         for (int h = 0; h < 2; ++h)
-                            if (i * 16 + h * 8 >= lim) S[i][2 * h + j] = -INFINITY;
+                            if (key0 + i * 16 + h * 8 + g < cur.len) {
+                                float* at = sr + (i * 16 + h * 8) * nrows;
+                                if ((nrows & 1) == 0) {
+                                    if (r < nrows) *reinterpret_cast<float2*>(at) = make_float2(x[i][2 * h], x[i][2 * h + 1]);
+                                } else {
+                                    if (r < nrows) at[0] = x[i][2 * h];
+                                    if (r + 1 < nrows) at[1] = x[i][2 * h + 1];
+                                }
+                            }
                 }
-            }
-            if (a.scores) {  // [key][row of the tile]: a lane's two rows are neighbours
-                const int r = rg * 8 + 2 * t;
-                float* sr = a.scores + scores_at<ROWS>(a, bh, cur.rt, cap) + (long long)(key0 + g) * nrows + r;
+                // ---- softmax: p = 2^(x - m) into l; w = 2^(x + log2 vs - M) for the value product.  m and M need not be
+                // the maxima, only within 2^8 of them (fp16 holds 2^15): most steps find no larger one and skip the
+                // reductions.
+                float mx[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    mx[j] = fmaxf(x[0][j], x[0][2 + j]);
+#pragma unroll
+                    for (int i = 1; i < MT; ++i) mx[j] = fmax3(mx[j], x[i][j], x[i][2 + j]);
+                }
+                if (__any_sync(0xffffffffu, mx[0] > m[nb][0] + kSlack || mx[1] > m[nb][1] + kSlack)) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        float top = fmaxf(m[nb][j], mx[j]);
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                        l[nb][j] *= ex2(m[nb][j] - top);
+                        m[nb][j] = top;
+                    }
+                }
 #pragma unroll
                 for (int i = 0; i < MT; ++i)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        if (key0 + i * 16 + h * 8 + g < cur.len) {
-                            float* at = sr + (i * 16 + h * 8) * nrows;
-                            if ((nrows & 1) == 0) {
-                                if (r < nrows) *reinterpret_cast<float2*>(at) = make_float2(S[i][2 * h], S[i][2 * h + 1]);
-                            } else {
-                                if (r < nrows) at[0] = S[i][2 * h];
-                                if (r + 1 < nrows) at[1] = S[i][2 * h + 1];
-                            }
+                    for (int h = 0; h < 2; ++h) {
+                        const float lv = ksf[kKeys + i * 16 + h * 8];
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            l[nb][j] += ex2(x[i][2 * h + j] - m[nb][j]);
+                            x[i][2 * h + j] += lv;
                         }
-            }
-            // ---- softmax: p = 2^(x - m) into l; w = 2^(x + log2 vs - M) for the value product.  m and M need not be
-            // the maxima, only within 2^8 of them (fp16 holds 2^15): most steps find no larger one and skip the
-            // reductions.
-            float mx[2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                mx[j] = fmaxf(S[0][j], S[0][2 + j]);
-#pragma unroll
-                for (int i = 1; i < MT; ++i) mx[j] = fmax3(mx[j], S[i][j], S[i][2 + j]);
-            }
-            if (__any_sync(0xffffffffu, mx[0] > m[0] + kSlack || mx[1] > m[1] + kSlack)) {
+                    }
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    float x = fmaxf(m[j], mx[j]);
+                    mx[j] = fmaxf(x[0][j], x[0][2 + j]);
 #pragma unroll
-                    for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-                    l[j] *= ex2(m[j] - x);
-                    m[j] = x;
+                    for (int i = 1; i < MT; ++i) mx[j] = fmax3(mx[j], x[i][j], x[i][2 + j]);
                 }
-            }
-#pragma unroll
-            for (int i = 0; i < MT; ++i)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float lv = ksf[kKeys + i * 16 + h * 8];
+                if (__any_sync(0xffffffffu, mx[0] > M[nb][0] + kSlack || mx[1] > M[nb][1] + kSlack)) {
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        l[j] += ex2(S[i][2 * h + j] - m[j]);
-                        S[i][2 * h + j] += lv;
+                        float top = fmaxf(M[nb][j], mx[j]);
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                        const float f = ex2(M[nb][j] - top);
+                        M[nb][j] = top;
+#pragma unroll
+                        for (int i = 0; i < D / 16; ++i) {
+                            acc[nb][i][j] *= f;
+                            acc[nb][i][2 + j] *= f;
+                        }
                     }
                 }
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                mx[j] = fmaxf(S[0][j], S[0][2 + j]);
+                for (int i = 0; i < MT; ++i)
 #pragma unroll
-                for (int i = 1; i < MT; ++i) mx[j] = fmax3(mx[j], S[i][j], S[i][2 + j]);
-            }
-            if (__any_sync(0xffffffffu, mx[0] > M[0] + kSlack || mx[1] > M[1] + kSlack)) {
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    float x = fmaxf(M[j], mx[j]);
-#pragma unroll
-                    for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-                    const float f = ex2(M[j] - x);
-                    M[j] = x;
-#pragma unroll
-                    for (int i = 0; i < D / 16; ++i) {
-                        acc[i][j] *= f;
-                        acc[i][2 + j] *= f;
+                    for (int h = 0; h < 2; ++h) {
+                        const __half2 w = __floats2half2_rn(ex2(x[i][2 * h] - M[nb][0]), ex2(x[i][2 * h + 1] - M[nb][1]));
+                        pb[nb][i][h] = transpose8x8(*reinterpret_cast<const uint32_t*>(&w));
                     }
-                }
             }
-            uint32_t pb[MT][2];
-#pragma unroll
-            for (int i = 0; i < MT; ++i)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const __half2 w = __floats2half2_rn(ex2(S[i][2 * h] - M[0]), ex2(S[i][2 * h + 1] - M[1]));
-                    pb[i][h] = transpose8x8(*reinterpret_cast<const uint32_t*>(&w));
-                }
             const uint8_t* vf = st + C::HALF;
 #pragma unroll
             for (int i = 0; i < MT; ++i) {
@@ -528,7 +547,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, RG>::REGS_FOR) decode_fp8_ker
                         const uint32_t x = __byte_perm(v[0][c], v[1][c], sel), y = __byte_perm(v[2][c], v[3][c], sel);
                         const uint32_t va[4] = {e4m3x2_to_half2(x), e4m3x2_hi_to_half2(x), e4m3x2_to_half2(y),
                                                 e4m3x2_hi_to_half2(y)};
-                        mma_16816(acc[2 * c + h], va, pb[i][0], pb[i][1]);
+#pragma unroll
+                        for (int nb = 0; nb < NB; ++nb) mma_16816(acc[nb][2 * c + h], va, pb[nb][i][0], pb[nb][i][1]);
                     }
             }
         }
@@ -542,87 +562,95 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, RG>::REGS_FOR) decode_fp8_ker
         const bool item_ends = cur.s + 1 == cur.n;
         begins = item_ends || it + 1 == count;
         if (begins) {
+            float f[NB][2];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-#pragma unroll
-                for (int d = 4; d < 32; d <<= 1) l[j] += __shfl_xor_sync(0xffffffffu, l[j], d);
-                if (KG > 1 && g == 0) s_stat[warp][0][2 * t + j] = m[j], s_stat[warp][1][2 * t + j] = l[j];
-            }
-            float f[2];
-            if constexpr (KG > 1) {
-                __syncthreads();
+            for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const int r = 2 * t + j;
-                    float top = m[j], sum = 0.f;
 #pragma unroll
-                    for (int w = 0; w < KG; ++w) top = fmaxf(top, s_stat[w * RG + rg][0][r]);
-#pragma unroll
-                    for (int w = 0; w < KG; ++w) sum += s_stat[w * RG + rg][1][r] * ex2(s_stat[w * RG + rg][0][r] - top);
-                    f[j] = ex2(M[j] - top);
-                    m[j] = top;
-                    l[j] = sum;
+                    for (int d = 4; d < 32; d <<= 1) l[nb][j] += __shfl_xor_sync(0xffffffffu, l[nb][j], d);
+                    const int r = nb * 8 + 2 * t + j;
+                    if (KG > 1 && g == 0) s_stat[warp][0][r] = m[nb][j], s_stat[warp][1][r] = l[nb][j];
+                    f[nb][j] = ex2(M[nb][j] - m[nb][j]);
                 }
-                float* buf = reinterpret_cast<float*>(smem + C::MERGE);
-                if (kg > 0) {
+            if constexpr (KG > 1) {
+                __syncthreads();
+                float* buf = reinterpret_cast<float*>(smem + C::MERGE) + g * 2;
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
+                for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                        for (int i = 0; i < D / 16; ++i)
-                            *reinterpret_cast<float2*>(buf + ((warp - RG) * 8 + 2 * t + j) * C::OROW + i * 16 + g * 2) =
-                                make_float2(acc[i][j] * f[j], acc[i][2 + j] * f[j]);
-                }
+                    for (int j = 0; j < 2; ++j) {
+                        const int r = nb * 8 + 2 * t + j;
+                        float top = m[nb][j], sum = 0.f;
+#pragma unroll
+                        for (int w = 0; w < KG; ++w) top = fmaxf(top, s_stat[w * RG + rg][0][r]);
+#pragma unroll
+                        for (int w = 0; w < KG; ++w)
+                            sum += s_stat[w * RG + rg][1][r] * ex2(s_stat[w * RG + rg][0][r] - top);
+                        f[nb][j] = ex2(M[nb][j] - top);
+                        m[nb][j] = top;
+                        l[nb][j] = sum;
+                        if (kg > 0)
+#pragma unroll
+                            for (int i = 0; i < D / 16; ++i)
+                                *reinterpret_cast<float2*>(buf + ((warp - RG) * 8 * NB + r) * C::OROW + i * 16) =
+                                    make_float2(acc[nb][i][j] * f[nb][j], acc[nb][i][2 + j] * f[nb][j]);
+                    }
                 __syncthreads();
                 if (kg == 0) {
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
+                    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                        for (int i = 0; i < D / 16; ++i) {
-                            float2 x = make_float2(acc[i][j] * f[j], acc[i][2 + j] * f[j]);
+                        for (int j = 0; j < 2; ++j) {
 #pragma unroll
-                            for (int w = 1; w < KG; ++w) {
-                                const float2 y = *reinterpret_cast<const float2*>(
-                                    buf + (((w - 1) * RG + rg) * 8 + 2 * t + j) * C::OROW + i * 16 + g * 2);
-                                x.x += y.x;
-                                x.y += y.y;
+                            for (int i = 0; i < D / 16; ++i) {
+                                float2 x = make_float2(acc[nb][i][j] * f[nb][j], acc[nb][i][2 + j] * f[nb][j]);
+#pragma unroll
+                                for (int w = 1; w < KG; ++w) {
+                                    const float2 y = *reinterpret_cast<const float2*>(
+                                        buf + (((w - 1) * RG + rg) * 8 * NB + nb * 8 + 2 * t + j) * C::OROW + i * 16);
+                                    x.x += y.x;
+                                    x.y += y.y;
+                                }
+                                acc[nb][i][j] = x.x;
+                                acc[nb][i][2 + j] = x.y;
                             }
-                            acc[i][j] = x.x;
-                            acc[i][2 + j] = x.y;
+                            f[nb][j] = 1.f;
                         }
-                    f[0] = f[1] = 1.f;
                 }
-            } else {
-                f[0] = ex2(M[0] - m[0]);
-                f[1] = ex2(M[1] - m[1]);
             }
             if (kg == 0) {
                 const bool whole = seg == 0 && item_ends;
                 const long long slot_out = blockIdx.x + bh * a.row_tiles + cur.rt;
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int r = rg * 8 + 2 * t + j;
-                    if (r >= nrows) continue;
-                    const float scale = l[j] == 0.f ? 0.f : f[j] / l[j];  // l = 0: the row sees no key; NaN stays
-                    const float lse2 = l[j] == 0.f ? -INFINITY : m[j] + lg2(l[j]);
-                    const long long row = bh * a.rows + cur.rt * ROWS + r;  // (b, head, token) flattened
-                    float o[DT];
+                for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                    for (int i = 0; i < D / 16; ++i) o[2 * i] = acc[i][j] * scale, o[2 * i + 1] = acc[i][2 + j] * scale;
-                    if (whole) {
-                        uint4* dst = reinterpret_cast<uint4*>(a.o + row * D + g * DT);
+                    for (int j = 0; j < 2; ++j) {
+                        const int r = (rg * NB + nb) * 8 + 2 * t + j;
+                        if (r >= nrows) continue;
+                        const float sum = l[nb][j];
+                        const float scale = sum == 0.f ? 0.f : f[nb][j] / sum;  // 0: the row sees no key; NaN stays
+                        const float lse2 = sum == 0.f ? -INFINITY : m[nb][j] + lg2(sum);
+                        const long long row = bh * a.rows + cur.rt * ROWS + r;  // (b, head, token) flattened
+                        float o[DT];
 #pragma unroll
-                        for (int i = 0; i < DT / 8; ++i)
-                            dst[i] = make_uint4(pack_bf16(o[8 * i], o[8 * i + 1]), pack_bf16(o[8 * i + 2], o[8 * i + 3]),
-                                                pack_bf16(o[8 * i + 4], o[8 * i + 5]), pack_bf16(o[8 * i + 6], o[8 * i + 7]));
-                        if (a.lse && g == 0) a.lse[row] = lse2 * kLn2;
-                    } else {
-                        float4* dst = reinterpret_cast<float4*>(a.part_o + (slot_out * ROWS + r) * D + g * DT);
+                        for (int i = 0; i < D / 16; ++i)
+                            o[2 * i] = acc[nb][i][j] * scale, o[2 * i + 1] = acc[nb][i][2 + j] * scale;
+                        if (whole) {
+                            uint4* dst = reinterpret_cast<uint4*>(a.o + row * D + g * DT);
 #pragma unroll
-                        for (int i = 0; i < DT / 4; ++i)
-                            dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                            for (int i = 0; i < DT / 8; ++i)
+                                dst[i] = make_uint4(pack_bf16(o[8 * i], o[8 * i + 1]), pack_bf16(o[8 * i + 2], o[8 * i + 3]),
+                                                    pack_bf16(o[8 * i + 4], o[8 * i + 5]), pack_bf16(o[8 * i + 6], o[8 * i + 7]));
+                            if (a.lse && g == 0) a.lse[row] = lse2 * kLn2;
+                        } else {
+                            float4* dst = reinterpret_cast<float4*>(a.part_o + (slot_out * ROWS + r) * D + g * DT);
+#pragma unroll
+                            for (int i = 0; i < DT / 4; ++i)
+                                dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                        }
+                        if (g == 0) a.part_lse[slot_out * ROWS + r] = lse2;
                     }
-                    if (g == 0) a.part_lse[slot_out * ROWS + r] = lse2;
-                }
             }
         }
         if (it + 1 < count) advance(cur, a, cap);
@@ -724,7 +752,8 @@ __global__ void __launch_bounds__(kFinishThreads) finish_fp8_kernel(const Params
 }
 
 // weights[j] += sum over the rows of 2^(x_j - LSE), in a fixed order.  A thread takes four pieces of 16 bytes of scores.
-// With 4, 8, 16 or 32 rows (VEC) a token's scores are 1, 2, 4 or 8 lanes' pieces; otherwise a thread takes whole tokens.
+// With 4, 8, 16 or 32 rows (VEC) a token's scores are 1, 2, 4 or 8 lanes' pieces; otherwise a thread takes whole tokens
+// (that for all: a decode of 32 sequences of 4096 tokens, 8 kv heads, 4 rows 71.6 us against 70.4).
 constexpr int kWeightThreads = 256, kPieces = 4;
 
 template <int ROWS, bool VEC>
@@ -785,10 +814,10 @@ __global__ void __launch_bounds__(kWeightThreads) weights_fp8_kernel(const Param
     }
 }
 
-template <int D, int RG>
+template <int D, int ROWS>
 cudaError_t launch_d(const PagedDecodeFp8Launch& a, cudaStream_t s) {
-    using C = Cfg<D, RG>;
-    cudaError_t e = set_smem_limit_once<decode_fp8_kernel<D, RG>>(C::SMEM);
+    using C = Cfg<D, ROWS>;
+    cudaError_t e = set_smem_limit_once<decode_fp8_kernel<D, ROWS>>(C::SMEM);
     if (e != cudaSuccess) return e;
     Params p;
     p.q = (const __nv_bfloat16*)a.q;
@@ -813,7 +842,7 @@ cudaError_t launch_d(const PagedDecodeFp8Launch& a, cudaStream_t s) {
     p.max_pages = a.max_pages;
     p.num_pages = a.num_pages;
     p.rows = a.Hq / a.Hkv * a.Nq;
-    p.row_tiles = (p.rows + C::ROWS - 1) / C::ROWS;
+    p.row_tiles = (p.rows + ROWS - 1) / ROWS;
     p.blocks_per_page = (uint32_t)(a.page / a.sb);
     p.page = FastDiv((uint32_t)a.page);
     p.sb = FastDiv((uint32_t)a.sb);
@@ -823,24 +852,24 @@ cudaError_t launch_d(const PagedDecodeFp8Launch& a, cudaStream_t s) {
     const long long bh = (long long)a.B * a.Hkv;
     // no more CTAs than steps at full lengths
     p.workers = (int)std::min<long long>(a.workers, bh * p.row_tiles * ((cap + kStep - 1) / kStep));
-    e = launch_dependent(decode_fp8_kernel<D, RG>, dim3(p.workers), dim3(kThreads), C::SMEM, s, p);
+    e = launch_dependent(decode_fp8_kernel<D, ROWS>, dim3(p.workers), dim3(kThreads), C::SMEM, s, p);
     if (e != cudaSuccess) return e;
     const long long row_blocks = bh * p.rows;
-    e = launch_dependent(finish_fp8_kernel<D, C::ROWS>, dim3((unsigned)row_blocks), dim3(kFinishThreads), 0, s, p);
+    e = launch_dependent(finish_fp8_kernel<D, ROWS>, dim3((unsigned)row_blocks), dim3(kFinishThreads), 0, s, p);
     if (e != cudaSuccess || !a.weights) return e;
     const bool vec = p.rows == 4 || p.rows == 8 || p.rows == 16 || p.rows == 32;
     const int tokens = kWeightThreads * kPieces / (vec ? p.rows / 4 : 1), blocks = (cap + tokens - 1) / tokens;
     const dim3 grid((unsigned)(bh * blocks)), block(kWeightThreads);
-    return vec ? launch_dependent(weights_fp8_kernel<C::ROWS, true>, grid, block, 0, s, p, blocks)
-               : launch_dependent(weights_fp8_kernel<C::ROWS, false>, grid, block, 0, s, p, blocks);
+    return vec ? launch_dependent(weights_fp8_kernel<ROWS, true>, grid, block, 0, s, p, blocks)
+               : launch_dependent(weights_fp8_kernel<ROWS, false>, grid, block, 0, s, p, blocks);
 }
 
-template <int D, int RG>
+template <int D, int ROWS>
 cudaError_t blocks_per_sm(int* blocks) {
-    using C = Cfg<D, RG>;
-    const cudaError_t e = set_smem_limit_once<decode_fp8_kernel<D, RG>>(C::SMEM);
+    using C = Cfg<D, ROWS>;
+    const cudaError_t e = set_smem_limit_once<decode_fp8_kernel<D, ROWS>>(C::SMEM);
     if (e != cudaSuccess) return e;
-    const cudaError_t f = cudaOccupancyMaxActiveBlocksPerMultiprocessor(blocks, decode_fp8_kernel<D, RG>, kThreads, C::SMEM);
+    const cudaError_t f = cudaOccupancyMaxActiveBlocksPerMultiprocessor(blocks, decode_fp8_kernel<D, ROWS>, kThreads, C::SMEM);
     *blocks = std::min(*blocks, C::CTAS);
     return f;
 }
@@ -849,13 +878,13 @@ cudaError_t blocks_per_sm(int* blocks) {
 
 cudaError_t launch_decode_paged_fp8(const PagedDecodeFp8Launch& a, cudaStream_t s) {
     const int tile = fp8_tile_rows(a.Hq / a.Hkv * a.Nq);
-    if (a.d == 128) return tile == 8 ? launch_d<128, 1>(a, s) : tile == 16 ? launch_d<128, 2>(a, s) : launch_d<128, 4>(a, s);
-    return tile == 8 ? launch_d<64, 1>(a, s) : tile == 16 ? launch_d<64, 2>(a, s) : launch_d<64, 4>(a, s);
+    if (a.d == 128) return tile == 8 ? launch_d<128, 8>(a, s) : tile == 16 ? launch_d<128, 16>(a, s) : launch_d<128, 32>(a, s);
+    return tile == 8 ? launch_d<64, 8>(a, s) : tile == 16 ? launch_d<64, 16>(a, s) : launch_d<64, 32>(a, s);
 }
 
 cudaError_t decode_fp8_blocks_per_sm(int d, int tile, int* n) {
-    if (d == 128) return tile == 8 ? blocks_per_sm<128, 1>(n) : tile == 16 ? blocks_per_sm<128, 2>(n) : blocks_per_sm<128, 4>(n);
-    return tile == 8 ? blocks_per_sm<64, 1>(n) : tile == 16 ? blocks_per_sm<64, 2>(n) : blocks_per_sm<64, 4>(n);
+    if (d == 128) return tile == 8 ? blocks_per_sm<128, 8>(n) : tile == 16 ? blocks_per_sm<128, 16>(n) : blocks_per_sm<128, 32>(n);
+    return tile == 8 ? blocks_per_sm<64, 8>(n) : tile == 16 ? blocks_per_sm<64, 16>(n) : blocks_per_sm<64, 32>(n);
 }
 
 }  // namespace fa
