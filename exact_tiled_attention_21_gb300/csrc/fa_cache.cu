@@ -221,10 +221,11 @@ cudaError_t launch_append_d(const CacheAppendLaunch& a, cudaStream_t s) {
 // ------------------------------------------------------------------ eviction
 // Which tokens stay: the last `recent`, and of the others the keep - recent with the largest weights (ties: lowest
 // index).  A cluster of 1 to 8 CTAs per (sequence, kv head), each with a run of the tokens, whose order-preserving
-// integer keys stay in its registers: three histograms (11, 11 and 10 bits), summed over the cluster's shared
-// memories, find the smallest key that stays and how many equal ones do; one count over the cluster then gives every
-// kept token its place in index order.  The weights are read once.
-constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32, kSelBins = 2048;
+// integer keys stay in its registers: four histograms of 8 bits, summed over the cluster's shared memories, find the
+// smallest key that stays and how many equal ones do, and how many of either the CTAs before this one have; a count
+// per warp then gives every kept token its place in index order.  The weights are read once.  (Three histograms of 11,
+// 11 and 10 bits moved eight times the bins between the CTAs: @@.)
+constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32, kSelBins = 256, kSelCtas = 8;
 
 // Integer whose order is the float's, with -0 = +0 and NaN above everything.
 __device__ __forceinline__ uint32_t order_key(float w) {
@@ -234,29 +235,20 @@ __device__ __forceinline__ uint32_t order_key(float w) {
     return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-__device__ __forceinline__ uint4 ld_cluster_u4(const uint32_t* p, uint32_t rank) {
-    uint4 v;
-    asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "r"(mapa_shared(smem_u32(p), rank))
-                 : "memory");
-    return v;
-}
-
 __device__ __forceinline__ uint32_t ld_cluster_u32(const uint32_t* p, uint32_t rank) {
     uint32_t v;
     asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(mapa_shared(smem_u32(p), rank)) : "memory");
     return v;
 }
-
-static_assert(kSelBins == 4 * kSelThreads, "four bins per thread");
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 // PER: keys of a thread in registers (0: any number; they are read again in each pass).
 template <int PER>
 __global__ void __launch_bounds__(kSelThreads, PER > 8 ? 1 : 2) evict_select_kernel(const CacheEvictLaunch a, int ctas) {
-    __shared__ __align__(16) uint32_t s_hist[2][kSelBins];
-    __shared__ uint32_t s_warp[kSelWarps];
-    __shared__ uint32_t s_digit, s_left, s_counts[2];
+    __shared__ uint32_t s_hist[4][kSelBins];
+    __shared__ uint2 s_warp[kSelBins / 32];
+    __shared__ uint32_t s_above[kSelWarps], s_equal[kSelWarps], s_digit, s_left, s_prior[2];
     pdl_launch_dependents();
     pdl_wait();
     const int rank = blockIdx.x % ctas;
@@ -290,98 +282,103 @@ __global__ void __launch_bounds__(kSelThreads, PER > 8 ? 1 : 2) evict_select_ker
     const int first = (rank * kSelWarps + warp) * per_warp + lane, rounds = per_warp / 32;
     const int cand = n - a.recent;  // candidates [0, cand): `left` of them stay
     float held[PER ? PER : 1] = {};  // loaded all at once, from clamped places
+    uint32_t keys[PER ? PER : 1] = {};
     if constexpr (PER > 0) {
 #pragma unroll
         for (int i = 0; i < PER; ++i) held[i] = w[min(first + i * 32, n - 1)];
     }
-    auto weight = [&](int i) { return PER ? held[PER ? i : 0] : w[first + i * 32]; };
-    auto key_of = [&](int i) { return order_key(weight(i)); };
-    uint32_t left = (uint32_t)(a.keep - a.recent), key = 0, known = 0;  // key's bits under the mask `known` are settled
-    for (int i = tid; i < 2 * kSelBins; i += kSelThreads) s_hist[0][i] = 0;
+    for (int i = tid; i < 4 * kSelBins; i += kSelThreads) s_hist[0][i] = 0;
+    if (tid < 2) s_prior[tid] = 0;
     __syncthreads();
+    if constexpr (PER > 0) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) keys[i] = order_key(held[i]);
+    }
+    auto key_of = [&](int i) { return PER ? keys[PER ? i : 0] : order_key(w[first + i * 32]); };
+    uint32_t left = (uint32_t)(a.keep - a.recent), key = 0, known = 0;  // key's bits under the mask `known` are settled
     if (left > 0) {
-        int shift = 21;
 #pragma unroll 1
-        for (int pass = 0; pass < 3; ++pass) {
-            uint32_t* hist = s_hist[pass & 1];
-            const uint32_t mask = pass == 2 ? 1023 : 2047;
+        for (int pass = 0; pass < 4; ++pass) {
+            uint32_t* hist = s_hist[pass];
+            const int shift = 24 - 8 * pass;
 #pragma unroll
             for (int i = 0; i < (PER ? PER : rounds); ++i)
                 if (i < rounds && first + i * 32 < cand) {
                     const uint32_t k = key_of(i);
-                    if ((k & known) == key) atomicAdd(&hist[(k >> shift) & mask], 1u);
+                    if ((k & known) == key) atomicAdd(&hist[(k >> shift) & (kSelBins - 1)], 1u);
                 }
             if (ctas > 1)
                 cluster_sync();
             else
                 __syncthreads();
-            // bins from the largest down: thread t holds bins 2047 - 4t .. 2044 - 4t of the cluster
-            const uint32_t* mine = hist + kSelBins - 4 - 4 * tid;
-            uint4 c = *reinterpret_cast<const uint4*>(mine);
-            uint4 o[7];
+            // bins from the largest down: thread t holds bin 255 - t, of the cluster and of the CTAs before this one
+            const uint32_t* bin = hist + kSelBins - 1 - tid;
+            uint32_t c = 0, ours = 0, incl = 0, incl_ours = 0;
+            if (tid < kSelBins) {
+                if (ctas > 1) {
+                    uint32_t v[kSelCtas];
 #pragma unroll
-            for (int r = 1; r < 8; ++r)
-                if (r < ctas) o[r - 1] = ld_cluster_u4(mine, (rank + r) % ctas);
+                    for (int r = 0; r < kSelCtas; ++r) v[r] = r < ctas ? ld_cluster_u32(bin, r) : 0;
 #pragma unroll
-            for (int r = 1; r < 8; ++r)
-                if (r < ctas) c.x += o[r - 1].x, c.y += o[r - 1].y, c.z += o[r - 1].z, c.w += o[r - 1].w;
-            if (pass == 1)  // everyone has read the first histogram by now: the third takes its place
-                *reinterpret_cast<uint4*>(s_hist[0] + 4 * tid) = make_uint4(0, 0, 0, 0);
-            const uint32_t sum = (c.x + c.y) + (c.z + c.w);
-            uint32_t incl = sum;
+                    for (int r = 0; r < kSelCtas; ++r) {
+                        c += v[r];
+                        if (r < rank) ours += v[r];
+                    }
+                } else {
+                    c = *bin;
+                }
+                incl = c, incl_ours = ours;
 #pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const uint32_t up = __shfl_up_sync(0xffffffffu, incl, d);
-                if (lane >= d) incl += up;
+                for (int d = 1; d < 32; d <<= 1) {
+                    const uint32_t up = __shfl_up_sync(0xffffffffu, incl, d);
+                    const uint32_t up_ours = __shfl_up_sync(0xffffffffu, incl_ours, d);
+                    if (lane >= d) incl += up, incl_ours += up_ours;
+                }
+                if (lane == 31) s_warp[warp] = make_uint2(incl, incl_ours);
             }
-            if (lane == 31) s_warp[warp] = incl;
             __syncthreads();
-            uint32_t before = lane < warp ? s_warp[lane] : 0;
-            before = __reduce_add_sync(0xffffffffu, before) + incl - sum;
-            if (before < left && before + sum >= left) {  // exactly one thread
-                const uint32_t count[4] = {c.w, c.z, c.y, c.x};
-                uint32_t skip = 0;
-                int i = 0;
-                while (i < 3 && before + skip + count[i] < left) skip += count[i++];
-                s_digit = (uint32_t)(kSelBins - 1 - 4 * tid - i);
-                s_left = left - before - skip;
+            if (tid < kSelBins) {
+                const uint2 x = lane < warp ? s_warp[lane] : make_uint2(0, 0);
+                const uint32_t seen = __reduce_add_sync(0xffffffffu, x.x) + incl - c;
+                const uint32_t seen_ours = __reduce_add_sync(0xffffffffu, x.y) + incl_ours - ours;
+                if (seen < left && seen + c >= left) {  // exactly one thread
+                    s_digit = (uint32_t)(kSelBins - 1 - tid);
+                    s_left = left - seen;
+                    s_prior[0] += seen_ours;
+                    s_prior[1] = ours;  // equal so far: the last pass's stays
+                }
             }
             __syncthreads();
             key |= s_digit << shift;
-            known |= mask << shift;
+            known |= (kSelBins - 1) << shift;
             left = s_left;
-            shift -= pass == 0 ? 11 : 10;
         }
     } else {
         key = 0xFFFFFFFFu;  // none of the candidates: no equal one is admitted either
     }
+    if (ctas > 1) cluster_arrive();  // this CTA has read the others' histograms
     // in index order: keys above `key` and the recent tokens stay, and the first `left` equal ones
     uint32_t above = 0, equal = 0;
 #pragma unroll
     for (int i = 0; i < (PER ? PER : rounds); ++i)
         if (i < rounds) {
             const int j = first + i * 32;
-            const uint32_t k = j < cand ? key_of(i) : 0;
-            above += __popc(__ballot_sync(0xffffffffu, j < n && (j >= cand || k > key)));
-            equal += __popc(__ballot_sync(0xffffffffu, j < cand && k == key));
+            if (j < cand) {
+                const uint32_t k = key_of(i);
+                above += k > key;
+                equal += k == key;
+            } else {
+                above += j < n;
+            }
         }
+    above = __reduce_add_sync(0xffffffffu, above);
+    equal = __reduce_add_sync(0xffffffffu, equal);
     // counts before this warp: of the CTA's other warps, and of the cluster's CTAs before this one
-    __shared__ uint32_t s_above[kSelWarps], s_equal[kSelWarps];
     if (lane == 0) s_above[warp] = above, s_equal[warp] = equal;
     __syncthreads();
-    uint32_t ba = __reduce_add_sync(0xffffffffu, lane < warp ? s_above[lane] : 0);
-    uint32_t be = __reduce_add_sync(0xffffffffu, lane < warp ? s_equal[lane] : 0);
-    if (ctas > 1) {
-        if (warp == kSelWarps - 1 && lane == 0) s_counts[0] = ba + above, s_counts[1] = be + equal;
-        cluster_sync();
-        uint32_t oa = 0, oe = 0;
-        if (lane < rank) {
-            oa = ld_cluster_u32(&s_counts[0], lane);
-            oe = ld_cluster_u32(&s_counts[1], lane);
-        }
-        ba += __reduce_add_sync(0xffffffffu, oa);
-        be += __reduce_add_sync(0xffffffffu, oe);
-    }
+    uint32_t ba = __reduce_add_sync(0xffffffffu, lane < warp ? s_above[lane] : 0) + s_prior[0];
+    uint32_t be = __reduce_add_sync(0xffffffffu, lane < warp ? s_equal[lane] : 0) + s_prior[1];
+    ba += (uint32_t)max(min(rank * kSelWarps * per_warp, n) - cand, 0);  // recent tokens among them
     const uint32_t below = (1u << lane) - 1;
 #pragma unroll
     for (int i = 0; i < (PER ? PER : rounds); ++i)
@@ -389,17 +386,17 @@ __global__ void __launch_bounds__(kSelThreads, PER > 8 ? 1 : 2) evict_select_ker
             const int j = first + i * 32;
             const uint32_t k = j < cand ? key_of(i) : 0;
             const bool up = j < n && (j >= cand || k > key), eq = j < cand && k == key;
-            const uint32_t ma = __ballot_sync(0xffffffffu, up), me = __ballot_sync(0xffffffffu, eq);
+            const uint32_t ma = __ballot_sync(0xffffffffu, up), me = equal ? __ballot_sync(0xffffffffu, eq) : 0;
             const uint32_t ra = ba + __popc(ma & below), re = be + __popc(me & below);  // before j
             if (up || (eq && re < left)) {
                 const uint32_t at = ra + min(re, left);
                 kept[at] = j;
-                nw[at] = weight(i);
+                nw[at] = PER ? held[PER ? i : 0] : w[j];
             }
             ba += __popc(ma);
             be += __popc(me);
         }
-    if (ctas > 1) cluster_sync();  // the others may still read this CTA's counts
+    if (ctas > 1) cluster_wait();  // the others have read this CTA's
 }
 
 // Moves the kept tokens, a block of sb of them per turn of a CTA: K by the first 128 threads, V by the others.  The
@@ -547,7 +544,7 @@ cudaError_t launch_cache_evict(const CacheEvictLaunch& a, cudaStream_t s) {
     // sequence of 64k tokens, 8 heads, with the move: 1 CTA 191 us, 2 109, 4 32.5, 8 31.8)
     const long long bh = (long long)a.B * a.Hkv, cap = (long long)a.max_pages * a.page;
     int ctas = 1;
-    while (ctas < 8 && cap >= 4096ll * ctas && bh * ctas * 2 <= a.num_sms) ctas *= 2;
+    while (ctas < kSelCtas && cap >= 4096ll * ctas && bh * ctas * 2 <= a.num_sms) ctas *= 2;
     const long long per = (cap + (long long)ctas * kSelThreads - 1) / ((long long)ctas * kSelThreads);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(bh * ctas));
