@@ -281,6 +281,8 @@ __global__ void __launch_bounds__(kSelThreads, PER > 8 ? 1 : 2) evict_select_ker
     const int per_warp = ((n + ctas * kSelWarps - 1) / (ctas * kSelWarps) + 31) / 32 * 32;
     const int first = (rank * kSelWarps + warp) * per_warp + lane, rounds = per_warp / 32;
     const int cand = n - a.recent;  // candidates [0, cand): `left` of them stay
+    // of this thread's tokens first + 32 i: candidates are those with i < ic, recent ones those with ic <= i < in
+    const int ic = min(max(cand - first + 31, 0) / 32, rounds), in = min(max(n - first + 31, 0) / 32, rounds);
     float held[PER ? PER : 1] = {};  // loaded all at once, from clamped places
     uint32_t keys[PER ? PER : 1] = {};
     if constexpr (PER > 0) {
@@ -303,7 +305,7 @@ __global__ void __launch_bounds__(kSelThreads, PER > 8 ? 1 : 2) evict_select_ker
             const int shift = 24 - 8 * pass;
 #pragma unroll
             for (int i = 0; i < (PER ? PER : rounds); ++i)
-                if (i < rounds && first + i * 32 < cand) {
+                if (i < ic) {
                     const uint32_t k = key_of(i);
                     if ((k & known) == key) atomicAdd(&hist[(k >> shift) & (kSelBins - 1)], 1u);
                 }
@@ -361,16 +363,12 @@ __global__ void __launch_bounds__(kSelThreads, PER > 8 ? 1 : 2) evict_select_ker
     uint32_t above = 0, equal = 0;
 #pragma unroll
     for (int i = 0; i < (PER ? PER : rounds); ++i)
-        if (i < rounds) {
-            const int j = first + i * 32;
-            if (j < cand) {
-                const uint32_t k = key_of(i);
-                above += k > key;
-                equal += k == key;
-            } else {
-                above += j < n;
-            }
+        if (i < ic) {
+            const uint32_t k = key_of(i);
+            above += k > key;
+            equal += k == key;
         }
+    above += in - ic;
     above = __reduce_add_sync(0xffffffffu, above);
     equal = __reduce_add_sync(0xffffffffu, equal);
     // counts before this warp: of the CTA's other warps, and of the cluster's CTAs before this one
@@ -384,8 +382,8 @@ __global__ void __launch_bounds__(kSelThreads, PER > 8 ? 1 : 2) evict_select_ker
     for (int i = 0; i < (PER ? PER : rounds); ++i)
         if (i < rounds) {
             const int j = first + i * 32;
-            const uint32_t k = j < cand ? key_of(i) : 0;
-            const bool up = j < n && (j >= cand || k > key), eq = j < cand && k == key;
+            const uint32_t k = i < ic ? key_of(i) : 0;
+            const bool up = i < ic ? k > key : i < in, eq = i < ic && k == key;
             const uint32_t ma = __ballot_sync(0xffffffffu, up), me = equal ? __ballot_sync(0xffffffffu, eq) : 0;
             const uint32_t ra = ba + __popc(ma & below), re = be + __popc(me & below);  // before j
             if (up || (eq && re < left)) {
