@@ -15,14 +15,16 @@
 namespace fa {
 namespace {
 
-constexpr int kHalf = 128;  // threads of a block's K half (the V half has as many)
 
-// Largest value over the 128 threads of a half (w: 0 for K, 1 for V), the same in each of them.
-__device__ __forceinline__ uint32_t half_max(uint32_t v, uint32_t (&s)[2][4], int w) {
+// Largest value over the 32 W threads of a block's half (w: 0 for K, 1 for V), the same in each of them.
+template <int W>
+__device__ __forceinline__ uint32_t half_max(uint32_t v, uint32_t (&s)[2][W], int w) {
     v = __reduce_max_sync(0xffffffffu, v);
-    if ((threadIdx.x & 31) == 0) s[w][(threadIdx.x >> 5) & 3] = v;
+    if ((threadIdx.x & 31) == 0) s[w][(threadIdx.x >> 5) % W] = v;
     __syncthreads();
-    return max(max(s[w][0], s[w][1]), max(s[w][2], s[w][3]));
+#pragma unroll
+    for (int i = 0; i < W; ++i) v = max(v, s[w][i]);
+    return v;
 }
 
 // Smallest power of two s >= 2^-126 with amax <= 448 s, from the bits of a bf16 amax: 448 = 1.75 * 2^8.
@@ -65,27 +67,36 @@ __device__ __forceinline__ uint2 quantise8(uint4 x, float inv, float s, bool pow
     return make_uint2(e4m3x4(f[0], f[1], f[2], f[3]), e4m3x4(f[4], f[5], f[6], f[7]));
 }
 
-// One CTA per (sequence, touched block of sb tokens, run of kv heads); the first 128 threads take K, the others V.
+// One CTA per (sequence, touched block of sb tokens, run of kv heads); the first HALF threads take K, the others V.
 // The block's cosines and sines are made once, in shared memory, by all threads, and serve every head of the run: with
 // a pair of them per head and element the sines alone were half of the instructions.  A thread holds TPT tasks (16
 // columns of a token: the pieces that a rotation pairs) in registers between the block's maximum and the quantisation,
-// so new tokens are read once.  If the scale grows, the block's earlier tokens are requantised in place.
+// so new tokens are read once, the next head's while this one's are worked on.  If the scale grows, the block's earlier
+// tokens are requantised in place.  Reads two bytes per element and writes one; bound by instructions, about 250 per warp
+// and 512 elements (54% of the ALU pipe): 8 ragged prompts of up to 2048 tokens, 8 heads, d = 128 26.5 us (2.9 TB/s);
+// one token of each of 32 sequences 6.1 us, the latency of a launch and four dependent loads.
 struct AppendPlan {
     int blocks, heads, groups;  // blocks of sb tokens that N tokens can touch; kv heads per CTA, and runs of them
     FastDiv page, sb;
 };
 
-template <int D, int TPT, bool INTER>
-__global__ void __launch_bounds__(2 * kHalf, TPT > 2 ? 2 : 4) cache_append_kernel(const CacheAppendLaunch a, const AppendPlan plan) {
+// Threads of an SM: as many as their registers leave without spills (8 sequences of 2048 tokens in blocks of 32: 28.7 us
+// with 768, 33.1 with 1024).
+template <int TPT>
+constexpr int kAppendThreads = TPT > 2 ? 512 : TPT == 2 ? 768 : 1024;
+
+template <int D, int HALF, int TPT, bool INTER>
+__global__ void __launch_bounds__(2 * HALF, kAppendThreads<TPT> / (2 * HALF))
+    cache_append_kernel(const CacheAppendLaunch a, const AppendPlan plan) {
     extern __shared__ __align__(16) float2 s_turn[];  // [token][pair of pairs j < 4][task][2]
-    __shared__ uint32_t s_max[2][2][4];
+    __shared__ uint32_t s_max[2][2][HALF / 32];
     pdl_launch_dependents();
     pdl_wait();
     constexpr int TPR = D / 16;
     const int group = blockIdx.x % plan.groups;
     const int blk = (blockIdx.x / plan.groups) % plan.blocks;
     const int b = blockIdx.x / plan.groups / plan.blocks;
-    const int is_v = threadIdx.x / kHalf, tid = threadIdx.x % kHalf;
+    const int is_v = threadIdx.x / HALF, tid = threadIdx.x % HALF;
     const int cap = a.max_pages * a.page;
     int len = a.lens[b], n = a.new_lens ? a.new_lens[b] : a.N;
     if (len < 0 || len > cap || n < 0 || n > a.N || n > cap - len) {
@@ -107,7 +118,7 @@ __global__ void __launch_bounds__(2 * kHalf, TPT > 2 ? 2 : 4) cache_append_kerne
         const int q = threadIdx.x % 64;  // one pair for each of up to 64 threads, four tokens at a time
         if (q < turned * 8) {
             const uint64_t turns = a.turns[q];
-            for (int tok = t0 + threadIdx.x / 64; tok < t1; tok += 2 * kHalf / 64) {
+            for (int tok = t0 + threadIdx.x / 64; tok < t1; tok += 2 * HALF / 64) {
                 const int pos = a.positions ? a.positions[(long long)b * a.N + first + tok - len] : first + tok;
                 float2 cs;
                 turn_cos_sin(pos, turns, a.magnitude, cs.x, cs.y);
@@ -124,7 +135,7 @@ __global__ void __launch_bounds__(2 * kHalf, TPT > 2 ? 2 : 4) cache_append_kerne
     const float2* cs[TPT];
 #pragma unroll
     for (int i = 0; i < TPT; ++i) {
-        const int task = tid + i * kHalf, tok = task / TPR, p = task % TPR;
+        const int task = tid + i * HALF, tok = task / TPR, p = task % TPR;
         int c0, c1;
         task_columns<INTER>(p, is_v ? 0 : turned * 16, c0, c1);
         apart[i] = tok >= t0 && tok < t1 ? c1 - c0 : 0;
@@ -135,17 +146,26 @@ __global__ void __launch_bounds__(2 * kHalf, TPT > 2 ? 2 : 4) cache_append_kerne
     }
     uint8_t* dst = (is_v ? a.vp : a.kp) + (((long long)pg * a.Hkv + h0) * a.page + at) * D;
     float* sc = (is_v ? a.vs : a.ks) + ((long long)pg * a.Hkv + h0) * nb + plan.sb.div(at);
-    for (int h = h0; h < h1; ++h, dst += (long long)a.page * D, sc += nb) {
-        const float old = t0 > 0 ? *sc : 0.f;
-        uint4 x[TPT], y[TPT];
-        uint32_t big = 0;
+    uint4 nx[TPT], ny[TPT];  // the next head's, loaded while this one's are worked on
+    float nold;
+    auto load = [&](const float* scale) {
+        nold = t0 > 0 ? *scale : 0.f;
 #pragma unroll
         for (int i = 0; i < TPT; ++i)
             if (apart[i]) {
-                x[i] = *reinterpret_cast<const uint4*>(src[i]);
-                y[i] = *reinterpret_cast<const uint4*>(src[i] + apart[i]);
+                nx[i] = *reinterpret_cast<const uint4*>(src[i]);
+                ny[i] = *reinterpret_cast<const uint4*>(src[i] + apart[i]);
                 src[i] += sh;
             }
+    };
+    load(sc);
+    for (int h = h0; h < h1; ++h, dst += (long long)a.page * D, sc += nb) {
+        uint4 x[TPT], y[TPT];
+        const float old = nold;
+        uint32_t big = 0;
+#pragma unroll
+        for (int i = 0; i < TPT; ++i) x[i] = nx[i], y[i] = ny[i];
+        if (h + 1 < h1) load(sc + nb);
 #pragma unroll
         for (int i = 0; i < TPT; ++i) {
             if (!apart[i]) continue;
@@ -164,7 +184,7 @@ __global__ void __launch_bounds__(2 * kHalf, TPT > 2 ? 2 : 4) cache_append_kerne
         const bool pow2 = is_pow2(to) && to <= 1.7e38f;                            // 1 / to is normal
         const float inv = pow2 ? __uint_as_float((254u << 23) - __float_as_uint(to)) : 0.f;
         if (to != old) {
-            for (int i = tid; i < t0 * TPR; i += kHalf) {
+            for (int i = tid; i < t0 * TPR; i += HALF) {
                 uint4* at16 = reinterpret_cast<uint4*>(dst) + i;
                 *at16 = e4m3_rescale16(*at16, old, to);
             }
@@ -184,38 +204,42 @@ __global__ void __launch_bounds__(2 * kHalf, TPT > 2 ? 2 : 4) cache_append_kerne
     }
 }
 
-template <int D, int TPT, bool INTER>
+template <int D, int HALF, int TPT, bool INTER>
 cudaError_t launch_append_dti(const CacheAppendLaunch& a, cudaStream_t s) {
     AppendPlan plan;
     plan.blocks = (a.N + a.sb - 2) / a.sb + 1;
     plan.page = FastDiv((uint32_t)a.page);
     plan.sb = FastDiv((uint32_t)a.sb);
-    // heads per CTA: up to eight share the sines while there are four CTAs for every SM (8 ragged prompts of up to 2048 tokens, 8
-    // heads: 1 head 37.3 us, 2 28.8, 4 28.1, 8 28.0; 32 single tokens of 8 heads: 8.9 us with 8, 6.2 with 1)
-    plan.heads = 8;
-    const long long cells = (long long)a.B * plan.blocks;
-    while (plan.heads > 1 && cells * ((a.Hkv + plan.heads - 1) / plan.heads) < 4ll * a.num_sms) plan.heads /= 2;
+    // kv heads per CTA, which share the sines: the fewest waves of resident CTAs times the work of one, whose start
+    // counts for one and a half heads (8 sequences of 2048 tokens, 8 heads, d = 128: with blocks of 32 tokens 1 head 37.3
+    // us, 2 28.8, 4 28.1, 8 30.3; blocks of 128 tokens 51.3 for 2 heads, 39.0 for 8; 32 single tokens 6.2 for 1, 8.9 for 8)
+    const long long cells = (long long)a.B * plan.blocks, slots = (long long)kAppendThreads<TPT> / (2 * HALF) * a.num_sms;
+    long long best = -1;
+    for (int h = 8; h >= 1; h /= 2) {
+        const long long waves = (cells * ((a.Hkv + h - 1) / h) + slots - 1) / slots, cost = waves * (2 * h + 3);
+        if (best < 0 || cost < best) best = cost, plan.heads = h;
+    }
     plan.groups = (a.Hkv + plan.heads - 1) / plan.heads;
     const long long ctas = cells * plan.groups;
     const int smem = a.turns ? a.sb * (a.rot / 2) * 8 : 0;  // at most 64 KB
-    cudaError_t e = set_smem_limit_once<cache_append_kernel<D, TPT, INTER>>(64 * 1024);
+    cudaError_t e = set_smem_limit_once<cache_append_kernel<D, HALF, TPT, INTER>>(64 * 1024);
     if (e != cudaSuccess) return e;
-    return launch_dependent(cache_append_kernel<D, TPT, INTER>, dim3((unsigned)ctas), dim3(2 * kHalf), (size_t)smem, s, a,
+    return launch_dependent(cache_append_kernel<D, HALF, TPT, INTER>, dim3((unsigned)ctas), dim3(2 * HALF), (size_t)smem, s, a,
                             plan);
 }
 
-template <int D, int TPT>
+template <int D, int HALF, int TPT>
 cudaError_t launch_append_dt(const CacheAppendLaunch& a, cudaStream_t s) {
-    return a.interleaved ? launch_append_dti<D, TPT, true>(a, s) : launch_append_dti<D, TPT, false>(a, s);
+    return a.interleaved ? launch_append_dti<D, HALF, TPT, true>(a, s) : launch_append_dti<D, HALF, TPT, false>(a, s);
 }
 
 template <int D>
 cudaError_t launch_append_d(const CacheAppendLaunch& a, cudaStream_t s) {
-    const int tasks = a.sb * (D / 16);  // of a block, at most 8 per thread (sb <= 128)
-    if (tasks <= kHalf) return launch_append_dt<D, 1>(a, s);
-    if (tasks <= 2 * kHalf) return launch_append_dt<D, 2>(a, s);
-    if (tasks <= 4 * kHalf) return launch_append_dt<D, 4>(a, s);
-    return launch_append_dt<D, 8>(a, s);
+    const int tasks = a.sb * (D / 16);  // of a block (sb <= 128)
+    if (tasks <= 128) return launch_append_dt<D, 128, 1>(a, s);
+    if (tasks <= 256) return launch_append_dt<D, 128, 2>(a, s);
+    if (tasks <= 512) return launch_append_dt<D, 128, 4>(a, s);
+    return launch_append_dt<D, 256, 4>(a, s);
 }
 
 // ------------------------------------------------------------------ eviction
@@ -223,8 +247,9 @@ cudaError_t launch_append_d(const CacheAppendLaunch& a, cudaStream_t s) {
 // index).  A cluster of 1 to 8 CTAs per (sequence, kv head), each with a run of the tokens, whose order-preserving
 // integer keys stay in its registers: four histograms of 8 bits, summed over the cluster's shared memories, find the
 // smallest key that stays and how many equal ones do, and how many of either the CTAs before this one have; a count
-// per warp then gives every kept token its place in index order.  The weights are read once.  (Three histograms of 11,
-// 11 and 10 bits moved eight times the bins between the CTAs: @@.)
+// per warp then gives every kept token its place in index order.  The weights are read once.  Bound by latency: four
+// rounds of shared-memory atomics and of exchange between the CTAs, 15 us for one sequence of 64k tokens, whose eviction
+// takes 26.7 us (32.0 with three histograms of 11, 11 and 10 bits, which move six times the bins).
 constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32, kSelBins = 256, kSelCtas = 8;
 
 // Integer whose order is the float's, with -0 = +0 and NaN above everything.
@@ -397,11 +422,17 @@ __global__ void __launch_bounds__(kSelThreads, PER > 8 ? 1 : 2) evict_select_ker
     if (ctas > 1) cluster_wait();  // the others have read this CTA's
 }
 
-// Moves the kept tokens, a block of sb of them per turn of a CTA: K by the first 128 threads, V by the others.  The
+// Moves the kept tokens, a block of sb of them per turn of a CTA: K by the first HALF threads, V by the others.  The
 // block's scale is the largest of its tokens' source scales; tokens that came with that scale are copied byte for byte.
 // Reading a token takes three loads that depend on each other (its index, its page, its row), so the CTAs are resident
-// ones that run over the blocks with the index two blocks ahead and the page one block ahead of the row.
-constexpr int kMoveCtas = 4;  // per SM (the eviction of 32 sequences of 4096 tokens, 8 heads: 3 CTAs 46.8 us, 4 44.9, 6 54.6)
+// ones that run over the blocks with the index two blocks ahead and the page one block ahead of the row.  Bound by HBM:
+// 134 MB for 1024 of 4096 tokens of 32 sequences of 8 heads in 26 us, 5.2 TB/s.
+// Threads of an SM, by the pieces that one holds (the eviction of 32 sequences of 4096 tokens, 8 heads, d = 128: blocks
+// of 64 tokens 45.1 us with 512, 38.9 with 768, 36.8 with 1024, 41.7 with 1280; blocks of 16 49.3 with 1024, 43.2 with
+// 1536, 43.0 with 2048; 4 sequences of 16k tokens, blocks of 32: 29.1 with 768, 27.8 with 1024, 26.7 with 1536).
+template <int TPT>
+constexpr int kMoveThreads = TPT == 1 ? 2048 : TPT == 2 ? 1536 : 1024;
+
 
 struct MovePlan {
     int blocks, step_bh, step_blk;  // blocks per (sequence, kv head); the grid's size as (sequence, kv head)s and blocks
@@ -409,13 +440,14 @@ struct MovePlan {
     FastDiv page, sb, heads;
 };
 
-template <int D, int TPT>
-__global__ void __launch_bounds__(2 * kHalf, kMoveCtas) evict_move_kernel(const CacheEvictLaunch a, const MovePlan plan) {
-    __shared__ uint32_t s_max[2][2][4];
+template <int D, int HALF, int TPT>
+__global__ void __launch_bounds__(2 * HALF, kMoveThreads<TPT> / (2 * HALF))
+    evict_move_kernel(const CacheEvictLaunch a, const MovePlan plan) {
+    __shared__ uint32_t s_max[2][2][HALF / 32];
     pdl_launch_dependents();
     pdl_wait();
     constexpr int TPR = D / 16;
-    const int is_v = threadIdx.x / kHalf, tid = threadIdx.x % kHalf;
+    const int is_v = threadIdx.x / HALF, tid = threadIdx.x % HALF;
     const int ncap = a.new_max_pages * a.page, bpp = (int)plan.sb.div(a.page);
     uint8_t* pool = is_v ? a.vp : a.kp;
     float* scales = is_v ? a.vs : a.ks;
@@ -433,7 +465,7 @@ __global__ void __launch_bounds__(2 * kHalf, kMoveCtas) evict_move_kernel(const 
         const int* list = a.kept + (long long)it.bh * ncap + first;
 #pragma unroll
         for (int i = 0; i < TPT; ++i) {
-            const int tok = (tid + i * kHalf) / TPR;
+            const int tok = (tid + i * HALF) / TPR;
             kept[i] = it.bh < plan.bhs && tok < a.sb && first + tok < ncap ? list[tok] : -1;
         }
     };
@@ -469,7 +501,7 @@ __global__ void __launch_bounds__(2 * kHalf, kMoveCtas) evict_move_kernel(const 
             const uint32_t o = kept[i] - plan.page.div(kept[i]) * a.page;
             const uint32_t head = (uint32_t)page[i] * a.Hkv + h;  // rows are counted in 32 bits
             sc[i] = scales[head * bpp + plan.sb.div(o)];
-            x[i] = *reinterpret_cast<const uint4*>(pool + (size_t)(head * a.page + o) * D + (tid + i * kHalf) % TPR * 16);
+            x[i] = *reinterpret_cast<const uint4*>(pool + (size_t)(head * a.page + o) * D + (tid + i * HALF) % TPR * 16);
         }
         // the stages of the blocks behind this one
         int kept2[TPT], page1[TPT], to_page1;
@@ -490,7 +522,7 @@ __global__ void __launch_bounds__(2 * kHalf, kMoveCtas) evict_move_kernel(const 
                 if (tid == 0) scales[head * bpp + plan.sb.div(at)] = to;
 #pragma unroll
                 for (int i = 0; i < TPT; ++i)
-                    if (kept[i] >= 0) dst[tid + i * kHalf] = sc[i] == to ? x[i] : e4m3_rescale16(x[i], sc[i], to);
+                    if (kept[i] >= 0) dst[tid + i * HALF] = sc[i] == to ? x[i] : e4m3_rescale16(x[i], sc[i], to);
             } else if (tid == 0) {
                 record_invalid(a.err, kSiteCacheTable, to_page);
             }
@@ -507,7 +539,7 @@ __global__ void __launch_bounds__(2 * kHalf, kMoveCtas) evict_move_kernel(const 
     }
 }
 
-template <int D, int TPT>
+template <int D, int HALF, int TPT>
 cudaError_t launch_move_t(const CacheEvictLaunch& a, cudaStream_t s) {
     MovePlan plan;
     plan.blocks = (a.keep + a.sb - 1) / a.sb;
@@ -515,20 +547,20 @@ cudaError_t launch_move_t(const CacheEvictLaunch& a, cudaStream_t s) {
     plan.page = FastDiv((uint32_t)a.page);
     plan.sb = FastDiv((uint32_t)a.sb);
     plan.heads = FastDiv((uint32_t)a.Hkv);
-    const long long items = (long long)plan.bhs * plan.blocks, most = (long long)kMoveCtas * a.num_sms;
+    const long long items = (long long)plan.bhs * plan.blocks, most = (long long)kMoveThreads<TPT> / (2 * HALF) * a.num_sms;
     const int grid = (int)(items < most ? items : most);
     plan.step_bh = grid / plan.blocks;
     plan.step_blk = grid % plan.blocks;
-    return launch_dependent(evict_move_kernel<D, TPT>, dim3(grid), dim3(2 * kHalf), 0, s, a, plan);
+    return launch_dependent(evict_move_kernel<D, HALF, TPT>, dim3(grid), dim3(2 * HALF), 0, s, a, plan);
 }
 
 template <int D>
 cudaError_t launch_move(const CacheEvictLaunch& a, cudaStream_t s) {
     const int tasks = a.sb * (D / 16);
-    if (tasks <= kHalf) return launch_move_t<D, 1>(a, s);
-    if (tasks <= 2 * kHalf) return launch_move_t<D, 2>(a, s);
-    if (tasks <= 4 * kHalf) return launch_move_t<D, 4>(a, s);
-    return launch_move_t<D, 8>(a, s);
+    if (tasks <= 128) return launch_move_t<D, 128, 1>(a, s);
+    if (tasks <= 256) return launch_move_t<D, 128, 2>(a, s);
+    if (tasks <= 512) return launch_move_t<D, 128, 4>(a, s);
+    return launch_move_t<D, 256, 4>(a, s);
 }
 
 }  // namespace
@@ -556,7 +588,7 @@ cudaError_t launch_cache_evict(const CacheEvictLaunch& a, cudaStream_t s) {
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     // keys in registers: 8 per thread leave two CTAs per SM (32 sequences of 4096 tokens, 8 heads: 45 us; 32 registers 55,
-    // none 51), 32 save a long sequence the second and third read (64k tokens: 32 us; none 51)
+    // none 51), 32 save a long sequence the reads of later rounds (64k tokens: 32 us; none 51)
     cudaError_t e = per <= 8    ? cudaLaunchKernelEx(&cfg, evict_select_kernel<8>, a, ctas)
                     : per <= 32 ? cudaLaunchKernelEx(&cfg, evict_select_kernel<32>, a, ctas)
                                 : cudaLaunchKernelEx(&cfg, evict_select_kernel<0>, a, ctas);
