@@ -906,7 +906,7 @@ def run_ours(args, rank, world, local_rank):
 
 # ------------------------------------------------------------------ one kernel for a profiler
 PROFILE_TARGETS = ("fwd", "dkdv", "dq", "fused", "pair", "window", "decode", "decode64", "paged", "paged48",
-                   "paged20", "fp8")
+                   "paged20", "fp8", "rope", "append", "decode_fp8", "evict")
 
 
 def run_profile(target, launches):
@@ -917,8 +917,10 @@ def run_profile(target, launches):
     B=32, H=32, Nk=4096 (d=128 or d=64); paged at B=32, Hq=32, Hkv=8, page 16 (the
     tensor-core kernel), paged48 with 48-token pages, 85 per sequence (4080 tokens:
     the tensor-core kernel in 16-row boxes) and paged20 with 20-token pages, 204 per
-    sequence (4080 tokens: the general kernel); fp8 the FP8 forward.  Prints one
-    line; no timing."""
+    sequence (4080 tokens: the general kernel); fp8 the FP8 forward; rope 8192
+    tokens of 32 heads; append (2048 tokens per sequence, rotated), decode_fp8 and
+    evict (1024 tokens stay) the cache held in 8 bits, at B=32, Hq=32, Hkv=8,
+    Nk=4096, page 64.  Prints one line; no timing."""
     import torch
     import exact_tiled_attention_21_gb300 as fa
     dev = torch.device("cuda", 0)
@@ -965,6 +967,28 @@ def run_profile(target, launches):
         ws = torch.empty(fa.fa_decode_paged_workspace_bytes(DEC_B, DEC_H, D, 0), dtype=torch.uint8, device=dev)
         call = lambda: fa.fa_decode_paged(qd, kp, vp, table, lens, od, lsed, DEC_B, DEC_H, hkv, page, DEC_NK // page,
                                           npages, D, SCALE, 0, ws, ws.numel(), s)
+    elif target == "rope":
+        x = rnd(1, N, H, D).transpose(1, 2)
+        turns = fa.rope_table(fa.rope_frequencies(D)[0], dev)
+        call = lambda: fa.rope(x, turns, out=o)
+        o = torch.empty(1, H, N, D, dtype=torch.bfloat16, device=dev)
+    elif target in ("append", "decode_fp8", "evict"):
+        hkv, page, keep, new = 8, 64, 1024, 2048
+        used, room = DEC_B * (DEC_NK // page), DEC_B * (keep // page)
+        kp, vp = (torch.randint(0, 126, (used + room, hkv, page, D), generator=g, device=dev, dtype=torch.uint8)
+                  for _ in range(2))
+        ks, vs = (torch.full((used + room, hkv, 1), 1.0 / 64, device=dev) for _ in range(2))
+        order = torch.randperm(used + room, generator=torch.Generator().manual_seed(5)).to(torch.int32).to(dev)
+        table, new_table = order[:used].reshape(DEC_B, -1), order[used:].reshape(DEC_B, -1)
+        lens = torch.full((DEC_B,), DEC_NK, dtype=torch.int32, device=dev)
+        kn, vn, qd = rnd(DEC_B, hkv, new, D), rnd(DEC_B, hkv, new, D), rnd(DEC_B, DEC_H, 1, D)
+        w = torch.rand(DEC_B, hkv, DEC_NK, generator=g, device=dev)
+        turns = fa.rope_table(fa.rope_frequencies(D)[0], dev)
+        call = {
+            "append": lambda: fa.cache_append_fp8(kn, vn, kp, vp, ks, vs, table, lens - new, turns=turns),
+            "decode_fp8": lambda: fa.decode_paged_fp8(qd, kp, vp, ks, vs, table, lens),
+            "evict": lambda: fa.cache_evict_fp8(kp, vp, ks, vs, table, lens, w, new_table, keep, 128),
+        }[target]
     else:  # fp8
         mk = lambda: torch.randint(0, 126, (1, H, N, D), generator=torch.Generator().manual_seed(7),
                                    dtype=torch.int32).to(torch.uint8).to(dev)
