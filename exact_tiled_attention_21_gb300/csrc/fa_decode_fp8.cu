@@ -765,66 +765,73 @@ __global__ void __launch_bounds__(kFinishThreads) finish_fp8_kernel(const Params
     }
 }
 
-// weights[j] += sum over the rows of 2^(x_j - LSE), in a fixed order.  A thread takes four pieces of 16 bytes of scores.
-// With 4, 8, 16 or 32 rows (VEC) a token's scores are 1, 2, 4 or 8 lanes' pieces; otherwise a thread takes whole tokens
-// (that for all: a decode of 32 sequences of 4096 tokens, 8 kv heads, 4 rows 71.6 us against 70.4).
-constexpr int kWeightThreads = 256, kPieces = 4;
+// weights[j] += sum over the rows of 2^(x_j - LSE), in a fixed order.  A block takes up to 1024 tokens, row tile after row
+// tile.  With 4, 8, 16 or 32 rows in a tile a token's scores are 16-byte pieces of 1, 2, 4 or 8 lanes; else a thread reads
+// its token's.  (That for all: 7 sequences of 30000 tokens, 2 kv heads, 80 rows 119 us against 31, 4.4 TB/s; with 4 rows,
+// 32 sequences of 4096 tokens, 8 kv heads, the whole decode 71.6 us against 70.4.)
+constexpr int kWeightThreads = 256, kPart = 4096, kPieces = kPart / 4 / kWeightThreads;  // scores of a block and tile
 
-template <int ROWS, bool VEC>
-__global__ void __launch_bounds__(kWeightThreads) weights_fp8_kernel(const Params a, int blocks) {
+template <int ROWS>
+__global__ void __launch_bounds__(kWeightThreads) weights_fp8_kernel(const Params a, int blocks, int tokens) {
+    __shared__ float s_sum[kPart / 4];
     pdl_launch_dependents();
     pdl_wait();
+    const int tid = threadIdx.x, cap = a.max_pages * (int)a.page.d;
     const long long bh = blockIdx.x / blocks;
-    const int cap = a.max_pages * (int)a.page.d, len = clamp_len(a.lens[bh / a.Hkv], cap), tid = threadIdx.x;
-    const int lanes = VEC ? a.rows / 4 : 1, per = kWeightThreads / lanes;  // lanes per token, tokens per piece of the block
-    const int begin = (int)(blockIdx.x % blocks) * per * kPieces, first = begin + tid / lanes;
-    if (begin >= len) return;
-    float* weights = a.weights + bh * cap;
-    const float* lse2 = a.lse2 + bh * a.rows;
-    float sum[kPieces], before[kPieces];
-    if constexpr (VEC) {
-        const float* scores = a.scores + scores_at<ROWS>(a, bh, 0, cap) + tid % lanes * 4;
-        float4 x[kPieces];
+    const int len = clamp_len(a.lens[bh / a.Hkv], cap), begin = (int)(blockIdx.x % blocks) * tokens;
+    const int many = min(tokens, len - begin);
+    if (many <= 0) return;
+    float* weights = a.weights + bh * cap + begin;
+    float before[kPieces];
 #pragma unroll
-        for (int q = 0; q < kPieces; ++q) {
-            const int j = first + q * per;
-            if (j >= cap) continue;  // (behind the sequence's end: read, not used)
-            x[q] = *reinterpret_cast<const float4*>(scores + (long long)j * a.rows);
-            before[q] = weights[j];
-        }
-        float4 z = *reinterpret_cast<const float4*>(lse2 + tid % lanes * 4);
-        if (z.x == -INFINITY) z.x = INFINITY;  // a row without keys: every weight 2^-inf = 0
-        if (z.y == -INFINITY) z.y = INFINITY;
-        if (z.z == -INFINITY) z.z = INFINITY;
-        if (z.w == -INFINITY) z.w = INFINITY;
+    for (int q = 0; q < kPieces; ++q)
+        if (tid + q * kWeightThreads < many) before[q] = weights[tid + q * kWeightThreads];
+    for (int rt = 0; rt < a.row_tiles; ++rt) {
+        const int nrows = min(ROWS, a.rows - rt * ROWS);
+        const float* scores = a.scores + scores_at<ROWS>(a, bh, rt, cap) + (long long)begin * nrows;
+        const float* lse2 = a.lse2 + bh * a.rows + rt * ROWS;
+        const bool vec = nrows >= 4 && (nrows & (nrows - 1)) == 0;
+        const int lanes = vec ? nrows / 4 : 1, shift = __ffs(lanes) - 1, lane = tid & (lanes - 1);
+        float sum[kPieces] = {};
+        if (vec) {
+            float4 x[kPieces];
 #pragma unroll
-        for (int q = 0; q < kPieces; ++q) {
-            sum[q] = (ex2(x[q].x - z.x) + ex2(x[q].y - z.y)) + (ex2(x[q].z - z.z) + ex2(x[q].w - z.w));
-            for (int w = lanes / 2; w >= 1; w >>= 1) sum[q] += __shfl_xor_sync(0xffffffffu, sum[q], w);
-        }
-    } else {
+            for (int q = 0; q < kPieces; ++q)
+                if ((tid + q * kWeightThreads) >> shift < many)
+                    x[q] = reinterpret_cast<const float4*>(scores)[tid + q * kWeightThreads];
+            float z[4];
 #pragma unroll
-        for (int q = 0; q < kPieces; ++q) {
-            sum[q] = 0.f;
-            before[q] = first + q * per < len ? weights[first + q * per] : 0.f;
-        }
-        for (int rt = 0; rt < a.row_tiles; ++rt) {
-            const int nrows = min(ROWS, a.rows - rt * ROWS);
-            const float* scores = a.scores + scores_at<ROWS>(a, bh, rt, cap);
+            for (int i = 0; i < 4; ++i) {
+                const float l = lse2[lane * 4 + i];
+                z[i] = l == -INFINITY ? INFINITY : l;  // a row without keys: every weight 2^-inf = 0
+            }
+#pragma unroll
+            for (int q = 0; q < kPieces; ++q) {
+                sum[q] = (ex2(x[q].x - z[0]) + ex2(x[q].y - z[1])) + (ex2(x[q].z - z[2]) + ex2(x[q].w - z[3]));
+                for (int w = lanes / 2; w >= 1; w >>= 1) sum[q] += __shfl_xor_sync(0xffffffffu, sum[q], w);
+            }
+        } else {
             for (int r = 0; r < nrows; ++r) {
-                const float l = lse2[rt * ROWS + r], z = l == -INFINITY ? INFINITY : l;
+                const float l = lse2[r], z = l == -INFINITY ? INFINITY : l;
 #pragma unroll
                 for (int q = 0; q < kPieces; ++q) {
-                    const int j = first + q * per;
-                    if (j < len) sum[q] += ex2(scores[(long long)j * nrows + r] - z);
+                    const int j = tid + q * kWeightThreads;
+                    if (j < many) sum[q] += ex2(scores[j * nrows + r] - z);
                 }
             }
         }
+        if (rt > 0) __syncthreads();
+#pragma unroll
+        for (int q = 0; q < kPieces; ++q) {
+            const int j = (tid + q * kWeightThreads) >> shift;
+            if (lane == 0 && j < many) s_sum[j] = rt > 0 ? s_sum[j] + sum[q] : sum[q];
+        }
     }
+    __syncthreads();
 #pragma unroll
     for (int q = 0; q < kPieces; ++q) {
-        const int j = first + q * per;
-        if (j < len && tid % lanes == 0) weights[j] = before[q] + sum[q];
+        const int j = tid + q * kWeightThreads;
+        if (j < many) weights[j] = before[q] + s_sum[j];
     }
 }
 
@@ -871,11 +878,11 @@ cudaError_t launch_d(const PagedDecodeFp8Launch& a, cudaStream_t s) {
     const long long row_blocks = bh * p.rows;
     e = launch_dependent(finish_fp8_kernel<D, ROWS>, dim3((unsigned)row_blocks), dim3(kFinishThreads), 0, s, p);
     if (e != cudaSuccess || !a.weights) return e;
-    const bool vec = p.rows == 4 || p.rows == 8 || p.rows == 16 || p.rows == 32;
-    const int tokens = kWeightThreads * kPieces / (vec ? p.rows / 4 : 1), blocks = (cap + tokens - 1) / tokens;
-    const dim3 grid((unsigned)(bh * blocks)), block(kWeightThreads);
-    return vec ? launch_dependent(weights_fp8_kernel<ROWS, true>, grid, block, 0, s, p, blocks)
-               : launch_dependent(weights_fp8_kernel<ROWS, false>, grid, block, 0, s, p, blocks);
+    int tokens = kPart / 4;  // of a block: as many as its rows leave room for
+    while (tokens * std::min(p.rows, ROWS) > kPart) tokens /= 2;
+    const int blocks = (cap + tokens - 1) / tokens;
+    return launch_dependent(weights_fp8_kernel<ROWS>, dim3((unsigned)(bh * blocks)), dim3(kWeightThreads), 0, s, p, blocks,
+                            tokens);
 }
 
 template <int D, int ROWS>
