@@ -8,6 +8,8 @@
 // only exponents, so a token's bytes do not depend on which later tokens raised
 // its block's scale (unless they become subnormal); e4m3's relative step
 // is the same at every scale, so nothing is lost against amax / 448 either.
+#include <algorithm>
+
 #include "fa_e4m3.cuh"
 #include "fa_internal.h"
 #include "fa_rope.cuh"
@@ -24,6 +26,18 @@ __device__ __forceinline__ uint32_t half_max(uint32_t v, uint32_t (&s)[2][W], in
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < W; ++i) v = max(v, s[w][i]);
+    return v;
+}
+
+// The same over the threads of a block of sb tokens, where a half holds several and every token has TPR threads: `token`
+// is the thread's and `first` its block's first one.
+template <int W, int TPR>
+__device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t (&s)[2][32 * W / TPR], int w, int token, int first, int sb) {
+#pragma unroll
+    for (int d = 1; d < TPR; d <<= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, d));
+    s[w][token] = v;
+    __syncthreads();
+    for (int i = first; i < min(first + sb, 32 * W / TPR); ++i) v = max(v, s[w][i]);
     return v;
 }
 
@@ -67,7 +81,9 @@ __device__ __forceinline__ uint2 quantise8(uint4 x, float inv, float s, bool pow
     return make_uint2(e4m3x4(f[0], f[1], f[2], f[3]), e4m3x4(f[4], f[5], f[6], f[7]));
 }
 
-// One CTA per (sequence, touched block of sb tokens, run of kv heads); the first HALF threads take K, the others V.
+// One CTA per (sequence, touched block of sb tokens, run of kv heads); the first HALF threads take K, the others V.  Of
+// blocks too small for 128 threads a CTA takes several (one with blocks of 4 tokens, 17 sequences of 5624 tokens, 1 head:
+// 101 us against 44).
 // The block's cosines and sines are made once, in shared memory, by all threads, and serve every head of the run: with
 // a pair of them per head and element the sines alone were half of the instructions.  A thread holds TPT tasks (16
 // columns of a token: the pieces that a rotation pairs) in registers between the block's maximum and the quantisation,
@@ -76,7 +92,7 @@ __device__ __forceinline__ uint2 quantise8(uint4 x, float inv, float s, bool pow
 // and 512 elements (54% of the ALU pipe): 8 ragged prompts of up to 2048 tokens, 8 heads, d = 128 26.5 us (2.9 TB/s);
 // one token of each of 32 sequences 6.1 us, the latency of a launch and four dependent loads.
 struct AppendPlan {
-    int blocks, heads, groups;  // blocks of sb tokens that N tokens can touch; kv heads per CTA, and runs of them
+    int unit, units, heads, groups;  // blocks per CTA, and runs of them that N tokens can touch; the same of kv heads
     FastDiv page, sb;
 };
 
@@ -85,17 +101,18 @@ struct AppendPlan {
 template <int TPT>
 constexpr int kAppendThreads = TPT > 2 ? 512 : TPT == 2 ? 768 : 1024;
 
-template <int D, int HALF, int TPT, bool INTER>
+// SEV: the CTA has several blocks (of HALF threads or fewer in all, one task each).
+template <int D, int HALF, int TPT, bool SEV, bool INTER>
 __global__ void __launch_bounds__(2 * HALF, kAppendThreads<TPT> / (2 * HALF))
     cache_append_kernel(const CacheAppendLaunch a, const AppendPlan plan) {
     extern __shared__ __align__(16) float2 s_turn[];  // [token][pair of pairs j < 4][task][2]
-    __shared__ uint32_t s_max[2][2][HALF / 32];
+    constexpr int TPR = D / 16;
+    __shared__ uint32_t s_max[2][2][HALF / 32], s_block[2][2][SEV ? HALF / TPR : 1];
     pdl_launch_dependents();
     pdl_wait();
-    constexpr int TPR = D / 16;
     const int group = blockIdx.x % plan.groups;
-    const int blk = (blockIdx.x / plan.groups) % plan.blocks;
-    const int b = blockIdx.x / plan.groups / plan.blocks;
+    const int unit = (blockIdx.x / plan.groups) % plan.units;
+    const int b = blockIdx.x / plan.groups / plan.units;
     const int is_v = threadIdx.x / HALF, tid = threadIdx.x % HALF;
     const int cap = a.max_pages * a.page;
     int len = a.lens[b], n = a.new_lens ? a.new_lens[b] : a.N;
@@ -104,16 +121,21 @@ __global__ void __launch_bounds__(2 * HALF, kAppendThreads<TPT> / (2 * HALF))
         len = min(max(len, 0), cap);
         n = min(min(max(n, 0), a.N), cap - len);
     }
-    const int first = ((int)plan.sb.div(len) + blk) * a.sb;  // the block's first token
+    const int first = ((int)plan.sb.div(len) + unit * plan.unit) * a.sb;  // the CTA's first token
     if (first >= len + n) return;
-    const int lpage = (int)plan.page.div(first), at = first - lpage * a.page;  // logical page, token within it
+    const int t0 = max(len - first, 0), t1 = min(plan.unit * a.sb, len + n - first);  // its new tokens [t0, t1)
+    // the thread's block: its first token (of the CTA's), the earlier tokens in it, its page and place in it
+    const int own = SEV ? (int)plan.sb.div(tid / TPR) * a.sb : 0, begin = first + own;
+    const int earlier = max(t0 - own, 0);
+    bool mine = !SEV || own < t1;
+    const int lpage = mine ? (int)plan.page.div(begin) : 0, at = mine ? begin - lpage * a.page : 0;
     const int pg = a.table[(long long)b * a.max_pages + lpage];
-    if ((unsigned)pg >= (unsigned)a.num_pages) {
-        if (threadIdx.x == 0) record_invalid(a.err, kSiteCacheTable, pg);
-        return;
+    if (mine && (unsigned)pg >= (unsigned)a.num_pages) {
+        if (threadIdx.x == own * TPR) record_invalid(a.err, kSiteCacheTable, pg);
+        if (!SEV) return;
+        mine = false;
     }
-    const int t0 = max(len - first, 0), t1 = min(a.sb, len + n - first);  // new tokens [t0, t1) of the block
-    const int turned = a.turns ? a.rot / 16 : 0;                          // tasks of a row that rotate
+    const int turned = a.turns ? a.rot / 16 : 0;  // tasks of a row that rotate
     if (turned) {
         const int q = threadIdx.x % 64;  // one pair for each of up to 64 threads, four tokens at a time
         if (q < turned * 8) {
@@ -138,8 +160,8 @@ __global__ void __launch_bounds__(2 * HALF, kAppendThreads<TPT> / (2 * HALF))
         const int task = tid + i * HALF, tok = task / TPR, p = task % TPR;
         int c0, c1;
         task_columns<INTER>(p, is_v ? 0 : turned * 16, c0, c1);
-        apart[i] = tok >= t0 && tok < t1 ? c1 - c0 : 0;
-        out[i] = tok * D + c0;
+        apart[i] = (!SEV || mine) && tok >= t0 && tok < t1 ? c1 - c0 : 0;
+        out[i] = (tok - own) * D + c0;
         src[i] = (is_v ? (const __nv_bfloat16*)a.v + b * a.vb : (const __nv_bfloat16*)a.k + b * a.kb) +
                  (first + tok - len) * sn + h0 * sh + c0;
         cs[i] = !is_v && p < turned ? s_turn + (tok * 4 * turned + p) * 2 : nullptr;
@@ -149,7 +171,7 @@ __global__ void __launch_bounds__(2 * HALF, kAppendThreads<TPT> / (2 * HALF))
     uint4 nx[TPT], ny[TPT];  // the next head's, loaded while this one's are worked on
     float nold;
     auto load = [&](const float* scale) {
-        nold = t0 > 0 ? *scale : 0.f;
+        nold = (!SEV || mine) && earlier > 0 ? *scale : 0.f;
 #pragma unroll
         for (int i = 0; i < TPT; ++i)
             if (apart[i]) {
@@ -180,15 +202,19 @@ __global__ void __launch_bounds__(2 * HALF, kAppendThreads<TPT> / (2 * HALF))
             }
             big = max(big, abs_max(x[i], y[i]));
         }
-        const float to = fmaxf(old, scale_for(half_max(big, s_max[h & 1], is_v)));  // all threads have read the old scale
-        const bool pow2 = is_pow2(to) && to <= 1.7e38f;                            // 1 / to is normal
+        if constexpr (SEV)
+            big = block_max<HALF / 32, TPR>(big, s_block[h & 1], is_v, tid / TPR, own, a.sb);
+        else
+            big = half_max(big, s_max[h & 1], is_v);
+        const float to = fmaxf(old, scale_for(big));     // all threads have read the old scale
+        const bool pow2 = is_pow2(to) && to <= 1.7e38f;  // 1 / to is normal
         const float inv = pow2 ? __uint_as_float((254u << 23) - __float_as_uint(to)) : 0.f;
-        if (to != old) {
-            for (int i = tid; i < t0 * TPR; i += HALF) {
+        if ((!SEV || mine) && to != old) {
+            for (int i = tid - own * TPR; i < earlier * TPR; i += HALF) {
                 uint4* at16 = reinterpret_cast<uint4*>(dst) + i;
                 *at16 = e4m3_rescale16(*at16, old, to);
             }
-            if (tid == 0) *sc = to;
+            if (tid == own * TPR) *sc = to;
         }
 #pragma unroll
         for (int i = 0; i < TPT; ++i) {
@@ -204,16 +230,18 @@ __global__ void __launch_bounds__(2 * HALF, kAppendThreads<TPT> / (2 * HALF))
     }
 }
 
-template <int D, int HALF, int TPT, bool INTER>
+template <int D, int HALF, int TPT, bool SEV, bool INTER>
 cudaError_t launch_append_dti(const CacheAppendLaunch& a, cudaStream_t s) {
     AppendPlan plan;
-    plan.blocks = (a.N + a.sb - 2) / a.sb + 1;
+    const int blocks = (a.N + a.sb - 2) / a.sb + 1;  // that N tokens can touch
+    plan.unit = SEV ? std::min(HALF / (a.sb * (D / 16)), blocks) : 1;
+    plan.units = (blocks + plan.unit - 1) / plan.unit;
     plan.page = FastDiv((uint32_t)a.page);
     plan.sb = FastDiv((uint32_t)a.sb);
     // kv heads per CTA, which share the sines: the fewest waves of resident CTAs times the work of one, whose start
     // counts for one and a half heads (8 sequences of 2048 tokens, 8 heads, d = 128: with blocks of 32 tokens 1 head 37.3
     // us, 2 28.8, 4 28.1, 8 30.3; blocks of 128 tokens 51.3 for 2 heads, 39.0 for 8; 32 single tokens 6.2 for 1, 8.9 for 8)
-    const long long cells = (long long)a.B * plan.blocks, slots = (long long)kAppendThreads<TPT> / (2 * HALF) * a.num_sms;
+    const long long cells = (long long)a.B * plan.units, slots = (long long)kAppendThreads<TPT> / (2 * HALF) * a.num_sms;
     long long best = -1;
     for (int h = 8; h >= 1; h /= 2) {
         const long long waves = (cells * ((a.Hkv + h - 1) / h) + slots - 1) / slots, cost = waves * (2 * h + 3);
@@ -221,25 +249,27 @@ cudaError_t launch_append_dti(const CacheAppendLaunch& a, cudaStream_t s) {
     }
     plan.groups = (a.Hkv + plan.heads - 1) / plan.heads;
     const long long ctas = cells * plan.groups;
-    const int smem = a.turns ? a.sb * (a.rot / 2) * 8 : 0;  // at most 64 KB
-    cudaError_t e = set_smem_limit_once<cache_append_kernel<D, HALF, TPT, INTER>>(64 * 1024);
+    const int smem = a.turns ? plan.unit * a.sb * (a.rot / 2) * 8 : 0;  // at most 64 KB
+    cudaError_t e = set_smem_limit_once<cache_append_kernel<D, HALF, TPT, SEV, INTER>>(64 * 1024);
     if (e != cudaSuccess) return e;
-    return launch_dependent(cache_append_kernel<D, HALF, TPT, INTER>, dim3((unsigned)ctas), dim3(2 * HALF), (size_t)smem, s, a,
+    return launch_dependent(cache_append_kernel<D, HALF, TPT, SEV, INTER>, dim3((unsigned)ctas), dim3(2 * HALF), (size_t)smem, s, a,
                             plan);
 }
 
-template <int D, int HALF, int TPT>
+template <int D, int HALF, int TPT, bool SEV>
 cudaError_t launch_append_dt(const CacheAppendLaunch& a, cudaStream_t s) {
-    return a.interleaved ? launch_append_dti<D, HALF, TPT, true>(a, s) : launch_append_dti<D, HALF, TPT, false>(a, s);
+    return a.interleaved ? launch_append_dti<D, HALF, TPT, SEV, true>(a, s)
+                         : launch_append_dti<D, HALF, TPT, SEV, false>(a, s);
 }
 
 template <int D>
 cudaError_t launch_append_d(const CacheAppendLaunch& a, cudaStream_t s) {
     const int tasks = a.sb * (D / 16);  // of a block (sb <= 128)
-    if (tasks <= 128) return launch_append_dt<D, 128, 1>(a, s);
-    if (tasks <= 256) return launch_append_dt<D, 128, 2>(a, s);
-    if (tasks <= 512) return launch_append_dt<D, 128, 4>(a, s);
-    return launch_append_dt<D, 256, 4>(a, s);
+    if (tasks <= 64) return launch_append_dt<D, 128, 1, true>(a, s);
+    if (tasks <= 128) return launch_append_dt<D, 128, 1, false>(a, s);
+    if (tasks <= 256) return launch_append_dt<D, 128, 2, false>(a, s);
+    if (tasks <= 512) return launch_append_dt<D, 128, 4, false>(a, s);
+    return launch_append_dt<D, 256, 4, false>(a, s);
 }
 
 // ------------------------------------------------------------------ eviction
@@ -422,7 +452,8 @@ __global__ void __launch_bounds__(kSelThreads, PER > 8 ? 1 : 2) evict_select_ker
     if (ctas > 1) cluster_wait();  // the others have read this CTA's
 }
 
-// Moves the kept tokens, a block of sb of them per turn of a CTA: K by the first HALF threads, V by the others.  The
+// Moves the kept tokens, a block of sb of them per turn of a CTA (of small blocks several: with blocks of 4 tokens, 7
+// sequences of 4681 kept tokens, 8 heads, one takes 103 us against 50): K by the first HALF threads, V by the others.  A
 // block's scale is the largest of its tokens' source scales; tokens that came with that scale are copied byte for byte.
 // Reading a token takes three loads that depend on each other (its index, its page, its row), so the CTAs are resident
 // ones that run over the blocks with the index two blocks ahead and the page one block ahead of the row.  Bound by HBM:
@@ -430,55 +461,57 @@ __global__ void __launch_bounds__(kSelThreads, PER > 8 ? 1 : 2) evict_select_ker
 // Threads of an SM, by the pieces that one holds (the eviction of 32 sequences of 4096 tokens, 8 heads, d = 128: blocks
 // of 64 tokens 45.1 us with 512, 38.9 with 768, 36.8 with 1024, 41.7 with 1280; blocks of 16 49.3 with 1024, 43.2 with
 // 1536, 43.0 with 2048; 4 sequences of 16k tokens, blocks of 32: 29.1 with 768, 27.8 with 1024, 26.7 with 1536).
-template <int TPT>
-constexpr int kMoveThreads = TPT == 1 ? 2048 : TPT == 2 ? 1536 : 1024;
-
+template <int TPT, bool SEV>
+constexpr int kMoveThreads = SEV ? 1536 : TPT == 1 ? 2048 : TPT == 2 ? 1536 : 1024;
 
 struct MovePlan {
-    int blocks, step_bh, step_blk;  // blocks per (sequence, kv head); the grid's size as (sequence, kv head)s and blocks
+    int unit, units;          // tokens per turn, and turns per (sequence, kv head)
+    int step_bh, step_units;  // the grid's size as (sequence, kv head)s and turns
     int bhs;
     FastDiv page, sb, heads;
 };
 
-template <int D, int HALF, int TPT>
-__global__ void __launch_bounds__(2 * HALF, kMoveThreads<TPT> / (2 * HALF))
+template <int D, int HALF, int TPT, bool SEV>
+__global__ void __launch_bounds__(2 * HALF, kMoveThreads<TPT, SEV> / (2 * HALF))
     evict_move_kernel(const CacheEvictLaunch a, const MovePlan plan) {
-    __shared__ uint32_t s_max[2][2][HALF / 32];
+    constexpr int TPR = D / 16;
+    __shared__ uint32_t s_max[2][2][HALF / 32], s_block[2][2][SEV ? HALF / TPR : 1];
     pdl_launch_dependents();
     pdl_wait();
-    constexpr int TPR = D / 16;
     const int is_v = threadIdx.x / HALF, tid = threadIdx.x % HALF;
     const int ncap = a.new_max_pages * a.page, bpp = (int)plan.sb.div(a.page);
     uint8_t* pool = is_v ? a.vp : a.kp;
     float* scales = is_v ? a.vs : a.ks;
+    const int own = SEV ? (int)plan.sb.div(tid / TPR) * a.sb : 0;  // first token of the thread's block in the turn
+    const bool leads = tid == own * TPR && own < plan.unit;             // writes the block's scale
     struct Item {
-        int bh, blk;
+        int bh, first;  // first token (its place among the kept)
     };
     auto advance = [&](Item& it) {
         it.bh += plan.step_bh;
-        it.blk += plan.step_blk;
-        if (it.blk >= plan.blocks) it.blk -= plan.blocks, ++it.bh;
+        const int left = plan.units * plan.unit - it.first, step = plan.step_units * plan.unit;
+        it.first = step < left ? it.first + step : step - left;
+        if (step >= left) ++it.bh;
     };
     // stage 1: the source indices of an item's tokens (-1: none)
     auto load_kept = [&](const Item& it, int (&kept)[TPT]) {
-        const int first = it.blk * a.sb;
-        const int* list = a.kept + (long long)it.bh * ncap + first;
+        const int* list = a.kept + (long long)it.bh * ncap + it.first;
 #pragma unroll
         for (int i = 0; i < TPT; ++i) {
             const int tok = (tid + i * HALF) / TPR;
-            kept[i] = it.bh < plan.bhs && tok < a.sb && first + tok < ncap ? list[tok] : -1;
+            kept[i] = it.bh < plan.bhs && tok < plan.unit && it.first + tok < ncap ? list[tok] : -1;
         }
     };
-    // stage 2: their pages, and the page that the block goes to
+    // stage 2: their pages, and the page that the thread's block goes to
     auto load_pages = [&](const Item& it, const int (&kept)[TPT], int (&page)[TPT], int& to) {
         const int b = it.bh < plan.bhs ? (int)plan.heads.div(it.bh) : 0;
         const int* trow = a.table + (long long)b * a.max_pages;
 #pragma unroll
         for (int i = 0; i < TPT; ++i) page[i] = kept[i] >= 0 ? trow[plan.page.div(kept[i])] : 0;
-        to = a.new_table[(long long)b * a.new_max_pages + plan.page.div(it.blk * a.sb)];
+        to = a.new_table[(long long)b * a.new_max_pages + plan.page.div(SEV ? min(it.first + own, ncap - 1) : it.first)];
     };
     int kept[TPT], page[TPT], kept1[TPT], to_page;
-    Item item{(int)(blockIdx.x / plan.blocks), (int)(blockIdx.x % plan.blocks)}, next = item;
+    Item item{(int)(blockIdx.x / plan.units), (int)(blockIdx.x % plan.units) * plan.unit}, next = item;
     load_kept(item, kept);
     advance(next);
     load_kept(next, kept1);
@@ -512,18 +545,21 @@ __global__ void __launch_bounds__(2 * HALF, kMoveThreads<TPT> / (2 * HALF))
 #pragma unroll
         for (int i = 0; i < TPT; ++i)
             if (kept[i] >= 0) big = max(big, (__float_as_uint(sc[i]) & 0x7FFFFFFFu) + 1);
-        big = half_max(big, s_max[turn], is_v);
+        if constexpr (SEV)
+            big = block_max<HALF / 32, TPR>(big, s_block[turn], is_v, tid / TPR, own, a.sb);
+        else
+            big = half_max(big, s_max[turn], is_v);
         if (big) {
             const float to = __uint_as_float(big - 1);
             if ((unsigned)to_page < (unsigned)a.num_pages) {
-                const uint32_t at = item.blk * a.sb - plan.page.div(item.blk * a.sb) * a.page;
+                const uint32_t to_first = item.first + own, at = to_first - plan.page.div(to_first) * a.page;
                 const uint32_t head = (uint32_t)to_page * a.Hkv + h;
                 uint4* dst = reinterpret_cast<uint4*>(pool + (size_t)(head * a.page + at) * D);
-                if (tid == 0) scales[head * bpp + plan.sb.div(at)] = to;
+                if (leads) scales[head * bpp + plan.sb.div(at)] = to;
 #pragma unroll
                 for (int i = 0; i < TPT; ++i)
-                    if (kept[i] >= 0) dst[tid + i * HALF] = sc[i] == to ? x[i] : e4m3_rescale16(x[i], sc[i], to);
-            } else if (tid == 0) {
+                    if (kept[i] >= 0) dst[tid - own * TPR + i * HALF] = sc[i] == to ? x[i] : e4m3_rescale16(x[i], sc[i], to);
+            } else if (leads) {
                 record_invalid(a.err, kSiteCacheTable, to_page);
             }
         }
@@ -539,28 +575,30 @@ __global__ void __launch_bounds__(2 * HALF, kMoveThreads<TPT> / (2 * HALF))
     }
 }
 
-template <int D, int HALF, int TPT>
+template <int D, int HALF, int TPT, bool SEV>
 cudaError_t launch_move_t(const CacheEvictLaunch& a, cudaStream_t s) {
     MovePlan plan;
-    plan.blocks = (a.keep + a.sb - 1) / a.sb;
+    plan.unit = a.sb * (SEV ? HALF / (a.sb * (D / 16)) : 1);
+    plan.units = (a.keep + plan.unit - 1) / plan.unit;
     plan.bhs = a.B * a.Hkv;
     plan.page = FastDiv((uint32_t)a.page);
     plan.sb = FastDiv((uint32_t)a.sb);
     plan.heads = FastDiv((uint32_t)a.Hkv);
-    const long long items = (long long)plan.bhs * plan.blocks, most = (long long)kMoveThreads<TPT> / (2 * HALF) * a.num_sms;
+    const long long items = (long long)plan.bhs * plan.units, most = (long long)kMoveThreads<TPT, SEV> / (2 * HALF) * a.num_sms;
     const int grid = (int)(items < most ? items : most);
-    plan.step_bh = grid / plan.blocks;
-    plan.step_blk = grid % plan.blocks;
-    return launch_dependent(evict_move_kernel<D, HALF, TPT>, dim3(grid), dim3(2 * HALF), 0, s, a, plan);
+    plan.step_bh = grid / plan.units;
+    plan.step_units = grid % plan.units;
+    return launch_dependent(evict_move_kernel<D, HALF, TPT, SEV>, dim3(grid), dim3(2 * HALF), 0, s, a, plan);
 }
 
 template <int D>
 cudaError_t launch_move(const CacheEvictLaunch& a, cudaStream_t s) {
     const int tasks = a.sb * (D / 16);
-    if (tasks <= 128) return launch_move_t<D, 128, 1>(a, s);
-    if (tasks <= 256) return launch_move_t<D, 128, 2>(a, s);
-    if (tasks <= 512) return launch_move_t<D, 128, 4>(a, s);
-    return launch_move_t<D, 256, 4>(a, s);
+    if (tasks <= 64) return launch_move_t<D, 128, 1, true>(a, s);
+    if (tasks <= 128) return launch_move_t<D, 128, 1, false>(a, s);
+    if (tasks <= 256) return launch_move_t<D, 128, 2, false>(a, s);
+    if (tasks <= 512) return launch_move_t<D, 128, 4, false>(a, s);
+    return launch_move_t<D, 256, 4, false>(a, s);
 }
 
 }  // namespace

@@ -29,6 +29,12 @@ CASES = [
     (1, 9, 128, 1, 1, [0, 4], None),
     (1, 40, 64, 33, 11, [10, 11], None),
     (1, 3, 64, 96, 96, [95, 90], None),
+    # several small blocks per CTA: of odd sizes, over ends of pages, behind a partly filled block
+    (2, 150, 128, 12, 3, [0, 1, 2, 3, 100], None),
+    (1, 200, 64, 4, 2, [0, 7], [200, 0]),
+    (2, 90, 128, 4, 1, [5, 0], [90, 13]),
+    (3, 100, 64, 40, 8, [7, 33, 39], [1, 100, 64]),
+    (1, 61, 128, 8, 8, [4], None),
 ]
 
 
@@ -65,7 +71,8 @@ def test_append_bytes(cuda_lib, Hkv, N, d, page, sb, lens, new, layout):
 @pytest.mark.parametrize("inter", [False, True])
 @pytest.mark.parametrize("given", [False, True])
 @pytest.mark.parametrize("N,d,rot,page,sb,lens", [(1, 128, 128, 16, 16, [5, 16, 900]), (70, 64, 32, 32, 32, [0, 17]),
-                                                  (33, 128, 48, 64, 64, [3])])
+                                                  (33, 128, 48, 64, 64, [3]), (75, 128, 128, 20, 4, [3, 0]),
+                                                  (41, 64, 16, 2, 1, [6])])
 def test_append_rotates_as_rope_does(cuda_lib, N, d, rot, page, sb, lens, given, inter):
     """Rotation on the way: bit for bit fa_rope followed by the append; V is never rotated."""
     B, Hkv = len(lens), 2
@@ -89,7 +96,7 @@ def test_append_rotates_as_rope_does(cuda_lib, N, d, rot, page, sb, lens, given,
     assert_same_cache(one, c)
 
 
-@pytest.mark.parametrize("sb,page", [(16, 16), (24, 48), (128, 128)])
+@pytest.mark.parametrize("sb,page", [(16, 16), (24, 48), (128, 128), (4, 20), (1, 8)])
 def test_append_token_by_token(cuda_lib, sb, page):
     """A sequence written one token at a time holds what one call writes (no element becomes subnormal here), and
     tokens of growing size rescale the block's earlier ones."""
@@ -192,6 +199,26 @@ def test_append_overflow_and_bad_tables(cuda_lib):
     oc.append(c, table[2:], [0], f64(k)[2:], f64(v)[2:])
     assert_same_cache(g, c)
     assert run([0, 16, 24])[2] == 0
+
+
+def test_append_bad_page_among_small_blocks(cuda_lib):
+    """A CTA's blocks of 4 tokens lie in several pages: those of one that does not exist are left out, the others
+    written."""
+    Hkv, d, page, sb, N = 2, 128, 8, 4, 60
+    rng = np.random.default_rng(2)
+    k, v = bf16(rng, (1, Hkv, N, d)), bf16(rng, (1, Hkv, N, d))
+    c = random_cache(3, 10, Hkv, page, sb, d)
+    table = table_of(9, 1, 8, 10)
+    g, bad = to_gpu(c), table.copy()
+    bad[0, 1], bad[0, 4] = -1, 10
+    cuda_lib.cache_append_fp8(k.to(DEV), v.to(DEV), *args(g), ints(bad), ints([2]))
+    assert cuda_lib.fa_get_last_device_error()[0] == fa_mod.FA_ERR_INVALID_ARG
+    ref = copy(c)
+    oc.append(ref, table, [2], f64(k), f64(v))
+    for n in c:
+        for j in (1, 4):
+            ref[n][table[0, j]] = c[n][table[0, j]]
+    assert_same_cache(g, ref)
 
 
 def test_append_far_pages(cuda_lib):

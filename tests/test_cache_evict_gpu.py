@@ -49,6 +49,11 @@ CASES = [
     (2, 48, 24, [2500, 2049], 1, 0, 64),
     (1, 33, 11, [1025], 1024, 1, 64),                # one token goes
     (2, 256, 64, [5000], 700, 77, 128),
+    # several small blocks per turn
+    (2, 12, 3, [400, 77], 150, 11, 128),
+    (1, 4, 1, [200, 99], 90, 7, 128),
+    (2, 40, 8, [900, 20], 333, 20, 64),
+    (3, 6, 2, [700], 613, 100, 64),
     (8, 64, 32, [5000, 4000, 1, 3000, 80, 0, 64, 2500, 5000, 700], 70, 10, 64),  # one CTA per kv head, many tokens each
     (1, 256, 128, [140000], 90, 5, 64),              # more tokens than a cluster's registers hold
     (2, 128, 128, [40000, 39999], 300, 300, 64),     # a cluster of eight, recent ones only
@@ -103,6 +108,26 @@ def test_evict_bad_lengths_and_pages(cuda_lib):
     assert len(lost)
     for s in lost:
         assert (g["k"][new[0, s // page], 0, s % page].cpu().numpy() == 0).all()
+
+
+def test_evict_bad_page_among_small_blocks(cuda_lib):
+    """Blocks of 4 tokens whose new page does not exist are left out, the others of the same turn written."""
+    page, sb, d, Hkv = 8, 4, 128, 2
+    c = random_cache(5, 30, Hkv, page, sb, d)
+    both = table_of(3, 1, 30, 30)
+    table, new = both[:, :20], both[:, 20:28]
+    w = np.random.default_rng(4).random((1, Hkv, 160)).astype(np.float32)
+    bad = new.copy()
+    bad[0, 0], bad[0, 3] = 30, -7
+    g, got = _run(cuda_lib, c, table, [155], w, bad, 61, 9)
+    assert cuda_lib.fa_get_last_device_error()[0] == fa_mod.FA_ERR_INVALID_ARG
+    ref = copy(c)
+    want = oc.evict(ref, table, np.array([155]), w, new, 61, 9)
+    for n in c:
+        for j in (0, 3):
+            ref[n][new[0, j]] = c[n][new[0, j]]
+    assert all(np.array_equal(a, b) for a, b in zip(got, want))
+    assert_same_cache(g, ref)
 
 
 def test_evict_far_pages(cuda_lib):
