@@ -942,10 +942,9 @@ int fa_decode_paged_fp8(const void* q, const void* k_pages, const void* v_pages,
         return FA_ERR_ALIGNMENT;
     if (o == q) return FA_ERR_INVALID_ARG;  // other CTAs may still read the row that one writes
     PagedDecodeFp8Launch a;
-    int num_sms = 0;
-    st = device_state(&a.err, &num_sms);
+    st = device_state(&a.err, &a.num_sms);
     if (st != FA_OK) return st;
-    st = fp8_workers(d, tile, num_sms, &a.workers);
+    st = fp8_workers(d, tile, a.num_sms, &a.workers);
     if (st != FA_OK) return st;
     const Fp8Workspace ws = fp8_workspace(B, Hq, Hkv, Nq, d, (long long)max_pages * page_size, weights != nullptr);
     if (!workspace || workspace_bytes < ws.bytes) return FA_ERR_WORKSPACE;

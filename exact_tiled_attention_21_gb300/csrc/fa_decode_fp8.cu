@@ -657,13 +657,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, ROWS>::REGS_FOR) decode_fp8_k
                                 dst[i] = make_uint4(pack_bf16(o[8 * i], o[8 * i + 1]), pack_bf16(o[8 * i + 2], o[8 * i + 3]),
                                                     pack_bf16(o[8 * i + 4], o[8 * i + 5]), pack_bf16(o[8 * i + 6], o[8 * i + 7]));
                             if (a.lse && g == 0) a.lse[row] = lse2 * kLn2;
+                            if (a.weights && g == 0) a.lse2[row] = lse2;
                         } else {
                             float4* dst = reinterpret_cast<float4*>(a.part_o + (slot_out * ROWS + r) * D + g * DT);
 #pragma unroll
                             for (int i = 0; i < DT / 4; ++i)
                                 dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                            if (g == 0) a.part_lse[slot_out * ROWS + r] = lse2;
                         }
-                        if (g == 0) a.part_lse[slot_out * ROWS + r] = lse2;
                     }
             }
         }
@@ -691,77 +692,109 @@ __device__ __forceinline__ int find_segments(const Params& a, int b, int item_b,
 __device__ __forceinline__ float merge_lse(const float* pl, int stride, int segs, float& base) {
     const int lane = threadIdx.x & 31;
     float M = -INFINITY;
+#pragma unroll 4
     for (int s = lane; s < segs; s += 32) M = fmaxf(M, pl[(long long)s * stride]);
     for (int w = 16; w >= 1; w >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
     base = M == -INFINITY ? 0.f : M;
     float sum = 0.f;
+#pragma unroll 4
     for (int s = lane; s < segs; s += 32) sum += ex2(pl[(long long)s * stride] - base);
     for (int w = 16; w >= 1; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
     return sum;
 }
 
-constexpr int kFinishThreads = 128;
-
-// One block per row: LSE = M + log2 sum 2^(lse_s - M), O = sum 2^(lse_s - M) o_s / sum, the segments dealt to groups of
-// D / 4 threads.  A row without keys gets O = 0, LSE = -inf; a row whose item was one segment is already written.  (A
-// warp per row where there are few segments: one sequence of 777 tokens 12.3 us against 10.3.)
-template <int D, int ROWS>
-__global__ void __launch_bounds__(kFinishThreads) finish_fp8_kernel(const Params a) {
-    constexpr int LANES = D / 4, GROUPS = kFinishThreads / LANES, AHEAD = 4;
+// One block per run of `run` rows of a tile, one after the other: LSE = M + log2 sum 2^(lse_s - M), O = sum 2^(lse_s - M)
+// o_s / sum, the segments dealt to groups of D / 4 threads.  A row without keys gets O = 0, LSE = -inf; rows whose item was
+// one segment are already written.  Of rows in longer runs with few segments a group takes one each (47 sequences of 1200
+// tokens, 2 heads, 80 rows: 7.7 us, one after the other 13.4); single rows are faster with the groups sharing the segments
+// (one sequence of 777 tokens: 10.3 us in all against 12.3).  Bound by latency.
+template <int D, int ROWS, int THREADS>
+__global__ void __launch_bounds__(THREADS) finish_fp8_kernel(const Params a, int run, int runs) {
+    constexpr int LANES = D / 4, GROUPS = THREADS / LANES, AHEAD = 4;
     __shared__ float4 s_o[GROUPS][LANES];
     pdl_launch_dependents();
     pdl_wait();
-    const int tid = threadIdx.x;
-    const long long row = blockIdx.x, bh = row / a.rows;
-    const int r = (int)(row - bh * a.rows), b = (int)(bh / a.Hkv), rt = r / ROWS;
+    const int tid = threadIdx.x, grp = tid / LANES, col = tid % LANES;
+    const long long bh = blockIdx.x / runs;
+    const int r0 = (int)(blockIdx.x % runs) * run, b = (int)(bh / a.Hkv), rt = r0 / ROWS;
     long long slot = 0;
     const int segs = find_segments(a, b, (int)(bh % a.Hkv) * a.row_tiles + rt, slot);
-    const long long at = slot * ROWS + (r - rt * ROWS);
-    const float* pl = a.part_lse + at;
-    if (segs == 1) {
-        if (a.weights && tid == 0) a.lse2[row] = pl[0];
-        return;
-    }
-    const int grp = tid / LANES, col = tid % LANES;
-    const float4* po = reinterpret_cast<const float4*>(a.part_o + at * D) + col;
-    float4 v[AHEAD];  // the first segments, loaded before the weights are known
-#pragma unroll
-    for (int i = 0; i < AHEAD; ++i)
-        if (grp + i * GROUPS < segs) v[i] = po[(long long)(grp + i * GROUPS) * ROWS * LANES];
-    float base;
-    const float sum = merge_lse(pl, ROWS, segs, base);
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s0 = grp; s0 < segs; s0 += AHEAD * GROUPS) {
-#pragma unroll
-        for (int i = 0; i < AHEAD; ++i) {
-            const int s = s0 + i * GROUPS;
-            if (s < segs) {
-                const float w = ex2(pl[(long long)s * ROWS] - base) * inv;
-                o.x = fmaf(w, v[i].x, o.x);
-                o.y = fmaf(w, v[i].y, o.y);
-                o.z = fmaf(w, v[i].z, o.z);
-                o.w = fmaf(w, v[i].w, o.w);
-            }
-            if (s + AHEAD * GROUPS < segs) v[i] = po[(long long)(s + AHEAD * GROUPS) * ROWS * LANES];
-        }
-    }
-    s_o[grp][col] = o;
-    __syncthreads();
-    if (grp > 0) return;
-#pragma unroll
-    for (int i = 1; i < GROUPS; ++i) {
-        const float4 x = s_o[i][col];
-        o.x += x.x;
-        o.y += x.y;
-        o.z += x.z;
-        o.w += x.w;
-    }
-    *reinterpret_cast<uint2*>(a.o + row * D + col * 4) = make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
-    if (col == 0) {
+    auto write = [&](long long row, float4 o, float sum, float base) {
+        *reinterpret_cast<uint2*>(a.o + row * D + col * 4) = make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
+        if (col > 0) return;
         const float lse2 = sum == 0.f ? -INFINITY : base + lg2(sum);
         if (a.lse) a.lse[row] = lse2 * kLn2;
         if (a.weights) a.lse2[row] = lse2;
+    };
+    if (segs == 1) return;
+    if (run > 1 && segs <= AHEAD) {  // a group for each row
+        for (int r = r0 + grp; r < min(r0 + run, a.rows); r += GROUPS) {
+            const long long at = slot * ROWS + (r - rt * ROWS), row = bh * a.rows + r;
+            float4 v[AHEAD];
+            float w[AHEAD], top = -INFINITY, sum = 0.f;
+#pragma unroll
+            for (int s = 0; s < AHEAD; ++s) {
+                w[s] = s < segs ? a.part_lse[at + s * ROWS] : -INFINITY;
+                v[s] = s < segs ? reinterpret_cast<const float4*>(a.part_o + (at + s * ROWS) * D)[col]
+                                : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+#pragma unroll
+            for (int s = 0; s < AHEAD; ++s) top = fmaxf(top, w[s]);
+            const float base = top == -INFINITY ? 0.f : top;
+#pragma unroll
+            for (int s = 0; s < AHEAD; ++s) sum += w[s] = ex2(w[s] - base);
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int s = 0; s < AHEAD; ++s) {
+                o.x = fmaf(w[s] * inv, v[s].x, o.x);
+                o.y = fmaf(w[s] * inv, v[s].y, o.y);
+                o.z = fmaf(w[s] * inv, v[s].z, o.z);
+                o.w = fmaf(w[s] * inv, v[s].w, o.w);
+            }
+            write(row, o, sum, base);
+        }
+        return;
+    }
+    for (int r = r0; r < min(r0 + run, a.rows); ++r) {
+        const long long at = slot * ROWS + (r - rt * ROWS), row = bh * a.rows + r;
+        const float* pl = a.part_lse + at;
+        const float4* po = reinterpret_cast<const float4*>(a.part_o + at * D) + col;
+        float4 v[AHEAD];  // the first segments, loaded before the weights are known
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i)
+            if (grp + i * GROUPS < segs) v[i] = po[(long long)(grp + i * GROUPS) * ROWS * LANES];
+        float base;
+        const float sum = merge_lse(pl, ROWS, segs, base);
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int s0 = grp; s0 < segs; s0 += AHEAD * GROUPS) {
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) {
+                const int s = s0 + i * GROUPS;
+                if (s < segs) {
+                    const float w = ex2(pl[(long long)s * ROWS] - base) * inv;
+                    o.x = fmaf(w, v[i].x, o.x);
+                    o.y = fmaf(w, v[i].y, o.y);
+                    o.z = fmaf(w, v[i].z, o.z);
+                    o.w = fmaf(w, v[i].w, o.w);
+                }
+                if (s + AHEAD * GROUPS < segs) v[i] = po[(long long)(s + AHEAD * GROUPS) * ROWS * LANES];
+            }
+        }
+        if (r > r0) __syncthreads();  // the row before is read
+        s_o[grp][col] = o;
+        __syncthreads();
+        if (grp > 0) continue;
+#pragma unroll
+        for (int i = 1; i < GROUPS; ++i) {
+            const float4 x = s_o[i][col];
+            o.x += x.x;
+            o.y += x.y;
+            o.z += x.z;
+            o.w += x.w;
+        }
+        write(row, o, sum, base);
     }
 }
 
@@ -875,8 +908,16 @@ cudaError_t launch_d(const PagedDecodeFp8Launch& a, cudaStream_t s) {
     p.workers = (int)std::min<long long>(a.workers, bh * p.row_tiles * ((cap + kStep - 1) / kStep));
     e = launch_dependent(decode_fp8_kernel<D, ROWS>, dim3(p.workers), dim3(kThreads), C::SMEM, s, p);
     if (e != cudaSuccess) return e;
-    const long long row_blocks = bh * p.rows;
-    e = launch_dependent(finish_fp8_kernel<D, ROWS>, dim3((unsigned)row_blocks), dim3(kFinishThreads), 0, s, p);
+    // rows per finishing block: one up to 16 blocks per SM (45 sequences of 20 tokens, 8 heads, 80 rows: 32.5 us with one,
+    // 5.0 with 16); its threads: 512 where an item has 32 segments or more (a single one of 70000 tokens, 16 rows: 17.7 us
+    // with 128, 11.2 with 512; 8 of 128k tokens the same)
+    int run = 1;
+    while (run < ROWS && bh * p.rows > 16ll * run * a.num_sms) run *= 2;
+    const int runs = (p.rows + run - 1) / run;
+    const dim3 rows((unsigned)(bh * runs));
+    e = p.workers >= 32 * bh * p.row_tiles
+            ? launch_dependent(finish_fp8_kernel<D, ROWS, 512>, rows, dim3(512), 0, s, p, run, runs)
+            : launch_dependent(finish_fp8_kernel<D, ROWS, 128>, rows, dim3(128), 0, s, p, run, runs);
     if (e != cudaSuccess || !a.weights) return e;
     int tokens = kPart / 4;  // of a block: as many as its rows leave room for
     while (tokens * std::min(p.rows, ROWS) > kPart) tokens /= 2;

@@ -222,6 +222,7 @@ struct PagedDecodeFp8Launch {
     float* lse2;           // fp32 [B*Hq*Nq], with weights only
     int B, Hq, Hkv, Nq, page, sb, max_pages, num_pages, d;
     int workers;           // CTAs to share the steps among
+    int num_sms;
     float scale;
     DevError* err;
 };

@@ -50,6 +50,9 @@ CASES = [
     (4, 1, 1, 64, 64, [70000], 128),                   # one kv head over every SM: hundreds of segments to merge
     (1, 1, 1, 16, 16, list(range(0, 200, 3)) * 2, 64),  # more sequences than one scan step, some empty
     (2, 1, 2, 16, 16, [130] * 300, 128),               # more items than CTAs: shares that cross several
+    (16, 1, 5, 16, 16, [0, 20, 3, 300, 1, 129] * 10, 128),   # 4800 rows: finished by runs
+    (16, 1, 5, 16, 16, [7, 0, 140, 16] * 60, 64),            # 19200
+    (9, 1, 1, 64, 64, [2000, 700] * 140, 128),               # 2520, of one tile each
 ]
 
 
