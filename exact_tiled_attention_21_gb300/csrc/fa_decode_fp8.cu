@@ -65,10 +65,7 @@ struct Cfg {
     static constexpr int RING = kStages * SLOT;            // per warp
     static constexpr int MERGE = kWarps * RING;            // byte offset of the merge buffers, one for each warp but the
                                                            // first group's
-    // The merge takes the columns in PIECES turns: smaller buffers leave more L1 for tables and scales (64 sequences of
-    // 8192 tokens, 8 kv heads, 64 query heads: 192 us in one turn, 183 in two).
-    static constexpr int PIECES = D == 64 ? 1 : ROWS == 16 ? 4 : 2;
-    static constexpr int OROW = D / PIECES + 4;            // a row of them, floats; within it column d (of 8 runs of
+    static constexpr int OROW = D + 4;                     // a row of them, floats; within it column d (of 8 runs of
                                                            // D / 8: g, then 2 i + e) is at 16 i + 2 g + e: no bank conflicts
     static constexpr int SMEM = MERGE + (kWarps - RG) * 8 * NB * OROW * 4;
     // CTAs per SM, and those that the registers are made for.  d = 128, up to 8 rows: bound by HBM, and a third CTA
@@ -593,30 +590,21 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, ROWS>::REGS_FOR) decode_fp8_k
                         f[nb][j] = ex2(M[nb][j] - top);
                         m[nb][j] = top;
                         l[nb][j] = sum;
+                        if (kg > 0)
+#pragma unroll
+                            for (int i = 0; i < D / 16; ++i)
+                                *reinterpret_cast<float2*>(buf + ((warp - RG) * 8 * NB + r) * C::OROW + i * 16) =
+                                    make_float2(acc[nb][i][j] * f[nb][j], acc[nb][i][2 + j] * f[nb][j]);
                     }
-                constexpr int PART = D / 16 / C::PIECES;
-#pragma unroll
-                for (int p = 0; p < C::PIECES; ++p) {
-                    if (p > 0) __syncthreads();
+                __syncthreads();
+                if (kg == 0) {
 #pragma unroll
                     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
-                            if (kg == 0) continue;
 #pragma unroll
-                            for (int i = 0; i < PART; ++i)
-                                *reinterpret_cast<float2*>(buf + ((warp - RG) * 8 * NB + nb * 8 + 2 * t + j) * C::OROW + i * 16) =
-                                    make_float2(acc[nb][p * PART + i][j] * f[nb][j], acc[nb][p * PART + i][2 + j] * f[nb][j]);
-                        }
-                    __syncthreads();
-#pragma unroll
-                    for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            if (kg > 0) continue;
-#pragma unroll
-                            for (int i = 0; i < PART; ++i) {
-                                float2 x = make_float2(acc[nb][p * PART + i][j] * f[nb][j], acc[nb][p * PART + i][2 + j] * f[nb][j]);
+                            for (int i = 0; i < D / 16; ++i) {
+                                float2 x = make_float2(acc[nb][i][j] * f[nb][j], acc[nb][i][2 + j] * f[nb][j]);
 #pragma unroll
                                 for (int w = 1; w < KG; ++w) {
                                     const float2 y = *reinterpret_cast<const float2*>(
@@ -624,14 +612,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, ROWS>::REGS_FOR) decode_fp8_k
                                     x.x += y.x;
                                     x.y += y.y;
                                 }
-                                acc[nb][p * PART + i][j] = x.x;
-                                acc[nb][p * PART + i][2 + j] = x.y;
+                                acc[nb][i][j] = x.x;
+                                acc[nb][i][2 + j] = x.y;
                             }
+                            f[nb][j] = 1.f;
                         }
                 }
-                if (kg == 0)
-#pragma unroll
-                    for (int nb = 0; nb < NB; ++nb) f[nb][0] = f[nb][1] = 1.f;
             }
             if (kg == 0) {
                 const bool whole = seg == 0 && item_ends;
