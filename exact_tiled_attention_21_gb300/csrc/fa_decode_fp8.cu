@@ -68,7 +68,9 @@ struct Cfg {
     static constexpr int OROW = D + 4;                     // a row of them, floats; within it column d (of 8 runs of
                                                            // D / 8: g, then 2 i + e) is at 16 i + 2 g + e: no bank conflicts
     static constexpr int SMEM = MERGE + (kWarps - RG) * 8 * NB * OROW * 4;
-    // CTAs per SM, and those that the registers are made for.  d = 128, up to 8 rows: bound by HBM, and a third CTA
+    // CTAs per SM, and those that the registers are made for; shared memory or registers must leave no room for one more,
+    // or the next call's CTAs, started early, fill SMs unevenly (smaller merge buffers that let a third one in: 32 sequences
+    // of 4096 tokens, calls back to back, 61.2 us against 52.4).  d = 128, up to 8 rows: bound by HBM, and a third CTA
     // only costs (128k tokens: 68 us with one, 55 with two, 58 with three; the copies alone 51 with one).  d = 64: bound
     // by instructions, four CTAs 28.9 us, three 30.2, five 30.6 (16 sequences of 3000 tokens, 16 heads).  16 rows per
     // warp take 249 registers at d = 128 and more than 128 at d = 64.
@@ -698,8 +700,9 @@ template <int D, int ROWS, int THREADS>
 __global__ void __launch_bounds__(THREADS) finish_fp8_kernel(const Params a, int run, int runs) {
     constexpr int LANES = D / 4, GROUPS = THREADS / LANES, AHEAD = 4;
     __shared__ float4 s_o[GROUPS][LANES];
-    pdl_launch_dependents();
     pdl_wait();
+    pdl_launch_dependents();  // after the wait: the next call's CTAs, started earlier, would fill SMs unevenly (16
+                              // sequences of 2300 tokens, 16 heads, d = 64, calls back to back: 27.6 us against 22.4)
     const int tid = threadIdx.x, grp = tid / LANES, col = tid % LANES;
     const long long bh = blockIdx.x / runs;
     const int r0 = (int)(blockIdx.x % runs) * run, b = (int)(bh / a.Hkv), rt = r0 / ROWS;
@@ -793,8 +796,8 @@ constexpr int kWeightThreads = 256, kPart = 4096, kPieces = kPart / 4 / kWeightT
 template <int ROWS>
 __global__ void __launch_bounds__(kWeightThreads) weights_fp8_kernel(const Params a, int blocks, int tokens) {
     __shared__ float s_sum[kPart / 4];
-    pdl_launch_dependents();
     pdl_wait();
+    pdl_launch_dependents();
     const int tid = threadIdx.x, cap = a.max_pages * (int)a.page.d;
     const long long bh = blockIdx.x / blocks;
     const int len = clamp_len(a.lens[bh / a.Hkv], cap), begin = (int)(blockIdx.x % blocks) * tokens;
