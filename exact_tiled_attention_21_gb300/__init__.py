@@ -8,7 +8,11 @@ names and arguments of ``include/fa.h`` and only marshal arguments: every step
 of the computation runs in the CUDA kernels of ``libfa_gb300.so``.  PyTorch
 supplies device memory (``data_ptr``) and the stream.  ``forward``,
 ``backward`` and ``decode`` are conveniences that allocate the outputs and the
-workspace with torch and then call the same entry points.
+workspace with torch and then call the same entry points.  So are those of the
+serving cache held in 8 bits, ``rope``, ``cache_append_fp8``,
+``decode_paged_fp8`` and ``cache_evict_fp8``, through a compiled binding
+(``csrc/fa_torch.cpp``, ``_fa_torch.so``), since their small calls take less time
+on the GPU than ctypes does on the host.
 
 There is no fallback: if the shared library is missing, or a call returns an
 error status, a ``FAError`` is raised.
