@@ -609,10 +609,13 @@ cudaError_t launch_cache_append(const CacheAppendLaunch& a, cudaStream_t s) {
 
 cudaError_t launch_cache_evict(const CacheEvictLaunch& a, cudaStream_t s) {
     // CTAs per (sequence, kv head): more while that still leaves each 2048 tokens and all of them fit at once (one
-    // sequence of 64k tokens, 8 heads, with the move: 1 CTA 191 us, 2 109, 4 32.5, 8 31.8)
+    // sequence of 64k tokens, 8 heads, with the move: 1 CTA 208 us, 2 117, 4 28.7, 8 27.5), and while a CTA's registers do
+    // not hold its keys (20 sequences of 64k tokens, 8 heads: 1 CTA 236 us, 4 93; 8, with 16 keys per thread, 162)
     const long long bh = (long long)a.B * a.Hkv, cap = (long long)a.max_pages * a.page;
     int ctas = 1;
-    while (ctas < kSelCtas && cap >= 4096ll * ctas && bh * ctas * 2 <= a.num_sms) ctas *= 2;
+    while (ctas < kSelCtas &&
+           (cap > 32ll * kSelThreads * ctas || (cap >= 4096ll * ctas && bh * ctas * 2 <= a.num_sms)))
+        ctas *= 2;
     const long long per = (cap + (long long)ctas * kSelThreads - 1) / ((long long)ctas * kSelThreads);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(bh * ctas));
@@ -625,8 +628,8 @@ cudaError_t launch_cache_evict(const CacheEvictLaunch& a, cudaStream_t s) {
     attr[1].val.clusterDim = {(unsigned)ctas, 1, 1};
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    // keys in registers: 8 per thread leave two CTAs per SM (32 sequences of 4096 tokens, 8 heads: 45 us; 32 registers 55,
-    // none 51), 32 save a long sequence the reads of later rounds (64k tokens: 32 us; none 51)
+    // keys in registers: 8 per thread leave two CTAs per SM (32 sequences of 4096 tokens, 8 heads: 37.8 us; 32 registers
+    // 49.4, none 46.5), 32 save a long sequence the reads of later rounds (64k tokens: 27.5 us; none 50.3)
     cudaError_t e = per <= 8    ? cudaLaunchKernelEx(&cfg, evict_select_kernel<8>, a, ctas)
                     : per <= 32 ? cudaLaunchKernelEx(&cfg, evict_select_kernel<32>, a, ctas)
                                 : cudaLaunchKernelEx(&cfg, evict_select_kernel<0>, a, ctas);

@@ -78,6 +78,20 @@ def test_evict_bytes(cuda_lib, Hkv, page, sb, lens, keep, recent, d, kind):
     assert_same_cache(g, c)   # the kept tokens, and every other byte as it was
 
 
+def test_evict_many_long_heads(cuda_lib):
+    """More clusters than run at once, over a cache whose logical pages share four physical ones."""
+    Hkv, page, sb, d, n, keep = 90, 64, 64, 64, 20000, 100
+    c = random_cache(2, 6, Hkv, page, sb, d)
+    table = (np.arange(-(-n // page)) % 4).astype(np.int32)[None]
+    new = np.array([[5, 4]], dtype=np.int32)
+    w = _weights(np.random.default_rng(6), (1, Hkv, table.shape[1] * page), "ties")
+    g, got = _run(cuda_lib, c, table, [n], w, new, keep, 30)
+    _ok(cuda_lib)
+    want = oc.evict(c, table, np.array([n]), w, new, keep, 30)
+    assert all(np.array_equal(a, b) for a, b in zip(got, want))
+    assert_same_cache(g, c)
+
+
 def test_evict_bad_lengths_and_pages(cuda_lib):
     page, sb, d, Hkv = 16, 16, 64, 2
     c = random_cache(1, 20, Hkv, page, sb, d)
