@@ -876,7 +876,7 @@ int fa_cache_append_fp8(const void* k, const void* v, long long k_sb, long long 
     int st = check_cache(B, Hkv, page_size, scale_block, max_pages, num_pages, d);
     if (st != FA_OK) return st;
     if (turns && (st = check_rotation(d, rot, interleaved, magnitude)) != FA_OK) return st;
-    if (N > kMaxCacheTokens || (long long)B * Hkv * N > 0x7FFFFFFFll) return FA_ERR_UNSUPPORTED;
+    if (N > kMaxCacheTokens / 2 || (long long)B * Hkv * N > 0x7FFFFFFFll) return FA_ERR_UNSUPPORTED;
     if (!aligned16(k) || !aligned16(v) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(turns) ||
         !aligned4(k_scale) || !aligned4(v_scale) || !aligned4(block_table) || !aligned4(seq_lens) ||
         !aligned4(new_lens) || !aligned4(positions))

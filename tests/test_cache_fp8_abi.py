@@ -95,7 +95,7 @@ def _append(lib, p=(16,) * 8, extra=(0, 0, 0), ks=(0, 0, 64), vs=(0, 0, 64), B=1
 
 @pytest.mark.parametrize("bad,status", CACHE_BAD + [
     (dict(N=0), fa.FA_ERR_INVALID_ARG), (dict(N=(1 << 30) + 1), fa.FA_ERR_UNSUPPORTED),
-    (dict(N=1 << 30), fa.FA_ERR_UNSUPPORTED),
+    (dict(N=1 << 30), fa.FA_ERR_UNSUPPORTED), (dict(N=(1 << 29) + 8, Hkv=1), fa.FA_ERR_UNSUPPORTED),
     (dict(ks=(0, 0, 4)), fa.FA_ERR_ALIGNMENT), (dict(vs=(0, -8, 64)), fa.FA_ERR_INVALID_ARG),
     (dict(extra=(0, 0, 16), rot=20), fa.FA_ERR_UNSUPPORTED), (dict(extra=(0, 0, 16), rot=80), fa.FA_ERR_INVALID_ARG),
     (dict(extra=(0, 0, 16), mag=NAN), fa.FA_ERR_INVALID_ARG), (dict(extra=(0, 0, 8)), fa.FA_ERR_ALIGNMENT),
