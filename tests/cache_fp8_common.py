@@ -77,7 +77,7 @@ def check_decode(o, lse, ref, w=None, w_ref=None, what=""):
     over = np.abs(o - o_ref) - bound
     assert over.max() <= 0, "%s: O exceeds its bound by %g at %s" % (what, over.max(), np.unravel_index(over.argmax(), over.shape))
     fin = ~none
-    err = np.abs(lse - lse_ref)[fin] - (rel + 2.0 ** -22 * np.abs(np.where(none, 0, lse_ref)))[fin]
+    err = np.abs(np.where(none, 0, lse) - np.where(none, 0, lse_ref))[fin] - (rel + 2.0 ** -22 * np.abs(np.where(none, 0, lse_ref)))[fin]
     assert not err.size or err.max() <= 0, "%s: LSE exceeds its bound by %g" % (what, err.max())
     if w is not None:
         r = rel.max() if rel.size else 0.0
