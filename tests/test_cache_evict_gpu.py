@@ -256,3 +256,45 @@ def test_serving_run(cuda_lib, d, page, sb, inter):
     for n in (1, 4, 1, 3):
         step(n)
     _ok(fa)
+
+
+def _shifted(x):
+    """The same values 4 bytes behind an aligned address."""
+    y = torch.empty(x.numel() + 1, dtype=x.dtype, device=x.device)[1:].view(x.shape)
+    return y.copy_(x)
+
+
+@pytest.mark.parametrize("rows", [(4, 1), (7, 5)])
+def test_four_byte_alignment_and_shared_pages(cuda_lib, rows):
+    """Scales, tables, lengths, positions and weights on 4-byte addresses, and a prefix of pages that sequences share
+    while they are read: the results of aligned tensors, bit for bit, and of a cache of their own."""
+    G, Nq = rows
+    Hkv, page, sb, d, B = 2, 16, 4, 64, 3
+    c = random_cache(8, 24, Hkv, page, sb, d)
+    own = table_of(5, B, 6, 24)
+    shared = own.copy()
+    shared[:, :2] = own[0, :2]
+    for b in range(1, B):                       # the same tokens in pages of their own
+        for n in c:
+            c[n][own[b, :2]] = c[n][own[0, :2]]
+    rng = np.random.default_rng(11)
+    k, v = bf16(rng, (B, Hkv, 5, d)).to(DEV), bf16(rng, (B, Hkv, 5, d)).to(DEV)
+    q = bf16(rng, (B, Hkv * G, Nq, d)).to(DEV)
+    turns = cuda_lib.rope_table(10000.0 ** (-2.0 * np.arange(16) / 32))
+    pos, lens, new = ints(rng.integers(0, 999, (B, 5))), ints([40, 33, 70]), ints([5, 0, 3])
+    after = ints([45, 33, 73])
+    out = []
+    for table, move in ((own, lambda x: x), (own, _shifted), (shared, _shifted)):
+        g = to_gpu(c)
+        for n in ("ks", "vs"):
+            g[n] = move(g[n])
+        tab, w = move(ints(table)), move(torch.zeros((B, Hkv, 96), device=DEV))
+        cuda_lib.cache_append_fp8(k, v, *args(g), tab, move(lens), move(new), turns, move(pos))
+        got = list(cuda_lib.decode_paged_fp8(q, *args(g), tab, move(after), weights=w)) + [w]
+        fresh = np.setdiff1d(np.arange(24), own)[:6].reshape(B, 2)
+        got += list(cuda_lib.cache_evict_fp8(*args(g), tab, move(after), w, move(ints(fresh)), 30, 4))
+        got += [g[n][torch.from_numpy(fresh.reshape(-1)).long()] for n in g]
+        out.append(got)
+    _ok(cuda_lib)
+    for other in out[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(out[0], other))
