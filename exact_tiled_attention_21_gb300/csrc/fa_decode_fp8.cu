@@ -701,8 +701,9 @@ __global__ void __launch_bounds__(THREADS) finish_fp8_kernel(const Params a, int
     constexpr int LANES = D / 4, GROUPS = THREADS / LANES, AHEAD = 4;
     __shared__ float4 s_o[GROUPS][LANES];
     pdl_wait();
-    pdl_launch_dependents();  // after the wait: the next call's CTAs, started earlier, would fill SMs unevenly (16
-                              // sequences of 2300 tokens, 16 heads, d = 64, calls back to back: 27.6 us against 22.4)
+    // The last kernel of a call starts nothing early: the next call's CTAs, sharing SMs with this one's, would begin
+    // unevenly (32 sequences of 4096 tokens, 8 heads, d = 64, calls back to back: 39.4 us against 31.6).
+    if (a.weights) pdl_launch_dependents();
     const int tid = threadIdx.x, grp = tid / LANES, col = tid % LANES;
     const long long bh = blockIdx.x / runs;
     const int r0 = (int)(blockIdx.x % runs) * run, b = (int)(bh / a.Hkv), rt = r0 / ROWS;
@@ -797,7 +798,6 @@ template <int ROWS>
 __global__ void __launch_bounds__(kWeightThreads) weights_fp8_kernel(const Params a, int blocks, int tokens) {
     __shared__ float s_sum[kPart / 4];
     pdl_wait();
-    pdl_launch_dependents();
     const int tid = threadIdx.x, cap = a.max_pages * (int)a.page.d;
     const long long bh = blockIdx.x / blocks;
     const int len = clamp_len(a.lens[bh / a.Hkv], cap), begin = (int)(blockIdx.x % blocks) * tokens;
