@@ -70,11 +70,15 @@ __device__ __forceinline__ uint32_t abs_max(uint4 x, uint4 y) {
 
 // Eight bf16 as e4m3 bytes of their values divided by s; pow2: by its exact inverse.
 __device__ __forceinline__ uint2 quantise8(uint4 x, float inv, float s, bool pow2) {
+    if (pow2) {  // as bf16 pairs: exact but for what underflows, which rounds to zero either way
+        const uint32_t two = __byte_perm(__float_as_uint(inv), 0, 0x3232);
+        asm("mul.bf16x2 %0, %0, %1;" : "+r"(x.x) : "r"(two));
+        asm("mul.bf16x2 %0, %0, %1;" : "+r"(x.y) : "r"(two));
+        asm("mul.bf16x2 %0, %0, %1;" : "+r"(x.z) : "r"(two));
+        asm("mul.bf16x2 %0, %0, %1;" : "+r"(x.w) : "r"(two));
+    }
     float f[8] = {bf_lo(x.x), bf_hi(x.x), bf_lo(x.y), bf_hi(x.y), bf_lo(x.z), bf_hi(x.z), bf_lo(x.w), bf_hi(x.w)};
-    if (pow2) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] *= inv;
-    } else {
+    if (!pow2) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) f[i] = __fdiv_rn(f[i], s);
     }
@@ -83,14 +87,14 @@ __device__ __forceinline__ uint2 quantise8(uint4 x, float inv, float s, bool pow
 
 // One CTA per (sequence, touched block of sb tokens, run of kv heads); the first HALF threads take K, the others V.  Of
 // blocks too small for 128 threads a CTA takes several (one with blocks of 4 tokens, 17 sequences of 5624 tokens, 1 head:
-// 101 us against 44).
-// The block's cosines and sines are made once, in shared memory, by all threads, and serve every head of the run: with
+// 101 us against 44).  The block's cosines and sines are made once, in shared memory, and serve every head of the run: with
 // a pair of them per head and element the sines alone were half of the instructions.  A thread holds TPT tasks (16
 // columns of a token: the pieces that a rotation pairs) in registers between the block's maximum and the quantisation,
 // so new tokens are read once, the next head's while this one's are worked on.  If the scale grows, the block's earlier
-// tokens are requantised in place.  Reads two bytes per element and writes one; bound by instructions, about 250 per warp
-// and 512 elements (54% of the ALU pipe): 8 ragged prompts of up to 2048 tokens, 8 heads, d = 128 26.5 us (2.9 TB/s);
-// one token of each of 32 sequences 6.1 us, the latency of a launch and four dependent loads.
+// tokens are requantised in place.  Reads two bytes per element and writes one; bound by instructions, about 240 per warp
+// and 512 elements (54% of the ALU pipe): 8 ragged prompts of up to 2048 tokens, 8 heads, d = 128, calls back to back 21.8
+// us (3.5 TB/s; 22.6 with the products by the inverse scale in fp32); one token of each of 32 sequences 6.1 us, the latency
+// of a launch and four dependent loads.
 struct AppendPlan {
     int unit, units, heads, groups;  // blocks per CTA, and runs of them that N tokens can touch; the same of kv heads
     FastDiv page, sb;

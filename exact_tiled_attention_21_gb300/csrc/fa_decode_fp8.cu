@@ -9,10 +9,9 @@
 // holds 8 query rows, or 16 where there are more, so that a widened fragment
 // serves two products.  Up to 16 rows the warps take different keys and wait for
 // nobody until the end; with 32 two warps read each other's keys, each for rows
-// of its own.  8 sequences of 8000 tokens, 4 kv heads, d = 128: 24.5 us for 8 rows,
-// 29.8 for 16, 39.2 for 32 (8 rows in each of four warps that share keys: 42.6, and
-// 99.6 against 83.8 for 80 rows; 32 rows in every warp: spills, 50 against 33 without
-// the second kernel).
+// of its own.  8 sequences of 8000 tokens, 4 kv heads, d = 128: 24.4 us for 8 rows,
+// 28.7 for 16, 37.5 for 32 (8 rows in each of four warps that share keys: 9% more,
+// and 19% for 80 rows; 32 rows in every warp, the queries in shared memory: 20%).
 //
 // The work is one list of steps of 128 keys over all sequences, kv heads and row
 // tiles, cut into equal shares for as many CTAs as run at once, from the lengths
