@@ -559,10 +559,16 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, ROWS>::REGS_FOR) decode_fp8_k
         fetch_page();
         slot ^= 1;
 
-        // ---- at the segment's end: O = sum over the warps with these rows of O_w 2^(M_w - m) / l
+        // ---- at the segment's end: O = sum over the warps with these rows of O_w 2^(M_w - m) / l.  The factor is made
+        // before it meets O_w (a mean of values near the largest bf16 number is in range, their sum is not), from two
+        // halves of the exponent (one power of two is flushed below 2^-126, infinite from 2^128).
         const bool item_ends = cur.s + 1 == cur.n;
         begins = item_ends || it + 1 == count;
         if (begins) {
+            auto factor = [](float M, float m, float l) {
+                const float half = ex2(0.5f * (M - m));
+                return l == 0.f ? 0.f : half * (half / l);  // 0: the row sees no key; NaN stays
+            };
             float f[NB][2];
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
@@ -572,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, ROWS>::REGS_FOR) decode_fp8_k
                     for (int d = 4; d < 32; d <<= 1) l[nb][j] += __shfl_xor_sync(0xffffffffu, l[nb][j], d);
                     const int r = nb * 8 + 2 * t + j;
                     if (KG > 1 && g == 0) s_stat[warp][0][r] = m[nb][j], s_stat[warp][1][r] = l[nb][j];
-                    f[nb][j] = ex2(M[nb][j] - m[nb][j]);
+                    if (KG == 1) f[nb][j] = factor(M[nb][j], m[nb][j], l[nb][j]);
                 }
             if constexpr (KG > 1) {
                 __syncthreads();
@@ -588,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, ROWS>::REGS_FOR) decode_fp8_k
 #pragma unroll
                         for (int w = 0; w < KG; ++w)
                             sum += s_stat[w * RG + rg][1][r] * ex2(s_stat[w * RG + rg][0][r] - top);
-                        f[nb][j] = ex2(M[nb][j] - top);
+                        f[nb][j] = factor(M[nb][j], top, sum);
                         m[nb][j] = top;
                         l[nb][j] = sum;
                         if (kg > 0)
@@ -630,13 +636,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, ROWS>::REGS_FOR) decode_fp8_k
                         const int r = (rg * NB + nb) * 8 + 2 * t + j;
                         if (r >= nrows) continue;
                         const float sum = l[nb][j];
-                        const float scale = sum == 0.f ? 0.f : f[nb][j] / sum;  // 0: the row sees no key; NaN stays
                         const float lse2 = sum == 0.f ? -INFINITY : m[nb][j] + lg2(sum);
                         const long long row = bh * a.rows + cur.rt * ROWS + r;  // (b, head, token) flattened
                         float o[DT];
 #pragma unroll
                         for (int i = 0; i < D / 16; ++i)
-                            o[2 * i] = acc[nb][i][j] * scale, o[2 * i + 1] = acc[nb][i][2 + j] * scale;
+                            o[2 * i] = acc[nb][i][j] * f[nb][j], o[2 * i + 1] = acc[nb][i][2 + j] * f[nb][j];
                         if (whole) {
                             uint4* dst = reinterpret_cast<uint4*>(a.o + row * D + g * DT);
 #pragma unroll
