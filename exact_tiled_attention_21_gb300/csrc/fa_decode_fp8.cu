@@ -36,9 +36,14 @@
 // q is scaled by a power of two per row into fp16's range (exact but for
 // elements 2^-28 below the row's largest).  With x_j the score in log2 units,
 // the softmax sums l = sum 2^(x_j - m) stay in fp32; the V product takes
-// 2^(x_j + log2 vs_j - M) in fp16 (relative 2^-11, an eighth of the result's
-// own bf16 step) with its own reference M, so that a block's scale can have any
-// size.  Result: O 2^(M - m) / l.
+// 2^(x_j + log2 vs_j - M) in fp16 with its own reference M, so that a block's
+// scale can have any size.  M puts the largest weight between 2^11 and 2^15, as
+// high as fp16 goes, so that the rounding is a relative 2^-11 (an eighth of the
+// result's own bf16 step) down to 2^-25 of that weight and 2^-36 of it below: a
+// long flat tail behind a token that takes almost all the weight keeps its value.
+// (References at the maximum lost 12% of O for 65k tokens 2^23.6 below the first,
+// where one warp has a quarter of them; 7 octaves below it with a slack of 8 took
+// the same time.)  Result: O 2^(M - m) / l.
 #include <algorithm>
 #include <cfloat>
 #include <climits>
@@ -52,7 +57,10 @@ namespace {
 constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kKeys = 32, kStep = kWarps * kKeys;  // keys per warp and step, and per CTA
 constexpr int kStages = 2;                         // steps in flight
-constexpr float kSlack = 8.f;  // how far (log2) a score may exceed the reference that its weight is relative to
+constexpr float kSlack = 8.f;  // how far (log2) a score may exceed the reference that its softmax term is relative to
+// The same for the value product, whose weights are fp16: the reference is set so that the largest one is 2^kTopV, and is
+// kept until one would pass 2^(kTopV + kSlackV) = 2^15.  What lies below 2^-14 loses bits, so the range is put to use.
+constexpr float kTopV = 11.f, kSlackV = 4.f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
 
 template <int D, int ROWS_>
@@ -464,9 +472,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, ROWS>::REGS_FOR) decode_fp8_k
                                 }
                             }
                 }
-                // ---- softmax: p = 2^(x - m) into l; w = 2^(x + log2 vs - M) for the value product.  m and M need not be
-                // the maxima, only within 2^8 of them (fp16 holds 2^15): most steps find no larger one and skip the
-                // reductions.
+                // ---- softmax: p = 2^(x - m) into l; w = 2^(x + log2 vs - M) for the value product.  m need not be the
+                // maximum, only within 2^8 of it, and M not 2^11 below, only within 2^4 of that: most steps find no larger
+                // one and skip the reductions.
                 float mx[2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
@@ -501,10 +509,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, ROWS>::REGS_FOR) decode_fp8_k
 #pragma unroll
                     for (int i = 1; i < MT; ++i) mx[j] = fmax3(mx[j], x[i][j], x[i][2 + j]);
                 }
-                if (__any_sync(0xffffffffu, mx[0] > M[nb][0] + kSlack || mx[1] > M[nb][1] + kSlack)) {
+                if (__any_sync(0xffffffffu, mx[0] > M[nb][0] + (kTopV + kSlackV) || mx[1] > M[nb][1] + (kTopV + kSlackV))) {
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        float top = fmaxf(M[nb][j], mx[j]);
+                        float top = fmaxf(M[nb][j], mx[j] - kTopV);
 #pragma unroll
                         for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
                         const float f = ex2(M[nb][j] - top);
@@ -559,17 +567,17 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, ROWS>::REGS_FOR) decode_fp8_k
         fetch_page();
         slot ^= 1;
 
-        // ---- at the segment's end: O = sum over the warps with these rows of O_w 2^(M_w - m) / l.  The factor is made
-        // before it meets O_w (a mean of values near the largest bf16 number is in range, their sum is not), from two
-        // halves of the exponent (one power of two is flushed below 2^-126, infinite from 2^128).
+        // ---- at the segment's end: O = sum over the warps with these rows of O_w 2^(M_w - m) / l.  The factor meets
+        // O_w as two, 2^((M_w - m) / 2) and the same / l: O is in range where O l is not (values near the largest bf16
+        // number), or where 2^(M_w - m) is not (below 2^-126 or subnormal, where every block has the smallest scale).
         const bool item_ends = cur.s + 1 == cur.n;
         begins = item_ends || it + 1 == count;
         if (begins) {
-            auto factor = [](float M, float m, float l) {
-                const float half = ex2(0.5f * (M - m));
-                return l == 0.f ? 0.f : half * (half / l);  // 0: the row sees no key; NaN stays
+            float f[NB][2], fl[NB][2];
+            auto factors = [](float M, float m, float l, float& f, float& fl) {
+                f = ex2(0.5f * (M - m));
+                fl = l == 0.f ? 0.f : f / l;  // 0: the row sees no key; NaN stays
             };
-            float f[NB][2];
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -578,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, ROWS>::REGS_FOR) decode_fp8_k
                     for (int d = 4; d < 32; d <<= 1) l[nb][j] += __shfl_xor_sync(0xffffffffu, l[nb][j], d);
                     const int r = nb * 8 + 2 * t + j;
                     if (KG > 1 && g == 0) s_stat[warp][0][r] = m[nb][j], s_stat[warp][1][r] = l[nb][j];
-                    if (KG == 1) f[nb][j] = factor(M[nb][j], m[nb][j], l[nb][j]);
+                    if (KG == 1) factors(M[nb][j], m[nb][j], l[nb][j], f[nb][j], fl[nb][j]);
                 }
             if constexpr (KG > 1) {
                 __syncthreads();
@@ -594,14 +602,15 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, ROWS>::REGS_FOR) decode_fp8_k
 #pragma unroll
                         for (int w = 0; w < KG; ++w)
                             sum += s_stat[w * RG + rg][1][r] * ex2(s_stat[w * RG + rg][0][r] - top);
-                        f[nb][j] = factor(M[nb][j], top, sum);
+                        factors(M[nb][j], top, sum, f[nb][j], fl[nb][j]);
                         m[nb][j] = top;
                         l[nb][j] = sum;
                         if (kg > 0)
 #pragma unroll
                             for (int i = 0; i < D / 16; ++i)
                                 *reinterpret_cast<float2*>(buf + ((warp - RG) * 8 * NB + r) * C::OROW + i * 16) =
-                                    make_float2(acc[nb][i][j] * f[nb][j], acc[nb][i][2 + j] * f[nb][j]);
+                                    make_float2(acc[nb][i][j] * f[nb][j] * fl[nb][j],
+                                                acc[nb][i][2 + j] * f[nb][j] * fl[nb][j]);
                     }
                 __syncthreads();
                 if (kg == 0) {
@@ -611,7 +620,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, ROWS>::REGS_FOR) decode_fp8_k
                         for (int j = 0; j < 2; ++j) {
 #pragma unroll
                             for (int i = 0; i < D / 16; ++i) {
-                                float2 x = make_float2(acc[nb][i][j] * f[nb][j], acc[nb][i][2 + j] * f[nb][j]);
+                                float2 x = make_float2(acc[nb][i][j] * f[nb][j] * fl[nb][j],
+                                                       acc[nb][i][2 + j] * f[nb][j] * fl[nb][j]);
 #pragma unroll
                                 for (int w = 1; w < KG; ++w) {
                                     const float2 y = *reinterpret_cast<const float2*>(
@@ -622,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, ROWS>::REGS_FOR) decode_fp8_k
                                 acc[nb][i][j] = x.x;
                                 acc[nb][i][2 + j] = x.y;
                             }
-                            f[nb][j] = 1.f;
+                            f[nb][j] = fl[nb][j] = 1.f;
                         }
                 }
             }
@@ -641,7 +651,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, ROWS>::REGS_FOR) decode_fp8_k
                         float o[DT];
 #pragma unroll
                         for (int i = 0; i < D / 16; ++i)
-                            o[2 * i] = acc[nb][i][j] * f[nb][j], o[2 * i + 1] = acc[nb][i][2 + j] * f[nb][j];
+                            o[2 * i] = acc[nb][i][j] * f[nb][j] * fl[nb][j],
+                                  o[2 * i + 1] = acc[nb][i][2 + j] * f[nb][j] * fl[nb][j];
                         if (whole) {
                             uint4* dst = reinterpret_cast<uint4*>(a.o + row * D + g * DT);
 #pragma unroll

@@ -380,8 +380,9 @@ size_t fa_decode_paged_fp8_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d
  * [B, Hq, Nq, d]; lse fp32 [B, Hq, Nq] or NULL.  Query head h reads kv head h /
  * (Hq / Hkv); query t sees the tokens j <= seq_lens[b] - Nq + t (the bottom-right
  * mask of fa_fwd).  A query that sees none (an empty sequence) gets O = 0,
- * LSE = -inf.  Scores and sums are fp32; the softmax weights are rounded to fp16
- * (relative 2^-11) for the value product only.
+ * LSE = -inf.  Scores and sums are fp32; for the value product only, a softmax
+ * weight times its block's V scale is rounded to fp16: by 2^-11 of itself, or,
+ * where it is below 2^-25 of the largest one of its row, by 2^-36 of that.
  * weights fp32 [B, Hkv, max_pages * page_size] or NULL: weights[b, kvh, j] +=
  * the sum of token j's attention weights over the group's heads and the Nq
  * queries (what fa_cache_evict_fp8 selects by); tokens >= seq_lens[b] are left
