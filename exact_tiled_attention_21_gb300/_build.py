@@ -41,28 +41,32 @@ def _stale(srcs, out):
 TORCH_OBJ = os.path.join(BUILD, "fa_torch.o")
 
 
+def _torch_stamp():
+    """The file that names the torch which TORCH_LIB was compiled and linked against."""
+    return os.path.join(BUILD, "fa_torch.version")
+
+
 def _cxx():
     return shutil.which("g++") or "g++"
 
 
 def _build_torch(run, force):
     """Compiles the native binding against the torch that is installed here, if the source, the C ABI or that torch is
-    another one; whether it did."""
+    another one."""
     import sysconfig
     import torch
-    src, made_for = os.path.join(CSRC, "fa_torch.cpp"), os.path.join(BUILD, "fa_torch.version")
+    src, stamp = os.path.join(CSRC, "fa_torch.cpp"), _torch_stamp()
     if not force and not _stale([src, os.path.join(ROOT, "include", "fa.h")], TORCH_OBJ):
-        if os.path.exists(made_for) and open(made_for).read() == torch.__version__:
-            return False
+        if os.path.exists(stamp) and open(stamp).read() == torch.__version__:
+            return
+    if os.path.exists(stamp):
+        os.remove(stamp)  # until the binding is linked
     root = os.path.dirname(torch.__file__)
     inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
            sysconfig.get_path("include"), os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
     run([_cxx(), "-O2", "-std=c++20", "-fPIC", "-fvisibility=hidden",
          "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI)] + ["-isystem" + i for i in inc]
         + ["-c", src, "-o", TORCH_OBJ])
-    with open(made_for, "w") as f:
-        f.write(torch.__version__)
-    return True
 
 
 def _torch_link(out):
@@ -96,15 +100,18 @@ def build(force=False, verbose=False, ptxas_info=False):
         for out in ex.map(run, jobs):
             if verbose and out.strip():
                 print(out)
-        compiled = binding.result()
+        binding.result()
     if force or jobs or _stale(objs, LIB):
         tmp = LIB + ".tmp%d" % os.getpid()
         run([cc] + ARCH + ["-shared", "-cudart", "static", "-o", tmp] + objs)
         os.replace(tmp, LIB)
-    if compiled or not os.path.exists(TORCH_LIB):
+    if force or not os.path.exists(_torch_stamp()) or _stale([TORCH_OBJ], TORCH_LIB):
+        import torch
         tmp = TORCH_LIB + ".tmp%d" % os.getpid()
         run(_torch_link(tmp))
         os.replace(tmp, TORCH_LIB)
+        with open(_torch_stamp(), "w") as f:
+            f.write(torch.__version__)
     return LIB
 
 
