@@ -157,7 +157,7 @@ __device__ __forceinline__ void advance(Cursor& c, const Params& a, int cap) {
     c.kvh = 0;
     do {
         ++c.b;
-        c.len = c.b < a.B ? clamp_len(__ldg(a.lens + c.b), cap) : 0;
+        c.len = c.b < a.B ? clamp_len(a.lens[c.b], cap) : 0;
     } while (c.len == 0 && c.b < a.B);
     c.n = (c.len + kStep - 1) / kStep;
 }
@@ -296,7 +296,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, ROWS>::REGS_FOR) decode_fp8_k
         }
     };
     // Scales are loaded, not copied (a 4-byte copy asks L2 once per lane, a load once per sector), and put into the
-    // ring one step later, when they have arrived; V's as logarithms.
+    // ring one step later, when they have arrived; V's as logarithms.  Plain loads here and of the lengths: the read-only
+    // path is for data that stays as it is while the kernel runs, and this one starts before its wait for the append.
     float ks_next = 0.f, vs_next = 0.f;
     auto put_scales = [&](int slot, float ks, float vs) {
         float* f = reinterpret_cast<float*>(ring + slot * C::SLOT + 2 * C::HALF) + lane;
@@ -331,8 +332,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, ROWS>::REGS_FOR) decode_fp8_k
             const uint32_t head = (uint32_t)pg * a.Hkv + to_issue.kvh;
             const uint32_t row = ok ? head * P + at : ~0u;  // cache row of the lane's key, ~0 for none
             const uint32_t blk = ok ? head * a.blocks_per_page + a.sb.div(at) : 0u;
-            ks = ok ? __ldg(a.ks + blk) : 0.f;
-            vs = ok ? __ldg(a.vs + blk) : 0.f;
+            ks = ok ? a.ks[blk] : 0.f;
+            vs = ok ? a.vs[blk] : 0.f;
             if (__all_sync(0xffffffffu, ok))
                 copy(ring_u + slot * C::SLOT, row, true);
             else

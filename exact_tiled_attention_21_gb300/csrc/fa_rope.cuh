@@ -41,7 +41,7 @@ __device__ __forceinline__ void turn_cos_sin(int pos, uint64_t turns, float mag,
 __device__ __forceinline__ void task_cos_sin(int pos, const uint64_t* turns, float mag, float (&c)[8], float (&s)[8]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const ulonglong2 f = __ldg(reinterpret_cast<const ulonglong2*>(turns) + i);
+        const ulonglong2 f = reinterpret_cast<const ulonglong2*>(turns)[i];
         turn_cos_sin(pos, f.x, mag, c[2 * i], s[2 * i]);
         turn_cos_sin(pos, f.y, mag, c[2 * i + 1], s[2 * i + 1]);
     }

@@ -1,0 +1,66 @@
+"""The serving-cache calls as a program chains them: one behind the other without a wait of the host."""
+import numpy as np
+import pytest
+import torch
+
+from tests.cache_fp8_common import DEV, args, bf16, ints, random_cache, table_of, to_gpu
+
+pytestmark = pytest.mark.gpu
+
+
+def _ok(fa):
+    st, detail = fa.fa_get_last_device_error()
+    assert st == 0, detail
+
+
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("d,Hkv,G,page,sb", [(128, 4, 4, 64, 32), (64, 8, 1, 16, 8), (128, 2, 16, 32, 32)])
+def test_chain_without_waits_is_the_chain_with_them(cuda_lib, d, Hkv, G, page, sb, captured):
+    """Append (whose blocks' scales grow), decode with weights and eviction, twice over, then a second round on the
+    evicted cache: every output and the whole cache are bit for bit those of the same calls with the device idle in
+    between.  Each kernel reads what the one before wrote: scales, lengths, weights."""
+    fa, B, steps = cuda_lib, 5, 6
+    rng = np.random.default_rng(d + Hkv)
+    lens0 = np.array([333, 7, 0, 129, 500], dtype=np.int32)
+    maxp, newp = -(-520 // page), -(-200 // page)
+    c = random_cache(3, B * (maxp + newp), Hkv, page, sb, d)
+    both = table_of(4, B, maxp + newp, B * (maxp + newp))
+    tab, new = ints(both[:, :maxp]), ints(both[:, maxp:])
+    turns = fa.rope_table(10000.0 ** (-2.0 * np.arange(d // 2) / d))
+    kv = [[(bf16(rng, (B, Hkv, 3, d), 0.3) * 1.5 ** i).to(DEV) for _ in range(2)] for i in range(steps)]
+    qs = [bf16(rng, (B, Hkv * G, 1, d), 0.3).to(DEV) for _ in range(steps)]
+
+    def program(g, lens, w, wait):
+        out, t = [], tab
+        for i in range(steps):
+            fa.cache_append_fp8(kv[i][0], kv[i][1], *args(g), t, lens, turns=turns)
+            wait()
+            lens = lens + 3
+            wait()
+            out += fa.decode_paged_fp8(fa.rope(qs[i], turns, (lens - 1)[:, None].contiguous()), *args(g), t, lens, weights=w)
+            wait()
+            if i == steps // 2:
+                lens, w, kept = fa.cache_evict_fp8(*args(g), t, lens, w, new, 150, 20)
+                wait()
+                out, t = out + [kept], new
+        return out + [lens, w] + list(args(g))
+
+    want = program(to_gpu(c), ints(lens0), torch.zeros((B, Hkv, maxp * page), device=DEV), torch.cuda.synchronize)
+    g, lens, w = to_gpu(c), ints(lens0), torch.zeros((B, Hkv, maxp * page), device=DEV)
+    start = [t.clone() for t in args(g)]
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            got = program(g, lens, w, lambda: None)
+    for _ in range(5):
+        for t, s in zip(args(g), start):
+            t.copy_(s)
+        w.zero_()
+        if captured:
+            graph.replay()
+        else:
+            got = program(g, lens, w, lambda: None)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    _ok(fa)
