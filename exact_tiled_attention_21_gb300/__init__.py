@@ -541,9 +541,12 @@ def _need(ok, what):
 
 
 def _on_stream(stream, t):
-    """torch's current stream set to ``stream``, so that what a call allocates belongs to the stream that uses it."""
+    """torch's current stream set to ``stream``, so that what a call allocates belongs to the stream that uses it.
+    A handle of 0 is the default stream (of which ExternalStream would make a new one)."""
     if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=t.device)
+        handle = int(stream)
+        stream = torch.cuda.ExternalStream(handle, device=t.device) if handle else torch.cuda.default_stream(t.device)
+    _need(stream.device == t.device, "stream is on another device than the tensors")
     return torch.cuda.stream(stream)
 
 

@@ -1,4 +1,4 @@
-"""The serving-cache calls as a program chains them: one behind the other without a wait of the host."""
+"""The serving-cache calls as a program chains them: one behind the other without a wait of the host, on any stream."""
 import numpy as np
 import pytest
 import torch
@@ -64,3 +64,18 @@ def test_chain_without_waits_is_the_chain_with_them(cuda_lib, d, Hkv, G, page, s
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
     _ok(fa)
+
+
+def test_stream_handles(cuda_lib):
+    """0 is the default stream, as for the framework's other calls, and any other handle itself."""
+    x = torch.zeros((1, 1, 8, 64), dtype=torch.bfloat16, device=DEV)
+    s = torch.cuda.Stream()
+    for stream, handle in ((0, 0), (s, s.cuda_stream), (s.cuda_stream, s.cuda_stream), (torch.cuda.default_stream(), 0)):
+        with cuda_lib._on_stream(stream, x):
+            assert torch.cuda.current_stream().cuda_stream == handle
+    want = torch.zeros((1, 1, 8, 64), dtype=torch.bfloat16, device=DEV)
+    turns = cuda_lib.rope_table([0.5] * 32)
+    for i in range(20):                      # ordered behind what the default stream does before it
+        x.fill_(i + 1)
+        y = cuda_lib.rope(x, turns, positions=ints([[0] * 8]), stream=0)
+        assert torch.equal(y, want + (i + 1))
