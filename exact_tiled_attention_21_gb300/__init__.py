@@ -12,7 +12,9 @@ workspace with torch and then call the same entry points.  So are those of the
 serving cache held in 8 bits, ``rope``, ``cache_append_fp8``,
 ``decode_paged_fp8`` and ``cache_evict_fp8``, through a compiled binding
 (``csrc/fa_torch.cpp``, ``_fa_torch.so``), since their small calls take less time
-on the GPU than ctypes does on the host.
+on the GPU than ctypes does on the host.  Only ``rope`` takes part in autograd;
+the others return results that record no gradient (``backward`` is called for
+it).
 
 There is no fallback: if the shared library is missing, or a call returns an
 error status, a ``FAError`` is raised.
@@ -586,14 +588,36 @@ def rope_table(inv_freq, device="cuda"):
     return torch.tensor([t - (1 << 64) if t >= 1 << 63 else t for t in turns], dtype=torch.int64, device=device)
 
 
+class _Rope(torch.autograd.Function):
+    """rope where a gradient is recorded: the gradient is the rotation by the opposite angles."""
+
+    @staticmethod
+    def forward(ctx, x, turns, positions, interleaved, magnitude, inverse):
+        ctx.save_for_backward(turns, positions)
+        ctx.form = interleaved, magnitude, inverse
+        return rope(x, turns, positions, interleaved, magnitude, inverse)
+
+    @staticmethod
+    def backward(ctx, g):
+        turns, positions = ctx.saved_tensors
+        interleaved, magnitude, inverse = ctx.form
+        if g.stride(3) != 1 or g.data_ptr() % 16 or any(s % 8 for s in g.stride()[:3]):
+            g = g.clone(memory_format=torch.contiguous_format)  # rows that the kernel does not take
+        return (rope(g, turns, positions, interleaved, magnitude, not inverse),) + (None,) * 5
+
+
 def rope(x, turns, positions=None, interleaved=False, magnitude=1.0, inverse=False, out=None, stream=None):
     """x [B,H,N,d] (bf16, any strides that fa_rope takes) rotated by its tokens' positions: pairs 0 .. len(turns) - 1,
     the columns behind them copied.  turns: rope_table(...).  positions: int32 [B,N] on the device, or None (0..N-1).
-    inverse=True turns back: the gradient of x from the gradient of the result.  out: where to write (may be x);
-    default a new contiguous tensor."""
+    inverse=True turns back: the gradient of x from the gradient of the result.  out: where to write (may be x, but not
+    overlap it otherwise); default a new contiguous tensor.  Where x requires a gradient, the result records it (out
+    must then be None)."""
     if stream is not None:
         with _on_stream(stream, x):
             return rope(x, turns, positions, interleaved, magnitude, inverse, out)
+    if (getattr(x, "requires_grad", False) or getattr(out, "requires_grad", False)) and torch.is_grad_enabled():
+        _need(out is None, "out does not record a gradient: call under torch.no_grad(), or without out")
+        return _Rope.apply(x, turns, positions, interleaved, magnitude, inverse)
     r = (_torch_binding or _native()).rope(x, turns, positions, interleaved, magnitude, inverse, out)
     if r.__class__ is int:
         raise FAError(r, "fa_rope")
