@@ -41,6 +41,12 @@ void* optional(PyObject* o, const char* name, at::ScalarType type, at::IntArrayR
     return o == Py_None ? nullptr : checked(o, name, type, shape, dev);
 }
 
+// Counts a write in place, so that autograd refuses a gradient that would take the old values.
+void written(const Tensor& t) {
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();  // inference tensors have no counter
+}
+void written(PyObject* o) { written(THPVariable_Unpack(o)); }
+
 // A bf16 CUDA tensor [B, H, N, d] whose innermost dimension is dense.
 const Tensor& bhnd(PyObject* o, const char* name) {
     const Tensor& t = tensor(o, name);
@@ -159,7 +165,9 @@ PyObject* rope(PyObject*, PyObject* const* o, Py_ssize_t n) {
         return fa_rope(x.data_ptr(), y.data_ptr(), x.stride(0), x.stride(1), x.stride(2), y.stride(0), y.stride(1),
                        y.stride(2), pos, turns, B, H, N, d, rot, inter, magnitude, inverse, stream);
     });
-    return st == FA_OK ? THPVariable_Wrap(y) : status(st);
+    if (st != FA_OK) return status(st);
+    if (o[6] != Py_None) written(y);
+    return THPVariable_Wrap(y);
     END_HANDLE_TH_ERRORS
 }
 
@@ -182,12 +190,15 @@ PyObject* append(PyObject*, PyObject* const* o, Py_ssize_t n) {
     const float magnitude = number(o[12]);
     const c10::cuda::CUDAGuard guard(c.dev);
     void* stream = stream_of(c.dev);
-    return status(call([&] {
+    const int st = call([&] {
         return fa_cache_append_fp8(k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), k.stride(2), v.stride(0),
                                    v.stride(1), v.stride(2), c.k, c.v, (float*)c.ks, (float*)c.vs, (const int*)c.table,
                                    (const int*)c.lens, fresh, pos, turns, c.B, c.Hkv, N, c.d, rot, inter, magnitude,
                                    c.page, c.sb, c.max_pages, c.num_pages, stream);
-    }));
+    });
+    if (st == FA_OK)
+        for (int i = 2; i < 6; ++i) written(o[i]);
+    return status(st);
     END_HANDLE_TH_ERRORS
 }
 
@@ -224,6 +235,7 @@ PyObject* decode(PyObject*, PyObject* const* o, Py_ssize_t n) {
                                    c.page, c.sb, c.max_pages, c.num_pages, c.d, scale, ws.data_ptr(), ws.nbytes(), stream);
     });
     if (st != FA_OK) return status(st);
+    if (weights) written(o[8]);
     return Py_BuildValue("(NN)", THPVariable_Wrap(out), THPVariable_Wrap(lse));
     END_HANDLE_TH_ERRORS
 }
@@ -249,6 +261,7 @@ PyObject* evict(PyObject*, PyObject* const* o, Py_ssize_t n) {
                                   c.page, c.sb, c.max_pages, new_max_pages, c.num_pages, c.d, keep, recent, stream);
     });
     if (st != FA_OK) return status(st);
+    for (int i = 0; i < 4; ++i) written(o[i]);
     return Py_BuildValue("(NNN)", THPVariable_Wrap(lens), THPVariable_Wrap(w), THPVariable_Wrap(kept));
     END_HANDLE_TH_ERRORS
 }
