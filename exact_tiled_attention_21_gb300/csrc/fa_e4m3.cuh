@@ -59,6 +59,10 @@ __device__ __forceinline__ uint4 e4m3_rescale16(uint4 x, float from, float to) {
         }
         return x;
     }
+    // Both scales times the same power of two: a value times a scale near either end of the range would overflow or lose
+    // its low bits.
+    const float shift = to >= 1.f ? 0x1p-32f : 0x1p32f;
+    from *= shift, to *= shift;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const float2 a = half2_to_float2(e4m3x2_to_half2(w[i])), b = half2_to_float2(e4m3x2_hi_to_half2(w[i]));
