@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(2 * HALF, kAppendThreads<TPT> / (2 * HALF))
         n = min(min(max(n, 0), a.N), cap - len);
     }
     const int first = ((int)plan.sb.div(len) + unit * plan.unit) * a.sb;  // the CTA's first token
-    if (first >= len + n) return;
+    if (n == 0 || first >= len + n) return;  // without new tokens the block that len lies in is not touched either
     const int t0 = max(len - first, 0), t1 = min(plan.unit * a.sb, len + n - first);  // its new tokens [t0, t1)
     // the thread's block: its first token (of the CTA's), the earlier tokens in it, its page and place in it
     const int own = SEV ? (int)plan.sb.div(tid / TPR) * a.sb : 0, begin = first + own;

@@ -349,8 +349,9 @@ int fa_rope(const void *x, void *y, long long x_sb, long long x_sh, long long x_
  * fa_rope's x.  Sequence b has seq_lens[b] tokens in the cache and gets its
  * first n_b = new_lens[b] (0..N; NULL: N) tokens at seq_lens[b], seq_lens[b] + 1,
  * ...; tokens that would not fit max_pages * page_size are left out and
- * recorded.  seq_lens is not changed.  B * Hkv * N <= 2^31 - 1
- * and N <= 2^29 (FA_ERR_UNSUPPORTED).  If turns is not NULL, K is rotated first
+ * recorded.  seq_lens is not changed, and a sequence with n_b = 0 is not
+ * touched, nor its table's pages looked at.  B * Hkv * N <= 2^31 - 1 and
+ * N <= 2^29 (FA_ERR_UNSUPPORTED).  If turns is not NULL, K is rotated first
  * as by fa_rope (same arguments; positions NULL: seq_lens[b] + i) and rounded
  * to bf16: the result is, bit for bit, that of fa_rope followed by this call
  * without turns.  With turns NULL, rot, interleaved, magnitude and positions

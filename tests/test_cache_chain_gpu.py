@@ -1,9 +1,11 @@
-"""The serving-cache calls as a program chains them: one behind the other without a wait of the host, on any stream."""
+"""The serving-cache calls as a program chains them: one behind the other without a wait of the host, on any stream,
+with sequences that pause."""
 import numpy as np
 import pytest
 import torch
 
-from tests.cache_fp8_common import DEV, args, bf16, ints, random_cache, table_of, to_gpu
+from oracle import cache as oc
+from tests.cache_fp8_common import DEV, args, assert_same_cache, bf16, copy, f64, ints, random_cache, table_of, to_gpu
 
 pytestmark = pytest.mark.gpu
 
@@ -79,3 +81,21 @@ def test_stream_handles(cuda_lib):
         x.fill_(i + 1)
         y = cuda_lib.rope(x, turns, positions=ints([[0] * 8]), stream=0)
         assert torch.equal(y, want + (i + 1))
+
+
+def test_append_leaves_paused_sequences_alone(cuda_lib):
+    """A sequence without new tokens is not touched, even in the middle of a block: neither its scale (here a subnormal
+    one, which a write would raise) nor its table, whose pages may be gone."""
+    Hkv, d, page, sb = 2, 64, 16, 8
+    rng = np.random.default_rng(1)
+    c = random_cache(2, 6, Hkv, page, sb, d)
+    c["ks"][1] = 2.0 ** -140
+    table = np.array([[0, 3], [1, -1], [-1, -1]], dtype=np.int32)
+    k = bf16(rng, (3, Hkv, 4, d))
+    for lens, new in (([5, 3, 20], [4, 0, 0]), ([8, 11, 0], [0, 0, 0])):
+        g = to_gpu(c)
+        cuda_lib.cache_append_fp8(k.to(DEV), k.to(DEV), *args(g), ints(table), ints(lens), ints(new))
+        _ok(cuda_lib)
+        ref = copy(c)
+        oc.append(ref, table, lens, f64(k), f64(k), new)
+        assert_same_cache(g, ref)
