@@ -818,11 +818,12 @@ int fa_rope_table(const double* inv_freq, int n, uint64_t* turns) {
     for (int i = 0; i < n; ++i)
         if (!std::isfinite(inv_freq[i])) return FA_ERR_INVALID_ARG;
     for (int i = 0; i < n; ++i) {
-        const double t = inv_freq[i] / 6.283185307179586;  // turns per position; whole turns drop out
-        const double f = t - std::floor(t);                // [0, 1]
+        const double t = std::fabs(inv_freq[i]) / 6.283185307179586;  // turns per position; whole turns drop out
+        const double f = t - std::floor(t);                           // [0, 1), exact
         // 2^64 f in two 32-bit steps, each exact in a double
         const double hi = std::floor(f * 4294967296.0), lo = std::nearbyint((f * 4294967296.0 - hi) * 4294967296.0);
-        turns[i] = ((uint64_t)hi << 32) + (uint64_t)lo;
+        const uint64_t u = ((uint64_t)hi << 32) + (uint64_t)lo;
+        turns[i] = inv_freq[i] < 0 ? 0 - u : u;  // modulo a turn; 1 - f would lose the low bits of a small f
     }
     return FA_OK;
 }

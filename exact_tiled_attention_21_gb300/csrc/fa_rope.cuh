@@ -2,9 +2,10 @@
 //
 // Pair i of a head turns by pos * f_i radians.  The frequencies come as turns
 // per position, in units of 2^-64 turn: pos * turns mod 2^64 is then the exact
-// fraction of a turn for every 32-bit position, in one 64-bit integer product,
-// where pos * f_i in fp32 is off by up to 2^-24 pos f_i radians (0.008 at
-// position 131072), and fp64 has no throughput to speak of on this GPU.
+// fraction of a turn for every 32-bit position, in one 64-bit integer product
+// (what is left is the table's own 2^-52 pos f_i), where pos * f_i in fp32 is off
+// by up to 2^-24 pos f_i radians (0.008 at position 131072), and fp64 has no
+// throughput to speak of on this GPU.
 #pragma once
 
 #include "fa_ptx.cuh"

@@ -321,10 +321,11 @@ int fa_decode_paged(const void *q, const void *k_pages, const void *v_pages, con
  * page_size must stay below 2^32 - 1 (FA_ERR_UNSUPPORTED). */
 
 /* Turns per position for fa_rope and fa_cache_append_fp8: turns[i] =
- * inv_freq[i] / (2 pi) modulo whole turns, in units of 2^-64 turn.  inv_freq[i]
- * (finite, host memory) is pair i's angle per position in radians; scalings for
- * long contexts change these frequencies (and the magnitude below).  n >= 1.
- * Host only; copy the n values to the device. */
+ * inv_freq[i] / (2 pi) modulo whole turns, in units of 2^-64 turn: the quotient
+ * as a double has it (within 2^-52 of itself), rounded to 2^-65 turn; -x gives
+ * the negative of x's.  inv_freq[i] (finite, host memory) is pair i's angle per
+ * position in radians; scalings for long contexts change these frequencies (and
+ * the magnitude below).  n >= 1.  Host only; copy the n values to the device. */
 int fa_rope_table(const double *inv_freq, int n, uint64_t *turns);
 
 /* Rotary positions.  x and y: bf16 [B, H, N, d] with element strides (sb, sh,
@@ -337,8 +338,10 @@ int fa_rope_table(const double *inv_freq, int n, uint64_t *turns);
  * where the pair is columns (2i, 2i + 1) if interleaved, else (i, i + rot / 2);
  * columns from rot on are copied.  inverse = 1 turns by -a with the same
  * magnitude: the transpose, i.e. the gradient of x from the gradient of y.  The
- * angle is reduced exactly at any position (see fa_rope_table); cos and sin are
- * within 2^-23; computed in fp32, rounded to bf16 once.  rot: a multiple of 16
+ * angle of the table's turns is reduced exactly at any position, and its cos and
+ * sin are within 2^-23; the table itself is off by at most 2^-52 |p inv_freq[i]| +
+ * 2^-62 |p| radians (below 2^-24 up to 2^27 radians).  Computed in fp32, rounded
+ * to bf16 once.  rot: a multiple of 16
  * (FA_ERR_UNSUPPORTED), 16 <= rot <= d; turns: device [rot / 2], 16-byte
  * aligned; magnitude finite.  B * N <= 2^31 - 1, B * H <= 2^24. */
 int fa_rope(const void *x, void *y, long long x_sb, long long x_sh, long long x_sn, long long y_sb,
