@@ -351,6 +351,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, ROWS>::REGS_FOR) decode_fp8_k
         else
             bar_sync(2, RG * 32);
     };
+    // Where the D / 8 bytes of columns col D / 8 ... of a stage's key are, among the V bytes.
+    auto v_piece = [&](int key, int col) {
+        const int i = key / 16, t2 = key % 8 / 2, r = key % 2 + key % 16 / 8 * 2;
+        if constexpr (D == 128) return ((i * 4 + r) * 16 + 4 * (col >> 1) + (t2 ^ (col >> 1))) * 32 + (col & 1) * 16;
+        return ((i * 4 + r) * 8 + 4 * (col >> 2) + (t2 ^ ((col >> 2) | (r & 1) << 1))) * 32 + (col & 3) * 8;
+    };
+    // The high bits of the NaN bytes of a word of e4m3.
+    auto nan_bytes = [](uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; };
     static_assert(kStages == 2, "the start");
     {   // the loads of the first steps depend on each other (lengths, pages, rows): the queries' come in between
         uint32_t w[NB][D / 8];
@@ -399,6 +407,48 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, ROWS>::REGS_FOR) decode_fp8_k
         }
         cp_async_wait<kStages - 1>();
         group_sync();  // every lane's copies are there
+        // A value product multiplies a key's V by the zero weights of the rows that do not see it, and 0 NaN is NaN.  Of
+        // the keys that some rows do not see (the last Nq - 1) NaN bytes are put into the sums of the rows that do, and
+        // become zeros in the stage.
+        if (a.Nq > 1 && cur.s * kStep + (kg + 1) * RG * kKeys > cur.len - a.Nq + 1) {
+            const int part0 = kg * RG, base = cur.s * kStep + part0 * kKeys;  // the group's first key of this step
+            const int from = max(cur.len - a.Nq + 1 - base, 0), to = min(cur.len - base, RG * kKeys);
+            auto v_word = [&](int key, int col, int c) {  // columns col DT + 4 c .. + 3 of one of the group's keys
+                return reinterpret_cast<uint32_t*>(smem + (part0 + key / kKeys) * C::RING + slot * C::SLOT + C::HALF +
+                                                   v_piece(key % kKeys, col)) + c;
+            };
+            const int my = lane % (D / 4);  // the lane's word of a row
+            bool nan = false;
+            for (int key = from; key < to; ++key) nan |= nan_bytes(*v_word(key, my / (DT / 4), my % (DT / 4))) != 0;
+            if (__any_sync(0xffffffffu, nan)) {  // in all warps of the group alike
+#pragma unroll 1
+                for (int key = from; key < to; ++key) {
+                    const uint32_t* w = v_word(key, g, 0);
+#pragma unroll
+                    for (int c = 0; c < DT / 4; ++c) {
+                        const uint32_t z = nan_bytes(w[c]);
+#pragma unroll
+                        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                const bool sees = base + key <= cur.len - a.Nq + (r0 + nb * 8 + 2 * t + j) % a.Nq;
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)  // column 4 c + e
+                                    if (sees && (z >> (8 * e + 7) & 1))
+                                        acc[nb][2 * c + e / 2][e % 2 * 2 + j] = __int_as_float(0x7FFFFFFF);
+                            }
+                    }
+                }
+                group_sync();  // every warp has read them
+#pragma unroll 1
+                for (int key = from; key < to; ++key)
+                    if (key / kKeys == rg && lane < D / 4) {
+                        uint32_t* w = v_word(key, my / (DT / 4), my % (DT / 4));
+                        *w &= ~((nan_bytes(*w) >> 7) * 0xFFu);
+                    }
+                group_sync();
+            }
+        }
 #pragma unroll 1
         for (int part = 0; part < RG; ++part) {
             const int key0 = cur.s * kStep + (kg * RG + part) * kKeys;

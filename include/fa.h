@@ -396,9 +396,9 @@ size_t fa_decode_paged_fp8_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d
  * not depend on the run (fixed order of additions), but for rounding on the
  * batch that a sequence is in.  Steps of 128 tokens over all sequences at full
  * capacity, kv heads and tiles of 32 query rows must stay below 2^31
- * (FA_ERR_UNSUPPORTED).  Tokens past seq_lens[b] are never used.  A NaN in V
- * reaches every query of its sequence and kv head, also those of the Nq that do
- * not see its token.  No output may overlap an input or the cache (o = q:
+ * (FA_ERR_UNSUPPORTED).  Tokens past seq_lens[b] are never used, and one that a
+ * query does not see does not reach it, whatever it holds (a padded draft's NaN
+ * too).  No output may overlap an input or the cache (o = q:
  * FA_ERR_INVALID_ARG).  workspace: 16-byte aligned, at least
  * fa_decode_paged_fp8_workspace_bytes(...); contents do not matter; calls that
  * may overlap need one each. */
