@@ -169,7 +169,10 @@ __device__ __forceinline__ long long scores_at(const Params& a, long long bh, in
     return (bh * ((a.rows + 3) & ~3) + rt * ROWS) * cap;
 }
 
-template <int D, int ROWS>
+// DRAFTS: more than one new token per sequence.  (8 sequences of 8000 tokens, 4 kv heads, d = 128, back to back: the code
+// for keys that some rows do not see takes 26.3 us with 16 rows and 35.3 with 32, whether it runs or not; without it 25.3
+// and 33.7.)
+template <int D, int ROWS, bool DRAFTS>
 __global__ void __launch_bounds__(kThreads, Cfg<D, ROWS>::REGS_FOR) decode_fp8_kernel(const Params a) {
     using C = Cfg<D, ROWS>;
     constexpr int MT = kKeys / 16, KS = D / 16, DT = D / 8, NB = C::NB, RG = C::RG, KG = C::KG;
@@ -181,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, ROWS>::REGS_FOR) decode_fp8_k
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int rg = warp % RG, kg = warp / RG;  // row group, and group of warps that share keys
-    const int P = (int)a.page.d, cap = a.max_pages * P;
+    const int P = (int)a.page.d, cap = a.max_pages * P, Nq = DRAFTS ? a.Nq : 1;
     if (blockIdx.x == 0)
         for (int i = tid; i < a.B; i += kThreads)
             if (a.lens[i] < 0 || a.lens[i] > cap) record_invalid(a.err, kSiteCacheLen, a.lens[i]);
@@ -410,9 +413,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, ROWS>::REGS_FOR) decode_fp8_k
         // A value product multiplies a key's V by the zero weights of the rows that do not see it, and 0 NaN is NaN.  Of
         // the keys that some rows do not see (the last Nq - 1) NaN bytes are put into the sums of the rows that do, and
         // become zeros in the stage.
-        if (a.Nq > 1 && cur.s * kStep + (kg + 1) * RG * kKeys > cur.len - a.Nq + 1) {
+        if (DRAFTS && cur.s * kStep + (kg + 1) * RG * kKeys > cur.len - Nq + 1) {
             const int part0 = kg * RG, base = cur.s * kStep + part0 * kKeys;  // the group's first key of this step
-            const int from = max(cur.len - a.Nq + 1 - base, 0), to = min(cur.len - base, RG * kKeys);
+            const int from = max(cur.len - Nq + 1 - base, 0), to = min(cur.len - base, RG * kKeys);
             auto v_word = [&](int key, int col, int c) {  // columns col DT + 4 c .. + 3 of one of the group's keys
                 return reinterpret_cast<uint32_t*>(smem + (part0 + key / kKeys) * C::RING + slot * C::SLOT + C::HALF +
                                                    v_piece(key % kKeys, col)) + c;
@@ -431,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, ROWS>::REGS_FOR) decode_fp8_k
                         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                             for (int j = 0; j < 2; ++j) {
-                                const bool sees = base + key <= cur.len - a.Nq + (r0 + nb * 8 + 2 * t + j) % a.Nq;
+                                const bool sees = base + key <= cur.len - Nq + (r0 + nb * 8 + 2 * t + j) % Nq;
 #pragma unroll
                                 for (int e = 0; e < 4; ++e)  // column 4 c + e
                                     if (sees && (z >> (8 * e + 7) & 1))
@@ -495,10 +498,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, ROWS>::REGS_FOR) decode_fp8_k
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
                 auto& x = S[nb];
-                if (key0 + kKeys > cur.len - a.Nq + 1) {  // some row does not see every key
+                if (key0 + kKeys > cur.len - Nq + 1) {  // some row does not see every key
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        const int lim = cur.len - a.Nq + (r0 + nb * 8 + 2 * t + j) % a.Nq + 1 - key0 - g;
+                        const int lim = cur.len - Nq + (r0 + nb * 8 + 2 * t + j) % Nq + 1 - key0 - g;
 #pragma unroll
                         for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -926,7 +929,8 @@ __global__ void __launch_bounds__(kWeightThreads) weights_fp8_kernel(const Param
 template <int D, int ROWS>
 cudaError_t launch_d(const PagedDecodeFp8Launch& a, cudaStream_t s) {
     using C = Cfg<D, ROWS>;
-    cudaError_t e = set_smem_limit_once<decode_fp8_kernel<D, ROWS>>(C::SMEM);
+    cudaError_t e = a.Nq > 1 ? set_smem_limit_once<decode_fp8_kernel<D, ROWS, true>>(C::SMEM)
+                             : set_smem_limit_once<decode_fp8_kernel<D, ROWS, false>>(C::SMEM);
     if (e != cudaSuccess) return e;
     Params p;
     p.q = (const __nv_bfloat16*)a.q;
@@ -961,7 +965,8 @@ cudaError_t launch_d(const PagedDecodeFp8Launch& a, cudaStream_t s) {
     const long long bh = (long long)a.B * a.Hkv;
     // no more CTAs than steps at full lengths
     p.workers = (int)std::min<long long>(a.workers, bh * p.row_tiles * ((cap + kStep - 1) / kStep));
-    e = launch_dependent(decode_fp8_kernel<D, ROWS>, dim3(p.workers), dim3(kThreads), C::SMEM, s, p);
+    e = launch_dependent(a.Nq > 1 ? decode_fp8_kernel<D, ROWS, true> : decode_fp8_kernel<D, ROWS, false>, dim3(p.workers),
+                         dim3(kThreads), C::SMEM, s, p);
     if (e != cudaSuccess) return e;
     // rows per finishing block: one up to 16 blocks per SM (45 sequences of 20 tokens, 8 heads, 80 rows: 32.5 us with one,
     // 5.0 with 16); its threads: 512 where an item has 32 segments or more (a single one of 70000 tokens, 16 rows: 17.7 us
@@ -981,14 +986,21 @@ cudaError_t launch_d(const PagedDecodeFp8Launch& a, cudaStream_t s) {
                             tokens);
 }
 
+template <int D, int ROWS, bool DRAFTS>
+cudaError_t resident(int* blocks) {
+    using C = Cfg<D, ROWS>;
+    const cudaError_t e = set_smem_limit_once<decode_fp8_kernel<D, ROWS, DRAFTS>>(C::SMEM);
+    if (e != cudaSuccess) return e;
+    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(blocks, decode_fp8_kernel<D, ROWS, DRAFTS>, kThreads, C::SMEM);
+}
+
 template <int D, int ROWS>
 cudaError_t blocks_per_sm(int* blocks) {
-    using C = Cfg<D, ROWS>;
-    const cudaError_t e = set_smem_limit_once<decode_fp8_kernel<D, ROWS>>(C::SMEM);
-    if (e != cudaSuccess) return e;
-    const cudaError_t f = cudaOccupancyMaxActiveBlocksPerMultiprocessor(blocks, decode_fp8_kernel<D, ROWS>, kThreads, C::SMEM);
-    *blocks = std::min(*blocks, C::CTAS);
-    return f;
+    int one = 0, drafts = 0;
+    cudaError_t e = resident<D, ROWS, false>(&one);
+    if (e == cudaSuccess) e = resident<D, ROWS, true>(&drafts);
+    *blocks = std::min({one, drafts, Cfg<D, ROWS>::CTAS});
+    return e;
 }
 
 }  // namespace
