@@ -560,7 +560,8 @@ def rope_frequencies(rot, base=10000.0, scaling=None, factor=1.0, original_conte
     factor^(rot / (rot - 2)), which stretches the longest wave by factor and leaves the shortest.  "yarn": by parts;
     pairs that turn more than beta_fast times within original_context tokens keep their frequency, those that turn
     less than beta_slow times are divided by factor, the ones between are blended linearly in their number of turns;
-    magnitude 0.1 ln(factor) + 1.
+    magnitude 0.1 ln(factor) + 1.  A model that was trained with other frequencies (such as a blend that is linear in
+    the pair's index between two rounded bounds) takes its own: any list goes to ``rope_table``.
     """
     _need(rot >= 2 and rot % 2 == 0, "rot must be even and at least 2")
     _need(base > 0 and factor >= 1.0, "base must be positive and factor at least 1")
@@ -643,7 +644,8 @@ def decode_paged_fp8(q, k_pages, v_pages, k_scale, v_scale, block_table, seq_len
                      stream=None, workspace=None):
     """O [B,Hq,Nq,d] bf16 and LSE [B,Hq,Nq] fp32 of the last Nq tokens (q [B,Hq,Nq,d], or [B,Hq,d] for one, which
     gives O [B,Hq,d] and LSE [B,Hq]) over the paged 8-bit cache, which holds them already.  weights: fp32
-    [B,Hkv,max_pages*page] to which every token's attention weight is added, or None."""
+    [B,Hkv,max_pages*page] to which every token's attention weight is added, or None; with them the workspace holds a
+    score per query row and slot of the table, so the table should be no wider than the longest sequence needs."""
     if stream is not None:
         with _on_stream(stream, q):
             return decode_paged_fp8(q, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, scale, weights,

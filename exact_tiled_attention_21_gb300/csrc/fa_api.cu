@@ -773,7 +773,7 @@ int check_cache(int B, int Hkv, int page, int sb, int max_pages, int num_pages, 
 
 int g_fp8_blocks[kMaxDevices][2][3] = {};  // resident CTAs per SM of the 8-bit decode, by device, d and tile rows
 
-constexpr int kFp8MostWorkers = 1024;  // bounds the workspace; three CTAs on each of 152 SMs are 456
+constexpr int kFp8MostWorkers = 1024;  // bounds the workspace; four CTAs (d = 64) on each of 152 SMs are 608
 
 // CTAs that the 8-bit decode shares its steps among: as many as run at once.
 int fp8_workers(int d, int tile, int num_sms, int* workers) {

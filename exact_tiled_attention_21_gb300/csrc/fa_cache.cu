@@ -468,7 +468,7 @@ __global__ void __launch_bounds__(kSelThreads, PER > 8 ? 1 : 2) evict_select_ker
 // block's scale is the largest of its tokens' source scales; tokens that came with that scale are copied byte for byte.
 // Reading a token takes three loads that depend on each other (its index, its page, its row), so the CTAs are resident
 // ones that run over the blocks with the index two blocks ahead and the page one block ahead of the row.  Bound by HBM:
-// 134 MB for 1024 of 4096 tokens of 32 sequences of 8 heads in 26 us, 5.2 TB/s.
+// 134 MB for 1024 of up to 4096 tokens of 32 sequences of 8 heads in about 24 of the eviction's 33.9 us, 5.6 TB/s.
 // Threads of an SM, by the pieces that one holds (the eviction of 32 sequences of 4096 tokens, 8 heads, d = 128: blocks
 // of 64 tokens 45.1 us with 512, 38.9 with 768, 36.8 with 1024, 41.7 with 1280; blocks of 16 49.3 with 1024, 43.2 with
 // 1536, 43.0 with 2048; 4 sequences of 16k tokens, blocks of 32: 29.1 with 768, 27.8 with 1024, 26.7 with 1536).

@@ -3,15 +3,17 @@
 //
 // Every byte of the cache is read once per 32 query rows (the Hq / Hkv heads of
 // a group times the new tokens), 2 d bytes per key for 4 d flops per row: bound
-// by HBM for 8 rows, by the latencies of widening and multiplying for more (32
-// rows: 2 warps per scheduler, 35% of the issue slots, HBM 25%).  A CTA has four
+// by HBM for 8 rows of d = 128 (5.2 TB/s, start and end included), by the latencies
+// of widening and multiplying for more (32 rows: 2 warps per scheduler, 35% of the
+// issue slots, a quarter of HBM's rate) and at d = 64.  A CTA has four
 // warps.  Each streams 32 keys per step through a ring of cp.async copies and
 // holds 8 query rows, or 16 where there are more, so that a widened fragment
 // serves two products.  Up to 16 rows the warps take different keys and wait for
 // nobody until the end; with 32 two warps read each other's keys, each for rows
-// of its own.  8 sequences of 8000 tokens, 4 kv heads, d = 128: 24.4 us for 8 rows,
-// 28.7 for 16, 37.5 for 32 (8 rows in each of four warps that share keys: 9% more,
-// and 19% for 80 rows; 32 rows in every warp, the queries in shared memory: 20%).
+// of its own.  8 sequences of 8000 tokens, 4 kv heads, d = 128, one token each, calls
+// back to back: 20.7 us for 8 rows, 25.3 for 16, 33.7 for 32 (8 rows in each of four
+// warps that share keys: 9% more, and 19% for 80 rows; 32 rows in every warp, the
+// queries in shared memory: 20%).
 //
 // The work is one list of steps of 128 keys over all sequences, kv heads and row
 // tiles, cut into equal shares for as many CTAs as run at once, from the lengths

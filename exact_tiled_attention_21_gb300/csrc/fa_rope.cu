@@ -4,8 +4,8 @@
 // Read and written once, ~6 flops per element: bound by HBM.  A thread takes 16
 // columns (two 16-byte pieces: eight pairs) of one token and up to four heads
 // with the same cosines and sines, all their loads in flight at once.  A warp
-// covers whole rows of consecutive tokens.  8192 tokens of 32 heads, d = 128: 26.7
-// us, 5.0 TB/s (launch and first loads included); 32 single tokens: 5.5 us.
+// covers whole rows of consecutive tokens.  Calls back to back: 8192 tokens of 32
+// heads, d = 128, 23.4 us (5.7 TB/s); one token of 32 sequences 4.0 to 4.7 us.
 #include "fa_internal.h"
 #include "fa_rope.cuh"
 
@@ -61,8 +61,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeLaunch a) 
 
 cudaError_t launch_rope(RopeLaunch a, cudaStream_t s) {
     const long long blocks = (a.tokens * (a.d / 16) + kRopeThreads - 1) / kRopeThreads;
-    // heads per thread: up to four share the sines while every SM still has four CTAs (8192 tokens of 32 heads: 1 head
-    // 55.3 us, 2 34.9, 4 26.7, 8 26.8)
+    // heads per thread: up to four share the sines while every SM still has four CTAs (8192 tokens of 32 heads, as
+    // single graph replays: 1 head 55.3 us, 2 34.9, 4 26.7, 8 26.8)
     a.hpt = 4;
     while (a.hpt > 1 && blocks * ((a.H + a.hpt - 1) / a.hpt) < 4ll * a.num_sms) a.hpt /= 2;
     int groups = (a.H + a.hpt - 1) / a.hpt;

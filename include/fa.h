@@ -374,9 +374,11 @@ int fa_cache_append_fp8(const void *k, const void *v, long long k_sb, long long 
                         int max_pages, int num_pages, void *stream);
 
 /* Bytes of workspace fa_decode_paged_fp8 needs; max_tokens = max_pages *
- * page_size, weights = 1 if it is given accumulated weights (which takes fp32
- * scores of every query row and token besides the partials).  Returns 0 for
- * invalid sizes.  Host only, no device call. */
+ * page_size, weights = 1 if it is given accumulated weights.  Those take fp32
+ * scores of every query row (rounded up to 4 per kv head) and slot of the table
+ * besides the partials, 4 * B * Hq * Nq * max_tokens bytes, whatever the lengths
+ * are: give such calls a table no wider than the longest sequence needs.  Returns
+ * 0 for invalid sizes.  Host only, no device call. */
 size_t fa_decode_paged_fp8_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d, int max_tokens, int weights);
 
 /* Attention of the last Nq (1..16) tokens of each sequence over the 8-bit
