@@ -38,9 +38,8 @@ __device__ __forceinline__ bool is_pow2(float s) {
 // Sixteen e4m3 bytes with scale `from` as e4m3 bytes with scale `to`, each
 // value rounded to nearest once more.  Between powers of two, downwards, that
 // is a product in fp16: it is exact wherever the result does not round to zero
-// (four significant bits above 2^-14), 3 instructions for 2 values against 40
-// with fp32 divisions, which bound the eviction at 62 us of B = 32, 1024 of
-// 4096 tokens.
+// (four significant bits above 2^-14), 3 instructions for 2 values.  (40 with a
+// division for each bound the eviction at 62 us of B = 32, 1024 of 4096 tokens.)
 __device__ __forceinline__ uint4 e4m3_rescale16(uint4 x, float from, float to) {
     uint32_t* w = reinterpret_cast<uint32_t*>(&x);
     if (from <= to && is_pow2(from) && is_pow2(to)) {
@@ -59,15 +58,11 @@ __device__ __forceinline__ uint4 e4m3_rescale16(uint4 x, float from, float to) {
         }
         return x;
     }
-    // Both scales times the same power of two: a value times a scale near either end of the range would overflow or lose
-    // its low bits.
-    const float shift = to >= 1.f ? 0x1p-32f : 0x1p32f;
-    from *= shift, to *= shift;
+    const float by = __fdiv_rn(from, to);  // first: a value times a scale may overflow, or lose bits among the subnormals
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const float2 a = half2_to_float2(e4m3x2_to_half2(w[i])), b = half2_to_float2(e4m3x2_hi_to_half2(w[i]));
-        w[i] = e4m3x4(__fdiv_rn(__fmul_rn(a.x, from), to), __fdiv_rn(__fmul_rn(a.y, from), to),
-                      __fdiv_rn(__fmul_rn(b.x, from), to), __fdiv_rn(__fmul_rn(b.y, from), to));
+        w[i] = e4m3x4(a.x * by, a.y * by, b.x * by, b.y * by);
     }
     return x;
 }
