@@ -10,7 +10,9 @@ supplies device memory (``data_ptr``) and the stream.  ``forward``,
 ``backward`` and ``decode`` are conveniences that allocate the outputs and the
 workspace with torch and then call the same entry points.  So are those of the
 serving cache held in 8 bits, ``rope``, ``cache_append_fp8``,
-``decode_paged_fp8`` and ``cache_evict_fp8``, through a compiled binding
+``decode_paged_fp8`` and ``cache_evict_fp8``, and those of long contexts out of the
+bf16 cache, ``cache_append``, ``select_blocks``, ``decode_blocks`` and
+``decode_shared``, through a compiled binding
 (``csrc/fa_torch.cpp``, ``_fa_torch.so``), since their small calls take less time
 on the GPU than ctypes does on the host.  Only ``rope`` takes part in autograd;
 the others return results that record no gradient (``backward`` is called for
@@ -116,6 +118,18 @@ def load():
     lib.fa_decode_paged_fp8.restype = i
     lib.fa_cache_evict_fp8.argtypes = [vp] * 11 + [i] * 10 + [vp]
     lib.fa_cache_evict_fp8.restype = i
+    lib.fa_cache_append.argtypes = [vp, vp] + [ll] * 6 + [vp] * 8 + [i] * 6 + [f] + [i] * 4 + [vp]
+    lib.fa_cache_append.restype = i
+    lib.fa_select_blocks_workspace_bytes.argtypes = [i] * 3
+    lib.fa_select_blocks_workspace_bytes.restype = sz
+    lib.fa_select_blocks.argtypes = [vp] * 5 + [i] * 12 + [vp, sz, vp]
+    lib.fa_select_blocks.restype = i
+    for fn in (lib.fa_decode_blocks_workspace_bytes, lib.fa_decode_shared_workspace_bytes):
+        fn.argtypes, fn.restype = [i] * 5, sz
+    lib.fa_decode_blocks.argtypes = [vp] * 8 + [i] * 10 + [f, vp, sz, vp]
+    lib.fa_decode_blocks.restype = i
+    lib.fa_decode_shared.argtypes = [vp] * 8 + [i] * 8 + [f, vp, sz, vp]
+    lib.fa_decode_shared.restype = i
     _lib = lib
     return lib
 
@@ -439,6 +453,50 @@ def fa_cache_evict_fp8(k_pages, v_pages, k_scale, v_scale, block_table, seq_lens
            "fa_cache_evict_fp8")
 
 
+def fa_cache_append(k, v, k_strides, v_strides, k_pages, v_pages, bounds, block_table, seq_lens, new_lens, positions,
+                    turns, B, Hkv, N, d, rot, interleaved, magnitude, page_size, block, max_pages, num_pages,
+                    stream=None):
+    _raise(load().fa_cache_append(_ptr(k), _ptr(v), *k_strides, *v_strides, _ptr(k_pages), _ptr(v_pages), _ptr(bounds),
+                                  _ptr(block_table), _ptr(seq_lens), _ptr(new_lens), _ptr(positions), _ptr(turns), B,
+                                  Hkv, N, d, rot, int(bool(interleaved)), float(magnitude), page_size, block, max_pages,
+                                  num_pages, _stream(stream)), "fa_cache_append")
+
+
+def fa_select_blocks_workspace_bytes(B, Hkv, max_blocks):
+    return load().fa_select_blocks_workspace_bytes(B, Hkv, max_blocks)
+
+
+def fa_select_blocks(q, bounds, block_table, seq_lens, blocks, B, Hq, Hkv, Nq, block, page_blocks, max_pages, num_pages,
+                     d, keep, first, recent, workspace, workspace_bytes, stream=None):
+    _raise(load().fa_select_blocks(_ptr(q), _ptr(bounds), _ptr(block_table), _ptr(seq_lens), _ptr(blocks), B, Hq, Hkv, Nq,
+                                   block, page_blocks, max_pages, num_pages, d, int(keep), int(first), int(recent),
+                                   _ptr(workspace), int(workspace_bytes), _stream(stream)), "fa_select_blocks")
+
+
+def fa_decode_blocks_workspace_bytes(B, Hq, Hkv, Nq, d):
+    return load().fa_decode_blocks_workspace_bytes(B, Hq, Hkv, Nq, d)
+
+
+def fa_decode_blocks(q, k_pages, v_pages, block_table, seq_lens, blocks, o, lse, B, Hq, Hkv, Nq, page_size, block, keep,
+                     max_pages, num_pages, d, scale, workspace, workspace_bytes, stream=None):
+    _raise(load().fa_decode_blocks(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(block_table), _ptr(seq_lens),
+                                   _ptr(blocks), _ptr(o), _ptr(lse), B, Hq, Hkv, Nq, page_size, block, keep, max_pages,
+                                   num_pages, d, float(scale), _ptr(workspace), int(workspace_bytes), _stream(stream)),
+           "fa_decode_blocks")
+
+
+def fa_decode_shared_workspace_bytes(B, Hq, Hkv, Nq, d):
+    return load().fa_decode_shared_workspace_bytes(B, Hq, Hkv, Nq, d)
+
+
+def fa_decode_shared(q, k_pages, v_pages, block_table, seq_lens, shared_len, o, lse, B, Hq, Hkv, Nq, page_size, max_pages,
+                     num_pages, d, scale, workspace, workspace_bytes, stream=None):
+    _raise(load().fa_decode_shared(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(block_table), _ptr(seq_lens),
+                                   _ptr(shared_len), _ptr(o), _ptr(lse), B, Hq, Hkv, Nq, page_size, max_pages, num_pages,
+                                   d, float(scale), _ptr(workspace), int(workspace_bytes), _stream(stream)),
+           "fa_decode_shared")
+
+
 # ------------------------------------------------------------------ conveniences
 def _check(t, name, shape):
     if not (t.is_cuda and t.dtype == torch.bfloat16 and t.is_contiguous()):
@@ -671,4 +729,64 @@ def cache_evict_fp8(k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, w
                                             new_table, keep, recent)
     if r.__class__ is int:
         raise FAError(r, "fa_cache_evict_fp8")
+    return r
+
+
+# ------------------------------------------------------------------ long contexts out of the bf16 cache
+def cache_append(k, v, k_pages, v_pages, block_table, seq_lens, new_lens=None, turns=None, positions=None,
+                 interleaved=False, magnitude=1.0, bounds=None, stream=None):
+    """Writes k, v [B,Hkv,N,d] (bf16, any strides that fa_rope takes) behind the seq_lens[b] tokens that the paged bf16
+    cache (the one of ``decode_paged``) holds of each sequence: the first new_lens[b] of them (None: all N).  With turns, k
+    is rotated on the way (positions int32 [B,N], or None: seq_lens[b] + i).  bounds: bf16 [num_pages, Hkv, page / block,
+    2, d], the smallest and largest key elements of each block of tokens, kept up to date, or None.  Changes the pages and
+    bounds, not seq_lens."""
+    if stream is not None:
+        with _on_stream(stream, k):
+            return cache_append(k, v, k_pages, v_pages, block_table, seq_lens, new_lens, turns, positions, interleaved,
+                                magnitude, bounds)
+    st = (_torch_binding or _native()).paged_append(k, v, k_pages, v_pages, block_table, seq_lens, new_lens, turns,
+                                                    positions, interleaved, magnitude, bounds)
+    if st != FA_OK:
+        raise FAError(st, "fa_cache_append")
+
+
+def select_blocks(q, bounds, block_table, seq_lens, block, keep, first=0, recent=1, stream=None, workspace=None):
+    """int32 [B,Hkv,keep]: the blocks of ``block`` tokens that the last Nq tokens (q [B,Hq,Nq,d], or [B,Hq,d] for one) are
+    to attend to, ascending, -1 behind them: the first ``first``, the last ``recent``, and of the others those in whose
+    bounds (``cache_append``) a key could score highest with a row of the kv head's group."""
+    if stream is not None:
+        with _on_stream(stream, bounds):
+            return select_blocks(q, bounds, block_table, seq_lens, block, keep, first, recent, None, workspace)
+    r = (_torch_binding or _native()).select_blocks(q, bounds, block_table, seq_lens, block, keep, first, recent,
+                                                    workspace)
+    if r.__class__ is int:
+        raise FAError(r, "fa_select_blocks")
+    return r
+
+
+def decode_blocks(q, k_pages, v_pages, block_table, seq_lens, blocks, block, scale=None, stream=None, workspace=None):
+    """O [B,Hq,Nq,d] bf16 and LSE [B,Hq,Nq] fp32 of the last Nq tokens (q [B,Hq,Nq,d], or [B,Hq,d] for one, which gives O
+    [B,Hq,d] and LSE [B,Hq]) over the listed blocks of ``block`` tokens (int32 [B,Hkv,keep], distinct, any order, negative
+    ones skipped) of the paged bf16 cache, which holds those tokens already."""
+    if stream is not None:
+        with _on_stream(stream, q):
+            return decode_blocks(q, k_pages, v_pages, block_table, seq_lens, blocks, block, scale, None, workspace)
+    r = (_torch_binding or _native()).decode_blocks(q, k_pages, v_pages, block_table, seq_lens, blocks, block, scale,
+                                                    workspace)
+    if r.__class__ is int:
+        raise FAError(r, "fa_decode_blocks")
+    return r
+
+
+def decode_shared(q, k_pages, v_pages, block_table, seq_lens, shared_len, scale=None, stream=None, workspace=None):
+    """O and LSE (shapes as ``decode_blocks``) of the last Nq tokens over the whole paged bf16 cache, where the first
+    shared_len[0] tokens (int32 [1] on the device) are the same for all sequences and are read once for all of them.
+    seq_lens counts them too; a sequence whose new tokens do not all see all of them reads its own row of the table."""
+    if stream is not None:
+        with _on_stream(stream, q):
+            return decode_shared(q, k_pages, v_pages, block_table, seq_lens, shared_len, scale, None, workspace)
+    r = (_torch_binding or _native()).decode_shared(q, k_pages, v_pages, block_table, seq_lens, shared_len, scale,
+                                                    workspace)
+    if r.__class__ is int:
+        raise FAError(r, "fa_decode_shared")
     return r

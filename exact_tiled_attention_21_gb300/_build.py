@@ -18,7 +18,8 @@ LIB = os.path.join(HERE, "libfa_gb300.so")
 TORCH_LIB = os.path.join(HERE, "_fa_torch.so")  # the native binding of the serving-cache conveniences
 BUILD = os.path.join(ROOT, "_build")
 SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_fwd_fp8.cu", "fa_bwd.cu", "fa_decode.cu", "fa_decode_mma.cu",
-           "fa_rope.cu", "fa_cache.cu", "fa_decode_fp8.cu"]
+           "fa_rope.cu", "fa_cache.cu", "fa_decode_fp8.cu", "fa_append.cu", "fa_select.cu",
+           "fa_decode_rows.cu", "fa_prefix.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I" + os.path.join(ROOT, "include")]

@@ -809,6 +809,107 @@ Fp8Workspace fp8_workspace(int B, int Hq, int Hkv, int Nq, int d, long long max_
     return w;
 }
 
+// Workspace of the block selection: exact keys and scores of every block of the table, the largest bound of every CTA.
+struct SelectWorkspace {
+    size_t scores, big, bytes;
+};
+SelectWorkspace select_workspace(int B, int Hkv, long long max_blocks) {
+    const size_t bh = (size_t)B * Hkv;
+    SelectWorkspace w;
+    w.scores = align256(bh * (size_t)max_blocks * 8);
+    w.big = w.scores + align256(bh * (size_t)max_blocks * 4);
+    w.bytes = w.big + align256(bh * kSelectCtas * 4);
+    return w;
+}
+
+// Workspace of the bf16 row decode: partial outputs and LSEs of every segment (at most one more per CTA than there are
+// items), and the sequences' first steps.
+struct RowsWorkspace {
+    size_t part_lse, prefix, bytes;
+};
+RowsWorkspace rows_workspace(int B, int Hq, int Hkv, int Nq, int d) {
+    const int rows = Hq / Hkv * Nq, tile = rows_tile(rows);
+    const size_t slots = (size_t)kRowsMostWorkers + (size_t)B * Hkv * ((rows + tile - 1) / tile);
+    RowsWorkspace w;
+    w.part_lse = align256(slots * tile * d * 4);
+    w.prefix = w.part_lse + align256(slots * tile * 4);
+    w.bytes = w.prefix + align256(((size_t)B + 1) * 8);
+    return w;
+}
+
+// Workspace of the shared prefix: the same of (kv head, tile of the batch's query rows) items.
+struct PrefixWorkspace {
+    int tiles, tile_rows;
+    size_t part_lse, bytes;
+};
+PrefixWorkspace prefix_workspace(int B, int Hq, int Hkv, int Nq, int d) {
+    const long long rows = (long long)B * (Hq / Hkv) * Nq;
+    PrefixWorkspace w;
+    w.tile_rows = rows <= 128 ? 128 : 256;
+    w.tiles = (int)((rows + w.tile_rows - 1) / w.tile_rows);
+    const size_t slots = (size_t)kPrefixMostWorkers + (size_t)Hkv * w.tiles;
+    w.part_lse = align256(slots * w.tile_rows * d * 4);
+    w.bytes = w.part_lse + align256(slots * w.tile_rows * 4);
+    return w;
+}
+
+bool rows_sizes_ok(int B, int Hq, int Hkv, int Nq, int d) {
+    return B >= 1 && Hq >= 1 && Hkv >= 1 && Hq % Hkv == 0 && Nq >= 1 && Nq <= 16 && (d == 64 || d == 128) &&
+           (long long)B * Hq <= (1ll << 24);
+}
+
+// Checks and fields that the attention over blocks and the one with a shared prefix have in common.
+int rows_prepare(DecodeRowsLaunch& a, const void* q, const void* k_pages, const void* v_pages, const int* block_table,
+                 const int* seq_lens, void* o, float* lse, int B, int Hq, int Hkv, int Nq, int page_size, int block,
+                 int max_pages, int num_pages, int d, float scale) {
+    if (!q || !k_pages || !v_pages || !block_table || !seq_lens || !o) return FA_ERR_INVALID_ARG;
+    if (!scale_ok(scale) || Hq < 1 || Nq < 1) return FA_ERR_INVALID_ARG;
+    int st = check_cache(B, Hkv, page_size, block, max_pages, num_pages, d);
+    if (st != FA_OK) return st;
+    if (Hq % Hkv) return FA_ERR_INVALID_ARG;
+    if (!rows_sizes_ok(B, Hq, Hkv, Nq, d)) return FA_ERR_UNSUPPORTED;
+    // steps of 64 keys over all sequences, kv heads and row tiles are counted in 32 bits per CTA
+    const int rows = Hq / Hkv * Nq, tile = rows_tile(rows);
+    if ((long long)B * Hkv * ((rows + tile - 1) / tile) > 0x7FFFFFFFll / (((long long)max_pages * page_size + block + 63) / 64))
+        return FA_ERR_UNSUPPORTED;
+    if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(o) || !aligned4(block_table) ||
+        !aligned4(seq_lens) || !aligned4(lse))
+        return FA_ERR_ALIGNMENT;
+    if (o == q) return FA_ERR_INVALID_ARG;  // other CTAs may still read the row that one writes
+    st = device_state(&a.err, &a.num_sms);
+    if (st != FA_OK) return st;
+    a.q = q;
+    a.kp = k_pages;
+    a.vp = v_pages;
+    a.table = block_table;
+    a.lens = seq_lens;
+    a.list = nullptr;
+    a.shared = nullptr;
+    a.o = o;
+    a.lse = lse;
+    a.pre_o = a.pre_lse = nullptr;
+    a.B = B;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.Nq = Nq;
+    a.page = page_size;
+    a.block = block;
+    a.keep = 0;
+    a.max_pages = max_pages;
+    a.num_pages = num_pages;
+    a.d = d;
+    a.pre_workers = a.pre_tiles = a.pre_rows = 0;
+    a.scale = scale;
+    return FA_OK;
+}
+
+void rows_place(DecodeRowsLaunch& a, char* base) {
+    const RowsWorkspace w = rows_workspace(a.B, a.Hq, a.Hkv, a.Nq, a.d);
+    a.part_o = reinterpret_cast<float*>(base);
+    a.part_lse = reinterpret_cast<float*>(base + w.part_lse);
+    a.prefix = reinterpret_cast<long long*>(base + w.prefix);
+}
+
 }  // namespace
 
 extern "C" {
@@ -1021,6 +1122,183 @@ int fa_cache_evict_fp8(void* k_pages, void* v_pages, float* k_scale, float* v_sc
     a.keep = keep;
     a.recent = recent;
     return launched(launch_cache_evict(a, (cudaStream_t)stream));
+}
+
+int fa_cache_append(const void* k, const void* v, long long k_sb, long long k_sh, long long k_sn, long long v_sb,
+                    long long v_sh, long long v_sn, void* k_pages, void* v_pages, void* bounds, const int* block_table,
+                    const int* seq_lens, const int* new_lens, const int* positions, const uint64_t* turns, int B, int Hkv,
+                    int N, int d, int rot, int interleaved, float magnitude, int page_size, int block, int max_pages,
+                    int num_pages, void* stream) {
+    if (!k || !v || !k_pages || !v_pages || !block_table || !seq_lens || N < 1) return FA_ERR_INVALID_ARG;
+    int st = check_cache(B, Hkv, page_size, bounds ? block : 1, max_pages, num_pages, d);
+    if (st != FA_OK) return st;
+    if (turns && (st = check_rotation(d, rot, interleaved, magnitude)) != FA_OK) return st;
+    if (N > kMaxCacheTokens / 2 || (long long)B * Hkv * N > 0x7FFFFFFFll) return FA_ERR_UNSUPPORTED;
+    if (!aligned16(k) || !aligned16(v) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(bounds) ||
+        !aligned16(turns) || !aligned4(block_table) || !aligned4(seq_lens) || !aligned4(new_lens) || !aligned4(positions))
+        return FA_ERR_ALIGNMENT;
+    if ((st = check_strides(&k_sb, &k_sh, &k_sn, B, Hkv, N)) != FA_OK) return st;
+    if ((st = check_strides(&v_sb, &v_sh, &v_sn, B, Hkv, N)) != FA_OK) return st;
+    PagedAppendLaunch a;
+    st = device_state(&a.err, &a.num_sms);
+    if (st != FA_OK) return st;
+    a.k = k;
+    a.v = v;
+    a.kb = k_sb;
+    a.kh = k_sh;
+    a.kn = k_sn;
+    a.vb = v_sb;
+    a.vh = v_sh;
+    a.vn = v_sn;
+    a.kp = k_pages;
+    a.vp = v_pages;
+    a.bounds = bounds;
+    a.table = block_table;
+    a.lens = seq_lens;
+    a.new_lens = new_lens;
+    a.positions = positions;
+    a.turns = turns;
+    a.B = B;
+    a.Hkv = Hkv;
+    a.N = N;
+    a.d = d;
+    a.rot = turns ? rot : 0;
+    a.interleaved = turns ? interleaved : 0;
+    a.page = page_size;
+    a.block = bounds ? block : 1;
+    a.max_pages = max_pages;
+    a.num_pages = num_pages;
+    a.magnitude = magnitude;
+    return launched(launch_paged_append(a, (cudaStream_t)stream));
+}
+
+size_t fa_select_blocks_workspace_bytes(int B, int Hkv, int max_blocks) {
+    if (B < 1 || Hkv < 1 || max_blocks < 1 || max_blocks > kMaxCacheTokens || (long long)B * Hkv > (1ll << 24)) return 0;
+    return select_workspace(B, Hkv, max_blocks).bytes;
+}
+
+int fa_select_blocks(const void* q, const void* bounds, const int* block_table, const int* seq_lens, int* blocks, int B,
+                     int Hq, int Hkv, int Nq, int block, int page_blocks, int max_pages, int num_pages, int d, int keep,
+                     int first, int recent, void* workspace, size_t workspace_bytes, void* stream) {
+    if (!q || !bounds || !block_table || !seq_lens || !blocks || Hq < 1 || Nq < 1 || page_blocks < 1 || block < 1)
+        return FA_ERR_INVALID_ARG;
+    if (block > 128 || page_blocks > kMaxCacheTokens / block) return FA_ERR_UNSUPPORTED;
+    int st = check_cache(B, Hkv, page_blocks * block, block, max_pages, num_pages, d);
+    if (st != FA_OK) return st;
+    if (Hq % Hkv || first < 0 || recent < 0 || keep < 1 || (long long)first + recent > keep) return FA_ERR_INVALID_ARG;
+    if (Nq > 16 || (long long)B * Hq > (1ll << 24)) return FA_ERR_UNSUPPORTED;
+    if (!aligned16(q) || !aligned16(bounds) || !aligned4(block_table) || !aligned4(seq_lens) || !aligned4(blocks))
+        return FA_ERR_ALIGNMENT;
+    SelectLaunch a;
+    st = device_state(&a.err, &a.num_sms);
+    if (st != FA_OK) return st;
+    const SelectWorkspace ws = select_workspace(B, Hkv, (long long)max_pages * page_blocks);
+    if (!workspace || workspace_bytes < ws.bytes) return FA_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return FA_ERR_ALIGNMENT;
+    char* base = static_cast<char*>(workspace);
+    a.q = q;
+    a.bounds = bounds;
+    a.table = block_table;
+    a.lens = seq_lens;
+    a.out = blocks;
+    a.exact = base;
+    a.scores = reinterpret_cast<float*>(base + ws.scores);
+    a.big = reinterpret_cast<uint32_t*>(base + ws.big);
+    a.stride = (long long)max_pages * page_blocks;
+    a.B = B;
+    a.Hkv = Hkv;
+    a.rows = Hq / Hkv * Nq;
+    a.block = block;
+    a.page_blocks = page_blocks;
+    a.max_pages = max_pages;
+    a.num_pages = num_pages;
+    a.d = d;
+    a.keep = keep;
+    a.first = first;
+    a.recent = recent;
+    return launched(launch_select_blocks(a, (cudaStream_t)stream));
+}
+
+size_t fa_decode_blocks_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d) {
+    if (!rows_sizes_ok(B, Hq, Hkv, Nq, d)) return 0;
+    return rows_workspace(B, Hq, Hkv, Nq, d).bytes;
+}
+
+int fa_decode_blocks(const void* q, const void* k_pages, const void* v_pages, const int* block_table, const int* seq_lens,
+                     const int* blocks, void* o, float* lse, int B, int Hq, int Hkv, int Nq, int page_size, int block, int keep,
+                     int max_pages, int num_pages, int d, float scale, void* workspace, size_t workspace_bytes, void* stream) {
+    if (!blocks || keep < 1) return FA_ERR_INVALID_ARG;
+    DecodeRowsLaunch a;
+    const int st = rows_prepare(a, q, k_pages, v_pages, block_table, seq_lens, o, lse, B, Hq, Hkv, Nq, page_size, block,
+                                max_pages, num_pages, d, scale);
+    if (st != FA_OK) return st;
+    if (!aligned4(blocks)) return FA_ERR_ALIGNMENT;
+    if (!workspace || workspace_bytes < rows_workspace(B, Hq, Hkv, Nq, d).bytes) return FA_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return FA_ERR_ALIGNMENT;
+    rows_place(a, static_cast<char*>(workspace));
+    a.list = blocks;
+    a.keep = keep;
+    return launched(launch_decode_rows(a, (cudaStream_t)stream));
+}
+
+size_t fa_decode_shared_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d) {
+    if (!rows_sizes_ok(B, Hq, Hkv, Nq, d)) return 0;
+    return rows_workspace(B, Hq, Hkv, Nq, d).bytes + prefix_workspace(B, Hq, Hkv, Nq, d).bytes;
+}
+
+int fa_decode_shared(const void* q, const void* k_pages, const void* v_pages, const int* block_table, const int* seq_lens,
+                     const int* shared_len, void* o, float* lse, int B, int Hq, int Hkv, int Nq, int page_size,
+                     int max_pages, int num_pages, int d, float scale, void* workspace, size_t workspace_bytes, void* stream) {
+    if (!shared_len) return FA_ERR_INVALID_ARG;
+    DecodeRowsLaunch a;
+    int st = rows_prepare(a, q, k_pages, v_pages, block_table, seq_lens, o, lse, B, Hq, Hkv, Nq, page_size, 1, max_pages,
+                          num_pages, d, scale);
+    if (st != FA_OK) return st;
+    if (page_size % 8) return FA_ERR_UNSUPPORTED;  // boxes of 8 rows at least
+    if (!aligned4(shared_len)) return FA_ERR_ALIGNMENT;
+    const RowsWorkspace ws = rows_workspace(B, Hq, Hkv, Nq, d);
+    const PrefixWorkspace pw = prefix_workspace(B, Hq, Hkv, Nq, d);
+    if (!workspace || workspace_bytes < ws.bytes + pw.bytes) return FA_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return FA_ERR_ALIGNMENT;
+    char* base = static_cast<char*>(workspace);
+    rows_place(a, base);
+    base += ws.bytes;
+    PrefixLaunch p;
+    p.q = q;
+    p.table = block_table;
+    p.lens = seq_lens;
+    p.shared = shared_len;
+    p.part_o = reinterpret_cast<float*>(base);
+    p.part_lse = reinterpret_cast<float*>(base + pw.part_lse);
+    p.B = B;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.Nq = Nq;
+    p.page = page_size;
+    p.box = page_box_rows(page_size);
+    p.max_pages = max_pages;
+    p.num_pages = num_pages;
+    p.d = d;
+    p.tiles = pw.tiles;
+    p.tile_rows = pw.tile_rows;
+    const long long steps = ((long long)max_pages * page_size + 127) / 128 * Hkv * pw.tiles;  // no more CTAs than at most
+    p.workers = (int)std::min<long long>(std::min(a.num_sms, kPrefixMostWorkers), steps);
+    p.scale = scale;
+    p.err = a.err;
+    p.timeout_ns = g_timeout_ns.load();
+    const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)page_size, (cuuint64_t)Hkv, (cuuint64_t)num_pages};
+    const cuuint64_t strides[3] = {(cuuint64_t)d * 2, (cuuint64_t)page_size * d * 2, (cuuint64_t)Hkv * page_size * d * 2};
+    const cuuint32_t box[4] = {64, (cuuint32_t)p.box, 1, 1};
+    if (make_map_nd(&p.map_k, k_pages, 4, dims, strides, box) || make_map_nd(&p.map_v, v_pages, 4, dims, strides, box))
+        return FA_ERR_CUDA;
+    a.shared = shared_len;
+    a.pre_o = p.part_o;
+    a.pre_lse = p.part_lse;
+    a.pre_workers = p.workers;
+    a.pre_tiles = p.tiles;
+    a.pre_rows = p.tile_rows;
+    st = launched(launch_prefix(p, (cudaStream_t)stream));
+    return st != FA_OK ? st : launched(launch_decode_rows(a, (cudaStream_t)stream));
 }
 
 int fa_selftest_wait_timeout(uint64_t timeout_ns, void* stream) {

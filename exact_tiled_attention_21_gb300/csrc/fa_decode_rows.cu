@@ -1,0 +1,804 @@
+// Attention of 1..16 new tokens per sequence over the paged bf16 cache: over the
+// blocks of a list, or over the tokens that follow a prefix which all sequences
+// share (the prefix itself is fa_prefix.cu's), and the merge of the parts.
+//
+// 4 d bytes per key for 4 d flops per query row: bound by HBM.  The work is one
+// list of steps of 4 x KEYS keys over all sequences, kv heads and row tiles, cut
+// into equal shares for as many CTAs as run at once, from the lengths on the
+// device: a batch of any lengths keeps every SM busy to the end.  A CTA's share
+// crosses from one (sequence, kv head, row tile) to the next as it comes, the
+// copies running ahead; the part of one that a CTA holds is a segment.  Segment
+// results go to the workspace at slot CTA + item (which grows by one from each
+// segment to the next), and a second kernel merges the segments of each row.
+//
+// A CTA has four warps.  Each streams KEYS keys per step through a ring of its own
+// of cp.async copies, three steps deep, and holds 8 query rows, or 16 where there
+// are more; with 32 two warps read each other's keys, each for rows of its own.
+// Up to 16 rows the warps wait for nobody until a segment's end.
+//
+// The products are mma.sync m16n8k16 in bf16 with fp32 sums, taken transposed,
+// S^T = K Q^T and O^T = V^T P^T, so that keys (and d) fill the 16 rows of a product
+// and the queries its 8 columns: with a handful of query rows per kv head the
+// 128-row products of tcgen05 would be nearly empty, and its operands would have to
+// pass through shared memory again.  Softmax sums are fp32.  A row's weights are
+// taken relative to a running reference within 2^8 of its largest score, and enter
+// the value product as bf16 pairs of a rounded weight and what the rounding left:
+// one bf16 (2^-9) would cost as much as the rounding of the result.
+#include <algorithm>
+#include <cfloat>
+#include <climits>
+
+#include "fa_internal.h"
+
+namespace fa {
+namespace {
+
+constexpr int kWarps = 4, kThreads = kWarps * 32, kStages = 3;
+constexpr float kSlack = 8.f;  // how far (log2) a score may exceed the reference that its weight is relative to
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
+
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+// 16 bytes into shared memory; zeros if !ok (src must still be a valid address).
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool ok) {
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+}
+
+template <int D, int ROWS_>
+struct Cfg {
+    static constexpr int ROWS = ROWS_, NB = ROWS == 8 ? 1 : 2;   // query rows per tile; a warp's, in eights
+    static constexpr int RG = ROWS / (8 * NB), KG = kWarps / RG;  // row groups; groups of warps with different keys
+    static constexpr int KEYS = D == 128 ? 16 : 32;              // per warp and step
+    static constexpr int STEP = kWarps * KEYS;                   // per CTA
+    static constexpr int HALF = KEYS * D * 2;                    // bytes of K (and of V) per warp and step
+    static constexpr int SLOT = 2 * HALF + 128;                  // K, V, the keys' tokens
+    static constexpr int RING = kStages * SLOT;                  // per warp
+    static constexpr int OROW = D + 4;                           // a row of the merge buffers, floats
+    static constexpr int MERGE = kWarps * RING;                  // one of 8 rows for each warp but the first group's
+    static constexpr int SMEM = MERGE + (kWarps - RG) * 8 * OROW * 4;
+    static constexpr int CTAS = 2;                               // per SM
+    static_assert(CTAS * (SMEM + 2048) <= 227 * 1024, "shared memory");
+    static_assert(HALF == 4096, "the swizzle's offsets");
+};
+
+struct Params {
+    const __nv_bfloat16* q;
+    const __nv_bfloat16* kp;
+    const __nv_bfloat16* vp;
+    const int* table;
+    const int* lens;
+    const int* list;        // [B, Hkv, keep] blocks, or null: the tokens behind the shared ones
+    const int* shared;      // [1], null with a list
+    __nv_bfloat16* o;
+    float* lse;
+    float* part_o;          // [slot][ROWS][D], normalised
+    float* part_lse;        // [slot][ROWS], log2
+    long long* prefix;      // [B + 1] steps before each sequence, per (kv head, row tile)
+    const float* pre_o;     // the shared prefix's parts: [slot][pre_rows][D] and [slot][pre_rows]
+    const float* pre_lse;
+    int B, Hkv, Nq, max_pages, num_pages, rows, row_tiles, workers, keep;
+    int pre_workers, pre_tiles, pre_rows;
+    FastDiv page, block;
+    float scale_log2;
+    DevError* err;
+};
+
+__device__ __forceinline__ int clamp_len(int len, int cap) { return min(max(len, 0), cap); }
+
+// The shared tokens that sequences of these lengths read from the common prefix: none if some new token of it does not see
+// all of them.
+__device__ __forceinline__ int shared_of(int shared, int len, int Nq) { return len - Nq >= shared ? shared : 0; }
+
+// A sequence's keys in this pass.
+template <bool LIST>
+__device__ __forceinline__ int keys_of(const Params& a, int len, int shared) {
+    if (LIST) return min(a.keep, (int)a.block.div(len + a.block.d - 1)) * (int)a.block.d;
+    return len - shared_of(shared, len, a.Nq);
+}
+
+// Steps of all sequences before q (64-bit warp scan of the lengths): the sequence that step q falls in, its first step
+// and length.  With q beyond the end: sequence B and the total.  prefix: also written, if not null.
+template <int STEP, bool LIST>
+__device__ __forceinline__ void find_sequence(const Params& a, int cap, int shared, long long q, long long* prefix, int& b,
+                                              long long& start, int& len) {
+    const int lane = threadIdx.x & 31;
+    long long base = 0;
+    b = a.B;
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+        const int l = b0 + lane < a.B ? clamp_len(a.lens[b0 + lane], cap) : 0;
+        const uint32_t n = (uint32_t)(keys_of<LIST>(a, l, shared) + STEP - 1) / STEP;
+        uint32_t incl = n;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const uint32_t up = __shfl_up_sync(0xffffffffu, incl, d);
+            if (lane >= d) incl += up;
+        }
+        if (prefix && b0 + lane < a.B) prefix[b0 + lane] = base + incl - n;
+        const uint32_t hit = __ballot_sync(0xffffffffu, base + incl > q);
+        if (hit) {
+            const int f = __ffs(hit) - 1;
+            b = b0 + f;
+            len = __shfl_sync(0xffffffffu, l, f);
+            start = base + __shfl_sync(0xffffffffu, incl - n, f);
+            return;
+        }
+        base += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    start = base;
+    len = 0;
+    if (prefix && lane == 0) prefix[a.B] = base;
+}
+
+// A position in the list of steps.
+struct Cursor {
+    int b, len, keys, n;  // sequence, its length, its keys in this pass and their steps
+    int kvh, rt, s;       // kv head, row tile and step
+};
+
+template <int STEP, bool LIST>
+__device__ __forceinline__ void advance(Cursor& c, const Params& a, int cap, int shared) {
+    if (++c.s < c.n) return;
+    c.s = 0;
+    if (++c.rt < a.row_tiles) return;
+    c.rt = 0;
+    if (++c.kvh < a.Hkv) return;
+    c.kvh = 0;
+    do {
+        ++c.b;
+        c.len = c.b < a.B ? clamp_len(a.lens[c.b], cap) : 0;
+        c.keys = keys_of<LIST>(a, c.len, shared);
+    } while (c.keys == 0 && c.b < a.B);
+    c.n = (c.keys + STEP - 1) / STEP;
+}
+
+constexpr int kNone = INT_MAX;  // in the place of a token: no such key
+
+// DRAFTS: more than one new token per sequence.
+template <int D, int ROWS, bool DRAFTS, bool LIST>
+__global__ void __launch_bounds__(kThreads, Cfg<D, ROWS>::CTAS) decode_rows_kernel(const Params a) {
+    using C = Cfg<D, ROWS>;
+    constexpr int KEYS = C::KEYS, MT = KEYS / 16, KS = D / 16, NB = C::NB, RG = C::RG, KG = C::KG, STEP = C::STEP;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ float s_stat[kWarps][2][8 * NB];  // m and l of a warp's rows
+    __shared__ Cursor s_ahead[kWarps];
+    pdl_launch_dependents();
+    pdl_wait();
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    const int rg = warp % RG, kg = warp / RG;  // row group, and group of warps that share keys
+    const int P = (int)a.page.d, cap = a.max_pages * P, Nq = DRAFTS ? a.Nq : 1;
+    const int given = LIST ? 0 : *a.shared, shared = clamp_len(given, cap);
+    if (blockIdx.x == 0) {
+        for (int i = tid; i < a.B; i += kThreads)
+            if (a.lens[i] < 0 || a.lens[i] > cap) record_invalid(a.err, kSiteCacheLen, a.lens[i]);
+        if (given != shared && tid == 0) record_invalid(a.err, kSiteCacheLen, given);
+    }
+    // ---- this CTA's share of the steps: `count` of them from `cur`
+    const long long per_step = (long long)a.Hkv * a.row_tiles;
+    Cursor cur;
+    int count;
+    {
+        int b, len;
+        long long total, start;
+        find_sequence<STEP, LIST>(a, cap, shared, LLONG_MAX, blockIdx.x == 0 && warp == 0 ? a.prefix : nullptr, b, total, len);
+        total *= per_step;
+        const long long workers = min((long long)a.workers, total);  // at least one step each
+        if (blockIdx.x >= workers) return;
+        const long long u = blockIdx.x * total / workers;
+        count = (int)((blockIdx.x + 1ll) * total / workers - u);
+        find_sequence<STEP, LIST>(a, cap, shared, u / per_step, nullptr, cur.b, start, cur.len);
+        cur.keys = keys_of<LIST>(a, cur.len, shared);
+        cur.n = (cur.keys + STEP - 1) / STEP;
+        const long long in_b = u - start * per_step;
+        const int item_b = (int)(in_b / cur.n);
+        cur.s = (int)(in_b - (long long)item_b * cur.n);
+        cur.kvh = item_b / a.row_tiles;
+        cur.rt = item_b - cur.kvh * a.row_tiles;
+    }
+
+    // ---- the ring: this warp's keys of the steps ahead, whatever item they are of.  A key's row is D / 8 pieces of 16
+    // bytes, piece c at c ^ (key % 8) (the lowest three bits), which keeps copies and ldmatrix free of bank conflicts.
+    uint8_t* ring = smem + warp * C::RING;
+    const uint32_t ring_u = smem_u32(ring);
+    constexpr int LPR = D / 8, RPI = 32 / LPR;  // lanes per row, rows per copy instruction
+    const int cr = lane / LPR, cc = lane % LPR;
+    const __nv_bfloat16* kp = a.kp + cc * 8;
+    const __nv_bfloat16* vp = a.vp + cc * 8;
+    Cursor& ahead = s_ahead[warp];  // the step to be looked up next; in shared memory to spare registers
+    if (lane == 0) ahead = cur;
+    __syncwarp();
+    bool bad = false;
+    // A step's keys are found in two loads that depend on each other (list, table), each a step ahead of its use.
+    struct Keys {
+        int tok, page, at;  // the lane's key: its token (kNone: none), logical page and place there
+        int head, b;
+    };
+    int looked = 0, issued = 0;
+    struct {
+        int entry, off, len, kvh, b;  // the block list's entry for the lane's key, and the key's place in the block
+    } from_list;
+    Keys next;       // its page's entry of the table is loaded
+    int next_entry;
+    auto move_on = [&]() {
+        if (++looked < count) {
+            Cursor c = ahead;
+            advance<STEP, LIST>(c, a, cap, shared);
+            __syncwarp();
+            if (lane == 0) ahead = c;
+            __syncwarp();
+        }
+    };
+    auto look_list = [&]() {  // LIST: the list's entries of step `looked`
+        const int key = ahead.s * STEP + warp * KEYS + lane % KEYS;
+        from_list.len = ahead.len;
+        from_list.kvh = ahead.kvh;
+        from_list.b = ahead.b;
+        const int i = (int)a.block.div(key);
+        from_list.off = key - i * (int)a.block.d;
+        from_list.entry = looked < count && key < ahead.keys
+                              ? a.list[((long long)ahead.b * a.Hkv + ahead.kvh) * a.keep + i]
+                              : -1;
+        move_on();
+    };
+    auto look_table = [&]() {  // the table's entries of the step after the one issued next
+        if constexpr (LIST) {
+            next.b = from_list.b;
+            next.head = from_list.kvh;
+            const int blocks = (int)a.block.div(from_list.len + a.block.d - 1);
+            if (from_list.entry >= blocks) bad = true;
+            next.tok = from_list.entry >= 0 && from_list.entry < blocks ? from_list.entry * (int)a.block.d + from_list.off : kNone;
+            if (next.tok >= from_list.len) next.tok = kNone;
+        } else {
+            const int key = ahead.s * STEP + warp * KEYS + lane % KEYS;
+            next.b = ahead.b;
+            next.head = ahead.kvh;
+            next.tok = looked < count && key < ahead.keys ? key + ahead.len - ahead.keys : kNone;
+        }
+        const int lpage = next.tok == kNone ? 0 : (int)a.page.div(next.tok);
+        next.at = next.tok - lpage * P;
+        next_entry = next.tok == kNone ? -1 : a.table[(long long)next.b * a.max_pages + lpage];
+        if (!LIST) move_on();
+    };
+    auto issue = [&](int slot) {
+        if (issued < count) {
+            const bool in = next.tok != kNone, ok = in && (unsigned)next_entry < (unsigned)a.num_pages;
+            bad |= in && !ok;
+            const uint32_t row = ok ? ((uint32_t)next_entry * a.Hkv + next.head) * P + next.at : ~0u;  // cache row
+            const uint32_t base = ring_u + slot * C::SLOT;
+            if (lane < KEYS) reinterpret_cast<int*>(ring + slot * C::SLOT + 2 * C::HALF)[lane] = next.tok;
+#pragma unroll
+            for (int n = 0; n < KEYS / RPI; ++n) {
+                const int key = n * RPI + cr;
+                const uint32_t rr = __shfl_sync(0xffffffffu, row, key);
+                const bool there = rr != ~0u;
+                const size_t off = (size_t)(there ? rr : 0u) * D;
+                const uint32_t to = base + key * (D * 2) + ((cc ^ (key & 7)) << 4);
+                copy16(to, kp + off, there);
+                copy16(to + C::HALF, vp + off, there);
+            }
+        }
+        ++issued;
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    // a step's keys are read by the warps of the group
+    auto group_sync = [&]() {
+        if constexpr (RG == 1)
+            __syncwarp();
+        else if (kg == 0)
+            bar_sync(1, RG * 32);
+        else
+            bar_sync(2, RG * 32);
+    };
+    // ---- Q fragments: k-step s of lane (g, t): row g, columns 16 s + 2 t, + 1 and 16 s + 8 + 2 t, + 1
+    uint32_t qb[NB][KS][2];
+    auto load_q = [&]() {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+            const int r = cur.rt * ROWS + (rg * NB + nb) * 8 + g;
+            const uint32_t* src = reinterpret_cast<const uint32_t*>(
+                                      a.q + (((long long)cur.b * a.Hkv + cur.kvh) * a.rows + (r < a.rows ? r : 0)) * D) + t;
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+                qb[nb][s][0] = r < a.rows ? src[s * 8] : 0u;
+                qb[nb][s][1] = r < a.rows ? src[s * 8 + 4] : 0u;
+            }
+        }
+    };
+    if (LIST) look_list();
+    look_table();
+    if (LIST) look_list();
+    load_q();
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) {
+        issue(i);
+        look_table();
+        if (LIST) look_list();
+    }
+
+    // ---- the steps
+    float acc[NB][D / 16][4];           // O^T: columns 16 i + g + 8 (c / 2) of rows 2 t + c % 2 of each eight
+    float m[NB][2], l[NB][2];           // of rows 2 t + j; the references start at the lowest number: a row that sees no
+                                        // key keeps l = 0 (2^(-inf - m))
+    int seg = 0, slot = 0;              // first step of the segment within its item; ring slot
+    bool begins = true;
+    // fragment addresses: rows of the lane's part of ldmatrix, and its piece of 16 bytes
+    const int kr = lane % 16, kc = lane / 16, vr = lane % 8 + lane / 16 * 8, vc = lane / 8 % 2;
+    for (int it = 0; it < count; ++it) {
+        const int r0 = cur.rt * ROWS + rg * NB * 8, nrows = min(ROWS, a.rows - cur.rt * ROWS);  // of the warp, of the tile
+        const long long bh = (long long)cur.b * a.Hkv + cur.kvh;
+        if (begins) {
+            seg = cur.s;
+            if (it > 0) load_q();
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) acc[nb][i][0] = acc[nb][i][1] = acc[nb][i][2] = acc[nb][i][3] = 0.f;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) m[nb][j] = -FLT_MAX, l[nb][j] = 0.f;
+            }
+        }
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+        group_sync();  // every lane's copies are there, and the slot before is read
+        issue(slot == 0 ? kStages - 1 : slot - 1);
+        look_table();
+        if (LIST) look_list();
+        const int sees_all = cur.len - Nq;  // every row sees the tokens up to this one
+        // A value product multiplies a key's V by the zero weights of the rows that do not see it, and 0 x infinity is NaN.
+        // Where some rows see a key and others do not (the last Nq - 1 tokens), infinities and NaN are added to the sums of
+        // the rows that do, and become zeros in the stage.
+        if (DRAFTS) {
+            uint8_t* group = smem + kg * RG * C::RING + slot * C::SLOT;  // of key part * KEYS + k: + part * RING
+            auto tok_of = [&](int key) {
+                return reinterpret_cast<const int*>(group + key / KEYS * C::RING + 2 * C::HALF)[key % KEYS];
+            };
+            bool partly = false;
+            for (int key = lane; key < RG * KEYS; key += 32) partly |= tok_of(key) > sees_all && tok_of(key) != kNone;
+            if (__any_sync(0xffffffffu, partly)) {
+                auto word_of = [&](int key, int col) {  // the word of columns col, col + 1
+                    return reinterpret_cast<uint32_t*>(group + key / KEYS * C::RING + C::HALF + key % KEYS * (D * 2) +
+                                                       (((col / 8) ^ (key & 7)) << 4)) + col % 8 / 2;
+                };
+                auto wild = [](uint32_t half) { return (half & 0x7F80u) == 0x7F80u; };
+                bool found = false;
+                for (int key = 0; key < RG * KEYS; ++key)
+                    if (tok_of(key) > sees_all && tok_of(key) != kNone)
+                        for (int c = lane * 2; c < D; c += 64) {
+                            const uint32_t w = *word_of(key, c);
+                            found |= wild(w & 0xFFFFu) || wild(w >> 16);
+                        }
+                if (__any_sync(0xffffffffu, found)) {  // in all warps of the group alike
+#pragma unroll 1
+                    for (int key = 0; key < RG * KEYS; ++key) {
+                        const int tok = tok_of(key);
+                        if (tok <= sees_all || tok == kNone) continue;
+#pragma unroll
+                        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const int col = 16 * i + g + 8 * h;
+                                const uint32_t half = *word_of(key, col & ~1) >> (col & 1) * 16 & 0xFFFFu;
+                                if (!wild(half)) continue;
+#pragma unroll
+                                for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                                    for (int j = 0; j < 2; ++j)
+                                        if (tok <= sees_all + (r0 + nb * 8 + 2 * t + j) % Nq)
+                                            acc[nb][i][2 * h + j] += __uint_as_float(half << 16);
+                            }
+                    }
+                    group_sync();  // every warp has read them
+#pragma unroll 1
+                    for (int key = 0; key < RG * KEYS; ++key) {
+                        if (key / KEYS != rg || tok_of(key) <= sees_all || tok_of(key) == kNone) continue;
+                        for (int c = lane * 2; c < D; c += 64) {
+                            uint32_t* w = word_of(key, c);
+                            *w &= (wild(*w & 0xFFFFu) ? 0u : 0xFFFFu) | (wild(*w >> 16) ? 0u : 0xFFFF0000u);
+                        }
+                    }
+                    group_sync();
+                }
+            }
+        }
+#pragma unroll 1
+        for (int part = 0; part < RG; ++part) {
+            if (cur.s * STEP + (kg * RG + part) * KEYS >= cur.keys || rg * NB * 8 >= nrows) break;
+            const uint8_t* st = smem + (kg * RG + part) * C::RING + slot * C::SLOT;
+            const uint32_t st_u = smem_u32(st);
+            float S[NB][MT][4];  // keys 16 i + g, + 8 (c / 2) of rows 2 t + c % 2
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int i = 0; i < MT; ++i) S[nb][i][0] = S[nb][i][1] = S[nb][i][2] = S[nb][i][3] = 0.f;
+#pragma unroll
+            for (int s = 0; s < KS; ++s)
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    uint32_t ka[4];
+                    ldmatrix4(ka, st_u + (i * 16 + kr) * (D * 2) + (((2 * s + kc) ^ (kr & 7)) << 4));
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb) mma_bf16(S[nb][i], ka, qb[nb][s][0], qb[nb][s][1]);
+                }
+            const int* toks = reinterpret_cast<const int*>(st + 2 * C::HALF);
+            const bool masked = __any_sync(0xffffffffu, toks[lane % KEYS] > sees_all);
+            uint32_t pb[NB][MT][2], pl[NB][MT][2];
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+                auto& x = S[nb];
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) x[i][c] *= a.scale_log2;
+                if (masked) {
+#pragma unroll
+                    for (int i = 0; i < MT; ++i)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int tok = toks[i * 16 + h * 8 + g];
+#pragma unroll
+                            for (int j = 0; j < 2; ++j)
+                                if (tok > sees_all + (DRAFTS ? (r0 + nb * 8 + 2 * t + j) % Nq : 0)) x[i][2 * h + j] = -INFINITY;
+                        }
+                }
+                // softmax: m need not be the maximum, only within 2^8 of it: most steps find no larger one and skip the
+                // reductions
+                float mx[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    mx[j] = fmaxf(x[0][j], x[0][2 + j]);
+#pragma unroll
+                    for (int i = 1; i < MT; ++i) mx[j] = fmax3(mx[j], x[i][j], x[i][2 + j]);
+                }
+                if (__any_sync(0xffffffffu, mx[0] > m[nb][0] + kSlack || mx[1] > m[nb][1] + kSlack)) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        float top = fmaxf(m[nb][j], mx[j]);
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                        const float f = ex2(fmaxf(m[nb][j] - top, -120.f));  // not 0: an infinite sum stays one
+                        l[nb][j] *= f;
+                        m[nb][j] = top;
+#pragma unroll
+                        for (int i = 0; i < D / 16; ++i) {
+                            acc[nb][i][j] *= f;
+                            acc[nb][i][2 + j] *= f;
+                        }
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float p0 = ex2(x[i][2 * h] - m[nb][0]), p1 = ex2(x[i][2 * h + 1] - m[nb][1]);
+                        l[nb][0] += p0;
+                        l[nb][1] += p1;
+                        const uint32_t hi = pack_bf16(p0, p1);
+                        pb[nb][i][h] = transpose8x8(hi);
+                        pl[nb][i][h] = transpose8x8(
+                            pack_bf16(p0 - __uint_as_float(hi << 16), p1 - __uint_as_float(hi & 0xFFFF0000u)));
+                    }
+            }
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int c = 0; c < D / 16; ++c) {
+                    uint32_t va[4];
+                    ldmatrix4_trans(va, st_u + C::HALF + (i * 16 + vr) * (D * 2) + (((2 * c + vc) ^ (vr & 7)) << 4));
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb) {
+                        mma_bf16(acc[nb][c], va, pb[nb][i][0], pb[nb][i][1]);
+                        mma_bf16(acc[nb][c], va, pl[nb][i][0], pl[nb][i][1]);
+                    }
+                }
+        }
+        slot = slot + 1 == kStages ? 0 : slot + 1;
+
+        // ---- at the segment's end: O = sum over the warps with these rows of O_w 2^(m_w - m) / l
+        const bool item_ends = cur.s + 1 == cur.n;
+        begins = item_ends || it + 1 == count;
+        if (begins) {
+            float f[NB][2];
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) l[nb][j] += __shfl_xor_sync(0xffffffffu, l[nb][j], d);
+                    const int r = nb * 8 + 2 * t + j;
+                    if (g == 0) s_stat[warp][0][r] = m[nb][j], s_stat[warp][1][r] = l[nb][j];
+                }
+            __syncthreads();
+            float* buf = reinterpret_cast<float*>(smem + C::MERGE) + g;
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int r = nb * 8 + 2 * t + j;
+                    float top = m[nb][j], sum = 0.f;
+#pragma unroll
+                    for (int w = 0; w < KG; ++w) top = fmaxf(top, s_stat[w * RG + rg][0][r]);
+#pragma unroll
+                    for (int w = 0; w < KG; ++w) sum += s_stat[w * RG + rg][1][r] * ex2(s_stat[w * RG + rg][0][r] - top);
+                    // a warp that saw none of the row's keys adds nothing (its V may have been infinite); NaN stays
+                    f[nb][j] = l[nb][j] == 0.f ? 0.f : ex2(m[nb][j] - top) / sum;
+                    if (l[nb][j] == 0.f)
+#pragma unroll
+                        for (int i = 0; i < D / 16; ++i) acc[nb][i][j] = acc[nb][i][2 + j] = 0.f;
+                    m[nb][j] = top;
+                    l[nb][j] = sum;
+                    if (kg > 0)
+#pragma unroll
+                        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+                                buf[((warp - RG) * 8 + 2 * t + j) * C::OROW + 16 * i + 8 * h] = acc[nb][i][2 * h + j] * f[nb][j];
+                }
+                __syncthreads();
+                if (kg == 0) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                float x = acc[nb][i][2 * h + j] * f[nb][j];
+#pragma unroll
+                                for (int w = 1; w < KG; ++w)
+                                    x += buf[((w - 1) * RG + rg) * 8 * C::OROW + (2 * t + j) * C::OROW + 16 * i + 8 * h];
+                                acc[nb][i][2 * h + j] = x;
+                            }
+                }
+                if (nb + 1 < NB) __syncthreads();
+            }
+            if (kg == 0) {
+                const bool whole = seg == 0 && item_ends && (LIST || shared_of(shared, cur.len, Nq) == 0);
+                const long long slot_out = blockIdx.x + bh * a.row_tiles + cur.rt;
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int r = (rg * NB + nb) * 8 + 2 * t + j;
+                        if (r >= nrows) continue;
+                        const float sum = l[nb][j], lse2 = sum == 0.f ? -INFINITY : m[nb][j] + lg2(sum);
+                        if (whole) {
+                            const long long row = bh * a.rows + cur.rt * ROWS + r;  // (b, head, token) flattened
+                            __nv_bfloat16* dst = a.o + row * D + g;
+#pragma unroll
+                            for (int i = 0; i < D / 16; ++i) {
+                                dst[16 * i] = __float2bfloat16_rn(acc[nb][i][j]);
+                                dst[16 * i + 8] = __float2bfloat16_rn(acc[nb][i][2 + j]);
+                            }
+                            if (a.lse && g == 0) a.lse[row] = lse2 * kLn2;
+                        } else {
+                            float* dst = a.part_o + (slot_out * ROWS + r) * D + g;
+#pragma unroll
+                            for (int i = 0; i < D / 16; ++i) {
+                                dst[16 * i] = acc[nb][i][j];
+                                dst[16 * i + 8] = acc[nb][i][2 + j];
+                            }
+                            if (g == 0) a.part_lse[slot_out * ROWS + r] = lse2;
+                        }
+                    }
+            }
+            __syncthreads();  // the statistics and buffers are read
+        }
+        if (it + 1 < count) advance<STEP, LIST>(cur, a, cap, shared);
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    if (__any_sync(0xffffffffu, bad) && lane == 0) record_invalid(a.err, kSiteCacheTable, -1);
+}
+
+// ------------------------------------------------------------------ merge
+// A row's parts: `n` slots from `slot` on of the segments, `pn` from `pslot` on of the shared prefix.
+struct Parts {
+    long long slot, pslot;
+    int n, pn;
+    bool done;  // written already
+};
+
+// The segments of item i (sequence b, kv head, row tile) are those of the CTAs that hold its first to its last step;
+// CTA c's is in slot c + i.
+template <bool LIST>
+__device__ __forceinline__ Parts find_parts(const Params& a, int b, int kvh, int rt, int row) {
+    const long long per_step = (long long)a.Hkv * a.row_tiles;
+    const int item_b = kvh * a.row_tiles + rt;
+    const long long p0 = a.prefix[b], n = a.prefix[b + 1] - p0, total = a.prefix[a.B] * per_step;
+    Parts x{0, 0, 0, 0, false};
+    if (n > 0) {
+        const long long s0 = p0 * per_step + item_b * n, s1 = s0 + n - 1;  // first and last step
+        const long long workers = min((long long)a.workers, total);
+        const long long c0 = ((s0 + 1) * workers - 1) / total, c1 = ((s1 + 1) * workers - 1) / total;
+        x.slot = c0 + b * per_step + item_b;
+        x.n = (int)(c1 - c0) + 1;
+    }
+    if constexpr (!LIST) {
+        const int cap = a.max_pages * (int)a.page.d, shared = clamp_len(*a.shared, cap);
+        if (shared_of(shared, clamp_len(a.lens[b], cap), a.Nq) > 0) {
+            const PrefixShare w = prefix_share(shared, a.Hkv, a.pre_tiles, a.pre_workers);
+            const int item = kvh * a.pre_tiles + (int)(((long long)b * a.rows + row) / a.pre_rows);
+            const long long s0 = (long long)item * w.steps, s1 = s0 + w.steps - 1;
+            const long long c0 = ((s0 + 1) * w.workers - 1) / w.total, c1 = ((s1 + 1) * w.workers - 1) / w.total;
+            x.pslot = c0 + item;
+            x.pn = (int)(c1 - c0) + 1;
+        }
+    }
+    x.done = x.n == 1 && x.pn == 0;
+    return x;
+}
+
+// LSE = M + log2 sum 2^(lse_s - M), O = sum 2^(lse_s - M) o_s / sum over a row's parts.  D / 4 threads per row and group;
+// SPLIT: one row per block, its parts dealt to the groups, else a row per group.  A row without keys gets O = 0, LSE = -inf.
+template <int D, int ROWS, bool LIST, bool SPLIT, int THREADS>
+__global__ void __launch_bounds__(THREADS) merge_rows_kernel(const Params a) {
+    constexpr int LANES = D / 4, GROUPS = THREADS / LANES, AHEAD = 4;
+    __shared__ float4 s_o[SPLIT ? GROUPS : 1][LANES];
+    __shared__ float2 s_ms[SPLIT ? GROUPS : 1];
+    pdl_wait();
+    const int tid = threadIdx.x, grp = tid / LANES, col = tid % LANES;
+    const long long all = (long long)a.B * a.Hkv * a.rows, row = SPLIT ? blockIdx.x : (long long)blockIdx.x * GROUPS + grp;
+    if (row >= all) return;
+    const long long bh = row / a.rows;
+    const int r = (int)(row - bh * a.rows), b = (int)(bh / a.Hkv), kvh = (int)(bh - (long long)b * a.Hkv), rt = r / ROWS;
+    const Parts x = find_parts<LIST>(a, b, kvh, rt, r);
+    if (x.done) return;
+    const int n = x.n + x.pn, prow = LIST ? 0 : (int)(((long long)b * a.rows + r) % a.pre_rows);
+    auto lse_at = [&](int s) {
+        return s < x.n ? a.part_lse[(x.slot + s) * ROWS + (r - rt * ROWS)]
+                       : a.pre_lse[(x.pslot + s - x.n) * a.pre_rows + prow];
+    };
+    auto o_at = [&](int s) {
+        return reinterpret_cast<const float4*>(s < x.n ? a.part_o + ((x.slot + s) * ROWS + (r - rt * ROWS)) * D
+                                                       : a.pre_o + ((x.pslot + s - x.n) * a.pre_rows + prow) * D)[col];
+    };
+    float m = -INFINITY, sum = 0.f;  // running maximum and sum of this group's parts
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    constexpr int STRIDE = SPLIT ? GROUPS : 1;
+    for (int s0 = SPLIT ? grp : 0; s0 < n; s0 += AHEAD * STRIDE) {
+        float w[AHEAD];
+        float4 v[AHEAD];
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const int s = s0 + i * STRIDE;
+            w[i] = s < n ? lse_at(s) : -INFINITY;
+            v[i] = s < n ? o_at(s) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        float top = m;
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) top = fmaxf(top, w[i]);
+        const float base = top == -INFINITY ? 0.f : top, f = ex2(m - base);
+        o.x *= f, o.y *= f, o.z *= f, o.w *= f;
+        sum *= f;
+        m = top;
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const float e = ex2(w[i] - base);
+            sum += e;
+            if (e != 0.f) {  // a part without keys is zero, whatever is in its place; NaN stays
+                o.x = fmaf(e, v[i].x, o.x);
+                o.y = fmaf(e, v[i].y, o.y);
+                o.z = fmaf(e, v[i].z, o.z);
+                o.w = fmaf(e, v[i].w, o.w);
+            }
+        }
+    }
+    if constexpr (SPLIT) {
+        s_o[grp][col] = o;
+        if (col == 0) s_ms[grp] = make_float2(m, sum);
+        __syncthreads();
+        if (grp > 0) return;
+        float top = m;
+#pragma unroll
+        for (int i = 1; i < GROUPS; ++i) top = fmaxf(top, s_ms[i].x);
+        const float base = top == -INFINITY ? 0.f : top;
+        sum = 0.f;
+        o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < GROUPS; ++i) {
+            const float f = ex2(s_ms[i].x - base);
+            sum += s_ms[i].y * f;
+            if (f != 0.f) {
+                const float4 y = s_o[i][col];
+                o.x = fmaf(f, y.x, o.x);
+                o.y = fmaf(f, y.y, o.y);
+                o.z = fmaf(f, y.z, o.z);
+                o.w = fmaf(f, y.w, o.w);
+            }
+        }
+        m = top;
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    *reinterpret_cast<uint2*>(a.o + row * D + col * 4) = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+    if (a.lse && col == 0) a.lse[row] = sum == 0.f ? -INFINITY : (m + lg2(sum)) * kLn2;
+}
+
+template <int D, int ROWS, bool LIST>
+cudaError_t launch_merge(const DecodeRowsLaunch& a, const Params& p, cudaStream_t s) {
+    const long long rows = (long long)a.B * a.Hkv * p.rows;
+    // rows alone in a block where there are few of them: their parts are read by more threads
+    if (rows <= 4ll * a.num_sms)
+        return launch_dependent(merge_rows_kernel<D, ROWS, LIST, true, 256>, dim3((unsigned)rows), dim3(256), 0, s, p);
+    constexpr int PER = 128 / (D / 4);
+    return launch_dependent(merge_rows_kernel<D, ROWS, LIST, false, 128>, dim3((unsigned)((rows + PER - 1) / PER)), dim3(128), 0,
+                            s, p);
+}
+
+template <int D, int ROWS, bool LIST>
+cudaError_t launch_l(const DecodeRowsLaunch& a, cudaStream_t s) {
+    using C = Cfg<D, ROWS>;
+    cudaError_t e = a.Nq > 1 ? set_smem_limit_once<decode_rows_kernel<D, ROWS, true, LIST>>(C::SMEM)
+                             : set_smem_limit_once<decode_rows_kernel<D, ROWS, false, LIST>>(C::SMEM);
+    if (e != cudaSuccess) return e;
+    Params p;
+    p.q = (const __nv_bfloat16*)a.q;
+    p.kp = (const __nv_bfloat16*)a.kp;
+    p.vp = (const __nv_bfloat16*)a.vp;
+    p.table = a.table;
+    p.lens = a.lens;
+    p.list = a.list;
+    p.shared = a.shared;
+    p.o = (__nv_bfloat16*)a.o;
+    p.lse = a.lse;
+    p.part_o = a.part_o;
+    p.part_lse = a.part_lse;
+    p.prefix = a.prefix;
+    p.pre_o = a.pre_o;
+    p.pre_lse = a.pre_lse;
+    p.B = a.B;
+    p.Hkv = a.Hkv;
+    p.Nq = a.Nq;
+    p.max_pages = a.max_pages;
+    p.num_pages = a.num_pages;
+    p.rows = a.Hq / a.Hkv * a.Nq;
+    p.row_tiles = (p.rows + ROWS - 1) / ROWS;
+    p.keep = a.keep;
+    p.pre_workers = a.pre_workers;
+    p.pre_tiles = a.pre_tiles;
+    p.pre_rows = a.pre_rows;
+    p.page = FastDiv((uint32_t)a.page);
+    p.block = FastDiv((uint32_t)std::max(a.block, 1));
+    p.scale_log2 = a.scale * kLog2e;
+    p.err = a.err;
+    // no more CTAs than steps at full lengths
+    const long long most = LIST ? std::min((long long)a.keep * a.block, (long long)a.max_pages * a.page + a.block)
+                                : (long long)a.max_pages * a.page;
+    p.workers = (int)std::min<long long>(std::min(C::CTAS * a.num_sms, kRowsMostWorkers),
+                                         (long long)a.B * a.Hkv * p.row_tiles * ((most + C::STEP - 1) / C::STEP));
+    e = launch_dependent(a.Nq > 1 ? decode_rows_kernel<D, ROWS, true, LIST> : decode_rows_kernel<D, ROWS, false, LIST>,
+                         dim3(p.workers), dim3(kThreads), C::SMEM, s, p);
+    return e != cudaSuccess ? e : launch_merge<D, ROWS, LIST>(a, p, s);
+}
+
+template <int D, int ROWS>
+cudaError_t launch_r(const DecodeRowsLaunch& a, cudaStream_t s) {
+    return a.list ? launch_l<D, ROWS, true>(a, s) : launch_l<D, ROWS, false>(a, s);
+}
+
+}  // namespace
+
+cudaError_t launch_decode_rows(const DecodeRowsLaunch& a, cudaStream_t s) {
+    const int tile = rows_tile(a.Hq / a.Hkv * a.Nq);
+    if (a.d == 128) return tile == 8 ? launch_r<128, 8>(a, s) : tile == 16 ? launch_r<128, 16>(a, s) : launch_r<128, 32>(a, s);
+    return tile == 8 ? launch_r<64, 8>(a, s) : tile == 16 ? launch_r<64, 16>(a, s) : launch_r<64, 32>(a, s);
+}
+
+}  // namespace fa

@@ -227,6 +227,91 @@ struct PagedDecodeFp8Launch {
     DevError* err;
 };
 
+struct PagedAppendLaunch {
+    const void* k;        // bf16 [B, Hkv, N, d] by strides
+    const void* v;
+    long long kb, kh, kn, vb, vh, vn;
+    void* kp;             // bf16 [num_pages, Hkv, page, d]
+    void* vp;
+    void* bounds;         // bf16 [num_pages, Hkv, page / block, 2, d], or null
+    const int* table;     // int32 [B, max_pages]
+    const int* lens;      // int32 [B] tokens already in the cache
+    const int* new_lens;  // int32 [B], or null (N)
+    const int* positions; // int32 [B, N], or null (lens[b] + i)
+    const uint64_t* turns;  // [rot / 2], or null (no rotation)
+    int B, Hkv, N, d, rot, interleaved, page, block, max_pages, num_pages;
+    float magnitude;
+    int num_sms;
+    DevError* err;
+};
+
+constexpr int kSelectCtas = 8;  // of a cluster, at most
+
+struct SelectLaunch {
+    const void* q;        // bf16 [B, Hkv, rows, d]
+    const void* bounds;   // bf16 [num_pages, Hkv, page_blocks, 2, d]
+    const int* table;     // int32 [B, max_pages]
+    const int* lens;      // int32 [B]
+    int* out;             // int32 [B, Hkv, keep]
+    float* scores;        // workspace: [B * Hkv, stride]
+    void* exact;          // 64-bit [B * Hkv, stride]
+    uint32_t* big;        // [B * Hkv, kSelectCtas]
+    long long stride;
+    int B, Hkv, rows, block, page_blocks, max_pages, num_pages, d, keep, first, recent;
+    int num_sms;
+    DevError* err;
+};
+
+// The shares of a shared prefix's steps of 128 keys over (kv head, tile of query rows): `total` of them for `workers` CTAs,
+// of which CTA c takes those from c total / workers on.
+struct PrefixShare {
+    int steps;  // of a (kv head, tile)
+    long long total, workers;
+};
+__host__ __device__ inline PrefixShare prefix_share(int shared, int Hkv, int tiles, int ctas) {
+    PrefixShare w;
+    w.steps = (shared + 127) / 128;
+    w.total = (long long)Hkv * tiles * w.steps;
+    w.workers = ctas < w.total ? ctas : w.total;
+    return w;
+}
+
+struct PrefixLaunch {
+    CUtensorMap map_k, map_v;  // 4-D (d, page, Hkv, num_pages), box (64, box, 1, 1), 128B swizzle
+    const void* q;             // bf16 [B, Hq, Nq, d]
+    const int* table;          // int32 [B, max_pages]
+    const int* lens;           // int32 [B]
+    const int* shared;         // int32 [1]
+    float* part_o;             // fp32 [workers + Hkv * tiles, tile_rows, d]
+    float* part_lse;           // fp32 [workers + Hkv * tiles, tile_rows]
+    int B, Hq, Hkv, Nq, page, box, max_pages, num_pages, d, tiles, tile_rows, workers;
+    float scale;
+    DevError* err;
+    uint64_t timeout_ns;
+};
+
+struct DecodeRowsLaunch {
+    const void* q;         // bf16 [B, Hq, Nq, d]
+    const void* kp;        // bf16 [num_pages, Hkv, page, d]
+    const void* vp;
+    const int* table;      // int32 [B, max_pages]
+    const int* lens;       // int32 [B]
+    const int* list;       // int32 [B, Hkv, keep] blocks, or null: the tokens behind the shared ones
+    const int* shared;     // int32 [1], or null with a list
+    void* o;               // bf16 [B, Hq, Nq, d]
+    float* lse;            // fp32 [B, Hq, Nq], or null
+    float* part_o;         // fp32 [workers + items, tile rows, d]
+    float* part_lse;       // fp32 [workers + items, tile rows]
+    long long* prefix;     // [B + 1]
+    const float* pre_o;    // the shared prefix's parts (PrefixLaunch), with `shared`
+    const float* pre_lse;
+    int B, Hq, Hkv, Nq, page, block, keep, max_pages, num_pages, d;
+    int pre_workers, pre_tiles, pre_rows;
+    int num_sms;
+    float scale;
+    DevError* err;
+};
+
 // The dynamic shared-memory limit of kernel K, raised once per device: the
 // attribute stays with the function in the context, and setting it costs a
 // driver call per launch otherwise.
@@ -298,6 +383,14 @@ cudaError_t launch_decode_paged_fp8(const PagedDecodeFp8Launch& a, cudaStream_t 
 // Query rows (of one kv head) that a pass over the cache serves: the tile that holds `rows`, or the largest.
 inline int fp8_tile_rows(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
 cudaError_t decode_fp8_blocks_per_sm(int d, int tile_rows, int* blocks);  // resident CTAs of its first kernel on one SM
+cudaError_t launch_paged_append(const PagedAppendLaunch& a, cudaStream_t s);
+cudaError_t launch_select_blocks(const SelectLaunch& a, cudaStream_t s);
+cudaError_t launch_prefix(const PrefixLaunch& a, cudaStream_t s);
+cudaError_t launch_decode_rows(const DecodeRowsLaunch& a, cudaStream_t s);  // the parts, then their merge
+// Query rows (of one kv head) that a pass over the keys serves: the tile that holds `rows`, or the largest.
+inline int rows_tile(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
+constexpr int kRowsMostWorkers = 512;    // CTAs of decode_rows at most (bounds the workspace; two on each of 152 SMs are 304)
+constexpr int kPrefixMostWorkers = 256;  // CTAs of the prefix at most
 // LSE-weighted merge of per-split partials into o (bf16) and lse (fp32, may be null).
 cudaError_t launch_decode_combine(const float* part_o, const float* part_lse, void* o, float* lse, int BH,
                                   int splits, int d, cudaStream_t s);

@@ -1,5 +1,6 @@
 // Native binding of the serving-cache conveniences (rope, cache_append_fp8,
-// decode_paged_fp8, cache_evict_fp8): checks the tensors, allocates the outputs
+// decode_paged_fp8, cache_evict_fp8 and, for the bf16 cache, cache_append,
+// select_blocks, decode_blocks, decode_shared): checks the tensors, allocates the outputs
 // and the workspace with torch on its current stream, and calls the C ABI.  The
 // same steps in Python took 21 to 40 us of host time per call, these take 4 to
 // 10; the small calls take about 4 us on the GPU.
@@ -8,6 +9,7 @@
 // same name, and returns its result, or the status of a C call that failed.
 #include <Python.h>
 
+#include <algorithm>
 #include <climits>
 #include <cmath>
 
@@ -266,8 +268,174 @@ PyObject* evict(PyObject*, PyObject* const* o, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+// The paged bf16 cache: pages, table and lengths.
+struct Pages {
+    c10::Device dev = c10::Device(c10::kCPU);
+    int B, Hkv, page, d, max_pages, num_pages;
+    void *k, *v, *table, *lens;
+
+    Pages(PyObject* kp, PyObject* vp, PyObject* tab, PyObject* len) {
+        const Tensor &p = tensor(kp, "k_pages"), &t = tensor(tab, "block_table");
+        TORCH_CHECK_VALUE(p.is_cuda() && p.dim() == 4, "k_pages must be a CUDA tensor [num_pages, Hkv, page, d]");
+        TORCH_CHECK_VALUE(t.dim() == 2, "block_table must have 2 dimensions");
+        dev = p.device();
+        k = checked(kp, "k_pages", at::kBFloat16, p.sizes(), dev);
+        v = checked(vp, "v_pages", at::kBFloat16, p.sizes(), dev);
+        table = checked(tab, "block_table", at::kInt, t.sizes(), dev);
+        lens = checked(len, "seq_lens", at::kInt, {t.size(0)}, dev);
+        num_pages = size(p.size(0), "num_pages");
+        Hkv = size(p.size(1), "Hkv");
+        page = size(p.size(2), "page");
+        d = size(p.size(3), "d");
+        B = size(t.size(0), "B");
+        max_pages = size(t.size(1), "max_pages");
+    }
+};
+
+// q [B, Hq, Nq, d], or [B, Hq, d] for one new token.
+struct Queries {
+    const Tensor& t;
+    int Hq, Nq;
+
+    Queries(PyObject* o, c10::Device dev, int B, int d) : t(tensor(o, "q")) {
+        const int64_t dims = t.dim();
+        TORCH_CHECK_VALUE((dims == 3 || dims == 4) && t.scalar_type() == at::kBFloat16 && t.device() == dev &&
+                              t.is_contiguous() && t.size(0) == B && t.size(dims - 1) == d,
+                          "q must be a contiguous bf16 tensor [B, Hq, Nq, d] or [B, Hq, d] on the cache's device");
+        Hq = size(t.size(1), "Hq");
+        Nq = dims == 4 ? size(t.size(2), "Nq") : 1;
+    }
+};
+
+Tensor workspace(PyObject* o, size_t bytes, c10::Device dev) {
+    if (o == Py_None) return make({(int64_t)bytes}, at::kByte, dev);
+    const Tensor& t = tensor(o, "workspace");
+    TORCH_CHECK_VALUE(t.device() == dev && t.is_contiguous(), "workspace must be contiguous, on the cache's device");
+    return t;
+}
+
+// cache_append(k, v, k_pages, v_pages, block_table, seq_lens, new_lens, turns, positions, interleaved, magnitude, bounds)
+PyObject* paged_append(PyObject*, PyObject* const* o, Py_ssize_t n) {
+    if (!count(n, 12)) return nullptr;
+    HANDLE_TH_ERRORS
+    const Pages c(o[2], o[3], o[4], o[5]);
+    const Tensor &k = bhnd(o[0], "k"), &v = bhnd(o[1], "v");
+    TORCH_CHECK_VALUE(k.device() == c.dev && v.device() == c.dev && k.size(0) == c.B && k.size(1) == c.Hkv &&
+                          k.size(3) == c.d && v.sizes() == k.sizes(),
+                      "k and v must have shape [B, Hkv, N, d], on the cache's device");
+    const int N = size(k.size(2), "N");
+    const auto fresh = static_cast<const int*>(optional(o[6], "new_lens", at::kInt, {c.B}, c.dev));
+    int rot = 0, block = 1;
+    const uint64_t* turns = o[7] == Py_None ? nullptr : turns_of(o[7], c.dev, &rot);
+    const auto pos = static_cast<const int*>(turns ? optional(o[8], "positions", at::kInt, {c.B, N}, c.dev) : nullptr);
+    const int inter = truth(o[9]);
+    const float magnitude = number(o[10]);
+    void* bounds = nullptr;
+    if (o[11] != Py_None) {
+        const Tensor& t = tensor(o[11], "bounds");
+        TORCH_CHECK_VALUE(t.dim() == 5 && t.size(2) >= 1 && c.page % t.size(2) == 0,
+                          "bounds must have shape [num_pages, Hkv, a divisor of the page size, 2, d]");
+        bounds = checked(o[11], "bounds", at::kBFloat16, {c.num_pages, c.Hkv, t.size(2), 2, c.d}, c.dev);
+        block = (int)(c.page / t.size(2));
+    }
+    const c10::cuda::CUDAGuard guard(c.dev);
+    void* stream = stream_of(c.dev);
+    const int st = call([&] {
+        return fa_cache_append(k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), k.stride(2), v.stride(0), v.stride(1),
+                               v.stride(2), c.k, c.v, bounds, (const int*)c.table, (const int*)c.lens, fresh, pos, turns,
+                               c.B, c.Hkv, N, c.d, rot, inter, magnitude, c.page, block, c.max_pages, c.num_pages, stream);
+    });
+    if (st == FA_OK) {
+        written(o[2]);
+        written(o[3]);
+        if (bounds) written(o[11]);
+    }
+    return status(st);
+    END_HANDLE_TH_ERRORS
+}
+
+// select_blocks(q, bounds, block_table, seq_lens, block, keep, first, recent, workspace)
+PyObject* select_blocks(PyObject*, PyObject* const* o, Py_ssize_t n) {
+    if (!count(n, 9)) return nullptr;
+    HANDLE_TH_ERRORS
+    const Tensor &bounds = tensor(o[1], "bounds"), &tab = tensor(o[2], "block_table");
+    TORCH_CHECK_VALUE(bounds.is_cuda() && bounds.dim() == 5 && bounds.size(3) == 2,
+                      "bounds must be a CUDA tensor [num_pages, Hkv, page / block, 2, d]");
+    TORCH_CHECK_VALUE(tab.dim() == 2, "block_table must have 2 dimensions");
+    const c10::Device dev = bounds.device();
+    const void* bp = checked(o[1], "bounds", at::kBFloat16, bounds.sizes(), dev);
+    const auto table = static_cast<const int*>(checked(o[2], "block_table", at::kInt, tab.sizes(), dev));
+    const auto lens = static_cast<const int*>(checked(o[3], "seq_lens", at::kInt, {tab.size(0)}, dev));
+    const int num_pages = size(bounds.size(0), "num_pages"), Hkv = size(bounds.size(1), "Hkv"),
+              per_page = size(bounds.size(2), "page / block"), d = size(bounds.size(4), "d"), B = size(tab.size(0), "B"),
+              max_pages = size(tab.size(1), "max_pages");
+    const Queries q(o[0], dev, B, d);
+    const int block = integer(o[4]), keep = integer(o[5]), first = integer(o[6]), recent = integer(o[7]);
+    const c10::cuda::CUDAGuard guard(dev);
+    const int64_t most = (int64_t)max_pages * per_page;
+    const Tensor ws = workspace(o[8], fa_select_blocks_workspace_bytes(B, Hkv, most <= INT_MAX ? (int)most : 0), dev);
+    const Tensor out = make({B, Hkv, std::max(keep, 0)}, at::kInt, dev);
+    void* stream = stream_of(dev);
+    const int st = call([&] {
+        return fa_select_blocks(q.t.data_ptr(), bp, table, lens, (int*)out.data_ptr(), B, q.Hq, Hkv, q.Nq, block, per_page,
+                                max_pages, num_pages, d, keep, first, recent, ws.data_ptr(), ws.nbytes(), stream);
+    });
+    return st != FA_OK ? status(st) : THPVariable_Wrap(out);
+    END_HANDLE_TH_ERRORS
+}
+
+// decode_blocks(q, k_pages, v_pages, block_table, seq_lens, blocks, block, scale, workspace)
+PyObject* decode_blocks(PyObject*, PyObject* const* o, Py_ssize_t n) {
+    if (!count(n, 9)) return nullptr;
+    HANDLE_TH_ERRORS
+    const Pages c(o[1], o[2], o[3], o[4]);
+    const Queries q(o[0], c.dev, c.B, c.d);
+    const Tensor& list = tensor(o[5], "blocks");
+    TORCH_CHECK_VALUE(list.dim() == 3, "blocks must have shape [B, Hkv, keep]");
+    const auto blocks = static_cast<const int*>(checked(o[5], "blocks", at::kInt, {c.B, c.Hkv, list.size(2)}, c.dev));
+    const int keep = size(list.size(2), "keep"), block = integer(o[6]);
+    const float scale = o[7] == Py_None ? (float)(1.0 / std::sqrt((double)c.d)) : number(o[7]);
+    const c10::cuda::CUDAGuard guard(c.dev);
+    const Tensor ws = workspace(o[8], fa_decode_blocks_workspace_bytes(c.B, q.Hq, c.Hkv, q.Nq, c.d), c.dev);
+    const Tensor out = make(q.t.sizes(), at::kBFloat16, c.dev);
+    const Tensor lse = make(q.t.sizes().slice(0, q.t.dim() - 1), at::kFloat, c.dev);
+    void* stream = stream_of(c.dev);
+    const int st = call([&] {
+        return fa_decode_blocks(q.t.data_ptr(), c.k, c.v, (const int*)c.table, (const int*)c.lens, blocks, out.data_ptr(),
+                                (float*)lse.data_ptr(), c.B, q.Hq, c.Hkv, q.Nq, c.page, block, keep, c.max_pages,
+                                c.num_pages, c.d, scale, ws.data_ptr(), ws.nbytes(), stream);
+    });
+    if (st != FA_OK) return status(st);
+    return Py_BuildValue("(NN)", THPVariable_Wrap(out), THPVariable_Wrap(lse));
+    END_HANDLE_TH_ERRORS
+}
+
+// decode_shared(q, k_pages, v_pages, block_table, seq_lens, shared_len, scale, workspace)
+PyObject* decode_shared(PyObject*, PyObject* const* o, Py_ssize_t n) {
+    if (!count(n, 8)) return nullptr;
+    HANDLE_TH_ERRORS
+    const Pages c(o[1], o[2], o[3], o[4]);
+    const Queries q(o[0], c.dev, c.B, c.d);
+    const auto shared = static_cast<const int*>(checked(o[5], "shared_len", at::kInt, {1}, c.dev));
+    const float scale = o[6] == Py_None ? (float)(1.0 / std::sqrt((double)c.d)) : number(o[6]);
+    const c10::cuda::CUDAGuard guard(c.dev);
+    const Tensor ws = workspace(o[7], fa_decode_shared_workspace_bytes(c.B, q.Hq, c.Hkv, q.Nq, c.d), c.dev);
+    const Tensor out = make(q.t.sizes(), at::kBFloat16, c.dev);
+    const Tensor lse = make(q.t.sizes().slice(0, q.t.dim() - 1), at::kFloat, c.dev);
+    void* stream = stream_of(c.dev);
+    const int st = call([&] {
+        return fa_decode_shared(q.t.data_ptr(), c.k, c.v, (const int*)c.table, (const int*)c.lens, shared, out.data_ptr(),
+                                (float*)lse.data_ptr(), c.B, q.Hq, c.Hkv, q.Nq, c.page, c.max_pages, c.num_pages, c.d,
+                                scale, ws.data_ptr(), ws.nbytes(), stream);
+    });
+    if (st != FA_OK) return status(st);
+    return Py_BuildValue("(NN)", THPVariable_Wrap(out), THPVariable_Wrap(lse));
+    END_HANDLE_TH_ERRORS
+}
+
 #define FA_FN(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {FA_FN(rope), FA_FN(append), FA_FN(decode), FA_FN(evict), {nullptr, nullptr, 0, nullptr}};
+PyMethodDef methods[] = {FA_FN(rope), FA_FN(append), FA_FN(decode), FA_FN(evict), FA_FN(paged_append),
+                         FA_FN(select_blocks), FA_FN(decode_blocks), FA_FN(decode_shared), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fa_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -431,6 +431,113 @@ int fa_cache_evict_fp8(void *k_pages, void *v_pages, float *k_scale, float *v_sc
                        float *new_weights, int *kept, int B, int Hkv, int page_size, int scale_block,
                        int max_pages, int new_max_pages, int num_pages, int d, int keep, int recent, void *stream);
 
+/* ---- Long contexts out of the paged bf16 cache -------------------------------
+ * The cache of fa_decode_paged (k_pages, v_pages bf16 [num_pages, Hkv, page_size,
+ * d], block_table int32 [B, max_pages], seq_lens int32 [B]), its writer and two
+ * ways to read less of it: fa_cache_append writes new tokens, the keys rotated on
+ * the way; fa_select_blocks and fa_decode_blocks attend to the blocks that a
+ * score from bounds of their keys selects; fa_decode_shared reads a prefix that
+ * all sequences have in common once for the whole batch.  (The cache is
+ * streamed, not shrunk: zimaspace.com "Wie reduziert Flash Attention ...",
+ * section "Weniger IO bedeutet nicht, dass der KV-Cache entfaellt"; pages: johe.ru
+ * "Flash Attention: ...", section "Альтернативы", PagedAttention.)
+ *
+ * Any page size >= 1 (fa_decode_shared: a multiple of 8).  A block is `block`
+ * consecutive tokens of a page and kv head; block divides page_size and is at
+ * most 128.  Tables, lengths, positions, lists of blocks and lse need 4-byte
+ * alignment only.  0 <= seq_lens[b] <= max_pages * page_size <= 2^30.  A length
+ * out of range is clamped, a page index outside [0, num_pages) is never
+ * dereferenced (reads give zeros, writes are left out); either is recorded as
+ * FA_ERR_INVALID_ARG in the device error word.  num_pages * Hkv * page_size must
+ * stay below 2^32 - 1 (FA_ERR_UNSUPPORTED). */
+
+/* Writes new tokens into the cache.  k, v, strides, seq_lens, new_lens, turns,
+ * rot, interleaved, magnitude and positions as for fa_cache_append_fp8: sequence b
+ * gets its first n_b tokens at seq_lens[b], seq_lens[b] + 1, ..., the keys rotated
+ * as by fa_rope if turns is not NULL, and rounded to bf16 once.  bounds: bf16
+ * [num_pages, Hkv, page_size / block, 2, d] or NULL: the smallest and the largest
+ * element of each key column over the block's tokens, as they are stored (NaN
+ * where one of them is NaN).  Those of a block that tokens of the sequence before
+ * seq_lens[b] are in are widened, those of a block that starts with new tokens
+ * are replaced.  With bounds NULL, block is ignored.  Slots behind the new
+ * tokens keep their contents.  No page may be written for two sequences at once. */
+int fa_cache_append(const void *k, const void *v, long long k_sb, long long k_sh, long long k_sn, long long v_sb,
+                    long long v_sh, long long v_sn, void *k_pages, void *v_pages, void *bounds, const int *block_table,
+                    const int *seq_lens, const int *new_lens, const int *positions, const uint64_t *turns, int B,
+                    int Hkv, int N, int d, int rot, int interleaved, float magnitude, int page_size, int block,
+                    int max_pages, int num_pages, void *stream);
+
+/* Bytes of workspace fa_select_blocks needs; max_blocks = max_pages * page_blocks.
+ * 12 bytes per kv head and block of the table, whatever the lengths are.  Returns
+ * 0 for invalid sizes.  Host only, no device call. */
+size_t fa_select_blocks_workspace_bytes(int B, int Hkv, int max_blocks);
+
+/* The blocks that the last Nq (1..16) tokens of each sequence are to attend to.
+ * q bf16 [B, Hq, Nq, d]; bounds bf16 [num_pages, Hkv, page_blocks, 2, d] as
+ * fa_cache_append keeps them, page_blocks = page_size / block.  No key of a block
+ * gives a row r of q more than u_r = sum_c max(q_rc, 0) max_c + min(q_rc, 0) min_c
+ * (before the scale); the block's score is the largest u_r of the kv head's Hq /
+ * Hkv x Nq rows.  blocks int32 [B, Hkv, keep] out: of the n_b = ceil(seq_lens[b] /
+ * block) blocks of sequence b the first `first` ones, the last `recent` ones
+ * (first + recent <= keep) and, of the others, the keep - first - recent of
+ * largest score, in ascending order; all of them and -1 behind them if n_b <= keep.
+ * The choice is that of exact scores: of equal ones (+0 = -0) the lowest index
+ * stays; NaN (also an infinite bound times zero) counts as largest.  recent should
+ * cover the Nq tokens.  workspace: 16-byte aligned, at least
+ * fa_select_blocks_workspace_bytes(...); contents do not matter; calls that may
+ * overlap need one each. */
+int fa_select_blocks(const void *q, const void *bounds, const int *block_table, const int *seq_lens, int *blocks, int B,
+                     int Hq, int Hkv, int Nq, int block, int page_blocks, int max_pages, int num_pages, int d, int keep,
+                     int first, int recent, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace fa_decode_blocks needs.  Returns 0 for invalid sizes.  Host
+ * only, no device call. */
+size_t fa_decode_blocks_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d);
+
+/* Attention of the last Nq (1..16) tokens of each sequence over listed blocks of
+ * the cache, which holds them already.  q, o bf16 [B, Hq, Nq, d]; lse fp32 [B, Hq,
+ * Nq] or NULL; blocks int32 [B, Hkv, keep]: distinct blocks of the sequence, in any
+ * order (a block listed twice counts twice).  Of a list the first min(keep, n_b)
+ * entries are looked at, n_b = ceil(seq_lens[b] / block); negative ones are
+ * skipped, ones >= n_b too, and recorded as FA_ERR_INVALID_ARG.  Query head h reads
+ * kv head h / (Hq / Hkv); query t sees the tokens j <= seq_lens[b] - Nq + t of the
+ * listed blocks.  A query that sees none gets O = 0, LSE = -inf.  Scores and sums
+ * are fp32; for the value product a softmax weight is rounded to 16 bits (2^-17).
+ * The keys of all sequences are dealt out evenly to the CTAs that run at once.
+ * Results do not depend on the run (fixed order of additions), but for rounding on
+ * the batch that a sequence is in.  Tokens past seq_lens[b] are never used, and one
+ * that a query does not see does not reach it, whatever it holds.  Steps of 64 keys
+ * over all sequences at full capacity, kv heads and tiles of 32 query rows must
+ * stay below 2^31 (FA_ERR_UNSUPPORTED).  No output may overlap an input (o = q:
+ * FA_ERR_INVALID_ARG).  workspace as for fa_select_blocks. */
+int fa_decode_blocks(const void *q, const void *k_pages, const void *v_pages, const int *block_table,
+                     const int *seq_lens, const int *blocks, void *o, float *lse, int B, int Hq, int Hkv, int Nq,
+                     int page_size, int block, int keep, int max_pages, int num_pages, int d, float scale,
+                     void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace fa_decode_shared needs.  Returns 0 for invalid sizes.  Host
+ * only, no device call. */
+size_t fa_decode_shared_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d);
+
+/* Attention of the last Nq (1..16) tokens of each sequence over the whole cache,
+ * where the first shared_len[0] tokens are the same for all sequences (a system
+ * prompt, a document with many questions, samples of one prompt).  q, o, lse and the
+ * mask as for fa_decode_blocks with every block listed.  shared_len: device int32
+ * [1], 0 <= shared_len[0] <= max_pages * page_size, any number of tokens.
+ * seq_lens[b] counts the shared tokens too.  A sequence with seq_lens[b] - Nq >=
+ * shared_len[0] takes part: its first shared_len[0] tokens are read through the
+ * table's row of the first sequence that takes part (its own entries for whole
+ * shared pages are not looked at), the others through its own row.  Others (a slot
+ * without a sequence, or a shorter one) read all their tokens through their own
+ * row.  For the product of a shared token's weight and value the weight is rounded
+ * to bf16 (2^-9), for own tokens to 16 bits.  Errors, workspace (its size:
+ * fa_decode_shared_workspace_bytes) and the rest as for fa_decode_blocks; page_size
+ * must be a multiple of 8 (FA_ERR_UNSUPPORTED). */
+int fa_decode_shared(const void *q, const void *k_pages, const void *v_pages, const int *block_table,
+                     const int *seq_lens, const int *shared_len, void *o, float *lse, int B, int Hq, int Hkv, int Nq,
+                     int page_size, int max_pages, int num_pages, int d, float scale, void *workspace,
+                     size_t workspace_bytes, void *stream);
+
 /* Size of the scratch array that fa_decode_noalloc uses instead of a workspace. */
 #define FA_DECODE_NOALLOC_SCRATCH_BYTES ((size_t)16 << 20)
 

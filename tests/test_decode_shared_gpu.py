@@ -1,0 +1,144 @@
+"""fa_decode_shared against float64."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import paged as op
+from tests.paged_common import DEV, bf16, check_rows, f64, ints, ok, random_pages, table_of, to_gpu
+
+pytestmark = pytest.mark.gpu
+ONE, PAIR = 2.0 ** -8, 2.0 ** -16
+
+
+def _case(seed, lens, shared, Hkv, page, d):
+    """Pages and a table whose rows begin with the same pages; the page that the prefix ends in is each one's own copy."""
+    B, full = len(lens), shared // page
+    own = max(1, -(-max(max(lens), shared) // page) - full)
+    c = random_pages(seed, full + B * own + 2, Hkv, page, d)
+    p = np.random.default_rng(seed).permutation(full + B * own + 2).astype(np.int32)
+    table = np.concatenate([np.tile(p[:full], (B, 1)), p[full:full + B * own].reshape(B, own)], 1)
+    if shared % page:
+        for n in c:
+            c[n][table[:, full], :, :shared % page] = c[n][table[0, full], :, :shared % page]
+    return c, np.ascontiguousarray(table)
+
+
+# (own tokens, shared, Hkv, G, Nq, d, page); None: an empty slot
+CASES = [
+    ([1], 1, 1, 1, 1, 64, 8),
+    ([1, 2], 128, 1, 1, 1, 128, 16),
+    ([5, None, 17, 100], 129, 2, 4, 1, 128, 16),
+    ([1] * 32, 777, 2, 4, 1, 128, 16),                  # 128 rows
+    ([3] * 33, 1000, 1, 4, 1, 64, 48),                  # 132 rows
+    ([1, 300, None, 64] * 9, 1024, 2, 8, 1, 128, 64),   # 288 rows: a second tile of 32
+    ([9, 40, None, 8] * 4, 2000, 1, 5, 5, 64, 40),      # 400 rows, pages of 40
+    ([16, 20], 300, 3, 1, 16, 128, 8),
+    ([4, 1], 5000, 1, 16, 1, 128, 256),
+    ([10] * 140, 130, 1, 8, 1, 64, 32),                 # 1120 rows
+    ([2, 1, 700], 64, 4, 2, 1, 128, 128),
+    ([600, 5], 0, 2, 4, 1, 128, 16),                    # nothing shared
+]
+
+
+@pytest.mark.parametrize("own,shared,Hkv,G,Nq,d,page", CASES)
+def test_decode_shared(cuda_lib, own, shared, Hkv, G, Nq, d, page):
+    """What lies behind a sequence's last token may hold anything, and the entries of whole shared pages are looked at in
+    one row only."""
+    lens = [0 if n is None else shared + n for n in own]
+    B, scale = len(lens), 1.0 / math.sqrt(d)
+    rng = np.random.default_rng(sum(lens) + d)
+    c, table = _case(d + page, lens, shared, Hkv, page, d)
+    q = bf16(rng, (B, Hkv * G, Nq, d), 0.3)
+    ref = op.attend(f64(q), c, table, lens, scale)
+    used = {n: np.full_like(c[n], np.nan) for n in c}
+    for b, n in enumerate(lens):
+        j = np.arange(n)
+        for m in c:
+            used[m][table[b][j // page], :, j % page] = c[m][table[b][j // page], :, j % page]
+    seen = table.copy()
+    seen[1:, :shared // page] = -1
+    g = to_gpu(used)
+    for t in (table, seen):
+        o, lse = cuda_lib.decode_shared(q.to(DEV), g["k"], g["v"], ints(t), ints(lens), ints([shared]))
+        ok(cuda_lib)
+        check_rows(o, lse, ref, ONE)
+    again = cuda_lib.decode_shared(q.to(DEV), g["k"], g["v"], ints(table), ints(lens), ints([shared]))
+    assert torch.equal(again[0], o) and torch.equal(again[1], lse)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_sequences_that_do_not_see_all_of_the_prefix(cuda_lib, d):
+    """Empty, shorter, and drafted queries of which the first does not see the prefix's end: they read their own rows, from
+    pages of their own; also where the first sequences of the batch are such ones, or all."""
+    rng = np.random.default_rng(d)
+    Hkv, G, Nq, page, shared = 2, 2, 4, 16, 100
+    for lens in ([0, 30, 103, 104, 150, 2], [3, 0, 99, 100, 101, 0], [0] * 6):
+        c = random_pages(d, 80, Hkv, page, d)
+        table = table_of(9, 6, 10, 80)
+        share = [b for b in range(6) if lens[b] - Nq >= shared]
+        for b in share[1:]:                              # of those that take part, the first one's pages
+            table[b, :shared // page] = table[share[0], :shared // page]
+            for n in c:
+                c[n][table[b, 6], :, :4] = c[n][table[share[0], 6], :, :4]
+        q, g = bf16(rng, (6, Hkv * G, Nq, d), 0.3), to_gpu(c)
+        o, lse = cuda_lib.decode_shared(q.to(DEV), g["k"], g["v"], ints(table), ints(lens), ints([shared]))
+        ok(cuda_lib)
+        check_rows(o, lse, op.attend(f64(q), c, table, lens, 1 / math.sqrt(d)), ONE)
+
+
+def test_nothing_shared_is_paged_decode(cuda_lib):
+    rng = np.random.default_rng(3)
+    lens, Hkv, G, d, page = [300, 1, 77], 2, 4, 128, 16
+    c, table = _case(4, lens, 0, Hkv, page, d)
+    q, g = bf16(rng, (3, Hkv * G, d), 0.3), to_gpu(c)
+    o, lse = cuda_lib.decode_shared(q.to(DEV), g["k"], g["v"], ints(table), ints(lens), ints([0]))
+    ok(cuda_lib)
+    check_rows(o, lse, op.attend(f64(q)[:, :, None], c, table, lens, 1 / math.sqrt(d)), PAIR)
+    o2, lse2 = cuda_lib.decode_paged(q.to(DEV), g["k"], g["v"], ints(table), ints(lens))
+    check_rows(o2, lse2, op.attend(f64(q)[:, :, None], c, table, lens, 1 / math.sqrt(d)), ONE)
+
+
+def test_large_scores(cuda_lib):
+    """A dominant token at the start or end of the prefix, or among the own ones; scores around +-2000."""
+    rng = np.random.default_rng(11)
+    Hkv, G, d, page, shared, lens = 1, 4, 128, 64, 3000, [3100, 3001, 3050]
+    for hot in (0, 2999, 3000):
+        c, table = _case(5, lens, shared, Hkv, page, d)
+        q = bf16(rng, (3, G, 1, d), 0.3)
+        for n in c:
+            c[n] = f64(torch.from_numpy(c[n] * (0.05 if n == "k" else 1.0)).to(torch.bfloat16))
+        for b in range(3):
+            c["k"][table[b][hot // page], 0, hot % page] = f64(torch.from_numpy(f64(q)[0, 0, 0] * 1.1).to(torch.bfloat16))
+        for scale in (1 / math.sqrt(d), 15.0):
+            g = to_gpu(c)
+            o, lse = cuda_lib.decode_shared(q.to(DEV), g["k"], g["v"], ints(table), ints(lens), ints([shared]), scale=scale)
+            ok(cuda_lib)
+            check_rows(o, lse, op.attend(f64(q), c, table, lens, scale), ONE, "hot %d scale %g" % (hot, scale))
+
+
+def test_bad_pages_and_lengths(cuda_lib):
+    fa, Hkv, G, d, page, shared = cuda_lib, 1, 4, 64, 16, 64
+    rng = np.random.default_rng(6)
+    lens = [75, 70]
+    c, table = _case(6, lens, shared, Hkv, page, d)
+    q, g, pages = bf16(rng, (2, G, 1, d), 0.3), to_gpu(c), c["k"].shape[0]
+    for bad in (-1, pages, 2 ** 31 - 1):
+        for at in ((0, 1), (1, 4)):                      # a shared page, an own one
+            t = table.copy()
+            t[at] = bad
+            o, lse = fa.decode_shared(q.to(DEV), g["k"], g["v"], ints(t), ints(lens), ints([shared]))
+            assert fa.fa_get_last_device_error()[0] == fa.FA_ERR_INVALID_ARG
+            t[at] = pages
+            if at[0] == 0:
+                t[:, 1] = pages
+            grown = {n: np.concatenate([c[n], np.zeros_like(c[n][:1])]) for n in c}
+            check_rows(o, lse, op.attend(f64(q), grown, t, lens, 0.125), ONE)
+    for length in (-5, 1000):
+        o, lse = fa.decode_shared(q.to(DEV), g["k"], g["v"], ints(table), ints(lens), ints([length]))
+        assert fa.fa_get_last_device_error()[0] == fa.FA_ERR_INVALID_ARG
+        check_rows(o, lse, op.attend(f64(q), c, table, lens, 0.125), ONE)
+    o, lse = fa.decode_shared(q.to(DEV), g["k"], g["v"], ints(table), ints([-1, 70]), ints([shared]))
+    assert fa.fa_get_last_device_error()[0] == fa.FA_ERR_INVALID_ARG
+    check_rows(o, lse, op.attend(f64(q), c, table, [0, 70], 0.125), ONE)
