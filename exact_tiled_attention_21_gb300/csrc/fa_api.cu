@@ -809,16 +809,15 @@ Fp8Workspace fp8_workspace(int B, int Hq, int Hkv, int Nq, int d, long long max_
     return w;
 }
 
-// Workspace of the block selection: exact keys and scores of every block of the table, the largest bound of every CTA.
+// Workspace of the block selection: exact keys and scores of every block of the table.
 struct SelectWorkspace {
-    size_t scores, big, bytes;
+    size_t scores, bytes;
 };
 SelectWorkspace select_workspace(int B, int Hkv, long long max_blocks) {
     const size_t bh = (size_t)B * Hkv;
     SelectWorkspace w;
     w.scores = align256(bh * (size_t)max_blocks * 8);
-    w.big = w.scores + align256(bh * (size_t)max_blocks * 4);
-    w.bytes = w.big + align256(bh * kSelectCtas * 4);
+    w.bytes = w.scores + align256(bh * (size_t)max_blocks * 4);
     return w;
 }
 
@@ -1202,8 +1201,7 @@ int fa_select_blocks(const void* q, const void* bounds, const int* block_table, 
     a.lens = seq_lens;
     a.out = blocks;
     a.exact = base;
-    a.scores = reinterpret_cast<float*>(base + ws.scores);
-    a.big = reinterpret_cast<uint32_t*>(base + ws.big);
+    a.scores = reinterpret_cast<uint32_t*>(base + ws.scores);
     a.stride = (long long)max_pages * page_blocks;
     a.B = B;
     a.Hkv = Hkv;

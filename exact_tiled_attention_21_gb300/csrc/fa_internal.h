@@ -253,9 +253,8 @@ struct SelectLaunch {
     const int* table;     // int32 [B, max_pages]
     const int* lens;      // int32 [B]
     int* out;             // int32 [B, Hkv, keep]
-    float* scores;        // workspace: [B * Hkv, stride]
+    uint32_t* scores;     // workspace: [B * Hkv, stride]
     void* exact;          // 64-bit [B * Hkv, stride]
-    uint32_t* big;        // [B * Hkv, kSelectCtas]
     long long stride;
     int B, Hkv, rows, block, page_blocks, max_pages, num_pages, d, keep, first, recent;
     int num_sms;

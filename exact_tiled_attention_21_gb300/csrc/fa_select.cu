@@ -7,16 +7,25 @@
 // and a block's score is the largest u_j of the kv head's query rows.  The first
 // blocks, the most recent ones and, of the others, those of largest score stay.
 //
-// The choice is that of exact scores.  They are summed in fp32: the products of
-// bf16 numbers are exact, and at most 9 roundings of 2^-24 follow, each of at most
-// A = |q|_1 max |bound|, so a score is within E = 2^-19.9 A.  Blocks further than
-// 2 E from the smallest score that stays are decided; if the others do not all
-// stay, theirs are summed again in fp64 (whose products and, but for elements 2^30
-// apart, sums are exact), and equal ones go by index.
+// The scores are products on the tensor cores (mma.sync m16n8k16: 16 blocks, 8
+// rows, the bounds as they come from memory, q split into its two parts), four
+// chains of sums per block and row: with fp32 FMAs, of which a row needs 2 d per
+// block, and sums over lanes the instructions took ten times as long as the bytes.
+//
+// The choice is that of exact scores.  The products of bf16 numbers are exact; a
+// step adds 16 of them to a sum, off by at most 17 x 2^-24 of the largest term even
+// if each is cut to 24 bits, and a chain has 2 d / 64 steps: the score is within E
+// = 2^-17.9 A, with A the largest sum of |q_c| |bound_c| a row can have, bounded
+// by 8 columns at a time.  Blocks further than 2 E from the smallest score that
+// stays are decided; if the others do not all stay, theirs are summed again in fp64
+// (whose products and, but for elements 2^30 apart, sums are exact), and equal ones
+// go by index.
 //
 // 4 d bytes per block and 4 d flops per block and row: bound by HBM where contexts
 // are long, by latency otherwise.  One cluster of up to 8 CTAs per (sequence, kv
-// head) shares the scores, through the workspace; its first CTA chooses.
+// head) makes the scores, in the shared memory of its first CTA, which chooses: a
+// histogram over the scores' range finds the bin that the smallest one that stays
+// is in, and counting greater ones within that bin finds it.
 #include <algorithm>
 
 #include "fa_internal.h"
@@ -24,27 +33,37 @@
 namespace fa {
 namespace {
 
-constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32;
-constexpr int kRowTile = 32;   // query rows in shared memory at once
-constexpr int kBatch = 8;      // 16-byte loads in flight per lane
-constexpr float kError = 1e-6f;  // E / A: 2^-19.9
+constexpr int kSelThreads = 256, kSelWarps = kSelThreads / 32;
+constexpr int kRowTile = 64;      // query rows in shared memory at once
+constexpr int kBatch = 16;        // blocks of a warp's batch
+constexpr int kBins = 1024, kList = 256;
+constexpr int kMostKeys = 16384;  // scores in shared memory; more go through the workspace
+constexpr float kError = 4e-6f;   // E / A: 2^-17.9
 
-__device__ __forceinline__ void cluster_barrier() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// Largest magnitudes of the two halves of bf16 pairs, as bits: infinities and NaN on top.
+__device__ __forceinline__ uint32_t abs_max2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b & 0x7FFF7FFFu));
+    return r;
 }
 
-// Sums over W lanes of NV values per lane: lane l (of W) gets those of values l NV / W + k in v[k], k < NV / W.
-template <int W, int NV>
-__device__ __forceinline__ void lane_sums(float (&v)[NV], int lane) {
-#pragma unroll
-    for (int m = W / 2, n = NV / 2; m >= 1; m >>= 1, n >>= 1) {
-        const bool hi = lane & m;
-#pragma unroll
-        for (int i = 0; i < n; ++i) {
-            const float send = hi ? v[i] : v[i + n], keep = hi ? v[i + n] : v[i];
-            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, m);
-        }
-    }
+// The negative (or positive) elements of a pair of bf16, zeros in the others' places; NaN stays.
+__device__ __forceinline__ uint32_t part2(uint32_t w, bool negative) {
+    auto keep = [&](uint32_t h) { return ((h >> 15) != 0) == negative || (h & 0x7FFFu) > 0x7F80u; };
+    return (keep(w & 0xFFFFu) ? w & 0xFFFFu : 0u) | (keep(w >> 16) ? w & 0xFFFF0000u : 0u);
+}
+__device__ __forceinline__ float abs_sum2(uint32_t w) {
+    return fabsf(__uint_as_float(w << 16)) + fabsf(__uint_as_float(w & 0xFFFF0000u));
+}
+
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 // Integers whose order is the numbers', -0 = +0; of a double also NaN, above everything.
@@ -52,35 +71,33 @@ __device__ __forceinline__ uint32_t key32(float x) {
     const uint32_t u = __float_as_uint(x + 0.f);
     return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
+__device__ __forceinline__ float score_of(uint32_t key) {
+    return __uint_as_float((key & 0x80000000u) ? key ^ 0x80000000u : ~key);
+}
 __device__ __forceinline__ uint64_t key64(double x) {
     if (x != x) return ~0ull;
     const uint64_t u = (uint64_t)__double_as_longlong(x + 0.0);
     return (u >> 63) ? ~u : u | (1ull << 63);
 }
 
-// Sum over the CTA, the same in every thread.  Buffers alternate by `turn`, so one barrier per call is enough.
-__device__ __forceinline__ int block_sum(int v, int (&s)[2][kSelWarps], int& turn) {
-    v = __reduce_add_sync(0xffffffffu, v);
-    turn ^= 1;
-    if ((threadIdx.x & 31) == 0) s[turn][threadIdx.x >> 5] = v;
-    __syncthreads();
-    return __reduce_add_sync(0xffffffffu, (threadIdx.x & 31) < kSelWarps ? s[turn][threadIdx.x & 31] : 0);
-}
-
 struct SelectPlan {
-    int ctas;            // of a cluster
-    FastDiv per_page;    // blocks of a page
+    int ctas;          // of a cluster
+    FastDiv per_page;  // blocks of a page
 };
 
-// PER: scores that a thread of the choosing CTA holds in registers (0: any number, read again in each pass).
-template <int D, int PER>
-__global__ void __launch_bounds__(kSelThreads, 1) select_blocks_kernel(const SelectLaunch a, const SelectPlan plan) {
-    constexpr int LANES = D / 4, APART = 32 / LANES;  // lanes of a block's bounds; blocks of a warp's load
-    constexpr int GROUP = kBatch * APART;             // blocks of a warp's batch
-    __shared__ float4 s_q[kRowTile][2][LANES];        // min(q, 0) and max(q, 0): first, then second four of a lane's columns
-    __shared__ int s_count[2][kSelWarps];
-    __shared__ uint32_t s_big[kSelWarps];
-    __shared__ float s_norm[kSelWarps];
+// GLOBAL: the scores go through the workspace (too many of them, or several tiles of query rows).
+template <int D, bool GLOBAL>
+__global__ void __launch_bounds__(kSelThreads, 2) select_blocks_kernel(const SelectLaunch a, const SelectPlan plan) {
+    constexpr int S = D / 16, CHUNKS = 4 * S;  // 64-byte pieces of a block's bounds, a lane's part of which is a chunk
+    extern __shared__ __align__(16) uint32_t s_keys[];
+    __shared__ uint4 s_q[kRowTile / 8][S][32];  // by tile of 8 rows and piece: the lanes' B fragments of two products
+    __shared__ uint32_t s_sum8[CHUNKS], s_big[CHUNKS], s_all[kSelectCtas][CHUNKS];  // bits of the largest sum of |q| and |bound|
+    __shared__ int s_hist[kBins];
+    __shared__ uint64_t s_exact[kList];
+    __shared__ uint32_t s_list[kList];
+    __shared__ int2 s_sum[2][kSelWarps];
+    __shared__ int s_found[2], s_many;
+    __shared__ uint32_t s_key;
     pdl_launch_dependents();
     pdl_wait();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -99,8 +116,15 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_blocks_kernel(const Sel
             for (int i = tid; i < a.keep; i += kSelThreads) out[i] = i < n ? i : -1;
         return;
     }
-    const int j0 = a.first, j1 = n - a.recent, want = a.keep - a.first - a.recent;  // choose `want` of [j0, j1)
-    float* scores = a.scores + (long long)bh * a.stride;
+    const int j0 = a.first, mid = n - a.recent - j0, want = a.keep - a.first - a.recent;  // `want` of the `mid` from j0 on
+    if (rank == 0) {
+        for (int i = tid; i < a.first; i += kSelThreads) out[i] = i;
+        for (int i = tid; i < a.recent; i += kSelThreads) out[a.first + want + i] = j0 + mid + i;
+    }
+    if (want == 0) return;
+    if (plan.ctas > 1) cluster_arrive();  // waited for below: the first CTA runs before the others write to it
+    uint32_t* keys = GLOBAL ? a.scores + (long long)bh * a.stride : s_keys;  // of block j0 + i
+    const uint32_t keys0 = mapa_shared(smem_u32(s_keys), 0);                 // those of the first CTA
     const __nv_bfloat16* q = (const __nv_bfloat16*)a.q + (long long)bh * a.rows * D;
     const __nv_bfloat16* bounds = (const __nv_bfloat16*)a.bounds;
     // the row of `bounds` (2 D elements) of block j, ~0u without a page
@@ -112,229 +136,345 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_blocks_kernel(const Sel
         }
         return ((uint32_t)pg * a.Hkv + kvh) * bpp + (uint32_t)(j - lpage * bpp);
     };
-    float norm = 0.f;   // largest |q|_1 of this warp's rows
-    uint32_t big = 0;   // bits of the largest |bound|; infinities and NaN on top
-    const int share = (j1 - j0 + plan.ctas - 1) / plan.ctas;
-    const int s0 = j0 + rank * share, s1 = min(s0 + share, j1);
-    for (int r0 = 0; want > 0 && r0 < a.rows; r0 += kRowTile) {
-        const int many = min(kRowTile, a.rows - r0), padded = (many + 3) & ~3;
-        if (r0 > 0) __syncthreads();
-        for (int r = warp; r < padded; r += kSelWarps) {
-            float sum = 0.f;
-            for (int c = lane; c < D / 4; c += 32) {  // four columns
-                const uint2 w = r < many ? reinterpret_cast<const uint2*>(q + (long long)(r0 + r) * D)[c] : make_uint2(0, 0);
-                const float4 x = make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u),
-                                             __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xFFFF0000u));
-                // NaN stays in both parts
-                auto neg = [](float v) { return v > 0.f ? 0.f : v; };
-                auto pos = [](float v) { return v < 0.f ? 0.f : v; };
-                s_q[r][c & 1][c >> 1] = make_float4(neg(x.x), neg(x.y), neg(x.z), neg(x.w));
-                s_q[r][c & 1][LANES / 2 + (c >> 1)] = make_float4(pos(x.x), pos(x.y), pos(x.z), pos(x.w));
-                sum += (fabsf(x.x) + fabsf(x.y)) + (fabsf(x.z) + fabsf(x.w));
-            }
-            for (int w = 16; w >= 1; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
-            if (!(sum <= norm)) norm = sum;  // NaN stays
+    const int share = ((mid + plan.ctas - 1) / plan.ctas + kBatch - 1) & ~(kBatch - 1), i0 = rank * share, i1 = min(i0 + share, mid);
+    const int g8 = lane >> 2, t4 = lane & 3;
+    auto rows_of = [&](int g) { return lane < kBatch && g + lane < i1 ? row_of(j0 + g + lane) : ~0u; };
+    // the B fragments of query rows [r0, r0 + many): a lane's chunk is 8 columns of a row's negative part (times the
+    // smallest keys), then of its positive part
+    auto stage = [&](int r0, int many) {
+        for (int i = tid; i < (many + 7) / 8 * S * 32; i += kSelThreads) {
+            const int l = i % 32, s = i / 32 % S, r = i / 32 / S * 8 + l / 4, chunk = s * 4 + l % 4;
+            uint4 w = make_uint4(0, 0, 0, 0);
+            if (r < many) w = *reinterpret_cast<const uint4*>(q + (long long)(r0 + r) * D + chunk * 8 % D);
+            const bool neg = chunk * 8 < D;
+            w = make_uint4(part2(w.x, neg), part2(w.y, neg), part2(w.z, neg), part2(w.w, neg));
+            s_q[r / 8][s][l] = w;
+            // rounded up: a sum of eight is off by 2^-21 at most
+            const float sum = (abs_sum2(w.x) + abs_sum2(w.y) + abs_sum2(w.z) + abs_sum2(w.w)) * 1.00001f;
+            atomicMax(&s_sum8[chunk], __float_as_uint(sum) & 0x7FFFFFFFu);
         }
+    };
+    if (tid < CHUNKS) s_sum8[tid] = s_big[tid] = 0;
+    for (int i = tid; i < kBins; i += kSelThreads) s_hist[i] = 0;
+    if (tid == 0) s_many = 0;
+    uint32_t big[S];
+#pragma unroll
+    for (int s = 0; s < S; ++s) big[s] = 0;
+    for (int r0 = 0; r0 < a.rows; r0 += kRowTile) {
+        const int many = min(kRowTile, a.rows - r0);
+        uint32_t rows = rows_of(i0 + warp * kBatch);  // of the next batch
         __syncthreads();
-        for (int g0 = s0 + warp * GROUP; g0 < s1; g0 += kSelWarps * GROUP) {
-            const uint32_t mine = lane < GROUP && g0 + lane < s1 ? row_of(g0 + lane) : ~0u;
-            uint4 w[kBatch];
+        stage(r0, many);
+        __syncthreads();
+        if (r0 == 0 && plan.ctas > 1) cluster_wait();
+        for (int g = i0 + warp * kBatch; g < i1; g += kSelWarps * kBatch) {
+            uint4 w[2][S];  // of blocks g8 and g8 + 8 of the batch
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                const uint32_t row = __shfl_sync(0xffffffffu, mine, i * APART + lane / LANES);
-                w[i] = row != ~0u ? *reinterpret_cast<const uint4*>(bounds + (size_t)row * (2 * D) + lane % LANES * 8)
-                                  : make_uint4(0, 0, 0, 0);
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t row = __shfl_sync(0xffffffffu, rows, g8 + 8 * h);
+                const uint4* src = reinterpret_cast<const uint4*>(bounds + (size_t)(row != ~0u ? row : 0) * (2 * D)) + t4;
+#pragma unroll
+                for (int s = 0; s < S; ++s) w[h][s] = row != ~0u ? src[s * 4] : make_uint4(0, 0, 0, 0);
             }
-            float2 x[kBatch][4];
+            rows = rows_of(g + kSelWarps * kBatch);
+            float best[2] = {-INFINITY, -INFINITY};
+            for (int n = 0; n * 8 < many; ++n) {
+                float c[4][4] = {};
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+                for (int s = 0; s < S; ++s) {
+                    const uint4 x = s_q[n][s][lane];
+                    mma_bf16(c[2 * s % 4], w[0][s].x, w[1][s].x, w[0][s].y, w[1][s].y, x.x, x.y);
+                    mma_bf16(c[(2 * s + 1) % 4], w[0][s].z, w[1][s].z, w[0][s].w, w[1][s].w, x.z, x.w);
+                }
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    x[i][c] = make_float2(__uint_as_float(u[c] << 16), __uint_as_float(u[c] & 0xFFFF0000u));
-                    big = max(big, max(u[c] << 16 & 0x7FFFFFFFu, u[c] & 0x7FFF0000u));
+                for (int k = 0; k < 4; ++k)  // rows 2 t4 + k % 2 of block g8 + 8 (k / 2)
+                    if (n * 8 + 2 * t4 + k % 2 < many) best[k / 2] = fmaxf(best[k / 2], (c[0][k] + c[1][k]) + (c[2][k] + c[3][k]));
+            }
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                big[s] = abs_max2(abs_max2(big[s], w[0][s].x), w[0][s].y);
+                big[s] = abs_max2(abs_max2(big[s], w[0][s].z), w[0][s].w);
+                big[s] = abs_max2(abs_max2(big[s], w[1][s].x), w[1][s].y);
+                big[s] = abs_max2(abs_max2(big[s], w[1][s].z), w[1][s].w);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                best[h] = fmaxf(best[h], __shfl_xor_sync(0xffffffffu, best[h], 1));
+                best[h] = fmaxf(best[h], __shfl_xor_sync(0xffffffffu, best[h], 2));
+                const int i = g + g8 + 8 * h;
+                if (t4 == 0 && i < i1) {
+                    const uint32_t key = key32(best[h]);
+                    if (GLOBAL)
+                        keys[i] = r0 > 0 ? max(keys[i], key) : key;
+                    else
+                        st_cluster_u32(keys0 + 4 * i, key);
                 }
             }
-            float best[APART];  // lane l (of LANES): block l APART / 4 ... of the batch (see lane_sums)
-#pragma unroll
-            for (int k = 0; k < APART; ++k) best[k] = -INFINITY;
-            for (int r = 0; r < padded; r += 4) {
-                float v[kBatch * 4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float4 qa = s_q[r + k][0][lane % LANES], qb = s_q[r + k][1][lane % LANES];
-#pragma unroll
-                    for (int i = 0; i < kBatch; ++i) {
-                        float2 s = ffma2(x[i][0], make_float2(qa.x, qa.y), make_float2(0.f, 0.f));
-                        s = ffma2(x[i][1], make_float2(qa.z, qa.w), s);
-                        s = ffma2(x[i][2], make_float2(qb.x, qb.y), s);
-                        s = ffma2(x[i][3], make_float2(qb.z, qb.w), s);
-                        v[i * 4 + k] = s.x + s.y;
-                    }
-                }
-                lane_sums<LANES>(v, lane);  // value l APART + k is load (l APART + k) / 4, row (l APART + k) % 4
-#pragma unroll
-                for (int k = 0; k < APART; ++k)
-                    if (r + (lane * APART + k) % 4 < many) best[k] = fmaxf(best[k], v[k]);
-            }
-            float top = best[0];
-#pragma unroll
-            for (int k = 1; k < APART; ++k) top = fmaxf(top, best[k]);
-#pragma unroll
-            for (int m = 1; m < 4 / APART; m <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
-            const int j = g0 + lane % LANES * APART / 4 * APART + lane / LANES;
-            if (lane % (4 / APART) == 0 && j < s1) scores[j] = r0 > 0 ? fmaxf(scores[j], top) : top;
         }
     }
     // ---- what the cluster found goes to its first CTA
-    big = __reduce_max_sync(0xffffffffu, big);
-    if (lane == 0) s_big[warp] = big, s_norm[warp] = norm;
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+#pragma unroll
+        for (int m = 4; m < 32; m <<= 1) big[s] = abs_max2(big[s], __shfl_xor_sync(0xffffffffu, big[s], m));
+        if (g8 == 0) atomicMax(&s_big[s * 4 + t4], max(big[s] << 16, big[s] & 0xFFFF0000u));
+    }
     __syncthreads();
-    big = __reduce_max_sync(0xffffffffu, lane < kSelWarps ? s_big[lane] : 0);
-    if (tid == 0) a.big[bh * kSelectCtas + rank] = big;
-    if (plan.ctas > 1)
-        cluster_barrier();
-    else
+    if (tid < CHUNKS) st_cluster_u32(mapa_shared(smem_u32(&s_all[rank][tid]), 0), s_big[tid]);
+    if (plan.ctas > 1) {
+        cluster_arrive();
+        cluster_wait();
+    } else {
         __syncthreads();
+    }
     if (rank > 0) return;
-    // ---- the first CTA: thread t holds V consecutive scores
-    const int V = (j1 - j0 + kSelThreads - 1) / kSelThreads, jt = j0 + tid * V, jn = min(V, max(0, j1 - jt));
-    uint32_t key[PER ? PER : 1];
+    // ---- the first CTA chooses.  A warp has a run of the scores, the lanes in turn.
+    const int run = ((mid + kSelWarps - 1) / kSelWarps + 31) & ~31, wi = warp * run, we = min(wi + run, mid);
+    auto each = [&](auto f) {  // f(i, key)
+        int i = wi + lane;
+        for (; i + 96 < we; i += 128) {
+            const uint32_t k[4] = {keys[i], keys[i + 32], keys[i + 64], keys[i + 96]};
 #pragma unroll
-    for (int i = 0; i < PER; ++i) key[i] = i < jn && want > 0 ? key32(scores[jt + i]) : 0;
-    auto each = [&](auto f) {  // f(block, key of its score)
-        if constexpr (PER > 0) {
-#pragma unroll
-            for (int i = 0; i < PER; ++i)
-                if (i < jn) f(jt + i, key[i]);
-        } else {
-            for (int i = 0; i < jn; ++i) f(jt + i, key32(scores[jt + i]));
+            for (int u = 0; u < 4; ++u) f(i + 32 * u, k[u]);
         }
+        for (; i < we; i += 32) f(i, keys[i]);
     };
     int turn = 0;
-    // a block stays if its key is above `over`, or from `from` on and picked by the exact scores
+    // sums over the CTA, the same in every thread; buffers alternate, so one barrier per call is enough
+    auto block_sums = [&](int x, int y) {
+        x = __reduce_add_sync(0xffffffffu, x);
+        y = __reduce_add_sync(0xffffffffu, y);
+        turn ^= 1;
+        if (lane == 0) s_sum[turn][warp] = make_int2(x, y);
+        __syncthreads();
+        const int2 v = lane < kSelWarps ? s_sum[turn][lane] : make_int2(0, 0);
+        return make_int2(__reduce_add_sync(0xffffffffu, v.x), __reduce_add_sync(0xffffffffu, v.y));
+    };
+    uint32_t lo = 0xFFFFFFFFu, hi = 0;
+    each([&](int, uint32_t k) { lo = min(lo, k), hi = max(hi, k); });
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    if (lane == 0) s_sum[0][warp] = make_int2((int)lo, (int)hi);
+    float A = 0.f;  // the largest sum of |q_c| |bound_c| that a row can have; NaN and infinities stay
+    for (int c = lane; c < CHUNKS; c += 32) {
+        uint32_t m = s_all[0][c];
+        for (int r = 1; r < plan.ctas; ++r) m = max(m, s_all[r][c]);
+        A += __uint_as_float(s_sum8[c]) * __uint_as_float(m);
+    }
+    for (int w = 16; w >= 1; w >>= 1) A += __shfl_xor_sync(0xffffffffu, A, w);
+    __syncthreads();
+    for (int w = 0; w < kSelWarps; ++w) {
+        lo = min(lo, (uint32_t)s_sum[0][w].x);
+        hi = max(hi, (uint32_t)s_sum[0][w].y);
+    }
+    const float E = kError * 1.001f * A + 1e-30f;  // A itself is rounded; products may underflow
+    // a score stays if its key is above `over`, or from `from` on and picked by the exact scores
     uint32_t from = 0, over = 0xFFFFFFFFu;
-    uint64_t exact_from = 0;  // of the undecided: exact keys above it stay, and the first `equal` that are equal to it
-    int equal = INT_MAX;
-    uint64_t* exact = reinterpret_cast<uint64_t*>(a.exact) + (long long)bh * a.stride;
-    if (want > 0) {
-        float A = s_norm[0];
-        for (int w = 1; w < kSelWarps; ++w)
-            if (!(s_norm[w] <= A)) A = s_norm[w];
-        uint32_t top = 0;
-        for (int r = 0; r < plan.ctas; ++r) top = max(top, a.big[bh * kSelectCtas + r]);
-        const float E = kError * 1.01f * (A * __uint_as_float(top)) + 1e-30f;  // A itself is rounded; products may underflow
-        bool open = true;  // some are undecided and not all of them stay
-        int left = want;   // of the undecided
-        if (E < 1e38f) {   // every score is finite
-            // the smallest key that stays, bit by bit
-            uint32_t T = 0;
-            for (int bit = 31; bit >= 0; --bit) {
-                const uint32_t cand = T | 1u << bit;
-                int c = 0;
-                each([&](int, uint32_t k) { c += k >= cand; });
-                c = block_sum(c, s_count, turn);
-                if (c >= want) T = cand;
-            }
-            const float t = __uint_as_float((T & 0x80000000u) ? T ^ 0x80000000u : ~T);
-            over = key32(t + 2.5f * E);
-            from = key32(t - 2.5f * E);
-            int above = 0, near = 0;
+    int left = want, near = mid;
+    bool open = true;  // some are undecided and not all of them stay
+    const bool finite = E < 1e33f;  // every score, and E's parts
+    if (finite) {
+        // the smallest key that stays, T: the bin that it is in, then itself
+        uint32_t T = lo;
+        int need = want;  // of those in [lo, hi]
+        while (lo < hi) {
+            const int shift = max(0, 32 - __clz(hi - lo) - 10);  // at most kBins bins
             each([&](int, uint32_t k) {
-                above += k > over;
-                near += k >= from && k <= over;
+                if (k >= lo && k <= hi) atomicAdd(&s_hist[(k - lo) >> shift], 1);
             });
-            above = block_sum(above, s_count, turn);
-            near = block_sum(near, s_count, turn);
-            left = want - above;
-            open = near > left;
-        }
-        if (open) {
-            // exact scores of the undecided, a warp for each
-            for (int g = j0 + warp * 32; g < j1; g += kSelThreads) {
-                const uint32_t k = g + lane < j1 ? key32(scores[g + lane]) : 0;
-                uint32_t todo = __ballot_sync(0xffffffffu, g + lane < j1 && k >= from && k <= over);
-                const uint32_t mine = todo >> lane & 1 ? row_of(g + lane) : ~0u;
-                while (todo) {
-                    const int l = __ffs(todo) - 1;
-                    todo &= todo - 1;
-                    const uint32_t row = __shfl_sync(0xffffffffu, mine, l);
-                    double best = -INFINITY;
-                    for (int r = 0; r < a.rows; ++r) {
-                        double sum = 0.0;
-                        for (int c = lane; c < D; c += 32) {
-                            const double qc = (double)__bfloat162float(q[(long long)r * D + c]);
-                            const __nv_bfloat16* at = bounds + (size_t)row * (2 * D) + c;
-                            const double lo = row != ~0u ? (double)__bfloat162float(at[0]) : 0.0;
-                            const double hi = row != ~0u ? (double)__bfloat162float(at[D]) : 0.0;
-                            sum += (qc > 0.0 ? 0.0 : qc) * lo + (qc < 0.0 ? 0.0 : qc) * hi;
-                        }
-                        for (int m = 16; m >= 1; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-                        if (!(sum <= best)) best = best != best ? best : sum;  // NaN stays
-                    }
-                    if (lane == 0) exact[g + l] = key64(best);
+            __syncthreads();
+            constexpr int PER = kBins / kSelThreads;  // bins of a thread, from the top down
+            int c[PER], sum = 0;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) sum += c[i] = s_hist[kBins - 1 - (tid * PER + i)];
+            int incl = sum;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int up = __shfl_up_sync(0xffffffffu, incl, d);
+                if (lane >= d) incl += up;
+            }
+            turn ^= 1;
+            if (lane == 31) s_sum[turn][warp].x = incl;
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < PER; ++i) s_hist[kBins - 1 - (tid * PER + i)] = 0;
+            int above = incl - sum + __reduce_add_sync(0xffffffffu, lane < warp ? s_sum[turn][lane].x : 0);
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                if (above < need && need <= above + c[i]) {
+                    s_found[0] = kBins - 1 - (tid * PER + i);
+                    s_found[1] = above;
+                    s_many = c[i];
                 }
+                above += c[i];
             }
             __syncthreads();
-            auto each_open = [&](auto f) {
-                each([&](int j, uint32_t k) {
-                    if (k >= from && k <= over) f(exact[j]);
+            const int bin = s_found[0], many = s_many;
+            need -= s_found[1];
+            lo += (uint32_t)bin << shift;
+            hi = min(hi, lo + ((1u << shift) - 1));
+            T = lo;
+            if (many <= kList && lo < hi) {  // count greater ones within the bin
+                __syncthreads();
+                if (tid == 0) s_many = 0;
+                __syncthreads();
+                each([&](int, uint32_t k) {
+                    if (k >= lo && k <= hi) s_list[atomicAdd(&s_many, 1)] = k;
                 });
-            };
-            for (int bit = 63; bit >= 0; --bit) {
-                const uint64_t cand = exact_from | 1ull << bit;
-                int c = 0;
-                each_open([&](uint64_t k) { c += k >= cand; });
-                if (block_sum(c, s_count, turn) >= left) exact_from = cand;
+                __syncthreads();
+                if (tid < many) {
+                    const uint32_t k = s_list[tid];
+                    int greater = 0, same = 0;
+                    for (int i = 0; i < many; ++i) greater += s_list[i] > k, same += s_list[i] == k;
+                    if (greater < need && need <= greater + same) s_key = k;
+                }
+                __syncthreads();
+                T = s_key;
+                break;
             }
-            int c = 0;
-            each_open([&](uint64_t k) { c += k > exact_from; });
-            equal = left - block_sum(c, s_count, turn);
         }
+        over = key32(score_of(T) + 2.5f * E);
+        from = key32(score_of(T) - 2.5f * E);
+        int above = 0, there = 0;
+        each([&](int, uint32_t k) {
+            above += k > over;
+            there += k >= from && k <= over;
+        });
+        const int2 sums = block_sums(above, there);
+        left = want - sums.x;
+        near = sums.y;
+        open = near > left;
     }
-    const bool by_exact = equal != INT_MAX;
-    // equal ones before this thread's, then the places of those that stay
-    auto before = [&](int mine) {  // exclusive sum over the threads
-        int incl = mine;
+    // ---- exact scores of the undecided, a warp for each, 8 lanes for each row: sums of whole numbers, in units of 2^-61 A
+    // (what is below half a unit is lost: 2^-54 A in all), or, where something is not finite or tiny, in fp64, which has next to
+    // no throughput here (a block of 32 rows took 40 us).  What is decided by them is written over the scores: the largest key
+    // or the smallest.
+    const bool fixed = finite && A >= 1e-18f;  // no product that counts is subnormal
+    auto exact_key = [&](int i) -> uint64_t {
+        const uint32_t row = row_of(j0 + i);
+        const int part = lane & 7;
+        // 2^61 / A rounded down to a power of two
+        const float unit = __uint_as_float((uint32_t)min(max(127 + 61 + 126 - (int)(__float_as_uint(A) >> 23), 1), 254) << 23);
+        const uint4* at = reinterpret_cast<const uint4*>(bounds + (size_t)(row != ~0u ? row : 0) * (2 * D));
+        uint64_t top = 0;
+        for (int r = lane >> 3; r < ((a.rows + 3) & ~3); r += 4) {
+            const uint4* qr = reinterpret_cast<const uint4*>(q + (long long)min(r, a.rows - 1) * D);
+            long long whole = 0;
+            double sum = 0.0;
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int up = __shfl_up_sync(0xffffffffu, incl, d);
-            if (lane >= d) incl += up;
-        }
-        turn ^= 1;
-        if (lane == 31) s_count[turn][warp] = incl;
-        __syncthreads();
-        return incl - mine + __reduce_add_sync(0xffffffffu, lane < warp ? s_count[turn][lane] : 0);
-    };
-    int ties = 0;
-    if (by_exact) {
-        int c = 0;
-        each([&](int j, uint32_t k) { c += k >= from && k <= over && exact[j] == exact_from; });
-        ties = before(c);
-    }
-    auto stay = [&](auto f) {
-        if (want == 0) return;
-        int t = ties;
-        each([&](int j, uint32_t k) {
-            bool in = k > over;
-            if (k >= from && k <= over) {
-                if (!by_exact) {
-                    in = true;
-                } else {
-                    const uint64_t e = exact[j];
-                    in = e > exact_from || (e == exact_from && t < equal);
-                    t += e == exact_from;
+            for (int c = part; c < D / 8; c += 8) {
+                const uint4 x = qr[c], l = row != ~0u ? at[c] : make_uint4(0, 0, 0, 0),
+                            h = row != ~0u ? at[c + D / 8] : make_uint4(0, 0, 0, 0);
+                const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, lw[4] = {l.x, l.y, l.z, l.w}, hw[4] = {h.x, h.y, h.z, h.w};
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    auto el = [&](const uint32_t (&w)[4]) { return __uint_as_float(e & 1 ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16); };
+                    const float qe = el(xw), le = el(lw), he = el(hw);
+                    if (fixed)
+                        whole += __float2ll_rn(qe * (qe < 0.f ? le : he) * unit);
+                    else
+                        sum += (double)(qe > 0.f ? 0.f : qe) * le + (double)(qe < 0.f ? 0.f : qe) * he;
                 }
             }
-            if (in) f(j);
-        });
+#pragma unroll
+            for (int m = 1; m < 8; m <<= 1) {
+                whole += __shfl_xor_sync(0xffffffffu, whole, m);
+                if (!fixed) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+            }
+            const uint64_t key = fixed ? (uint64_t)whole ^ (1ull << 63) : key64(sum);
+            top = max(top, key);  // NaN on top
+        }
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 8));
+        return max(top, __shfl_xor_sync(0xffffffffu, top, 16));
     };
+    if (open && near <= kList) {
+        __syncthreads();
+        if (tid == 0) s_many = 0;
+        __syncthreads();
+        each([&](int i, uint32_t k) {
+            if (k >= from && k <= over) s_list[atomicAdd(&s_many, 1)] = i;
+        });
+        __syncthreads();
+        for (int u = warp; u < near; u += kSelWarps) {
+            const uint64_t e = exact_key((int)s_list[u]);
+            if (lane == 0) s_exact[u] = e;
+        }
+        __syncthreads();
+        if (tid < near) {
+            const uint64_t e = s_exact[tid];
+            int before = 0;
+            for (int u = 0; u < near; ++u) before += s_exact[u] > e || (s_exact[u] == e && s_list[u] < s_list[tid]);
+            keys[s_list[tid]] = before < left ? 0xFFFFFFFFu : 0;
+        }
+        __syncthreads();
+        from = max(from, 1u);
+    } else if (open) {
+        uint64_t* exact = reinterpret_cast<uint64_t*>(a.exact) + (long long)bh * a.stride;
+        auto undecided = [&](int i, uint32_t k) { return i < we && k >= from && k <= over; };
+        for (int g = wi; g < we; g += 32) {
+            uint32_t todo = __ballot_sync(0xffffffffu, undecided(g + lane, g + lane < we ? keys[g + lane] : 0));
+            while (todo) {
+                const int l = __ffs(todo) - 1;
+                todo &= todo - 1;
+                const uint64_t e = exact_key(g + l);
+                if (lane == 0) exact[g + l] = e;
+            }
+        }
+        __syncthreads();
+        auto each_open = [&](auto f) {
+            each([&](int i, uint32_t k) {
+                if (k >= from && k <= over) f(exact[i]);
+            });
+        };
+        uint64_t least = 0;  // of the exact keys that stay; of those equal to it the first `equal`
+        for (int bit = 63; bit >= 0; --bit) {
+            const uint64_t cand = least | 1ull << bit;
+            int c = 0;
+            each_open([&](uint64_t k) { c += k >= cand; });
+            if (block_sums(c, 0).x >= left) least = cand;
+        }
+        int above = 0, same = 0;
+        each_open([&](uint64_t k) { above += k > least, same += k == least; });
+        const int equal = left - block_sums(above, 0).x;
+        same = __reduce_add_sync(0xffffffffu, same);
+        turn ^= 1;
+        if (lane == 0) s_sum[turn][warp].x = same;
+        __syncthreads();
+        int ties = __reduce_add_sync(0xffffffffu, lane < warp ? s_sum[turn][lane].x : 0);  // before this warp's
+        for (int g = wi; g < we; g += 32) {
+            const int i = g + lane;
+            const uint32_t k = i < we ? keys[i] : 0;
+            const bool u = undecided(i, k);
+            const uint64_t e = u ? exact[i] : 0;
+            const uint32_t eq = __ballot_sync(0xffffffffu, u && e == least);
+            if (u) keys[i] = e > least || (e == least && ties + __popc(eq & ((1u << lane) - 1)) < equal) ? 0xFFFFFFFFu : 0;
+            ties += __popc(eq);
+        }
+        __syncthreads();
+        from = max(from, 1u);
+    }
+    // ---- the places of those that stay, in order: the warps' counts first
     int kept = 0;
-    stay([&](int) { ++kept; });
-    int at = a.first + before(kept);
-    stay([&](int j) { out[at++] = j; });
-    for (int i = tid; i < a.first; i += kSelThreads) out[i] = i;
-    for (int i = tid; i < a.recent; i += kSelThreads) out[a.first + want + i] = j1 + i;
+    each([&](int, uint32_t k) { kept += k >= from; });
+    kept = __reduce_add_sync(0xffffffffu, kept);
+    turn ^= 1;
+    if (lane == 0) s_sum[turn][warp].x = kept;
+    __syncthreads();
+    out += a.first + __reduce_add_sync(0xffffffffu, lane < warp ? s_sum[turn][lane].x : 0);
+    constexpr int U = 4;
+    for (int g = wi; g < we; g += 32 * U) {
+        uint32_t in[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = g + 32 * u + lane;
+            in[u] = __ballot_sync(0xffffffffu, i < we && keys[i] >= from);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (in[u] >> lane & 1) out[__popc(in[u] & ((1u << lane) - 1))] = j0 + g + 32 * u + lane;
+            out += __popc(in[u]);
+        }
+    }
 }
 
 template <int D>
@@ -345,10 +485,15 @@ cudaError_t launch_d(const SelectLaunch& a, cudaStream_t s) {
     // CTAs per (sequence, kv head): more while each has a batch for every warp and all of them fit at once
     const long long bh = (long long)a.B * a.Hkv, cap = (long long)a.max_pages * bpp;
     plan.ctas = 1;
-    while (plan.ctas < kSelectCtas && cap > 128ll * plan.ctas && bh * plan.ctas * 2 <= 2 * a.num_sms) plan.ctas *= 2;
+    while (plan.ctas < kSelectCtas && cap > 128ll * plan.ctas && bh * plan.ctas <= a.num_sms) plan.ctas *= 2;
+    const bool global = cap > kMostKeys || a.rows > kRowTile;
+    const int smem = global ? 0 : (int)cap * 4;
+    cudaError_t e = set_smem_limit_once<select_blocks_kernel<D, false>>(kMostKeys * 4);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(bh * plan.ctas));
     cfg.blockDim = dim3(kSelThreads);
+    cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -357,11 +502,8 @@ cudaError_t launch_d(const SelectLaunch& a, cudaStream_t s) {
     attr[1].val.clusterDim = {(unsigned)plan.ctas, 1, 1};
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    const long long per = (cap + kSelThreads - 1) / kSelThreads;
-    return per <= 1   ? cudaLaunchKernelEx(&cfg, select_blocks_kernel<D, 1>, a, plan)
-           : per <= 4 ? cudaLaunchKernelEx(&cfg, select_blocks_kernel<D, 4>, a, plan)
-           : per <= 16 ? cudaLaunchKernelEx(&cfg, select_blocks_kernel<D, 16>, a, plan)
-                      : cudaLaunchKernelEx(&cfg, select_blocks_kernel<D, 0>, a, plan);
+    return global ? cudaLaunchKernelEx(&cfg, select_blocks_kernel<D, true>, a, plan)
+                  : cudaLaunchKernelEx(&cfg, select_blocks_kernel<D, false>, a, plan);
 }
 
 }  // namespace
