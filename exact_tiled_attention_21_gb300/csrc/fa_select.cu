@@ -33,7 +33,6 @@
 namespace fa {
 namespace {
 
-constexpr int kSelThreads = 256, kSelWarps = kSelThreads / 32;
 constexpr int kRowTile = 64;      // query rows in shared memory at once
 constexpr int kBatch = 16;        // blocks of a warp's batch
 constexpr int kBins = 1024, kList = 256;
@@ -85,13 +84,27 @@ struct SelectPlan {
     FastDiv per_page;  // blocks of a page
 };
 
-// GLOBAL: the scores go through the workspace (too many of them, or several tiles of query rows).
-template <int D, bool GLOBAL>
-__global__ void __launch_bounds__(kSelThreads, 2) select_blocks_kernel(const SelectLaunch a, const SelectPlan plan) {
+// Score of a row and a block in fp64, by 8 lanes; its key.  On its own: it is called where something is not finite, or tiny.
+__device__ __noinline__ uint64_t slow_key(const __nv_bfloat16* q, const __nv_bfloat16* ends, int d, int part) {
+    double sum = 0.0;
+    for (int c = part; c < d; c += 8) {
+        const double x = (double)__bfloat162float(q[c]);
+        sum += (x > 0.0 ? 0.0 : x) * (ends ? (double)__bfloat162float(ends[c]) : 0.0) +
+               (x < 0.0 ? 0.0 : x) * (ends ? (double)__bfloat162float(ends[d + c]) : 0.0);
+    }
+    for (int m = 1; m < 8; m <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+    return key64(sum);
+}
+
+// GLOBAL: the scores go through the workspace (too many of them, or several tiles of query rows).  THREADS: 512 where a CTA
+// has an SM to itself.
+template <int D, bool GLOBAL, int THREADS>
+__global__ void __launch_bounds__(THREADS, 512 / THREADS) select_blocks_kernel(const SelectLaunch a, const SelectPlan plan) {
+    constexpr int kSelThreads = THREADS, kSelWarps = THREADS / 32;
     constexpr int S = D / 16, CHUNKS = 4 * S;  // 64-byte pieces of a block's bounds, a lane's part of which is a chunk
     extern __shared__ __align__(16) uint32_t s_keys[];
     __shared__ uint4 s_q[kRowTile / 8][S][32];  // by tile of 8 rows and piece: the lanes' B fragments of two products
-    __shared__ uint32_t s_sum8[CHUNKS], s_big[CHUNKS], s_all[kSelectCtas][CHUNKS];  // bits of the largest sum of |q| and |bound|
+    __shared__ uint32_t s_sum8[CHUNKS], s_big[CHUNKS];  // bits of the largest sum of |q|, and |bound|, of each chunk
     __shared__ int s_hist[kBins];
     __shared__ uint64_t s_exact[kList];
     __shared__ uint32_t s_list[kList];
@@ -122,6 +135,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_blocks_kernel(const Sel
         for (int i = tid; i < a.recent; i += kSelThreads) out[a.first + want + i] = j0 + mid + i;
     }
     if (want == 0) return;
+    if (tid < CHUNKS) s_sum8[tid] = s_big[tid] = 0;
     if (plan.ctas > 1) cluster_arrive();  // waited for below: the first CTA runs before the others write to it
     uint32_t* keys = GLOBAL ? a.scores + (long long)bh * a.stride : s_keys;  // of block j0 + i
     const uint32_t keys0 = mapa_shared(smem_u32(s_keys), 0);                 // those of the first CTA
@@ -154,7 +168,6 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_blocks_kernel(const Sel
             atomicMax(&s_sum8[chunk], __float_as_uint(sum) & 0x7FFFFFFFu);
         }
     };
-    if (tid < CHUNKS) s_sum8[tid] = s_big[tid] = 0;
     for (int i = tid; i < kBins; i += kSelThreads) s_hist[i] = 0;
     if (tid == 0) s_many = 0;
     uint32_t big[S];
@@ -220,7 +233,8 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_blocks_kernel(const Sel
         if (g8 == 0) atomicMax(&s_big[s * 4 + t4], max(big[s] << 16, big[s] & 0xFFFF0000u));
     }
     __syncthreads();
-    if (tid < CHUNKS) st_cluster_u32(mapa_shared(smem_u32(&s_all[rank][tid]), 0), s_big[tid]);
+    if (rank > 0 && tid < CHUNKS)
+        asm volatile("red.shared::cluster.max.u32 [%0], %1;" ::"r"(mapa_shared(smem_u32(&s_big[tid]), 0)), "r"(s_big[tid]) : "memory");
     if (plan.ctas > 1) {
         cluster_arrive();
         cluster_wait();
@@ -256,11 +270,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_blocks_kernel(const Sel
     hi = __reduce_max_sync(0xffffffffu, hi);
     if (lane == 0) s_sum[0][warp] = make_int2((int)lo, (int)hi);
     float A = 0.f;  // the largest sum of |q_c| |bound_c| that a row can have; NaN and infinities stay
-    for (int c = lane; c < CHUNKS; c += 32) {
-        uint32_t m = s_all[0][c];
-        for (int r = 1; r < plan.ctas; ++r) m = max(m, s_all[r][c]);
-        A += __uint_as_float(s_sum8[c]) * __uint_as_float(m);
-    }
+    if (lane < CHUNKS) A = __uint_as_float(s_sum8[lane]) * __uint_as_float(s_big[lane]);
     for (int w = 16; w >= 1; w >>= 1) A += __shfl_xor_sync(0xffffffffu, A, w);
     __syncthreads();
     for (int w = 0; w < kSelWarps; ++w) {
@@ -283,7 +293,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_blocks_kernel(const Sel
                 if (k >= lo && k <= hi) atomicAdd(&s_hist[(k - lo) >> shift], 1);
             });
             __syncthreads();
-            constexpr int PER = kBins / kSelThreads;  // bins of a thread, from the top down
+            constexpr int PER = kBins / THREADS;  // bins of a thread, from the top down
             int c[PER], sum = 0;
 #pragma unroll
             for (int i = 0; i < PER; ++i) sum += c[i] = s_hist[kBins - 1 - (tid * PER + i)];
@@ -346,42 +356,66 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_blocks_kernel(const Sel
         open = near > left;
     }
     // ---- exact scores of the undecided, a warp for each, 8 lanes for each row: sums of whole numbers, in units of 2^-61 A
-    // (what is below half a unit is lost: 2^-54 A in all), or, where something is not finite or tiny, in fp64, which has next to
-    // no throughput here (a block of 32 rows took 40 us).  What is decided by them is written over the scores: the largest key
-    // or the smallest.
-    const bool fixed = finite && A >= 1e-18f;  // no product that counts is subnormal
+    // (what is lost below them is 2^-58 A at most), or, where something is not finite or tiny, in fp64, which has next
+    // to no throughput here (a block of 32 rows took 40 us).  What is decided by them is written over the scores: the largest
+    // key or the smallest.
+    const bool fixed = finite && A >= 1e-12f;  // no product that counts is subnormal
     auto exact_key = [&](int i) -> uint64_t {
         const uint32_t row = row_of(j0 + i);
         const int part = lane & 7;
-        // 2^61 / A rounded down to a power of two
-        const float unit = __uint_as_float((uint32_t)min(max(127 + 61 + 126 - (int)(__float_as_uint(A) >> 23), 1), 254) << 23);
+        // a product is taken apart in whole multiples of 2^21 / A, 2^43 / A and 2^65 / A (A rounded up to a power of two),
+        // each found by adding 1.5 x 2^23, which rounds to whole numbers, and exact to take off
+        constexpr float kMagic = 12582912.f;
+        const float one = __uint_as_float((uint32_t)(127 + 21 + 126 - (fixed ? (int)(__float_as_uint(A) >> 23) : 127)) << 23);
         const uint4* at = reinterpret_cast<const uint4*>(bounds + (size_t)(row != ~0u ? row : 0) * (2 * D));
+        constexpr int C = D / 64;
+        uint4 l[C], h[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            l[c] = row != ~0u ? at[c * 8 + part] : make_uint4(0, 0, 0, 0);
+            h[c] = row != ~0u ? at[D / 8 + c * 8 + part] : make_uint4(0, 0, 0, 0);
+        }
         uint64_t top = 0;
+#pragma unroll 1
         for (int r = lane >> 3; r < ((a.rows + 3) & ~3); r += 4) {
-            const uint4* qr = reinterpret_cast<const uint4*>(q + (long long)min(r, a.rows - 1) * D);
-            long long whole = 0;
-            double sum = 0.0;
+            const __nv_bfloat16* qr = q + (long long)min(r, a.rows - 1) * D;
+            uint64_t key;
+            if (fixed) {
+                int s0 = 0, s1 = 0, s2 = 0;
+                auto add = [&](float qe, float le, float he) {
+                    float x = qe * (qe < 0.f ? le : he) * one;  // at most 2^21
+                    auto whole = [&](int& s) {
+                        const float t = x + kMagic;
+                        s += __float_as_int(t) - __float_as_int(kMagic);
+                        x = (x - (t - kMagic)) * 4194304.f;
+                    };
+                    whole(s0);
+                    whole(s1);
+                    whole(s2);
+                };
+                auto add2 = [&](uint32_t x, uint32_t l, uint32_t h) {
+                    add(__uint_as_float(x << 16), __uint_as_float(l << 16), __uint_as_float(h << 16));
+                    add(__uint_as_float(x & 0xFFFF0000u), __uint_as_float(l & 0xFFFF0000u), __uint_as_float(h & 0xFFFF0000u));
+                };
 #pragma unroll
-            for (int c = part; c < D / 8; c += 8) {
-                const uint4 x = qr[c], l = row != ~0u ? at[c] : make_uint4(0, 0, 0, 0),
-                            h = row != ~0u ? at[c + D / 8] : make_uint4(0, 0, 0, 0);
-                const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, lw[4] = {l.x, l.y, l.z, l.w}, hw[4] = {h.x, h.y, h.z, h.w};
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    auto el = [&](const uint32_t (&w)[4]) { return __uint_as_float(e & 1 ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16); };
-                    const float qe = el(xw), le = el(lw), he = el(hw);
-                    if (fixed)
-                        whole += __float2ll_rn(qe * (qe < 0.f ? le : he) * unit);
-                    else
-                        sum += (double)(qe > 0.f ? 0.f : qe) * le + (double)(qe < 0.f ? 0.f : qe) * he;
+                for (int c = 0; c < C; ++c) {
+                    const uint4 x = reinterpret_cast<const uint4*>(qr)[c * 8 + part];
+                    add2(x.x, l[c].x, h[c].x);
+                    add2(x.y, l[c].y, h[c].y);
+                    add2(x.z, l[c].z, h[c].z);
+                    add2(x.w, l[c].w, h[c].w);
                 }
-            }
 #pragma unroll
-            for (int m = 1; m < 8; m <<= 1) {
-                whole += __shfl_xor_sync(0xffffffffu, whole, m);
-                if (!fixed) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+                for (int m = 1; m < 8; m <<= 1) {  // |s| <= 128 x 2^22
+                    s0 += __shfl_xor_sync(0xffffffffu, s0, m);
+                    s1 += __shfl_xor_sync(0xffffffffu, s1, m);
+                    s2 += __shfl_xor_sync(0xffffffffu, s2, m);
+                }
+                // in units of 2^-61 A, which 64 bits hold: the last part rounded to them
+                key = (uint64_t)(((long long)s0 << 40) + ((long long)s1 << 18) + ((s2 + 8) >> 4)) ^ (1ull << 63);
+            } else {
+                key = slow_key(qr, row != ~0u ? reinterpret_cast<const __nv_bfloat16*>(at) : nullptr, D, part);
             }
-            const uint64_t key = fixed ? (uint64_t)whole ^ (1ull << 63) : key64(sum);
             top = max(top, key);  // NaN on top
         }
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 8));
@@ -477,22 +511,13 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_blocks_kernel(const Sel
     }
 }
 
-template <int D>
-cudaError_t launch_d(const SelectLaunch& a, cudaStream_t s) {
-    SelectPlan plan;
-    const int bpp = a.page_blocks;
-    plan.per_page = FastDiv((uint32_t)bpp);
-    // CTAs per (sequence, kv head): more while each has a batch for every warp and all of them fit at once
-    const long long bh = (long long)a.B * a.Hkv, cap = (long long)a.max_pages * bpp;
-    plan.ctas = 1;
-    while (plan.ctas < kSelectCtas && cap > 128ll * plan.ctas && bh * plan.ctas <= a.num_sms) plan.ctas *= 2;
-    const bool global = cap > kMostKeys || a.rows > kRowTile;
-    const int smem = global ? 0 : (int)cap * 4;
-    cudaError_t e = set_smem_limit_once<select_blocks_kernel<D, false>>(kMostKeys * 4);
+template <int D, bool GLOBAL, int THREADS>
+cudaError_t launch_t(const SelectLaunch& a, const SelectPlan& plan, int smem, cudaStream_t s) {
+    cudaError_t e = set_smem_limit_once<select_blocks_kernel<D, GLOBAL, THREADS>>(kMostKeys * 4);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(bh * plan.ctas));
-    cfg.blockDim = dim3(kSelThreads);
+    cfg.gridDim = dim3((unsigned)(a.B * a.Hkv * plan.ctas));
+    cfg.blockDim = dim3(THREADS);
     cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
@@ -502,8 +527,23 @@ cudaError_t launch_d(const SelectLaunch& a, cudaStream_t s) {
     attr[1].val.clusterDim = {(unsigned)plan.ctas, 1, 1};
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return global ? cudaLaunchKernelEx(&cfg, select_blocks_kernel<D, true>, a, plan)
-                  : cudaLaunchKernelEx(&cfg, select_blocks_kernel<D, false>, a, plan);
+    return cudaLaunchKernelEx(&cfg, select_blocks_kernel<D, GLOBAL, THREADS>, a, plan);
+}
+
+template <int D>
+cudaError_t launch_d(const SelectLaunch& a, cudaStream_t s) {
+    SelectPlan plan;
+    const int bpp = a.page_blocks;
+    plan.per_page = FastDiv((uint32_t)bpp);
+    // CTAs per (sequence, kv head): more while each has a batch for every warp and all of them fit at once
+    const long long bh = (long long)a.B * a.Hkv, cap = (long long)a.max_pages * bpp;
+    plan.ctas = 1;
+    while (plan.ctas < kSelectCtas && cap > 128ll * plan.ctas && bh * plan.ctas <= a.num_sms) plan.ctas *= 2;
+    const bool wide = bh * plan.ctas <= a.num_sms;  // a CTA has an SM to itself
+    if (cap > kMostKeys || a.rows > kRowTile)
+        return wide ? launch_t<D, true, 512>(a, plan, 0, s) : launch_t<D, true, 256>(a, plan, 0, s);
+    const int smem = (int)cap * 4;
+    return wide ? launch_t<D, false, 512>(a, plan, smem, s) : launch_t<D, false, 256>(a, plan, smem, s);
 }
 
 }  // namespace
