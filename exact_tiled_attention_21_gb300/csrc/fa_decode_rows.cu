@@ -735,7 +735,8 @@ template <int D, int ROWS, bool LIST>
 cudaError_t launch_merge(const DecodeRowsLaunch& a, const Params& p, cudaStream_t s) {
     const long long rows = (long long)a.B * a.Hkv * p.rows;
     // rows alone in a block where there are few of them: their parts are read by more threads
-    if (rows <= 4ll * a.num_sms)
+    const long long parts = LIST ? p.workers / ((long long)a.B * a.Hkv * p.row_tiles) : p.pre_workers / ((long long)a.Hkv * p.pre_tiles);
+    if (rows <= (parts >= 4 ? 16ll : 4ll) * a.num_sms)
         return launch_dependent(merge_rows_kernel<D, ROWS, LIST, true, 256>, dim3((unsigned)rows), dim3(256), 0, s, p);
     constexpr int PER = 128 / (D / 4);
     return launch_dependent(merge_rows_kernel<D, ROWS, LIST, false, 128>, dim3((unsigned)((rows + PER - 1) / PER)), dim3(128), 0,

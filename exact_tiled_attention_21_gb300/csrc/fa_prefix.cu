@@ -36,8 +36,8 @@ struct Pre {
     static constexpr int Q_BYTES = 128 * D * 2, KV_BYTES = BN * D * 2, CHUNK = 128 * 128;
     static constexpr int NSLOT = D == 128 ? 5 : 8;
     static constexpr int OFF_Q = 0, OFF_KV = 2 * Q_BYTES, OFF_BAR = OFF_KV + NSLOT * KV_BYTES;
-    // barriers: kv_full[NSLOT], kv_empty[NSLOT], q_full[2], s_full[2], p_full[2], o_final[2], teardown
-    static constexpr int NBAR = 2 * NSLOT + 9, OFF_MISC = OFF_BAR + NBAR * 8, SMEM = OFF_MISC + 16 + 1024;
+    // barriers: kv_full[NSLOT], kv_empty[NSLOT], q_full[2], s_full[2], p_full[2], o_final[2], pv_done, teardown
+    static constexpr int NBAR = 2 * NSLOT + 10, OFF_MISC = OFF_BAR + NBAR * 8, SMEM = OFF_MISC + 16 + 1024;
     static constexpr int THREADS = 320;
     static constexpr uint32_t TMEM_COLS = 512, COL_S = 0, COL_O = 256;  // tile t: + 128 t, + D t
     static constexpr uint32_t IDESC_S = idesc_bf16(128, BN, 0, 0);      // Q, K both K-major
@@ -53,6 +53,7 @@ struct PreParams {
     float* part_o;      // [slot][tile_rows][D]
     float* part_lse;    // [slot][tile_rows], log2
     int B, Hkv, Nq, rows, page, max_pages, num_pages, tiles, tile_rows, box;
+    FastDiv per_row;  // rows
     float scale_log2;
     DevError* err;
     uint64_t timeout_ns;
@@ -67,7 +68,8 @@ prefix_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
     const uint32_t s_base = smem_u32(smem), bar0 = s_base + C::OFF_BAR;
     auto bar_full = [&](int s) { return bar0 + 8 * s; };
     auto bar_empty = [&](int s) { return bar0 + 8 * C::NSLOT + 8 * s; };
-    const uint32_t BAR_Q = bar0 + 16 * C::NSLOT, BAR_S = BAR_Q + 16, BAR_P = BAR_S + 16, BAR_O = BAR_P + 16, BAR_TD = BAR_O + 16;
+    const uint32_t BAR_Q = bar0 + 16 * C::NSLOT, BAR_S = BAR_Q + 16, BAR_P = BAR_S + 16, BAR_O = BAR_P + 16, BAR_PV = BAR_O + 16,
+                   BAR_TD = BAR_PV + 8;
     uint32_t* tmem_slot = (uint32_t*)(smem + C::OFF_MISC);
     volatile int* abort_flag = (volatile int*)(smem + C::OFF_MISC + 4);
     const WaitCtl ctl{p.err, p.timeout_ns, abort_flag};
@@ -81,6 +83,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
             mbar_init(BAR_P + 8 * t, 128);
             mbar_init(BAR_O + 8 * t, 1);
         }
+        mbar_init(BAR_PV, 1);
         mbar_init(BAR_TD, 1);
         fence_mbar_init();
         if ((s_base & 1023u) != 0) record_error(ctl, kErrTimeout, kSiteAlign, (int)(s_base & 1023u));
@@ -184,9 +187,9 @@ prefix_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
         if (lane == 0 && !*abort_flag) {
             int slot = 0;
             uint32_t phase = 0, p_iter = 0, q_iter = 0, p1_iter = 0, q1_iter = 0;
-            auto issue_s = [&](int t, uint32_t sK) {
+            auto issue_s = [&](int t, uint32_t sK, int buf) {
                 const uint64_t a0 = sdesc_sw128(s_base + C::OFF_Q + t * C::Q_BYTES, 16, 1024), b0 = sdesc_sw128(sK, 16, 1024);
-                const uint32_t d = tmem + C::COL_S + 128 * t;
+                const uint32_t d = tmem + C::COL_S + 128 * buf;
                 mma_ss_first(d, a0, b0, C::IDESC_S);
 #pragma unroll
                 for (int k = 1; k < D / 16; ++k) {
@@ -194,9 +197,9 @@ prefix_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
                     mma_ss_acc(d, sdesc_add(a0, off), sdesc_add(b0, off), C::IDESC_S);
                 }
             };
-            auto issue_o = [&](int t, uint32_t sV, bool acc) {
+            auto issue_o = [&](int t, uint32_t sV, bool acc, int buf) {
                 const uint64_t b0 = sdesc_sw128(sV, C::CHUNK, 1024);
-                const uint32_t d = tmem + C::COL_O + D * t, pc = tmem + C::COL_S + 128 * t;
+                const uint32_t d = tmem + C::COL_O + D * t, pc = tmem + C::COL_S + 128 * buf;
                 mma_ts(d, pc, b0, C::IDESC_O, acc ? 1u : 0u);
 #pragma unroll
                 for (int k = 1; k < C::BN / 16; ++k) mma_ts_acc(d, pc + k * 8, sdesc_add(b0, k * 2048), C::IDESC_O);
@@ -217,12 +220,35 @@ prefix_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
                 if (!mbar_wait(bar_full(kslot), phase, ctl, kSiteKvFull)) break;
                 tc_fence_after();
                 next();
-                issue_s(0, kv_at(kslot));
+                issue_s(0, kv_at(kslot), 0);
                 mma_commit(BAR_S);
-                if (g.two) {
-                    issue_s(1, kv_at(kslot));
-                    mma_commit(BAR_S + 8);
+                if (!g.two) {
+                    // one tile: the scores of the next block, into the other tile's columns, before the product of this one
+                    mma_commit(bar_empty(kslot));
+                    for (int s = g.s0; s < g.s1; ++s, ++u) {
+                        const int buf = (s - g.s0) & 1, vslot = slot;
+                        const uint32_t vphase = phase;
+                        next();
+                        if (s + 1 < g.s1) {
+                            kslot = slot;
+                            if (!mbar_wait(bar_full(kslot), phase, ctl, kSiteKvFull)) { ok = false; break; }
+                            tc_fence_after();
+                            next();
+                            issue_s(0, kv_at(kslot), buf ^ 1);
+                            mma_commit(BAR_S + 8 * (buf ^ 1));
+                            mma_commit(bar_empty(kslot));
+                        }
+                        if (!mbar_wait(bar_full(vslot), vphase, ctl, kSiteKvFull)) { ok = false; break; }
+                        if (!mbar_wait(BAR_P + 8 * buf, (buf ? p1_iter++ : p_iter++) & 1, ctl, kSitePFull)) { ok = false; break; }
+                        tc_fence_after();
+                        issue_o(0, kv_at(vslot), s > g.s0, buf);
+                        mma_commit(bar_empty(vslot));
+                        mma_commit(s + 1 < g.s1 ? BAR_PV : BAR_O);
+                    }
+                    continue;
                 }
+                issue_s(1, kv_at(kslot), 1);
+                mma_commit(BAR_S + 8);
                 mma_commit(bar_empty(kslot));
                 for (int s = g.s0; s < g.s1; ++s, ++u) {
                     const bool more = s + 1 < g.s1;
@@ -231,30 +257,26 @@ prefix_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
                     next();
                     if (!mbar_wait(BAR_P, p_iter++ & 1, ctl, kSitePFull)) { ok = false; break; }
                     tc_fence_after();
-                    issue_o(0, kv_at(vslot), s > g.s0);
+                    issue_o(0, kv_at(vslot), s > g.s0, 0);
                     if (more) {
                         kslot = slot;
                         if (!mbar_wait(bar_full(kslot), phase, ctl, kSiteKvFull)) { ok = false; break; }
                         tc_fence_after();
                         next();
-                        issue_s(0, kv_at(kslot));
+                        issue_s(0, kv_at(kslot), 0);
                         mma_commit(BAR_S);
                     } else {
                         mma_commit(BAR_O);
                     }
-                    if (g.two) {
-                        if (!mbar_wait(BAR_P + 8, p1_iter++ & 1, ctl, kSitePFull)) { ok = false; break; }
-                        tc_fence_after();
-                        issue_o(1, kv_at(vslot), s > g.s0);
-                    }
+                    if (!mbar_wait(BAR_P + 8, p1_iter++ & 1, ctl, kSitePFull)) { ok = false; break; }
+                    tc_fence_after();
+                    issue_o(1, kv_at(vslot), s > g.s0, 1);
                     mma_commit(bar_empty(vslot));
                     if (more) {
-                        if (g.two) {
-                            issue_s(1, kv_at(kslot));
-                            mma_commit(BAR_S + 8);
-                        }
+                        issue_s(1, kv_at(kslot), 1);
+                        mma_commit(BAR_S + 8);
                         mma_commit(bar_empty(kslot));
-                    } else if (g.two) {
+                    } else {
                         mma_commit(BAR_O + 8);
                     }
                 }
@@ -269,29 +291,37 @@ prefix_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
         const int t = warp >> 2, r = tid & 127;  // tile; row within it = TMEM lane
         if (c == 0 && tid == 0 && given != shared) record_invalid(p.err, kSiteCacheLen, given);
         const uint32_t lane_addr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        const uint32_t col_s = C::COL_S + 128 * t, col_o = C::COL_O + D * t;
-        uint32_t s_iter = 0, o_iter = 0, kv_fill = 0;  // kv_fill: ring fills before the segment
+        const uint32_t col_o = C::COL_O + D * t;
+        // handoffs before the segment: of the scores' buffers, of the products of one tile, of the ring's fills; of O so far
+        uint32_t s_next0 = 0, s_next1 = 0, pv_next = 0, kv_fill = 0, o_iter = 0;
         for (long long u = u0; u < u1;) {
             const Segment g = segment_at(u);
             const int nst = g.s1 - g.s0;
             u += nst;
-            const uint32_t fill0 = kv_fill;
+            const uint32_t fill0 = kv_fill, s0 = s_next0, s1 = s_next1, pv0 = pv_next;
             kv_fill += 2 * nst;
+            s_next0 += g.two ? nst : (nst + 1) / 2;
+            s_next1 += g.two ? nst : nst / 2;
+            pv_next += g.two ? 0 : nst - 1;
             if (t == 1 && !g.two) continue;
             // ---- the tile's query rows, coalesced: D / 8 lanes a row; those past the last one are zeros
             {
                 uint8_t* sq = smem + C::OFF_Q + t * C::Q_BYTES;
-                constexpr int LPR = D / 8;
-                const int piece = r % LPR;
-#pragma unroll 4
-                for (int row = r / LPR; row < 128; row += 128 / LPR) {
-                    const int at = g.row0 + t * 128 + row;
-                    uint4 x = make_uint4(0, 0, 0, 0);
-                    if (at < all) {
-                        const int b = at / p.rows, i = at - b * p.rows;
-                        x = *reinterpret_cast<const uint4*>(p.q + (((long long)b * p.Hkv + g.kvh) * p.rows + i) * D + piece * 8);
-                    }
-                    *reinterpret_cast<uint4*>(sq + (piece >> 3) * C::CHUNK + row * 128 + (((piece & 7) ^ (row & 7)) << 4)) = x;
+                constexpr int LPR = D / 8, N = LPR;  // N rows of a thread, all in flight: the keys' copies fill the memory's queues
+                const int piece = r % LPR, row = r / LPR;
+                uint4 x[N];
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    const int at = g.row0 + t * 128 + row + i * (128 / LPR);
+                    const int b = (int)p.per_row.div(at);
+                    x[i] = at < all ? *reinterpret_cast<const uint4*>(
+                                          p.q + (((long long)b * p.Hkv + g.kvh) * p.rows + (at - b * p.rows)) * D + piece * 8)
+                                    : make_uint4(0, 0, 0, 0);
+                }
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    const int to = row + i * (128 / LPR);
+                    *reinterpret_cast<uint4*>(sq + (piece >> 3) * C::CHUNK + to * 128 + (((piece & 7) ^ (to & 7)) << 4)) = x[i];
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 mbar_arrive(BAR_Q + 8 * t);
@@ -299,8 +329,10 @@ prefix_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
             float m_use = -INFINITY, l = 0.f;
             bool ok = true;
             for (int j = 0; j < nst; ++j) {
-                if (!mbar_wait(BAR_S + 8 * t, s_iter & 1, ctl, kSiteSFull)) { ok = false; break; }
-                ++s_iter;
+                const int buf = g.two ? t : j & 1;  // one tile takes both buffers in turn
+                const uint32_t col_s = C::COL_S + 128 * buf;
+                const uint32_t nth = (buf ? s1 : s0) + (g.two ? j : j >> 1);
+                if (!mbar_wait(BAR_S + 8 * buf, nth & 1, ctl, kSiteSFull)) { ok = false; break; }
                 tc_fence_after();
                 const int nk = min(128, shared - (g.s0 + j) * 128);  // at least 1
                 const float mraw = nk < 128 ? row_max_pass<true>(lane_addr + col_s, nk - 1, 0)
@@ -309,7 +341,12 @@ prefix_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
                 if (j == 0) {
                     m_use = m_new;
                 } else if (__any_sync(0xffffffffu, m_new > m_use + 8.f)) {
-                    // rescale the accumulator so that O and l keep a common reference
+                    // rescale the accumulator so that O and l keep a common reference; with one tile the product before
+                    // may still be running
+                    if (!g.two) {
+                        if (!mbar_wait(BAR_PV, (pv0 + j - 1) & 1, ctl, kSitePFull)) { ok = false; break; }
+                        tc_fence_after();
+                    }
                     const float alpha = m_new == -INFINITY ? 1.f : ex2(m_use - m_new);
 #pragma unroll 1
                     for (int q4 = 0; q4 < D / 32; ++q4) {
@@ -339,13 +376,13 @@ prefix_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 }
                 tc_fence_before();
-                mbar_arrive(BAR_P + 8 * t);
+                mbar_arrive(BAR_P + 8 * buf);
             }
             if (!ok || !mbar_wait(BAR_O + 8 * t, o_iter & 1, ctl, kSiteOFinal)) break;
             ++o_iter;
             tc_fence_after();
             // ---- the part of each row whose sequence sees the whole prefix
-            const int at = g.row0 + t * 128 + r, b = at < all ? at / p.rows : 0;
+            const int at = g.row0 + t * 128 + r, b = at < all ? (int)p.per_row.div(at) : 0;
             const bool valid = at < all && min(max(p.lens[b], 0), cap) - p.Nq >= shared;
             const float inv = l == 0.f ? 0.f : 1.f / l;
             const long long place = (c + g.item) * p.tile_rows + t * 128 + r;
@@ -354,12 +391,15 @@ prefix_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
             for (int q4 = 0; q4 < D / 32; ++q4) {
                 uint32_t v[32];
                 tmem_ld32(lane_addr + col_o + q4 * 32, v);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * inv);
                 if (valid)
 #pragma unroll
-                    for (int i = 0; i < 32; i += 4)
-                        *reinterpret_cast<float4*>(dst + q4 * 32 + i) =
-                            make_float4(__uint_as_float(v[i]) * inv, __uint_as_float(v[i + 1]) * inv,
-                                        __uint_as_float(v[i + 2]) * inv, __uint_as_float(v[i + 3]) * inv);
+                    for (int i = 0; i < 32; i += 8)
+                        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + q4 * 32 + i), "r"(v[i]),
+                                     "r"(v[i + 1]), "r"(v[i + 2]), "r"(v[i + 3]), "r"(v[i + 4]), "r"(v[i + 5]), "r"(v[i + 6]),
+                                     "r"(v[i + 7])
+                                     : "memory");
             }
             if (valid) p.part_lse[place] = l == 0.f ? -INFINITY : m_use + lg2(l);
             tc_fence_before();
@@ -397,6 +437,7 @@ cudaError_t launch_d(const PrefixLaunch& a, cudaStream_t s) {
     p.tiles = a.tiles;
     p.tile_rows = a.tile_rows;
     p.box = a.box;
+    p.per_row = FastDiv((uint32_t)p.rows);
     p.scale_log2 = a.scale * 1.4426950408889634f;
     p.err = a.err;
     p.timeout_ns = a.timeout_ns;
