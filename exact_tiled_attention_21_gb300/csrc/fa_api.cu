@@ -822,33 +822,34 @@ SelectWorkspace select_workspace(int B, int Hkv, long long max_blocks) {
 }
 
 // Workspace of the bf16 row decode: partial outputs and LSEs of every segment (at most one more per CTA than there are
-// items), and the sequences' first steps.
+// items), and the first and last CTA of every item.
 struct RowsWorkspace {
-    size_t part_lse, prefix, bytes;
+    size_t part_lse, ends, bytes;
 };
 RowsWorkspace rows_workspace(int B, int Hq, int Hkv, int Nq, int d) {
     const int rows = Hq / Hkv * Nq, tile = rows_tile(rows);
-    const size_t slots = (size_t)kRowsMostWorkers + (size_t)B * Hkv * ((rows + tile - 1) / tile);
+    const size_t items = (size_t)B * Hkv * ((rows + tile - 1) / tile), slots = (size_t)kRowsMostWorkers + items;
     RowsWorkspace w;
     w.part_lse = align256(slots * tile * d * 4);
-    w.prefix = w.part_lse + align256(slots * tile * 4);
-    w.bytes = w.prefix + align256(((size_t)B + 1) * 8);
+    w.ends = w.part_lse + align256(slots * tile * 4);
+    w.bytes = w.ends + align256(items * 8);
     return w;
 }
 
 // Workspace of the shared prefix: the same of (kv head, tile of the batch's query rows) items.
 struct PrefixWorkspace {
     int tiles, tile_rows;
-    size_t part_lse, bytes;
+    size_t part_lse, ends, bytes;
 };
 PrefixWorkspace prefix_workspace(int B, int Hq, int Hkv, int Nq, int d) {
     const long long rows = (long long)B * (Hq / Hkv) * Nq;
     PrefixWorkspace w;
     w.tile_rows = rows <= 128 ? 128 : 256;
     w.tiles = (int)((rows + w.tile_rows - 1) / w.tile_rows);
-    const size_t slots = (size_t)kPrefixMostWorkers + (size_t)Hkv * w.tiles;
+    const size_t items = (size_t)Hkv * w.tiles, slots = (size_t)kPrefixMostWorkers + items;
     w.part_lse = align256(slots * w.tile_rows * d * 4);
-    w.bytes = w.part_lse + align256(slots * w.tile_rows * 4);
+    w.ends = w.part_lse + align256(slots * w.tile_rows * 4);
+    w.bytes = w.ends + align256(items * 8);
     return w;
 }
 
@@ -887,6 +888,7 @@ int rows_prepare(DecodeRowsLaunch& a, const void* q, const void* k_pages, const 
     a.o = o;
     a.lse = lse;
     a.pre_o = a.pre_lse = nullptr;
+    a.pre_ends = nullptr;
     a.B = B;
     a.Hq = Hq;
     a.Hkv = Hkv;
@@ -906,7 +908,7 @@ void rows_place(DecodeRowsLaunch& a, char* base) {
     const RowsWorkspace w = rows_workspace(a.B, a.Hq, a.Hkv, a.Nq, a.d);
     a.part_o = reinterpret_cast<float*>(base);
     a.part_lse = reinterpret_cast<float*>(base + w.part_lse);
-    a.prefix = reinterpret_cast<long long*>(base + w.prefix);
+    a.ends = reinterpret_cast<int*>(base + w.ends);
 }
 
 }  // namespace
@@ -1253,9 +1255,11 @@ int fa_decode_shared(const void* q, const void* k_pages, const void* v_pages, co
                           num_pages, d, scale);
     if (st != FA_OK) return st;
     if (page_size % 8) return FA_ERR_UNSUPPORTED;  // boxes of 8 rows at least
+    const PrefixWorkspace pw = prefix_workspace(B, Hq, Hkv, Nq, d);
+    const long long most = ((long long)max_pages * page_size + 127) / 128;  // steps of an item
+    if ((long long)Hkv * pw.tiles > 0x7FFFFFFFll / most) return FA_ERR_UNSUPPORTED;
     if (!aligned4(shared_len)) return FA_ERR_ALIGNMENT;
     const RowsWorkspace ws = rows_workspace(B, Hq, Hkv, Nq, d);
-    const PrefixWorkspace pw = prefix_workspace(B, Hq, Hkv, Nq, d);
     if (!workspace || workspace_bytes < ws.bytes + pw.bytes) return FA_ERR_WORKSPACE;
     if (!aligned16(workspace)) return FA_ERR_ALIGNMENT;
     char* base = static_cast<char*>(workspace);
@@ -1268,6 +1272,7 @@ int fa_decode_shared(const void* q, const void* k_pages, const void* v_pages, co
     p.shared = shared_len;
     p.part_o = reinterpret_cast<float*>(base);
     p.part_lse = reinterpret_cast<float*>(base + pw.part_lse);
+    p.ends = reinterpret_cast<int*>(base + pw.ends);
     p.B = B;
     p.Hq = Hq;
     p.Hkv = Hkv;
@@ -1279,8 +1284,7 @@ int fa_decode_shared(const void* q, const void* k_pages, const void* v_pages, co
     p.d = d;
     p.tiles = pw.tiles;
     p.tile_rows = pw.tile_rows;
-    const long long steps = ((long long)max_pages * page_size + 127) / 128 * Hkv * pw.tiles;  // no more CTAs than at most
-    p.workers = (int)std::min<long long>(std::min(a.num_sms, kPrefixMostWorkers), steps);
+    p.workers = (int)std::min<long long>(std::min(a.num_sms, kPrefixMostWorkers), most * Hkv * pw.tiles);  // a step each
     p.scale = scale;
     p.err = a.err;
     p.timeout_ns = g_timeout_ns.load();
@@ -1292,6 +1296,7 @@ int fa_decode_shared(const void* q, const void* k_pages, const void* v_pages, co
     a.shared = shared_len;
     a.pre_o = p.part_o;
     a.pre_lse = p.part_lse;
+    a.pre_ends = p.ends;
     a.pre_workers = p.workers;
     a.pre_tiles = p.tiles;
     a.pre_rows = p.tile_rows;

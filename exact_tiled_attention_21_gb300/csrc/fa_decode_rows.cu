@@ -94,12 +94,13 @@ struct Params {
     float* lse;
     float* part_o;          // [slot][ROWS][D], normalised
     float* part_lse;        // [slot][ROWS], log2
-    long long* prefix;      // [B + 1] steps before each sequence, per (kv head, row tile)
-    const float* pre_o;     // the shared prefix's parts: [slot][pre_rows][D] and [slot][pre_rows]
+    int* ends;              // [item][2]: the CTAs of its first and last step
+    const float* pre_o;     // the shared prefix's parts: [slot][pre_rows][D] and [slot][pre_rows], and ends as above
     const float* pre_lse;
+    const int* pre_ends;
     int B, Hkv, Nq, max_pages, num_pages, rows, row_tiles, workers, keep;
-    int pre_workers, pre_tiles, pre_rows;
-    FastDiv page, block;
+    int pre_tiles, pre_rows;
+    FastDiv page, block, per_row, heads;  // rows, Hkv
     float scale_log2;
     DevError* err;
 };
@@ -117,37 +118,19 @@ __device__ __forceinline__ int keys_of(const Params& a, int len, int shared) {
     return len - shared_of(shared, len, a.Nq);
 }
 
-// Steps of all sequences before q (64-bit warp scan of the lengths): the sequence that step q falls in, its first step
-// and length.  With q beyond the end: sequence B and the total.  prefix: also written, if not null.
+// Steps of all sequences in 32 bits: this lane's sequence b0 + lane has n of them (one scan of a warp's worth of lengths).
 template <int STEP, bool LIST>
-__device__ __forceinline__ void find_sequence(const Params& a, int cap, int shared, long long q, long long* prefix, int& b,
-                                              long long& start, int& len) {
+__device__ __forceinline__ uint32_t steps_before(const Params& a, int cap, int shared, int b0, int& len, uint32_t& n) {
     const int lane = threadIdx.x & 31;
-    long long base = 0;
-    b = a.B;
-    for (int b0 = 0; b0 < a.B; b0 += 32) {
-        const int l = b0 + lane < a.B ? clamp_len(a.lens[b0 + lane], cap) : 0;
-        const uint32_t n = (uint32_t)(keys_of<LIST>(a, l, shared) + STEP - 1) / STEP;
-        uint32_t incl = n;
+    len = b0 + lane < a.B ? clamp_len(a.lens[b0 + lane], cap) : 0;
+    n = (uint32_t)(keys_of<LIST>(a, len, shared) + STEP - 1) / STEP;
+    uint32_t incl = n;
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const uint32_t up = __shfl_up_sync(0xffffffffu, incl, d);
-            if (lane >= d) incl += up;
-        }
-        if (prefix && b0 + lane < a.B) prefix[b0 + lane] = base + incl - n;
-        const uint32_t hit = __ballot_sync(0xffffffffu, base + incl > q);
-        if (hit) {
-            const int f = __ffs(hit) - 1;
-            b = b0 + f;
-            len = __shfl_sync(0xffffffffu, l, f);
-            start = base + __shfl_sync(0xffffffffu, incl - n, f);
-            return;
-        }
-        base += __shfl_sync(0xffffffffu, incl, 31);
+    for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t up = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += up;
     }
-    start = base;
-    len = 0;
-    if (prefix && lane == 0) prefix[a.B] = base;
+    return incl;
 }
 
 // A position in the list of steps.
@@ -195,26 +178,38 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, ROWS>::CTAS) decode_rows_kern
         if (given != shared && tid == 0) record_invalid(a.err, kSiteCacheLen, given);
     }
     // ---- this CTA's share of the steps: `count` of them from `cur`
-    const long long per_step = (long long)a.Hkv * a.row_tiles;
+    const uint32_t per_step = (uint32_t)a.Hkv * a.row_tiles;
     Cursor cur;
     int count;
     {
-        int b, len;
-        long long total, start;
-        find_sequence<STEP, LIST>(a, cap, shared, LLONG_MAX, blockIdx.x == 0 && warp == 0 ? a.prefix : nullptr, b, total, len);
-        total *= per_step;
-        const long long workers = min((long long)a.workers, total);  // at least one step each
-        if (blockIdx.x >= workers) return;
-        const long long u = blockIdx.x * total / workers;
-        count = (int)((blockIdx.x + 1ll) * total / workers - u);
-        find_sequence<STEP, LIST>(a, cap, shared, u / per_step, nullptr, cur.b, start, cur.len);
+        int len;
+        uint32_t n, incl = steps_before<STEP, LIST>(a, cap, shared, 0, len, n), total = __shfl_sync(0xffffffffu, incl, 31);
+        for (int b0 = 32; b0 < a.B; b0 += 32) {
+            int l;
+            uint32_t k;
+            total += __shfl_sync(0xffffffffu, steps_before<STEP, LIST>(a, cap, shared, b0, l, k), 31);
+        }
+        const Share mine = share_of(total * per_step, a.workers, blockIdx.x);
+        if (mine.count == 0) return;
+        count = (int)mine.count;
+        const uint32_t q = mine.first / per_step;  // the sequence whose steps, over one kv head and row tile, hold this
+        uint32_t base = 0, hit;
+        int b0 = 0;
+        while (!(hit = __ballot_sync(0xffffffffu, base + incl > q))) {
+            base += __shfl_sync(0xffffffffu, incl, 31);
+            b0 += 32;
+            incl = steps_before<STEP, LIST>(a, cap, shared, b0, len, n);
+        }
+        const int f = __ffs(hit) - 1;
+        cur.b = b0 + f;
+        cur.len = __shfl_sync(0xffffffffu, len, f);
+        cur.n = (int)__shfl_sync(0xffffffffu, n, f);
         cur.keys = keys_of<LIST>(a, cur.len, shared);
-        cur.n = (cur.keys + STEP - 1) / STEP;
-        const long long in_b = u - start * per_step;
-        const int item_b = (int)(in_b / cur.n);
-        cur.s = (int)(in_b - (long long)item_b * cur.n);
-        cur.kvh = item_b / a.row_tiles;
-        cur.rt = item_b - cur.kvh * a.row_tiles;
+        const uint32_t in_b = mine.first - (base + __shfl_sync(0xffffffffu, incl - n, f)) * per_step;
+        const uint32_t item_b = in_b / (uint32_t)cur.n;
+        cur.s = (int)(in_b - item_b * cur.n);
+        cur.kvh = (int)(item_b / (uint32_t)a.row_tiles);
+        cur.rt = (int)item_b - cur.kvh * a.row_tiles;
     }
 
     // ---- the ring: this warp's keys of the steps ahead, whatever item they are of.  A key's row is D / 8 pieces of 16
@@ -349,7 +344,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, ROWS>::CTAS) decode_rows_kern
         const long long bh = (long long)cur.b * a.Hkv + cur.kvh;
         if (begins) {
             seg = cur.s;
-            if (it > 0) load_q();
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
@@ -367,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, ROWS>::CTAS) decode_rows_kern
         // A value product multiplies a key's V by the zero weights of the rows that do not see it, and 0 x infinity is NaN.
         // Where some rows see a key and others do not (the last Nq - 1 tokens), infinities and NaN are added to the sums of
         // the rows that do, and become zeros in the stage.
-        if (DRAFTS) {
+        if (DRAFTS && (LIST || (cur.s + 1) * STEP > cur.keys - Nq + 1)) {
             uint8_t* group = smem + kg * RG * C::RING + slot * C::SLOT;  // of key part * KEYS + k: + part * RING
             auto tok_of = [&](int key) {
                 return reinterpret_cast<const int*>(group + key / KEYS * C::RING + 2 * C::HALF)[key % KEYS];
@@ -426,29 +420,31 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, ROWS>::CTAS) decode_rows_kern
             const uint8_t* st = smem + (kg * RG + part) * C::RING + slot * C::SLOT;
             const uint32_t st_u = smem_u32(st);
             float S[NB][MT][4];  // keys 16 i + g, + 8 (c / 2) of rows 2 t + c % 2
+            {
+                float T[NB][MT][2][4] = {};  // two chains of products, which wait for each other half as often
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
+                for (int s = 0; s < KS; ++s)
 #pragma unroll
-                for (int i = 0; i < MT; ++i) S[nb][i][0] = S[nb][i][1] = S[nb][i][2] = S[nb][i][3] = 0.f;
+                    for (int i = 0; i < MT; ++i) {
+                        uint32_t ka[4];
+                        ldmatrix4(ka, st_u + (i * 16 + kr) * (D * 2) + (((2 * s + kc) ^ (kr & 7)) << 4));
 #pragma unroll
-            for (int s = 0; s < KS; ++s)
+                        for (int nb = 0; nb < NB; ++nb) mma_bf16(T[nb][i][s & 1], ka, qb[nb][s][0], qb[nb][s][1]);
+                    }
 #pragma unroll
-                for (int i = 0; i < MT; ++i) {
-                    uint32_t ka[4];
-                    ldmatrix4(ka, st_u + (i * 16 + kr) * (D * 2) + (((2 * s + kc) ^ (kr & 7)) << 4));
+                for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                    for (int nb = 0; nb < NB; ++nb) mma_bf16(S[nb][i], ka, qb[nb][s][0], qb[nb][s][1]);
-                }
+                    for (int i = 0; i < MT; ++i)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) S[nb][i][c] = (T[nb][i][0][c] + T[nb][i][1][c]) * a.scale_log2;
+            }
             const int* toks = reinterpret_cast<const int*>(st + 2 * C::HALF);
-            const bool masked = __any_sync(0xffffffffu, toks[lane % KEYS] > sees_all);
+            const bool masked = (LIST || (cur.s + 1) * STEP > cur.keys - Nq + 1) &&
+                                __any_sync(0xffffffffu, toks[lane % KEYS] > sees_all);
             uint32_t pb[NB][MT][2], pl[NB][MT][2];
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
                 auto& x = S[nb];
-#pragma unroll
-                for (int i = 0; i < MT; ++i)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) x[i][c] *= a.scale_log2;
                 if (masked) {
 #pragma unroll
                     for (int i = 0; i < MT; ++i)
@@ -516,7 +512,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, ROWS>::CTAS) decode_rows_kern
         // ---- at the segment's end: O = sum over the warps with these rows of O_w 2^(m_w - m) / l
         const bool item_ends = cur.s + 1 == cur.n;
         begins = item_ends || it + 1 == count;
+        const Cursor done = cur;
+        if (it + 1 < count) advance<STEP, LIST>(cur, a, cap, shared);
         if (begins) {
+            if (it + 1 < count) load_q();  // the next segment's queries come while this one's parts are joined
             float f[NB][2];
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
@@ -571,8 +570,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, ROWS>::CTAS) decode_rows_kern
                 if (nb + 1 < NB) __syncthreads();
             }
             if (kg == 0) {
-                const bool whole = seg == 0 && item_ends && (LIST || shared_of(shared, cur.len, Nq) == 0);
-                const long long slot_out = blockIdx.x + bh * a.row_tiles + cur.rt;
+                const bool whole = seg == 0 && item_ends && (LIST || shared_of(shared, done.len, Nq) == 0);
+                const long long item = bh * a.row_tiles + done.rt, slot_out = blockIdx.x + item;
+                if (tid == 0 && seg == 0) a.ends[2 * item] = blockIdx.x;
+                if (tid == 0 && item_ends) a.ends[2 * item + 1] = blockIdx.x;
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -581,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, ROWS>::CTAS) decode_rows_kern
                         if (r >= nrows) continue;
                         const float sum = l[nb][j], lse2 = sum == 0.f ? -INFINITY : m[nb][j] + lg2(sum);
                         if (whole) {
-                            const long long row = bh * a.rows + cur.rt * ROWS + r;  // (b, head, token) flattened
+                            const long long row = bh * a.rows + done.rt * ROWS + r;  // (b, head, token) flattened
                             __nv_bfloat16* dst = a.o + row * D + g;
 #pragma unroll
                             for (int i = 0; i < D / 16; ++i) {
@@ -602,7 +603,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, ROWS>::CTAS) decode_rows_kern
             }
             __syncthreads();  // the statistics and buffers are read
         }
-        if (it + 1 < count) advance<STEP, LIST>(cur, a, cap, shared);
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     if (__any_sync(0xffffffffu, bad) && lane == 0) record_invalid(a.err, kSiteCacheTable, -1);
@@ -616,31 +616,27 @@ struct Parts {
     bool done;  // written already
 };
 
-// The segments of item i (sequence b, kv head, row tile) are those of the CTAs that hold its first to its last step;
-// CTA c's is in slot c + i.
+// An item's segments are those of the CTAs from that of its first to that of its last step; CTA c's is in slot c + item.
 template <bool LIST>
 __device__ __forceinline__ Parts find_parts(const Params& a, int b, int kvh, int rt, int row) {
-    const long long per_step = (long long)a.Hkv * a.row_tiles;
-    const int item_b = kvh * a.row_tiles + rt;
-    const long long p0 = a.prefix[b], n = a.prefix[b + 1] - p0, total = a.prefix[a.B] * per_step;
-    Parts x{0, 0, 0, 0, false};
-    if (n > 0) {
-        const long long s0 = p0 * per_step + item_b * n, s1 = s0 + n - 1;  // first and last step
-        const long long workers = min((long long)a.workers, total);
-        const long long c0 = ((s0 + 1) * workers - 1) / total, c1 = ((s1 + 1) * workers - 1) / total;
-        x.slot = c0 + b * per_step + item_b;
-        x.n = (int)(c1 - c0) + 1;
-    }
+    const int item = (b * a.Hkv + kvh) * a.row_tiles + rt, cap = a.max_pages * (int)a.page.d;
+    int shared = 0, place = 0;
+    int2 pre = make_int2(0, -1);
     if constexpr (!LIST) {
-        const int cap = a.max_pages * (int)a.page.d, shared = clamp_len(*a.shared, cap);
-        if (shared_of(shared, clamp_len(a.lens[b], cap), a.Nq) > 0) {
-            const PrefixShare w = prefix_share(shared, a.Hkv, a.pre_tiles, a.pre_workers);
-            const int item = kvh * a.pre_tiles + (int)(((long long)b * a.rows + row) / a.pre_rows);
-            const long long s0 = (long long)item * w.steps, s1 = s0 + w.steps - 1;
-            const long long c0 = ((s0 + 1) * w.workers - 1) / w.total, c1 = ((s1 + 1) * w.workers - 1) / w.total;
-            x.pslot = c0 + item;
-            x.pn = (int)(c1 - c0) + 1;
-        }
+        shared = clamp_len(*a.shared, cap);
+        place = (b * a.rows + row) / a.pre_rows;
+        pre = reinterpret_cast<const int2*>(a.pre_ends)[kvh * a.pre_tiles + place];
+    }
+    const int2 own = reinterpret_cast<const int2*>(a.ends)[item];
+    const int len = clamp_len(a.lens[b], cap);
+    Parts x{0, 0, 0, 0, false};
+    if (keys_of<LIST>(a, len, shared) > 0) {
+        x.slot = (long long)own.x + item;
+        x.n = own.y - own.x + 1;
+    }
+    if (!LIST && shared_of(shared, len, a.Nq) > 0) {
+        x.pslot = pre.x + kvh * a.pre_tiles + place;
+        x.pn = pre.y - pre.x + 1;
     }
     x.done = x.n == 1 && x.pn == 0;
     return x;
@@ -657,11 +653,11 @@ __global__ void __launch_bounds__(THREADS) merge_rows_kernel(const Params a) {
     const int tid = threadIdx.x, grp = tid / LANES, col = tid % LANES;
     const long long all = (long long)a.B * a.Hkv * a.rows, row = SPLIT ? blockIdx.x : (long long)blockIdx.x * GROUPS + grp;
     if (row >= all) return;
-    const long long bh = row / a.rows;
-    const int r = (int)(row - bh * a.rows), b = (int)(bh / a.Hkv), kvh = (int)(bh - (long long)b * a.Hkv), rt = r / ROWS;
+    const int bh = (int)a.per_row.div((uint32_t)row), r = (int)row - bh * a.rows, b = (int)a.heads.div(bh),
+              kvh = bh - b * a.Hkv, rt = r / ROWS;
     const Parts x = find_parts<LIST>(a, b, kvh, rt, r);
     if (x.done) return;
-    const int n = x.n + x.pn, prow = LIST ? 0 : (int)(((long long)b * a.rows + r) % a.pre_rows);
+    const int n = x.n + x.pn, prow = LIST ? 0 : (b * a.rows + r) % a.pre_rows;
     auto lse_at = [&](int s) {
         return s < x.n ? a.part_lse[(x.slot + s) * ROWS + (r - rt * ROWS)]
                        : a.pre_lse[(x.pslot + s - x.n) * a.pre_rows + prow];
@@ -735,7 +731,7 @@ template <int D, int ROWS, bool LIST>
 cudaError_t launch_merge(const DecodeRowsLaunch& a, const Params& p, cudaStream_t s) {
     const long long rows = (long long)a.B * a.Hkv * p.rows;
     // rows alone in a block where there are few of them: their parts are read by more threads
-    const long long parts = LIST ? p.workers / ((long long)a.B * a.Hkv * p.row_tiles) : p.pre_workers / ((long long)a.Hkv * p.pre_tiles);
+    const long long parts = LIST ? p.workers / ((long long)a.B * a.Hkv * p.row_tiles) : a.pre_workers / ((long long)a.Hkv * p.pre_tiles);
     if (rows <= (parts >= 4 ? 16ll : 4ll) * a.num_sms)
         return launch_dependent(merge_rows_kernel<D, ROWS, LIST, true, 256>, dim3((unsigned)rows), dim3(256), 0, s, p);
     constexpr int PER = 128 / (D / 4);
@@ -761,7 +757,8 @@ cudaError_t launch_l(const DecodeRowsLaunch& a, cudaStream_t s) {
     p.lse = a.lse;
     p.part_o = a.part_o;
     p.part_lse = a.part_lse;
-    p.prefix = a.prefix;
+    p.ends = a.ends;
+    p.pre_ends = a.pre_ends;
     p.pre_o = a.pre_o;
     p.pre_lse = a.pre_lse;
     p.B = a.B;
@@ -771,8 +768,9 @@ cudaError_t launch_l(const DecodeRowsLaunch& a, cudaStream_t s) {
     p.num_pages = a.num_pages;
     p.rows = a.Hq / a.Hkv * a.Nq;
     p.row_tiles = (p.rows + ROWS - 1) / ROWS;
+    p.per_row = FastDiv((uint32_t)p.rows);
+    p.heads = FastDiv((uint32_t)a.Hkv);
     p.keep = a.keep;
-    p.pre_workers = a.pre_workers;
     p.pre_tiles = a.pre_tiles;
     p.pre_rows = a.pre_rows;
     p.page = FastDiv((uint32_t)a.page);

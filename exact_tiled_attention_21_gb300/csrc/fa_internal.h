@@ -261,18 +261,17 @@ struct SelectLaunch {
     DevError* err;
 };
 
-// The shares of a shared prefix's steps of 128 keys over (kv head, tile of query rows): `total` of them for `workers` CTAs,
-// of which CTA c takes those from c total / workers on.
-struct PrefixShare {
-    int steps;  // of a (kv head, tile)
-    long long total, workers;
+// `total` steps dealt out to CTAs in runs that differ by one at most: CTA c takes `count` steps from `first` on.  Fewer than
+// 2^31 steps, so that the divisions are 32-bit ones (64-bit ones cost a start of a microsecond and a half).
+struct Share {
+    uint32_t first, count;
 };
-__host__ __device__ inline PrefixShare prefix_share(int shared, int Hkv, int tiles, int ctas) {
-    PrefixShare w;
-    w.steps = (shared + 127) / 128;
-    w.total = (long long)Hkv * tiles * w.steps;
-    w.workers = ctas < w.total ? ctas : w.total;
-    return w;
+__host__ __device__ inline Share share_of(uint32_t total, uint32_t ctas, uint32_t c) {
+    const uint32_t n = total / ctas, more = total - n * ctas;
+    Share s;
+    s.first = c * n + (c < more ? c : more);
+    s.count = n + (c < more ? 1u : 0u);
+    return s;
 }
 
 struct PrefixLaunch {
@@ -283,6 +282,7 @@ struct PrefixLaunch {
     const int* shared;         // int32 [1]
     float* part_o;             // fp32 [workers + Hkv * tiles, tile_rows, d]
     float* part_lse;           // fp32 [workers + Hkv * tiles, tile_rows]
+    int* ends;                 // int32 [Hkv * tiles, 2]: the CTAs of an item's first and last step
     int B, Hq, Hkv, Nq, page, box, max_pages, num_pages, d, tiles, tile_rows, workers;
     float scale;
     DevError* err;
@@ -301,9 +301,10 @@ struct DecodeRowsLaunch {
     float* lse;            // fp32 [B, Hq, Nq], or null
     float* part_o;         // fp32 [workers + items, tile rows, d]
     float* part_lse;       // fp32 [workers + items, tile rows]
-    long long* prefix;     // [B + 1]
+    int* ends;             // int32 [items, 2]: the CTAs of an item's first and last step
     const float* pre_o;    // the shared prefix's parts (PrefixLaunch), with `shared`
     const float* pre_lse;
+    const int* pre_ends;
     int B, Hq, Hkv, Nq, page, block, keep, max_pages, num_pages, d;
     int pre_workers, pre_tiles, pre_rows;
     int num_sms;

@@ -52,6 +52,7 @@ struct PreParams {
     const int* shared;  // [1]
     float* part_o;      // [slot][tile_rows][D]
     float* part_lse;    // [slot][tile_rows], log2
+    int* ends;          // [item][2]: the CTAs of its first and last step
     int B, Hkv, Nq, rows, page, max_pages, num_pages, tiles, tile_rows, box;
     FastDiv per_row;  // rows
     float scale_log2;
@@ -105,21 +106,20 @@ prefix_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
         const uint32_t hit = __ballot_sync(0xffffffffu, b0 + lane < p.B && min(max(p.lens[min(b0 + lane, p.B - 1)], 0), cap) - p.Nq >= shared);
         if (hit) from = b0 + __ffs(hit) - 1;
     }
-    const PrefixShare w = prefix_share(shared, p.Hkv, p.tiles, gridDim.x);
-    const long long c = blockIdx.x;
-    const bool some = from >= 0 && c < w.workers;
-    const long long u0 = some ? c * w.total / w.workers : 0, u1 = some ? (c + 1) * w.total / w.workers : 0;
+    const uint32_t steps = (uint32_t)(shared + 127) / 128;  // of an item, a (kv head, tile of rows)
+    const Share mine = share_of(from >= 0 ? steps * p.Hkv * p.tiles : 0, gridDim.x, blockIdx.x);
+    const uint32_t u0 = mine.first, u1 = u0 + mine.count, c = blockIdx.x;
     const int all = p.B * p.rows;  // rows of a kv head
     // one role's walk over the CTA's segments: item, its steps [s0, s1)
     struct Segment {
         int item, kvh, row0, s0, s1;
         bool two;  // more than 128 rows
     };
-    auto segment_at = [&](long long u) {
+    auto segment_at = [&](uint32_t u) {
         Segment g;
-        g.item = (int)(u / w.steps);
-        g.s0 = (int)(u - (long long)g.item * w.steps);
-        g.s1 = (int)min((long long)w.steps, g.s0 + (u1 - u));
+        g.item = (int)(u / steps);
+        g.s0 = (int)(u - g.item * steps);
+        g.s1 = (int)min(steps, g.s0 + (u1 - u));
         g.kvh = g.item / p.tiles;
         g.row0 = (g.item - g.kvh * p.tiles) * p.tile_rows;
         g.two = min(p.tile_rows, all - g.row0) > 128;
@@ -147,12 +147,12 @@ prefix_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
             const Segment g = segment_at(u0);
             pg_next = page_of(g, g.s0);
         }
-        for (long long u = u0; u < u1 && ok;) {
+        for (uint32_t u = u0; u < u1 && ok;) {
             const Segment g = segment_at(u);
             for (int s = g.s0; s < g.s1 && ok; ++s, ++u) {
                 const int nk = min(128, shared - s * 128), nbox = (nk + R - 1) / R;
                 int pg = pg_next;
-                if (u + 1 < u1) pg_next = page_of(g, s + 1 < w.steps ? s + 1 : 0);
+                if (u + 1 < u1) pg_next = page_of(g, s + 1 < (int)steps ? s + 1 : 0);
                 const int key = s * 128 + lane * R, row = key - key / p.page * p.page;
                 if (lane < nbox && (unsigned)pg >= (unsigned)p.num_pages) {
                     record_invalid(p.err, kSitePagedTable, pg);
@@ -212,7 +212,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
             };
             auto kv_at = [&](int s) { return s_base + C::OFF_KV + s * C::KV_BYTES; };
             bool ok = true;
-            for (long long u = u0; u < u1 && ok;) {
+            for (uint32_t u = u0; u < u1 && ok;) {
                 const Segment g = segment_at(u);
                 if (!mbar_wait(BAR_Q, q_iter++ & 1, ctl, kSiteQFull)) break;
                 if (g.two && !mbar_wait(BAR_Q + 8, q1_iter++ & 1, ctl, kSiteQFull)) break;
@@ -294,7 +294,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
         const uint32_t col_o = C::COL_O + D * t;
         // handoffs before the segment: of the scores' buffers, of the products of one tile, of the ring's fills; of O so far
         uint32_t s_next0 = 0, s_next1 = 0, pv_next = 0, kv_fill = 0, o_iter = 0;
-        for (long long u = u0; u < u1;) {
+        for (uint32_t u = u0; u < u1;) {
             const Segment g = segment_at(u);
             const int nst = g.s1 - g.s0;
             u += nst;
@@ -385,7 +385,9 @@ prefix_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
             const int at = g.row0 + t * 128 + r, b = at < all ? (int)p.per_row.div(at) : 0;
             const bool valid = at < all && min(max(p.lens[b], 0), cap) - p.Nq >= shared;
             const float inv = l == 0.f ? 0.f : 1.f / l;
-            const long long place = (c + g.item) * p.tile_rows + t * 128 + r;
+            const long long place = (long long)(c + g.item) * p.tile_rows + t * 128 + r;
+            if (tid == 0 && g.s0 == 0) p.ends[2 * g.item] = c;
+            if (tid == 0 && g.s1 == (int)steps) p.ends[2 * g.item + 1] = c;
             float* dst = p.part_o + place * D;
 #pragma unroll 1
             for (int q4 = 0; q4 < D / 32; ++q4) {
@@ -427,6 +429,7 @@ cudaError_t launch_d(const PrefixLaunch& a, cudaStream_t s) {
     p.shared = a.shared;
     p.part_o = a.part_o;
     p.part_lse = a.part_lse;
+    p.ends = a.ends;
     p.B = a.B;
     p.Hkv = a.Hkv;
     p.Nq = a.Nq;
