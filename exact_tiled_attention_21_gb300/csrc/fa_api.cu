@@ -868,9 +868,9 @@ int rows_prepare(DecodeRowsLaunch& a, const void* q, const void* k_pages, const 
     if (st != FA_OK) return st;
     if (Hq % Hkv) return FA_ERR_INVALID_ARG;
     if (!rows_sizes_ok(B, Hq, Hkv, Nq, d)) return FA_ERR_UNSUPPORTED;
-    // steps of 64 keys over all sequences, kv heads and row tiles are counted in 32 bits per CTA
+    // steps of 64 keys over all sequences, kv heads and row tiles, and two more for each of these, are counted in 31 bits
     const int rows = Hq / Hkv * Nq, tile = rows_tile(rows);
-    if ((long long)B * Hkv * ((rows + tile - 1) / tile) > 0x7FFFFFFFll / (((long long)max_pages * page_size + block + 63) / 64))
+    if ((long long)B * Hkv * ((rows + tile - 1) / tile) > 0x7FFFFFFFll / (((long long)max_pages * page_size + block + 63) / 64 + 2))
         return FA_ERR_UNSUPPORTED;
     if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(o) || !aligned4(block_table) ||
         !aligned4(seq_lens) || !aligned4(lse))

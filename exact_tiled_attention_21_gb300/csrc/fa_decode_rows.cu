@@ -118,19 +118,30 @@ __device__ __forceinline__ int keys_of(const Params& a, int len, int shared) {
     return len - shared_of(shared, len, a.Nq);
 }
 
-// Steps of all sequences in 32 bits: this lane's sequence b0 + lane has n of them (one scan of a warp's worth of lengths).
+// What an item costs besides its steps, in steps: its queries, and joining its parts (64 sequences of 2 to 1000 own tokens, 8
+// kv heads: the CTAs that got the shortest ones took 53 us, the others 25).
+constexpr uint32_t kItemCost = 1;
+
+// A warp's worth of sequences from b0 on: a lane's length, steps (of each of its items) and the sums up to it, of costs and
+// of steps.
+struct Scan {
+    int len;
+    uint32_t n, cost, steps;
+};
 template <int STEP, bool LIST>
-__device__ __forceinline__ uint32_t steps_before(const Params& a, int cap, int shared, int b0, int& len, uint32_t& n) {
+__device__ __forceinline__ Scan scan_at(const Params& a, int cap, int shared, int b0) {
     const int lane = threadIdx.x & 31;
-    len = b0 + lane < a.B ? clamp_len(a.lens[b0 + lane], cap) : 0;
-    n = (uint32_t)(keys_of<LIST>(a, len, shared) + STEP - 1) / STEP;
-    uint32_t incl = n;
+    Scan x;
+    x.len = b0 + lane < a.B ? clamp_len(a.lens[b0 + lane], cap) : 0;
+    x.n = (uint32_t)(keys_of<LIST>(a, x.len, shared) + STEP - 1) / STEP;
+    x.steps = x.n;
+    x.cost = x.n ? x.n + kItemCost : 0;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const uint32_t up = __shfl_up_sync(0xffffffffu, incl, d);
-        if (lane >= d) incl += up;
+        const uint32_t s = __shfl_up_sync(0xffffffffu, x.steps, d), c = __shfl_up_sync(0xffffffffu, x.cost, d);
+        if (lane >= d) x.steps += s, x.cost += c;
     }
-    return incl;
+    return x;
 }
 
 // A position in the list of steps.
@@ -182,34 +193,42 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, ROWS>::CTAS) decode_rows_kern
     Cursor cur;
     int count;
     {
-        int len;
-        uint32_t n, incl = steps_before<STEP, LIST>(a, cap, shared, 0, len, n), total = __shfl_sync(0xffffffffu, incl, 31);
-        for (int b0 = 32; b0 < a.B; b0 += 32) {
-            int l;
-            uint32_t k;
-            total += __shfl_sync(0xffffffffu, steps_before<STEP, LIST>(a, cap, shared, b0, l, k), 31);
-        }
+        const Scan head = scan_at<STEP, LIST>(a, cap, shared, 0);
+        uint32_t total = __shfl_sync(0xffffffffu, head.cost, 31);
+        for (int b0 = 32; b0 < a.B; b0 += 32) total += __shfl_sync(0xffffffffu, scan_at<STEP, LIST>(a, cap, shared, b0).cost, 31);
         const Share mine = share_of(total * per_step, a.workers, blockIdx.x);
-        if (mine.count == 0) return;
-        count = (int)mine.count;
-        const uint32_t q = mine.first / per_step;  // the sequence whose steps, over one kv head and row tile, hold this
-        uint32_t base = 0, hit;
-        int b0 = 0;
-        while (!(hit = __ballot_sync(0xffffffffu, base + incl > q))) {
-            base += __shfl_sync(0xffffffffu, incl, 31);
-            b0 += 32;
-            incl = steps_before<STEP, LIST>(a, cap, shared, b0, len, n);
-        }
-        const int f = __ffs(hit) - 1;
-        cur.b = b0 + f;
-        cur.len = __shfl_sync(0xffffffffu, len, f);
-        cur.n = (int)__shfl_sync(0xffffffffu, n, f);
+        // the steps before a place in the list of costs, and the item and step there
+        auto steps_before = [&](uint32_t at, Cursor& c) -> uint32_t {
+            const uint32_t q = at / per_step;  // the sequence whose costs, of one item each, hold this
+            uint32_t cost = 0, steps = 0, hit;
+            Scan x = head;
+            int b0 = 0;
+            while (!(hit = __ballot_sync(0xffffffffu, cost + x.cost > q))) {
+                cost += __shfl_sync(0xffffffffu, x.cost, 31);
+                steps += __shfl_sync(0xffffffffu, x.steps, 31);
+                b0 += 32;
+                if (b0 >= a.B) return steps * per_step;  // the end
+                x = scan_at<STEP, LIST>(a, cap, shared, b0);
+            }
+            const int f = __ffs(hit) - 1;
+            c.b = b0 + f;
+            c.len = __shfl_sync(0xffffffffu, x.len, f);
+            const uint32_t n = __shfl_sync(0xffffffffu, x.n, f);
+            cost += __shfl_sync(0xffffffffu, x.cost, f) - (n + kItemCost);
+            steps += __shfl_sync(0xffffffffu, x.steps, f) - n;
+            const uint32_t in_b = at - cost * per_step, item = in_b / (n + kItemCost), off = in_b - item * (n + kItemCost),
+                           s = off < kItemCost ? 0 : off - kItemCost;
+            c.n = (int)n;
+            c.s = (int)s;
+            c.kvh = (int)(item / (uint32_t)a.row_tiles);
+            c.rt = (int)item - c.kvh * a.row_tiles;
+            return steps * per_step + item * n + s;
+        };
+        const uint32_t first = steps_before(mine.first, cur);
+        Cursor end;
+        count = (int)(steps_before(mine.first + mine.count, end) - first);
+        if (count == 0) return;
         cur.keys = keys_of<LIST>(a, cur.len, shared);
-        const uint32_t in_b = mine.first - (base + __shfl_sync(0xffffffffu, incl - n, f)) * per_step;
-        const uint32_t item_b = in_b / (uint32_t)cur.n;
-        cur.s = (int)(in_b - item_b * cur.n);
-        cur.kvh = (int)(item_b / (uint32_t)a.row_tiles);
-        cur.rt = (int)item_b - cur.kvh * a.row_tiles;
     }
 
     // ---- the ring: this warp's keys of the steps ahead, whatever item they are of.  A key's row is D / 8 pieces of 16
