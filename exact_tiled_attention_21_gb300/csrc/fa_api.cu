@@ -826,9 +826,9 @@ SelectWorkspace select_workspace(int B, int Hkv, long long max_blocks) {
 struct RowsWorkspace {
     size_t part_lse, ends, bytes;
 };
-RowsWorkspace rows_workspace(int B, int Hq, int Hkv, int Nq, int d) {
-    const int rows = Hq / Hkv * Nq, tile = rows_tile(rows);
-    const size_t items = (size_t)B * Hkv * ((rows + tile - 1) / tile), slots = (size_t)kRowsMostWorkers + items;
+RowsWorkspace rows_workspace(int B, int Hq, int Hkv, int Nq, int d, int joint = 0) {
+    const int rows = Hq / Hkv * Nq, tile = rows_tile(joint ? joint : rows);
+    const size_t items = ((size_t)B + (joint > 0)) * Hkv * ((rows + tile - 1) / tile), slots = (size_t)kRowsMostWorkers + items;
     RowsWorkspace w;
     w.part_lse = align256(slots * tile * d * 4);
     w.ends = w.part_lse + align256(slots * tile * 4);
@@ -853,6 +853,12 @@ PrefixWorkspace prefix_workspace(int B, int Hq, int Hkv, int Nq, int d) {
     return w;
 }
 
+// Query rows of all sequences where decode_rows takes the prefix too, 0 where it does not.
+int joint_rows(int B, int Hq, int Hkv, int Nq) {
+    const long long rows = (long long)B * (Hq / Hkv) * Nq;
+    return rows <= kRowsJoint ? (int)rows : 0;
+}
+
 bool rows_sizes_ok(int B, int Hq, int Hkv, int Nq, int d) {
     return B >= 1 && Hq >= 1 && Hkv >= 1 && Hq % Hkv == 0 && Nq >= 1 && Nq <= 16 && (d == 64 || d == 128) &&
            (long long)B * Hq <= (1ll << 24);
@@ -870,7 +876,7 @@ int rows_prepare(DecodeRowsLaunch& a, const void* q, const void* k_pages, const 
     if (!rows_sizes_ok(B, Hq, Hkv, Nq, d)) return FA_ERR_UNSUPPORTED;
     // steps of 64 keys over all sequences, kv heads and row tiles, and two more for each of these, are counted in 31 bits
     const int rows = Hq / Hkv * Nq, tile = rows_tile(rows);
-    if ((long long)B * Hkv * ((rows + tile - 1) / tile) > 0x7FFFFFFFll / (((long long)max_pages * page_size + block + 63) / 64 + 2))
+    if (((long long)B + 1) * Hkv * ((rows + tile - 1) / tile) > 0x7FFFFFFFll / (((long long)max_pages * page_size + block + 63) / 64 + 2))
         return FA_ERR_UNSUPPORTED;
     if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(o) || !aligned4(block_table) ||
         !aligned4(seq_lens) || !aligned4(lse))
@@ -899,13 +905,13 @@ int rows_prepare(DecodeRowsLaunch& a, const void* q, const void* k_pages, const 
     a.max_pages = max_pages;
     a.num_pages = num_pages;
     a.d = d;
-    a.pre_workers = a.pre_tiles = a.pre_rows = 0;
+    a.pre_workers = a.pre_tiles = a.pre_rows = a.joint = 0;
     a.scale = scale;
     return FA_OK;
 }
 
 void rows_place(DecodeRowsLaunch& a, char* base) {
-    const RowsWorkspace w = rows_workspace(a.B, a.Hq, a.Hkv, a.Nq, a.d);
+    const RowsWorkspace w = rows_workspace(a.B, a.Hq, a.Hkv, a.Nq, a.d, a.joint);
     a.part_o = reinterpret_cast<float*>(base);
     a.part_lse = reinterpret_cast<float*>(base + w.part_lse);
     a.ends = reinterpret_cast<int*>(base + w.ends);
@@ -1243,6 +1249,7 @@ int fa_decode_blocks(const void* q, const void* k_pages, const void* v_pages, co
 
 size_t fa_decode_shared_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d) {
     if (!rows_sizes_ok(B, Hq, Hkv, Nq, d)) return 0;
+    if (const int joint = joint_rows(B, Hq, Hkv, Nq)) return rows_workspace(B, Hq, Hkv, Nq, d, joint).bytes;
     return rows_workspace(B, Hq, Hkv, Nq, d).bytes + prefix_workspace(B, Hq, Hkv, Nq, d).bytes;
 }
 
@@ -1255,10 +1262,18 @@ int fa_decode_shared(const void* q, const void* k_pages, const void* v_pages, co
                           num_pages, d, scale);
     if (st != FA_OK) return st;
     if (page_size % 8) return FA_ERR_UNSUPPORTED;  // boxes of 8 rows at least
+    if (!aligned4(shared_len)) return FA_ERR_ALIGNMENT;
+    a.shared = shared_len;
+    a.joint = joint_rows(B, Hq, Hkv, Nq);
+    if (a.joint) {
+        if (!workspace || workspace_bytes < rows_workspace(B, Hq, Hkv, Nq, d, a.joint).bytes) return FA_ERR_WORKSPACE;
+        if (!aligned16(workspace)) return FA_ERR_ALIGNMENT;
+        rows_place(a, static_cast<char*>(workspace));
+        return launched(launch_decode_rows(a, (cudaStream_t)stream));
+    }
     const PrefixWorkspace pw = prefix_workspace(B, Hq, Hkv, Nq, d);
     const long long most = ((long long)max_pages * page_size + 127) / 128;  // steps of an item
     if ((long long)Hkv * pw.tiles > 0x7FFFFFFFll / most) return FA_ERR_UNSUPPORTED;
-    if (!aligned4(shared_len)) return FA_ERR_ALIGNMENT;
     const RowsWorkspace ws = rows_workspace(B, Hq, Hkv, Nq, d);
     if (!workspace || workspace_bytes < ws.bytes + pw.bytes) return FA_ERR_WORKSPACE;
     if (!aligned16(workspace)) return FA_ERR_ALIGNMENT;
@@ -1293,7 +1308,6 @@ int fa_decode_shared(const void* q, const void* k_pages, const void* v_pages, co
     const cuuint32_t box[4] = {64, (cuuint32_t)p.box, 1, 1};
     if (make_map_nd(&p.map_k, k_pages, 4, dims, strides, box) || make_map_nd(&p.map_v, v_pages, 4, dims, strides, box))
         return FA_ERR_CUDA;
-    a.shared = shared_len;
     a.pre_o = p.part_o;
     a.pre_lse = p.part_lse;
     a.pre_ends = p.ends;

@@ -1,6 +1,8 @@
 // Attention of 1..16 new tokens per sequence over the paged bf16 cache: over the
 // blocks of a list, or over the tokens that follow a prefix which all sequences
-// share (the prefix itself is fa_prefix.cu's), and the merge of the parts.
+// share, and the merge of the parts.  The prefix itself is fa_prefix.cu's, or, where
+// all sequences together have no more than 32 query rows per kv head, one more
+// sequence here, whose rows are theirs: a kernel less.
 //
 // 4 d bytes per key for 4 d flops per query row: bound by HBM.  The work is one
 // list of steps of 4 x KEYS keys over all sequences, kv heads and row tiles, cut
@@ -99,7 +101,8 @@ struct Params {
     const float* pre_lse;
     const int* pre_ends;
     int B, Hkv, Nq, max_pages, num_pages, rows, row_tiles, workers, keep;
-    int pre_tiles, pre_rows;
+    int pre_tiles, pre_rows, pre_item;  // its tiles of pre_rows query rows; the first one's slots are CTA + pre_item
+    int joint;              // the prefix is this kernel's too, as sequence B with `joint` rows
     FastDiv page, block, per_row, heads;  // rows, Hkv
     float scale_log2;
     DevError* err;
@@ -118,6 +121,18 @@ __device__ __forceinline__ int keys_of(const Params& a, int len, int shared) {
     return len - shared_of(shared, len, a.Nq);
 }
 
+// The same of any place in the list of sequences; sequence B is the prefix, if it is this kernel's: every row sees all of it.
+template <bool LIST>
+__device__ __forceinline__ int length_of(const Params& a, int b, int cap, int shared) {
+    if (b < a.B) return clamp_len(a.lens[b], cap);
+    return !LIST && a.joint && b == a.B ? shared + a.Nq : 0;
+}
+template <bool LIST>
+__device__ __forceinline__ int keys_in(const Params& a, int b, int len, int shared) {
+    if (!LIST && b >= a.B) return b == a.B && a.joint ? shared : 0;
+    return keys_of<LIST>(a, len, shared);
+}
+
 // What an item costs besides its steps, in steps: its queries, and joining its parts (64 sequences of 2 to 1000 own tokens, 8
 // kv heads: the CTAs that got the shortest ones took 53 us, the others 25).
 constexpr uint32_t kItemCost = 1;
@@ -132,8 +147,8 @@ template <int STEP, bool LIST>
 __device__ __forceinline__ Scan scan_at(const Params& a, int cap, int shared, int b0) {
     const int lane = threadIdx.x & 31;
     Scan x;
-    x.len = b0 + lane < a.B ? clamp_len(a.lens[b0 + lane], cap) : 0;
-    x.n = (uint32_t)(keys_of<LIST>(a, x.len, shared) + STEP - 1) / STEP;
+    x.len = length_of<LIST>(a, b0 + lane, cap, shared);
+    x.n = (uint32_t)(keys_in<LIST>(a, b0 + lane, x.len, shared) + STEP - 1) / STEP;
     x.steps = x.n;
     x.cost = x.n ? x.n + kItemCost : 0;
 #pragma unroll
@@ -146,7 +161,7 @@ __device__ __forceinline__ Scan scan_at(const Params& a, int cap, int shared, in
 
 // A position in the list of steps.
 struct Cursor {
-    int b, len, keys, n;  // sequence, its length, its keys in this pass and their steps
+    int b, len, keys, n;  // sequence (B: the prefix), its length, its keys in this pass and their steps
     int kvh, rt, s;       // kv head, row tile and step
 };
 
@@ -160,8 +175,8 @@ __device__ __forceinline__ void advance(Cursor& c, const Params& a, int cap, int
     c.kvh = 0;
     do {
         ++c.b;
-        c.len = c.b < a.B ? clamp_len(a.lens[c.b], cap) : 0;
-        c.keys = keys_of<LIST>(a, c.len, shared);
+        c.len = length_of<LIST>(a, c.b, cap, shared);
+        c.keys = keys_in<LIST>(a, c.b, c.len, shared);
     } while (c.keys == 0 && c.b < a.B);
     c.n = (c.keys + STEP - 1) / STEP;
 }
@@ -182,11 +197,21 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, ROWS>::CTAS) decode_rows_kern
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int rg = warp % RG, kg = warp / RG;  // row group, and group of warps that share keys
     const int P = (int)a.page.d, cap = a.max_pages * P, Nq = DRAFTS ? a.Nq : 1;
-    const int given = LIST ? 0 : *a.shared, shared = clamp_len(given, cap);
+    const int given = LIST ? 0 : *a.shared;
+    int shared = clamp_len(given, cap);
     if (blockIdx.x == 0) {
         for (int i = tid; i < a.B; i += kThreads)
             if (a.lens[i] < 0 || a.lens[i] > cap) record_invalid(a.err, kSiteCacheLen, a.lens[i]);
         if (given != shared && tid == 0) record_invalid(a.err, kSiteCacheLen, given);
+    }
+    int from = 0;  // the prefix is read through this sequence's row of the table, the first one that sees all of it
+    if (!LIST && a.joint) {
+        uint32_t hit = 0;
+        for (int b0 = 0; b0 < a.B && !hit; b0 += 32) {
+            hit = __ballot_sync(0xffffffffu, b0 + lane < a.B && clamp_len(a.lens[min(b0 + lane, a.B - 1)], cap) - Nq >= shared);
+            from = b0 + __ffs(hit) - 1;
+        }
+        if (!hit) shared = 0;  // nobody does
     }
     // ---- this CTA's share of the steps: `count` of them from `cur`
     const uint32_t per_step = (uint32_t)a.Hkv * a.row_tiles;
@@ -195,7 +220,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, ROWS>::CTAS) decode_rows_kern
     {
         const Scan head = scan_at<STEP, LIST>(a, cap, shared, 0);
         uint32_t total = __shfl_sync(0xffffffffu, head.cost, 31);
-        for (int b0 = 32; b0 < a.B; b0 += 32) total += __shfl_sync(0xffffffffu, scan_at<STEP, LIST>(a, cap, shared, b0).cost, 31);
+        const int all = a.B + (a.joint > 0);
+        for (int b0 = 32; b0 < all; b0 += 32) total += __shfl_sync(0xffffffffu, scan_at<STEP, LIST>(a, cap, shared, b0).cost, 31);
         const Share mine = share_of(total * per_step, a.workers, blockIdx.x);
         // the steps before a place in the list of costs, and the item and step there
         auto steps_before = [&](uint32_t at, Cursor& c) -> uint32_t {
@@ -207,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, ROWS>::CTAS) decode_rows_kern
                 cost += __shfl_sync(0xffffffffu, x.cost, 31);
                 steps += __shfl_sync(0xffffffffu, x.steps, 31);
                 b0 += 32;
-                if (b0 >= a.B) return steps * per_step;  // the end
+                if (b0 >= all) return steps * per_step;  // the end
                 x = scan_at<STEP, LIST>(a, cap, shared, b0);
             }
             const int f = __ffs(hit) - 1;
@@ -228,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, ROWS>::CTAS) decode_rows_kern
         Cursor end;
         count = (int)(steps_before(mine.first + mine.count, end) - first);
         if (count == 0) return;
-        cur.keys = keys_of<LIST>(a, cur.len, shared);
+        cur.keys = keys_in<LIST>(a, cur.b, cur.len, shared);
     }
 
     // ---- the ring: this warp's keys of the steps ahead, whatever item they are of.  A key's row is D / 8 pieces of 16
@@ -287,7 +313,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, ROWS>::CTAS) decode_rows_kern
             const int key = ahead.s * STEP + warp * KEYS + lane % KEYS;
             next.b = ahead.b;
             next.head = ahead.kvh;
-            next.tok = looked < count && key < ahead.keys ? key + ahead.len - ahead.keys : kNone;
+            const bool prefix = ahead.b == a.B;
+            if (prefix) next.b = from;
+            next.tok = looked < count && key < ahead.keys ? (prefix ? key : key + ahead.len - ahead.keys) : kNone;
         }
         const int lpage = next.tok == kNone ? 0 : (int)a.page.div(next.tok);
         next.at = next.tok - lpage * P;
@@ -329,13 +357,19 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, ROWS>::CTAS) decode_rows_kern
     auto load_q = [&]() {
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-            const int r = cur.rt * ROWS + (rg * NB + nb) * 8 + g;
-            const uint32_t* src = reinterpret_cast<const uint32_t*>(
-                                      a.q + (((long long)cur.b * a.Hkv + cur.kvh) * a.rows + (r < a.rows ? r : 0)) * D) + t;
+            int r = cur.rt * ROWS + (rg * NB + nb) * 8 + g, b = cur.b;
+            bool there = r < a.rows;
+            if (!LIST && cur.b == a.B) {  // row r of the prefix is row r % rows of sequence r / rows
+                there = r < a.joint;
+                b = there ? r / a.rows : 0;
+                r -= b * a.rows;
+            }
+            const uint32_t* src =
+                reinterpret_cast<const uint32_t*>(a.q + (((long long)b * a.Hkv + cur.kvh) * a.rows + (there ? r : 0)) * D) + t;
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
-                qb[nb][s][0] = r < a.rows ? src[s * 8] : 0u;
-                qb[nb][s][1] = r < a.rows ? src[s * 8 + 4] : 0u;
+                qb[nb][s][0] = there ? src[s * 8] : 0u;
+                qb[nb][s][1] = there ? src[s * 8 + 4] : 0u;
             }
         }
     };
@@ -359,7 +393,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, ROWS>::CTAS) decode_rows_kern
     // fragment addresses: rows of the lane's part of ldmatrix, and its piece of 16 bytes
     const int kr = lane % 16, kc = lane / 16, vr = lane % 8 + lane / 16 * 8, vc = lane / 8 % 2;
     for (int it = 0; it < count; ++it) {
-        const int r0 = cur.rt * ROWS + rg * NB * 8, nrows = min(ROWS, a.rows - cur.rt * ROWS);  // of the warp, of the tile
+        const bool prefix = !LIST && cur.b == a.B;
+        const int r0 = cur.rt * ROWS + rg * NB * 8;                                           // of the warp
+        const int nrows = min(ROWS, (prefix ? a.joint : a.rows) - cur.rt * ROWS);             // of the tile
         const long long bh = (long long)cur.b * a.Hkv + cur.kvh;
         if (begins) {
             seg = cur.s;
@@ -589,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, ROWS>::CTAS) decode_rows_kern
                 if (nb + 1 < NB) __syncthreads();
             }
             if (kg == 0) {
-                const bool whole = seg == 0 && item_ends && (LIST || shared_of(shared, done.len, Nq) == 0);
+                const bool whole = seg == 0 && item_ends && !prefix && (LIST || shared_of(shared, done.len, Nq) == 0);
                 const long long item = bh * a.row_tiles + done.rt, slot_out = blockIdx.x + item;
                 if (tid == 0 && seg == 0) a.ends[2 * item] = blockIdx.x;
                 if (tid == 0 && item_ends) a.ends[2 * item + 1] = blockIdx.x;
@@ -654,7 +690,7 @@ __device__ __forceinline__ Parts find_parts(const Params& a, int b, int kvh, int
         x.n = own.y - own.x + 1;
     }
     if (!LIST && shared_of(shared, len, a.Nq) > 0) {
-        x.pslot = pre.x + kvh * a.pre_tiles + place;
+        x.pslot = pre.x + a.pre_item + kvh * a.pre_tiles + place;
         x.pn = pre.y - pre.x + 1;
     }
     x.done = x.n == 1 && x.pn == 0;
@@ -750,7 +786,7 @@ template <int D, int ROWS, bool LIST>
 cudaError_t launch_merge(const DecodeRowsLaunch& a, const Params& p, cudaStream_t s) {
     const long long rows = (long long)a.B * a.Hkv * p.rows;
     // rows alone in a block where there are few of them: their parts are read by more threads
-    const long long parts = LIST ? p.workers / ((long long)a.B * a.Hkv * p.row_tiles) : a.pre_workers / ((long long)a.Hkv * p.pre_tiles);
+    const long long parts = LIST ? p.workers / ((long long)a.B * a.Hkv * p.row_tiles) : (a.joint ? p.workers : a.pre_workers) / ((long long)a.Hkv * p.pre_tiles);
     if (rows <= (parts >= 4 ? 16ll : 4ll) * a.num_sms)
         return launch_dependent(merge_rows_kernel<D, ROWS, LIST, true, 256>, dim3((unsigned)rows), dim3(256), 0, s, p);
     constexpr int PER = 128 / (D / 4);
@@ -792,6 +828,16 @@ cudaError_t launch_l(const DecodeRowsLaunch& a, cudaStream_t s) {
     p.keep = a.keep;
     p.pre_tiles = a.pre_tiles;
     p.pre_rows = a.pre_rows;
+    p.pre_item = 0;
+    p.joint = a.joint;
+    if (a.joint) {  // its parts are among the others'
+        p.pre_o = a.part_o;
+        p.pre_lse = a.part_lse;
+        p.pre_tiles = 1;
+        p.pre_rows = ROWS;
+        p.pre_item = a.B * a.Hkv;
+        p.pre_ends = a.ends + 2 * p.pre_item;
+    }
     p.page = FastDiv((uint32_t)a.page);
     p.block = FastDiv((uint32_t)std::max(a.block, 1));
     p.scale_log2 = a.scale * kLog2e;
@@ -800,7 +846,7 @@ cudaError_t launch_l(const DecodeRowsLaunch& a, cudaStream_t s) {
     const long long most = LIST ? std::min((long long)a.keep * a.block, (long long)a.max_pages * a.page + a.block)
                                 : (long long)a.max_pages * a.page;
     p.workers = (int)std::min<long long>(std::min(C::CTAS * a.num_sms, kRowsMostWorkers),
-                                         (long long)a.B * a.Hkv * p.row_tiles * ((most + C::STEP - 1) / C::STEP));
+                                         ((long long)a.B + (a.joint > 0)) * a.Hkv * p.row_tiles * ((most + C::STEP - 1) / C::STEP));
     e = launch_dependent(a.Nq > 1 ? decode_rows_kernel<D, ROWS, true, LIST> : decode_rows_kernel<D, ROWS, false, LIST>,
                          dim3(p.workers), dim3(kThreads), C::SMEM, s, p);
     return e != cudaSuccess ? e : launch_merge<D, ROWS, LIST>(a, p, s);
@@ -814,7 +860,7 @@ cudaError_t launch_r(const DecodeRowsLaunch& a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_decode_rows(const DecodeRowsLaunch& a, cudaStream_t s) {
-    const int tile = rows_tile(a.Hq / a.Hkv * a.Nq);
+    const int tile = rows_tile(a.joint ? a.joint : a.Hq / a.Hkv * a.Nq);
     if (a.d == 128) return tile == 8 ? launch_r<128, 8>(a, s) : tile == 16 ? launch_r<128, 16>(a, s) : launch_r<128, 32>(a, s);
     return tile == 8 ? launch_r<64, 8>(a, s) : tile == 16 ? launch_r<64, 16>(a, s) : launch_r<64, 32>(a, s);
 }
