@@ -13,12 +13,18 @@
 namespace fa {
 namespace {
 
-// One CTA per (sequence, run of blocks, run of kv heads); the first HALF threads take K, the others V.  Every element is
-// read once and written once: bound by HBM for prompts, by the latency of a launch and three dependent loads (length,
-// table, token) for single tokens.  A thread holds TPT tasks (16 columns of a token, the pieces that a rotation pairs) and
-// loads the next head's while it works on this one's; the cosines and sines of the CTA's tokens are made once, in shared
-// memory, and serve every head of the run.  For the bounds the rotated keys also go to a tile in shared memory: each warp
-// takes the extremes over a part of a block's tokens, and one warp per block joins the parts with what the block had.
+// Every element is read once and written once: bound by HBM for prompts, by the latency of a launch and three dependent
+// loads (length, table, token) for single tokens.
+//
+// append_kernel: a CTA takes a run of tokens, in whole blocks, of up to eight kv heads.  The tokens' places in the cache and
+// their cosines and sines are made once, in shared memory; then each warp takes the keys of a head, or its values, for
+// itself, without waiting for others: RP rows at a time, four of these loaded ahead, 16 columns of a row (the two pieces
+// that a rotation pairs) per lane.  The extremes of a block gather in the lanes' registers over its rows and are joined by
+// shuffles at its end.
+//
+// blocks_append_kernel is for blocks that are no multiple of RP rows (4, at d = 64 8): the rotated keys go to a tile in shared
+// memory, and warps take the extremes from there.  (For blocks of any size, with two barriers per head, it took 26.8 us for
+// 8 ragged prompts of up to 2048 tokens, 8 heads, d = 128, a third of the issue slots waiting for barriers.)
 struct PagedAppendPlan {
     int unit, units, heads, groups;  // blocks per CTA (tokens without bounds), runs of them; kv heads per CTA, runs of them
     int tokens;                      // most new tokens of a CTA
@@ -45,9 +51,202 @@ __device__ __forceinline__ uint4 ends4(uint4 a, uint4 b, bool is_max) {
                   : make_uint4(min2(a.x, b.x), min2(a.y, b.y), min2(a.z, b.z), min2(a.w, b.w));
 }
 
-template <int D, int HALF, int TPT, bool BOUNDS, bool INTER>
+// The new tokens [t0, t1) of a unit that begins at token `first`; false if there are none.
+struct AppendRun {
+    int len, n, first, t0, t1;
+};
+__device__ __forceinline__ bool append_run(const PagedAppendLaunch& a, const PagedAppendPlan& plan, int b, int unit, AppendRun& r) {
+    const int cap = a.max_pages * a.page, block = a.bounds ? a.block : 1;
+    r.len = a.lens[b];
+    r.n = a.new_lens ? a.new_lens[b] : a.N;
+    if (r.len < 0 || r.len > cap || r.n < 0 || r.n > a.N || r.n > cap - r.len) {
+        if (threadIdx.x == 0) record_invalid(a.err, kSiteCacheLen, r.len);
+        r.len = min(max(r.len, 0), cap);
+        r.n = min(min(max(r.n, 0), a.N), cap - r.len);
+    }
+    r.first = ((a.bounds ? (int)plan.block.div(r.len) : r.len) + unit * plan.unit) * block;
+    r.t0 = max(r.len - r.first, 0);
+    r.t1 = min(plan.unit * block, r.len + r.n - r.first);
+    return r.n > 0 && r.first < r.len + r.n;
+}
+
+// Cosines and sines of `fresh` tokens, the first of which is new token `from`: [token][pair of pairs j < 4][task][2].  The
+// positions are loaded for several tokens at once: one after the other the loads alone took 3 us.
+__device__ __forceinline__ void make_turns(const PagedAppendLaunch& a, float2* s_turn, int turned, int b, int len, int from, int fresh) {
+    const int q = threadIdx.x % 64, step = blockDim.x / 64;  // one pair for each of up to 64 threads, several tokens at a time
+    if (q >= turned * 8) return;
+    const uint64_t turns = a.turns[q];
+    const int* positions = a.positions ? a.positions + (long long)b * a.N + from : nullptr;
+    constexpr int AHEAD = 8;
+    for (int t0 = threadIdx.x / 64; t0 < fresh; t0 += AHEAD * step) {
+        int pos[AHEAD];
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const int tok = t0 + i * step;
+            pos[i] = positions && tok < fresh ? positions[tok] : len + from + tok;
+        }
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const int tok = t0 + i * step;
+            if (tok >= fresh) break;
+            float2 cs;
+            turn_cos_sin(pos[i], turns, a.magnitude, cs.x, cs.y);
+            s_turn[((tok * 4 + q % 8 / 2) * turned + q / 8) * 2 + q % 2] = cs;
+        }
+    }
+}
+template <bool INTER>
+__device__ __forceinline__ void turn_task(uint4& x, uint4& y, const float2* s_turn, int turned, int tok, int p) {
+    const float2* cs = s_turn + (tok * 4 * turned + p) * 2;
+    float c[8], s[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float4 v = *reinterpret_cast<const float4*>(cs + j * turned * 2);
+        c[2 * j] = v.x, s[2 * j] = v.y, c[2 * j + 1] = v.z, s[2 * j + 1] = v.w;
+    }
+    rotate16<INTER>(x, y, c, s);
+}
+
+constexpr int kAppendWarps = 8, kMostTokens = 128;
+
+// U: passes loaded ahead.
+template <int D, int U, bool BOUNDS, bool INTER>
+__global__ void __launch_bounds__(kAppendWarps * 32, 2) append_kernel(const PagedAppendLaunch a, const PagedAppendPlan plan) {
+    extern __shared__ __align__(16) uint8_t s_mem[];
+    __shared__ uint32_t s_row[kMostTokens], s_block[kMostTokens];  // places of the tokens' rows and of the blocks' bounds, head 0
+    constexpr int TPR = D / 16, RP = 32 / TPR;
+    pdl_launch_dependents();
+    pdl_wait();
+    const int group = blockIdx.x % plan.groups, unit = (blockIdx.x / plan.groups) % plan.units;
+    const int b = blockIdx.x / plan.groups / plan.units, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    AppendRun run;
+    if (!append_run(a, plan, b, unit, run)) return;
+    const int block = BOUNDS ? a.block : 1, from = run.first + run.t0 - run.len, fresh = run.t1 - run.t0;
+    const int turned = a.turns ? a.rot / 16 : 0;  // tasks of a row that rotate
+    const float2* s_turn = reinterpret_cast<const float2*>(s_mem);
+    // jobs: the keys of heads h0, h0 + 1, ..., then the values
+    const int h0 = group * plan.heads, heads = min(plan.heads, a.Hkv - h0);
+    const int r = lane / TPR, p = lane % TPR;
+    int c0, c1;
+    task_columns<INTER>(p, turned * 16, c0, c1);
+    uint4 x[U], y[U];
+    const int p0 = run.t0 / RP, p1 = (run.t1 + RP - 1) / RP;  // passes of RP tokens of the unit
+    auto load_keys = [&](int h, int pass) {
+        const __nv_bfloat16* src = (const __nv_bfloat16*)a.k + b * a.kb + h * a.kh;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int t = (pass + u) * RP + r;
+            if (t >= run.t0 && t < run.t1) {
+                const __nv_bfloat16* at = src + (long long)(from + t - run.t0) * a.kn;
+                x[u] = *reinterpret_cast<const uint4*>(at + c0);
+                y[u] = *reinterpret_cast<const uint4*>(at + c1);
+            }
+        }
+    };
+    if (warp < heads) load_keys(h0 + warp, p0);
+    // the tokens' rows of the cache and the blocks' bounds
+    for (int i = threadIdx.x; i < fresh; i += kAppendWarps * 32) {
+        const int at = run.first + run.t0 + i, lpage = (int)plan.page.div(at), pg = a.table[(long long)b * a.max_pages + lpage];
+        const bool ok = (unsigned)pg < (unsigned)a.num_pages;
+        if (!ok) record_invalid(a.err, kSiteCacheTable, pg);
+        s_row[i] = ok ? (uint32_t)pg * a.Hkv * a.page + (uint32_t)(at - lpage * a.page) : ~0u;
+        if (BOUNDS) {
+            const int blk = (int)plan.block.div(run.t0 + i);
+            if (i == 0 || run.t0 + i == blk * block)
+                s_block[blk] = ok ? (uint32_t)pg * a.Hkv * (a.page / block) + plan.block.div(at - lpage * a.page) : ~0u;
+        }
+    }
+    if (turned) make_turns(a, reinterpret_cast<float2*>(s_mem), turned, b, run.len, from, fresh);
+    __syncthreads();
+    for (int job = warp; job < 2 * heads; job += kAppendWarps) {
+        if (job >= heads) {  // values: whole rows, D / 8 lanes each
+            constexpr int LPR = D / 8, RV = 32 / LPR, UV = 8;
+            const int h = h0 + job - heads, vr = lane / LPR, c = lane % LPR * 8;
+            const __nv_bfloat16* src = (const __nv_bfloat16*)a.v + b * a.vb + h * a.vh + (long long)(from + vr) * a.vn + c;
+            for (int t = 0; t < fresh; t += UV * RV) {
+                uint4 v[UV];
+#pragma unroll
+                for (int u = 0; u < UV; ++u)
+                    if (t + u * RV + vr < fresh) v[u] = *reinterpret_cast<const uint4*>(src + (long long)(t + u * RV) * a.vn);
+#pragma unroll
+                for (int u = 0; u < UV; ++u) {
+                    const uint32_t row = t + u * RV + vr < fresh ? s_row[t + u * RV + vr] : ~0u;
+                    if (row != ~0u) *reinterpret_cast<uint4*>((__nv_bfloat16*)a.vp + (size_t)(row + h * a.page) * D + c) = v[u];
+                }
+            }
+            continue;
+        }
+        const int h = h0 + job;
+        if (job != warp) load_keys(h, p0);
+        uint4 lo[2], hi[2], had = make_uint4(0, 0, 0, 0);
+        // a block's bounds are four pieces per column pair: lanes r = 0 .. 3 have the smallest x, y and the largest x, y
+        auto ends_at = [&](int blk) {
+            const uint32_t row = s_block[blk];
+            return row == ~0u || r > 3 ? nullptr
+                                       : (__nv_bfloat16*)a.bounds + (size_t)(row + h * (a.page / block)) * (2 * D) +
+                                             (r >= 2 ? D : 0) + (r & 1 ? c1 : c0);
+        };
+        const bool old = BOUNDS && run.len > run.first;  // the first block begins with earlier tokens
+        if (old && ends_at(0)) had = *reinterpret_cast<const uint4*>(ends_at(0));
+        bool begins = true;
+        for (int pass = p0; pass < p1; pass += U) {
+            uint4 u0[U], u1[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) u0[u] = x[u], u1[u] = y[u];
+            if (pass + U < p1) load_keys(h, pass + U);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (pass + u >= p1) break;
+                const int t = (pass + u) * RP + r, tok = t - run.t0;
+                const bool there = t >= run.t0 && t < run.t1;
+                if (there) {
+                    if (p < turned) turn_task<INTER>(u0[u], u1[u], s_turn, turned, tok, p);
+                    const uint32_t row = s_row[tok];
+                    if (row != ~0u) {
+                        __nv_bfloat16* dst = (__nv_bfloat16*)a.kp + (size_t)(row + h * a.page) * D;
+                        *reinterpret_cast<uint4*>(dst + c0) = u0[u];
+                        *reinterpret_cast<uint4*>(dst + c1) = u1[u];
+                    }
+                }
+                if constexpr (BOUNDS) {
+                    if (begins) {
+                        lo[0] = lo[1] = make_uint4(0x7F807F80u, 0x7F807F80u, 0x7F807F80u, 0x7F807F80u);
+                        hi[0] = hi[1] = make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u);
+                    }
+                    if (there) {
+                        lo[0] = ends4(lo[0], u0[u], false), lo[1] = ends4(lo[1], u1[u], false);
+                        hi[0] = ends4(hi[0], u0[u], true), hi[1] = ends4(hi[1], u1[u], true);
+                    }
+                    const int blk = (int)plan.block.div((pass + u) * RP);
+                    begins = pass + u + 1 == p1 || (pass + u + 1) * RP == (blk + 1) * block;
+                    if (begins) {  // the block's end
+                        auto join = [&](uint4& v, bool is_max) {
+#pragma unroll
+                            for (int m = TPR; m < 32; m <<= 1)
+                                v = ends4(v, make_uint4(__shfl_xor_sync(0xffffffffu, v.x, m), __shfl_xor_sync(0xffffffffu, v.y, m),
+                                                        __shfl_xor_sync(0xffffffffu, v.z, m), __shfl_xor_sync(0xffffffffu, v.w, m)),
+                                          is_max);
+                        };
+                        join(lo[0], false);
+                        join(lo[1], false);
+                        join(hi[0], true);
+                        join(hi[1], true);
+                        __nv_bfloat16* to = ends_at(blk);
+                        if (to) {
+                            uint4 v = r == 0 ? lo[0] : r == 1 ? lo[1] : r == 2 ? hi[0] : hi[1];
+                            if (old && blk == 0) v = ends4(v, had, r >= 2);
+                            *reinterpret_cast<uint4*>(to) = v;
+                        }
+                    }
+                }
+            }
+        }
+    }
+}
+
+template <int D, int HALF, int TPT, bool INTER>
 __global__ void __launch_bounds__(2 * HALF, kPagedAppendThreads<TPT> / (2 * HALF))
-    paged_append_kernel(const PagedAppendLaunch a, const PagedAppendPlan plan) {
+    blocks_append_kernel(const PagedAppendLaunch a, const PagedAppendPlan plan) {
     extern __shared__ __align__(16) uint8_t s_mem[];
     constexpr int TPR = D / 16, WARPS = 2 * HALF / 32, STEP = HALF / TPR;  // STEP: tokens of one task per thread
     pdl_launch_dependents();
@@ -56,30 +255,14 @@ __global__ void __launch_bounds__(2 * HALF, kPagedAppendThreads<TPT> / (2 * HALF
     const int unit = (blockIdx.x / plan.groups) % plan.units;
     const int b = blockIdx.x / plan.groups / plan.units;
     const int is_v = threadIdx.x / HALF, tid = threadIdx.x % HALF, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int cap = a.max_pages * a.page, block = BOUNDS ? a.block : 1;
-    int len = a.lens[b], n = a.new_lens ? a.new_lens[b] : a.N;
-    if (len < 0 || len > cap || n < 0 || n > a.N || n > cap - len) {
-        if (threadIdx.x == 0) record_invalid(a.err, kSiteCacheLen, len);
-        len = min(max(len, 0), cap);
-        n = min(min(max(n, 0), a.N), cap - len);
-    }
-    const int first = ((BOUNDS ? (int)plan.block.div(len) : len) + unit * plan.unit) * block;  // the CTA's first token
-    if (n == 0 || first >= len + n) return;
-    const int t0 = max(len - first, 0), t1 = min(plan.unit * block, len + n - first);  // its new tokens [t0, t1)
-    const int fresh = t1 - t0, from = first + t0 - len;                                // their number, the first one's index
-    const int turned = a.turns ? a.rot / 16 : 0;                                       // tasks of a row that rotate
-    float2* s_turn = reinterpret_cast<float2*>(s_mem);                                 // [token][pair of pairs j < 4][task][2]
+    AppendRun run;
+    if (!append_run(a, plan, b, unit, run)) return;
+    const int block = a.block, len = run.len, first = run.first, t0 = run.t0, t1 = run.t1;
+    const int fresh = t1 - t0, from = first + t0 - len;  // new tokens, the first one's index
+    const int turned = a.turns ? a.rot / 16 : 0;  // tasks of a row that rotate
+    float2* s_turn = reinterpret_cast<float2*>(s_mem);
     if (turned) {
-        const int q = threadIdx.x % 64;  // one pair for each of up to 64 threads, several tokens at a time
-        if (q < turned * 8) {
-            const uint64_t turns = a.turns[q];
-            for (int tok = threadIdx.x / 64; tok < fresh; tok += 2 * HALF / 64) {
-                const int pos = a.positions ? a.positions[(long long)b * a.N + from + tok] : len + from + tok;
-                float2 cs;
-                turn_cos_sin(pos, turns, a.magnitude, cs.x, cs.y);
-                s_turn[((tok * 4 + q % 8 / 2) * turned + q / 8) * 2 + q % 2] = cs;
-            }
-        }
+        make_turns(a, s_turn, turned, b, len, from, fresh);
         __syncthreads();
     }
     // ---- the thread's tasks: the same columns of tokens tid / TPR, + STEP, ...
@@ -123,9 +306,9 @@ __global__ void __launch_bounds__(2 * HALF, kPagedAppendThreads<TPT> / (2 * HALF
     uint8_t* s_tile = s_mem + (size_t)plan.tokens * turned * 64;
     uint4* s_part = reinterpret_cast<uint4*>(s_tile + (size_t)plan.tokens * D * 2);  // [item][2][D] bf16
     constexpr int LANES = D / 4, PER = (kMostBlocks + WARPS - 1) / WARPS;            // 16-byte pieces of a block's bounds
-    const int blocks = BOUNDS ? (t1 + block - 1) / block : 0, parts = BOUNDS && blocks < WARPS ? WARPS / blocks : 1;
+    const int blocks = (t1 + block - 1) / block, parts = blocks < WARPS ? WARPS / blocks : 1;
     __nv_bfloat16* ends[PER];
-    if constexpr (BOUNDS) {
+    {
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int blk = warp + i * WARPS, at = first + blk * block, lpage = blk < blocks ? (int)plan.page.div(at) : 0;
@@ -138,7 +321,7 @@ __global__ void __launch_bounds__(2 * HALF, kPagedAppendThreads<TPT> / (2 * HALF
     }
     for (int h = h0; h < h1; ++h) {
         uint4 x[TPT], y[TPT], had;
-        const bool old = BOUNDS && warp == 0 && len > first && ends[0];  // the block that earlier tokens begin
+        const bool old = warp == 0 && len > first && ends[0];  // the block that earlier tokens begin
         if (old) had = *reinterpret_cast<const uint4*>(ends[0]);
 #pragma unroll
         for (int i = 0; i < TPT; ++i) x[i] = nx[i], y[i] = ny[i];
@@ -147,27 +330,18 @@ __global__ void __launch_bounds__(2 * HALF, kPagedAppendThreads<TPT> / (2 * HALF
         for (int i = 0; i < TPT; ++i) {
             if (!there[i]) continue;
             const int tok = tid / TPR + i * STEP;
-            if (turn) {
-                const float2* cs = s_turn + (tok * 4 * turned + p) * 2;
-                float c[8], s[8];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float4 v = *reinterpret_cast<const float4*>(cs + j * turned * 2);
-                    c[2 * j] = v.x, s[2 * j] = v.y, c[2 * j + 1] = v.z, s[2 * j + 1] = v.w;
-                }
-                rotate16<INTER>(x[i], y[i], c, s);
-            }
+            if (turn) turn_task<INTER>(x[i], y[i], s_turn, turned, tok, p);
             if (dst[i]) {
                 *reinterpret_cast<uint4*>(dst[i]) = x[i];
                 *reinterpret_cast<uint4*>(dst[i] + apart) = y[i];
                 dst[i] += (long long)a.page * D;
             }
-            if (BOUNDS && !is_v) {
+            if (!is_v) {
                 *reinterpret_cast<uint4*>(s_tile + (tok * D + c0) * 2) = x[i];
                 *reinterpret_cast<uint4*>(s_tile + (tok * D + c0 + apart) * 2) = y[i];
             }
         }
-        if constexpr (BOUNDS) {
+        {
             __syncthreads();
             for (int it = warp; it < blocks * parts; it += WARPS) {
                 const int blk = it / parts, part = it - blk * parts;
@@ -209,8 +383,8 @@ __global__ void __launch_bounds__(2 * HALF, kPagedAppendThreads<TPT> / (2 * HALF
     }
 }
 
-template <int D, int HALF, int TPT, bool BOUNDS, bool INTER>
-cudaError_t launch_t(const PagedAppendLaunch& a, PagedAppendPlan plan, cudaStream_t s) {
+template <int D, int HALF, int TPT, bool INTER>
+cudaError_t launch_blocks_t(const PagedAppendLaunch& a, PagedAppendPlan plan, cudaStream_t s) {
     // kv heads per CTA, which share the sines: the fewest waves of resident CTAs times the work of one
     const long long cells = (long long)a.B * plan.units, slots = (long long)kPagedAppendThreads<TPT> / (2 * HALF) * a.num_sms;
     long long best = -1;
@@ -219,38 +393,65 @@ cudaError_t launch_t(const PagedAppendLaunch& a, PagedAppendPlan plan, cudaStrea
         if (best < 0 || cost < best) best = cost, plan.heads = h;
     }
     plan.groups = (a.Hkv + plan.heads - 1) / plan.heads;
-    const long long ctas = cells * plan.groups;
-    const int smem = plan.tokens * ((a.turns ? a.rot * 4 : 0) + (BOUNDS ? D * 2 : 0)) +
-                     (BOUNDS ? std::max(kMostBlocks, 2 * HALF / 32) * D * 4 : 0);
-    cudaError_t e = set_smem_limit_once<paged_append_kernel<D, HALF, TPT, BOUNDS, INTER>>(112 * 1024);
+    const int smem = plan.tokens * ((a.turns ? a.rot * 4 : 0) + D * 2) + std::max(kMostBlocks, 2 * HALF / 32) * D * 4;
+    cudaError_t e = set_smem_limit_once<blocks_append_kernel<D, HALF, TPT, INTER>>(112 * 1024);
     if (e != cudaSuccess) return e;
-    return launch_dependent(paged_append_kernel<D, HALF, TPT, BOUNDS, INTER>, dim3((unsigned)ctas), dim3(2 * HALF),
+    return launch_dependent(blocks_append_kernel<D, HALF, TPT, INTER>, dim3((unsigned)(cells * plan.groups)), dim3(2 * HALF),
                             (size_t)smem, s, a, plan);
 }
 
 template <int D, int HALF, int TPT>
-cudaError_t launch_ht(const PagedAppendLaunch& a, const PagedAppendPlan& plan, cudaStream_t s) {
+cudaError_t launch_blocks(const PagedAppendLaunch& a, const PagedAppendPlan& plan, cudaStream_t s) {
+    return a.interleaved ? launch_blocks_t<D, HALF, TPT, true>(a, plan, s) : launch_blocks_t<D, HALF, TPT, false>(a, plan, s);
+}
+
+template <int D, int U, bool BOUNDS, bool INTER>
+cudaError_t launch_append(const PagedAppendLaunch& a, const PagedAppendPlan& plan, cudaStream_t s) {
+    const int smem = a.turns ? plan.tokens * a.rot * 4 : 0;
+    cudaError_t e = set_smem_limit_once<append_kernel<D, U, BOUNDS, INTER>>(64 * 1024);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(append_kernel<D, U, BOUNDS, INTER>, dim3((unsigned)((long long)a.B * plan.units * plan.groups)),
+                            dim3(kAppendWarps * 32), (size_t)smem, s, a, plan);
+}
+
+template <int D, int U>
+cudaError_t launch_u(const PagedAppendLaunch& a, const PagedAppendPlan& plan, cudaStream_t s) {
     if (a.bounds)
-        return a.interleaved ? launch_t<D, HALF, TPT, true, true>(a, plan, s) : launch_t<D, HALF, TPT, true, false>(a, plan, s);
-    return a.interleaved ? launch_t<D, HALF, TPT, false, true>(a, plan, s) : launch_t<D, HALF, TPT, false, false>(a, plan, s);
+        return a.interleaved ? launch_append<D, U, true, true>(a, plan, s) : launch_append<D, U, true, false>(a, plan, s);
+    return a.interleaved ? launch_append<D, U, false, true>(a, plan, s) : launch_append<D, U, false, false>(a, plan, s);
 }
 
 template <int D>
 cudaError_t launch_d(const PagedAppendLaunch& a, cudaStream_t s) {
-    // a CTA's tokens: up to 64 (blocks of more than 64 tokens: one block), in whole blocks
-    PagedAppendPlan plan;
+    constexpr int RP = 512 / D;
+    const bool rows = !a.bounds || a.block % RP == 0;  // blocks are whole passes of append_kernel
     const int block = a.bounds ? a.block : 1;
     const int touched = a.bounds ? (a.N + block - 2) / block + 1 : a.N;  // blocks that N tokens can touch
-    plan.unit = a.bounds ? std::min(std::max(1, std::min(64 / block, kMostBlocks)), touched) : std::min(64, a.N);
-    plan.units = (touched + plan.unit - 1) / plan.unit;
-    plan.tokens = std::min(plan.unit * block, a.N);
+    PagedAppendPlan plan;
     plan.page = FastDiv((uint32_t)a.page);
     plan.block = FastDiv((uint32_t)block);
+    auto units = [&](int tokens) {  // of whole blocks, about so many tokens each
+        plan.unit = std::min(std::max(1, tokens / block), touched);
+        plan.units = (touched + plan.unit - 1) / plan.unit;
+        plan.tokens = std::min(plan.unit * block, a.N);
+    };
+    if (rows) {
+        // four kv heads per CTA, a job for each warp (eight, which halve the sines: 26.6 us against 24.3 for 8 ragged prompts of
+        // up to 2048 tokens, 8 heads, d = 128); 32 tokens, or 16 where that leaves SMs without two CTAs (16 sequences of up to
+        // 200 tokens: 8.2 us with 32, 6.4 with 16); passes ahead: four (two: 26.1 us), for a few tokens two (32 single tokens
+        // 3.9 us with four, 3.5 with two)
+        plan.heads = 4;
+        plan.groups = (a.Hkv + 3) / 4;
+        units(32);
+        if ((long long)a.B * plan.units * plan.groups < 2ll * a.num_sms) units(16);
+        return a.N <= 2 * RP ? launch_u<D, 2>(a, plan, s) : launch_u<D, 4>(a, plan, s);
+    }
+    units(std::min(64, kMostBlocks * block));
     const int tasks = plan.tokens * (D / 16);
-    if (tasks <= 128) return launch_ht<D, 128, 1>(a, plan, s);
-    if (tasks <= 256) return launch_ht<D, 128, 2>(a, plan, s);
-    if (tasks <= 512) return launch_ht<D, 128, 4>(a, plan, s);
-    return launch_ht<D, 256, 4>(a, plan, s);
+    if (tasks <= 128) return launch_blocks<D, 128, 1>(a, plan, s);
+    if (tasks <= 256) return launch_blocks<D, 128, 2>(a, plan, s);
+    if (tasks <= 512) return launch_blocks<D, 128, 4>(a, plan, s);
+    return launch_blocks<D, 256, 4>(a, plan, s);
 }
 
 }  // namespace
