@@ -376,9 +376,19 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) select_blocks_kernel(c
             h[c] = row != ~0u ? at[D / 8 + c * 8 + part] : make_uint4(0, 0, 0, 0);
         }
         uint64_t top = 0;
+        uint4 next[C];  // the next row
+        auto load_row = [&](int r) {
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+                next[c] = reinterpret_cast<const uint4*>(q + (long long)min(r, a.rows - 1) * D)[c * 8 + part];
+        };
+        load_row(lane >> 3);
 #pragma unroll 1
         for (int r = lane >> 3; r < ((a.rows + 3) & ~3); r += 4) {
-            const __nv_bfloat16* qr = q + (long long)min(r, a.rows - 1) * D;
+            uint4 row4[C];
+#pragma unroll
+            for (int c = 0; c < C; ++c) row4[c] = next[c];
+            load_row(r + 4);
             uint64_t key;
             if (fixed) {
                 int s0 = 0, s1 = 0, s2 = 0;
@@ -399,7 +409,7 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) select_blocks_kernel(c
                 };
 #pragma unroll
                 for (int c = 0; c < C; ++c) {
-                    const uint4 x = reinterpret_cast<const uint4*>(qr)[c * 8 + part];
+                    const uint4 x = row4[c];
                     add2(x.x, l[c].x, h[c].x);
                     add2(x.y, l[c].y, h[c].y);
                     add2(x.z, l[c].z, h[c].z);
@@ -414,7 +424,7 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) select_blocks_kernel(c
                 // in units of 2^-61 A, which 64 bits hold: the last part rounded to them
                 key = (uint64_t)(((long long)s0 << 40) + ((long long)s1 << 18) + ((s2 + 8) >> 4)) ^ (1ull << 63);
             } else {
-                key = slow_key(qr, row != ~0u ? reinterpret_cast<const __nv_bfloat16*>(at) : nullptr, D, part);
+                key = slow_key(q + (long long)min(r, a.rows - 1) * D, row != ~0u ? reinterpret_cast<const __nv_bfloat16*>(at) : nullptr, D, part);
             }
             top = max(top, key);  // NaN on top
         }
