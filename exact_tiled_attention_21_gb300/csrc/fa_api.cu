@@ -828,7 +828,7 @@ struct RowsWorkspace {
 };
 RowsWorkspace rows_workspace(int B, int Hq, int Hkv, int Nq, int d, int joint = 0) {
     const int rows = Hq / Hkv * Nq, tile = rows_tile(joint ? joint : rows);
-    const size_t items = ((size_t)B + (joint > 0)) * Hkv * ((rows + tile - 1) / tile), slots = (size_t)kRowsMostWorkers + items;
+    const size_t items = ((size_t)B + (joint + tile - 1) / tile) * Hkv * ((rows + tile - 1) / tile), slots = (size_t)kRowsMostWorkers + items;
     RowsWorkspace w;
     w.part_lse = align256(slots * tile * d * 4);
     w.ends = w.part_lse + align256(slots * tile * 4);
@@ -853,10 +853,15 @@ PrefixWorkspace prefix_workspace(int B, int Hq, int Hkv, int Nq, int d) {
     return w;
 }
 
-// Query rows of all sequences where decode_rows takes the prefix too, 0 where it does not.
-int joint_rows(int B, int Hq, int Hkv, int Nq) {
-    const long long rows = (long long)B * (Hq / Hkv) * Nq;
-    return rows <= kRowsJoint ? (int)rows : 0;
+// Query rows of all sequences where decode_rows takes the prefix too, 0 where it does not: it reads the prefix once for each
+// 32 of them, which saves the other kernel's start and end where that is little work.  Up to 32 rows always (32 rows, 8 kv
+// heads, d = 128, 32768 shared tokens 39.2 us, the other kernel with 48 rows 38.1; 777 tokens 9.7 against 15.4); up to 128
+// rows by the work of the table's tokens (48 rows: 2000 tokens 14.2 against 19.5, 8192 24.3 against 24.1; 128 rows: 2000
+// tokens 23.0 against 25.4, 8192 43.4 against 31.0).  tokens: of the table; 0: where any table of such a batch would do.
+int joint_rows(int B, int Hq, int Hkv, int Nq, int d, long long tokens) {
+    const long long rows = (long long)B * (Hq / Hkv) * Nq, tiles = (rows + 31) / 32;
+    if (rows > 128 || Hq / Hkv * Nq > 32) return 0;
+    return tiles == 1 || tokens <= (12288ll * 8 * 128) / (tiles * Hkv * d) ? (int)rows : 0;
 }
 
 bool rows_sizes_ok(int B, int Hq, int Hkv, int Nq, int d) {
@@ -876,7 +881,7 @@ int rows_prepare(DecodeRowsLaunch& a, const void* q, const void* k_pages, const 
     if (!rows_sizes_ok(B, Hq, Hkv, Nq, d)) return FA_ERR_UNSUPPORTED;
     // steps of 64 keys over all sequences, kv heads and row tiles, and two more for each of these, are counted in 31 bits
     const int rows = Hq / Hkv * Nq, tile = rows_tile(rows);
-    if (((long long)B + 1) * Hkv * ((rows + tile - 1) / tile) > 0x7FFFFFFFll / (((long long)max_pages * page_size + block + 63) / 64 + 2))
+    if (((long long)B + 4) * Hkv * ((rows + tile - 1) / tile) > 0x7FFFFFFFll / (((long long)max_pages * page_size + block + 63) / 64 + 2))
         return FA_ERR_UNSUPPORTED;
     if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(o) || !aligned4(block_table) ||
         !aligned4(seq_lens) || !aligned4(lse))
@@ -1249,8 +1254,9 @@ int fa_decode_blocks(const void* q, const void* k_pages, const void* v_pages, co
 
 size_t fa_decode_shared_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d) {
     if (!rows_sizes_ok(B, Hq, Hkv, Nq, d)) return 0;
-    if (const int joint = joint_rows(B, Hq, Hkv, Nq)) return rows_workspace(B, Hq, Hkv, Nq, d, joint).bytes;
-    return rows_workspace(B, Hq, Hkv, Nq, d).bytes + prefix_workspace(B, Hq, Hkv, Nq, d).bytes;
+    // the larger of the two forms', whichever the table's width will choose
+    return std::max(rows_workspace(B, Hq, Hkv, Nq, d, joint_rows(B, Hq, Hkv, Nq, d, 0)).bytes,
+                    rows_workspace(B, Hq, Hkv, Nq, d).bytes + prefix_workspace(B, Hq, Hkv, Nq, d).bytes);
 }
 
 int fa_decode_shared(const void* q, const void* k_pages, const void* v_pages, const int* block_table, const int* seq_lens,
@@ -1264,7 +1270,7 @@ int fa_decode_shared(const void* q, const void* k_pages, const void* v_pages, co
     if (page_size % 8) return FA_ERR_UNSUPPORTED;  // boxes of 8 rows at least
     if (!aligned4(shared_len)) return FA_ERR_ALIGNMENT;
     a.shared = shared_len;
-    a.joint = joint_rows(B, Hq, Hkv, Nq);
+    a.joint = joint_rows(B, Hq, Hkv, Nq, d, (long long)max_pages * page_size);
     if (a.joint) {
         if (!workspace || workspace_bytes < rows_workspace(B, Hq, Hkv, Nq, d, a.joint).bytes) return FA_ERR_WORKSPACE;
         if (!aligned16(workspace)) return FA_ERR_ALIGNMENT;

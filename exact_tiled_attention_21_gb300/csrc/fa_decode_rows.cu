@@ -1,8 +1,8 @@
 // Attention of 1..16 new tokens per sequence over the paged bf16 cache: over the
 // blocks of a list, or over the tokens that follow a prefix which all sequences
 // share, and the merge of the parts.  The prefix itself is fa_prefix.cu's, or, where
-// all sequences together have no more than 32 query rows per kv head, one more
-// sequence here, whose rows are theirs: a kernel less.
+// all sequences together have few query rows per kv head, one more sequence here for
+// each 32 of them: a kernel less.
 //
 // 4 d bytes per key for 4 d flops per query row: bound by HBM.  The work is one
 // list of steps of 4 x KEYS keys over all sequences, kv heads and row tiles, cut
@@ -102,7 +102,7 @@ struct Params {
     const int* pre_ends;
     int B, Hkv, Nq, max_pages, num_pages, rows, row_tiles, workers, keep;
     int pre_tiles, pre_rows, pre_item;  // its tiles of pre_rows query rows; the first one's slots are CTA + pre_item
-    int joint;              // the prefix is this kernel's too, as sequence B with `joint` rows
+    int joint, tiles;       // the prefix is this kernel's too: `joint` rows, as `tiles` sequences B, B + 1, ... of ROWS each
     FastDiv page, block, per_row, heads;  // rows, Hkv
     float scale_log2;
     DevError* err;
@@ -121,15 +121,16 @@ __device__ __forceinline__ int keys_of(const Params& a, int len, int shared) {
     return len - shared_of(shared, len, a.Nq);
 }
 
-// The same of any place in the list of sequences; sequence B is the prefix, if it is this kernel's: every row sees all of it.
+// The same of any place in the list of sequences; from B on it is the prefix, if that is this kernel's: every row sees all
+// of it.
 template <bool LIST>
 __device__ __forceinline__ int length_of(const Params& a, int b, int cap, int shared) {
     if (b < a.B) return clamp_len(a.lens[b], cap);
-    return !LIST && a.joint && b == a.B ? shared + a.Nq : 0;
+    return !LIST && b < a.B + a.tiles ? shared + a.Nq : 0;
 }
 template <bool LIST>
 __device__ __forceinline__ int keys_in(const Params& a, int b, int len, int shared) {
-    if (!LIST && b >= a.B) return b == a.B && a.joint ? shared : 0;
+    if (!LIST && b >= a.B) return b < a.B + a.tiles ? shared : 0;
     return keys_of<LIST>(a, len, shared);
 }
 
@@ -161,7 +162,7 @@ __device__ __forceinline__ Scan scan_at(const Params& a, int cap, int shared, in
 
 // A position in the list of steps.
 struct Cursor {
-    int b, len, keys, n;  // sequence (B: the prefix), its length, its keys in this pass and their steps
+    int b, len, keys, n;  // sequence (from B on the prefix), its length, its keys in this pass and their steps
     int kvh, rt, s;       // kv head, row tile and step
 };
 
@@ -177,7 +178,7 @@ __device__ __forceinline__ void advance(Cursor& c, const Params& a, int cap, int
         ++c.b;
         c.len = length_of<LIST>(a, c.b, cap, shared);
         c.keys = keys_in<LIST>(a, c.b, c.len, shared);
-    } while (c.keys == 0 && c.b < a.B);
+    } while (c.keys == 0 && c.b < a.B + (LIST ? 0 : a.tiles));
     c.n = (c.keys + STEP - 1) / STEP;
 }
 
@@ -220,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, ROWS>::CTAS) decode_rows_kern
     {
         const Scan head = scan_at<STEP, LIST>(a, cap, shared, 0);
         uint32_t total = __shfl_sync(0xffffffffu, head.cost, 31);
-        const int all = a.B + (a.joint > 0);
+        const int all = a.B + (LIST ? 0 : a.tiles);
         for (int b0 = 32; b0 < all; b0 += 32) total += __shfl_sync(0xffffffffu, scan_at<STEP, LIST>(a, cap, shared, b0).cost, 31);
         const Share mine = share_of(total * per_step, a.workers, blockIdx.x);
         // the steps before a place in the list of costs, and the item and step there
@@ -313,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, ROWS>::CTAS) decode_rows_kern
             const int key = ahead.s * STEP + warp * KEYS + lane % KEYS;
             next.b = ahead.b;
             next.head = ahead.kvh;
-            const bool prefix = ahead.b == a.B;
+            const bool prefix = ahead.b >= a.B;
             if (prefix) next.b = from;
             next.tok = looked < count && key < ahead.keys ? (prefix ? key : key + ahead.len - ahead.keys) : kNone;
         }
@@ -359,7 +360,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, ROWS>::CTAS) decode_rows_kern
         for (int nb = 0; nb < NB; ++nb) {
             int r = cur.rt * ROWS + (rg * NB + nb) * 8 + g, b = cur.b;
             bool there = r < a.rows;
-            if (!LIST && cur.b == a.B) {  // row r of the prefix is row r % rows of sequence r / rows
+            if (!LIST && cur.b >= a.B) {  // row r of the prefix is row r % rows of sequence r / rows
+                r += (cur.b - a.B) * ROWS;
                 there = r < a.joint;
                 b = there ? r / a.rows : 0;
                 r -= b * a.rows;
@@ -393,9 +395,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, ROWS>::CTAS) decode_rows_kern
     // fragment addresses: rows of the lane's part of ldmatrix, and its piece of 16 bytes
     const int kr = lane % 16, kc = lane / 16, vr = lane % 8 + lane / 16 * 8, vc = lane / 8 % 2;
     for (int it = 0; it < count; ++it) {
-        const bool prefix = !LIST && cur.b == a.B;
+        const bool prefix = !LIST && cur.b >= a.B;
         const int r0 = cur.rt * ROWS + rg * NB * 8;                                           // of the warp
-        const int nrows = min(ROWS, (prefix ? a.joint : a.rows) - cur.rt * ROWS);             // of the tile
+        const int nrows = min(ROWS, prefix ? a.joint - (cur.b - a.B) * ROWS : a.rows - cur.rt * ROWS);  // of the tile
         const long long bh = (long long)cur.b * a.Hkv + cur.kvh;
         if (begins) {
             seg = cur.s;
@@ -680,7 +682,8 @@ __device__ __forceinline__ Parts find_parts(const Params& a, int b, int kvh, int
     if constexpr (!LIST) {
         shared = clamp_len(*a.shared, cap);
         place = (b * a.rows + row) / a.pre_rows;
-        pre = reinterpret_cast<const int2*>(a.pre_ends)[kvh * a.pre_tiles + place];
+        place = a.joint ? place * a.Hkv + kvh : kvh * a.pre_tiles + place;
+        pre = reinterpret_cast<const int2*>(a.pre_ends)[place];
     }
     const int2 own = reinterpret_cast<const int2*>(a.ends)[item];
     const int len = clamp_len(a.lens[b], cap);
@@ -690,7 +693,7 @@ __device__ __forceinline__ Parts find_parts(const Params& a, int b, int kvh, int
         x.n = own.y - own.x + 1;
     }
     if (!LIST && shared_of(shared, len, a.Nq) > 0) {
-        x.pslot = pre.x + a.pre_item + kvh * a.pre_tiles + place;
+        x.pslot = pre.x + a.pre_item + place;
         x.pn = pre.y - pre.x + 1;
     }
     x.done = x.n == 1 && x.pn == 0;
@@ -830,10 +833,11 @@ cudaError_t launch_l(const DecodeRowsLaunch& a, cudaStream_t s) {
     p.pre_rows = a.pre_rows;
     p.pre_item = 0;
     p.joint = a.joint;
+    p.tiles = (a.joint + ROWS - 1) / ROWS;
     if (a.joint) {  // its parts are among the others'
         p.pre_o = a.part_o;
         p.pre_lse = a.part_lse;
-        p.pre_tiles = 1;
+        p.pre_tiles = p.tiles;
         p.pre_rows = ROWS;
         p.pre_item = a.B * a.Hkv;
         p.pre_ends = a.ends + 2 * p.pre_item;
@@ -846,7 +850,7 @@ cudaError_t launch_l(const DecodeRowsLaunch& a, cudaStream_t s) {
     const long long most = LIST ? std::min((long long)a.keep * a.block, (long long)a.max_pages * a.page + a.block)
                                 : (long long)a.max_pages * a.page;
     p.workers = (int)std::min<long long>(std::min(C::CTAS * a.num_sms, kRowsMostWorkers),
-                                         ((long long)a.B + (a.joint > 0)) * a.Hkv * p.row_tiles * ((most + C::STEP - 1) / C::STEP));
+                                         ((long long)a.B + p.tiles) * a.Hkv * p.row_tiles * ((most + C::STEP - 1) / C::STEP));
     e = launch_dependent(a.Nq > 1 ? decode_rows_kernel<D, ROWS, true, LIST> : decode_rows_kernel<D, ROWS, false, LIST>,
                          dim3(p.workers), dim3(kThreads), C::SMEM, s, p);
     return e != cudaSuccess ? e : launch_merge<D, ROWS, LIST>(a, p, s);

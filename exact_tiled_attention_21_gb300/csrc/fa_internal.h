@@ -390,7 +390,6 @@ cudaError_t launch_prefix(const PrefixLaunch& a, cudaStream_t s);
 cudaError_t launch_decode_rows(const DecodeRowsLaunch& a, cudaStream_t s);  // the parts, then their merge
 // Query rows (of one kv head) that a pass over the keys serves: the tile that holds `rows`, or the largest.
 inline int rows_tile(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
-constexpr int kRowsJoint = 32;           // with that many query rows of all sequences together the prefix is decode_rows' too
 constexpr int kRowsMostWorkers = 512;    // CTAs of decode_rows at most (bounds the workspace; two on each of 152 SMs are 304)
 constexpr int kPrefixMostWorkers = 256;  // CTAs of the prefix at most
 // LSE-weighted merge of per-split partials into o (bf16) and lse (fp32, may be null).
