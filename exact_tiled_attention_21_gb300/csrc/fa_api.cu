@@ -887,8 +887,6 @@ int rows_prepare(DecodeRowsLaunch& a, const void* q, const void* k_pages, const 
         !aligned4(seq_lens) || !aligned4(lse))
         return FA_ERR_ALIGNMENT;
     if (o == q) return FA_ERR_INVALID_ARG;  // other CTAs may still read the row that one writes
-    st = device_state(&a.err, &a.num_sms);
-    if (st != FA_OK) return st;
     a.q = q;
     a.kp = k_pages;
     a.vp = v_pages;
@@ -1240,10 +1238,11 @@ int fa_decode_blocks(const void* q, const void* k_pages, const void* v_pages, co
                      int max_pages, int num_pages, int d, float scale, void* workspace, size_t workspace_bytes, void* stream) {
     if (!blocks || keep < 1) return FA_ERR_INVALID_ARG;
     DecodeRowsLaunch a;
-    const int st = rows_prepare(a, q, k_pages, v_pages, block_table, seq_lens, o, lse, B, Hq, Hkv, Nq, page_size, block,
-                                max_pages, num_pages, d, scale);
+    int st = rows_prepare(a, q, k_pages, v_pages, block_table, seq_lens, o, lse, B, Hq, Hkv, Nq, page_size, block, max_pages,
+                          num_pages, d, scale);
     if (st != FA_OK) return st;
     if (!aligned4(blocks)) return FA_ERR_ALIGNMENT;
+    if ((st = device_state(&a.err, &a.num_sms)) != FA_OK) return st;
     if (!workspace || workspace_bytes < rows_workspace(B, Hq, Hkv, Nq, d).bytes) return FA_ERR_WORKSPACE;
     if (!aligned16(workspace)) return FA_ERR_ALIGNMENT;
     rows_place(a, static_cast<char*>(workspace));
@@ -1269,6 +1268,7 @@ int fa_decode_shared(const void* q, const void* k_pages, const void* v_pages, co
     if (st != FA_OK) return st;
     if (page_size % 8) return FA_ERR_UNSUPPORTED;  // boxes of 8 rows at least
     if (!aligned4(shared_len)) return FA_ERR_ALIGNMENT;
+    if ((st = device_state(&a.err, &a.num_sms)) != FA_OK) return st;
     a.shared = shared_len;
     a.joint = joint_rows(B, Hq, Hkv, Nq, d, (long long)max_pages * page_size);
     if (a.joint) {
