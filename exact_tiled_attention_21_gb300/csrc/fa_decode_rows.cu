@@ -13,6 +13,10 @@
 // results go to the workspace at slot CTA + item (which grows by one from each
 // segment to the next), and a second kernel merges the segments of each row.
 //
+// Where a list's items are few enough for a CTA of their own each, a cluster of up to
+// eight takes an item, a run of its steps each, and joins the parts through its
+// shared memories: no second kernel.
+//
 // A CTA has four warps.  Each streams KEYS keys per step through a ring of its own
 // of cp.async copies, three steps deep, and holds 8 query rows, or 16 where there
 // are more; with 32 two warps read each other's keys, each for rows of its own.
@@ -101,6 +105,8 @@ struct Params {
     const float* pre_lse;
     const int* pre_ends;
     int B, Hkv, Nq, max_pages, num_pages, rows, row_tiles, workers, keep;
+    int cluster;            // CTAs of an item (LIST), 0: shares of all items' steps
+    int pre_workers;        // its CTAs
     int pre_tiles, pre_rows, pre_item;  // its tiles of pre_rows query rows; the first one's slots are CTA + pre_item
     int joint, tiles;       // the prefix is this kernel's too: `joint` rows, as `tiles` sequences B, B + 1, ... of ROWS each
     FastDiv page, block, per_row, heads;  // rows, Hkv
@@ -182,6 +188,21 @@ __device__ __forceinline__ void advance(Cursor& c, const Params& a, int cap, int
     c.n = (c.keys + STEP - 1) / STEP;
 }
 
+constexpr int kMostCluster = 8;
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr, uint32_t rank) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(mapa_shared(addr, rank)) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr, uint32_t rank) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(mapa_shared(addr, rank))
+                 : "memory");
+    return v;
+}
+
 constexpr int kNone = INT_MAX;  // in the place of a token: no such key
 
 // DRAFTS: more than one new token per sequence.
@@ -218,7 +239,18 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, ROWS>::CTAS) decode_rows_kern
     const uint32_t per_step = (uint32_t)a.Hkv * a.row_tiles;
     Cursor cur;
     int count;
-    {
+    if (LIST && a.cluster) {  // a part of one item, perhaps none
+        const uint32_t item = blockIdx.x / (uint32_t)a.cluster, bh = item / (uint32_t)a.row_tiles;
+        cur.b = (int)a.heads.div(bh);
+        cur.kvh = (int)bh - cur.b * a.Hkv;
+        cur.rt = (int)(item - bh * a.row_tiles);
+        cur.len = clamp_len(a.lens[cur.b], cap);
+        cur.keys = keys_of<LIST>(a, cur.len, shared);
+        cur.n = (cur.keys + STEP - 1) / STEP;
+        const Share mine = share_of((uint32_t)cur.n, a.cluster, blockIdx.x % (uint32_t)a.cluster);
+        cur.s = (int)mine.first;
+        count = (int)mine.count;
+    } else {
         const Scan head = scan_at<STEP, LIST>(a, cap, shared, 0);
         uint32_t total = __shfl_sync(0xffffffffu, head.cost, 31);
         const int all = a.B + (LIST ? 0 : a.tiles);
@@ -626,7 +658,21 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, ROWS>::CTAS) decode_rows_kern
                 }
                 if (nb + 1 < NB) __syncthreads();
             }
-            if (kg == 0) {
+            if (kg == 0 && LIST && a.cluster) {  // into this CTA's shared memory, whose ring is done with
+                float* to = reinterpret_cast<float*>(smem);
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int r = (rg * NB + nb) * 8 + 2 * t + j;
+#pragma unroll
+                        for (int i = 0; i < D / 16; ++i) {
+                            to[r * D + 16 * i + g] = acc[nb][i][j];
+                            to[r * D + 16 * i + 8 + g] = acc[nb][i][2 + j];
+                        }
+                        if (g == 0) to[ROWS * D + r] = l[nb][j] == 0.f ? -INFINITY : m[nb][j] + lg2(l[nb][j]);
+                    }
+            } else if (kg == 0) {
                 const bool whole = seg == 0 && item_ends && !prefix && (LIST || shared_of(shared, done.len, Nq) == 0);
                 const long long item = bh * a.row_tiles + done.rt, slot_out = blockIdx.x + item;
                 if (tid == 0 && seg == 0) a.ends[2 * item] = blockIdx.x;
@@ -662,6 +708,42 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, ROWS>::CTAS) decode_rows_kern
         }
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
+    if (LIST && a.cluster) {
+        // the rows in turn to the cluster's CTAs: LSE = M + log2 sum 2^(lse_c - M), O = sum 2^(lse_c - M) o_c / sum
+        float* mine = reinterpret_cast<float*>(smem);
+        if (count == 0 && tid < ROWS) mine[ROWS * D + tid] = -INFINITY;
+        if (a.cluster > 1) cluster_sync(); else __syncthreads();
+        const int rank = blockIdx.x % a.cluster, bh = cur.b * a.Hkv + cur.kvh;
+        constexpr int LANES = D / 4, AT_ONCE = kThreads / LANES;  // four columns of a row per thread
+        const int col = tid % LANES * 4, nrows = min(ROWS, a.rows - cur.rt * ROWS);
+        for (int r = rank * AT_ONCE + tid / LANES; r < nrows; r += a.cluster * AT_ONCE) {
+            float lse[kMostCluster], M = -INFINITY, sum = 0.f;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int c = 0; c < kMostCluster; ++c) {
+                lse[c] = c < a.cluster ? ld_cluster_f32(smem_u32(mine + ROWS * D + r), c) : -INFINITY;
+                M = fmaxf(M, lse[c]);
+            }
+            const float base = M == -INFINITY ? 0.f : M;
+#pragma unroll
+            for (int c = 0; c < kMostCluster; ++c) {
+                const float f = ex2(lse[c] - base);
+                sum += f;
+                if (c < a.cluster && f != 0.f) {  // a part without keys is nothing, whatever is in its place; NaN stays
+                    const float4 x = ld_cluster_f4(smem_u32(mine + r * D + col), c);
+                    o.x = fmaf(f, x.x, o.x);
+                    o.y = fmaf(f, x.y, o.y);
+                    o.z = fmaf(f, x.z, o.z);
+                    o.w = fmaf(f, x.w, o.w);
+                }
+            }
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            const long long row = (long long)bh * a.rows + cur.rt * ROWS + r;
+            *reinterpret_cast<uint2*>(a.o + row * D + col) = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+            if (a.lse && col == 0) a.lse[row] = sum == 0.f ? -INFINITY : (M + lg2(sum)) * kLn2;
+        }
+        if (a.cluster > 1) cluster_sync();  // the others have read this CTA's
+    }
     if (__any_sync(0xffffffffu, bad) && lane == 0) record_invalid(a.err, kSiteCacheTable, -1);
 }
 
@@ -692,7 +774,8 @@ __device__ __forceinline__ Parts find_parts(const Params& a, int b, int kvh, int
         x.slot = (long long)own.x + item;
         x.n = own.y - own.x + 1;
     }
-    if (!LIST && shared_of(shared, len, a.Nq) > 0) {
+    // (a prefix kernel whose waits ran out may not have noted its items' ends)
+    if (!LIST && shared_of(shared, len, a.Nq) > 0 && pre.x >= 0 && pre.x <= pre.y && pre.y < a.pre_workers) {
         x.pslot = pre.x + a.pre_item + place;
         x.pn = pre.y - pre.x + 1;
     }
@@ -797,6 +880,24 @@ cudaError_t launch_merge(const DecodeRowsLaunch& a, const Params& p, cudaStream_
                             s, p);
 }
 
+template <int D, int ROWS>
+cudaError_t launch_clusters(const DecodeRowsLaunch& a, const Params& p, int ctas, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Cfg<D, ROWS>::SMEM;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {(unsigned)p.cluster, 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return a.Nq > 1 ? cudaLaunchKernelEx(&cfg, decode_rows_kernel<D, ROWS, true, true>, p)
+                    : cudaLaunchKernelEx(&cfg, decode_rows_kernel<D, ROWS, false, true>, p);
+}
+
 template <int D, int ROWS, bool LIST>
 cudaError_t launch_l(const DecodeRowsLaunch& a, cudaStream_t s) {
     using C = Cfg<D, ROWS>;
@@ -829,6 +930,7 @@ cudaError_t launch_l(const DecodeRowsLaunch& a, cudaStream_t s) {
     p.per_row = FastDiv((uint32_t)p.rows);
     p.heads = FastDiv((uint32_t)a.Hkv);
     p.keep = a.keep;
+    p.pre_workers = a.pre_workers;
     p.pre_tiles = a.pre_tiles;
     p.pre_rows = a.pre_rows;
     p.pre_item = 0;
@@ -849,8 +951,22 @@ cudaError_t launch_l(const DecodeRowsLaunch& a, cudaStream_t s) {
     // no more CTAs than steps at full lengths
     const long long most = LIST ? std::min((long long)a.keep * a.block, (long long)a.max_pages * a.page + a.block)
                                 : (long long)a.max_pages * a.page;
-    p.workers = (int)std::min<long long>(std::min(C::CTAS * a.num_sms, kRowsMostWorkers),
+    const int slots = std::min(C::CTAS * a.num_sms, kRowsMostWorkers);  // CTAs that run at once
+    p.cluster = 0;
+    const long long items = (long long)a.B * a.Hkv * p.row_tiles;
+    if (LIST && items <= slots) {
+        p.cluster = 1;
+        const long long steps = (most + C::STEP - 1) / C::STEP;  // of an item
+        while (p.cluster < kMostCluster && items * p.cluster * 2 <= slots && steps > p.cluster) p.cluster *= 2;
+        // unless a few items leave most SMs idle: the second kernel costs about three steps (8 items of 64 steps: 11.5 us in
+        // clusters, 9.5 in shares; 32 of 10: 10.2 and 12.2; 256 of 16, alone: 25.4 and 28.5)
+        if ((steps + p.cluster - 1) / p.cluster <= (steps * items + slots - 1) / slots + 3)
+            return launch_clusters<D, ROWS>(a, p, (int)(items * p.cluster), s);
+        p.cluster = 0;
+    }
+    p.workers = (int)std::min<long long>(slots,
                                          ((long long)a.B + p.tiles) * a.Hkv * p.row_tiles * ((most + C::STEP - 1) / C::STEP));
+    if (a.joint) p.pre_workers = p.workers;
     e = launch_dependent(a.Nq > 1 ? decode_rows_kernel<D, ROWS, true, LIST> : decode_rows_kernel<D, ROWS, false, LIST>,
                          dim3(p.workers), dim3(kThreads), C::SMEM, s, p);
     return e != cudaSuccess ? e : launch_merge<D, ROWS, LIST>(a, p, s);

@@ -177,3 +177,18 @@ def test_bad_entries_pages_and_lengths(cuda_lib):
     o, lse = fa.decode_blocks(q.to(DEV), g["k"], g["v"], ints(table), ints([-7, 1000]), ints(good), block=block)
     assert fa.fa_get_last_device_error()[0] == fa.FA_ERR_INVALID_ARG
     check_rows(o, lse, op.attend(f64(q), c, table, [0, 80], 0.125, op.tokens_of(good, block)), PAIR)
+
+
+@pytest.mark.parametrize("G,Nq,d", [(4, 1, 128), (4, 3, 64), (3, 8, 128)])
+def test_many_sequences(cuda_lib, G, Nq, d):
+    """More (sequence, kv head) pairs than CTAs run at once, of very different lengths, some of them empty."""
+    rng = np.random.default_rng(G + Nq)
+    B, Hkv, page, block, keep, scale = 80, 5, 32, 16, 12, 1.0 / math.sqrt(d)
+    lens = [int(n) for n in rng.integers(0, 400, B)]
+    lens[:4] = [0, 1, 0, 399]
+    c, table = random_pages(5, B * 13, Hkv, page, d), table_of(6, B, 13, B * 13)
+    lists = _lists(rng, lens, Hkv, block, keep)
+    g, q = to_gpu(c), bf16(rng, (B, Hkv * G, Nq, d), 0.3)
+    o, lse = cuda_lib.decode_blocks(q.to(DEV), g["k"], g["v"], ints(table), ints(lens), ints(lists), block=block)
+    ok(cuda_lib)
+    check_rows(o, lse, op.attend(f64(q), c, table, lens, scale, op.tokens_of(lists, block)), PAIR)

@@ -142,3 +142,55 @@ def test_bad_pages_and_lengths(cuda_lib):
     o, lse = fa.decode_shared(q.to(DEV), g["k"], g["v"], ints(table), ints([-1, 70]), ints([shared]))
     assert fa.fa_get_last_device_error()[0] == fa.FA_ERR_INVALID_ARG
     check_rows(o, lse, op.attend(f64(q), c, table, [0, 70], 0.125), ONE)
+
+
+@pytest.mark.parametrize("B,G,Nq,d", [(3, 2, 3, 128), (3, 8, 4, 64), (20, 4, 4, 128)])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+def test_wild_values_of_drafted_tokens_stay_with_the_queries_that_see_them(cuda_lib, B, G, Nq, d, value):
+    """Own tokens that some of the drafted queries see and others do not, beside a shared prefix; 20 sequences of 16 rows go
+    through the prefix's matrix kernel."""
+    rng = np.random.default_rng(G + d)
+    Hkv, page, shared = 2, 16, 150
+    lens = shared + rng.integers(Nq, 70, B)
+    c, table = _case(7, lens, shared, Hkv, page, d)
+    for b, n in enumerate(lens):
+        for i, col in ((1, 3), (2, 17)):                 # the last token and the one before
+            c["v"][table[b][(n - i) // page], b % Hkv, (n - i) % page, col] = value
+    g, q = to_gpu(c), bf16(rng, (B, Hkv * G, Nq, d), 0.3)
+    o, lse = cuda_lib.decode_shared(q.to(DEV), g["k"], g["v"], ints(table), ints(lens), ints([shared]))
+    ok(cuda_lib)
+    c["v"][~np.isfinite(c["v"])] = 0.0
+    ref = op.attend(f64(q), c, table, lens, 1 / math.sqrt(d))
+    got, want = f64(o), np.zeros_like(ref[0], dtype=bool)
+    for b in range(B):
+        heads = slice(b % Hkv * G, (b % Hkv + 1) * G)
+        want[b, heads, Nq - 1, 3] = True                 # the last token is seen by the last query alone
+        want[b, heads, Nq - 2:, 17] = True
+    assert np.array_equal(~np.isfinite(got), want)
+    if not math.isnan(value):
+        assert (got[want] == value).all()
+    check_rows(torch.from_numpy(np.where(want, ref[0], got)), lse, ref, ONE)
+
+
+def test_wild_values_of_the_prefix_and_of_its_page(cuda_lib):
+    """A NaN in a shared value reaches every sequence that takes part, one behind the prefix in its last page none."""
+    rng = np.random.default_rng(1)
+    Hkv, G, d, page, shared = 1, 4, 128, 16, 150
+    for B in (3, 40):
+        lens = np.full(B, shared + 2)
+        lens[1] = 0
+        c, table = _case(8, lens, shared, Hkv, page, d)
+        last = table[:, shared // page]
+        c["k"][last, :, shared % page + 2:] = np.nan
+        c["v"][last, :, shared % page + 2:] = np.inf
+        q = bf16(rng, (B, G, 1, d), 0.3)
+        g = to_gpu(c)
+        o, lse = cuda_lib.decode_shared(q.to(DEV), g["k"], g["v"], ints(table), ints(lens), ints([shared]))
+        ok(cuda_lib)
+        check_rows(o, lse, op.attend(f64(q), c, table, lens, 1 / math.sqrt(d)), ONE)
+        c["v"][table[0, 3], 0, 5, 40] = np.nan
+        g = to_gpu(c)
+        o, lse = cuda_lib.decode_shared(q.to(DEV), g["k"], g["v"], ints(table), ints(lens), ints([shared]))
+        ok(cuda_lib)
+        there = np.isnan(f64(o))
+        assert there[lens > 0, :, :, 40].all() and there.sum() == (B - 1) * G
