@@ -45,6 +45,9 @@ struct Pre {
     static_assert(SMEM <= 232448, "shared memory budget");
 };
 
+// What a CTA's second (kv head, tile of rows) costs, in steps: queries, a start of the pipeline and a part to write.
+constexpr uint32_t kCrossing = 2;
+
 struct PreParams {
     const __nv_bfloat16* q;
     const int* table;   // int32 [B, max_pages]
@@ -106,8 +109,14 @@ prefix_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
         const uint32_t hit = __ballot_sync(0xffffffffu, b0 + lane < p.B && min(max(p.lens[min(b0 + lane, p.B - 1)], 0), cap) - p.Nq >= shared);
         if (hit) from = b0 + __ffs(hit) - 1;
     }
-    const uint32_t steps = (uint32_t)(shared + 127) / 128;  // of an item, a (kv head, tile of rows)
-    const Share mine = share_of(from >= 0 ? steps * p.Hkv * p.tiles : 0, gridDim.x, blockIdx.x);
+    const uint32_t steps = from < 0 ? 0 : (uint32_t)(shared + 127) / 128;  // of an item, a (kv head, tile of rows)
+    const uint32_t items = (uint32_t)p.Hkv * p.tiles, per = gridDim.x / items;
+    Share mine = share_of(steps * items, gridDim.x, blockIdx.x);
+    if (per && (steps + per - 1) / per <= (steps * items + gridDim.x - 1) / gridDim.x + kCrossing) {  // `per` CTAs for each item
+        const uint32_t item = blockIdx.x / per;
+        mine = item < items ? share_of(steps, per, blockIdx.x - item * per) : Share{0, 0};
+        mine.first += item * steps;
+    }
     const uint32_t u0 = mine.first, u1 = u0 + mine.count, c = blockIdx.x;
     const int all = p.B * p.rows;  // rows of a kv head
     // one role's walk over the CTA's segments: item, its steps [s0, s1)
