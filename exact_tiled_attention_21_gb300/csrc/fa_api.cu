@@ -853,15 +853,22 @@ PrefixWorkspace prefix_workspace(int B, int Hq, int Hkv, int Nq, int d) {
     return w;
 }
 
+// Up to 8 query rows of a sequence and kv head, the prefix's kernel takes the own tokens too.
+bool prefix_takes_own(int Hq, int Hkv, int Nq) { return rows_tile(Hq / Hkv * Nq) == 8; }
+
 // Query rows of all sequences where decode_rows takes the prefix too, 0 where it does not: it reads the prefix once for each
-// 32 of them, which saves the other kernel's start and end where that is little work.  Up to 32 rows always (32 rows, 8 kv
-// heads, d = 128, 32768 shared tokens 39.2 us, the other kernel with 48 rows 38.1; 777 tokens 9.7 against 15.4); up to 128
-// rows by the work of the table's tokens (48 rows: 2000 tokens 14.2 against 19.5, 8192 24.3 against 24.1; 128 rows: 2000
-// tokens 23.0 against 25.4, 8192 43.4 against 31.0).  tokens: of the table; 0: where any table of such a batch would do.
+// 32 of them, which saves the other kernel's start and end where that is little work.  Measured with 4 heads per kv head, 8
+// kv heads, d = 128 against the prefix's kernel with the own tokens in it: 32 rows, 500 tokens 10.2 and 11.9 us, 2000 13.5
+// and 13.3, 8000 20.2 and 17.2; 64 rows 11.7 and 12.4, 14.4 and 14.5, 25.5 and 18.2; 128 rows, 500 tokens 15.8 and 15.0.
+// Against it and a kernel of their own: 48 rows, 2000 tokens 14.2 and 19.5, 8192 24.3 and 24.1; 128 rows 23.0 and 25.4,
+// 43.4 and 31.0; 32 rows, 32768 tokens 39.2 and (48 rows) 38.1.  tokens: of the table; 0: where any table of such a batch
+// would do.
 int joint_rows(int B, int Hq, int Hkv, int Nq, int d, long long tokens) {
     const long long rows = (long long)B * (Hq / Hkv) * Nq, tiles = (rows + 31) / 32;
     if (rows > 128 || Hq / Hkv * Nq > 32) return 0;
-    return tiles == 1 || tokens <= (12288ll * 8 * 128) / (tiles * Hkv * d) ? (int)rows : 0;
+    const bool own = prefix_takes_own(Hq, Hkv, Nq);
+    const long long most = (own ? tiles <= 2 ? 4096ll : 2048ll : 12288ll) * 8 * 128;  // elements of keys
+    return (tiles == 1 && !own) || tokens <= most / (tiles * Hkv * d) ? (int)rows : 0;
 }
 
 bool rows_sizes_ok(int B, int Hq, int Hkv, int Nq, int d) {
@@ -909,6 +916,7 @@ int rows_prepare(DecodeRowsLaunch& a, const void* q, const void* k_pages, const 
     a.num_pages = num_pages;
     a.d = d;
     a.pre_workers = a.pre_tiles = a.pre_rows = a.joint = 0;
+    a.merge_only = false;
     a.scale = scale;
     return FA_OK;
 }
@@ -1305,7 +1313,9 @@ int fa_decode_shared(const void* q, const void* k_pages, const void* v_pages, co
     p.d = d;
     p.tiles = pw.tiles;
     p.tile_rows = pw.tile_rows;
-    p.workers = (int)std::min<long long>(std::min(a.num_sms, kPrefixMostWorkers), most * Hkv * pw.tiles);  // a step each
+    p.own = prefix_takes_own(Hq, Hkv, Nq);
+    p.workers = std::min(a.num_sms, kPrefixMostWorkers);
+    if (!p.own) p.workers = (int)std::min<long long>(p.workers, most * Hkv * pw.tiles);  // a step each
     p.scale = scale;
     p.err = a.err;
     p.timeout_ns = g_timeout_ns.load();
@@ -1320,7 +1330,8 @@ int fa_decode_shared(const void* q, const void* k_pages, const void* v_pages, co
     a.pre_workers = p.workers;
     a.pre_tiles = p.tiles;
     a.pre_rows = p.tile_rows;
-    st = launched(launch_prefix(p, (cudaStream_t)stream));
+    a.merge_only = p.own;
+    st = launched(launch_prefix(p, a, (cudaStream_t)stream));
     return st != FA_OK ? st : launched(launch_decode_rows(a, (cudaStream_t)stream));
 }
 

@@ -284,6 +284,7 @@ struct PrefixLaunch {
     float* part_lse;           // fp32 [workers + Hkv * tiles, tile_rows]
     int* ends;                 // int32 [Hkv * tiles, 2]: the CTAs of an item's first and last step
     int B, Hq, Hkv, Nq, page, box, max_pages, num_pages, d, tiles, tile_rows, workers;
+    bool own;                  // the own tokens are this kernel's too (up to 8 rows of a sequence and kv head)
     float scale;
     DevError* err;
     uint64_t timeout_ns;
@@ -307,6 +308,7 @@ struct DecodeRowsLaunch {
     const int* pre_ends;
     int B, Hq, Hkv, Nq, page, block, keep, max_pages, num_pages, d;
     int pre_workers, pre_tiles, pre_rows;
+    bool merge_only;       // the prefix kernel did the rest
     int joint;             // query rows of all sequences per kv head where the prefix is this kernel's too, else 0
     int num_sms;
     float scale;
@@ -386,7 +388,7 @@ inline int fp8_tile_rows(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32
 cudaError_t decode_fp8_blocks_per_sm(int d, int tile_rows, int* blocks);  // resident CTAs of its first kernel on one SM
 cudaError_t launch_paged_append(const PagedAppendLaunch& a, cudaStream_t s);
 cudaError_t launch_select_blocks(const SelectLaunch& a, cudaStream_t s);
-cudaError_t launch_prefix(const PrefixLaunch& a, cudaStream_t s);
+cudaError_t launch_prefix(const PrefixLaunch& a, const DecodeRowsLaunch& rows, cudaStream_t s);
 cudaError_t launch_decode_rows(const DecodeRowsLaunch& a, cudaStream_t s);  // the parts, then their merge
 // Query rows (of one kv head) that a pass over the keys serves: the tile that holds `rows`, or the largest.
 inline int rows_tile(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }

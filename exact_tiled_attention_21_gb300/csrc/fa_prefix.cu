@@ -18,13 +18,25 @@
 //               tile's query rows, which come from all sequences, into shared memory
 //               and write the part of each row, O / l in fp32 and its LSE.
 // Work: steps of 128 keys over (kv head, 256 rows), cut into equal shares for the
-// CTAs; the part of a (kv head, 256 rows) that a CTA holds goes to the workspace at
-// slot CTA + item, and the merge of fa_decode_rows.cu joins the parts with each
-// sequence's own.  Rows of a sequence that does not see all of the prefix are
-// computed and not written: its own pass takes all its keys.
+// CTAs, or an equal number of CTAs for each (kv head, 256 rows) where that costs a few
+// steps at most: a second start of the pipeline and a second part to write cost four
+// (64 sequences, 512 rows per kv head, 32768 tokens: 111 us against 106).  The part of
+// a (kv head, 256 rows) that a CTA holds goes to the workspace at slot CTA + item, and
+// the merge of fa_decode_rows.cu joins the parts with each sequence's own.  Rows of a
+// sequence that does not see all of the prefix are computed and not written: its own
+// pass takes all its keys.
+//
+// Up to 8 rows of a sequence and kv head, the own tokens are this kernel's too: the
+// prefix is bound by the tensor cores or, where it is short, by latencies, the own
+// tokens by HBM, and run after one another they wait for each other's start and end.
+// The CTAs are divided by the times that both would take; one with own tokens runs
+// fa_decode_rows.cuh twice, on four warps each.  (32 sequences, 8192 shared tokens and up
+// to 512 own ones, 4 heads per kv head: 31.3 us in two kernels, 23.7 in one; 64, 32768
+// and 1000, two new tokens: 106 and 94.)  With 16 rows and more the own tokens' registers
+// do not fit beside.
 #include <algorithm>
 
-#include "fa_internal.h"
+#include "fa_decode_rows.cuh"
 #include "fa_softmax.cuh"
 
 namespace fa {
@@ -35,7 +47,10 @@ struct Pre {
     static constexpr int BN = 128, KCH = D / 64;
     static constexpr int Q_BYTES = 128 * D * 2, KV_BYTES = BN * D * 2, CHUNK = 128 * 128;
     static constexpr int NSLOT = D == 128 ? 5 : 8;
-    static constexpr int OFF_Q = 0, OFF_KV = 2 * Q_BYTES, OFF_BAR = OFF_KV + NSLOT * KV_BYTES;
+    static constexpr int OFF_Q = 0, OFF_KV = 2 * Q_BYTES;
+    static constexpr int ROWS_BYTES = Cfg<D, 8>::SMEM, OFF_SHARED = 2 * ROWS_BYTES;  // the own tokens' two lots of four warps
+    static constexpr int OFF_BAR = std::max(OFF_KV + NSLOT * KV_BYTES, OFF_SHARED + 2 * 1024);
+    static_assert(sizeof(RowsShared<8>) <= 1024 && ROWS_BYTES % 128 == 0, "layout");
     // barriers: kv_full[NSLOT], kv_empty[NSLOT], q_full[2], s_full[2], p_full[2], o_final[2], pv_done, teardown
     static constexpr int NBAR = 2 * NSLOT + 10, OFF_MISC = OFF_BAR + NBAR * 8, SMEM = OFF_MISC + 16 + 1024;
     static constexpr int THREADS = 320;
@@ -46,7 +61,19 @@ struct Pre {
 };
 
 // What a CTA's second (kv head, tile of rows) costs, in steps: queries, a start of the pipeline and a part to write.
-constexpr uint32_t kCrossing = 2;
+constexpr uint32_t kCrossing = 4;
+
+// What the CTAs are divided by, in microseconds, from timings of nine batches at eight to twenty divisions each (64 sequences,
+// 4096 shared tokens and up to 1000 own ones: 83.7 us with 8 CTAs for the prefix, 41.9 with 32, 51.1 with 64, 132 with 128): a
+// step of the prefix, of one tile and of two, how much later a CTA's first is done than one of own tokens, and a second item;
+// of own tokens, a step of four warps, and an item's start and end, both beside a prefix.  The times are within a tenth of
+// the best division's.
+template <int D, int OWN>
+struct Times {
+    static constexpr float ONE_STEP = D == 128 ? 0.92f : 0.75f, TWO_STEP = D == 128 ? 1.8f : 1.45f;
+    static constexpr float ONE_START = 5.f, TWO_START = D == 128 ? 9.f : 5.f, CROSSING = 6.5f;
+    static constexpr float OWN_STEP = D == 64 ? 1.1f : OWN == 2 ? 1.45f : 1.2f, OWN_ITEM = D == 64 ? 1.6f : 2.5f;
+};
 
 struct PreParams {
     const __nv_bfloat16* q;
@@ -63,9 +90,10 @@ struct PreParams {
     uint64_t timeout_ns;
 };
 
-template <int D>
+template <int D, int OWN>
 __global__ void __launch_bounds__(Pre<D>::THREADS, 1)
-prefix_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const PreParams p) {
+prefix_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const PreParams p,
+              const __grid_constant__ Params own) {
     using C = Pre<D>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -104,18 +132,39 @@ prefix_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
     pdl_wait();
 
     const int cap = p.max_pages * p.page, given = *p.shared, shared = min(max(given, 0), cap);
+    if (blockIdx.x == 0) check_lengths(p.lens, OWN > 0 ? p.B : 0, cap, given, p.err);
     int from = -1;  // the first sequence that sees all of the prefix
     for (int b0 = 0; b0 < p.B && from < 0; b0 += 32) {
         const uint32_t hit = __ballot_sync(0xffffffffu, b0 + lane < p.B && min(max(p.lens[min(b0 + lane, p.B - 1)], 0), cap) - p.Nq >= shared);
         if (hit) from = b0 + __ffs(hit) - 1;
     }
     const uint32_t steps = from < 0 ? 0 : (uint32_t)(shared + 127) / 128;  // of an item, a (kv head, tile of rows)
-    const uint32_t items = (uint32_t)p.Hkv * p.tiles, per = gridDim.x / items;
-    Share mine = share_of(steps * items, gridDim.x, blockIdx.x);
-    if (per && (steps + per - 1) / per <= (steps * items + gridDim.x - 1) / gridDim.x + kCrossing) {  // `per` CTAs for each item
+    const uint32_t items = (uint32_t)p.Hkv * p.tiles;
+    uint32_t ctas = gridDim.x;  // of the prefix; the others have the own tokens
+    if constexpr (OWN > 0) {
+        using T = Times<D, OWN>;
+        const uint2 cost = cost_of_all<Cfg<D, 8>::STEP, false>(own, cap, shared);  // of one kv head's items: steps and costs
+        const float each = (float)(own.Hkv * own.row_tiles),
+                    rest = each * (T::OWN_STEP * (float)cost.x + T::OWN_ITEM * (float)(cost.y - cost.x));
+        const float step = p.tile_rows > 128 ? T::TWO_STEP : T::ONE_STEP, start = p.tile_rows > 128 ? T::TWO_START : T::ONE_START;
+        // a lane has two divisions to compare: n CTAs, the same number for each item, and fewer than items
+        const uint32_t most = (gridDim.x - 1) / items, few = min(items, gridDim.x);
+        const uint32_t k = (lane + 1) * most / 32, n0 = k * items, n1 = max((lane + 1) * few / 33, 1u);
+        const float time0 = k ? fmaxf(start + step * ceilf(__fdividef((float)steps, (float)k)), __fdividef(rest, (float)(2 * (gridDim.x - n0))))
+                              : FLT_MAX,
+                    time1 = fmaxf(start + __fdividef((float)items, (float)n1) * (step * (float)steps + T::CROSSING),
+                                  __fdividef(rest, (float)(2 * (gridDim.x - n1))));
+        const uint32_t mine = __float_as_uint(fminf(time0, time1)), least = __reduce_min_sync(0xffffffffu, mine);
+        ctas = steps ? __reduce_min_sync(0xffffffffu, mine == least ? (time0 <= time1 ? n0 : n1) : ~0u) : 0;
+    }
+    const uint32_t per = ctas / items;
+    Share mine = {0, 0};
+    if (per && (steps + per - 1) / per <= (steps * items + ctas - 1) / ctas + kCrossing) {  // `per` CTAs for each item
         const uint32_t item = blockIdx.x / per;
-        mine = item < items ? share_of(steps, per, blockIdx.x - item * per) : Share{0, 0};
+        if (item < items) mine = share_of(steps, per, blockIdx.x - item * per);
         mine.first += item * steps;
+    } else if (blockIdx.x < ctas) {
+        mine = share_of(steps * items, ctas, blockIdx.x);
     }
     const uint32_t u0 = mine.first, u1 = u0 + mine.count, c = blockIdx.x;
     const int all = p.B * p.rows;  // rows of a kv head
@@ -135,7 +184,15 @@ prefix_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
         return g;
     };
 
-    if (warp == 8) {
+    if (OWN > 0 && blockIdx.x >= ctas) {
+        // ------------------------------------------------------------ own tokens
+        if (warp < 8) {
+            const int half = warp >> 2;
+            decode_rows<D, 8, OWN == 2, false, true>(own, smem + half * C::ROWS_BYTES,
+                                                     reinterpret_cast<RowsShared<8>*>(smem + C::OFF_SHARED)[half], tid & 127,
+                                                     2 * (blockIdx.x - ctas) + half, 2 * (gridDim.x - ctas), 1 + half);
+        }
+    } else if (warp == 8) {
         // ------------------------------------------------------------ TMA producer (whole warp)
         const uint64_t policy = l2_policy_evict_first();
         if (lane == 0) {
@@ -298,7 +355,6 @@ prefix_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
     } else {
         // ------------------------------------------------------------ queries, softmax, epilogue
         const int t = warp >> 2, r = tid & 127;  // tile; row within it = TMEM lane
-        if (c == 0 && tid == 0 && given != shared) record_invalid(p.err, kSiteCacheLen, given);
         const uint32_t lane_addr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t col_o = C::COL_O + D * t;
         // handoffs before the segment: of the scores' buffers, of the products of one tile, of the ring's fills; of O so far
@@ -426,10 +482,10 @@ prefix_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
     }
 }
 
-template <int D>
-cudaError_t launch_d(const PrefixLaunch& a, cudaStream_t s) {
+template <int D, int OWN>
+cudaError_t launch_o(const PrefixLaunch& a, const DecodeRowsLaunch& rows, cudaStream_t s) {
     using C = Pre<D>;
-    cudaError_t e = set_smem_limit_once<prefix_kernel<D>>(C::SMEM);
+    cudaError_t e = set_smem_limit_once<prefix_kernel<D, OWN>>(C::SMEM);
     if (e != cudaSuccess) return e;
     PreParams p;
     p.q = (const __nv_bfloat16*)a.q;
@@ -453,11 +509,20 @@ cudaError_t launch_d(const PrefixLaunch& a, cudaStream_t s) {
     p.scale_log2 = a.scale * 1.4426950408889634f;
     p.err = a.err;
     p.timeout_ns = a.timeout_ns;
-    return launch_dependent(prefix_kernel<D>, dim3((unsigned)a.workers), dim3(C::THREADS), C::SMEM, s, a.map_k, a.map_v, p);
+    return launch_dependent(prefix_kernel<D, OWN>, dim3((unsigned)a.workers), dim3(C::THREADS), C::SMEM, s, a.map_k, a.map_v, p,
+                            rows_params<D, 8>(rows));
+}
+
+template <int D>
+cudaError_t launch_d(const PrefixLaunch& a, const DecodeRowsLaunch& rows, cudaStream_t s) {
+    if (!a.own) return launch_o<D, 0>(a, rows, s);
+    return a.Nq == 1 ? launch_o<D, 1>(a, rows, s) : launch_o<D, 2>(a, rows, s);
 }
 
 }  // namespace
 
-cudaError_t launch_prefix(const PrefixLaunch& a, cudaStream_t s) { return a.d == 128 ? launch_d<128>(a, s) : launch_d<64>(a, s); }
+cudaError_t launch_prefix(const PrefixLaunch& a, const DecodeRowsLaunch& rows, cudaStream_t s) {
+    return a.d == 128 ? launch_d<128>(a, rows, s) : launch_d<64>(a, rows, s);
+}
 
 }  // namespace fa

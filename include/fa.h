@@ -503,7 +503,6 @@ size_t fa_decode_blocks_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d);
  * kv head h / (Hq / Hkv); query t sees the tokens j <= seq_lens[b] - Nq + t of the
  * listed blocks.  A query that sees none gets O = 0, LSE = -inf.  Scores and sums
  * are fp32; for the value product a softmax weight is rounded to 16 bits (2^-17).
- * The keys of all sequences are dealt out evenly to the CTAs that run at once.
  * Results do not depend on the run (fixed order of additions), but for rounding on
  * the batch that a sequence is in.  Tokens past seq_lens[b] are never used, and one
  * that a query does not see does not reach it, whatever it holds.  Steps of 64 keys

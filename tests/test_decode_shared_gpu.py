@@ -194,3 +194,51 @@ def test_wild_values_of_the_prefix_and_of_its_page(cuda_lib):
         ok(cuda_lib)
         there = np.isnan(f64(o))
         assert there[lens > 0, :, :, 40].all() and there.sum() == (B - 1) * G
+
+
+@pytest.mark.parametrize("B,Hkv,G,Nq,d,shared", [
+    (33, 2, 4, 1, 128, 700),      # 132 rows, one step of a second tile's
+    (40, 8, 1, 8, 64, 1500),      # drafts
+    (18, 1, 4, 2, 128, 2500),     # 144 rows of one kv head, the CTAs many to an item
+    (18, 1, 4, 2, 128, 0),
+    (160, 32, 8, 1, 64, 140),     # more (kv head, 256 rows) than CTAs
+    (130, 16, 2, 1, 128, 129),
+])
+def test_prefix_and_own_tokens_in_one_kernel(cuda_lib, B, Hkv, G, Nq, d, shared):
+    """Up to 8 query rows of a sequence and kv head, more than 128 of all: own tokens from none to much more than the prefix,
+    sequences that do not take part, and batches in which none does."""
+    rng = np.random.default_rng(B + d)
+    page, scale = 32, 1.0 / math.sqrt(d)
+    lens = shared + rng.integers(Nq, 60, B)
+    lens[1], lens[2], lens[3] = 0, shared // 2, shared + 900
+    q = bf16(rng, (B, Hkv * G, Nq, d), 0.3)
+    c, table = _case(8, lens, shared, Hkv, page, d)
+    g = to_gpu(c)
+    o, lse = cuda_lib.decode_shared(q.to(DEV), g["k"], g["v"], ints(table), ints(lens), ints([shared]))
+    ok(cuda_lib)
+    check_rows(o, lse, op.attend(f64(q), c, table, lens, scale), ONE)
+    again = cuda_lib.decode_shared(q.to(DEV), g["k"], g["v"], ints(table), ints(lens), ints([shared]))
+    assert torch.equal(again[0], o) and torch.equal(again[1], lse)
+    for short in (np.minimum(lens, shared), np.zeros_like(lens)):  # nobody has all of the prefix and new tokens
+        o, lse = cuda_lib.decode_shared(q.to(DEV), g["k"], g["v"], ints(table), ints(short), ints([shared]))
+        ok(cuda_lib)
+        check_rows(o, lse, op.attend(f64(q), c, table, short, scale), ONE)
+
+
+@pytest.mark.parametrize("B", [4, 40])
+def test_bad_lengths_are_noted_whichever_kernel_takes_them(cuda_lib, B):
+    """A length out of range, the prefix's too, is clamped and recorded."""
+    rng = np.random.default_rng(B)
+    Hkv, G, d, page, shared = 2, 4, 128, 16, 100
+    for where in ("negative", "long", "prefix"):
+        lens = np.full(B, shared + 7)
+        c, table = _case(3, lens, shared, Hkv, page, d)
+        cap, given = table.shape[1] * page, shared
+        if where == "prefix":
+            given = cap + 5                              # nobody takes part
+        else:
+            lens[B - 1] = -3 if where == "negative" else cap + 9
+        q, g = bf16(rng, (B, Hkv * G, 1, d), 0.3), to_gpu(c)
+        o, lse = cuda_lib.decode_shared(q.to(DEV), g["k"], g["v"], ints(table), ints(lens), ints([given]))
+        assert cuda_lib.fa_get_last_device_error()[0] == cuda_lib.FA_ERR_INVALID_ARG, where
+        check_rows(o, lse, op.attend(f64(q), c, table, np.clip(lens, 0, cap), 1 / math.sqrt(d)), ONE)
