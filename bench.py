@@ -906,7 +906,8 @@ def run_ours(args, rank, world, local_rank):
 
 # ------------------------------------------------------------------ one kernel for a profiler
 PROFILE_TARGETS = ("fwd", "dkdv", "dq", "fused", "pair", "window", "decode", "decode64", "paged", "paged48",
-                   "paged20", "fp8", "rope", "append", "decode_fp8", "evict")
+                   "paged20", "fp8", "rope", "append", "decode_fp8", "evict", "append_bf16", "select", "blocks",
+                   "shared")
 
 
 def run_profile(target, launches):
@@ -920,7 +921,10 @@ def run_profile(target, launches):
     sequence (4080 tokens: the general kernel); fp8 the FP8 forward; rope 8192
     tokens of 32 heads; append (2048 tokens per sequence, rotated), decode_fp8 and
     evict (1024 tokens stay) the cache held in 8 bits, at B=32, Hq=32, Hkv=8,
-    Nk=4096, page 64.  Prints one line; no timing."""
+    Nk=4096, page 64; append_bf16 (2048 tokens per sequence, rotated, bounds of
+    16-token blocks kept), select (64 blocks of 16384 tokens) and blocks (128 of 256
+    blocks) the bf16 cache at the same heads and pages; shared 64 sequences with 8192
+    tokens in common and 512 of their own.  Prints one line; no timing."""
     import torch
     import exact_tiled_attention_21_gb300 as fa
     dev = torch.device("cuda", 0)
@@ -988,6 +992,27 @@ def run_profile(target, launches):
             "append": lambda: fa.cache_append_fp8(kn, vn, kp, vp, ks, vs, table, lens - new, turns=turns),
             "decode_fp8": lambda: fa.decode_paged_fp8(qd, kp, vp, ks, vs, table, lens),
             "evict": lambda: fa.cache_evict_fp8(kp, vp, ks, vs, table, lens, w, new_table, keep, 128),
+        }[target]
+    elif target in ("append_bf16", "select", "blocks", "shared"):
+        hkv, page, block, new = 8, 64, 16, 2048
+        b, nk = (64, 8192 + 512) if target == "shared" else (DEC_B, 16384 if target == "select" else DEC_NK)
+        used = b * (nk // page)
+        table = torch.randperm(used, generator=torch.Generator().manual_seed(5)).to(torch.int32).reshape(b, -1).to(dev)
+        if target == "shared":
+            table[:, :8192 // page] = table[0, :8192 // page]
+        lens = torch.full((b,), nk, dtype=torch.int32, device=dev)
+        qd = rnd(b, DEC_H, 1, D)
+        kp, vp = (rnd(1 if target == "select" else used, hkv, page, D) for _ in range(2))
+        bounds = rnd(used, hkv, page // block, 2, D)
+        if target == "append_bf16":
+            kn, vn, turns = rnd(b, hkv, new, D), rnd(b, hkv, new, D), fa.rope_table(fa.rope_frequencies(D)[0], dev)
+        lists = torch.arange(0, nk // block, 2, dtype=torch.int32, device=dev).expand(b, hkv, -1).contiguous()
+        common = torch.tensor([8192], dtype=torch.int32, device=dev)
+        call = {
+            "append_bf16": lambda: fa.cache_append(kn, vn, kp, vp, table, lens - new, turns=turns, bounds=bounds),
+            "select": lambda: fa.select_blocks(qd, bounds, table, lens, block, 64, 1, 2),
+            "blocks": lambda: fa.decode_blocks(qd, kp, vp, table, lens, lists, block),
+            "shared": lambda: fa.decode_shared(qd, kp, vp, table, lens, common),
         }[target]
     else:  # fp8
         mk = lambda: torch.randint(0, 126, (1, H, N, D), generator=torch.Generator().manual_seed(7),

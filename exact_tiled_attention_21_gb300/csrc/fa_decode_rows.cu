@@ -138,10 +138,17 @@ __global__ void __launch_bounds__(THREADS) merge_rows_kernel(const Params a) {
 template <int D, int ROWS, bool LIST>
 cudaError_t launch_merge(const DecodeRowsLaunch& a, const Params& p, cudaStream_t s) {
     const long long rows = (long long)a.B * a.Hkv * p.rows;
-    // rows alone in a block where there are few of them: their parts are read by more threads
-    const long long parts = LIST ? p.workers / ((long long)a.B * a.Hkv * p.row_tiles) : (a.joint ? p.workers : a.pre_workers) / ((long long)a.Hkv * p.pre_tiles);
+    // Rows alone in a block where there are few of them: their parts are read by more threads, 8 groups of them where a row has
+    // many parts (288 rows of about 76: 24.2 us in 8 groups, 27.2 in 4; 1024 rows of about 19: 23.8 and 22.8; four rows to a
+    // block 47 and 25.9; 4096 rows of about 9: 99.7, 95.2 and 93.8 with four to a block, the whole call each).  Where one kernel
+    // has the prefix and own tokens, about half of its CTAs have the prefix.
+    const long long most = LIST ? (long long)a.keep * a.block : (long long)a.max_pages * a.page,
+                    ctas = LIST ? p.workers : a.joint ? p.workers / 2 : a.merge_only ? a.pre_workers / 2 : a.pre_workers,
+                    parts = std::min(ctas / (LIST ? (long long)a.B * a.Hkv * p.row_tiles : (long long)a.Hkv * p.pre_tiles),
+                                     most / Cfg<D, ROWS>::STEP);
     if (rows <= (parts >= 4 ? 16ll : 4ll) * a.num_sms)
-        return launch_dependent(merge_rows_kernel<D, ROWS, LIST, true, 256>, dim3((unsigned)rows), dim3(256), 0, s, p);
+        return parts >= 16 ? launch_dependent(merge_rows_kernel<D, ROWS, LIST, true, 256>, dim3((unsigned)rows), dim3(256), 0, s, p)
+                           : launch_dependent(merge_rows_kernel<D, ROWS, LIST, true, 128>, dim3((unsigned)rows), dim3(128), 0, s, p);
     constexpr int PER = 128 / (D / 4);
     return launch_dependent(merge_rows_kernel<D, ROWS, LIST, false, 128>, dim3((unsigned)((rows + PER - 1) / PER)), dim3(128), 0,
                             s, p);
@@ -172,10 +179,7 @@ cudaError_t launch_l(const DecodeRowsLaunch& a, cudaStream_t s) {
                              : set_smem_limit_once<decode_rows_kernel<D, ROWS, false, LIST>>(C::SMEM);
     if (e != cudaSuccess) return e;
     Params p = rows_params<D, ROWS>(a);
-    if (a.merge_only) {
-        p.workers = a.pre_workers;
-        return launch_merge<D, ROWS, LIST>(a, p, s);
-    }
+    if (a.merge_only) return launch_merge<D, ROWS, LIST>(a, p, s);
     // no more CTAs than steps at full lengths
     const long long most = LIST ? std::min((long long)a.keep * a.block, (long long)a.max_pages * a.page + a.block)
                                 : (long long)a.max_pages * a.page;
