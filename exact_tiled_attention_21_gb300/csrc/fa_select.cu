@@ -36,11 +36,14 @@ namespace {
 constexpr int kRowTile = 64;      // query rows in shared memory at once
 constexpr int kBatch = 16;        // blocks of a warp's batch
 constexpr int kBins = 1024, kList = 256;
-constexpr int kMostKeys = 16384;  // scores in shared memory; more go through the workspace
 constexpr float kError = 4e-6f;   // E / A: 2^-17.9
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// 16 bytes into shared memory; zeros if !ok (src must still be a valid address).
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool ok) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+}
 // Largest magnitudes of the two halves of bf16 pairs, as bits: infinities and NaN on top.
 __device__ __forceinline__ uint32_t abs_max2(uint32_t a, uint32_t b) {
     uint32_t r;
@@ -81,6 +84,7 @@ __device__ __forceinline__ uint64_t key64(double x) {
 
 struct SelectPlan {
     int ctas;          // of a cluster
+    int tiles;         // of 8 query rows in shared memory at once
     FastDiv per_page;  // blocks of a page
 };
 
@@ -102,8 +106,14 @@ template <int D, bool GLOBAL, int THREADS>
 __global__ void __launch_bounds__(THREADS, 512 / THREADS) select_blocks_kernel(const SelectLaunch a, const SelectPlan plan) {
     constexpr int kSelThreads = THREADS, kSelWarps = THREADS / 32;
     constexpr int S = D / 16, CHUNKS = 4 * S;  // 64-byte pieces of a block's bounds, a lane's part of which is a chunk
-    extern __shared__ __align__(16) uint32_t s_keys[];
-    __shared__ uint4 s_q[kRowTile / 8][S][32];  // by tile of 8 rows and piece: the lanes' B fragments of two products
+    extern __shared__ __align__(16) uint4 s_mem[];
+    // With 256 threads the next batch comes through shared memory while this one is worked on, a thread's pieces in places of its
+    // own (32 sequences of up to 16384 tokens, blocks of 16: 41.3 us without, 33.0 with; 4096 tokens 16.5 and 14.3).  With 512
+    // and an SM to itself a CTA has all its loads in flight anyway (one sequence of 131072 tokens: 16.4 without, 17.7 with).
+    constexpr bool RING = THREADS == 256;
+    uint4* s_ring = s_mem + threadIdx.x;                 // [2 S][THREADS]
+    uint4* s_q = s_mem + (RING ? 2 * S * THREADS : 0);  // [tile of 8 rows][piece][lane]: B fragments of two products
+    uint32_t* s_keys = reinterpret_cast<uint32_t*>(s_q + plan.tiles * S * 32);
     __shared__ uint32_t s_sum8[CHUNKS], s_big[CHUNKS];  // bits of the largest sum of |q|, and |bound|, of each chunk
     __shared__ int s_hist[kBins];
     __shared__ uint64_t s_exact[kList];
@@ -118,6 +128,27 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) select_blocks_kernel(c
     const int bh = blockIdx.x / plan.ctas, b = bh / a.Hkv, kvh = bh - b * a.Hkv;
     const int bpp = (int)plan.per_page.d, cap = a.max_pages * bpp * a.block;
     int len = a.lens[b];
+    const __nv_bfloat16* q = (const __nv_bfloat16*)a.q + (long long)bh * a.rows * D;
+    // the B fragments of query rows [r0, r0 + many): a lane's chunk is 8 columns of a row's negative part (times the
+    // smallest keys), then of its positive part
+    auto stage = [&](int r0, int many) {
+        for (int i = tid; i < (many + 7) / 8 * S * 32; i += kSelThreads) {
+            const int l = i % 32, s = i / 32 % S, r = i / 32 / S * 8 + l / 4, chunk = s * 4 + l % 4;
+            uint4 w = make_uint4(0, 0, 0, 0);
+            if (r < many) w = *reinterpret_cast<const uint4*>(q + (long long)(r0 + r) * D + chunk * 8 % D);
+            const bool neg = chunk * 8 < D;
+            w = make_uint4(part2(w.x, neg), part2(w.y, neg), part2(w.z, neg), part2(w.w, neg));
+            s_q[i] = w;
+            // rounded up: a sum of eight is off by 2^-21 at most
+            const float sum = (abs_sum2(w.x) + abs_sum2(w.y) + abs_sum2(w.z) + abs_sum2(w.w)) * 1.00001f;
+            atomicMax(&s_sum8[chunk], __float_as_uint(sum) & 0x7FFFFFFFu);
+        }
+    };
+    if (tid < CHUNKS) s_sum8[tid] = s_big[tid] = 0;
+    for (int i = tid; i < kBins; i += kSelThreads) s_hist[i] = 0;
+    if (tid == 0) s_many = 0;
+    __syncthreads();
+    stage(0, min(kRowTile, a.rows));  // while the length comes
     if (len < 0 || len > cap) {
         if (tid == 0 && rank == 0) record_invalid(a.err, kSiteCacheLen, len);
         len = min(max(len, 0), cap);
@@ -135,67 +166,72 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) select_blocks_kernel(c
         for (int i = tid; i < a.recent; i += kSelThreads) out[a.first + want + i] = j0 + mid + i;
     }
     if (want == 0) return;
-    if (tid < CHUNKS) s_sum8[tid] = s_big[tid] = 0;
     if (plan.ctas > 1) cluster_arrive();  // waited for below: the first CTA runs before the others write to it
     uint32_t* keys = GLOBAL ? a.scores + (long long)bh * a.stride : s_keys;  // of block j0 + i
     const uint32_t keys0 = mapa_shared(smem_u32(s_keys), 0);                 // those of the first CTA
-    const __nv_bfloat16* q = (const __nv_bfloat16*)a.q + (long long)bh * a.rows * D;
     const __nv_bfloat16* bounds = (const __nv_bfloat16*)a.bounds;
-    // the row of `bounds` (2 D elements) of block j, ~0u without a page
-    auto row_of = [&](int j) {
-        const int lpage = (int)plan.per_page.div(j), pg = a.table[(long long)b * a.max_pages + lpage];
+    // the row of `bounds` (2 D elements) of block j, ~0u without a page; its entry of the table is loaded beforehand
+    auto entry_of = [&](int j) { return a.table[(long long)b * a.max_pages + (int)plan.per_page.div(j)]; };
+    auto row_at = [&](int j, int pg) {
         if ((unsigned)pg >= (unsigned)a.num_pages) {
             record_invalid(a.err, kSiteCacheTable, pg);
             return ~0u;
         }
-        return ((uint32_t)pg * a.Hkv + kvh) * bpp + (uint32_t)(j - lpage * bpp);
+        return ((uint32_t)pg * a.Hkv + kvh) * bpp + (uint32_t)(j - (int)plan.per_page.div(j) * bpp);
     };
+    auto row_of = [&](int j) { return row_at(j, entry_of(j)); };
     const int share = ((mid + plan.ctas - 1) / plan.ctas + kBatch - 1) & ~(kBatch - 1), i0 = rank * share, i1 = min(i0 + share, mid);
     const int g8 = lane >> 2, t4 = lane & 3;
-    auto rows_of = [&](int g) { return lane < kBatch && g + lane < i1 ? row_of(j0 + g + lane) : ~0u; };
-    // the B fragments of query rows [r0, r0 + many): a lane's chunk is 8 columns of a row's negative part (times the
-    // smallest keys), then of its positive part
-    auto stage = [&](int r0, int many) {
-        for (int i = tid; i < (many + 7) / 8 * S * 32; i += kSelThreads) {
-            const int l = i % 32, s = i / 32 % S, r = i / 32 / S * 8 + l / 4, chunk = s * 4 + l % 4;
-            uint4 w = make_uint4(0, 0, 0, 0);
-            if (r < many) w = *reinterpret_cast<const uint4*>(q + (long long)(r0 + r) * D + chunk * 8 % D);
-            const bool neg = chunk * 8 < D;
-            w = make_uint4(part2(w.x, neg), part2(w.y, neg), part2(w.z, neg), part2(w.w, neg));
-            s_q[r / 8][s][l] = w;
-            // rounded up: a sum of eight is off by 2^-21 at most
-            const float sum = (abs_sum2(w.x) + abs_sum2(w.y) + abs_sum2(w.z) + abs_sum2(w.w)) * 1.00001f;
-            atomicMax(&s_sum8[chunk], __float_as_uint(sum) & 0x7FFFFFFFu);
-        }
-    };
-    for (int i = tid; i < kBins; i += kSelThreads) s_hist[i] = 0;
-    if (tid == 0) s_many = 0;
+    auto entries_of = [&](int g) { return lane < kBatch && g + lane < i1 ? entry_of(j0 + g + lane) : 0; };
     uint32_t big[S];
 #pragma unroll
     for (int s = 0; s < S; ++s) big[s] = 0;
     for (int r0 = 0; r0 < a.rows; r0 += kRowTile) {
         const int many = min(kRowTile, a.rows - r0);
-        uint32_t rows = rows_of(i0 + warp * kBatch);  // of the next batch
-        __syncthreads();
-        stage(r0, many);
-        __syncthreads();
-        if (r0 == 0 && plan.ctas > 1) cluster_wait();
-        for (int g = i0 + warp * kBatch; g < i1; g += kSelWarps * kBatch) {
-            uint4 w[2][S];  // of blocks g8 and g8 + 8 of the batch
+        int g = i0 + warp * kBatch;
+        int entries = entries_of(g);
+        if (r0 > 0) {
+            __syncthreads();
+            stage(r0, many);
+        }
+        uint4 w[2][S];  // of blocks g8 and g8 + 8 of the batch
+        auto load = [&](int g) {
+            const uint32_t rows = lane < kBatch && g + lane < i1 ? row_at(j0 + g + lane, entries) : ~0u;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const uint32_t row = __shfl_sync(0xffffffffu, rows, g8 + 8 * h);
                 const uint4* src = reinterpret_cast<const uint4*>(bounds + (size_t)(row != ~0u ? row : 0) * (2 * D)) + t4;
 #pragma unroll
-                for (int s = 0; s < S; ++s) w[h][s] = row != ~0u ? src[s * 4] : make_uint4(0, 0, 0, 0);
+                for (int s = 0; s < S; ++s) {
+                    if (RING)
+                        copy16(smem_u32(s_ring + (h * S + s) * THREADS), src + s * 4, row != ~0u);
+                    else
+                        w[h][s] = row != ~0u ? src[s * 4] : make_uint4(0, 0, 0, 0);
+                }
             }
-            rows = rows_of(g + kSelWarps * kBatch);
+            if (RING) asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        load(g);
+        entries = entries_of(g + kSelWarps * kBatch);
+        __syncthreads();
+        if (r0 == 0 && plan.ctas > 1) cluster_wait();
+        for (; g < i1; g += kSelWarps * kBatch) {
+            const int next = g + kSelWarps * kBatch;
+            if (RING) {
+                asm volatile("cp.async.wait_group 0;" ::: "memory");
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int s = 0; s < S; ++s) w[h][s] = s_ring[(h * S + s) * THREADS];
+                if (next < i1) load(next);
+                entries = entries_of(next + kSelWarps * kBatch);
+            }
             float best[2] = {-INFINITY, -INFINITY};
             for (int n = 0; n * 8 < many; ++n) {
                 float c[4][4] = {};
 #pragma unroll
                 for (int s = 0; s < S; ++s) {
-                    const uint4 x = s_q[n][s][lane];
+                    const uint4 x = s_q[(n * S + s) * 32 + lane];
                     mma_bf16(c[2 * s % 4], w[0][s].x, w[1][s].x, w[0][s].y, w[1][s].y, x.x, x.y);
                     mma_bf16(c[(2 * s + 1) % 4], w[0][s].z, w[1][s].z, w[0][s].w, w[1][s].w, x.z, x.w);
                 }
@@ -209,6 +245,10 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) select_blocks_kernel(c
                 big[s] = abs_max2(abs_max2(big[s], w[0][s].z), w[0][s].w);
                 big[s] = abs_max2(abs_max2(big[s], w[1][s].x), w[1][s].y);
                 big[s] = abs_max2(abs_max2(big[s], w[1][s].z), w[1][s].w);
+            }
+            if (!RING) {
+                if (next < i1) load(next);
+                entries = entries_of(next + kSelWarps * kBatch);
             }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -521,9 +561,12 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) select_blocks_kernel(c
     }
 }
 
+template <int THREADS>
+constexpr int kSmem = (THREADS == 512 ? 226 : 112) * 1024 - 10 * 1024;  // dynamic, beside the rest
+
 template <int D, bool GLOBAL, int THREADS>
 cudaError_t launch_t(const SelectLaunch& a, const SelectPlan& plan, int smem, cudaStream_t s) {
-    cudaError_t e = set_smem_limit_once<select_blocks_kernel<D, GLOBAL, THREADS>>(kMostKeys * 4);
+    cudaError_t e = set_smem_limit_once<select_blocks_kernel<D, GLOBAL, THREADS>>(kSmem<THREADS>);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.B * a.Hkv * plan.ctas));
@@ -540,6 +583,15 @@ cudaError_t launch_t(const SelectLaunch& a, const SelectPlan& plan, int smem, cu
     return cudaLaunchKernelEx(&cfg, select_blocks_kernel<D, GLOBAL, THREADS>, a, plan);
 }
 
+// Scores in shared memory while they and the rest fit (with 256 threads, twice on an SM), else in the workspace.
+template <int D, int THREADS>
+cudaError_t launch_s(const SelectLaunch& a, const SelectPlan& plan, long long cap, cudaStream_t s) {
+    const int fixed = (THREADS == 256 ? D / 8 * THREADS * 16 : 0) + plan.tiles * D * 32;
+    if (a.rows <= kRowTile && cap <= (kSmem<THREADS> - fixed) / 4)
+        return launch_t<D, false, THREADS>(a, plan, fixed + (int)cap * 4, s);
+    return launch_t<D, true, THREADS>(a, plan, fixed, s);
+}
+
 template <int D>
 cudaError_t launch_d(const SelectLaunch& a, cudaStream_t s) {
     SelectPlan plan;
@@ -550,10 +602,8 @@ cudaError_t launch_d(const SelectLaunch& a, cudaStream_t s) {
     plan.ctas = 1;
     while (plan.ctas < kSelectCtas && cap > 128ll * plan.ctas && bh * plan.ctas <= a.num_sms) plan.ctas *= 2;
     const bool wide = bh * plan.ctas <= a.num_sms;  // a CTA has an SM to itself
-    if (cap > kMostKeys || a.rows > kRowTile)
-        return wide ? launch_t<D, true, 512>(a, plan, 0, s) : launch_t<D, true, 256>(a, plan, 0, s);
-    const int smem = (int)cap * 4;
-    return wide ? launch_t<D, false, 512>(a, plan, smem, s) : launch_t<D, false, 256>(a, plan, smem, s);
+    plan.tiles = (std::min(a.rows, kRowTile) + 7) / 8;
+    return wide ? launch_s<D, 512>(a, plan, cap, s) : launch_s<D, 256>(a, plan, cap, s);
 }
 
 }  // namespace

@@ -141,3 +141,28 @@ def test_bad_lengths_and_pages(cuda_lib):
         t[0, 3] = 50
         grown = np.concatenate([bounds, np.zeros_like(bounds[:1])])
         assert np.array_equal(got, op.select(f64(q), grown, t, [600, 640], 16, 6, 1, 1))
+
+
+# (lens, Hkv, G, d, blocks per page, pages of the table, keep): scores in shared memory and in the workspace, CTAs with an SM to
+# themselves and two to an SM, one batch of blocks per warp and many, tables far wider than the lengths
+WIDE = [
+    ([1 << 15] + [40] * 39, 4, 4, 128, 8, 1024, 300),       # 160 pairs, 8192 blocks of 4
+    ([4 * 12000] + [40, 0, 9000] * 13, 4, 9, 64, 8, 1500, 900),  # 12000 blocks, 9 rows
+    ([4 * 13000 - 1] + [70] * 79, 2, 8, 128, 8, 2500, 64),  # 20000 blocks in the table
+    ([4 * 60000], 1, 2, 64, 16, 3750, 2000),                # 60000 blocks
+    ([4 * 60000, 333], 1, 1, 128, 16, 3760, 1),
+    ([2000] * 40, 8, 1, 64, 4, 125, 17),                    # 320 pairs
+]
+
+
+@pytest.mark.parametrize("lens,Hkv,G,d,per,maxp,keep", WIDE)
+def test_wide_tables_and_many_sequences(cuda_lib, lens, Hkv, G, d, per, maxp, keep):
+    """Pages that many sequences share, so that scores repeat within a sequence too."""
+    rng = np.random.default_rng(maxp + keep)
+    pages = 700
+    bounds, B = _bounds(rng, pages, Hkv, per, d), len(lens)
+    table = rng.integers(0, pages, (B, maxp)).astype(np.int32)
+    q = bf16(rng, (B, Hkv * G, 1, d))
+    got = _run(cuda_lib, q, bounds, table, lens, 4, keep, 0, 1)
+    ok(cuda_lib)
+    assert np.array_equal(got, op.select(f64(q), bounds, table, lens, 4, keep, 0, 1))
