@@ -16,6 +16,9 @@ namespace {
 // Every element is read once and written once: bound by HBM for prompts, by the latency of a launch and three dependent
 // loads (length, table, token) for single tokens.
 //
+// Measured, 8 kv heads, d = 128, rotated, with bounds: one token of 32 sequences 3.5 us; 8 ragged prompts of up to 2048 tokens
+// 24.4 us (15.3 at HBM's copy rate; 59% of DRAM's peak and half of the issue slots in a capture of 32 full ones).
+//
 // append_kernel: a CTA takes a run of tokens, in whole blocks, of up to eight kv heads.  The tokens' places in the cache and
 // their cosines and sines are made once, in shared memory; then each warp takes the keys of a head, or its values, for
 // itself, without waiting for others: RP rows at a time, four of these loaded ahead, 16 columns of a row (the two pieces

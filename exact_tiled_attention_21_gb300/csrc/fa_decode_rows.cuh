@@ -1,8 +1,8 @@
 // Attention of 1..16 new tokens per sequence over the paged bf16 cache: over the
 // blocks of a list, or over the tokens that follow a prefix which all sequences
-// share, and the merge of the parts.  The prefix itself is fa_prefix.cu's, or, where
-// all sequences together have few query rows per kv head, one more sequence here for
-// each 32 of them: a kernel less.
+// share.  The prefix itself is fa_prefix.cu's, which with up to 8 rows of a sequence and
+// kv head runs this beside it; or, where all sequences together have few query rows per
+// kv head and little to share, it is one more sequence here for each 32 of them.
 //
 // 4 d bytes per key for 4 d flops per query row: bound by HBM.  The work is one
 // list of steps of 4 x KEYS keys over all sequences, kv heads and row tiles, cut
@@ -11,11 +11,17 @@
 // crosses from one (sequence, kv head, row tile) to the next as it comes, the
 // copies running ahead; the part of one that a CTA holds is a segment.  Segment
 // results go to the workspace at slot CTA + item (which grows by one from each
-// segment to the next), and a second kernel merges the segments of each row.
+// segment to the next), and a second kernel (fa_decode_rows.cu) merges the segments of
+// each row.
 //
 // Where a list's items are few enough for a CTA of their own each, a cluster of up to
 // eight takes an item, a run of its steps each, and joins the parts through its
 // shared memories: no second kernel.
+//
+// Measured: 64 listed blocks of 16 tokens for each of 32 sequences, 4 heads on each of 8
+// kv heads, d = 128: 25.4 us, 19.3 at HBM's copy rate; 128 blocks 48.4 us under the
+// profiler, at 71% of DRAM's peak.  What is left is the start (three loads that depend on
+// one another behind the launch), the unequal ends and the join.
 //
 // A CTA has four warps.  Each streams KEYS keys per step through a ring of its own
 // of cp.async copies, three steps deep, and holds 8 query rows, or 16 where there
@@ -107,8 +113,8 @@ struct Params {
     const int* pre_ends;
     int B, Hkv, Nq, max_pages, num_pages, rows, row_tiles, workers, keep;
     int cluster;            // CTAs of an item (LIST), 0: shares of all items' steps
-    int pre_workers;        // its CTAs
-    int pre_tiles, pre_rows, pre_item;  // its tiles of pre_rows query rows; the first one's slots are CTA + pre_item
+    int pre_workers, pre_tiles, pre_rows, pre_item;  // its CTAs; its tiles of pre_rows query rows; the first one's slots are
+                                                     // CTA + pre_item
     int joint, tiles;       // the prefix is this kernel's too: `joint` rows, as `tiles` sequences B, B + 1, ... of ROWS each
     FastDiv page, block, per_row, heads;  // rows, Hkv
     float scale_log2;

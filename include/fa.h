@@ -481,8 +481,9 @@ size_t fa_select_blocks_workspace_bytes(int B, int Hkv, int max_blocks);
  * block) blocks of sequence b the first `first` ones, the last `recent` ones
  * (first + recent <= keep) and, of the others, the keep - first - recent of
  * largest score, in ascending order; all of them and -1 behind them if n_b <= keep.
- * The choice is that of exact scores: of equal ones (+0 = -0) the lowest index
- * stays; NaN (also an infinite bound times zero) counts as largest.  recent should
+ * The choice is that of exact scores, but for what is below 2^-58 of the largest
+ * sum_c |q_rc| |bound_c|: of equal ones (+0 = -0) the lowest index stays; NaN (also
+ * an infinite bound times zero) counts as largest.  recent should
  * cover the Nq tokens.  workspace: 16-byte aligned, at least
  * fa_select_blocks_workspace_bytes(...); contents do not matter; calls that may
  * overlap need one each. */

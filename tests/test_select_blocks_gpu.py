@@ -152,6 +152,8 @@ WIDE = [
     ([4 * 60000], 1, 2, 64, 16, 3750, 2000),                # 60000 blocks
     ([4 * 60000, 333], 1, 1, 128, 16, 3760, 1),
     ([2000] * 40, 8, 1, 64, 4, 125, 17),                    # 320 pairs
+    ([3000, 1500], 2, 80, 64, 8, 100, 50),                  # 80 rows: two tiles of them
+    ([900, 1500, 0, 30] * 10, 8, 70, 128, 8, 50, 50),
 ]
 
 
