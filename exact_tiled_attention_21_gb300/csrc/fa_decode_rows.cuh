@@ -485,26 +485,35 @@ __device__ __forceinline__ void decode_rows(const Params& a, uint8_t* smem, Rows
             auto tok_of = [&](int key) {
                 return reinterpret_cast<const int*>(group + key / KEYS * C::RING + 2 * C::HALF)[key % KEYS];
             };
-            bool partly = false;
-            for (int key = lane; key < RG * KEYS; key += 32) partly |= tok_of(key) > sees_all && tok_of(key) != kNone;
-            if (__any_sync(0xffffffffu, partly)) {
+            constexpr int WORDS = (RG * KEYS + 31) / 32;
+            uint32_t partly[WORDS], any = 0;  // the keys that some rows see and others do not
+#pragma unroll
+            for (int w = 0; w < WORDS; ++w) {
+                const int tok = tok_of(min(w * 32 + lane, RG * KEYS - 1));
+                any |= partly[w] = __ballot_sync(0xffffffffu, w * 32 + lane < RG * KEYS && tok > sees_all && tok != kNone);
+            }
+            auto each = [&](auto f) {
+#pragma unroll
+                for (int w = 0; w < WORDS; ++w)
+#pragma unroll 1
+                    for (uint32_t m = partly[w]; m; m &= m - 1) f(w * 32 + __ffs(m) - 1);
+            };
+            if (any) {
                 auto word_of = [&](int key, int col) {  // the word of columns col, col + 1
                     return reinterpret_cast<uint32_t*>(group + key / KEYS * C::RING + C::HALF + key % KEYS * (D * 2) +
                                                        (((col / 8) ^ (key & 7)) << 4)) + col % 8 / 2;
                 };
                 auto wild = [](uint32_t half) { return (half & 0x7F80u) == 0x7F80u; };
                 bool found = false;
-                for (int key = 0; key < RG * KEYS; ++key)
-                    if (tok_of(key) > sees_all && tok_of(key) != kNone)
-                        for (int c = lane * 2; c < D; c += 64) {
-                            const uint32_t w = *word_of(key, c);
-                            found |= wild(w & 0xFFFFu) || wild(w >> 16);
-                        }
+                each([&](int key) {
+                    for (int c = lane * 2; c < D; c += 64) {
+                        const uint32_t w = *word_of(key, c);
+                        found |= wild(w & 0xFFFFu) || wild(w >> 16);
+                    }
+                });
                 if (__any_sync(0xffffffffu, found)) {  // in all warps of the group alike
-#pragma unroll 1
-                    for (int key = 0; key < RG * KEYS; ++key) {
+                    each([&](int key) {
                         const int tok = tok_of(key);
-                        if (tok <= sees_all || tok == kNone) continue;
 #pragma unroll
                         for (int i = 0; i < D / 16; ++i)
 #pragma unroll
@@ -519,16 +528,15 @@ __device__ __forceinline__ void decode_rows(const Params& a, uint8_t* smem, Rows
                                         if (tok <= sees_all + (r0 + nb * 8 + 2 * t + j) % Nq)
                                             acc[nb][i][2 * h + j] += __uint_as_float(half << 16);
                             }
-                    }
+                    });
                     group_sync();  // every warp has read them
-#pragma unroll 1
-                    for (int key = 0; key < RG * KEYS; ++key) {
-                        if (key / KEYS != rg || tok_of(key) <= sees_all || tok_of(key) == kNone) continue;
+                    each([&](int key) {
+                        if (key / KEYS != rg) return;
                         for (int c = lane * 2; c < D; c += 64) {
                             uint32_t* w = word_of(key, c);
                             *w &= (wild(*w & 0xFFFFu) ? 0u : 0xFFFFu) | (wild(*w >> 16) ? 0u : 0xFFFF0000u);
                         }
-                    }
+                    });
                     group_sync();
                 }
             }
