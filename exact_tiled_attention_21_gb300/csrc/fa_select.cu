@@ -117,7 +117,8 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) select_blocks_kernel(c
     uint4* s_ring = s_mem + threadIdx.x;                 // [2 S][THREADS]
     uint4* s_q = s_mem + (RING ? 2 * S * THREADS : 0);  // [tile of 8 rows][piece][lane]: B fragments of two products
     uint32_t* s_keys = reinterpret_cast<uint32_t*>(s_q + plan.tiles * S * 32);
-    __shared__ uint32_t s_sum8[CHUNKS], s_big[CHUNKS];  // bits of the largest sum of |q|, and |bound|, of each chunk
+    // bits of the largest sum of |q|, and |bound|, of each chunk; behind these the complement of the smallest key and the largest
+    __shared__ uint32_t s_sum8[CHUNKS], s_big[CHUNKS + 2];
     __shared__ int s_hist[kBins];
     __shared__ uint64_t s_exact[kList];
     __shared__ uint32_t s_list[kList];
@@ -147,7 +148,8 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) select_blocks_kernel(c
             atomicMax(&s_sum8[chunk], __float_as_uint(sum) & 0x7FFFFFFFu);
         }
     };
-    if (tid < CHUNKS) s_sum8[tid] = s_big[tid] = 0;
+    if (tid < CHUNKS) s_sum8[tid] = 0;
+    if (tid < CHUNKS + 2) s_big[tid] = 0;
     for (int i = tid; i < kBins; i += kSelThreads) s_hist[i] = 0;
     if (tid == 0) s_many = 0;
     __syncthreads();
@@ -186,7 +188,7 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) select_blocks_kernel(c
     const int share = ((mid + plan.ctas - 1) / plan.ctas + kBatch - 1) & ~(kBatch - 1), i0 = rank * share, i1 = min(i0 + share, mid);
     const int g8 = lane >> 2, t4 = lane & 3;
     auto entries_of = [&](int g) { return lane < kBatch && g + lane < i1 ? entry_of(j0 + g + lane) : 0; };
-    uint32_t big[S];
+    uint32_t big[S], lo = 0xFFFFFFFFu, hi = 0;
 #pragma unroll
     for (int s = 0; s < S; ++s) big[s] = 0;
     for (int r0 = 0; r0 < a.rows; r0 += kRowTile) {
@@ -259,11 +261,14 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) select_blocks_kernel(c
                 best[h] = fmaxf(best[h], __shfl_xor_sync(0xffffffffu, best[h], 2));
                 const int i = g + g8 + 8 * h;
                 if (t4 == 0 && i < i1) {
-                    const uint32_t key = key32(best[h]);
-                    if (GLOBAL)
-                        keys[i] = r0 > 0 ? max(keys[i], key) : key;
-                    else
+                    uint32_t key = key32(best[h]);
+                    if (GLOBAL) {
+                        if (r0 > 0) key = max(keys[i], key);
+                        keys[i] = key;
+                    } else {
                         st_cluster_u32(keys0 + 4 * i, key);
+                    }
+                    if (r0 + kRowTile >= a.rows) lo = min(lo, key), hi = max(hi, key);
                 }
             }
         }
@@ -275,8 +280,14 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) select_blocks_kernel(c
         for (int m = 4; m < 32; m <<= 1) big[s] = abs_max2(big[s], __shfl_xor_sync(0xffffffffu, big[s], m));
         if (g8 == 0) atomicMax(&s_big[s * 4 + t4], max(big[s] << 16, big[s] & 0xFFFF0000u));
     }
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    if (lane == 0) {
+        atomicMax(&s_big[CHUNKS], ~lo);
+        atomicMax(&s_big[CHUNKS + 1], hi);
+    }
     __syncthreads();
-    if (rank > 0 && tid < CHUNKS)
+    if (rank > 0 && tid < CHUNKS + 2)
         asm volatile("red.shared::cluster.max.u32 [%0], %1;" ::"r"(mapa_shared(smem_u32(&s_big[tid]), 0)), "r"(s_big[tid]) : "memory");
     if (plan.ctas > 1) {
         cluster_arrive();
@@ -307,19 +318,10 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) select_blocks_kernel(c
         const int2 v = lane < kSelWarps ? s_sum[turn][lane] : make_int2(0, 0);
         return make_int2(__reduce_add_sync(0xffffffffu, v.x), __reduce_add_sync(0xffffffffu, v.y));
     };
-    uint32_t lo = 0xFFFFFFFFu, hi = 0;
-    each([&](int, uint32_t k) { lo = min(lo, k), hi = max(hi, k); });
-    lo = __reduce_min_sync(0xffffffffu, lo);
-    hi = __reduce_max_sync(0xffffffffu, hi);
-    if (lane == 0) s_sum[0][warp] = make_int2((int)lo, (int)hi);
+    lo = ~s_big[CHUNKS], hi = s_big[CHUNKS + 1];
     float A = 0.f;  // the largest sum of |q_c| |bound_c| that a row can have; NaN and infinities stay
     if (lane < CHUNKS) A = __uint_as_float(s_sum8[lane]) * __uint_as_float(s_big[lane]);
     for (int w = 16; w >= 1; w >>= 1) A += __shfl_xor_sync(0xffffffffu, A, w);
-    __syncthreads();
-    for (int w = 0; w < kSelWarps; ++w) {
-        lo = min(lo, (uint32_t)s_sum[0][w].x);
-        hi = max(hi, (uint32_t)s_sum[0][w].y);
-    }
     const float E = kError * 1.001f * A + 1e-30f;  // A itself is rounded; products may underflow
     // a score stays if its key is above `over`, or from `from` on and picked by the exact scores
     uint32_t from = 0, over = 0xFFFFFFFFu;
