@@ -22,9 +22,10 @@
 // tiny), and equal ones go by index.
 //
 // 4 d bytes per block and 4 d flops per block and row: bound by HBM where contexts
-// are long (32 sequences of up to 16384 tokens, blocks of 16, 8 kv heads, d = 128: 33 us,
-// 3 TB/s), by latency otherwise (of 4096 tokens 14.3 us: 2 to the queries' fragments, 8 to
-// the scores, which the first loads of all SMs at once take half of, 4 to the choice).  One
+// are long (32 sequences of up to 16384 tokens, blocks of 16, 8 kv heads, d = 128: 27.5 us,
+// 14.5 at the copy rate), by latency otherwise (of 4096 tokens 12.9 us: 2 to the queries'
+// fragments, 7 to the scores, which the first loads of all SMs at once take half of, 3.6 to
+// the choice).  One
 // cluster of up to 8 CTAs per (sequence, kv head) makes the scores, in the shared memory
 // of its first CTA (or in the workspace), which chooses: a histogram over the scores'
 // range finds the bin that the smallest one that stays is in, and counting greater
@@ -111,7 +112,7 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) select_blocks_kernel(c
     constexpr int S = D / 16, CHUNKS = 4 * S;  // 64-byte pieces of a block's bounds, a lane's part of which is a chunk
     extern __shared__ __align__(16) uint4 s_mem[];
     // With 256 threads the next batch comes through shared memory while this one is worked on, a thread's pieces in places of its
-    // own (32 sequences of up to 16384 tokens, blocks of 16: 41.3 us without, 33.0 with; 4096 tokens 16.5 and 14.3).  With 512
+    // own (32 sequences of up to 16384 tokens, blocks of 16: 39.3 us without, 33.0 with; 4096 tokens 15.9 and 14.3).  With 512
     // and an SM to itself a CTA has all its loads in flight anyway (one sequence of 131072 tokens: 16.4 without, 17.7 with).
     constexpr bool RING = THREADS == 256;
     uint4* s_ring = s_mem + threadIdx.x;                 // [2 S][THREADS]
