@@ -826,8 +826,8 @@ SelectWorkspace select_workspace(int B, int Hkv, long long max_blocks) {
 struct RowsWorkspace {
     size_t part_lse, ends, bytes;
 };
-RowsWorkspace rows_workspace(int B, int Hq, int Hkv, int Nq, int d, int joint = 0) {
-    const int rows = Hq / Hkv * Nq, tile = rows_tile(joint ? joint : rows);
+RowsWorkspace rows_workspace(int B, int Hq, int Hkv, int Nq, int d, int joint = 0, bool by_prefix = false) {
+    const int rows = Hq / Hkv * Nq, tile = by_prefix ? 8 : rows_tile(joint ? joint : rows);
     const size_t items = ((size_t)B + (joint + tile - 1) / tile) * Hkv * ((rows + tile - 1) / tile), slots = (size_t)kRowsMostWorkers + items;
     RowsWorkspace w;
     w.part_lse = align256(slots * tile * d * 4);
@@ -853,22 +853,26 @@ PrefixWorkspace prefix_workspace(int B, int Hq, int Hkv, int Nq, int d) {
     return w;
 }
 
-// Up to 8 query rows of a sequence and kv head, the prefix's kernel takes the own tokens too.
-bool prefix_takes_own(int Hq, int Hkv, int Nq) { return rows_tile(Hq / Hkv * Nq) == 8; }
+// Where the prefix's kernel takes the own tokens too, 8 query rows of a sequence and kv head at a time: up to 16 rows (64
+// sequences, 8 kv heads, d = 128, 1000 shared tokens and up to 20 own ones: 36.3 us apart, 31.5 together; 16 sequences 25.8 and
+// 19.2), and up to 32 where there are few (sequence, kv head) pairs to read four times (128 pairs of 24 rows 26.2 and 19.5; 512
+// pairs of 32 rows 41.2 and 53.5).
+bool prefix_takes_own(int B, int Hq, int Hkv, int Nq) {
+    const int rows = Hq / Hkv * Nq;
+    return rows <= 16 || (rows <= 32 && (long long)B * Hkv <= 128);
+}
 
 // Query rows of all sequences where decode_rows takes the prefix too, 0 where it does not: it reads the prefix once for each
-// 32 of them, which saves the other kernel's start and end where that is little work.  Measured with 4 heads per kv head, 8
-// kv heads, d = 128 against the prefix's kernel with the own tokens in it: 32 rows, 500 tokens 10.2 and 11.9 us, 2000 13.5
-// and 13.3, 8000 20.2 and 17.2; 64 rows 11.7 and 12.4, 14.4 and 14.5, 25.5 and 18.2; 128 rows, 500 tokens 15.8 and 15.0.
-// Against it and a kernel of their own: 48 rows, 2000 tokens 14.2 and 19.5, 8192 24.3 and 24.1; 128 rows 23.0 and 25.4,
-// 43.4 and 31.0; 32 rows, 32768 tokens 39.2 and (48 rows) 38.1.  tokens: of the table; 0: where any table of such a batch
-// would do.
+// 32 of them, which saves the other kernel's start and end where that is little work.  Measured with 8 kv heads, d = 128,
+// against the prefix's kernel with the own tokens in it: 4 rows of a sequence, 32 rows in all, 500 tokens 10.2 and 11.9 us, 2000
+// 13.5 and 13.3, 8000 20.2 and 17.2; 64 rows 11.7 and 12.4, 14.4 and 14.5, 25.5 and 18.2; 128 rows, 500 tokens 15.8 and 15.0;
+// 16 rows of a sequence, 128 in all, 500 tokens 13.0 and 14.4, 2000 17.6 and 16.8.  With fewer heads or d = 64 they meet where
+// tokens x heads x d does.  tokens: of the table; 0: where any table of such a batch would do.
 int joint_rows(int B, int Hq, int Hkv, int Nq, int d, long long tokens) {
     const long long rows = (long long)B * (Hq / Hkv) * Nq, tiles = (rows + 31) / 32;
     if (rows > 128 || Hq / Hkv * Nq > 32) return 0;
-    const bool own = prefix_takes_own(Hq, Hkv, Nq);
-    const long long most = (own ? tiles <= 2 ? 4096ll : 2048ll : 12288ll) * 8 * 128;  // elements of keys
-    return (tiles == 1 && !own) || tokens <= most / (tiles * Hkv * d) ? (int)rows : 0;
+    const long long most = (tiles <= 2 || Hq / Hkv * Nq > 8 ? 4096ll : 2048ll) * 8 * 128;  // elements of keys
+    return tokens <= most / (tiles * Hkv * d) ? (int)rows : 0;
 }
 
 bool rows_sizes_ok(int B, int Hq, int Hkv, int Nq, int d) {
@@ -879,7 +883,7 @@ bool rows_sizes_ok(int B, int Hq, int Hkv, int Nq, int d) {
 // Checks and fields that the attention over blocks and the one with a shared prefix have in common.
 int rows_prepare(DecodeRowsLaunch& a, const void* q, const void* k_pages, const void* v_pages, const int* block_table,
                  const int* seq_lens, void* o, float* lse, int B, int Hq, int Hkv, int Nq, int page_size, int block,
-                 int max_pages, int num_pages, int d, float scale) {
+                 int max_pages, int num_pages, int d, float scale, bool by_prefix = false) {
     if (!q || !k_pages || !v_pages || !block_table || !seq_lens || !o) return FA_ERR_INVALID_ARG;
     if (!scale_ok(scale) || Hq < 1 || Nq < 1) return FA_ERR_INVALID_ARG;
     int st = check_cache(B, Hkv, page_size, block, max_pages, num_pages, d);
@@ -887,7 +891,7 @@ int rows_prepare(DecodeRowsLaunch& a, const void* q, const void* k_pages, const 
     if (Hq % Hkv) return FA_ERR_INVALID_ARG;
     if (!rows_sizes_ok(B, Hq, Hkv, Nq, d)) return FA_ERR_UNSUPPORTED;
     // steps of 64 keys over all sequences, kv heads and row tiles, and two more for each of these, are counted in 31 bits
-    const int rows = Hq / Hkv * Nq, tile = rows_tile(rows);
+    const int rows = Hq / Hkv * Nq, tile = by_prefix ? 8 : rows_tile(rows);
     if (((long long)B + 4) * Hkv * ((rows + tile - 1) / tile) > 0x7FFFFFFFll / (((long long)max_pages * page_size + block + 63) / 64 + 2))
         return FA_ERR_UNSUPPORTED;
     if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(o) || !aligned4(block_table) ||
@@ -922,7 +926,7 @@ int rows_prepare(DecodeRowsLaunch& a, const void* q, const void* k_pages, const 
 }
 
 void rows_place(DecodeRowsLaunch& a, char* base) {
-    const RowsWorkspace w = rows_workspace(a.B, a.Hq, a.Hkv, a.Nq, a.d, a.joint);
+    const RowsWorkspace w = rows_workspace(a.B, a.Hq, a.Hkv, a.Nq, a.d, a.joint, a.merge_only);
     a.part_o = reinterpret_cast<float*>(base);
     a.part_lse = reinterpret_cast<float*>(base + w.part_lse);
     a.ends = reinterpret_cast<int*>(base + w.ends);
@@ -1263,7 +1267,7 @@ size_t fa_decode_shared_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d) {
     if (!rows_sizes_ok(B, Hq, Hkv, Nq, d)) return 0;
     // the larger of the two forms', whichever the table's width will choose
     return std::max(rows_workspace(B, Hq, Hkv, Nq, d, joint_rows(B, Hq, Hkv, Nq, d, 0)).bytes,
-                    rows_workspace(B, Hq, Hkv, Nq, d).bytes + prefix_workspace(B, Hq, Hkv, Nq, d).bytes);
+                    rows_workspace(B, Hq, Hkv, Nq, d, 0, prefix_takes_own(B, Hq, Hkv, Nq)).bytes + prefix_workspace(B, Hq, Hkv, Nq, d).bytes);
 }
 
 int fa_decode_shared(const void* q, const void* k_pages, const void* v_pages, const int* block_table, const int* seq_lens,
@@ -1272,7 +1276,7 @@ int fa_decode_shared(const void* q, const void* k_pages, const void* v_pages, co
     if (!shared_len) return FA_ERR_INVALID_ARG;
     DecodeRowsLaunch a;
     int st = rows_prepare(a, q, k_pages, v_pages, block_table, seq_lens, o, lse, B, Hq, Hkv, Nq, page_size, 1, max_pages,
-                          num_pages, d, scale);
+                          num_pages, d, scale, Hkv >= 1 && prefix_takes_own(B, Hq, Hkv, Nq));
     if (st != FA_OK) return st;
     if (page_size % 8) return FA_ERR_UNSUPPORTED;  // boxes of 8 rows at least
     if (!aligned4(shared_len)) return FA_ERR_ALIGNMENT;
@@ -1288,7 +1292,8 @@ int fa_decode_shared(const void* q, const void* k_pages, const void* v_pages, co
     const PrefixWorkspace pw = prefix_workspace(B, Hq, Hkv, Nq, d);
     const long long most = ((long long)max_pages * page_size + 127) / 128;  // steps of an item
     if ((long long)Hkv * pw.tiles > 0x7FFFFFFFll / most) return FA_ERR_UNSUPPORTED;
-    const RowsWorkspace ws = rows_workspace(B, Hq, Hkv, Nq, d);
+    a.merge_only = prefix_takes_own(B, Hq, Hkv, Nq);
+    const RowsWorkspace ws = rows_workspace(B, Hq, Hkv, Nq, d, 0, a.merge_only);
     if (!workspace || workspace_bytes < ws.bytes + pw.bytes) return FA_ERR_WORKSPACE;
     if (!aligned16(workspace)) return FA_ERR_ALIGNMENT;
     char* base = static_cast<char*>(workspace);
@@ -1313,7 +1318,7 @@ int fa_decode_shared(const void* q, const void* k_pages, const void* v_pages, co
     p.d = d;
     p.tiles = pw.tiles;
     p.tile_rows = pw.tile_rows;
-    p.own = prefix_takes_own(Hq, Hkv, Nq);
+    p.own = a.merge_only;
     p.workers = std::min(a.num_sms, kPrefixMostWorkers);
     if (!p.own) p.workers = (int)std::min<long long>(p.workers, most * Hkv * pw.tiles);  // a step each
     p.scale = scale;
@@ -1330,7 +1335,6 @@ int fa_decode_shared(const void* q, const void* k_pages, const void* v_pages, co
     a.pre_workers = p.workers;
     a.pre_tiles = p.tiles;
     a.pre_rows = p.tile_rows;
-    a.merge_only = p.own;
     st = launched(launch_prefix(p, a, (cudaStream_t)stream));
     return st != FA_OK ? st : launched(launch_decode_rows(a, (cudaStream_t)stream));
 }

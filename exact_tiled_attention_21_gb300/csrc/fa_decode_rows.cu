@@ -211,7 +211,7 @@ cudaError_t launch_r(const DecodeRowsLaunch& a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_decode_rows(const DecodeRowsLaunch& a, cudaStream_t s) {
-    const int tile = rows_tile(a.joint ? a.joint : a.Hq / a.Hkv * a.Nq);
+    const int tile = a.merge_only ? 8 : rows_tile(a.joint ? a.joint : a.Hq / a.Hkv * a.Nq);
     if (a.d == 128) return tile == 8 ? launch_r<128, 8>(a, s) : tile == 16 ? launch_r<128, 16>(a, s) : launch_r<128, 32>(a, s);
     return tile == 8 ? launch_r<64, 8>(a, s) : tile == 16 ? launch_r<64, 16>(a, s) : launch_r<64, 32>(a, s);
 }

@@ -1,7 +1,7 @@
 // Attention of 1..16 new tokens per sequence over the paged bf16 cache: over the
 // blocks of a list, or over the tokens that follow a prefix which all sequences
-// share.  The prefix itself is fa_prefix.cu's, which with up to 8 rows of a sequence and
-// kv head runs this beside it; or, where all sequences together have few query rows per
+// share.  The prefix itself is fa_prefix.cu's, which with few rows of a sequence and kv
+// head runs this beside it; or, where all sequences together have few query rows per
 // kv head and little to share, it is one more sequence here for each 32 of them.
 //
 // 4 d bytes per key for 4 d flops per query row: bound by HBM.  The work is one

@@ -284,7 +284,7 @@ struct PrefixLaunch {
     float* part_lse;           // fp32 [workers + Hkv * tiles, tile_rows]
     int* ends;                 // int32 [Hkv * tiles, 2]: the CTAs of an item's first and last step
     int B, Hq, Hkv, Nq, page, box, max_pages, num_pages, d, tiles, tile_rows, workers;
-    bool own;                  // the own tokens are this kernel's too (up to 8 rows of a sequence and kv head)
+    bool own;                  // the own tokens are this kernel's too, 8 rows of a sequence and kv head at a time
     float scale;
     DevError* err;
     uint64_t timeout_ns;
@@ -308,7 +308,7 @@ struct DecodeRowsLaunch {
     const int* pre_ends;
     int B, Hq, Hkv, Nq, page, block, keep, max_pages, num_pages, d;
     int pre_workers, pre_tiles, pre_rows;
-    bool merge_only;       // the prefix kernel did the rest
+    bool merge_only;       // the prefix kernel does the rest, in tiles of 8 rows
     int joint;             // query rows of all sequences per kv head where the prefix is this kernel's too, else 0
     int num_sms;
     float scale;

@@ -26,14 +26,16 @@
 // sequence that does not see all of the prefix are computed and not written: its own
 // pass takes all its keys.
 //
-// Up to 8 rows of a sequence and kv head, the own tokens are this kernel's too: the
+// Up to 16 rows of a sequence and kv head (32 in small batches), in eights, the own
+// tokens are this kernel's too: the
 // prefix is bound by the tensor cores or, where it is short, by latencies, the own
 // tokens by HBM, and run after one another they wait for each other's start and end.
 // The CTAs are divided by the times that both would take; one with own tokens runs
 // fa_decode_rows.cuh twice, on four warps each.  (32 sequences, 8192 shared tokens and up
 // to 512 own ones, 4 heads per kv head: 31.3 us in two kernels, 23.7 in one; 64, 32768
-// and 1000, two new tokens: 106 and 94.)  With 16 rows and more the own tokens' registers
-// do not fit beside.
+// and 1000, two new tokens: 106 and 94.)  A pass over 16 or 32 rows at a time needs more
+// registers than there are beside the prefix; the passes over eights read own tokens
+// again, mostly out of L2.
 #include <algorithm>
 
 #include "fa_decode_rows.cuh"

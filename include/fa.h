@@ -507,7 +507,7 @@ size_t fa_decode_blocks_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d);
  * Results do not depend on the run (fixed order of additions), but for rounding on
  * the batch that a sequence is in.  Tokens past seq_lens[b] are never used, and one
  * that a query does not see does not reach it, whatever it holds.  Steps of 64 keys
- * (and two more) over all sequences at full capacity, kv heads and tiles of 32
+ * (and two more) over all sequences at full capacity, kv heads and tiles of 8
  * query rows must stay below 2^31 (FA_ERR_UNSUPPORTED).  No output may overlap an input (o = q:
  * FA_ERR_INVALID_ARG).  workspace as for fa_select_blocks. */
 int fa_decode_blocks(const void *q, const void *k_pages, const void *v_pages, const int *block_table,

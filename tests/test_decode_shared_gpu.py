@@ -203,10 +203,15 @@ def test_wild_values_of_the_prefix_and_of_its_page(cuda_lib):
     (18, 1, 4, 2, 128, 0),
     (160, 32, 8, 1, 64, 140),     # more (kv head, 256 rows) than CTAs
     (130, 16, 2, 1, 128, 129),
+    (20, 2, 4, 4, 128, 600),      # 16 rows of a sequence, two passes over its own tokens
+    (33, 3, 1, 9, 64, 1000),      # 9
+    (9, 3, 5, 5, 128, 300),       # 25
+    (7, 2, 8, 4, 64, 1500),       # 32
+    (44, 3, 6, 4, 128, 260),      # 24 of more than 128 pairs: kernels of their own
 ])
 def test_prefix_and_own_tokens_in_one_kernel(cuda_lib, B, Hkv, G, Nq, d, shared):
-    """Up to 8 query rows of a sequence and kv head, more than 128 of all: own tokens from none to much more than the prefix,
-    sequences that do not take part, and batches in which none does."""
+    """More than 128 query rows of all sequences: own tokens from few to more than the prefix, sequences that do not take part,
+    and batches in which none does."""
     rng = np.random.default_rng(B + d)
     page, scale = 32, 1.0 / math.sqrt(d)
     lens = shared + rng.integers(Nq, 60, B)
