@@ -247,3 +247,43 @@ def test_bad_lengths_are_noted_whichever_kernel_takes_them(cuda_lib, B):
         o, lse = cuda_lib.decode_shared(q.to(DEV), g["k"], g["v"], ints(table), ints(lens), ints([given]))
         assert cuda_lib.fa_get_last_device_error()[0] == cuda_lib.FA_ERR_INVALID_ARG, where
         check_rows(o, lse, op.attend(f64(q), c, table, np.clip(lens, 0, cap), 1 / math.sqrt(d)), ONE)
+
+
+def test_one_kernel_replayed_with_other_lengths_and_on_two_streams(cuda_lib):
+    """The division of CTAs follows the lengths on the device: a captured call replayed with other lengths and another prefix
+    gives what a fresh call does; two calls at once on streams of their own give what they do one after the other."""
+    rng = np.random.default_rng(12)
+    B, Hkv, G, d, page, scale = 40, 4, 4, 128, 32, 1.0 / math.sqrt(128)
+    cases = []
+    for shared, most in ((600, 40), (64, 500), (0, 30), (600, 0)):
+        lens = shared + rng.integers(1, most + 2, B) if most else np.zeros(B, dtype=np.int64)
+        cases.append((shared, lens))
+    c, table = _case(4, np.full(B, 1200), 600, Hkv, page, d)
+    table[:, :600 // page] = table[0, :600 // page]
+    q, g, tab = bf16(rng, (B, Hkv * G, 1, d), 0.3).to(DEV), to_gpu(c), ints(table)
+    lens, shared = ints(cases[0][1]), ints([cases[0][0]])
+    cuda_lib.decode_shared(q, g["k"], g["v"], tab, lens, shared)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, lse = cuda_lib.decode_shared(q, g["k"], g["v"], tab, lens, shared)
+    fresh = []
+    for n, (s, l) in enumerate(cases * 2):
+        lens.copy_(ints(l))
+        shared.copy_(ints([s]))
+        graph.replay()
+        want = cuda_lib.decode_shared(q, g["k"], g["v"], tab, ints(l), ints([s]))
+        ok(cuda_lib)
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1]), n
+        fresh.append(want)
+        if n < 2:
+            check_rows(o, lse, op.attend(f64(q.cpu()), c, table, l, scale), ONE)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    args = [(ints(l), ints([s])) for s, l in cases]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        got = [cuda_lib.decode_shared(q, g["k"], g["v"], tab, *args[i], stream=streams[i % 2]) for i in range(4)]
+        torch.cuda.synchronize()
+        for a, b in zip(got, fresh):
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    ok(cuda_lib)
