@@ -53,8 +53,11 @@ struct Pre {
     static constexpr int ROWS_BYTES = Cfg<D, 8>::SMEM, OFF_SHARED = 2 * ROWS_BYTES;  // the own tokens' two lots of four warps
     static constexpr int OFF_BAR = std::max(OFF_KV + NSLOT * KV_BYTES, OFF_SHARED + 2 * 1024);
     static_assert(sizeof(RowsShared<8>) <= 1024 && ROWS_BYTES % 128 == 0, "layout");
-    // barriers: kv_full[NSLOT], kv_empty[NSLOT], q_full[2], s_full[2], p_full[2], o_final[2], pv_done, teardown
-    static constexpr int NBAR = 2 * NSLOT + 10, OFF_MISC = OFF_BAR + NBAR * 8, SMEM = OFF_MISC + 16 + 1024;
+    // barriers: kv_full[NSLOT], kv_empty[NSLOT], q_full[2], s_full[3], p_full[3], o_final[2], pv_done, teardown.  s_full and
+    // p_full: of tile 0's first buffer, of tile 1's, and of tile 0's second one where it is alone.  The last two share columns and not
+    // a barrier: tile 1 passes over the segments of one tile, and a wait by parity is right only if none of a barrier's
+    // earlier phases was passed over.
+    static constexpr int NBAR = 2 * NSLOT + 12, OFF_MISC = OFF_BAR + NBAR * 8, SMEM = OFF_MISC + 16 + 1024;
     static constexpr int THREADS = 320;
     static constexpr uint32_t TMEM_COLS = 512, COL_S = 0, COL_O = 256;  // tile t: + 128 t, + D t
     static constexpr uint32_t IDESC_S = idesc_bf16(128, BN, 0, 0);      // Q, K both K-major
@@ -102,7 +105,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
     const uint32_t s_base = smem_u32(smem), bar0 = s_base + C::OFF_BAR;
     auto bar_full = [&](int s) { return bar0 + 8 * s; };
     auto bar_empty = [&](int s) { return bar0 + 8 * C::NSLOT + 8 * s; };
-    const uint32_t BAR_Q = bar0 + 16 * C::NSLOT, BAR_S = BAR_Q + 16, BAR_P = BAR_S + 16, BAR_O = BAR_P + 16, BAR_PV = BAR_O + 16,
+    const uint32_t BAR_Q = bar0 + 16 * C::NSLOT, BAR_S = BAR_Q + 16, BAR_P = BAR_S + 24, BAR_O = BAR_P + 24, BAR_PV = BAR_O + 16,
                    BAR_TD = BAR_PV + 8;
     uint32_t* tmem_slot = (uint32_t*)(smem + C::OFF_MISC);
     volatile int* abort_flag = (volatile int*)(smem + C::OFF_MISC + 4);
@@ -113,9 +116,11 @@ prefix_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
         for (int s = 0; s < 2 * C::NSLOT; ++s) mbar_init(bar0 + 8 * s, 1);
         for (int t = 0; t < 2; ++t) {
             mbar_init(BAR_Q + 8 * t, 128);
-            mbar_init(BAR_S + 8 * t, 1);
-            mbar_init(BAR_P + 8 * t, 128);
             mbar_init(BAR_O + 8 * t, 1);
+        }
+        for (int i = 0; i < 3; ++i) {
+            mbar_init(BAR_S + 8 * i, 1);
+            mbar_init(BAR_P + 8 * i, 128);
         }
         mbar_init(BAR_PV, 1);
         mbar_init(BAR_TD, 1);
@@ -254,7 +259,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
         // ------------------------------------------------------------ MMA issuer
         if (lane == 0 && !*abort_flag) {
             int slot = 0;
-            uint32_t phase = 0, p_iter = 0, q_iter = 0, p1_iter = 0, q1_iter = 0;
+            uint32_t phase = 0, p_iter = 0, q_iter = 0, p1_iter = 0, p2_iter = 0, q1_iter = 0;
             auto issue_s = [&](int t, uint32_t sK, int buf) {
                 const uint64_t a0 = sdesc_sw128(s_base + C::OFF_Q + t * C::Q_BYTES, 16, 1024), b0 = sdesc_sw128(sK, 16, 1024);
                 const uint32_t d = tmem + C::COL_S + 128 * buf;
@@ -303,11 +308,11 @@ prefix_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
                             tc_fence_after();
                             next();
                             issue_s(0, kv_at(kslot), buf ^ 1);
-                            mma_commit(BAR_S + 8 * (buf ^ 1));
+                            mma_commit(BAR_S + 16 * (buf ^ 1));
                             mma_commit(bar_empty(kslot));
                         }
                         if (!mbar_wait(bar_full(vslot), vphase, ctl, kSiteKvFull)) { ok = false; break; }
-                        if (!mbar_wait(BAR_P + 8 * buf, (buf ? p1_iter++ : p_iter++) & 1, ctl, kSitePFull)) { ok = false; break; }
+                        if (!mbar_wait(BAR_P + 16 * buf, (buf ? p2_iter++ : p_iter++) & 1, ctl, kSitePFull)) { ok = false; break; }
                         tc_fence_after();
                         issue_o(0, kv_at(vslot), s > g.s0, buf);
                         mma_commit(bar_empty(vslot));
@@ -359,18 +364,23 @@ prefix_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
         const int t = warp >> 2, r = tid & 127;  // tile; row within it = TMEM lane
         const uint32_t lane_addr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t col_o = C::COL_O + D * t;
-        // handoffs before the segment: of the scores' buffers, of the products of one tile, of the ring's fills; of O so far
-        uint32_t s_next0 = 0, s_next1 = 0, pv_next = 0, kv_fill = 0, o_iter = 0;
+        // handoffs before the segment: by the three barriers of scores, of the products of one tile, of the ring's fills; of O so far
+        uint32_t s_next0 = 0, s_next1 = 0, s_next2 = 0, pv_next = 0, kv_fill = 0, o_iter = 0;
+        uint64_t skipped = 0;  // steps of one tile since tile 1's last segment
         for (uint32_t u = u0; u < u1;) {
             const Segment g = segment_at(u);
             const int nst = g.s1 - g.s0;
             u += nst;
-            const uint32_t fill0 = kv_fill, s0 = s_next0, s1 = s_next1, pv0 = pv_next;
+            const uint32_t fill0 = kv_fill, s0 = s_next0, s1 = g.two ? s_next1 : s_next2, pv0 = pv_next;
             kv_fill += 2 * nst;
             s_next0 += g.two ? nst : (nst + 1) / 2;
-            s_next1 += g.two ? nst : nst / 2;
+            s_next1 += g.two ? nst : 0;
+            s_next2 += g.two ? 0 : nst / 2;
             pv_next += g.two ? 0 : nst - 1;
-            if (t == 1 && !g.two) continue;
+            if (t == 1 && !g.two) {
+                skipped += nst;
+                continue;
+            }
             // ---- the tile's query rows, coalesced: D / 8 lanes a row; those past the last one are zeros
             {
                 uint8_t* sq = smem + C::OFF_Q + t * C::Q_BYTES;
@@ -397,9 +407,12 @@ prefix_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
             bool ok = true;
             for (int j = 0; j < nst; ++j) {
                 const int buf = g.two ? t : j & 1;  // one tile takes both buffers in turn
-                const uint32_t col_s = C::COL_S + 128 * buf;
+                const uint32_t col_s = C::COL_S + 128 * buf, bar = 8 * (g.two ? t : 2 * buf);
                 const uint32_t nth = (buf ? s1 : s0) + (g.two ? j : j >> 1);
-                if (!mbar_wait(BAR_S + 8 * buf, nth & 1, ctl, kSiteSFull)) { ok = false; break; }
+                WaitCtl limit = ctl;  // tile 1's first scores come behind the segments that it passed over: 10 us a step
+                limit.timeout_ns += skipped * 10000;
+                skipped = 0;
+                if (!mbar_wait(BAR_S + bar, nth & 1, limit, kSiteSFull)) { ok = false; break; }
                 tc_fence_after();
                 const int nk = min(128, shared - (g.s0 + j) * 128);  // at least 1
                 const float mraw = nk < 128 ? row_max_pass<true>(lane_addr + col_s, nk - 1, 0)
@@ -443,7 +456,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 }
                 tc_fence_before();
-                mbar_arrive(BAR_P + 8 * buf);
+                mbar_arrive(BAR_P + bar);
             }
             if (!ok || !mbar_wait(BAR_O + 8 * t, o_iter & 1, ctl, kSiteOFinal)) break;
             ++o_iter;
