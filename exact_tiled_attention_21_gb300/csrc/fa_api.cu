@@ -836,7 +836,9 @@ RowsWorkspace rows_workspace(int B, int Hq, int Hkv, int Nq, int d, int joint = 
     return w;
 }
 
-// Workspace of the shared prefix: the same of (kv head, tile of the batch's query rows) items.
+// Workspace of the shared prefix: the same of (kv head, tile of the batch's query rows) items.  Its parts are stored 32 bytes
+// at a time; a caller's workspace has 16-byte alignment, so the call may skip kPrefixSkip bytes at its start.
+constexpr size_t kPrefixSkip = 16;
 struct PrefixWorkspace {
     int tiles, tile_rows;
     size_t part_lse, ends, bytes;
@@ -1267,7 +1269,8 @@ size_t fa_decode_shared_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d) {
     if (!rows_sizes_ok(B, Hq, Hkv, Nq, d)) return 0;
     // the larger of the two forms', whichever the table's width will choose
     return std::max(rows_workspace(B, Hq, Hkv, Nq, d, joint_rows(B, Hq, Hkv, Nq, d, 0)).bytes,
-                    rows_workspace(B, Hq, Hkv, Nq, d, 0, prefix_takes_own(B, Hq, Hkv, Nq)).bytes + prefix_workspace(B, Hq, Hkv, Nq, d).bytes);
+                    rows_workspace(B, Hq, Hkv, Nq, d, 0, prefix_takes_own(B, Hq, Hkv, Nq)).bytes + prefix_workspace(B, Hq, Hkv, Nq, d).bytes +
+                        kPrefixSkip);
 }
 
 int fa_decode_shared(const void* q, const void* k_pages, const void* v_pages, const int* block_table, const int* seq_lens,
@@ -1294,9 +1297,9 @@ int fa_decode_shared(const void* q, const void* k_pages, const void* v_pages, co
     if ((long long)Hkv * pw.tiles > 0x7FFFFFFFll / most) return FA_ERR_UNSUPPORTED;
     a.merge_only = prefix_takes_own(B, Hq, Hkv, Nq);
     const RowsWorkspace ws = rows_workspace(B, Hq, Hkv, Nq, d, 0, a.merge_only);
-    if (!workspace || workspace_bytes < ws.bytes + pw.bytes) return FA_ERR_WORKSPACE;
+    if (!workspace || workspace_bytes < ws.bytes + pw.bytes + kPrefixSkip) return FA_ERR_WORKSPACE;
     if (!aligned16(workspace)) return FA_ERR_ALIGNMENT;
-    char* base = static_cast<char*>(workspace);
+    char* base = static_cast<char*>(workspace) + (reinterpret_cast<uintptr_t>(workspace) & kPrefixSkip);
     rows_place(a, base);
     base += ws.bytes;
     PrefixLaunch p;

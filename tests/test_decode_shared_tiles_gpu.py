@@ -1,5 +1,5 @@
 """fa_decode_shared where a kv head's query rows end in a tile of at most 128: CTAs that go from such an item to one of 256 rows
-of the next kv head."""
+of the next kv head; and its workspaces."""
 import math
 
 import numpy as np
@@ -38,4 +38,30 @@ def test_short_last_tiles(cuda_lib, B, Hkv, G, Nq, d, shared, most):
     for _ in range(20):                # whichever of the CTA's warps comes first
         again = cuda_lib.decode_shared(*args)
         assert torch.equal(again[0], o) and torch.equal(again[1], lse)
+    ok(cuda_lib)
+
+
+@pytest.mark.parametrize("B,Hkv,G,Nq,d,shared", [
+    (3, 2, 4, 1, 128, 100),            # one list of steps
+    (40, 2, 4, 1, 128, 300),           # own tokens in the prefix's kernel, one tile of rows and two
+    (40, 2, 8, 1, 64, 300),
+    (70, 2, 9, 4, 128, 300),           # in a kernel of their own
+])
+def test_a_workspace_of_16_byte_alignment(cuda_lib, B, Hkv, G, Nq, d, shared):
+    """What a call needs of its workspace is 16-byte alignment and the stated size; nothing is written beside it."""
+    rng = np.random.default_rng(B + d)
+    lens = shared + rng.integers(Nq, 40, B)
+    c, table = _case(3, lens, shared, Hkv, 8, d)
+    q, g = bf16(rng, (B, Hkv * G, Nq, d), 0.3), to_gpu(c)
+    args = (q.to(DEV), g["k"], g["v"], ints(table), ints(lens), ints([shared]))
+    o, lse = cuda_lib.decode_shared(*args)
+    check_rows(o, lse, op.attend(f64(q), c, table, lens, 1.0 / math.sqrt(d)), ONE)
+    size = cuda_lib.fa_decode_shared_workspace_bytes(B, Hkv * G, Hkv, Nq, d)
+    for at in (16, 32, 48, 208):
+        room = torch.full((size + 512,), 0xA5, dtype=torch.uint8, device=DEV)
+        w = room[at:at + size]
+        assert w.data_ptr() % 32 == at % 32
+        again = cuda_lib.decode_shared(*args, workspace=w)
+        assert torch.equal(again[0], o) and torch.equal(again[1], lse)
+        assert (room[:at] == 0xA5).all() and (room[at + size:] == 0xA5).all()
     ok(cuda_lib)
