@@ -15,41 +15,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, ROWS>::CTAS) decode_rows_kern
 }
 
 // ------------------------------------------------------------------ merge
-// A row's parts: `n` slots from `slot` on of the segments, `pn` from `pslot` on of the shared prefix.
-struct Parts {
-    long long slot, pslot;
-    int n, pn;
-    bool done;  // written already
-};
-
-// An item's segments are those of the CTAs from that of its first to that of its last step; CTA c's is in slot c + item.
-template <bool LIST>
-__device__ __forceinline__ Parts find_parts(const Params& a, int b, int kvh, int rt, int row) {
-    const int item = (b * a.Hkv + kvh) * a.row_tiles + rt, cap = a.max_pages * (int)a.page.d;
-    int shared = 0, place = 0;
-    int2 pre = make_int2(0, -1);
-    if constexpr (!LIST) {
-        shared = clamp_len(*a.shared, cap);
-        place = (b * a.rows + row) / a.pre_rows;
-        place = a.joint ? place * a.Hkv + kvh : kvh * a.pre_tiles + place;
-        pre = reinterpret_cast<const int2*>(a.pre_ends)[place];
-    }
-    const int2 own = reinterpret_cast<const int2*>(a.ends)[item];
-    const int len = clamp_len(a.lens[b], cap);
-    Parts x{0, 0, 0, 0, false};
-    if (keys_of<LIST>(a, len, shared) > 0) {
-        x.slot = (long long)own.x + item;
-        x.n = own.y - own.x + 1;
-    }
-    // (a prefix kernel whose waits ran out may not have noted its items' ends)
-    if (!LIST && shared_of(shared, len, a.Nq) > 0 && pre.x >= 0 && pre.x <= pre.y && pre.y < a.pre_workers) {
-        x.pslot = pre.x + a.pre_item + place;
-        x.pn = pre.y - pre.x + 1;
-    }
-    x.done = x.n == 1 && x.pn == 0;
-    return x;
-}
-
 // LSE = M + log2 sum 2^(lse_s - M), O = sum 2^(lse_s - M) o_s / sum over a row's parts.  D / 4 threads per row and group;
 // SPLIT: one row per block, its parts dealt to the groups, else a row per group.  A row without keys gets O = 0, LSE = -inf.
 template <int D, int ROWS, bool LIST, bool SPLIT, int THREADS>

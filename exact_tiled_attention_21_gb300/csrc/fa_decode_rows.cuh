@@ -121,17 +121,20 @@ struct Params {
     DevError* err;
 };
 
-__device__ __forceinline__ int clamp_len(int len, int cap) { return min(max(len, 0), cap); }
+__host__ __device__ __forceinline__ int clamp_len(int len, int cap) { return min(max(len, 0), cap); }
 
 // The shared tokens that sequences of these lengths read from the common prefix: none if some new token of it does not see
 // all of them.
-__device__ __forceinline__ int shared_of(int shared, int len, int Nq) { return len - Nq >= shared ? shared : 0; }
+__host__ __device__ __forceinline__ int shared_of(int shared, int len, int Nq) { return len - Nq >= shared ? shared : 0; }
 
 // A sequence's keys in this pass.
 template <bool LIST>
-__device__ __forceinline__ int keys_of(const Params& a, int len, int shared) {
-    if (LIST) return min(a.keep, (int)a.block.div(len + a.block.d - 1)) * (int)a.block.d;
-    return len - shared_of(shared, len, a.Nq);
+__host__ __device__ __forceinline__ int keys_of(const Params& a, int len, int shared) {
+    if constexpr (LIST) {
+        return min(a.keep, (int)a.block.div(len + a.block.d - 1)) * (int)a.block.d;
+    } else {
+        return len - shared_of(shared, len, a.Nq);
+    }
 }
 
 // The same of any place in the list of sequences; from B on it is the prefix, if that is this kernel's: every row sees all
@@ -783,6 +786,41 @@ __device__ __forceinline__ void decode_rows(const Params& a, uint8_t* smem, Rows
         if (a.cluster > 1) cluster_sync();  // the others have read this CTA's
     }
     if (__any_sync(0xffffffffu, bad) && lane == 0) record_invalid(a.err, kSiteCacheTable, -1);
+}
+
+// A row's parts: `n` slots from `slot` on of the segments, `pn` from `pslot` on of the shared prefix.
+struct Parts {
+    long long slot, pslot;
+    int n, pn;
+    bool done;  // written already
+};
+
+// An item's segments are those of the CTAs from that of its first to that of its last step; CTA c's is in slot c + item.
+template <bool LIST>
+__host__ __device__ __forceinline__ Parts find_parts(const Params& a, int b, int kvh, int rt, int row) {
+    const int item = (b * a.Hkv + kvh) * a.row_tiles + rt, cap = a.max_pages * (int)a.page.d;
+    int shared = 0, place = 0;
+    int2 pre = make_int2(0, -1);
+    if constexpr (!LIST) {
+        shared = clamp_len(*a.shared, cap);
+        place = (b * a.rows + row) / a.pre_rows;
+        place = a.joint ? place * a.Hkv + kvh : kvh * a.pre_tiles + place;
+        pre = reinterpret_cast<const int2*>(a.pre_ends)[place];
+    }
+    const int2 own = reinterpret_cast<const int2*>(a.ends)[item];
+    const int len = clamp_len(a.lens[b], cap);
+    Parts x{0, 0, 0, 0, false};
+    if (keys_of<LIST>(a, len, shared) > 0) {
+        x.slot = (long long)own.x + item;
+        x.n = own.y - own.x + 1;
+    }
+    // (a prefix kernel whose waits ran out may not have noted its items' ends)
+    if (!LIST && shared_of(shared, len, a.Nq) > 0 && pre.x >= 0 && pre.x <= pre.y && pre.y < a.pre_workers) {
+        x.pslot = pre.x + a.pre_item + place;
+        x.pn = pre.y - pre.x + 1;
+    }
+    x.done = x.n == 1 && (LIST || shared_of(shared, len, a.Nq) == 0);  // as decode_rows decides it, parts of the prefix or not
+    return x;
 }
 
 template <int D, int ROWS>
