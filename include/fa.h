@@ -506,10 +506,12 @@ size_t fa_decode_blocks_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d);
  * are fp32; for the value product a softmax weight is rounded to 16 bits (2^-17).
  * Results do not depend on the run (fixed order of additions), but for rounding on
  * the batch that a sequence is in.  Tokens past seq_lens[b] are never used, and one
- * that a query does not see does not reach it, whatever it holds.  Steps of 64 keys
- * (and two more) over all sequences at full capacity, kv heads and tiles of 8
- * query rows must stay below 2^31 (FA_ERR_UNSUPPORTED).  No output may overlap an input (o = q:
- * FA_ERR_INVALID_ARG).  workspace as for fa_select_blocks. */
+ * that a query does not see does not reach it, whatever it holds.  (B + 4) x Hkv x
+ * tiles x (steps + 2) must stay below 2^31 (FA_ERR_UNSUPPORTED), with steps = (max_pages *
+ * page_size + block) / 64, rounded up, and the tiles that a kv head's Hq / Hkv x Nq
+ * query rows make: of 8 rows, of 16 if there are more, of 32 if there are more than
+ * 16.  No output may overlap an input (o = q: FA_ERR_INVALID_ARG).  workspace as for
+ * fa_select_blocks. */
 int fa_decode_blocks(const void *q, const void *k_pages, const void *v_pages, const int *block_table,
                      const int *seq_lens, const int *blocks, void *o, float *lse, int B, int Hq, int Hkv, int Nq,
                      int page_size, int block, int keep, int max_pages, int num_pages, int d, float scale,
@@ -531,8 +533,9 @@ size_t fa_decode_shared_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d);
  * without a sequence, or a shorter one) read all their tokens through their own
  * row.  For the product of a shared token's weight and value the weight is rounded
  * to bf16 (2^-9), for own tokens to 16 bits.  Errors, workspace (its size:
- * fa_decode_shared_workspace_bytes) and the rest as for fa_decode_blocks; page_size
- * must be a multiple of 8 (FA_ERR_UNSUPPORTED). */
+ * fa_decode_shared_workspace_bytes) and the rest as for fa_decode_blocks (in its limit
+ * block is 1, and the tiles are of 8 rows up to 16 rows, and up to 32 where B * Hkv
+ * <= 128); page_size must be a multiple of 8 (FA_ERR_UNSUPPORTED). */
 int fa_decode_shared(const void *q, const void *k_pages, const void *v_pages, const int *block_table,
                      const int *seq_lens, const int *shared_len, void *o, float *lse, int B, int Hq, int Hkv, int Nq,
                      int page_size, int max_pages, int num_pages, int d, float scale, void *workspace,

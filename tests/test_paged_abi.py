@@ -98,6 +98,30 @@ def test_shared_refusals(lib, bad, status):
     assert _shared(lib, **bad) == status
 
 
+@pytest.mark.parametrize("call,G,Nq,Hkv,few,tile", [
+    (_blocks, 4, 2, 64, 0, 8), (_blocks, 4, 4, 64, 0, 16), (_blocks, 17, 1, 64, 0, 32), (_blocks, 8, 16, 16, 0, 32),
+    (_blocks, 1, 1, 1 << 14, 0, 8),
+    (_shared, 4, 2, 64, 0, 8), (_shared, 4, 4, 64, 0, 8), (_shared, 17, 1, 64, 0, 32), (_shared, 8, 16, 16, 0, 32),
+    (_shared, 17, 1, 8, 16, 8), (_shared, 17, 1, 8, 17, 32),
+])
+def test_most_steps(lib, call, G, Nq, Hkv, few, tile):
+    """(B + 4) Hkv tiles (steps + 2) < 2^31, at the largest B (few: at this one, by the largest table) that the rule takes and at the
+    next.  An alignment error, which is looked for later, shows that a call passes it."""
+    tiles, block = -(-G * Nq // tile), 16 if call is _blocks else 1
+    most = lambda B, tokens: (B + 4) * Hkv * tiles * (-(-(tokens + block) // 64) + 2) < 1 << 31
+    tokens = 1 << 18
+    if few:
+        steps = ((1 << 31) - 1) // ((few + 4) * Hkv * tiles) - 2
+        tokens = min(steps * 64 - block, 1 << 30) // 32 * 32
+        pairs = [(few, tokens)] + ([(few, tokens + 64)] if tokens + 64 <= 1 << 30 else [])
+    else:
+        B = ((1 << 31) - 1) // (Hkv * tiles * (-(-(tokens + block) // 64) + 2)) - 4
+        pairs = [(B, tokens), (B + 1, tokens)]
+    for B, tokens in pairs:
+        got = call(lib, B=B, Hq=G * Hkv, Hkv=Hkv, Nq=Nq, maxp=tokens // 32, pages=8, table=2)
+        assert got == (ALI if most(B, tokens) else UNS), (B, tokens)
+
+
 def test_workspaces():
     """Sizes for what the calls take, none for what they refuse; large enough for the partial results of every CTA."""
     f = fa.fa_select_blocks_workspace_bytes
