@@ -35,7 +35,8 @@
 // pass through shared memory again.  Softmax sums are fp32.  A row's weights are
 // taken relative to a running reference within 2^8 of its largest score, and enter
 // the value product as bf16 pairs of a rounded weight and what the rounding left:
-// one bf16 (2^-9) would cost as much as the rounding of the result.
+// one bf16 (2^-8) would cost as much as the rounding of the result; of a pair the
+// second number, below 2^-8 of the weight, is off by half a step, 2^-17 of it.
 #pragma once
 #include <algorithm>
 #include <cfloat>

@@ -532,7 +532,8 @@ size_t fa_decode_shared_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d);
  * shared pages are not looked at), the others through its own row.  Others (a slot
  * without a sequence, or a shorter one) read all their tokens through their own
  * row.  For the product of a shared token's weight and value the weight is rounded
- * to bf16 (2^-9), for own tokens to 16 bits.  Errors, workspace (its size:
+ * to bf16 (2^-8), or to 16 bits (2^-17) in small batches with narrow tables; for own
+ * tokens it is to 16 bits.  Errors, workspace (its size:
  * fa_decode_shared_workspace_bytes) and the rest as for fa_decode_blocks (in its limit
  * block is 1, and the tiles are of 8 rows up to 16 rows, and up to 32 where B * Hkv
  * <= 128); page_size must be a multiple of 8 (FA_ERR_UNSUPPORTED). */
