@@ -373,13 +373,20 @@ PyObject* select_blocks(PyObject*, PyObject* const* o, Py_ssize_t n) {
     const int block = integer(o[4]), keep = integer(o[5]), first = integer(o[6]), recent = integer(o[7]);
     const c10::cuda::CUDAGuard guard(dev);
     const int64_t most = (int64_t)max_pages * per_page;
+    void* stream = stream_of(dev);
+    auto select = [&](int* out, void* ws, size_t bytes) {
+        return call([&] {
+            return fa_select_blocks(q.t.data_ptr(), bp, table, lens, out, B, q.Hq, Hkv, q.Nq, block, per_page, max_pages,
+                                    num_pages, d, keep, first, recent, ws, bytes, stream);
+        });
+    };
+    if (keep > most) {  // lists longer than the table's blocks: whatever else is wrong is refused before they take memory
+        const int st = select(const_cast<int*>(table), nullptr, 0);
+        if (st != FA_ERR_WORKSPACE) return status(st);
+    }
     const Tensor ws = workspace(o[8], fa_select_blocks_workspace_bytes(B, Hkv, most <= INT_MAX ? (int)most : 0), dev);
     const Tensor out = make({B, Hkv, std::max(keep, 0)}, at::kInt, dev);
-    void* stream = stream_of(dev);
-    const int st = call([&] {
-        return fa_select_blocks(q.t.data_ptr(), bp, table, lens, (int*)out.data_ptr(), B, q.Hq, Hkv, q.Nq, block, per_page,
-                                max_pages, num_pages, d, keep, first, recent, ws.data_ptr(), ws.nbytes(), stream);
-    });
+    const int st = select((int*)out.data_ptr(), ws.data_ptr(), ws.nbytes());
     return st != FA_OK ? status(st) : THPVariable_Wrap(out);
     END_HANDLE_TH_ERRORS
 }

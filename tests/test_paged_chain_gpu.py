@@ -272,3 +272,20 @@ def test_conveniences_refuse(cuda_lib):
             f()
         assert err.value.status == status
     ok(fa)
+
+
+def test_selection_refuses_before_it_takes_memory(cuda_lib):
+    """Lists of 2^31 - 1 blocks for 64 kv heads would be half a terabyte; a long list that is all right is filled with -1."""
+    fa, Hkv, d = cuda_lib, 64, 64
+    bounds = torch.zeros((2, Hkv, 2, 2, d), dtype=torch.bfloat16, device=DEV)
+    q = torch.zeros((1, Hkv, 17, d), dtype=torch.bfloat16, device=DEV)
+    tab, n, most = ints([[1, 0]]), ints([20]), 2 ** 31 - 1
+    for f, status in [(lambda: fa.select_blocks(q[:, :, 0].contiguous(), bounds, tab, n, block=8, keep=most, first=-1), fa.FA_ERR_INVALID_ARG),
+                      (lambda: fa.select_blocks(q[:, :, 0].contiguous(), bounds, tab, n, block=0, keep=most), fa.FA_ERR_INVALID_ARG),
+                      (lambda: fa.select_blocks(q, bounds, tab, n, block=8, keep=most), fa.FA_ERR_UNSUPPORTED)]:
+        with pytest.raises(fa.FAError) as err:
+            f()
+        assert err.value.status == status
+    got = fa.select_blocks(q[:, :, 0].contiguous(), bounds, tab, n, block=8, keep=100000)
+    assert (got[..., :3] == ints([0, 1, 2])).all() and (got[..., 3:] == -1).all()
+    ok(fa)
