@@ -766,8 +766,9 @@ def select_blocks(q, bounds, block_table, seq_lens, block, keep, first=0, recent
 
 def decode_blocks(q, k_pages, v_pages, block_table, seq_lens, blocks, block, scale=None, stream=None, workspace=None):
     """O [B,Hq,Nq,d] bf16 and LSE [B,Hq,Nq] fp32 of the last Nq tokens (q [B,Hq,Nq,d], or [B,Hq,d] for one, which gives O
-    [B,Hq,d] and LSE [B,Hq]) over the listed blocks of ``block`` tokens (int32 [B,Hkv,keep], distinct, any order, negative
-    ones skipped) of the paged bf16 cache, which holds those tokens already."""
+    [B,Hq,d] and LSE [B,Hq]) over the listed blocks of ``block`` tokens (int32 [B,Hkv,keep], distinct, any order) of the
+    paged bf16 cache, which holds those tokens already.  Of a list the first min(keep, ceil(seq_lens[b] / block)) entries
+    are looked at, and negative ones among these skipped: one with gaps may be no longer than the sequence has blocks."""
     if stream is not None:
         with _on_stream(stream, q):
             return decode_blocks(q, k_pages, v_pages, block_table, seq_lens, blocks, block, scale, None, workspace)

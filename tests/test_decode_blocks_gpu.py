@@ -192,3 +192,19 @@ def test_many_sequences(cuda_lib, G, Nq, d):
     o, lse = cuda_lib.decode_blocks(q.to(DEV), g["k"], g["v"], ints(table), ints(lens), ints(lists), block=block)
     ok(cuda_lib)
     check_rows(o, lse, op.attend(f64(q), c, table, lens, scale, op.tokens_of(lists, block)), PAIR)
+
+
+def test_entries_behind_a_sequence_s_number_of_blocks_are_not_looked_at(cuda_lib):
+    """Of a list the first min(keep, n_b) entries count: what lies behind them, good or bad, is neither used nor recorded."""
+    rng = np.random.default_rng(8)
+    Hkv, G, d, page, block, lens = 2, 4, 128, 16, 8, [33, 3, 0]          # 5, 1 and no blocks
+    c, table = random_pages(5, 12, Hkv, page, d), table_of(3, 3, 3, 12)
+    lists = np.tile(np.array([[4, -1, 0, 2, -1, 1, 3], [0, 0, 5, 7, 9, 1, 2 ** 31 - 1], [0, 1, 2, 3, 4, 5, 6]], dtype=np.int32)[:, None],
+                    (1, Hkv, 1))
+    counted = lists.copy()
+    for b, n in enumerate(lens):
+        counted[b, :, -(-n // block):] = -1
+    q, g = bf16(rng, (3, Hkv * G, 1, d), 0.3), to_gpu(c)
+    o, lse = cuda_lib.decode_blocks(q.to(DEV), g["k"], g["v"], ints(table), ints(lens), ints(lists), block=block)
+    ok(cuda_lib)
+    check_rows(o, lse, op.attend(f64(q), c, table, lens, 1 / math.sqrt(d), op.tokens_of(counted, block)), PAIR)
