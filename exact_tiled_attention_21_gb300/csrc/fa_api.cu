@@ -865,11 +865,13 @@ bool prefix_takes_own(int B, int Hq, int Hkv, int Nq) {
 }
 
 // Query rows of all sequences where decode_rows takes the prefix too, 0 where it does not: it reads the prefix once for each
-// 32 of them, which saves the other kernel's start and end where that is little work.  Measured with 8 kv heads, d = 128,
-// against the prefix's kernel with the own tokens in it: 4 rows of a sequence, 32 rows in all, 500 tokens 10.2 and 11.9 us, 2000
-// 13.5 and 13.3, 8000 20.2 and 17.2; 64 rows 11.7 and 12.4, 14.4 and 14.5, 25.5 and 18.2; 128 rows, 500 tokens 15.8 and 15.0;
-// 16 rows of a sequence, 128 in all, 500 tokens 13.0 and 14.4, 2000 17.6 and 16.8.  With fewer heads or d = 64 they meet where
-// tokens x heads x d does.  tokens: of the table; 0: where any table of such a batch would do.
+// 32 of them, which saves the other kernel's start and end where that is little work.  Measured with 8 kv heads, d = 128, up to 100
+// own tokens, against the prefix's kernel with the own tokens in it (calls back to back on 24 sets of inputs): 4 rows of a sequence, 32
+// rows in all, 1000 shared tokens 11.7 and 13.6 us, 2000 15.0 and 15.5, 4000 16.4 and 16.9; 64 rows 13.4 and 14.2, 2000 16.3 and
+// 16.0; 128 rows, 250 tokens 14.4 and 14.6, 500 15.3 and 15.5; 16 rows of a sequence, 128 in all, 500 tokens 13.2 and 14.2, 1000 15.6
+// and 14.8.  Far beyond the limits the prefix's kernel gains (32 rows, 8000 tokens 20.2 and 17.2; 64 rows 25.5 and 18.2).  With fewer
+// heads or d = 64 they meet where tokens x heads x d does.  tokens: of the table, since the host does not know how many are shared,
+// so that a batch in a wide table has the prefix's kernel whatever it shares; 0: where any table of such a batch would do.
 int joint_rows(int B, int Hq, int Hkv, int Nq, int d, long long tokens) {
     const long long rows = (long long)B * (Hq / Hkv) * Nq, tiles = (rows + 31) / 32;
     if (rows > 128 || Hq / Hkv * Nq > 32) return 0;

@@ -13,13 +13,14 @@
 namespace fa {
 namespace {
 
-// Every element is read once and written once: bound by HBM for prompts, by the latency of a launch and three dependent
-// loads (length, table, token) for single tokens.
+// Every element is read once and written once.  Single tokens are bound by the latency of a launch and three dependent loads
+// (length, table, token); prompts by latency too: each CTA has these loads, the sines and a barrier before its first store, and
+// registers leave two of them on an SM (14 of 64 warps active).
 //
 // Measured, 8 kv heads, d = 128, rotated, with bounds: one token of 32 sequences 3.5 us; 8 ragged prompts of up to 2048 tokens
-// 24.4 us (15.3 at HBM's copy rate; 59% of DRAM's peak and half of the issue slots in a capture of 32 full ones).
+// 24.8 us (15.3 at HBM's copy rate; about 60% of DRAM's peak and half of the issue slots in a capture of 32 full ones).
 //
-// append_kernel: a CTA takes a run of tokens, in whole blocks, of up to eight kv heads.  The tokens' places in the cache and
+// append_kernel: a CTA takes a run of tokens, in whole blocks, of up to four kv heads.  The tokens' places in the cache and
 // their cosines and sines are made once, in shared memory; then each warp takes the keys of a head, or its values, for
 // itself, without waiting for others: RP rows at a time, four of these loaded ahead, 16 columns of a row (the two pieces
 // that a rotation pairs) per lane.  The extremes of a block gather in the lanes' registers over its rows and are joined by

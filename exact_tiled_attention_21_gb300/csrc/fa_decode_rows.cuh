@@ -19,8 +19,8 @@
 // shared memories: no second kernel.
 //
 // Measured: 64 listed blocks of 16 tokens for each of 32 sequences, 4 heads on each of 8
-// kv heads, d = 128: 25.4 us, 19.3 at HBM's copy rate; 128 blocks 48.4 us under the
-// profiler, at 71% of DRAM's peak.  What is left is the start (three loads that depend on
+// kv heads, d = 128: 25.4 us, 19.3 at HBM's copy rate; 128 blocks 49 us under the
+// profiler, at about 70% of DRAM's peak.  What is left is the start (three loads that depend on
 // one another behind the launch), the unequal ends and the join.
 //
 // A CTA has four warps.  Each streams KEYS keys per step through a ring of its own

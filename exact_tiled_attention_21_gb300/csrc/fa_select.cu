@@ -19,13 +19,17 @@
 // by 8 columns at a time.  Blocks further than 2 E from the smallest score that
 // stays are decided; if the others do not all stay, theirs are summed again in whole
 // numbers of 2^-61 A (off by 2^-58 A at most; in fp64 where something is not finite or
-// tiny), and equal ones go by index.
+// tiny), and equal ones go by index.  One element of q or the bounds that is not finite leaves
+// every block of its (sequence, kv head) to fp64: 5.0 ms for 4096 blocks, 0.64 ms for 256 of
+// each of 32 sequences (d = 128, 4 rows, 8 kv heads); more than 256 undecided blocks without that
+// are slower too (pages all alike: 131 us in place of 18, 25 in place of 14).
 //
-// 4 d bytes per block and 4 d flops per block and row: bound by HBM where contexts
-// are long (32 sequences of up to 16384 tokens, blocks of 16, 8 kv heads, d = 128: 27.5 us,
-// 14.5 at the copy rate), by latency otherwise (of 4096 tokens 12.9 us: 2 to the queries'
-// fragments, 7 to the scores, which the first loads of all SMs at once take half of, 3.6 to
-// the choice).  One
+// 4 d bytes per block and 4 d flops per block and row.  Where contexts are long the bounds'
+// way through shared memory and the queries' fragments, read again for every 16 blocks, bind it (32
+// sequences of up to 16384 tokens, blocks of 16, 8 kv heads, d = 128: 27.5 us, 14.5 at the
+// copy rate; DRAM below half of its peak under the profiler, short_scoreboard on top), otherwise
+// latency (of 4096 tokens 12.9 us: 2 to the queries' fragments, 7 to the scores, which the
+// first loads of all SMs at once take half of, 3.6 to the choice).  One
 // cluster of up to 8 CTAs per (sequence, kv head) makes the scores, in the shared memory
 // of its first CTA (or in the workspace), which chooses: a histogram over the scores'
 // range finds the bin that the smallest one that stays is in, and counting greater

@@ -483,7 +483,10 @@ size_t fa_select_blocks_workspace_bytes(int B, int Hkv, int max_blocks);
  * largest score, in ascending order; all of them and -1 behind them if n_b <= keep.
  * The choice is that of exact scores, but for what is below 2^-58 of the largest
  * sum_c |q_rc| |bound_c|: of equal ones (+0 = -0) the lowest index stays; NaN (also
- * an infinite bound times zero) counts as largest.  recent should
+ * an infinite bound times zero) counts as largest.  Where a query element or a bound
+ * is not finite, or all of a kv head's bounds are zero, its scores are summed in fp64,
+ * which takes a hundred times as long (milliseconds for thousands of blocks); several
+ * hundred equal scores around the last that stays take several times as long.  recent should
  * cover the Nq tokens.  workspace: 16-byte aligned, at least
  * fa_select_blocks_workspace_bytes(...); contents do not matter; calls that may
  * overlap need one each. */
